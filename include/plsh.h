@@ -399,10 +399,132 @@ plsh_status plsh_alibi_decode(const plsh_tensor* q, const plsh_tensor* K,
                               const plsh_tensor* V, const plsh_bins* bins, int64_t pos,
                               plsh_tensor* o, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit paged K/V cache.  The paper has no counterpart: this is a deployment
+ * variant of the decode step, not part of the method.
+ *
+ * A cache held in 4-bit codes takes 5 bits a value (codes and the scales of
+ * their groups) instead of bf16's 16, and a decode step, which reads its keys
+ * and values once, is bound by those bytes.  It is paged, so that sequences of
+ * different lengths share one pool, and every sequence of a batch has its own
+ * position, read on the device (a captured graph of a decode loop replays
+ * while the positions and the page table change).
+ *
+ * Format.  A row of d values is cut into groups of 32; a group is held as 32
+ * codes c in 0..15 and two bf16 numbers lo and step, and its values read back
+ * as lo + step c.  Writing x (each operation in fp32, rounded once; bit for
+ * bit the same from any implementation):
+ *   lo = min x rounded down to bf16,  step = (max x - lo) / 15 rounded up to
+ *   bf16,  c = (x - lo) / step rounded to the nearest integer, ties to even,
+ *   within 0..15 (0 where step is 0): a value is off by at most about step / 2.
+ * A group that holds a NaN or an infinity, or spans more than fp32 does, is
+ * stored as lo = 0, step = NaN: it reads back as NaN, and so does every
+ * attention row that gives one of its keys a weight.
+ * Positions are held in tiles of 16, 20 d bytes each, a page's tiles one after
+ * the other.  Within a tile, position r = 0..15 (= 8 blk + 2 t + par) and
+ * value e = 32 y + i of its row:
+ *   K codes  byte r d/2 + (i / 8) d/8 + 4 y + (i % 8) / 2
+ *   V codes  byte 8 d + (y / 2) 512 + (4 (i / 4) + t) 16 + (y % 2) 8 + 4 blk
+ *            + 2 par + (i % 4) / 2
+ *   (even values in the low nibble), then at 16 d + 4 (r d/32 + y) K's pairs
+ *   (lo, step) and from 18 d V's.
+ * These are the orders in which the decode step's matrix instructions take
+ * the codes, so that a lane loads its operands with 16-byte loads.
+ */
+typedef struct {
+  void* data;            /* device uint8 [pages, H, page / 16, 20 d], 16-byte
+                            aligned; the caller owns it */
+  const int32_t* table;  /* device int32 [B, max_pages]: sequence b holds its
+                            positions [i page, (i + 1) page) in page
+                            table[b, i] of data; entries past the pages a call
+                            needs are not read */
+  int64_t B;             /* sequences, >= 1 */
+  int64_t H;             /* KV heads, >= 1 */
+  int64_t pages;         /* pages of data, 1 .. 2^31 - 1 */
+  int64_t max_pages;     /* pages of a sequence, >= 1, max_pages page < 2^31 */
+  int32_t page;          /* positions of a page: 16, 32, 64, 128 or 256 */
+  int32_t d;             /* 64 or 128 */
+} plsh_q4_cache;
+
+/* Bytes of plsh_q4_cache.data: pages * H * (page / 16) * 20 d. */
+plsh_status plsh_q4_cache_bytes(int64_t pages, int64_t H, int32_t page, int32_t d,
+                                int64_t* bytes);
+
+/*
+ * plsh_q4_cache_write -- quantise rows of K and V into the cache: row i <
+ * len[b] of sequence b becomes its position pos[b] + i, for every head; the
+ * rest of the cache is left as it was.
+ *   K, V [B, H, m, d] (PLSH_BF16 or PLSH_F32) of the cache's B, H and d.
+ *   pos  device int32 [B].
+ *   len  device int32 [B], taken within 0..m, or NULL for m rows of each.
+ * A row whose position is negative or not below max_pages * page, or whose
+ * page index is not in [0, pages), is not written; plsh_stream_status then
+ * reports PLSH_ERR_INVALID.  Two sequences that write the same position of
+ * the same page leave one or a mixture of the two rows there: give each
+ * sequence pages of its own where it writes (shared pages may be read).
+ * Asynchronous on `stream`; allocates nothing.
+ */
+plsh_status plsh_q4_cache_write(const plsh_tensor* K, const plsh_tensor* V,
+                                const plsh_q4_cache* cache, const int32_t* pos,
+                                const int32_t* len, void* stream);
+
+/*
+ * plsh_q4_cache_read -- the values that positions pos[b] + i, i < len[b], of
+ * the cache stand for, as rows of K and V [B, H, m, d] (PLSH_BF16, rounded
+ * once, or PLSH_F32, exact up to one fp32 rounding).  Rows from len[b] on, and
+ * rows whose position or page index is out of range (reported as for
+ * plsh_q4_cache_write), are left as they were.  Asynchronous on `stream`;
+ * allocates nothing.
+ */
+plsh_status plsh_q4_cache_read(const plsh_q4_cache* cache, const int32_t* pos,
+                               const int32_t* len, plsh_tensor* K, plsh_tensor* V,
+                               void* stream);
+
+/* Bytes of workspace of a plsh_alibi_decode_q4 or plsh_alibi_exact_decode_q4
+ * call with these q and cache on the current device. */
+plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                      int64_t* bytes);
+
+/*
+ * plsh_alibi_decode_q4 -- plsh_alibi_decode over the 4-bit cache: for every
+ * sequence b the row of T~ at its own position pos[b],
+ *   o_b = sum_j c_j e^{S_j} v_j / sum_j c_j e^{S_j},  S_j = q_b . k_j / sqrt(d),
+ *   c_j = #{t : lo_t(pos[b]) <= j},  j in [min_t lo_t(pos[b]), pos[b]],
+ * with k_j, v_j the cached values.
+ *   q, o [B, Hq, 1, d], PLSH_BF16 or PLSH_F32; Hq a multiple of the cache's H;
+ *   bins->H == Hq, bins of any length: pos[b] must lie below bins->n.
+ *   pos  device int32 [B]; a negative one is an idle slot: o_b = 0.
+ *   work device memory of plsh_q4_decode_work_bytes, 16-byte aligned, used by
+ *        this call alone until it completes (calls that may overlap, and
+ *        graphs that may replay at once, take one each).
+ * A pos[b] not below max_pages * page or bins->n gives o_b = 0, and a key
+ * whose page index is not in [0, pages) counts as absent; either is reported
+ * as PLSH_ERR_INVALID by plsh_stream_status.  A key or value of c_j = 0, a
+ * position past pos[b] and whatever else a page holds have no effect, be it
+ * NaN.  Asynchronous on `stream`; allocates nothing; may be captured.
+ */
+plsh_status plsh_alibi_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                 const plsh_bins* bins, const int32_t* pos, plsh_tensor* o,
+                                 void* work, int64_t work_bytes, void* stream);
+
+/*
+ * plsh_alibi_exact_decode_q4 -- one decode step of exact ALiBi attention (the
+ * dense comparator, plsh_alibi_exact) over the 4-bit cache:
+ *   o_b = sum_j e^{S_j - (pos[b] - j) / sigma_h} v_j / sum_j (the weights),
+ *   0 <= j <= pos[b].
+ * sigma_h: host array [Hq], finite, > 0; at most 512 heads.  Everything else
+ * as for plsh_alibi_decode_q4.
+ */
+plsh_status plsh_alibi_exact_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                       const double* sigma_h, const int32_t* pos,
+                                       plsh_tensor* o, void* work, int64_t work_bytes,
+                                       void* stream);
+
 /* Synchronises `stream`, then reports CUDA errors and the library's device
  * error flag, clearing the flag: PLSH_ERR_TIMEOUT when a bounded device wait
  * ran out, else PLSH_ERR_RANGE when a tensor-core attention call met a value
- * of V beyond +-65504. */
+ * of V beyond +-65504, else PLSH_ERR_INVALID when a call on a 4-bit cache met
+ * a position or a page index out of range. */
 plsh_status plsh_stream_status(void* stream);
 
 /*

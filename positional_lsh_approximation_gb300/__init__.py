@@ -11,6 +11,7 @@ Linear Biases" (Wolfson & Wagner), technical summary, Methodology 1-3.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -23,6 +24,8 @@ from . import build as _build_mod
 __all__ = ["build", "load", "sample_bins", "bins_from_host", "bins_fixed", "bins_share_groups", "Bins", "alibi_attn",
            "alibi_attn_noalloc", "alibi_attn_host",
            "alibi_exact", "alibi_decode", "alibi_attn_backward", "bias_error", "stream_status",
+           "Q4Cache", "q4_cache_bytes", "q4_cache_write", "q4_cache_read", "q4_decode_work_bytes",
+           "alibi_decode_q4", "alibi_exact_decode_q4",
            "noalloc_status", "attn_path", "set_split_parts", "set_wait_limit_ns", "PlshError",
            "library_path"]
 
@@ -45,6 +48,12 @@ class _Tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("B", ctypes.c_int64), ("H", ctypes.c_int64),
                 ("n", ctypes.c_int64), ("d", ctypes.c_int64)]
+
+
+class _Q4Cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("B", ctypes.c_int64), ("H", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("page", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -71,6 +80,7 @@ def load():
         I32, I64, U64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
         D = ctypes.POINTER(ctypes.c_double)
         TP = ctypes.POINTER(_Tensor)
+        CP = ctypes.POINTER(_Q4Cache)
         sig = {
             "plsh_sample_bins": [I64, D, I32, I32, U64, P, ctypes.POINTER(P)],
             "plsh_bins_resample": [P, D, U64, P],
@@ -91,6 +101,12 @@ def load():
             "plsh_alibi_attn_host": [TP, TP, TP, P, I32, TP, P],
             "plsh_alibi_exact": [TP, TP, TP, D, I32, TP, P],
             "plsh_alibi_decode": [TP, TP, TP, P, I64, TP, P],
+            "plsh_q4_cache_bytes": [I64, I64, I32, I32, ctypes.POINTER(I64)],
+            "plsh_q4_cache_write": [TP, TP, CP, P, P, P],
+            "plsh_q4_cache_read": [CP, P, P, TP, TP, P],
+            "plsh_q4_decode_work_bytes": [TP, CP, ctypes.POINTER(I64)],
+            "plsh_alibi_decode_q4": [TP, CP, P, P, TP, P, I64, P],
+            "plsh_alibi_exact_decode_q4": [TP, CP, D, P, TP, P, I64, P],
             "plsh_stream_status": [P],
             "plsh_noalloc_status": [P],
             "plsh_attn_path": [TP, P, I32, ctypes.POINTER(I32)],
@@ -361,6 +377,144 @@ def alibi_attn_backward_lse(Q, K, V, O, lse, dO, bins: Bins, causal: bool, strea
         ctypes.c_void_p(lse.data_ptr()), ctypes.byref(t[4]), bins.handle, int(bool(causal)),
         ctypes.byref(t[5]), ctypes.byref(t[6]), ctypes.byref(t[7]), _stream(stream)))
     return dQ, dK, dV
+
+
+def q4_cache_bytes(pages: int, H: int, page: int, d: int) -> int:
+    """plsh_q4_cache_bytes: bytes of a 4-bit cache of `pages` pages of `page`
+    positions for H KV heads of d values."""
+    out = ctypes.c_int64()
+    _check(load().plsh_q4_cache_bytes(int(pages), int(H), int(page), int(d), ctypes.byref(out)))
+    return out.value
+
+
+def _on_device(what: str, *tensors):
+    """Every tensor on the current CUDA device (the device a call runs on)."""
+    for t in tensors:
+        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{what}: tensors must be on the current CUDA device")
+
+
+def _i32(what: str, t: torch.Tensor, B: int) -> ctypes.c_void_p:
+    if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of B = {B} entries")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+class Q4Cache:
+    """A 4-bit paged K/V cache (plsh_q4_cache): `data`, uint8 device memory of
+    pages * H * (page / 16) * 20 d bytes, and `table`, int32 [B, max_pages], the
+    page of every sequence's positions [i page, (i + 1) page).  Both belong to
+    the caller, who may change the table's entries between calls."""
+
+    def __init__(self, data: torch.Tensor, table: torch.Tensor, H: int, d: int, page: int = 64):
+        one = q4_cache_bytes(1, H, page, d)
+        if data.dtype != torch.uint8 or not data.is_contiguous() or data.numel() == 0 \
+                or data.numel() % one:
+            raise ValueError(f"Q4Cache: data must be contiguous uint8 of whole pages of {one} bytes")
+        if table.dtype != torch.int32 or table.dim() != 2 or not table.is_contiguous() \
+                or table.numel() == 0:
+            raise ValueError("Q4Cache: table must be contiguous int32 [B, max_pages]")
+        if data.device.type != "cuda" or table.device != data.device:
+            raise ValueError("Q4Cache: data and table must be on one CUDA device")
+        self.data, self.table = data, table
+        self.H, self.d, self.page = int(H), int(d), int(page)
+        self.B, self.max_pages = table.shape
+        self.pages = data.numel() // one
+        self._c = _Q4Cache(data.data_ptr(), table.data_ptr(), self.B, self.H, self.pages,
+                           self.max_pages, self.page, self.d)
+
+    @classmethod
+    def empty(cls, pages: int, H: int, d: int, table: torch.Tensor, page: int = 64) -> "Q4Cache":
+        """A cache of `pages` pages, not yet written, on the table's device."""
+        data = torch.empty(q4_cache_bytes(pages, H, page, d), dtype=torch.uint8, device=table.device)
+        return cls(data, table, H, d, page)
+
+
+def _stream_scope(stream):
+    """Allocations inside belong to the stream the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def q4_cache_write(cache: Q4Cache, K, V, pos, lens=None, stream=None):
+    """plsh_q4_cache_write: rows i < lens[b] (all m without lens) of K, V
+    [B, H, m, d] become positions pos[b] + i of the cache; pos, lens int32 [B]
+    on the device."""
+    rest = () if lens is None else (lens,)
+    _on_device("q4_cache_write", K, V, cache.data, pos, *rest)
+    tk, tv = _desc(K), _desc(V)
+    _check(load().plsh_q4_cache_write(
+        ctypes.byref(tk), ctypes.byref(tv), ctypes.byref(cache._c), _i32("pos", pos, cache.B),
+        None if lens is None else _i32("lens", lens, cache.B), _stream(stream)))
+
+
+def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=torch.bfloat16,
+                  out=None, stream=None):
+    """plsh_q4_cache_read: (K, V) [B, H, m, d], the values of positions
+    pos[b] + i, i < lens[b], of the cache.  `out`, a pair of tensors, keeps its
+    other rows; without it they are new, of `dtype` and m rows, and zero there."""
+    rest = () if lens is None else (lens,)
+    _on_device("q4_cache_read", cache.data, pos, *rest)
+    if out is None:
+        if m is None:
+            raise ValueError("q4_cache_read: give m, the rows of every sequence, or out")
+        with _stream_scope(stream):
+            out = tuple(torch.zeros(cache.B, cache.H, int(m), cache.d, dtype=dtype,
+                                    device=cache.data.device) for _ in range(2))
+    K, V = out
+    _on_device("q4_cache_read", K, V)
+    tk, tv = _desc(K), _desc(V)
+    _check(load().plsh_q4_cache_read(
+        ctypes.byref(cache._c), _i32("pos", pos, cache.B),
+        None if lens is None else _i32("lens", lens, cache.B), ctypes.byref(tk), ctypes.byref(tv),
+        _stream(stream)))
+    return K, V
+
+
+def q4_decode_work_bytes(q, cache: Q4Cache) -> int:
+    """plsh_q4_decode_work_bytes: workspace of a 4-bit decode call."""
+    out, tq = ctypes.c_int64(), _desc(q)
+    _check(load().plsh_q4_decode_work_bytes(ctypes.byref(tq), ctypes.byref(cache._c),
+                                            ctypes.byref(out)))
+    return out.value
+
+
+def _decode_q4(what, fn, q, cache, extra, pos, out, work, stream):
+    _on_device(what, q, cache.data, pos)
+    with _stream_scope(stream):
+        o = torch.empty_like(q) if out is None else out
+        if work is None:
+            work = torch.empty(q4_decode_work_bytes(q, cache), dtype=torch.uint8, device=q.device)
+    _on_device(what, o, work)
+    if not work.is_contiguous():
+        raise ValueError(f"{what}: work must be contiguous")
+    tq, to = _desc(q), _desc(o)
+    _check(fn(ctypes.byref(tq), ctypes.byref(cache._c), extra, _i32("pos", pos, cache.B),
+              ctypes.byref(to), ctypes.c_void_p(work.data_ptr()),
+              work.numel() * work.element_size(), _stream(stream)))
+    return o
+
+
+def alibi_decode_q4(q, cache: Q4Cache, bins: Bins, pos, out=None, work=None, stream=None):
+    """plsh_alibi_decode_q4: one decode step over the 4-bit cache, for every
+    sequence the row of T~ at its own position pos[b] (int32 [B] on the device;
+    negative: an idle slot, o = 0), for the queries q [B, Hq, 1, d].  `work`:
+    device memory of q4_decode_work_bytes, allocated when not given."""
+    return _decode_q4("alibi_decode_q4", load().plsh_alibi_decode_q4, q, cache, bins.handle, pos,
+                      out, work, stream)
+
+
+def alibi_exact_decode_q4(q, cache: Q4Cache, sigma, pos, out=None, work=None, stream=None):
+    """plsh_alibi_exact_decode_q4: one decode step of exact ALiBi attention over
+    the 4-bit cache (see alibi_decode_q4)."""
+    sig = _f64(sigma)
+    if sig.shape != (q.shape[1],):
+        raise ValueError("alibi_exact_decode_q4: sigma must hold a scale per query head")
+    return _decode_q4("alibi_exact_decode_q4", load().plsh_alibi_exact_decode_q4, q, cache,
+                      sig.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), pos, out, work, stream)
 
 
 def bias_error(bins: Bins, sigma: float, h: int, lanczos_iters: int = 60, seed: int = 0,

@@ -578,12 +578,15 @@ bool tc_path_ok(int dtype, int64_t d, int s, int causal, int exact) {
 }
 
 // Status of the device error word: bit 0 a bounded wait ran out, bit 1 a
-// value of V beyond f16's range on the tensor-core path.
+// value of V beyond f16's range on the tensor-core path, bit 2 a position or
+// page index of a 4-bit cache out of range.
 plsh_status device_flag_status(int flag) {
   if (flag & 1) return fail(PLSH_ERR_TIMEOUT, "a device-side wait ran out of time");
   if (flag & 2)
     return fail(PLSH_ERR_RANGE, "V holds a value beyond +-65504, which the tensor-core path "
                                 "takes in f16 (scale V down by a power of two: O scales with it)");
+  if (flag & plsh::kErrCachePlace)
+    return fail(PLSH_ERR_INVALID, "a position or a page index of a 4-bit cache is out of range");
   return PLSH_OK;
 }
 
@@ -1317,6 +1320,176 @@ plsh_status plsh_alibi_exact(const plsh_tensor* Q, const plsh_tensor* K, const p
   std::vector<float> slopes(Q->H);
   for (int64_t h = 0; h < Q->H; ++h) slopes[h] = (float)(1.4426950408889634 / sigma_h[h]);
   return run_attention(Q, K, V, O, causal, nullptr, slopes.data(), (cudaStream_t)stream);
+}
+
+// ----------------------------------------------------------- 4-bit paged cache
+namespace {
+
+plsh_status check_q4_shape(int64_t pages, int64_t H, int32_t page, int32_t d) {
+  if (pages < 1 || pages >= ((int64_t)1 << 31))
+    return fail(PLSH_ERR_INVALID, "cache: pages must be in [1, 2^31)");
+  if (H < 1 || H > 65535) return fail(PLSH_ERR_INVALID, "cache: H must be in [1, 65535]");
+  if (page != 16 && page != 32 && page != 64 && page != 128 && page != 256)
+    return fail(PLSH_ERR_INVALID, "cache: page must be 16, 32, 64, 128 or 256");
+  if (d != 64 && d != 128) return fail(PLSH_ERR_INVALID, "cache: d must be 64 or 128");
+  return PLSH_OK;
+}
+
+plsh_status check_q4_cache(const plsh_q4_cache* c, plsh::Q4Cache* out) {
+  if (c == nullptr) return fail(PLSH_ERR_INVALID, "cache is NULL");
+  plsh_status st = check_q4_shape(c->pages, c->H, c->page, c->d);
+  if (st != PLSH_OK) return st;
+  if (c->data == nullptr || ((uintptr_t)c->data & 15u) != 0)
+    return fail(PLSH_ERR_INVALID, "cache: data must be a 16-byte aligned device pointer");
+  if (c->table == nullptr || ((uintptr_t)c->table & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "cache: table must be an int32 device pointer");
+  if (c->B < 1 || c->B > 65535) return fail(PLSH_ERR_INVALID, "cache: B must be in [1, 65535]");
+  if (c->max_pages < 1 || c->max_pages >= ((int64_t)1 << 31) / c->page)
+    return fail(PLSH_ERR_INVALID, "cache: max_pages must be >= 1 and max_pages * page < 2^31");
+  out->data = static_cast<uint8_t*>(c->data);
+  out->table = c->table;
+  out->pages = c->pages;
+  out->max_pages = c->max_pages;
+  out->B = (int)c->B;
+  out->H = (int)c->H;
+  out->d = c->d;
+  out->page_shift = __builtin_ctz((unsigned)c->page);
+  return PLSH_OK;
+}
+
+plsh_status q4_rows(const plsh_tensor* K, const plsh_tensor* V, const plsh_q4_cache* cache,
+                    const int32_t* pos, const int32_t* len, bool write, cudaStream_t cs) {
+  plsh_status st;
+  plsh::Q4RowsArgs a;
+  if ((st = check_tensor(K, "K")) != PLSH_OK || (st = check_tensor(V, "V")) != PLSH_OK ||
+      (st = check_q4_cache(cache, &a.c)) != PLSH_OK)
+    return st;
+  if (V->dtype != K->dtype || V->B != K->B || V->H != K->H || V->n != K->n || V->d != K->d)
+    return fail(PLSH_ERR_INVALID, "V must have K's shape and dtype");
+  if (K->B != cache->B || K->H != cache->H || K->d != cache->d)
+    return fail(PLSH_ERR_INVALID, "K must be [B, H, m, d] with the cache's B, H and d");
+  if (K->n >= ((int64_t)1 << 31) || K->B * K->H * (K->n / 16 + 2) >= ((int64_t)1 << 31))
+    return fail(PLSH_ERR_UNSUPPORTED, "B * H * (m / 16 + 2) must be < 2^31");
+  if (pos == nullptr) return fail(PLSH_ERR_INVALID, "pos is NULL");
+  if ((((uintptr_t)pos | (uintptr_t)len) & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "pos and len must be int32 device pointers");
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  a.K = K->data;
+  a.V = V->data;
+  a.pos = pos;
+  a.len = len;
+  a.m = K->n;
+  a.dtype = K->dtype;
+  a.err = ctx->d_err;
+  PLSH_TRY_CUDA(write ? plsh::launch_q4_write(a, cs) : plsh::launch_q4_read(a, cs),
+                write ? "cache write launch" : "cache read launch");
+  return PLSH_OK;
+}
+
+plsh_status check_q4_query(const plsh_tensor* q, const plsh_q4_cache* cache, plsh::Q4Cache* c) {
+  plsh_status st;
+  if ((st = check_tensor(q, "q")) != PLSH_OK || (st = check_q4_cache(cache, c)) != PLSH_OK) return st;
+  if (q->n != 1) return fail(PLSH_ERR_INVALID, "q must be [B, Hq, 1, d]");
+  if (q->B != cache->B || q->d != cache->d)
+    return fail(PLSH_ERR_INVALID, "q must have the cache's B and d");
+  if (q->H % cache->H != 0) return fail(PLSH_ERR_INVALID, "Hq must be a multiple of the cache's H");
+  if (q->H >= ((int64_t)1 << 24) || q->B * q->H >= ((int64_t)1 << 24))
+    return fail(PLSH_ERR_UNSUPPORTED, "B * Hq must be < 2^24");
+  return PLSH_OK;
+}
+
+plsh_status q4_decode(const plsh_tensor* q, const plsh_q4_cache* cache, const plsh_bins* bins,
+                      const float* slopes, const int32_t* pos, plsh_tensor* o, void* work,
+                      int64_t work_bytes, cudaStream_t cs) {
+  plsh_status st;
+  plsh::Q4DecodeArgs a;
+  if ((st = check_q4_query(q, cache, &a.c)) != PLSH_OK || (st = check_tensor(o, "o")) != PLSH_OK)
+    return st;
+  if (o->dtype != q->dtype || o->B != q->B || o->H != q->H || o->n != 1 || o->d != q->d)
+    return fail(PLSH_ERR_INVALID, "o must have q's shape and dtype");
+  if (pos == nullptr || ((uintptr_t)pos & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "pos must be an int32 device pointer");
+  if (bins != nullptr) {
+    if (bins->H != q->H) return fail(PLSH_ERR_INVALID, "bins were drawn for another number of heads");
+    if ((st = check_bins_device(bins)) != PLSH_OK) return st;
+  }
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  const int64_t need = plsh::q4_decode_work_bytes(a.c.B, (int)q->H, a.c.H, a.c.d, ctx->num_sms);
+  if (work == nullptr || ((uintptr_t)work & 15u) != 0 || work_bytes < need)
+    return fail(PLSH_ERR_INVALID, "work must be 16-byte aligned device memory of at least " +
+                                      std::to_string(need) + " bytes");
+  a.q = q->data;
+  a.o = o->data;
+  a.pos = pos;
+  a.Hq = (int)q->H;
+  a.dtype = q->dtype;
+  a.rec = bins ? bins->d_rec : nullptr;
+  a.s = bins ? bins->s : 0;
+  a.W = bins ? bins->W : 0;
+  a.bins_n = bins ? bins->n : 0;
+  a.slope_log2 = slopes;
+  a.sigma = bins && (int64_t)bins->sigma_host.size() == q->H ? bins->sigma_host.data() : nullptr;
+  a.work = work;
+  a.num_sms = ctx->num_sms;
+  a.err = ctx->d_err;
+  PLSH_TRY_CUDA(plsh::launch_q4_decode(a, cs), "4-bit decode launch");
+  return PLSH_OK;
+}
+
+}  // namespace
+
+plsh_status plsh_q4_cache_bytes(int64_t pages, int64_t H, int32_t page, int32_t d,
+                                int64_t* bytes) {
+  if (bytes == nullptr) return fail(PLSH_ERR_INVALID, "bytes is NULL");
+  const plsh_status st = check_q4_shape(pages, H, page, d);
+  if (st != PLSH_OK) return st;
+  *bytes = pages * H * (page / 16) * (20 * (int64_t)d);
+  return PLSH_OK;
+}
+
+plsh_status plsh_q4_cache_write(const plsh_tensor* K, const plsh_tensor* V,
+                                const plsh_q4_cache* cache, const int32_t* pos,
+                                const int32_t* len, void* stream) {
+  return q4_rows(K, V, cache, pos, len, true, (cudaStream_t)stream);
+}
+
+plsh_status plsh_q4_cache_read(const plsh_q4_cache* cache, const int32_t* pos, const int32_t* len,
+                               plsh_tensor* K, plsh_tensor* V, void* stream) {
+  return q4_rows(K, V, cache, pos, len, false, (cudaStream_t)stream);
+}
+
+plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                      int64_t* bytes) {
+  if (bytes == nullptr) return fail(PLSH_ERR_INVALID, "bytes is NULL");
+  plsh::Q4Cache c;
+  plsh_status st = check_q4_query(q, cache, &c);
+  if (st != PLSH_OK) return st;
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  *bytes = plsh::q4_decode_work_bytes(c.B, (int)q->H, c.H, c.d, ctx->num_sms);
+  return PLSH_OK;
+}
+
+plsh_status plsh_alibi_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                 const plsh_bins* bins, const int32_t* pos, plsh_tensor* o,
+                                 void* work, int64_t work_bytes, void* stream) {
+  if (bins == nullptr) return fail(PLSH_ERR_INVALID, "bins is NULL");
+  return q4_decode(q, cache, bins, nullptr, pos, o, work, work_bytes, (cudaStream_t)stream);
+}
+
+plsh_status plsh_alibi_exact_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                       const double* sigma_h, const int32_t* pos, plsh_tensor* o,
+                                       void* work, int64_t work_bytes, void* stream) {
+  plsh_status st = check_tensor(q, "q");
+  if (st != PLSH_OK) return st;
+  if (q->H > plsh::kMaxExactHeads)
+    return fail(PLSH_ERR_UNSUPPORTED, "exact path serves at most 512 heads");
+  if ((st = check_sigma(sigma_h, (int32_t)q->H)) != PLSH_OK) return st;
+  float slopes[plsh::kMaxExactHeads];
+  for (int64_t h = 0; h < q->H; ++h) slopes[h] = (float)(1.4426950408889634 / sigma_h[h]);
+  return q4_decode(q, cache, nullptr, slopes, pos, o, work, work_bytes, (cudaStream_t)stream);
 }
 
 plsh_status plsh_stream_status(void* stream) {

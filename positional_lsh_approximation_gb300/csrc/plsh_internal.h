@@ -250,4 +250,48 @@ cudaError_t launch_attn_bwd_tc(const void* Q, const void* K, const void* V, cons
 cudaError_t launch_bwd_delta(const void* O, const void* dO, const float* lse, float* stats,
                              float* dq_acc, int64_t rows, cudaStream_t st);
 
+// 4-bit paged cache (the format stands in plsh.h): arguments of its kernels.
+// Positions and page indices are checked on the device; one out of range sets
+// kErrCachePlace in *err and the row or key it names is skipped.
+constexpr int kErrCachePlace = 4;
+struct Q4Cache {
+  uint8_t* data;           // [pages][H][page / 16][20 d]
+  const int32_t* table;    // [B][max_pages]
+  int64_t pages, max_pages;
+  int B, H, d;
+  int page_shift;          // log2(page)
+};
+// q4_cache.cu
+struct Q4RowsArgs {
+  Q4Cache c;
+  const void* K;           // [B, H, m, d]; written by a read
+  const void* V;
+  const int32_t* pos;      // [B]
+  const int32_t* len;      // [B] or null
+  int64_t m;
+  int dtype;
+  int* err;
+};
+cudaError_t launch_q4_write(const Q4RowsArgs& a, cudaStream_t st);
+cudaError_t launch_q4_read(const Q4RowsArgs& a, cudaStream_t st);
+// q4_decode.cu
+struct Q4DecodeArgs {
+  Q4Cache c;
+  const void* q;           // [B, Hq, 1, d]
+  void* o;
+  const int32_t* pos;      // [B]
+  int Hq;
+  int dtype;
+  const BinRecord* rec;    // [Hq*s][W], or null: exact ALiBi
+  int s;
+  int64_t W, bins_n;
+  const float* slope_log2;  // host [Hq], log2(e) / sigma_h (exact ALiBi)
+  const double* sigma;     // host [Hq], the bins' scales, or null if unknown
+  void* work;
+  int num_sms;
+  int* err;
+};
+int64_t q4_decode_work_bytes(int B, int Hq, int H, int d, int num_sms);
+cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st);
+
 }  // namespace plsh
