@@ -1416,7 +1416,7 @@ plsh_status q4_decode(const plsh_tensor* q, const plsh_q4_cache* cache, const pl
   }
   plsh::DeviceCtx* ctx = nullptr;
   if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
-  const int64_t need = plsh::q4_decode_work_bytes(a.c.B, (int)q->H, a.c.H, a.c.d, ctx->num_sms);
+  const int64_t need = plsh::q4_decode_work_bytes(a.c.d, ctx->num_sms);
   if (work == nullptr || ((uintptr_t)work & 15u) != 0 || work_bytes < need)
     return fail(PLSH_ERR_INVALID, "work must be 16-byte aligned device memory of at least " +
                                       std::to_string(need) + " bytes");
@@ -1468,7 +1468,7 @@ plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache*
   if (st != PLSH_OK) return st;
   plsh::DeviceCtx* ctx = nullptr;
   if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
-  *bytes = plsh::q4_decode_work_bytes(c.B, (int)q->H, c.H, c.d, ctx->num_sms);
+  *bytes = plsh::q4_decode_work_bytes(c.d, ctx->num_sms);
   return PLSH_OK;
 }
 

@@ -291,7 +291,7 @@ struct Q4DecodeArgs {
   int num_sms;
   int* err;
 };
-int64_t q4_decode_work_bytes(int B, int Hq, int H, int d, int num_sms);
+int64_t q4_decode_work_bytes(int d, int num_sms);
 cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st);
 
 }  // namespace plsh

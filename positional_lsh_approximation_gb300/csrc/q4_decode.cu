@@ -6,135 +6,806 @@
 //   approximate:  w_j = c_j = #{t : lo_t(pos) <= j},  j <= pos
 //   exact:        w_j = e^{-(pos - j) / sigma_h},     j <= pos
 // (Positional LSH, technical summary, Methodology 1 and 3, for one row.)
-// A CTA per (sequence, query head): a key per thread for the scores of 128
-// keys at a time, a running maximum and sum, then a value per thread for P V.
+//
+// What bounds it: the cache's bytes, 1.25 d a position and KV head.  At HBM
+// rate an SM has about 27 issue slots for a position of d = 128 (K and V), and
+// up to eight query heads share it; products on the CUDA cores would take
+// 2 d G / 32 of them alone, so they run as mma.sync m16n8k16 with the cached
+// values as the A operand (16 positions, or 16 values of a row) and the query
+// heads as the eight columns of B.  (tcgen05 takes A from shared or tensor
+// memory: the codes would be expanded to 16 bits, written there and read
+// again, which costs more than the products.)  The codes never become the
+// values they stand for:
+//   q . k_j = sum_y step_jy (sum_i q_yi c_jyi) + sum_y lo_jy (sum_i q_yi),
+//   sum_j p_j v_jyi = sum_j (p_j step_jy) c_jyi + sum_j p_j lo_jy,
+// so the products take the bare codes, step and lo act on sums of 32, in fp32.
+// A code becomes an f16 operand by one AND: c in the low bits of a half is the
+// subnormal c 2^-24, four bits up 16 c 2^-24, and the matrix instruction takes
+// subnormals exactly.  The cache holds the codes in the order of the operand
+// registers, so a word of eight codes gives four of them with four ANDs and a
+// shift.
+//   - q is scaled to f16 by a power of two per head (its largest magnitude in
+//     [2^14, 2^15); what is 2^-24 of that and less is lost); fp32 queries take
+//     two f16 terms, 22 bits.
+//   - p_j step_jy is scaled by a power of two per group that follows the
+//     largest step met, and rounded to f16 (2^-11 relative; fp32: two terms).
+//     f16 because bf16's 2^-8 would show beside the output's own rounding.
+// Each warp takes every kWarps-th tile of 16 positions with a maximum, row
+// sums and accumulators of its own, from a ring of asynchronous copies that
+// it alone fills and reads (no barrier in the loop); a warp's maximum moves
+// only when a score passes it by a factor 2^kLazy.  The warps of a CTA merge
+// in shared memory, pieces of a row that went to several CTAs in a second
+// kernel.
+//
+// Work split.  Exact: every CTA takes the same number of tiles of the flat
+// list (sequence, KV group, tile), found from the positions on the device, so
+// that ragged sequences balance.  Approximate: the row's key envelope is short
+// and known only after its bins are read; a CTA per (sequence, group), or a
+// few where the scales expect long envelopes and the grid is small.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "bins_dev.cuh"
 #include "plsh_internal.h"
 #include "q4.cuh"
+#include "tc_ptx.cuh"
 
 namespace plsh {
 namespace {
 
 using namespace q4;
+using namespace ptx;
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 5;          // tiles in flight per warp
+constexpr int kCtasPerSm = 4;
+constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
+constexpr int kMinTiles = 8;        // exact: tiles of a CTA at least
+constexpr int kMaxShares = 64;      // approximate: CTAs of one row at most
+constexpr int kMaxGroupOrder = 32;
+constexpr unsigned FULL = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
+
+struct Slopes {
+  float v[kMaxExactHeads];          // log2(e) / sigma_h
+};
+struct NoSlopes {};
 
 struct DecodeParams {
   Q4Cache c;
   const void* q;
   void* o;
   const int32_t* pos;
-  int Hq;
+  int Hq, G;                        // query heads, of a KV head
+  int chunks;                       // CTAs that share a KV head's query heads
   const BinRecord* rec;
   int s;
-  int64_t W, bins_n;
+  int64_t W;
+  int limit;                        // positions below this may be asked for
+  int shares;                       // approximate: CTAs of a (sequence, group)
+  int4* ends;                       // exact: per CTA {row, first CTA, first piece} of a row that ends in it
+  float* part;                      // pieces: o [8][D], m [8], l [8]
   int* err;
-  float slope[kMaxExactHeads];
 };
 
+template <int D>
+__host__ __device__ constexpr int part_floats() { return kHeads * (D + 2); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// c += A (16 x 16, row) B (16 x 8), f16 operands, fp32 sums
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 matrix of 16-bit values, two per lane and row
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// 2^e for -126 <= e <= 127, 0 below
+__device__ __forceinline__ float pow2(int e) {
+  return e < -126 ? 0.f : __int_as_float((e + 127) << 23);
+}
+__device__ __forceinline__ float sum_rows(float v) {      // over the lanes of one column pair
+  v += __shfl_xor_sync(FULL, v, 4);
+  v += __shfl_xor_sync(FULL, v, 8);
+  return v + __shfl_xor_sync(FULL, v, 16);
+}
+__device__ __forceinline__ float max_rows(float v) {
+  v = fmaxf(v, __shfl_xor_sync(FULL, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(FULL, v, 8));
+  return fmaxf(v, __shfl_xor_sync(FULL, v, 16));
+}
+
+// words of one lane: D / 32 consecutive 32-bit words of shared memory
+template <int N>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 v = ld_shared_v4(addr);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+  }
+}
+
+// What a CTA attends over: tiles [t0, t1) of sequence b, KV head kvh, for the
+// query heads h0 .. h0 + heads - 1.
+struct Piece {
+  int b, kvh, h0, heads, pos, t0, t1;
+  int first;         // first position any of the heads sees
+};
+
+template <typename T, int D>
+struct Smem {
+  alignas(128) uint8_t ring[kWarps][kStages][Layout<D>::kTileBytes];
+  float m[kWarps][kHeads], l[kWarps][kHeads];
+  int lo[kHeads][kMaxS];
+  int lo_min[kHeads];
+  int64_t scan[kThreads];
+  int64_t found[3];
+};
+// the merge of the warps reuses the ring
+static_assert(kWarps * kHeads * 128 * 4 <= kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
+static_assert(kWarps * kHeads * 64 * 4 <= kWarps * kStages * Layout<64>::kTileBytes, "merge buffer");
+
+// One piece; the result (all heads, the warps merged) goes to `o_row` (o of
+// head h0, divided by the row sums) or, when that is null, to `part`.
 template <typename T, int D, bool EXACT>
-__global__ void __launch_bounds__(kThreads) q4_decode_kernel(const __grid_constant__ DecodeParams p) {
+__device__ void attend(const DecodeParams& p, const Piece& pc, const float* slopes, Smem<T, D>& sm,
+                       T* o_row, float* part) {
   using L = Layout<D>;
-  __shared__ float qs[D], w_s[kThreads], red[4];
-  __shared__ int lo_s[kMaxS];
-  __shared__ const uint8_t* tile_s[kThreads / kTile];
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  T* o = static_cast<T*>(p.o) + (int64_t)blockIdx.x * D;
-  const int pos = p.pos[b];
-  const bool over = pos >= (p.c.max_pages << p.c.page_shift) || (!EXACT && pos >= p.bins_n);
-  if (pos < 0 || over) {
-    if (over && tid == 0) atomicOr(p.err, kErrCachePlace);
-    if (tid < D) o[tid] = Elem<T>::put(0.f);
-    return;
-  }
-  int first = 0;
-  if (!EXACT) {
-    if (tid < p.s)
-      lo_s[tid] = bin_lo(load_record(p.rec, ((int64_t)h * p.s + tid) * p.W + (pos >> 5)), pos);
-    __syncthreads();
-    first = pos;
-    for (int t = 0; t < p.s; ++t) first = min(first, lo_s[t]);
-  }
-  const float scale = kLog2e / sqrtf((float)D);
-  if (tid < D) qs[tid] = Elem<T>::get(static_cast<const T*>(p.q)[(int64_t)blockIdx.x * D + tid]) * scale;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int j0 = first & ~15; j0 <= pos; j0 += kThreads) {
-    __syncthreads();
-    if (tid < kThreads / kTile)
-      tile_s[tid] = j0 + tid * kTile <= pos ? tile_of<D>(p.c, b, h / (p.Hq / p.c.H), j0 + tid * kTile, p.err)
-                                            : nullptr;
-    __syncthreads();
-    const int j = j0 + tid, r = tid & 15;
-    const uint8_t* tile = tile_s[tid >> 4];
-    int c = j >= first && j <= pos && tile != nullptr;
-    if (!EXACT && c) {
-      c = 0;
-      for (int t = 0; t < p.s; ++t) c += lo_s[t] <= j;
+  constexpr int Y = L::kGroups;
+  constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
+  constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  // ---- the ring: tile pc.t0 + warp + kWarps i into stage i % kStages
+  const int mine = pc.t1 - pc.t0 > warp ? (pc.t1 - pc.t0 - warp + kWarps - 1) / kWarps : 0;
+  const uint32_t ring = smem_u32(sm.ring[warp][0]);
+  const int page_tiles_log = p.c.page_shift - 4;
+  const int32_t* table = p.c.table + (int64_t)pc.b * p.c.max_pages;
+  uint32_t absent = 0;                          // stages whose tile has no page
+  auto page_of = [&](int i) { return table[(pc.t0 + warp + kWarps * i) >> page_tiles_log]; };
+  auto fetch = [&](int i, int64_t pg) {
+    const int st = i % kStages;
+    absent &= ~(1u << st);
+    if (pg >= 0 && pg < p.c.pages) {
+      const int tile = (pc.t0 + warp + kWarps * i) & ((1 << page_tiles_log) - 1);
+      const uint8_t* src = p.c.data + (((pg * p.c.H + pc.kvh) << page_tiles_log) + tile) *
+                                          (int64_t)L::kTileBytes + 16 * lane;
+      const uint32_t dst = ring + st * L::kTileBytes + 16 * lane;
+#pragma unroll
+      for (int k = 0; k < (L::kTileBytes + 511) / 512; ++k)
+        if (L::kTileBytes % 512 == 0 || 512 * k + 16 * lane < L::kTileBytes)
+          cp_async16(dst + 512 * k, src + 512 * k);
+    } else {
+      absent |= 1u << st;
+      if (lane == 0) atomicOr(p.err, kErrCachePlace);
     }
-    float x = -INFINITY;
-    if (c > 0) {
-      x = 0.f;
-      for (int y = 0; y < L::kGroups; ++y) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + L::kKPairs + L::pair(r, y));
-        float dot = 0.f, sum = 0.f;
-        for (int i = 0; i < kGroup; i += 2) {
-          const uint32_t k = tile[L::k_code(r, y, i)];
-          const float q0 = qs[y * kGroup + i], q1 = qs[y * kGroup + i + 1];
-          dot = fmaf(q0, (float)(k & 15u), fmaf(q1, (float)(k >> 4), dot));
-          sum += q0 + q1;
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (i < mine) fetch(i, page_of(i));
+    cp_async_commit();
+  }
+  int32_t next_page = kStages - 1 < mine ? page_of(kStages - 1) : 0;
+
+  // ---- the queries as B operands: lane (g, t) holds values 8 t .. 8 t + 7 of
+  // every group of head g; the sums over a group and the scale for heads 2 t,
+  // 2 t + 1, whose scores it will hold
+  uint32_t qa[Y][4], qb[kTwo ? Y : 1][4];
+  float qsum[Y][2], qscale[2];
+  {
+    float v[Y][8], mx = 0.f;
+    bool bad = false;
+    const bool have = g < pc.heads;
+    const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + (have ? g : 0)) * D;
+#pragma unroll
+    for (int y = 0; y < Y; ++y)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[y][i] = have ? Elem<T>::get(q[32 * y + 8 * t + i]) : 0.f;
+        mx = fmaxf(mx, fabsf(v[y][i]));
+        bad |= !(fabsf(v[y][i]) < 1.2980742e33f);      // 2^110
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+    int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
+    bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
+    const float up = pow2(14 - min(e, 110));
+    const float norm = kLog2e / sqrtf((float)D);
+    const float scale = bad ? NAN : pow2(min(e, 110) + 10) * norm;       // 2^24 2^(e - 14)
+    qscale[0] = __shfl_sync(FULL, scale, 8 * t);
+    qscale[1] = __shfl_sync(FULL, scale, 8 * t + 4);
+#pragma unroll
+    for (int y = 0; y < Y; ++y) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[y][i];
+      sum += __shfl_xor_sync(FULL, sum, 1);
+      sum += __shfl_xor_sync(FULL, sum, 2);
+      sum *= norm;
+      qsum[y][0] = __shfl_sync(FULL, sum, 8 * t);
+      qsum[y][1] = __shfl_sync(FULL, sum, 8 * t + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // odd codes are taken four bits up, as 16 c
+        const float k = (i & 1) ? up * 0.0625f : up;
+        const float a = v[y][i] * k, b = v[y][i + 4] * k;
+        qa[y][i] = pack_f16(a, b);
+        if constexpr (kTwo) {
+          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&qa[y][i]));
+          qb[y][i] = pack_f16(a - f.x, b - f.y);
         }
-        x = fmaf(pair_step(w), dot, fmaf(pair_lo(w), sum, x));
-      }
-      if (EXACT) x = fmaf(-(float)(pos - j), p.slope[h], x);
-    }
-    float mx = x;
-    for (int e = 16; e > 0; e >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, e));
-    if (lane == 0) red[warp] = mx;
-    __syncthreads();
-    mx = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-    // every score NaN leaves the maximum at -inf: the weights come out NaN
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    w_s[tid] = c > 0 ? (float)c * exp2f(x - ref) : 0.f;
-    __syncthreads();
-    const float f = m == -INFINITY ? 1.f : exp2f(m - ref);
-    l *= f;
-    acc *= f;
-    m = mx;
-    const int y = tid / kGroup, i = tid & 31;
-    for (int k = 0; k < kThreads && j0 + k <= pos; ++k) {
-      const float w = w_s[k];
-      if (w == 0.f) continue;
-      l += w;
-      if (tid < D) {
-        const uint8_t* tl = tile_s[k >> 4];
-        const uint32_t pr = *reinterpret_cast<const uint32_t*>(tl + L::kVPairs + L::pair(k & 15, y));
-        const uint32_t v = tl[L::v_code(k & 15, y, i & ~1)] >> (4 * (i & 1));
-        acc = fmaf(w, fmaf(pair_step(pr), (float)(v & 15u), pair_lo(pr)), acc);
       }
     }
   }
-  if (tid < D) o[tid] = Elem<T>::put(l == 0.f ? 0.f : acc / l);
+  float slope[2] = {0.f, 0.f};
+  int lo_max[2] = {0, 0};
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) slope[k] = 2 * t + k < pc.heads ? slopes[pc.h0 + 2 * t + k] : 0.f;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      for (int x = 0; x < p.s; ++x) lo_max[k] = max(lo_max[k], sm.lo[2 * t + k][x]);
+  }
+
+  // ---- the loop
+  float acc[Y][2][4];             // P V: values 32 y + 4 g + 2 tau + (r >> 1), heads 2 t + (r & 1)
+  float low[Y][2];                // sum of p lo, this lane's positions
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float down[Y];                  // 2^-r of the group's weights
+  uint32_t most[Y];               // bits of the largest step that fits
+#pragma unroll
+  for (int y = 0; y < Y; ++y) {
+    down[y] = 1.f;
+    most[y] = 0;
+    low[y][0] = low[y][1] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[y][k >> 2][k & 3] = 0.f;
+  }
+  for (int i = 0; i < mine; ++i) {
+    if (i + kStages - 1 < mine) {
+      fetch(i + kStages - 1, next_page);
+      if (i + kStages < mine) next_page = page_of(i + kStages);
+    }
+    cp_async_commit();
+    cp_async_wait<kStages - 1>();
+    __syncwarp();
+    const int st = i % kStages;
+    if ((absent >> st) & 1) continue;
+    const uint32_t base = ring + st * L::kTileBytes;
+    const int j0 = (pc.t0 + warp + kWarps * i) * kTile;
+
+    // scores of positions j0 + g and j0 + g + 8, heads 2 t and 2 t + 1
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      uint32_t k0[Y], k1[Y], w0[Y], w1[Y];
+      lds(base + g * (D / 2) + t * (D / 8), k0);
+      lds(base + (g + 8) * (D / 2) + t * (D / 8), k1);
+      lds(base + L::kKPairs + L::pair(g, 0), w0);
+      lds(base + L::kKPairs + L::pair(g + 8, 0), w1);
+      float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int y = 0; y < Y; ++y) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t h0 = k0[y] >> 8, h1 = k1[y] >> 8;
+        const uint32_t a[8] = {k0[y] & 0x000f000fu, k1[y] & 0x000f000fu, k0[y] & 0x00f000f0u,
+                               k1[y] & 0x00f000f0u, h0 & 0x000f000fu,    h1 & 0x000f000fu,
+                               h0 & 0x00f000f0u,    h1 & 0x00f000f0u};
+        mma16816(c, a[0], a[1], a[2], a[3], qa[y][0], qa[y][1]);
+        mma16816(c, a[4], a[5], a[6], a[7], qa[y][2], qa[y][3]);
+        if constexpr (kTwo) {
+          mma16816(c, a[0], a[1], a[2], a[3], qb[y][0], qb[y][1]);
+          mma16816(c, a[4], a[5], a[6], a[7], qb[y][2], qb[y][3]);
+        }
+        const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
+        const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
+        x[0] = fmaf(s0, c[0], x[0]);
+        x[1] = fmaf(s0, c[1], x[1]);
+        x[2] = fmaf(s1, c[2], x[2]);
+        x[3] = fmaf(s1, c[3], x[3]);
+        z[0] = fmaf(b0, qsum[y][0], z[0]);
+        z[1] = fmaf(b0, qsum[y][1], z[1]);
+        z[2] = fmaf(b1, qsum[y][0], z[2]);
+        z[3] = fmaf(b1, qsum[y][1], z[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = fmaf(x[k], qscale[k & 1], z[k]);
+    }
+    // weights of the mask: -inf where a head does not see a position
+    const bool edge = j0 < pc.first || j0 + kTile - 1 > pc.pos;      // some positions unseen by all
+    float cnt[4] = {1.f, 1.f, 1.f, 1.f};
+    if constexpr (EXACT) {
+      const float d0 = (float)(j0 + g - pc.pos), d1 = d0 + 8.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = fmaf(k < 2 ? d0 : d1, slope[k & 1], x[k]);
+    } else {
+      int n[4] = {p.s, p.s, p.s, p.s};
+      if (!__all_sync(FULL, j0 >= lo_max[0] && j0 >= lo_max[1])) {
+        n[0] = n[1] = n[2] = n[3] = 0;
+        for (int k = 0; k < p.s; ++k) {
+          const int a = sm.lo[2 * t][k] - j0 - g, b = sm.lo[2 * t + 1][k] - j0 - g;
+          n[0] += a <= 0;
+          n[1] += b <= 0;
+          n[2] += a <= 8;
+          n[3] += b <= 8;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        cnt[k] = (float)n[k];
+        if (n[k] == 0) x[k] = -INFINITY;
+      }
+    }
+    uint32_t w0[Y], w1[Y];
+    lds(base + L::kVPairs + L::pair(g, 0), w0);
+    lds(base + L::kVPairs + L::pair(g + 8, 0), w1);
+    if (edge) {
+      // positions that no head sees may hold anything
+      const int j = j0 + g;
+      if (j < pc.first || j > pc.pos) {
+        x[0] = x[1] = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) w0[y] = 0;
+      }
+      if (j + 8 < pc.first || j + 8 > pc.pos) {
+        x[2] = x[3] = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) w1[y] = 0;
+      }
+    }
+    // does a score or a step outgrow what it is measured against?
+    bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
+#pragma unroll
+    for (int y = 0; y < Y; ++y) grow |= (w0[y] & 0xffff0000u) > most[y] || (w1[y] & 0xffff0000u) > most[y];
+    if (__any_sync(FULL, grow)) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float to = max_rows(fmaxf(m[k], fmaxf(x[k], x[k + 2])));
+        const float f = to == m[k] ? 1.f : ex2(m[k] - to);
+        m[k] = to;
+        l[k] *= f;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          low[y][k] *= f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[y][e >> 1][2 * (e & 1) + k] *= f;
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < Y; ++y) {
+        // a step that is not a number: its group of the row of every head
+        // that gives the position a weight is none either
+        const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
+        if (nan0) w0[y] = 0;
+        if (nan1) w1[y] = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
+        const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]) & 0xffff0000u);
+        if (top > most[y]) {
+          const int old = (int)(most[y] >> 23) - 132;          // most = 2^(r + 5)
+          const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
+          const float f = most[y] == 0 ? 0.f : pow2(old - r);
+          down[y] = pow2(-r);
+          most[y] = (uint32_t)(min(r + 5, 127) + 127) << 23;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[y][e >> 2][e & 3] *= f;
+        }
+      }
+    }
+    float pw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      pw[k] = x[k] == -INFINITY ? 0.f : ex2(x[k] - m[k & 1]);
+      if constexpr (!EXACT) pw[k] *= cnt[k];
+      l[k & 1] += pw[k];
+    }
+    // P V, group by group
+#pragma unroll
+    for (int yy = 0; yy < Y; yy += 2) {
+      const uint4 v4 = ld_shared_v4(base + L::kV + (yy >> 1) * 512 + lane * 16);
+#pragma unroll
+      for (int y = yy; y < yy + 2; ++y) {
+        const uint32_t v0 = y == yy ? v4.x : v4.z, v1 = y == yy ? v4.y : v4.w;
+        const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
+        low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
+        low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
+        const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
+        const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
+        uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
+        const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
+        const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
+                               v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
+                               h1 & 0x000f000fu, h1 & 0x00f000f0u};
+        uint32_t f0 = 0, f1 = 0;
+        if constexpr (kTwo) {
+          const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
+          const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
+          f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
+          f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
+        }
+        e0 = transpose8x8(e0);
+        e1 = transpose8x8(e1);
+        mma16816(acc[y][0], a[0], a[1], a[2], a[3], e0, e1);
+        mma16816(acc[y][1], a[4], a[5], a[6], a[7], e0, e1);
+        if constexpr (kTwo) {
+          mma16816(acc[y][0], a[0], a[1], a[2], a[3], f0, f1);
+          mma16816(acc[y][1], a[4], a[5], a[6], a[7], f0, f1);
+        }
+      }
+    }
+    __syncwarp();            // the stage may be filled again
+  }
+  cp_async_wait<0>();
+
+  // ---- merge the warps
+  __syncthreads();           // every ring is done with
+  float* merge = reinterpret_cast<float*>(sm.ring) + warp * kHeads * D;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float sum = sum_rows(l[k]);
+    if (g == 0) {
+      sm.m[warp][2 * t + k] = m[k];
+      sm.l[warp][2 * t + k] = sum;
+    }
+#pragma unroll
+    for (int y = 0; y < Y; ++y) {
+      const float b = sum_rows(low[y][k]);
+      const float up = most[y] == 0 ? 0.f : pow2((int)(most[y] >> 23) - 132);
+      float4 v;
+      v.x = fmaf(acc[y][0][k] * 0x1p24f, up, b);
+      v.y = fmaf(acc[y][0][2 + k] * 0x1p20f, up, b);
+      v.z = fmaf(acc[y][1][k] * 0x1p24f, up, b);
+      v.w = fmaf(acc[y][1][2 + k] * 0x1p20f, up, b);
+      *reinterpret_cast<float4*>(merge + (2 * t + k) * D + 32 * y + 4 * g) = v;
+    }
+  }
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(sm.ring);
+  for (int e = threadIdx.x; e < pc.heads * D; e += kThreads) {
+    const int h = e / D;
+    float mm = -INFINITY, ll = 0.f, o = 0.f;
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][h]);
+    for (int w = 0; w < kWarps; ++w) {
+      if (sm.l[w][h] == 0.f) continue;
+      const float f = sm.m[w][h] == mm ? 1.f : ex2(sm.m[w][h] - mm);
+      ll = fmaf(f, sm.l[w][h], ll);
+      o = fmaf(f, all[w * kHeads * D + e], o);
+    }
+    if (o_row != nullptr) {
+      o_row[e] = Elem<T>::put(ll == 0.f ? 0.f : o / ll);
+    } else {
+      part[e] = o;
+      if (e % D == 0) {
+        part[kHeads * D + h] = mm;
+        part[kHeads * D + kHeads + h] = ll;
+      }
+    }
+  }
+  __syncthreads();           // before the next piece fills the rings
+}
+
+// Tiles that the row of sequence b takes (exact); a position out of range
+// takes none.
+__device__ __forceinline__ int64_t row_tiles(const DecodeParams& p, int b) {
+  const int pos = p.pos[b];
+  return pos < 0 || pos >= p.limit ? 0 : (pos >> 4) + 1;
+}
+
+// heads of unit u (a KV head and a share of its query heads)
+__device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& pc) {
+  const int per = (p.G + p.chunks - 1) / p.chunks, c = u % p.chunks;
+  pc.kvh = u / p.chunks;
+  pc.h0 = pc.kvh * p.G + c * per;
+  pc.heads = min(per, p.G - c * per);
+}
+
+// Exact ALiBi.  The flat list of tiles runs over sequences, the units of a
+// sequence, and the row's tiles; CTA i takes tiles [i per, (i + 1) per) of it.
+// A row that lies within one CTA is finished there; of one that crosses CTAs,
+// each leaves a piece (slot 2 i when it begins with the CTA, else 2 i + 1),
+// and the CTA where it ends says in ends[i] which pieces to join.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Slopes slopes) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+  grid_dep_wait();
+  const int tid = threadIdx.x, units = p.c.H * p.chunks;
+  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
+    if (row_tiles(p, b) > 0) continue;
+    if (tid == 0 && p.pos[b] >= 0) atomicOr(p.err, kErrCachePlace);
+    for (int e = tid; e < p.Hq * D; e += kThreads)
+      static_cast<T*>(p.o)[(int64_t)b * p.Hq * D + e] = Elem<T>::put(0.f);
+  }
+  // prefix sums of the sequences' tiles, a run of sequences per thread
+  const int each = (p.c.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.c.B, tid * each), b1 = min(p.c.B, b0 + each);
+  int64_t sum = 0;
+  for (int b = b0; b < b1; ++b) sum += row_tiles(p, b);
+  sm.scan[tid] = sum;
+  __syncthreads();
+  for (int o = 1; o < kThreads; o <<= 1) {
+    const int64_t v = tid >= o ? sm.scan[tid - o] : 0;
+    __syncthreads();
+    sm.scan[tid] += v;
+    __syncthreads();
+  }
+  const int64_t total = sm.scan[kThreads - 1] * units;
+  const int64_t fair = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t per = fair < kMinTiles ? kMinTiles : fair;
+  const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
+  if (tid == 0) p.ends[blockIdx.x].x = -1;
+  if (begin >= end) return;
+  if (begin >= (sm.scan[tid] - sum) * units && begin < sm.scan[tid] * units) {
+    int64_t at = sm.scan[tid] - sum;
+    int b = b0;
+    for (;; ++b) {
+      const int64_t n = row_tiles(p, b);
+      if (begin < (at + n) * units) break;
+      at += n;
+    }
+    sm.found[0] = b;
+    sm.found[1] = at * units;
+  }
+  __syncthreads();
+  Piece pc;
+  pc.b = (int)sm.found[0];
+  pc.first = 0;
+  int64_t base = sm.found[1];
+  for (int64_t f = begin; f < end;) {
+    const int64_t n = row_tiles(p, pc.b), rel = f - base;
+    if (rel >= n * units) {
+      base += n * units;
+      ++pc.b;
+      continue;
+    }
+    const int u = (int)(rel / n);
+    pc.pos = p.pos[pc.b];
+    pc.t0 = (int)(rel - u * n);
+    pc.t1 = (int)min(n, pc.t0 + (end - f));
+    unit_heads(p, u, pc);
+    const bool whole = pc.t0 == 0 && pc.t1 == n;
+    if (tid == 0 && pc.t0 > 0 && pc.t1 == n) {
+      const int64_t row = f - pc.t0;              // where the row begins
+      const int i0 = (int)(row / per);
+      p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row == i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
+    }
+    attend<T, D, true>(p, pc, slopes.v, sm,
+                       whole ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D : nullptr,
+                       p.part + (2 * (int64_t)blockIdx.x + (f == begin ? 0 : 1)) * part_floats<D>());
+    f += pc.t1 - pc.t0;
+  }
+}
+
+// One head of a row from its pieces `first`, then from + step k below end.
+template <typename T, int D>
+__device__ void join_pieces(const DecodeParams& p, int first, int from, int end, int step, int h,
+                            T* o) {
+  const int e = threadIdx.x;
+  const float* m = p.part + kHeads * D + h;
+  float mm = m[(int64_t)first * part_floats<D>()];
+  for (int k = from; k < end; k += step) mm = fmaxf(mm, m[(int64_t)k * part_floats<D>()]);
+  float ll = 0.f, acc = 0.f;
+  auto add = [&](int k) {
+    const float* pt = p.part + (int64_t)k * part_floats<D>();
+    const float mk = pt[kHeads * D + h], lk = pt[kHeads * D + kHeads + h];
+    if (lk == 0.f) return;
+    const float f = mk == mm ? 1.f : ex2(mk - mm);
+    ll = fmaf(f, lk, ll);
+    acc = fmaf(f, pt[h * D + e], acc);
+  };
+  add(first);
+  for (int k = from; k < end; k += step) add(k);
+  o[e] = Elem<T>::put(ll == 0.f ? 0.f : acc / ll);
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const DecodeParams& p, bool exact, cudaStream_t st) {
-  const unsigned grid = (unsigned)(p.c.B * p.Hq);
-  if (exact)
-    q4_decode_kernel<T, D, true><<<grid, kThreads, 0, st>>>(p);
-  else
-    q4_decode_kernel<T, D, false><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+__global__ void __launch_bounds__(D) q4_exact_join_kernel(const __grid_constant__ DecodeParams p) {
+  grid_dep_wait();
+  const int4 end = p.ends[blockIdx.x];
+  if (end.x < 0) return;
+  const int units = p.c.H * p.chunks, h = blockIdx.y;
+  Piece pc;
+  unit_heads(p, end.x % units, pc);
+  if (h >= pc.heads) return;
+  join_pieces<T, D>(p, end.z, 2 * (end.y + 1), 2 * (int)blockIdx.x + 1, 2, h,
+                    static_cast<T*>(p.o) + ((int64_t)(end.x / units) * p.Hq + pc.h0 + h) * D);
+}
+
+// Approximate: KV heads by the largest scale of their query heads, widest
+// first (the longest envelopes start first), all sequences of a KV head
+// together; shares_of[kvh] CTAs for each row.
+struct Groups {
+  int first[kMaxGroupOrder + 1];          // first CTA of each, in order
+  uint8_t order[kMaxGroupOrder];
+  uint8_t shares_of[kMaxGroupOrder];      // by KV head
+  int ordered;                            // 0: index order, p.shares each
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Groups gr) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+  grid_dep_wait();
+  const int tid = threadIdx.x;
+  int cta = blockIdx.x, kvh, shares = p.shares;
+  if (gr.ordered) {
+    int k = 0;
+    while (k + 1 < p.c.H && cta >= gr.first[k + 1]) ++k;
+    cta -= gr.first[k];
+    kvh = gr.order[k];
+    shares = gr.shares_of[kvh];
+  } else {
+    kvh = cta / (p.c.B * p.chunks * shares);
+    cta -= kvh * p.c.B * p.chunks * shares;
+  }
+  const int share = cta % shares;
+  cta /= shares;
+  const int u = kvh * p.chunks + cta % p.chunks;
+  Piece pc;
+  pc.b = cta / p.chunks;
+  unit_heads(p, u, pc);
+  T* o = static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D;
+  float* part = p.part + ((int64_t)(pc.b * p.c.H * p.chunks + u) * p.shares + share) * part_floats<D>();
+  pc.pos = p.pos[pc.b];
+  const bool none = pc.pos < 0 || pc.pos >= p.limit;
+  if (none && tid == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
+  pc.first = pc.pos;
+  if (!none) {
+    for (int k = tid; k < kHeads * p.s; k += kThreads) {
+      const int h = k / p.s, x = k % p.s;
+      sm.lo[h][x] = h < pc.heads
+          ? bin_lo(load_record(p.rec, ((int64_t)(pc.h0 + h) * p.s + x) * p.W + (pc.pos >> 5)), pc.pos)
+          : 0;
+    }
+    __syncthreads();
+    if (tid < kHeads) {
+      int lo = pc.pos;
+      for (int x = 0; x < p.s; ++x) lo = min(lo, sm.lo[tid][x]);
+      sm.lo_min[tid] = lo;
+    }
+    __syncthreads();
+    for (int h = 0; h < pc.heads; ++h) pc.first = min(pc.first, sm.lo_min[h]);
+    const int t_first = pc.first >> 4, n = (pc.pos >> 4) + 1 - t_first;
+    const int len = (n + shares - 1) / shares;
+    pc.t0 = t_first + share * len;
+    pc.t1 = min(t_first + n, pc.t0 + len);
+  }
+  if (none || pc.t0 >= pc.t1) {
+    if (shares == 1)
+      for (int e = tid; e < pc.heads * D; e += kThreads) o[e] = Elem<T>::put(0.f);
+    else if (tid < kHeads)
+      part[kHeads * D + tid] = -INFINITY, part[kHeads * D + kHeads + tid] = 0.f;
+    return;
+  }
+  attend<T, D, false>(p, pc, nullptr, sm, shares == 1 ? o : nullptr, part);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(D)
+q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Groups gr) {
+  grid_dep_wait();
+  const int units = p.c.H * p.chunks, u = blockIdx.x % units, b = blockIdx.x / units, h = blockIdx.y;
+  Piece pc;
+  unit_heads(p, u, pc);
+  const int shares = gr.ordered ? gr.shares_of[pc.kvh] : p.shares;
+  if (h >= pc.heads || shares == 1) return;
+  const int first = (int)blockIdx.x * p.shares;
+  join_pieces<T, D>(p, first, first + 1, first + shares, 1, h,
+                    static_cast<T*>(p.o) + ((int64_t)b * p.Hq + pc.h0 + h) * D);
+}
+
+// Each kernel a programmatic dependent of the one before it: its launch
+// overlaps that one's tail, and it waits for its end before any access.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                   const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+int chunks_of(int G) { return (G + kHeads - 1) / kHeads; }
+int max_ctas(int num_sms) { return num_sms * kCtasPerSm; }
+
+template <typename T, int D>
+cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
+  Slopes s;
+  for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
+  const int64_t tiles = (int64_t)p.c.B * p.c.H * p.chunks * ((a.c.max_pages << a.c.page_shift) / kTile);
+  const int64_t want = (tiles + kMinTiles - 1) / kMinTiles;
+  const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
+  auto kern = q4_exact_kernel<T, D>;
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
+  if (e == cudaSuccess) e = launch(kern, dim3(grid), kThreads, sizeof(Smem<T, D>), st, p, s);
+  if (e == cudaSuccess) e = launch(q4_exact_join_kernel<T, D>, dim3(grid, kHeads), D, 0, st, p);
+  return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
+  const int H = p.c.H;
+  const int64_t rows = (int64_t)p.c.B * p.chunks;          // of one KV head
+  // a KV head's envelope reaches about 1.2 sigma + 32 keys back; a share per
+  // kShareKeys of it while the grid has room
+  constexpr double kShareKeys = 512.0;
+  const int64_t room = std::max<int64_t>(1, max_ctas(a.num_sms) / (rows * H));
+  auto shares = [&](double sigma) {
+    const double keys = std::min(1.2 * sigma + 32.0, (double)p.limit);
+    return (int)std::min<int64_t>(std::min<int64_t>(room, kMaxShares), (int64_t)(keys / kShareKeys) + 1);
+  };
+  Groups gr;
+  gr.ordered = H <= kMaxGroupOrder && a.sigma != nullptr;
+  double widest = a.sigma ? 0.0 : 1e30;
+  if (a.sigma)
+    for (int h = 0; h < a.Hq; ++h) widest = std::max(widest, a.sigma[h]);
+  p.shares = shares(widest);
+  int64_t grid = rows * H * p.shares;
+  if (gr.ordered) {
+    double key[kMaxGroupOrder];
+    for (int k = 0; k < H; ++k) {
+      key[k] = 0.0;
+      for (int h = k * p.G; h < (k + 1) * p.G; ++h) key[k] = std::max(key[k], a.sigma[h]);
+      gr.order[k] = (uint8_t)k;
+    }
+    std::stable_sort(gr.order, gr.order + H, [&](int x, int y) { return key[x] > key[y]; });
+    grid = 0;
+    for (int k = 0; k < H; ++k) {
+      gr.shares_of[gr.order[k]] = (uint8_t)shares(key[gr.order[k]]);
+      gr.first[k] = (int)grid;
+      grid += rows * gr.shares_of[gr.order[k]];
+    }
+    gr.first[H] = (int)grid;
+  }
+  auto kern = q4_approx_kernel<T, D>;
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
+  if (e == cudaSuccess) e = launch(kern, dim3((unsigned)grid), kThreads, sizeof(Smem<T, D>), st, p, gr);
+  if (e == cudaSuccess && p.shares > 1)
+    e = launch(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), kHeads), D, 0, st, p, gr);
+  return e;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
+  return a.rec ? launch_approx<T, D>(p, a, st) : launch_exact<T, D>(p, a, st);
 }
 
 }  // namespace
 
-int64_t q4_decode_work_bytes(int, int, int, int, int) { return 16; }
+// ends [CTAs] int4, then two pieces of a CTA (exact), or one of a share
+int64_t q4_decode_work_bytes(int d, int num_sms) {
+  return (int64_t)max_ctas(num_sms) * (sizeof(int4) + 2 * sizeof(float) * kHeads * (d + 2));
+}
 
 cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
   DecodeParams p;
@@ -143,17 +814,21 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
   p.o = a.o;
   p.pos = a.pos;
   p.Hq = a.Hq;
+  p.G = a.Hq / a.c.H;
+  p.chunks = chunks_of(p.G);
   p.rec = a.rec;
   p.s = a.s;
   p.W = a.W;
-  p.bins_n = a.bins_n;
+  const int64_t held = a.c.max_pages << a.c.page_shift;
+  p.limit = (int)(a.rec ? std::min(held, a.bins_n) : held);
+  p.shares = 1;
+  p.ends = static_cast<int4*>(a.work);
+  p.part = reinterpret_cast<float*>(p.ends + max_ctas(a.num_sms));
   p.err = a.err;
-  for (int h = 0; h < kMaxExactHeads; ++h) p.slope[h] = a.slope_log2 && h < a.Hq ? a.slope_log2[h] : 0.f;
-  const bool exact = a.rec == nullptr;
   if (a.dtype == PLSH_BF16)
-    return a.c.d == 64 ? launch_typed<__nv_bfloat16, 64>(p, exact, st)
-                       : launch_typed<__nv_bfloat16, 128>(p, exact, st);
-  return a.c.d == 64 ? launch_typed<float, 64>(p, exact, st) : launch_typed<float, 128>(p, exact, st);
+    return a.c.d == 64 ? launch_typed<__nv_bfloat16, 64>(p, a, st)
+                       : launch_typed<__nv_bfloat16, 128>(p, a, st);
+  return a.c.d == 64 ? launch_typed<float, 64>(p, a, st) : launch_typed<float, 128>(p, a, st);
 }
 
 }  // namespace plsh
