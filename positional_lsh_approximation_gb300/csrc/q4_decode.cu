@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -156,8 +157,9 @@ template <typename T, int D>
 struct Smem {
   alignas(128) uint8_t ring[kWarps][kStages][Layout<D>::kTileBytes];
   float m[kWarps][kHeads], l[kWarps][kHeads];
-  int lo[kHeads][kMaxS];
-  int lo_min[kHeads];
+  float weight[kWarps][kHeads];        // of a warp's part of a head
+  int raw_lo[kHeads][kMaxS];
+  int lo[kHeads][kMaxS];               // a head's bin starts, ascending
   int64_t scan[kThreads];
   int64_t found[3];
 };
@@ -176,20 +178,23 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
   constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-  // ---- the ring: tile pc.t0 + warp + kWarps i into stage i % kStages
-  const int mine = pc.t1 - pc.t0 > warp ? (pc.t1 - pc.t0 - warp + kWarps - 1) / kWarps : 0;
+  // ---- the ring: the warp's i-th tile, from the newest down, is
+  // pc.t1 - 1 - warp - kWarps i (ALiBi's weights fall with the distance: the
+  // running maximum is met early), in stage i % kStages
+  const int top = pc.t1 - 1 - warp;
+  const int mine = top >= pc.t0 ? (top - pc.t0) / kWarps + 1 : 0;
   const uint32_t ring = smem_u32(sm.ring[warp][0]);
   const int page_tiles_log = p.c.page_shift - 4;
   const int32_t* table = p.c.table + (int64_t)pc.b * p.c.max_pages;
+  const uint8_t* head_data = p.c.data + ((int64_t)pc.kvh << page_tiles_log) * L::kTileBytes + 16 * lane;
+  const int64_t page_bytes = ((int64_t)p.c.H << page_tiles_log) * L::kTileBytes;
   uint32_t absent = 0;                          // stages whose tile has no page
-  auto page_of = [&](int i) { return table[(pc.t0 + warp + kWarps * i) >> page_tiles_log]; };
-  auto fetch = [&](int i, int64_t pg) {
-    const int st = i % kStages;
+  auto page_of = [&](int i) { return table[(top - kWarps * i) >> page_tiles_log]; };
+  auto fetch = [&](int i, int st, int32_t pg) {
     absent &= ~(1u << st);
-    if (pg >= 0 && pg < p.c.pages) {
-      const int tile = (pc.t0 + warp + kWarps * i) & ((1 << page_tiles_log) - 1);
-      const uint8_t* src = p.c.data + (((pg * p.c.H + pc.kvh) << page_tiles_log) + tile) *
-                                          (int64_t)L::kTileBytes + 16 * lane;
+    if ((uint32_t)pg < (uint32_t)p.c.pages) {
+      const int in_page = (top - kWarps * i) & ((1 << page_tiles_log) - 1);
+      const uint8_t* src = head_data + pg * page_bytes + in_page * L::kTileBytes;
       const uint32_t dst = ring + st * L::kTileBytes + 16 * lane;
 #pragma unroll
       for (int k = 0; k < (L::kTileBytes + 511) / 512; ++k)
@@ -200,12 +205,18 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
       if (lane == 0) atomicOr(p.err, kErrCachePlace);
     }
   };
+  int32_t next_page;
+  {
+    int32_t pg[kStages];
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
-    if (i < mine) fetch(i, page_of(i));
-    cp_async_commit();
+    for (int i = 0; i < kStages; ++i) pg[i] = i < mine ? page_of(i) : 0;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < mine) fetch(i, i, pg[i]);
+      cp_async_commit();
+    }
+    next_page = pg[kStages - 1];
   }
-  int32_t next_page = kStages - 1 < mine ? page_of(kStages - 1) : 0;
 
   // ---- the queries as B operands: lane (g, t) holds values 8 t .. 8 t + 7 of
   // every group of head g; the sums over a group and the scale for heads 2 t,
@@ -218,13 +229,24 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
     const bool have = g < pc.heads;
     const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + (have ? g : 0)) * D;
 #pragma unroll
-    for (int y = 0; y < Y; ++y)
+    for (int y = 0; y < Y; ++y) {
+      const uint4* src = reinterpret_cast<const uint4*>(q + 32 * y + 8 * t);
+      uint32_t w[2 * sizeof(T)];
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+        const uint4 x = have ? src[k] : make_uint4(0, 0, 0, 0);
+        w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[y][i] = have ? Elem<T>::get(q[32 * y + 8 * t + i]) : 0.f;
+        if constexpr (kTwo)
+          v[y][i] = __uint_as_float(w[i]);
+        else
+          v[y][i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
         mx = fmaxf(mx, fabsf(v[y][i]));
         bad |= !(fabsf(v[y][i]) < 1.2980742e33f);      // 2^110
       }
+    }
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
     int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
@@ -258,14 +280,10 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
     }
   }
   float slope[2] = {0.f, 0.f};
-  int lo_max[2] = {0, 0};
+  int seen[2] = {p.s, p.s};        // bin starts at or before the last position of the tile
   if constexpr (EXACT) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) slope[k] = 2 * t + k < pc.heads ? slopes[pc.h0 + 2 * t + k] : 0.f;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      for (int x = 0; x < p.s; ++x) lo_max[k] = max(lo_max[k], sm.lo[2 * t + k][x]);
   }
 
   // ---- the loop
@@ -273,27 +291,28 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
   float low[Y][2];                // sum of p lo, this lane's positions
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   float down[Y];                  // 2^-r of the group's weights
-  uint32_t most[Y];               // bits of the largest step that fits
+  uint32_t most[Y];               // bits of the largest step that fits, low half set
 #pragma unroll
   for (int y = 0; y < Y; ++y) {
     down[y] = 1.f;
-    most[y] = 0;
+    most[y] = 0xffffu;
     low[y][0] = low[y][1] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[y][k >> 2][k & 3] = 0.f;
   }
-  for (int i = 0; i < mine; ++i) {
+  for (int i = 0, next = 0; i < mine; ++i) {
+    const int st = next, before = st == 0 ? kStages - 1 : st - 1;
+    next = st == kStages - 1 ? 0 : st + 1;
     if (i + kStages - 1 < mine) {
-      fetch(i + kStages - 1, next_page);
+      fetch(i + kStages - 1, before, next_page);
       if (i + kStages < mine) next_page = page_of(i + kStages);
     }
     cp_async_commit();
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    const int st = i % kStages;
     if ((absent >> st) & 1) continue;
     const uint32_t base = ring + st * L::kTileBytes;
-    const int j0 = (pc.t0 + warp + kWarps * i) * kTile;
+    const int j0 = (top - kWarps * i) * kTile;
 
     // scores of positions j0 + g and j0 + g + 8, heads 2 t and 2 t + 1
     float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -339,16 +358,26 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = fmaf(k < 2 ? d0 : d1, slope[k & 1], x[k]);
     } else {
-      int n[4] = {p.s, p.s, p.s, p.s};
-      if (!__all_sync(FULL, j0 >= lo_max[0] && j0 >= lo_max[1])) {
-        n[0] = n[1] = n[2] = n[3] = 0;
-        for (int k = 0; k < p.s; ++k) {
-          const int a = sm.lo[2 * t][k] - j0 - g, b = sm.lo[2 * t + 1][k] - j0 - g;
-          n[0] += a <= 0;
-          n[1] += b <= 0;
-          n[2] += a <= 8;
-          n[3] += b <= 8;
-        }
+      // starts past the tile are behind us; those inside it count from their
+      // position on
+      int n[4];
+      bool inside = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int* lo = sm.lo[2 * t + k];
+        while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
+        n[k] = n[k + 2] = seen[k];
+        inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
+      }
+      if (__any_sync(FULL, inside)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          for (int x = seen[k] - 1; x >= 0; --x) {
+            const int a = sm.lo[2 * t + k][x] - j0;
+            if (a <= 0) break;
+            n[k] -= a > g;
+            n[k + 2] -= a > g + 8;
+          }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -376,7 +405,7 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
     // does a score or a step outgrow what it is measured against?
     bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
 #pragma unroll
-    for (int y = 0; y < Y; ++y) grow |= (w0[y] & 0xffff0000u) > most[y] || (w1[y] & 0xffff0000u) > most[y];
+    for (int y = 0; y < Y; ++y) grow |= max(w0[y], w1[y]) > most[y];
     if (__any_sync(FULL, grow)) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -403,11 +432,11 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
           if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
         const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]) & 0xffff0000u);
         if (top > most[y]) {
-          const int old = (int)(most[y] >> 23) - 132;          // most = 2^(r + 5)
+          const int old = (int)(most[y] >> 23) - 132;          // most: 2^(r + 5)
           const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
-          const float f = most[y] == 0 ? 0.f : pow2(old - r);
+          const float f = most[y] == 0xffffu ? 0.f : pow2(old - r);
           down[y] = pow2(-r);
-          most[y] = (uint32_t)(min(r + 5, 127) + 127) << 23;
+          most[y] = ((uint32_t)(r + 132) << 23) | 0xffffu;
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[y][e >> 2][e & 3] *= f;
         }
@@ -471,7 +500,7 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
 #pragma unroll
     for (int y = 0; y < Y; ++y) {
       const float b = sum_rows(low[y][k]);
-      const float up = most[y] == 0 ? 0.f : pow2((int)(most[y] >> 23) - 132);
+      const float up = most[y] == 0xffffu ? 0.f : pow2((int)(most[y] >> 23) - 132);
       float4 v;
       v.x = fmaf(acc[y][0][k] * 0x1p24f, up, b);
       v.y = fmaf(acc[y][0][2 + k] * 0x1p20f, up, b);
@@ -481,26 +510,42 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
     }
   }
   __syncthreads();
+  if (threadIdx.x < kWarps * kHeads) {
+    const int h = threadIdx.x / kWarps, w = threadIdx.x % kWarps;
+    float mm = sm.m[w][h], ll = sm.l[w][h];
+#pragma unroll
+    for (int k = 1; k < kWarps; k <<= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
+    const float f = ll == 0.f ? 0.f : (sm.m[w][h] == mm ? 1.f : ex2(sm.m[w][h] - mm));
+    ll = ll == 0.f ? 0.f : ll * f;
+#pragma unroll
+    for (int k = 1; k < kWarps; k <<= 1) ll += __shfl_xor_sync(FULL, ll, k);
+    // a row divides by its sum; one that sees nothing is 0
+    sm.weight[w][h] = o_row == nullptr ? f : (ll == 0.f ? 0.f : __fdividef(f, ll));
+    if (o_row == nullptr && w == 0 && h < pc.heads) {
+      part[kHeads * D + h] = mm;
+      part[kHeads * D + kHeads + h] = ll;
+    }
+  }
+  __syncthreads();
   const float* all = reinterpret_cast<const float*>(sm.ring);
-  for (int e = threadIdx.x; e < pc.heads * D; e += kThreads) {
+  for (int e = 4 * threadIdx.x; e < pc.heads * D; e += 4 * kThreads) {
     const int h = e / D;
-    float mm = -INFINITY, ll = 0.f, o = 0.f;
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][h]);
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (sm.l[w][h] == 0.f) continue;
-      const float f = sm.m[w][h] == mm ? 1.f : ex2(sm.m[w][h] - mm);
-      ll = fmaf(f, sm.l[w][h], ll);
-      o = fmaf(f, all[w * kHeads * D + e], o);
+      const float f = sm.weight[w][h];
+      const float4 v = *reinterpret_cast<const float4*>(all + w * kHeads * D + e);
+      o[0] = fmaf(f, v.x, o[0]);
+      o[1] = fmaf(f, v.y, o[1]);
+      o[2] = fmaf(f, v.z, o[2]);
+      o[3] = fmaf(f, v.w, o[3]);
     }
-    if (o_row != nullptr) {
-      o_row[e] = Elem<T>::put(ll == 0.f ? 0.f : o / ll);
-    } else {
-      part[e] = o;
-      if (e % D == 0) {
-        part[kHeads * D + h] = mm;
-        part[kHeads * D + kHeads + h] = ll;
-      }
-    }
+    if (o_row == nullptr)
+      *reinterpret_cast<float4*>(part + e) = make_float4(o[0], o[1], o[2], o[3]);
+    else if constexpr (kTwo)
+      *reinterpret_cast<float4*>(o_row + e) = make_float4(o[0], o[1], o[2], o[3]);
+    else
+      *reinterpret_cast<uint2*>(o_row + e) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
   }
   __syncthreads();           // before the next piece fills the rings
 }
@@ -598,30 +643,62 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   }
 }
 
-// One head of a row from its pieces `first`, then from + step k below end.
+// One head of a row from its pieces: slot `first`, then first2 + step k, n
+// pieces in all.  A warp takes every kJoinWarps-th piece, a lane D / 32 values.
+constexpr int kJoinWarps = 4;
 template <typename T, int D>
-__device__ void join_pieces(const DecodeParams& p, int first, int from, int end, int step, int h,
+__device__ void join_pieces(const DecodeParams& p, int first, int first2, int step, int n, int h,
                             T* o) {
-  const int e = threadIdx.x;
-  const float* m = p.part + kHeads * D + h;
-  float mm = m[(int64_t)first * part_floats<D>()];
-  for (int k = from; k < end; k += step) mm = fmaxf(mm, m[(int64_t)k * part_floats<D>()]);
-  float ll = 0.f, acc = 0.f;
-  auto add = [&](int k) {
-    const float* pt = p.part + (int64_t)k * part_floats<D>();
-    const float mk = pt[kHeads * D + h], lk = pt[kHeads * D + kHeads + h];
-    if (lk == 0.f) return;
-    const float f = mk == mm ? 1.f : ex2(mk - mm);
-    ll = fmaf(f, lk, ll);
-    acc = fmaf(f, pt[h * D + e], acc);
+  constexpr int V = D / 32;
+  __shared__ float acc_s[kJoinWarps][D];
+  __shared__ float l_s[kJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot = [&](int k) {
+    return p.part + (int64_t)(k == 0 ? first : first2 + step * (k - 1)) * part_floats<D>();
   };
-  add(first);
-  for (int k = from; k < end; k += step) add(k);
-  o[e] = Elem<T>::put(ll == 0.f ? 0.f : acc / ll);
+  float mm = -INFINITY;
+  for (int k = lane; k < n; k += 32) mm = fmaxf(mm, slot(k)[kHeads * D + h]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
+  float ll = 0.f, acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int k = warp; k < n; k += kJoinWarps) {
+    const float* pt = slot(k);
+    const float mk = pt[kHeads * D + h], lk = pt[kHeads * D + kHeads + h];
+    float v[V];
+    if constexpr (V == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(pt + h * D + 4 * lane);
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(pt + h * D + 2 * lane);
+      v[0] = x.x, v[1] = x.y;
+    }
+    const float f = mk == mm ? 1.f : ex2(mk - mm);
+    if (lk != 0.f) {                   // else nothing of the piece was seen, or written
+      ll = fmaf(f, lk, ll);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc_s[warp][V * lane + e] = acc[e];
+  if (lane == 0) l_s[warp] = ll;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float sum = 0.f, a = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      sum += l_s[w];
+      a += acc_s[w][threadIdx.x];
+    }
+    o[threadIdx.x] = Elem<T>::put(sum == 0.f ? 0.f : a / sum);
+  }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(D) q4_exact_join_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __grid_constant__ DecodeParams p) {
   grid_dep_wait();
   const int4 end = p.ends[blockIdx.x];
   if (end.x < 0) return;
@@ -629,7 +706,7 @@ __global__ void __launch_bounds__(D) q4_exact_join_kernel(const __grid_constant_
   Piece pc;
   unit_heads(p, end.x % units, pc);
   if (h >= pc.heads) return;
-  join_pieces<T, D>(p, end.z, 2 * (end.y + 1), 2 * (int)blockIdx.x + 1, 2, h,
+  join_pieces<T, D>(p, end.z, 2 * (end.y + 1), 2, (int)blockIdx.x - end.y + 1, h,
                     static_cast<T*>(p.o) + ((int64_t)(end.x / units) * p.Hq + pc.h0 + h) * D);
 }
 
@@ -668,7 +745,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   pc.b = cta / p.chunks;
   unit_heads(p, u, pc);
   T* o = static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D;
-  float* part = p.part + ((int64_t)(pc.b * p.c.H * p.chunks + u) * p.shares + share) * part_floats<D>();
+  float* part = p.part + (int64_t)blockIdx.x * part_floats<D>();
   pc.pos = p.pos[pc.b];
   const bool none = pc.pos < 0 || pc.pos >= p.limit;
   if (none && tid == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
@@ -676,18 +753,23 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   if (!none) {
     for (int k = tid; k < kHeads * p.s; k += kThreads) {
       const int h = k / p.s, x = k % p.s;
-      sm.lo[h][x] = h < pc.heads
+      sm.raw_lo[h][x] = h < pc.heads
           ? bin_lo(load_record(p.rec, ((int64_t)(pc.h0 + h) * p.s + x) * p.W + (pc.pos >> 5)), pc.pos)
           : 0;
     }
     __syncthreads();
-    if (tid < kHeads) {
-      int lo = pc.pos;
-      for (int x = 0; x < p.s; ++x) lo = min(lo, sm.lo[tid][x]);
-      sm.lo_min[tid] = lo;
+    // each head's starts in ascending order, a start per thread by its rank
+    for (int k = tid; k < kHeads * p.s; k += kThreads) {
+      const int h = k / p.s, x = k % p.s, v = sm.raw_lo[h][x];
+      int rank = 0;
+      for (int y = 0; y < p.s; ++y) {
+        const int w = sm.raw_lo[h][y];
+        rank += w < v || (w == v && y < x);
+      }
+      sm.lo[h][rank] = v;
     }
     __syncthreads();
-    for (int h = 0; h < pc.heads; ++h) pc.first = min(pc.first, sm.lo_min[h]);
+    for (int h = 0; h < pc.heads; ++h) pc.first = min(pc.first, sm.lo[h][0]);
     const int t_first = pc.first >> 4, n = (pc.pos >> 4) + 1 - t_first;
     const int len = (n + shares - 1) / shares;
     pc.t0 = t_first + share * len;
@@ -704,7 +786,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(D)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Groups gr) {
   grid_dep_wait();
   const int units = p.c.H * p.chunks, u = blockIdx.x % units, b = blockIdx.x / units, h = blockIdx.y;
@@ -712,8 +794,15 @@ q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_const
   unit_heads(p, u, pc);
   const int shares = gr.ordered ? gr.shares_of[pc.kvh] : p.shares;
   if (h >= pc.heads || shares == 1) return;
-  const int first = (int)blockIdx.x * p.shares;
-  join_pieces<T, D>(p, first, first + 1, first + shares, 1, h,
+  // the row's first CTA: its KV head's, then (sequence, chunk, share)
+  int first = pc.kvh * p.c.B * p.chunks * shares;
+  if (gr.ordered) {
+    int k = 0;
+    while (gr.order[k] != pc.kvh) ++k;
+    first = gr.first[k];
+  }
+  first += (b * p.chunks + u % p.chunks) * shares;
+  join_pieces<T, D>(p, first, first + 1, 1, shares, h,
                     static_cast<T*>(p.o) + ((int64_t)b * p.Hq + pc.h0 + h) * D);
 }
 
@@ -748,7 +837,7 @@ cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st
   auto kern = q4_exact_kernel<T, D>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
   if (e == cudaSuccess) e = launch(kern, dim3(grid), kThreads, sizeof(Smem<T, D>), st, p, s);
-  if (e == cudaSuccess) e = launch(q4_exact_join_kernel<T, D>, dim3(grid, kHeads), D, 0, st, p);
+  if (e == cudaSuccess) e = launch(q4_exact_join_kernel<T, D>, dim3(grid, kHeads), 32 * kJoinWarps, 0, st, p);
   return e;
 }
 
@@ -756,42 +845,48 @@ template <typename T, int D>
 cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
   const int H = p.c.H;
   const int64_t rows = (int64_t)p.c.B * p.chunks;          // of one KV head
-  // a KV head's envelope reaches about 1.2 sigma + 32 keys back; a share per
-  // kShareKeys of it while the grid has room
-  constexpr double kShareKeys = 512.0;
-  const int64_t room = std::max<int64_t>(1, max_ctas(a.num_sms) / (rows * H));
-  auto shares = [&](double sigma) {
-    const double keys = std::min(1.2 * sigma + 32.0, (double)p.limit);
-    return (int)std::min<int64_t>(std::min<int64_t>(room, kMaxShares), (int64_t)(keys / kShareKeys) + 1);
-  };
+  // The furthest of the s n bin starts of a KV head's n query heads lies about
+  // sigma (1 + ln(s n)) back (the distance to a bin's start exceeds a with
+  // probability e^{-a/sigma} (1 + a / (2 sigma))).  A share for every
+  // kShareKeys of that, coarser while the shares outnumber two waves of CTAs.
+  constexpr double kShareKeys = 128.0;
+  const double reach = 1.0 + log((double)p.s * std::min(p.G, kHeads));
   Groups gr;
   gr.ordered = H <= kMaxGroupOrder && a.sigma != nullptr;
+  double key[kMaxGroupOrder] = {};
   double widest = a.sigma ? 0.0 : 1e30;
   if (a.sigma)
-    for (int h = 0; h < a.Hq; ++h) widest = std::max(widest, a.sigma[h]);
-  p.shares = shares(widest);
-  int64_t grid = rows * H * p.shares;
+    for (int h = 0; h < a.Hq; ++h) {
+      widest = std::max(widest, a.sigma[h]);
+      if (gr.ordered) key[h / p.G] = std::max(key[h / p.G], a.sigma[h]);
+    }
   if (gr.ordered) {
-    double key[kMaxGroupOrder];
-    for (int k = 0; k < H; ++k) {
-      key[k] = 0.0;
-      for (int h = k * p.G; h < (k + 1) * p.G; ++h) key[k] = std::max(key[k], a.sigma[h]);
-      gr.order[k] = (uint8_t)k;
-    }
+    for (int k = 0; k < H; ++k) gr.order[k] = (uint8_t)k;
     std::stable_sort(gr.order, gr.order + H, [&](int x, int y) { return key[x] > key[y]; });
-    grid = 0;
-    for (int k = 0; k < H; ++k) {
-      gr.shares_of[gr.order[k]] = (uint8_t)shares(key[gr.order[k]]);
-      gr.first[k] = (int)grid;
-      grid += rows * gr.shares_of[gr.order[k]];
+  }
+  int64_t grid = 0;
+  for (double keys = kShareKeys;; keys *= 2.0) {
+    auto shares = [&](double sigma) {
+      return (int)std::min((double)kMaxShares, std::min(reach * sigma, (double)p.limit) / keys + 1.0);
+    };
+    p.shares = shares(widest);
+    if (!gr.ordered) grid = rows * H * p.shares;
+    if (gr.ordered) {
+      grid = 0;
+      for (int k = 0; k < H; ++k) {
+        gr.shares_of[gr.order[k]] = (uint8_t)shares(key[gr.order[k]]);
+        gr.first[k] = (int)grid;
+        grid += rows * gr.shares_of[gr.order[k]];
+      }
+      gr.first[H] = (int)grid;
     }
-    gr.first[H] = (int)grid;
+    if (p.shares == 1 || grid <= 2 * max_ctas(a.num_sms)) break;
   }
   auto kern = q4_approx_kernel<T, D>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
   if (e == cudaSuccess) e = launch(kern, dim3((unsigned)grid), kThreads, sizeof(Smem<T, D>), st, p, gr);
   if (e == cudaSuccess && p.shares > 1)
-    e = launch(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), kHeads), D, 0, st, p, gr);
+    e = launch(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), kHeads), 32 * kJoinWarps, 0, st, p, gr);
   return e;
 }
 
