@@ -64,13 +64,14 @@ using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 5;          // tiles in flight per warp
-constexpr int kCtasPerSm = 4;
+constexpr int kStages = 6;          // tiles of a warp's ring
+constexpr int kCtasPerSm = 3;
 constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
 constexpr int kMinTiles = 8;        // exact: tiles of a CTA at least
 constexpr int kMaxShares = 64;      // approximate: CTAs of one row at most
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
+constexpr float kNothing = -3.402823466e38f;   // a maximum over no score
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Slopes {
@@ -110,6 +111,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with bf16 operands
+__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -161,116 +171,152 @@ struct Smem {
   int raw_lo[kHeads][kMaxS];
   int lo[kHeads][kMaxS];               // a head's bin starts, ascending
   int64_t scan[kThreads];
-  int64_t found[3];
+  int64_t found[2];
 };
 // the merge of the warps reuses the ring
 static_assert(kWarps * kHeads * 128 * 4 <= kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
 static_assert(kWarps * kHeads * 64 * 4 <= kWarps * kStages * Layout<64>::kTileBytes, "merge buffer");
 
-// One piece; the result (all heads, the warps merged) goes to `o_row` (o of
-// head h0, divided by the row sums) or, when that is null, to `part`.
-template <typename T, int D, bool EXACT>
-__device__ void attend(const DecodeParams& p, const Piece& pc, const float* slopes, Smem<T, D>& sm,
-                       T* o_row, float* part) {
-  using L = Layout<D>;
-  constexpr int Y = L::kGroups;
-  constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
-  constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+// Lane (g, t)'s values 8 t .. 8 t + 7 of every group of query head g.
+template <typename T, int D>
+struct Query {
+  uint4 w[Layout<D>::kGroups][sizeof(T) / 2];
+  __device__ void load(const DecodeParams& p, const Piece& pc) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + g) * D + 8 * t;
+#pragma unroll
+    for (int y = 0; y < Layout<D>::kGroups; ++y)
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+        w[y][k] = g < pc.heads ? reinterpret_cast<const uint4*>(q + 32 * y)[k] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ float get(int y, int i) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint4& x = w[y][i >> 2];
+      return __uint_as_float((i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w);
+    } else {
+      const uint4& x = w[y][0];
+      const uint32_t v = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
+      return __uint_as_float((i & 1) ? v & 0xffff0000u : v << 16);
+    }
+  }
+};
 
-  // ---- the ring: the warp's i-th tile, from the newest down, is
-  // pc.t1 - 1 - warp - kWarps i (ALiBi's weights fall with the distance: the
-  // running maximum is met early), in stage i % kStages
-  const int top = pc.t1 - 1 - warp;
-  const int mine = top >= pc.t0 ? (top - pc.t0) / kWarps + 1 : 0;
-  const uint32_t ring = smem_u32(sm.ring[warp][0]);
-  const int page_tiles_log = p.c.page_shift - 4;
-  const int32_t* table = p.c.table + (int64_t)pc.b * p.c.max_pages;
-  const uint8_t* head_data = p.c.data + ((int64_t)pc.kvh << page_tiles_log) * L::kTileBytes + 16 * lane;
-  const int64_t page_bytes = ((int64_t)p.c.H << page_tiles_log) * L::kTileBytes;
-  uint32_t absent = 0;                          // stages whose tile has no page
-  auto page_of = [&](int i) { return table[(top - kWarps * i) >> page_tiles_log]; };
-  auto fetch = [&](int i, int st, int32_t pg) {
+// A warp's ring of tiles of one piece.  The i-th tile is the piece's tile
+// number first + (i / PER) kWarps PER + i % PER from the newest down (ALiBi's
+// weights fall with the distance: the running maximum is met early).
+template <typename T, int D, int PER>
+struct Ring {
+  using L = Layout<D>;
+  const uint8_t* head_data;
+  const int32_t* table;
+  int64_t page_bytes;
+  int64_t pages;
+  uint32_t smem;
+  int log_tiles, lane;
+  uint32_t absent = 0;          // stages whose tile has no page
+  int* err;
+  __device__ Ring(const DecodeParams& p, const Piece& pc, const void* ring)
+      : table(p.c.table + (int64_t)pc.b * p.c.max_pages), pages(p.c.pages), smem(smem_u32(ring)),
+        log_tiles(p.c.page_shift - 4), lane(threadIdx.x & 31), err(p.err) {
+    page_bytes = ((int64_t)p.c.H << log_tiles) * L::kTileBytes;
+    head_data = p.c.data + ((int64_t)pc.kvh << log_tiles) * L::kTileBytes + 16 * lane;
+  }
+  __device__ int32_t page_of(int tile) const { return table[tile >> log_tiles]; }
+  __device__ void fetch(int tile, int st, int32_t pg) {
     absent &= ~(1u << st);
-    if ((uint32_t)pg < (uint32_t)p.c.pages) {
-      const int in_page = (top - kWarps * i) & ((1 << page_tiles_log) - 1);
-      const uint8_t* src = head_data + pg * page_bytes + in_page * L::kTileBytes;
-      const uint32_t dst = ring + st * L::kTileBytes + 16 * lane;
+    if ((uint32_t)pg < (uint32_t)pages) {
+      const uint8_t* src = head_data + pg * page_bytes + (tile & ((1 << log_tiles) - 1)) * L::kTileBytes;
+      const uint32_t dst = smem + st * L::kTileBytes + 16 * lane;
 #pragma unroll
       for (int k = 0; k < (L::kTileBytes + 511) / 512; ++k)
         if (L::kTileBytes % 512 == 0 || 512 * k + 16 * lane < L::kTileBytes)
           cp_async16(dst + 512 * k, src + 512 * k);
     } else {
       absent |= 1u << st;
-      if (lane == 0) atomicOr(p.err, kErrCachePlace);
+      if (lane == 0) atomicOr(err, kErrCachePlace);
     }
-  };
-  int32_t next_page;
+  }
+};
+
+// One piece; the result (all heads, the warps merged) goes to `o_row` (o of
+// head h0, divided by the row sums) or, when that is null, to `part`.  PER
+// tiles a step: the exact step's loop overhead is shared by two.  `ahead`: the
+// first warp's first tile is in its ring already, not yet committed.
+template <typename T, int D, bool EXACT, int PER>
+__device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Query<T, D>& query,
+                                       const float* slopes, Smem<T, D>& sm, Ring<T, D, PER>& ring,
+                                       bool ahead, T* o_row, float* part) {
+  using L = Layout<D>;
+  constexpr int Y = L::kGroups;
+  constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
+  constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
+  constexpr int kSteps = kStages / PER;         // steps that the ring holds
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  // ---- step i takes tiles newest - i kWarps PER - (0 .. PER - 1)
+  const int newest = pc.t1 - 1 - warp * PER;
+  const int steps = newest >= pc.t0 ? (newest - pc.t0) / (kWarps * PER) + 1 : 0;
+  auto tile_at = [&](int i, int u) { return newest - i * (kWarps * PER) - u; };
+  int32_t next_page[PER];
   {
-    int32_t pg[kStages];
+    int32_t pg[kSteps][PER];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) pg[i] = i < mine ? page_of(i) : 0;
+    for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < mine) fetch(i, i, pg[i]);
+      for (int u = 0; u < PER; ++u)
+        pg[i][u] = i < steps && tile_at(i, u) >= pc.t0 ? ring.page_of(tile_at(i, u)) : 0;
+#pragma unroll
+    for (int i = 0; i < kSteps - 1; ++i) {
+#pragma unroll
+      for (int u = 0; u < PER; ++u)
+        if (i < steps && tile_at(i, u) >= pc.t0 && !(ahead && i == 0 && u == 0 && warp == 0))
+          ring.fetch(tile_at(i, u), i * PER + u, pg[i][u]);
       cp_async_commit();
     }
-    next_page = pg[kStages - 1];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) next_page[u] = pg[kSteps - 1][u];
   }
 
-  // ---- the queries as B operands: lane (g, t) holds values 8 t .. 8 t + 7 of
-  // every group of head g; the sums over a group and the scale for heads 2 t,
-  // 2 t + 1, whose scores it will hold
-  uint32_t qa[Y][4], qb[kTwo ? Y : 1][4];
-  float qsum[Y][2], qscale[2];
+  // ---- the queries as B operands; qlow takes the products of q's sums over a
+  // group with K's lo, a bf16 number: k slots 2 t, 2 t + 1 and 2 t + 8 hold
+  // group t's sum as three bf16 terms (24 bits)
+  uint32_t qa[Y][4], qb[kTwo ? Y : 1][4], qlow[2];
+  float qscale[2];
   {
-    float v[Y][8], mx = 0.f;
+    float mx = 0.f;
     bool bad = false;
-    const bool have = g < pc.heads;
-    const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + (have ? g : 0)) * D;
 #pragma unroll
-    for (int y = 0; y < Y; ++y) {
-      const uint4* src = reinterpret_cast<const uint4*>(q + 32 * y + 8 * t);
-      uint32_t w[2 * sizeof(T)];
-#pragma unroll
-      for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
-        const uint4 x = have ? src[k] : make_uint4(0, 0, 0, 0);
-        w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
-      }
+    for (int y = 0; y < Y; ++y)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (kTwo)
-          v[y][i] = __uint_as_float(w[i]);
-        else
-          v[y][i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-        mx = fmaxf(mx, fabsf(v[y][i]));
-        bad |= !(fabsf(v[y][i]) < 1.2980742e33f);      // 2^110
+        const float v = fabsf(query.get(y, i));
+        mx = fmaxf(mx, v);
+        bad |= !(v < 1.2980742e33f);      // 2^110
       }
-    }
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-    int e = max((int)(__float_as_uint(mx) >> 23) - 127, -100);
+    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 110);
     bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
-    const float up = pow2(14 - min(e, 110));
+    const float up = pow2(14 - e);
     const float norm = kLog2e / sqrtf((float)D);
-    const float scale = bad ? NAN : pow2(min(e, 110) + 10) * norm;       // 2^24 2^(e - 14)
+    const float scale = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
     qscale[0] = __shfl_sync(FULL, scale, 8 * t);
     qscale[1] = __shfl_sync(FULL, scale, 8 * t + 4);
+    float mine = 0.f;
 #pragma unroll
     for (int y = 0; y < Y; ++y) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += v[y][i];
+      for (int i = 0; i < 8; ++i) sum += query.get(y, i);
       sum += __shfl_xor_sync(FULL, sum, 1);
       sum += __shfl_xor_sync(FULL, sum, 2);
-      sum *= norm;
-      qsum[y][0] = __shfl_sync(FULL, sum, 8 * t);
-      qsum[y][1] = __shfl_sync(FULL, sum, 8 * t + 4);
+      if (y == t) mine = sum * norm;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // odd codes are taken four bits up, as 16 c
         const float k = (i & 1) ? up * 0.0625f : up;
-        const float a = v[y][i] * k, b = v[y][i + 4] * k;
+        const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
         qa[y][i] = pack_f16(a, b);
         if constexpr (kTwo) {
           const float2 f = __half22float2(*reinterpret_cast<__half2*>(&qa[y][i]));
@@ -278,6 +324,10 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
         }
       }
     }
+    const float hi = __uint_as_float(__float_as_uint(mine) & 0xffff0000u);
+    const float mid = __uint_as_float(__float_as_uint(mine - hi) & 0xffff0000u);
+    qlow[0] = pack_bf16(hi, mid);
+    qlow[1] = pack_bf16(mine - hi - mid, 0.f);
   }
   float slope[2] = {0.f, 0.f};
   int seen[2] = {p.s, p.s};        // bin starts at or before the last position of the tile
@@ -289,7 +339,7 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
   // ---- the loop
   float acc[Y][2][4];             // P V: values 32 y + 4 g + 2 tau + (r >> 1), heads 2 t + (r & 1)
   float low[Y][2];                // sum of p lo, this lane's positions
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
   float down[Y];                  // 2^-r of the group's weights
   uint32_t most[Y];               // bits of the largest step that fits, low half set
 #pragma unroll
@@ -300,29 +350,65 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[y][k >> 2][k & 3] = 0.f;
   }
-  for (int i = 0, next = 0; i < mine; ++i) {
-    const int st = next, before = st == 0 ? kStages - 1 : st - 1;
-    next = st == kStages - 1 ? 0 : st + 1;
-    if (i + kStages - 1 < mine) {
-      fetch(i + kStages - 1, before, next_page);
-      if (i + kStages < mine) next_page = page_of(i + kStages);
+  // positions before `from` are unseen: by every head, or not of this piece
+  const int from = max(pc.first, pc.t0 * kTile);
+  const uint32_t k_at = ring.smem + g * (D / 2) + t * (D / 8);
+  const uint32_t pair_at = ring.smem + L::pair(g, 0);
+  const uint32_t low_at = ring.smem + L::kKPairs + L::pair(g, t & (Y - 1));
+  const uint32_t v_at = ring.smem + L::kV + 16 * lane;
+  for (int i = 0, st = 0; i < steps; ++i, st = st == kSteps - 1 ? 0 : st + 1) {
+    if (i + kSteps - 1 < steps) {
+      const int before = st == 0 ? kSteps - 1 : st - 1;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int at = tile_at(i + kSteps - 1, u);
+        if (u == 0 || at >= pc.t0) ring.fetch(at, before * PER + u, next_page[u]);
+        const int then = tile_at(i + kSteps, u);
+        if (then >= pc.t0) next_page[u] = ring.page_of(then);
+      }
     }
     cp_async_commit();
-    cp_async_wait<kStages - 1>();
+    cp_async_wait<kSteps - 1>();
     __syncwarp();
-    if ((absent >> st) & 1) continue;
-    const uint32_t base = ring + st * L::kTileBytes;
-    const int j0 = (top - kWarps * i) * kTile;
 
     // scores of positions j0 + g and j0 + g + 8, heads 2 t and 2 t + 1
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    {
+    float x[PER][4], cnt[PER][4];
+    uint32_t tops[Y];              // the largest pair of a group (by step), of this lane's
+    bool cut[PER];                 // some positions unseen by all: they may hold anything
+    // V's pairs of positions g and g + 8 of tile u, zero where no head sees them
+    auto v_pairs = [&](int u, uint32_t (&w0)[Y], uint32_t (&w1)[Y]) {
+      const uint32_t at = (uint32_t)((st * PER + u) * L::kTileBytes);
+      lds(pair_at + at + L::kVPairs, w0);
+      lds(pair_at + at + L::kVPairs + L::pair(8, 0), w1);
+      if (cut[u]) {
+        const bool gone = (ring.absent >> (st * PER + u)) & 1;
+        const int j = tile_at(i, u) * kTile + g;
+        const bool no0 = gone || j < from || j > pc.pos, no1 = gone || j + 8 < from || j + 8 > pc.pos;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          if (no0) w0[y] = 0;
+          if (no1) w1[y] = 0;
+        }
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const uint32_t at = (uint32_t)((st * PER + u) * L::kTileBytes);
+      const int j0 = tile_at(i, u) * kTile;
+      const bool gone = (ring.absent >> (st * PER + u)) & 1;
       uint32_t k0[Y], k1[Y], w0[Y], w1[Y];
-      lds(base + g * (D / 2) + t * (D / 8), k0);
-      lds(base + (g + 8) * (D / 2) + t * (D / 8), k1);
-      lds(base + L::kKPairs + L::pair(g, 0), w0);
-      lds(base + L::kKPairs + L::pair(g + 8, 0), w1);
+      lds(k_at + at, k0);
+      lds(k_at + at + 4 * D, k1);
+      lds(pair_at + at + L::kKPairs, w0);
+      lds(pair_at + at + L::kKPairs + L::pair(8, 0), w1);
       float z[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        const uint32_t b0 = __byte_perm(ld_shared_u32(low_at + at), 0, 0x1010);
+        const uint32_t b1 = __byte_perm(ld_shared_u32(low_at + at + L::pair(8, 0)), 0, 0x1010);
+        mma16816_bf16(z, b0, b1, b0, b1, qlow[0], qlow[1]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[u][k] = 0.f;
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
         float c[4] = {0.f, 0.f, 0.f, 0.f};
@@ -337,80 +423,72 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
           mma16816(c, a[4], a[5], a[6], a[7], qb[y][2], qb[y][3]);
         }
         const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
-        const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
-        x[0] = fmaf(s0, c[0], x[0]);
-        x[1] = fmaf(s0, c[1], x[1]);
-        x[2] = fmaf(s1, c[2], x[2]);
-        x[3] = fmaf(s1, c[3], x[3]);
-        z[0] = fmaf(b0, qsum[y][0], z[0]);
-        z[1] = fmaf(b0, qsum[y][1], z[1]);
-        z[2] = fmaf(b1, qsum[y][0], z[2]);
-        z[3] = fmaf(b1, qsum[y][1], z[3]);
+        x[u][0] = fmaf(s0, c[0], x[u][0]);
+        x[u][1] = fmaf(s0, c[1], x[u][1]);
+        x[u][2] = fmaf(s1, c[2], x[u][2]);
+        x[u][3] = fmaf(s1, c[3], x[u][3]);
       }
+      // the mask's weights; -inf where a head does not see a position
+      if constexpr (EXACT) {
+        const float d0 = (float)(j0 + g - pc.pos), d1 = d0 + 8.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = fmaf(x[k], qscale[k & 1], z[k]);
-    }
-    // weights of the mask: -inf where a head does not see a position
-    const bool edge = j0 < pc.first || j0 + kTile - 1 > pc.pos;      // some positions unseen by all
-    float cnt[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (EXACT) {
-      const float d0 = (float)(j0 + g - pc.pos), d1 = d0 + 8.f;
+        for (int k = 0; k < 4; ++k)
+          x[u][k] = fmaf(x[u][k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
+      } else {
+        // starts past the tile are behind us; those inside it count from
+        // their position on
+        int n[4];
+        bool inside = false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = fmaf(k < 2 ? d0 : d1, slope[k & 1], x[k]);
-    } else {
-      // starts past the tile are behind us; those inside it count from their
-      // position on
-      int n[4];
-      bool inside = false;
+        for (int k = 0; k < 2; ++k) {
+          const int* lo = sm.lo[2 * t + k];
+          while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
+          n[k] = n[k + 2] = seen[k];
+          inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
+        }
+        if (__any_sync(FULL, inside)) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int* lo = sm.lo[2 * t + k];
-        while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
-        n[k] = n[k + 2] = seen[k];
-        inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
+          for (int k = 0; k < 2; ++k)
+            for (int y = seen[k] - 1; y >= 0; --y) {
+              const int a = sm.lo[2 * t + k][y] - j0;
+              if (a <= 0) break;
+              n[k] -= a > g;
+              n[k + 2] -= a > g + 8;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          cnt[u][k] = (float)n[k];
+          x[u][k] = n[k] == 0 ? -INFINITY : fmaf(x[u][k], qscale[k & 1], z[k]);
+        }
       }
-      if (__any_sync(FULL, inside)) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          for (int x = seen[k] - 1; x >= 0; --x) {
-            const int a = sm.lo[2 * t + k][x] - j0;
-            if (a <= 0) break;
-            n[k] -= a > g;
-            n[k + 2] -= a > g + 8;
-          }
+      cut[u] = gone || j0 < from || j0 + kTile - 1 > pc.pos;
+      if (cut[u]) {
+        const int j = j0 + g;
+        if (gone || j < from || j > pc.pos) x[u][0] = x[u][1] = -INFINITY;
+        if (gone || j + 8 < from || j + 8 > pc.pos) x[u][2] = x[u][3] = -INFINITY;
       }
+      v_pairs(u, w0, w1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        cnt[k] = (float)n[k];
-        if (n[k] == 0) x[k] = -INFINITY;
-      }
-    }
-    uint32_t w0[Y], w1[Y];
-    lds(base + L::kVPairs + L::pair(g, 0), w0);
-    lds(base + L::kVPairs + L::pair(g + 8, 0), w1);
-    if (edge) {
-      // positions that no head sees may hold anything
-      const int j = j0 + g;
-      if (j < pc.first || j > pc.pos) {
-        x[0] = x[1] = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < Y; ++y) w0[y] = 0;
-      }
-      if (j + 8 < pc.first || j + 8 > pc.pos) {
-        x[2] = x[3] = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < Y; ++y) w1[y] = 0;
-      }
+      for (int y = 0; y < Y; ++y)
+        tops[y] = u == 0 ? max(w0[y], w1[y]) : max(tops[y], max(w0[y], w1[y]));
     }
     // does a score or a step outgrow what it is measured against?
-    bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
+    float xs[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])};
 #pragma unroll
-    for (int y = 0; y < Y; ++y) grow |= max(w0[y], w1[y]) > most[y];
+    for (int u = 1; u < PER; ++u) {
+      xs[0] = fmaxf(xs[0], fmaxf(x[u][0], x[u][2]));
+      xs[1] = fmaxf(xs[1], fmaxf(x[u][1], x[u][3]));
+    }
+    bool grow = xs[0] > m[0] + kLazy || xs[1] > m[1] + kLazy;
+#pragma unroll
+    for (int y = 0; y < Y; ++y) grow |= tops[y] > most[y];
+    bool spoilt = false;           // a step that is not a number among the tiles
     if (__any_sync(FULL, grow)) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float to = max_rows(fmaxf(m[k], fmaxf(x[k], x[k + 2])));
-        const float f = to == m[k] ? 1.f : ex2(m[k] - to);
+        const float to = max_rows(fmaxf(m[k], xs[k]));
+        const float f = ex2(m[k] - to);
         m[k] = to;
         l[k] *= f;
 #pragma unroll
@@ -422,18 +500,23 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
       }
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
-        // a step that is not a number: its group of the row of every head
-        // that gives the position a weight is none either
-        const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
-        if (nan0) w0[y] = 0;
-        if (nan1) w1[y] = 0;
+        uint32_t top = __reduce_max_sync(FULL, tops[y]);
+        if (top >= 0x7f800000u) {
+          spoilt = true;
+          top = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
-        const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]) & 0xffff0000u);
+          for (int u = 0; u < PER; ++u) {
+            uint32_t w0[Y], w1[Y];
+            v_pairs(u, w0, w1);
+            if (w0[y] < 0x7f800000u) top = max(top, w0[y]);
+            if (w1[y] < 0x7f800000u) top = max(top, w1[y]);
+          }
+          top = __reduce_max_sync(FULL, top);
+        }
         if (top > most[y]) {
           const int old = (int)(most[y] >> 23) - 132;          // most: 2^(r + 5)
-          const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
+          // the largest step in [2^2, 2^3) 2^r
+          const int r = max((int)(top >> 23) - 129, -100);
           const float f = most[y] == 0xffffu ? 0.f : pow2(old - r);
           down[y] = pow2(-r);
           most[y] = ((uint32_t)(r + 132) << 23) | 0xffffu;
@@ -442,48 +525,67 @@ __device__ void attend(const DecodeParams& p, const Piece& pc, const float* slop
         }
       }
     }
-    float pw[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      pw[k] = x[k] == -INFINITY ? 0.f : ex2(x[k] - m[k & 1]);
-      if constexpr (!EXACT) pw[k] *= cnt[k];
-      l[k & 1] += pw[k];
-    }
-    // P V, group by group
+    for (int u = 0; u < PER; ++u) {
+      const uint32_t at = (uint32_t)((st * PER + u) * L::kTileBytes);
+      uint32_t w0[Y], w1[Y];
+      v_pairs(u, w0, w1);
+      if (spoilt) {
+        // a step that is not a number: its group of the row of every head
+        // that gives the position a weight is none either
 #pragma unroll
-    for (int yy = 0; yy < Y; yy += 2) {
-      const uint4 v4 = ld_shared_v4(base + L::kV + (yy >> 1) * 512 + lane * 16);
+        for (int y = 0; y < Y; ++y) {
+          const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
+          if (nan0) w0[y] = 0;
+          if (nan1) w1[y] = 0;
 #pragma unroll
-      for (int y = yy; y < yy + 2; ++y) {
-        const uint32_t v0 = y == yy ? v4.x : v4.z, v1 = y == yy ? v4.y : v4.w;
-        const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
-        low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
-        low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
-        const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
-        const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
-        uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
-        const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
-        const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
-                               v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
-                               h1 & 0x000f000fu, h1 & 0x00f000f0u};
-        uint32_t f0 = 0, f1 = 0;
-        if constexpr (kTwo) {
-          const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
-          const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
-          f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
-          f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
+          for (int k = 0; k < 2; ++k)
+            if ((nan0 && x[u][k] != -INFINITY) || (nan1 && x[u][k + 2] != -INFINITY)) low[y][k] = NAN;
         }
-        e0 = transpose8x8(e0);
-        e1 = transpose8x8(e1);
-        mma16816(acc[y][0], a[0], a[1], a[2], a[3], e0, e1);
-        mma16816(acc[y][1], a[4], a[5], a[6], a[7], e0, e1);
-        if constexpr (kTwo) {
-          mma16816(acc[y][0], a[0], a[1], a[2], a[3], f0, f1);
-          mma16816(acc[y][1], a[4], a[5], a[6], a[7], f0, f1);
+      }
+      float pw[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        pw[k] = ex2(x[u][k] - m[k & 1]);
+        if constexpr (!EXACT) pw[k] *= cnt[u][k];
+        l[k & 1] += pw[k];
+      }
+      // P V, group by group
+#pragma unroll
+      for (int yy = 0; yy < Y; yy += 2) {
+        const uint4 v4 = ld_shared_v4(v_at + at + (yy >> 1) * 512);
+#pragma unroll
+        for (int y = yy; y < yy + 2; ++y) {
+          const uint32_t v0 = y == yy ? v4.x : v4.z, v1 = y == yy ? v4.y : v4.w;
+          const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
+          low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
+          low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
+          const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
+          const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
+          uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
+          const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
+          const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
+                                 v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
+                                 h1 & 0x000f000fu, h1 & 0x00f000f0u};
+          uint32_t f0 = 0, f1 = 0;
+          if constexpr (kTwo) {
+            const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
+            const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
+            f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
+            f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
+          }
+          e0 = transpose8x8(e0);
+          e1 = transpose8x8(e1);
+          mma16816(acc[y][0], a[0], a[1], a[2], a[3], e0, e1);
+          mma16816(acc[y][1], a[4], a[5], a[6], a[7], e0, e1);
+          if constexpr (kTwo) {
+            mma16816(acc[y][0], a[0], a[1], a[2], a[3], f0, f1);
+            mma16816(acc[y][1], a[4], a[5], a[6], a[7], f0, f1);
+          }
         }
       }
     }
-    __syncwarp();            // the stage may be filled again
+    __syncwarp();            // the stages may be filled again
   }
   cp_async_wait<0>();
 
@@ -636,7 +738,10 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
       const int i0 = (int)(row / per);
       p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row == i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
     }
-    attend<T, D, true>(p, pc, slopes.v, sm,
+    Query<T, D> query;
+    query.load(p, pc);
+    Ring<T, D, 2> ring(p, pc, sm.ring[tid >> 5]);
+    attend<T, D, true>(p, pc, query, slopes.v, sm, ring, false,
                        whole ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D : nullptr,
                        p.part + (2 * (int64_t)blockIdx.x + (f == begin ? 0 : 1)) * part_floats<D>());
     f += pc.t1 - pc.t0;
@@ -750,6 +855,12 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   const bool none = pc.pos < 0 || pc.pos >= p.limit;
   if (none && tid == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
   pc.first = pc.pos;
+  Query<T, D> query;
+  query.load(p, pc);
+  Ring<T, D, 1> ring(p, pc, sm.ring[tid >> 5]);
+  // the newest tile is always needed: its copy need not wait for the bins
+  const bool ahead = share == 0 && !none;
+  if (ahead && tid < 32) ring.fetch(pc.pos >> 4, 0, ring.page_of(pc.pos >> 4));
   if (!none) {
     for (int k = tid; k < kHeads * p.s; k += kThreads) {
       const int h = k / p.s, x = k % p.s;
@@ -772,8 +883,8 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     for (int h = 0; h < pc.heads; ++h) pc.first = min(pc.first, sm.lo[h][0]);
     const int t_first = pc.first >> 4, n = (pc.pos >> 4) + 1 - t_first;
     const int len = (n + shares - 1) / shares;
-    pc.t0 = t_first + share * len;
-    pc.t1 = min(t_first + n, pc.t0 + len);
+    pc.t1 = t_first + n - share * len;             // share 0 the newest
+    pc.t0 = max(t_first, pc.t1 - len);
   }
   if (none || pc.t0 >= pc.t1) {
     if (shares == 1)
@@ -782,7 +893,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
       part[kHeads * D + tid] = -INFINITY, part[kHeads * D + kHeads + tid] = 0.f;
     return;
   }
-  attend<T, D, false>(p, pc, nullptr, sm, shares == 1 ? o : nullptr, part);
+  attend<T, D, false>(p, pc, query, nullptr, sm, ring, ahead, shares == 1 ? o : nullptr, part);
 }
 
 template <typename T, int D>
