@@ -85,7 +85,7 @@ struct DecodeParams {
   void* o;
   const int32_t* pos;
   int Hq, G;                        // query heads, of a KV head
-  int chunks;                       // CTAs that share a KV head's query heads
+  int chunks, per_chunk;            // a KV head's query heads in shares of at most kHeads
   const BinRecord* rec;
   int s;
   int64_t W;
@@ -106,23 +106,22 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// c += A (16 x 16, row) B (16 x 8), f16 operands, fp32 sums
+// c = A (16 x 16, row) B (16 x 8) + (first ? 0 : c): f16 operands (bf16 with
+// BF), fp32 sums
+template <bool BF>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// the same with bf16 operands
-__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                         uint32_t a3, uint32_t b0, uint32_t b1, bool first) {
+#define PLSH_MMA(TYPES)                                                                        \
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPES ".f32 {%0, %1, %2, %3}, "        \
+               "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"                             \
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                \
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first ? 0.f : c[0]), \
+                 "f"(first ? 0.f : c[1]), "f"(first ? 0.f : c[2]), "f"(first ? 0.f : c[3]))
+  if constexpr (BF)
+    PLSH_MMA("bf16.bf16");
+  else
+    PLSH_MMA("f16.f16");
+#undef PLSH_MMA
 }
 // transpose of an 8 x 8 matrix of 16-bit values, two per lane and row
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -167,7 +166,7 @@ template <typename T, int D>
 struct Smem {
   alignas(128) uint8_t ring[kWarps][kStages][Layout<D>::kTileBytes];
   float m[kWarps][kHeads], l[kWarps][kHeads];
-  float weight[kWarps][kHeads];        // of a warp's part of a head
+  float weight[2 * kWarps][kHeads];    // of a warp's column in its head
   int raw_lo[kHeads][kMaxS];
   int lo[kHeads][kMaxS];               // a head's bin starts, ascending
   int64_t scan[kThreads];
@@ -177,12 +176,12 @@ struct Smem {
 static_assert(kWarps * kHeads * 128 * 4 <= kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
 static_assert(kWarps * kHeads * 64 * 4 <= kWarps * kStages * Layout<64>::kTileBytes, "merge buffer");
 
-// Lane (g, t)'s values 8 t .. 8 t + 7 of every group of query head g.
-template <typename T, int D>
+// Lane (g, t)'s values 8 t .. 8 t + 7 of every group of column g's query head.
+template <typename T, int D, int PACK>
 struct Query {
   uint4 w[Layout<D>::kGroups][sizeof(T) / 2];
   __device__ void load(const DecodeParams& p, const Piece& pc) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, g = (lane >> 2) % (kHeads / PACK), t = lane & 3;
     const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + g) * D + 8 * t;
 #pragma unroll
     for (int y = 0; y < Layout<D>::kGroups; ++y)
@@ -202,10 +201,8 @@ struct Query {
   }
 };
 
-// A warp's ring of tiles of one piece.  The i-th tile is the piece's tile
-// number first + (i / PER) kWarps PER + i % PER from the newest down (ALiBi's
-// weights fall with the distance: the running maximum is met early).
-template <typename T, int D, int PER>
+// A warp's ring of tiles of one piece.
+template <typename T, int D>
 struct Ring {
   using L = Layout<D>;
   const uint8_t* head_data;
@@ -240,47 +237,58 @@ struct Ring {
 };
 
 // One piece; the result (all heads, the warps merged) goes to `o_row` (o of
-// head h0, divided by the row sums) or, when that is null, to `part`.  PER
-// tiles a step: the exact step's loop overhead is shared by two.  `ahead`: the
-// first warp's first tile is in its ring already, not yet committed.
-template <typename T, int D, bool EXACT, int PER>
-__device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Query<T, D>& query,
-                                       const float* slopes, Smem<T, D>& sm, Ring<T, D, PER>& ring,
+// head h0, divided by the row sums) or, when that is null, to `part`.
+// PACK = 1: a step takes one tile, its scores for eight heads in the eight
+// columns of the product.  PACK = 2 (at most four heads): a step takes two
+// tiles, the newer one's scores in columns 0 - 3 and the older one's in 4 - 7
+// (B is zero in the other tile's columns), so that what follows the products
+// (a lane holds two positions and two columns either way) is done once for
+// both.  Every column keeps a maximum, sums and accumulators of its own.
+// `ahead`: the first warp's first tile is in its ring already, not committed.
+template <typename T, int D, bool EXACT, int PACK>
+__device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Query<T, D, PACK>& query,
+                                       const float* slopes, Smem<T, D>& sm, Ring<T, D>& ring,
                                        bool ahead, T* o_row, float* part) {
   using L = Layout<D>;
   constexpr int Y = L::kGroups;
   constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
   constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
-  constexpr int kSteps = kStages / PER;         // steps that the ring holds
+  constexpr int kSteps = kStages / PACK;        // steps that the ring holds
+  constexpr int kCols = kHeads / PACK;          // columns of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int mine = PACK == 2 ? t >> 1 : 0;      // the tile whose scores this lane holds
+  const int head = (2 * t) % kCols;             // and its heads: head, head + 1
 
-  // ---- step i takes tiles newest - i kWarps PER - (0 .. PER - 1)
-  const int newest = pc.t1 - 1 - warp * PER;
-  const int steps = newest >= pc.t0 ? (newest - pc.t0) / (kWarps * PER) + 1 : 0;
-  auto tile_at = [&](int i, int u) { return newest - i * (kWarps * PER) - u; };
-  int32_t next_page[PER];
+  // ---- step i takes tiles newest - i kWarps PACK - (0 .. PACK - 1), from the
+  // newest down (ALiBi's weights fall with the distance: the running maximum
+  // is met early)
+  const int newest = pc.t1 - 1 - warp * PACK;
+  const int steps = newest >= pc.t0 ? (newest - pc.t0) / (kWarps * PACK) + 1 : 0;
+  auto tile_at = [&](int i, int u) { return newest - i * (kWarps * PACK) - u; };
+  int32_t next_page[PACK];
   {
-    int32_t pg[kSteps][PER];
+    int32_t pg[kSteps][PACK];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-      for (int u = 0; u < PER; ++u)
+      for (int u = 0; u < PACK; ++u)
         pg[i][u] = i < steps && tile_at(i, u) >= pc.t0 ? ring.page_of(tile_at(i, u)) : 0;
 #pragma unroll
     for (int i = 0; i < kSteps - 1; ++i) {
 #pragma unroll
-      for (int u = 0; u < PER; ++u)
+      for (int u = 0; u < PACK; ++u)
         if (i < steps && tile_at(i, u) >= pc.t0 && !(ahead && i == 0 && u == 0 && warp == 0))
-          ring.fetch(tile_at(i, u), i * PER + u, pg[i][u]);
+          ring.fetch(tile_at(i, u), i * PACK + u, pg[i][u]);
       cp_async_commit();
     }
 #pragma unroll
-    for (int u = 0; u < PER; ++u) next_page[u] = pg[kSteps - 1][u];
+    for (int u = 0; u < PACK; ++u) next_page[u] = pg[kSteps - 1][u];
   }
 
-  // ---- the queries as B operands; qlow takes the products of q's sums over a
-  // group with K's lo, a bf16 number: k slots 2 t, 2 t + 1 and 2 t + 8 hold
-  // group t's sum as three bf16 terms (24 bits)
+  // ---- the queries as B operands (lane (g, t) holds rows 2 t, 2 t + 1, ... of
+  // column g); qlow takes the products of q's sums over a group with K's lo, a
+  // bf16 number: k slots 2 t, 2 t + 1 and 2 t + 8 hold group t's sum as three
+  // bf16 terms (24 bits)
   uint32_t qa[Y][4], qb[kTwo ? Y : 1][4], qlow[2];
   float qscale[2];
   {
@@ -303,7 +311,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     const float scale = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
     qscale[0] = __shfl_sync(FULL, scale, 8 * t);
     qscale[1] = __shfl_sync(FULL, scale, 8 * t + 4);
-    float mine = 0.f;
+    float group = 0.f;
 #pragma unroll
     for (int y = 0; y < Y; ++y) {
       float sum = 0.f;
@@ -311,7 +319,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
       for (int i = 0; i < 8; ++i) sum += query.get(y, i);
       sum += __shfl_xor_sync(FULL, sum, 1);
       sum += __shfl_xor_sync(FULL, sum, 2);
-      if (y == t) mine = sum * norm;
+      if (y == t) group = sum * norm;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // odd codes are taken four bits up, as 16 c
@@ -324,20 +332,24 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         }
       }
     }
-    const float hi = __uint_as_float(__float_as_uint(mine) & 0xffff0000u);
-    const float mid = __uint_as_float(__float_as_uint(mine - hi) & 0xffff0000u);
+    const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
+    const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
     qlow[0] = pack_bf16(hi, mid);
-    qlow[1] = pack_bf16(mine - hi - mid, 0.f);
+    qlow[1] = pack_bf16(group - hi - mid, 0.f);
   }
+  // all ones where column g belongs to tile u
+  uint32_t keep[PACK];
+#pragma unroll
+  for (int u = 0; u < PACK; ++u) keep[u] = g / kCols == u ? 0xffffffffu : 0u;
   float slope[2] = {0.f, 0.f};
   int seen[2] = {p.s, p.s};        // bin starts at or before the last position of the tile
   if constexpr (EXACT) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) slope[k] = 2 * t + k < pc.heads ? slopes[pc.h0 + 2 * t + k] : 0.f;
+    for (int k = 0; k < 2; ++k) slope[k] = head + k < pc.heads ? slopes[pc.h0 + head + k] : 0.f;
   }
 
   // ---- the loop
-  float acc[Y][2][4];             // P V: values 32 y + 4 g + 2 tau + (r >> 1), heads 2 t + (r & 1)
+  float acc[Y][2][4];             // P V: values 32 y + 4 g + 2 tau + (r >> 1), columns 2 t + (r & 1)
   float low[Y][2];                // sum of p lo, this lane's positions
   float m[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
   float down[Y];                  // 2^-r of the group's weights
@@ -353,16 +365,16 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   // positions before `from` are unseen: by every head, or not of this piece
   const int from = max(pc.first, pc.t0 * kTile);
   const uint32_t k_at = ring.smem + g * (D / 2) + t * (D / 8);
-  const uint32_t pair_at = ring.smem + L::pair(g, 0);
+  const uint32_t pair_at = ring.smem + mine * L::kTileBytes + L::pair(g, 0);
   const uint32_t low_at = ring.smem + L::kKPairs + L::pair(g, t & (Y - 1));
   const uint32_t v_at = ring.smem + L::kV + 16 * lane;
   for (int i = 0, st = 0; i < steps; ++i, st = st == kSteps - 1 ? 0 : st + 1) {
     if (i + kSteps - 1 < steps) {
       const int before = st == 0 ? kSteps - 1 : st - 1;
 #pragma unroll
-      for (int u = 0; u < PER; ++u) {
+      for (int u = 0; u < PACK; ++u) {
         const int at = tile_at(i + kSteps - 1, u);
-        if (u == 0 || at >= pc.t0) ring.fetch(at, before * PER + u, next_page[u]);
+        if (u == 0 || at >= pc.t0) ring.fetch(at, before * PACK + u, next_page[u]);
         const int then = tile_at(i + kSteps, u);
         if (then >= pc.t0) next_page[u] = ring.page_of(then);
       }
@@ -371,123 +383,117 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     cp_async_wait<kSteps - 1>();
     __syncwarp();
 
-    // scores of positions j0 + g and j0 + g + 8, heads 2 t and 2 t + 1
-    float x[PER][4], cnt[PER][4];
-    uint32_t tops[Y];              // the largest pair of a group (by step), of this lane's
-    bool cut[PER];                 // some positions unseen by all: they may hold anything
-    // V's pairs of positions g and g + 8 of tile u, zero where no head sees them
-    auto v_pairs = [&](int u, uint32_t (&w0)[Y], uint32_t (&w1)[Y]) {
-      const uint32_t at = (uint32_t)((st * PER + u) * L::kTileBytes);
-      lds(pair_at + at + L::kVPairs, w0);
-      lds(pair_at + at + L::kVPairs + L::pair(8, 0), w1);
-      if (cut[u]) {
-        const bool gone = (ring.absent >> (st * PER + u)) & 1;
-        const int j = tile_at(i, u) * kTile + g;
-        const bool no0 = gone || j < from || j > pc.pos, no1 = gone || j + 8 < from || j + 8 > pc.pos;
+    // scores of positions j + g and j + g + 8 of the lane's tile, its two heads
+    const uint32_t at = (uint32_t)(st * PACK * L::kTileBytes);
+    const uint32_t gone = (ring.absent >> (st * PACK)) & ((1u << PACK) - 1);
+    const bool edge = tile_at(i, PACK - 1) * kTile < from || tile_at(i, 0) * kTile + kTile - 1 > pc.pos || gone;
+    auto unseen = [&](int u, int j) { return ((gone >> u) & 1) || j < from || j > pc.pos; };
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
+    {
+      uint32_t k0[PACK][Y], k1[PACK][Y], w0[Y], w1[Y];
 #pragma unroll
-        for (int y = 0; y < Y; ++y) {
-          if (no0) w0[y] = 0;
-          if (no1) w1[y] = 0;
-        }
+      for (int u = 0; u < PACK; ++u) {
+        lds(k_at + at + u * L::kTileBytes, k0[u]);
+        lds(k_at + at + u * L::kTileBytes + 4 * D, k1[u]);
       }
-    };
-#pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const uint32_t at = (uint32_t)((st * PER + u) * L::kTileBytes);
-      const int j0 = tile_at(i, u) * kTile;
-      const bool gone = (ring.absent >> (st * PER + u)) & 1;
-      uint32_t k0[Y], k1[Y], w0[Y], w1[Y];
-      lds(k_at + at, k0);
-      lds(k_at + at + 4 * D, k1);
       lds(pair_at + at + L::kKPairs, w0);
       lds(pair_at + at + L::kKPairs + L::pair(8, 0), w1);
-      float z[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        const uint32_t b0 = __byte_perm(ld_shared_u32(low_at + at), 0, 0x1010);
-        const uint32_t b1 = __byte_perm(ld_shared_u32(low_at + at + L::pair(8, 0)), 0, 0x1010);
-        mma16816_bf16(z, b0, b1, b0, b1, qlow[0], qlow[1]);
-      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[u][k] = 0.f;
+      for (int u = 0; u < PACK; ++u) {
+        const uint32_t lo_at = low_at + at + u * L::kTileBytes;
+        uint32_t b0 = __byte_perm(ld_shared_u32(lo_at), 0, 0x1010);
+        uint32_t b1 = __byte_perm(ld_shared_u32(lo_at + L::pair(8, 0)), 0, 0x1010);
+        if (PACK > 1 && edge) {
+          // a NaN of one tile would reach the other's columns as NaN times 0
+          if (unseen(u, tile_at(i, u) * kTile + g)) b0 = 0;
+          if (unseen(u, tile_at(i, u) * kTile + g + 8)) b1 = 0;
+        }
+        mma16816<true>(z, b0, b1, b0, b1, qlow[0] & keep[u], qlow[1] & keep[u], u == 0);
+      }
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t h0 = k0[y] >> 8, h1 = k1[y] >> 8;
-        const uint32_t a[8] = {k0[y] & 0x000f000fu, k1[y] & 0x000f000fu, k0[y] & 0x00f000f0u,
-                               k1[y] & 0x00f000f0u, h0 & 0x000f000fu,    h1 & 0x000f000fu,
-                               h0 & 0x00f000f0u,    h1 & 0x00f000f0u};
-        mma16816(c, a[0], a[1], a[2], a[3], qa[y][0], qa[y][1]);
-        mma16816(c, a[4], a[5], a[6], a[7], qa[y][2], qa[y][3]);
-        if constexpr (kTwo) {
-          mma16816(c, a[0], a[1], a[2], a[3], qb[y][0], qb[y][1]);
-          mma16816(c, a[4], a[5], a[6], a[7], qb[y][2], qb[y][3]);
+        float c[4];
+#pragma unroll
+        for (int u = 0; u < PACK; ++u) {
+          const uint32_t v0 = k0[u][y], v1 = k1[u][y], h0 = v0 >> 8, h1 = v1 >> 8;
+          const uint32_t a[8] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u,
+                                 v1 & 0x00f000f0u, h0 & 0x000f000fu, h1 & 0x000f000fu,
+                                 h0 & 0x00f000f0u, h1 & 0x00f000f0u};
+          mma16816<false>(c, a[0], a[1], a[2], a[3], qa[y][0] & keep[u], qa[y][1] & keep[u], u == 0);
+          mma16816<false>(c, a[4], a[5], a[6], a[7], qa[y][2] & keep[u], qa[y][3] & keep[u], false);
+          if constexpr (kTwo) {
+            mma16816<false>(c, a[0], a[1], a[2], a[3], qb[y][0] & keep[u], qb[y][1] & keep[u], false);
+            mma16816<false>(c, a[4], a[5], a[6], a[7], qb[y][2] & keep[u], qb[y][3] & keep[u], false);
+          }
         }
         const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
-        x[u][0] = fmaf(s0, c[0], x[u][0]);
-        x[u][1] = fmaf(s0, c[1], x[u][1]);
-        x[u][2] = fmaf(s1, c[2], x[u][2]);
-        x[u][3] = fmaf(s1, c[3], x[u][3]);
+        x[0] = fmaf(s0, c[0], x[0]);
+        x[1] = fmaf(s0, c[1], x[1]);
+        x[2] = fmaf(s1, c[2], x[2]);
+        x[3] = fmaf(s1, c[3], x[3]);
       }
-      // the mask's weights; -inf where a head does not see a position
-      if constexpr (EXACT) {
-        const float d0 = (float)(j0 + g - pc.pos), d1 = d0 + 8.f;
+    }
+    // the mask's weights; -inf where a head does not see a position
+    const int j = tile_at(i, mine) * kTile + g;
+    float cnt[4];
+    if constexpr (EXACT) {
+      const float d0 = (float)(j - pc.pos), d1 = d0 + 8.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          x[u][k] = fmaf(x[u][k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
-      } else {
-        // starts past the tile are behind us; those inside it count from
-        // their position on
-        int n[4];
-        bool inside = false;
+      for (int k = 0; k < 4; ++k)
+        x[k] = fmaf(x[k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
+    } else {
+      // starts past the tile are behind us; those inside it count from their
+      // position on
+      const int j0 = j - g;
+      int n[4];
+      bool inside = false;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int* lo = sm.lo[2 * t + k];
-          while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
-          n[k] = n[k + 2] = seen[k];
-          inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
-        }
-        if (__any_sync(FULL, inside)) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            for (int y = seen[k] - 1; y >= 0; --y) {
-              const int a = sm.lo[2 * t + k][y] - j0;
-              if (a <= 0) break;
-              n[k] -= a > g;
-              n[k + 2] -= a > g + 8;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          cnt[u][k] = (float)n[k];
-          x[u][k] = n[k] == 0 ? -INFINITY : fmaf(x[u][k], qscale[k & 1], z[k]);
-        }
+      for (int k = 0; k < 2; ++k) {
+        const int* lo = sm.lo[head + k];
+        while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
+        n[k] = n[k + 2] = seen[k];
+        inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
       }
-      cut[u] = gone || j0 < from || j0 + kTile - 1 > pc.pos;
-      if (cut[u]) {
-        const int j = j0 + g;
-        if (gone || j < from || j > pc.pos) x[u][0] = x[u][1] = -INFINITY;
-        if (gone || j + 8 < from || j + 8 > pc.pos) x[u][2] = x[u][3] = -INFINITY;
-      }
-      v_pairs(u, w0, w1);
+      if (__any_sync(FULL, inside)) {
 #pragma unroll
-      for (int y = 0; y < Y; ++y)
-        tops[y] = u == 0 ? max(w0[y], w1[y]) : max(tops[y], max(w0[y], w1[y]));
+        for (int k = 0; k < 2; ++k)
+          for (int y = seen[k] - 1; y >= 0; --y) {
+            const int a = sm.lo[head + k][y] - j0;
+            if (a <= 0) break;
+            n[k] -= a > g;
+            n[k + 2] -= a > g + 8;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        cnt[k] = (float)n[k];
+        x[k] = n[k] == 0 ? -INFINITY : fmaf(x[k], qscale[k & 1], z[k]);
+      }
+    }
+    uint32_t w0[Y], w1[Y];         // V's pairs of the lane's positions
+    lds(pair_at + at + L::kVPairs, w0);
+    lds(pair_at + at + L::kVPairs + L::pair(8, 0), w1);
+    if (edge) {
+      // positions that no head sees may hold anything
+      if (unseen(mine, j)) {
+        x[0] = x[1] = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) w0[y] = 0;
+      }
+      if (unseen(mine, j + 8)) {
+        x[2] = x[3] = -INFINITY;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) w1[y] = 0;
+      }
     }
     // does a score or a step outgrow what it is measured against?
-    float xs[2] = {fmaxf(x[0][0], x[0][2]), fmaxf(x[0][1], x[0][3])};
+    bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
 #pragma unroll
-    for (int u = 1; u < PER; ++u) {
-      xs[0] = fmaxf(xs[0], fmaxf(x[u][0], x[u][2]));
-      xs[1] = fmaxf(xs[1], fmaxf(x[u][1], x[u][3]));
-    }
-    bool grow = xs[0] > m[0] + kLazy || xs[1] > m[1] + kLazy;
-#pragma unroll
-    for (int y = 0; y < Y; ++y) grow |= tops[y] > most[y];
-    bool spoilt = false;           // a step that is not a number among the tiles
+    for (int y = 0; y < Y; ++y) grow |= max(w0[y], w1[y]) > most[y];
     if (__any_sync(FULL, grow)) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float to = max_rows(fmaxf(m[k], xs[k]));
+        const float to = max_rows(fmaxf(m[k], fmaxf(x[k], x[k + 2])));
         const float f = ex2(m[k] - to);
         m[k] = to;
         l[k] *= f;
@@ -500,23 +506,18 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
       }
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
-        uint32_t top = __reduce_max_sync(FULL, tops[y]);
-        if (top >= 0x7f800000u) {
-          spoilt = true;
-          top = 0;
+        // a step that is not a number: its group of the row of every head
+        // that gives the position a weight is none either
+        const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
+        if (nan0) w0[y] = 0;
+        if (nan1) w1[y] = 0;
 #pragma unroll
-          for (int u = 0; u < PER; ++u) {
-            uint32_t w0[Y], w1[Y];
-            v_pairs(u, w0, w1);
-            if (w0[y] < 0x7f800000u) top = max(top, w0[y]);
-            if (w1[y] < 0x7f800000u) top = max(top, w1[y]);
-          }
-          top = __reduce_max_sync(FULL, top);
-        }
+        for (int k = 0; k < 2; ++k)
+          if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
+        const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]));
         if (top > most[y]) {
           const int old = (int)(most[y] >> 23) - 132;          // most: 2^(r + 5)
-          // the largest step in [2^2, 2^3) 2^r
-          const int r = max((int)(top >> 23) - 129, -100);
+          const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
           const float f = most[y] == 0xffffu ? 0.f : pow2(old - r);
           down[y] = pow2(-r);
           most[y] = ((uint32_t)(r + 132) << 23) | 0xffffu;
@@ -525,62 +526,49 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         }
       }
     }
+    float pw[4];
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      const uint32_t at = (uint32_t)((st * PER + u) * L::kTileBytes);
-      uint32_t w0[Y], w1[Y];
-      v_pairs(u, w0, w1);
-      if (spoilt) {
-        // a step that is not a number: its group of the row of every head
-        // that gives the position a weight is none either
+    for (int k = 0; k < 4; ++k) {
+      pw[k] = ex2(x[k] - m[k & 1]);
+      if constexpr (!EXACT) pw[k] *= cnt[k];
+      l[k & 1] += pw[k];
+    }
+    // P V, group by group
 #pragma unroll
-        for (int y = 0; y < Y; ++y) {
-          const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
-          if (nan0) w0[y] = 0;
-          if (nan1) w1[y] = 0;
+    for (int yy = 0; yy < Y; yy += 2) {
+      uint4 v4[PACK];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if ((nan0 && x[u][k] != -INFINITY) || (nan1 && x[u][k + 2] != -INFINITY)) low[y][k] = NAN;
+      for (int u = 0; u < PACK; ++u) v4[u] = ld_shared_v4(v_at + at + u * L::kTileBytes + (yy >> 1) * 512);
+#pragma unroll
+      for (int y = yy; y < yy + 2; ++y) {
+        const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
+        low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
+        low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
+        const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
+        const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
+        uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
+        uint32_t f0 = 0, f1 = 0;
+        if constexpr (kTwo) {
+          const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
+          const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
+          f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
+          f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
         }
-      }
-      float pw[4];
+        e0 = transpose8x8(e0);
+        e1 = transpose8x8(e1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        pw[k] = ex2(x[u][k] - m[k & 1]);
-        if constexpr (!EXACT) pw[k] *= cnt[u][k];
-        l[k & 1] += pw[k];
-      }
-      // P V, group by group
-#pragma unroll
-      for (int yy = 0; yy < Y; yy += 2) {
-        const uint4 v4 = ld_shared_v4(v_at + at + (yy >> 1) * 512);
-#pragma unroll
-        for (int y = yy; y < yy + 2; ++y) {
-          const uint32_t v0 = y == yy ? v4.x : v4.z, v1 = y == yy ? v4.y : v4.w;
-          const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
-          low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
-          low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
-          const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
-          const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
-          uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
+        for (int u = 0; u < PACK; ++u) {
+          const uint32_t v0 = y == yy ? v4[u].x : v4[u].z, v1 = y == yy ? v4[u].y : v4[u].w;
           const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
           const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
                                  v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
                                  h1 & 0x000f000fu, h1 & 0x00f000f0u};
-          uint32_t f0 = 0, f1 = 0;
+          const uint32_t b[4] = {e0 & keep[u], e1 & keep[u], f0 & keep[u], f1 & keep[u]};
+          mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[0], b[1], false);
+          mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[0], b[1], false);
           if constexpr (kTwo) {
-            const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
-            const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
-            f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
-            f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
-          }
-          e0 = transpose8x8(e0);
-          e1 = transpose8x8(e1);
-          mma16816(acc[y][0], a[0], a[1], a[2], a[3], e0, e1);
-          mma16816(acc[y][1], a[4], a[5], a[6], a[7], e0, e1);
-          if constexpr (kTwo) {
-            mma16816(acc[y][0], a[0], a[1], a[2], a[3], f0, f1);
-            mma16816(acc[y][1], a[4], a[5], a[6], a[7], f0, f1);
+            mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[2], b[3], false);
+            mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[2], b[3], false);
           }
         }
       }
@@ -589,7 +577,9 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   }
   cp_async_wait<0>();
 
-  // ---- merge the warps
+  // ---- merge the warps' columns: head h has column h of every warp, and with
+  // PACK = 2 column h + 4
+  constexpr int kWays = kWarps * PACK;
   __syncthreads();           // every ring is done with
   float* merge = reinterpret_cast<float*>(sm.ring) + warp * kHeads * D;
 #pragma unroll
@@ -612,15 +602,18 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     }
   }
   __syncthreads();
-  if (threadIdx.x < kWarps * kHeads) {
-    const int h = threadIdx.x / kWarps, w = threadIdx.x % kWarps;
-    float mm = sm.m[w][h], ll = sm.l[w][h];
+  static_assert(kWarps * kHeads == 32, "a warp weighs the parts");
+  if (threadIdx.x < 32) {
+    const int h = threadIdx.x / kWays, w = threadIdx.x % kWays;
+    const int column = (w % PACK) * kCols + h;
+    const float mine = sm.m[w / PACK][column];
+    float mm = mine, ll = sm.l[w / PACK][column];
 #pragma unroll
-    for (int k = 1; k < kWarps; k <<= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
-    const float f = ll == 0.f ? 0.f : (sm.m[w][h] == mm ? 1.f : ex2(sm.m[w][h] - mm));
+    for (int k = 1; k < kWays; k <<= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
+    const float f = ll == 0.f ? 0.f : (mine == mm ? 1.f : ex2(mine - mm));
     ll = ll == 0.f ? 0.f : ll * f;
 #pragma unroll
-    for (int k = 1; k < kWarps; k <<= 1) ll += __shfl_xor_sync(FULL, ll, k);
+    for (int k = 1; k < kWays; k <<= 1) ll += __shfl_xor_sync(FULL, ll, k);
     // a row divides by its sum; one that sees nothing is 0
     sm.weight[w][h] = o_row == nullptr ? f : (ll == 0.f ? 0.f : __fdividef(f, ll));
     if (o_row == nullptr && w == 0 && h < pc.heads) {
@@ -634,9 +627,10 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     const int h = e / D;
     float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kWays; ++w) {
       const float f = sm.weight[w][h];
-      const float4 v = *reinterpret_cast<const float4*>(all + w * kHeads * D + e);
+      const float4 v = *reinterpret_cast<const float4*>(
+          all + (w / PACK * kHeads + w % PACK * kCols) * D + e);
       o[0] = fmaf(f, v.x, o[0]);
       o[1] = fmaf(f, v.y, o[1]);
       o[2] = fmaf(f, v.z, o[2]);
@@ -661,10 +655,10 @@ __device__ __forceinline__ int64_t row_tiles(const DecodeParams& p, int b) {
 
 // heads of unit u (a KV head and a share of its query heads)
 __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& pc) {
-  const int per = (p.G + p.chunks - 1) / p.chunks, c = u % p.chunks;
+  const int c = u % p.chunks;
   pc.kvh = u / p.chunks;
-  pc.h0 = pc.kvh * p.G + c * per;
-  pc.heads = min(per, p.G - c * per);
+  pc.h0 = pc.kvh * p.G + c * p.per_chunk;
+  pc.heads = min(p.per_chunk, p.G - c * p.per_chunk);
 }
 
 // Exact ALiBi.  The flat list of tiles runs over sequences, the units of a
@@ -672,7 +666,7 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& 
 // A row that lies within one CTA is finished there; of one that crosses CTAs,
 // each leaves a piece (slot 2 i when it begins with the CTA, else 2 i + 1),
 // and the CTA where it ends says in ends[i] which pieces to join.
-template <typename T, int D>
+template <typename T, int D, int PACK>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Slopes slopes) {
   extern __shared__ __align__(128) uint8_t raw[];
@@ -738,10 +732,10 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
       const int i0 = (int)(row / per);
       p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row == i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
     }
-    Query<T, D> query;
+    Query<T, D, PACK> query;
     query.load(p, pc);
-    Ring<T, D, 2> ring(p, pc, sm.ring[tid >> 5]);
-    attend<T, D, true>(p, pc, query, slopes.v, sm, ring, false,
+    Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
+    attend<T, D, true, PACK>(p, pc, query, slopes.v, sm, ring, false,
                        whole ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D : nullptr,
                        p.part + (2 * (int64_t)blockIdx.x + (f == begin ? 0 : 1)) * part_floats<D>());
     f += pc.t1 - pc.t0;
@@ -825,7 +819,7 @@ struct Groups {
   int ordered;                            // 0: index order, p.shares each
 };
 
-template <typename T, int D>
+template <typename T, int D, int PACK>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Groups gr) {
   extern __shared__ __align__(128) uint8_t raw[];
@@ -855,9 +849,9 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   const bool none = pc.pos < 0 || pc.pos >= p.limit;
   if (none && tid == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
   pc.first = pc.pos;
-  Query<T, D> query;
+  Query<T, D, PACK> query;
   query.load(p, pc);
-  Ring<T, D, 1> ring(p, pc, sm.ring[tid >> 5]);
+  Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
   // the newest tile is always needed: its copy need not wait for the bins
   const bool ahead = share == 0 && !none;
   if (ahead && tid < 32) ring.fetch(pc.pos >> 4, 0, ring.page_of(pc.pos >> 4));
@@ -893,7 +887,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
       part[kHeads * D + tid] = -INFINITY, part[kHeads * D + kHeads + tid] = 0.f;
     return;
   }
-  attend<T, D, false>(p, pc, query, nullptr, sm, ring, ahead, shares == 1 ? o : nullptr, part);
+  attend<T, D, false, PACK>(p, pc, query, nullptr, sm, ring, ahead, shares == 1 ? o : nullptr, part);
 }
 
 template <typename T, int D>
@@ -935,7 +929,6 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cuda
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-int chunks_of(int G) { return (G + kHeads - 1) / kHeads; }
 int max_ctas(int num_sms) { return num_sms * kCtasPerSm; }
 
 template <typename T, int D>
@@ -945,7 +938,7 @@ cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st
   const int64_t tiles = (int64_t)p.c.B * p.c.H * p.chunks * ((a.c.max_pages << a.c.page_shift) / kTile);
   const int64_t want = (tiles + kMinTiles - 1) / kMinTiles;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
-  auto kern = q4_exact_kernel<T, D>;
+  auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2> : q4_exact_kernel<T, D, 1>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
   if (e == cudaSuccess) e = launch(kern, dim3(grid), kThreads, sizeof(Smem<T, D>), st, p, s);
   if (e == cudaSuccess) e = launch(q4_exact_join_kernel<T, D>, dim3(grid, kHeads), 32 * kJoinWarps, 0, st, p);
@@ -993,7 +986,7 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
     }
     if (p.shares == 1 || grid <= 2 * max_ctas(a.num_sms)) break;
   }
-  auto kern = q4_approx_kernel<T, D>;
+  auto kern = p.per_chunk <= 4 ? q4_approx_kernel<T, D, 2> : q4_approx_kernel<T, D, 1>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
   if (e == cudaSuccess) e = launch(kern, dim3((unsigned)grid), kThreads, sizeof(Smem<T, D>), st, p, gr);
   if (e == cudaSuccess && p.shares > 1)
@@ -1021,7 +1014,8 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
   p.pos = a.pos;
   p.Hq = a.Hq;
   p.G = a.Hq / a.c.H;
-  p.chunks = chunks_of(p.G);
+  p.chunks = (p.G + kHeads - 1) / kHeads;
+  p.per_chunk = (p.G + p.chunks - 1) / p.chunks;
   p.rec = a.rec;
   p.s = a.s;
   p.W = a.W;

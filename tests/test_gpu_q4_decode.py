@@ -223,6 +223,33 @@ def test_nan_past_the_position_or_outside_the_bins_has_no_effect(which, dtype):
     bins.free()
 
 
+@pytest.mark.parametrize("heads", [(4, 4), (8, 2), (8, 1)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_what_was_never_written_has_no_effect(heads, d, dtype):
+    """Pages of zeros and pages of NaN around the same rows: the same bits.
+    The rows begin inside a tile, behind positions that no head sees."""
+    Hq, H = heads
+    s = Setup(2, Hq, H, d, 32, 130, dtype, seed=21)
+    pos, start = [93, 129], 21
+    starts = np.array([0, start, 131])            # the second bin: positions start ..
+    off = np.arange(0, 3 * Hq + 1, 3)
+    bins = plsh.bins_from_host(131, Hq, 1, off, np.tile(starts, Hq))
+    sigma = alibi_sigmas(Hq)
+    got = []
+    for fill in (0, 255):
+        s.cache.data.fill_(fill)
+        plsh.q4_cache_write(s.cache, s.k[:, :, :109].contiguous(), s.v[:, :, :109].contiguous(),
+                            i32([start] * 2), i32([93 - start + 1, 109]))
+        a = plsh.alibi_decode_q4(s.q, s.cache, bins, i32(pos))
+        plsh.q4_cache_write(s.cache, s.k, s.v, i32([0, 0]), i32([94, 130]))
+        got.append((a, plsh.alibi_exact_decode_q4(s.q, s.cache, sigma, i32(pos))))
+        plsh.stream_status()
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+    bins.free()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_a_query_that_is_not_finite_spoils_its_own_head_alone(bad):
     s = Setup(1, 4, 1, 64, 16, 100, "f32", seed=2)
