@@ -64,10 +64,10 @@ using namespace ptx;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 6;          // tiles of a warp's ring
+constexpr int kStages = 3;          // blocks of 32 positions in a warp's ring
 constexpr int kCtasPerSm = 3;
 constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
-constexpr int kMinTiles = 8;        // exact: tiles of a CTA at least
+constexpr int kMinBlocks = 4;       // exact: blocks of a CTA at least
 constexpr int kMaxShares = 64;      // approximate: CTAs of one row at most
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
@@ -99,24 +99,40 @@ struct DecodeParams {
 template <int D>
 __host__ __device__ constexpr int part_floats() { return kHeads * (D + 2); }
 
+// 16 bytes from src + OFF to dst + OFF
+template <int OFF>
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(dst), "l"(src), "n"(OFF)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// c = A (16 x 16, row) B (16 x 8) + (first ? 0 : c): f16 operands (bf16 with
-// BF), fp32 sums
+// c += A (16 x 16, row) B (16 x 8): f16 operands (bf16 with BF), fp32 sums
 template <bool BF>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1, bool first) {
-#define PLSH_MMA(TYPES)                                                                        \
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPES ".f32 {%0, %1, %2, %3}, "        \
-               "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"                             \
-               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                                \
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first ? 0.f : c[0]), \
-                 "f"(first ? 0.f : c[1]), "f"(first ? 0.f : c[2]), "f"(first ? 0.f : c[3]))
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+#define PLSH_MMA(TYPES)                                                                       \
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPES ".f32 {%0, %1, %2, %3}, "       \
+               "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"                                \
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])                               \
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+  if constexpr (BF)
+    PLSH_MMA("bf16.bf16");
+  else
+    PLSH_MMA("f16.f16");
+#undef PLSH_MMA
+}
+// c = A B
+template <bool BF>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1) {
+#define PLSH_MMA(TYPES)                                                                       \
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPES ".f32 {%0, %1, %2, %3}, "       \
+               "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"                            \
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])                               \
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f))
   if constexpr (BF)
     PLSH_MMA("bf16.bf16");
   else
@@ -145,18 +161,24 @@ __device__ __forceinline__ float max_rows(float v) {
 }
 
 // words of one lane: D / 32 consecutive 32-bit words of shared memory
-template <int N>
+template <int OFF, int N>
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
-    const uint4 v = ld_shared_v4(addr);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-  }
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr), "n"(OFF)
+                 : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "r"(addr), "n"(OFF)
+                 : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(addr), "n"(OFF) : "memory");
 }
 
-// What a CTA attends over: tiles [t0, t1) of sequence b, KV head kvh, for the
-// query heads h0 .. h0 + heads - 1.
+// What a CTA attends over: blocks [t0, t1) of 32 positions (two tiles) of
+// sequence b, KV head kvh, for the query heads h0 .. h0 + heads - 1.
 struct Piece {
   int b, kvh, h0, heads, pos, t0, t1;
   int first;         // first position any of the heads sees
@@ -164,7 +186,7 @@ struct Piece {
 
 template <typename T, int D>
 struct Smem {
-  alignas(128) uint8_t ring[kWarps][kStages][Layout<D>::kTileBytes];
+  alignas(128) uint8_t ring[kWarps][kStages][2 * Layout<D>::kTileBytes];
   float m[kWarps][kHeads], l[kWarps][kHeads];
   float weight[2 * kWarps][kHeads];    // of a warp's column in its head
   int raw_lo[kHeads][kMaxS];
@@ -173,8 +195,8 @@ struct Smem {
   int64_t found[2];
 };
 // the merge of the warps reuses the ring
-static_assert(kWarps * kHeads * 128 * 4 <= kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
-static_assert(kWarps * kHeads * 64 * 4 <= kWarps * kStages * Layout<64>::kTileBytes, "merge buffer");
+static_assert(kWarps * kHeads * 128 * 4 <= 2 * kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
+static_assert(kWarps * kHeads * 64 * 4 <= 2 * kWarps * kStages * Layout<64>::kTileBytes, "merge buffer");
 
 // Lane (g, t)'s values 8 t .. 8 t + 7 of every group of column g's query head.
 template <typename T, int D, int PACK>
@@ -201,50 +223,73 @@ struct Query {
   }
 };
 
-// A warp's ring of tiles of one piece.
+// Copies N bytes, 16 a lane and turn; dst and src are the lane's own.
+template <int N, int OFF = 0>
+__device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, int lane) {
+  if (OFF + 512 <= N || 16 * lane < N - OFF) cp_async16<OFF>(dst, src);
+  if constexpr (OFF + 512 < N) copy_async<N, OFF + 512>(dst, src, lane);
+}
+
+// A warp's ring of blocks of one piece.  A block's two tiles lie one after the
+// other in a page, except with pages of 16 positions.
 template <typename T, int D>
 struct Ring {
   using L = Layout<D>;
   const uint8_t* head_data;
   const int32_t* table;
   int64_t page_bytes;
-  int64_t pages;
+  uint32_t pages;
   uint32_t smem;
-  int log_tiles, lane;
-  uint32_t absent = 0;          // stages whose tile has no page
+  int log_blocks, last, lane;
+  uint32_t absent = 0;          // two bits a stage: tiles that have no page
   int* err;
   __device__ Ring(const DecodeParams& p, const Piece& pc, const void* ring)
-      : table(p.c.table + (int64_t)pc.b * p.c.max_pages), pages(p.c.pages), smem(smem_u32(ring)),
-        log_tiles(p.c.page_shift - 4), lane(threadIdx.x & 31), err(p.err) {
-    page_bytes = ((int64_t)p.c.H << log_tiles) * L::kTileBytes;
-    head_data = p.c.data + ((int64_t)pc.kvh << log_tiles) * L::kTileBytes + 16 * lane;
+      : table(p.c.table + (int64_t)pc.b * p.c.max_pages), pages((uint32_t)p.c.pages),
+        smem(smem_u32(ring)), log_blocks(p.c.page_shift - 5), last(pc.pos >> 4),
+        lane(threadIdx.x & 31), err(p.err) {
+    page_bytes = ((int64_t)p.c.H << (p.c.page_shift - 4)) * L::kTileBytes;
+    head_data = p.c.data + ((int64_t)pc.kvh << (p.c.page_shift - 4)) * L::kTileBytes + 16 * lane;
   }
-  __device__ int32_t page_of(int tile) const { return table[tile >> log_tiles]; }
-  __device__ void fetch(int tile, int st, int32_t pg) {
-    absent &= ~(1u << st);
-    if ((uint32_t)pg < (uint32_t)pages) {
-      const uint8_t* src = head_data + pg * page_bytes + (tile & ((1 << log_tiles) - 1)) * L::kTileBytes;
-      const uint32_t dst = smem + st * L::kTileBytes + 16 * lane;
-#pragma unroll
-      for (int k = 0; k < (L::kTileBytes + 511) / 512; ++k)
-        if (L::kTileBytes % 512 == 0 || 512 * k + 16 * lane < L::kTileBytes)
-          cp_async16(dst + 512 * k, src + 512 * k);
+  // the page of a block's first tile (and, in general, of its second)
+  __device__ int32_t page_of(int block) const {
+    return table[log_blocks >= 0 ? block >> log_blocks : 2 * block];
+  }
+  __device__ void fetch(int block, int st, int32_t pg) {
+    const uint32_t dst = smem + st * (2 * L::kTileBytes) + 16 * lane;
+    absent &= ~(3u << (2 * st));
+    if (log_blocks >= 0) {
+      if ((uint32_t)pg < pages)
+        copy_async<2 * L::kTileBytes>(
+            dst, head_data + pg * page_bytes + (block & ((1 << log_blocks) - 1)) * (2 * L::kTileBytes), lane);
+      else
+        absent |= 3u << (2 * st);
     } else {
-      absent |= 1u << st;
-      if (lane == 0) atomicOr(err, kErrCachePlace);
+      // the second tile's page is looked up only if the row reaches it
+      const int32_t pg1 = 2 * block + 1 <= last ? table[2 * block + 1] : -1;
+      if ((uint32_t)pg < pages)
+        copy_async<L::kTileBytes>(dst, head_data + pg * page_bytes, lane);
+      else
+        absent |= 1u << (2 * st);
+      if ((uint32_t)pg1 < pages)
+        copy_async<L::kTileBytes>(dst + L::kTileBytes, head_data + pg1 * page_bytes, lane);
+      else
+        absent |= 2u << (2 * st);
+      if (2 * block + 1 > last && (uint32_t)pg < pages) return;     // nothing that is needed is absent
     }
+    if (((absent >> (2 * st)) & 3u) && lane == 0) atomicOr(err, kErrCachePlace);
   }
 };
 
 // One piece; the result (all heads, the warps merged) goes to `o_row` (o of
 // head h0, divided by the row sums) or, when that is null, to `part`.
-// PACK = 1: a step takes one tile, its scores for eight heads in the eight
-// columns of the product.  PACK = 2 (at most four heads): a step takes two
-// tiles, the newer one's scores in columns 0 - 3 and the older one's in 4 - 7
-// (B is zero in the other tile's columns), so that what follows the products
-// (a lane holds two positions and two columns either way) is done once for
-// both.  Every column keeps a maximum, sums and accumulators of its own.
-// `ahead`: the first warp's first tile is in its ring already, not committed.
+// A step takes a block of two tiles.  PACK = 1: one after the other, the scores
+// of eight heads in the eight columns of the product.  PACK = 2 (at most four
+// heads): both at once, the first one's scores in columns 0 - 3 and the second
+// one's in 4 - 7 (B is zero in the other tile's columns), so that what follows
+// the products (a lane holds two positions and two columns either way) is done
+// once for both.  Every column keeps a maximum, sums and accumulators of its
+// own.  `ahead`: the first warp's first block is in its ring already, not yet
+// committed.
 template <typename T, int D, bool EXACT, int PACK>
 __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Query<T, D, PACK>& query,
                                        const float* slopes, Smem<T, D>& sm, Ring<T, D>& ring,
@@ -253,36 +298,26 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   constexpr int Y = L::kGroups;
   constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
   constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
-  constexpr int kSteps = kStages / PACK;        // steps that the ring holds
   constexpr int kCols = kHeads / PACK;          // columns of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int mine = PACK == 2 ? t >> 1 : 0;      // the tile whose scores this lane holds
   const int head = (2 * t) % kCols;             // and its heads: head, head + 1
 
-  // ---- step i takes tiles newest - i kWarps PACK - (0 .. PACK - 1), from the
-  // newest down (ALiBi's weights fall with the distance: the running maximum
-  // is met early)
-  const int newest = pc.t1 - 1 - warp * PACK;
-  const int steps = newest >= pc.t0 ? (newest - pc.t0) / (kWarps * PACK) + 1 : 0;
-  auto tile_at = [&](int i, int u) { return newest - i * (kWarps * PACK) - u; };
-  int32_t next_page[PACK];
+  // ---- step i takes block newest - i kWarps, from the newest down (ALiBi's
+  // weights fall with the distance: the running maximum is met early)
+  const int newest = pc.t1 - 1 - warp;
+  const int steps = newest >= pc.t0 ? (newest - pc.t0) / kWarps + 1 : 0;
+  int32_t next_page;
   {
-    int32_t pg[kSteps][PACK];
+    int32_t pg[kStages];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < kStages; ++i) pg[i] = i < steps ? ring.page_of(newest - i * kWarps) : 0;
 #pragma unroll
-      for (int u = 0; u < PACK; ++u)
-        pg[i][u] = i < steps && tile_at(i, u) >= pc.t0 ? ring.page_of(tile_at(i, u)) : 0;
-#pragma unroll
-    for (int i = 0; i < kSteps - 1; ++i) {
-#pragma unroll
-      for (int u = 0; u < PACK; ++u)
-        if (i < steps && tile_at(i, u) >= pc.t0 && !(ahead && i == 0 && u == 0 && warp == 0))
-          ring.fetch(tile_at(i, u), i * PACK + u, pg[i][u]);
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < steps && !(ahead && i == 0 && warp == 0)) ring.fetch(newest - i * kWarps, i, pg[i]);
       cp_async_commit();
     }
-#pragma unroll
-    for (int u = 0; u < PACK; ++u) next_page[u] = pg[kSteps - 1][u];
+    next_page = pg[kStages - 1];
   }
 
   // ---- the queries as B operands (lane (g, t) holds rows 2 t, 2 t + 1, ... of
@@ -337,7 +372,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     qlow[0] = pack_bf16(hi, mid);
     qlow[1] = pack_bf16(group - hi - mid, 0.f);
   }
-  // all ones where column g belongs to tile u
+  // all ones where column g belongs to tile u of the block
   uint32_t keep[PACK];
 #pragma unroll
   for (int u = 0; u < PACK; ++u) keep[u] = g / kCols == u ? 0xffffffffu : 0u;
@@ -362,218 +397,229 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[y][k >> 2][k & 3] = 0.f;
   }
-  // positions before `from` are unseen: by every head, or not of this piece
-  const int from = max(pc.first, pc.t0 * kTile);
   const uint32_t k_at = ring.smem + g * (D / 2) + t * (D / 8);
   const uint32_t pair_at = ring.smem + mine * L::kTileBytes + L::pair(g, 0);
-  const uint32_t low_at = ring.smem + L::kKPairs + L::pair(g, t & (Y - 1));
-  const uint32_t v_at = ring.smem + L::kV + 16 * lane;
-  for (int i = 0, st = 0; i < steps; ++i, st = st == kSteps - 1 ? 0 : st + 1) {
-    if (i + kSteps - 1 < steps) {
-      const int before = st == 0 ? kSteps - 1 : st - 1;
-#pragma unroll
-      for (int u = 0; u < PACK; ++u) {
-        const int at = tile_at(i + kSteps - 1, u);
-        if (u == 0 || at >= pc.t0) ring.fetch(at, before * PACK + u, next_page[u]);
-        const int then = tile_at(i + kSteps, u);
-        if (then >= pc.t0) next_page[u] = ring.page_of(then);
-      }
+  const uint32_t low_at = ring.smem + L::pair(g, t & (Y - 1));
+  const uint32_t v_at = ring.smem + 16 * lane;
+  for (int i = 0, st = 0; i < steps; ++i, st = st == kStages - 1 ? 0 : st + 1) {
+    const int block = newest - i * kWarps;
+    if (i + kStages - 1 < steps) {
+      ring.fetch(block - (kStages - 1) * kWarps, st == 0 ? kStages - 1 : st - 1, next_page);
+      if (i + kStages < steps) next_page = ring.page_of(block - kStages * kWarps);
     }
     cp_async_commit();
-    cp_async_wait<kSteps - 1>();
+    cp_async_wait<kStages - 1>();
     __syncwarp();
-
-    // scores of positions j + g and j + g + 8 of the lane's tile, its two heads
-    const uint32_t at = (uint32_t)(st * PACK * L::kTileBytes);
-    const uint32_t gone = (ring.absent >> (st * PACK)) & ((1u << PACK) - 1);
-    const bool edge = tile_at(i, PACK - 1) * kTile < from || tile_at(i, 0) * kTile + kTile - 1 > pc.pos || gone;
-    auto unseen = [&](int u, int j) { return ((gone >> u) & 1) || j < from || j > pc.pos; };
-    float x[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
-    {
-      uint32_t k0[PACK][Y], k1[PACK][Y], w0[Y], w1[Y];
-#pragma unroll
-      for (int u = 0; u < PACK; ++u) {
-        lds(k_at + at + u * L::kTileBytes, k0[u]);
-        lds(k_at + at + u * L::kTileBytes + 4 * D, k1[u]);
-      }
-      lds(pair_at + at + L::kKPairs, w0);
-      lds(pair_at + at + L::kKPairs + L::pair(8, 0), w1);
-#pragma unroll
-      for (int u = 0; u < PACK; ++u) {
-        const uint32_t lo_at = low_at + at + u * L::kTileBytes;
-        uint32_t b0 = __byte_perm(ld_shared_u32(lo_at), 0, 0x1010);
-        uint32_t b1 = __byte_perm(ld_shared_u32(lo_at + L::pair(8, 0)), 0, 0x1010);
-        if (PACK > 1 && edge) {
-          // a NaN of one tile would reach the other's columns as NaN times 0
-          if (unseen(u, tile_at(i, u) * kTile + g)) b0 = 0;
-          if (unseen(u, tile_at(i, u) * kTile + g + 8)) b1 = 0;
+    const uint32_t gone = (ring.absent >> (2 * st)) & 3u;
+    const bool edge = 32 * block < pc.first || 32 * block + 31 > pc.pos || gone;
+#pragma unroll 1
+    for (int sub = 2 / PACK - 1; sub >= 0; --sub) {
+      // scores of positions j and j + 8 of the lane's tile, its two heads
+      const uint32_t at = (uint32_t)((2 * st + sub) * L::kTileBytes);
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
+      {
+        uint32_t k0[PACK][Y], k1[PACK][Y], w0[Y], w1[Y];
+        lds<0>(k_at + at, k0[0]);
+        lds<4 * D>(k_at + at, k1[0]);
+        if constexpr (PACK == 2) {
+          lds<L::kTileBytes>(k_at + at, k0[1]);
+          lds<L::kTileBytes + 4 * D>(k_at + at, k1[1]);
         }
-        mma16816<true>(z, b0, b1, b0, b1, qlow[0] & keep[u], qlow[1] & keep[u], u == 0);
-      }
+        lds<L::kKPairs>(pair_at + at, w0);
+        lds<L::kKPairs + L::pair(8, 0)>(pair_at + at, w1);
+        // q's sums times lo: every column for every tile, and the lane takes its
+        // own tile's (a NaN of one tile must not reach the other's columns)
+        auto low_products = [&](auto tile, float (&c)[4]) {
+          constexpr int off = decltype(tile)::value * L::kTileBytes + L::kKPairs;
+          uint32_t b0[1], b1[1];
+          lds<off>(low_at + at, b0);
+          lds<off + L::pair(8, 0)>(low_at + at, b1);
+          b0[0] = __byte_perm(b0[0], 0, 0x1010);
+          b1[0] = __byte_perm(b1[0], 0, 0x1010);
+          mma16816_first<true>(c, b0[0], b1[0], b0[0], b1[0], qlow[0], qlow[1]);
+        };
+        low_products(std::integral_constant<int, 0>{}, z);
+        if constexpr (PACK == 2) {
+          float c[4];
+          low_products(std::integral_constant<int, 1>{}, c);
 #pragma unroll
-      for (int y = 0; y < Y; ++y) {
-        float c[4];
-#pragma unroll
-        for (int u = 0; u < PACK; ++u) {
-          const uint32_t v0 = k0[u][y], v1 = k1[u][y], h0 = v0 >> 8, h1 = v1 >> 8;
-          const uint32_t a[8] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u,
-                                 v1 & 0x00f000f0u, h0 & 0x000f000fu, h1 & 0x000f000fu,
-                                 h0 & 0x00f000f0u, h1 & 0x00f000f0u};
-          mma16816<false>(c, a[0], a[1], a[2], a[3], qa[y][0] & keep[u], qa[y][1] & keep[u], u == 0);
-          mma16816<false>(c, a[4], a[5], a[6], a[7], qa[y][2] & keep[u], qa[y][3] & keep[u], false);
-          if constexpr (kTwo) {
-            mma16816<false>(c, a[0], a[1], a[2], a[3], qb[y][0] & keep[u], qb[y][1] & keep[u], false);
-            mma16816<false>(c, a[4], a[5], a[6], a[7], qb[y][2] & keep[u], qb[y][3] & keep[u], false);
-          }
+          for (int k = 0; k < 4; ++k) z[k] = mine ? c[k] : z[k];
         }
-        const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
-        x[0] = fmaf(s0, c[0], x[0]);
-        x[1] = fmaf(s0, c[1], x[1]);
-        x[2] = fmaf(s1, c[2], x[2]);
-        x[3] = fmaf(s1, c[3], x[3]);
-      }
-    }
-    // the mask's weights; -inf where a head does not see a position
-    const int j = tile_at(i, mine) * kTile + g;
-    float cnt[4];
-    if constexpr (EXACT) {
-      const float d0 = (float)(j - pc.pos), d1 = d0 + 8.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        x[k] = fmaf(x[k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
-    } else {
-      // starts past the tile are behind us; those inside it count from their
-      // position on
-      const int j0 = j - g;
-      int n[4];
-      bool inside = false;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int* lo = sm.lo[head + k];
-        while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
-        n[k] = n[k + 2] = seen[k];
-        inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
-      }
-      if (__any_sync(FULL, inside)) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          for (int y = seen[k] - 1; y >= 0; --y) {
-            const int a = sm.lo[head + k][y] - j0;
-            if (a <= 0) break;
-            n[k] -= a > g;
-            n[k + 2] -= a > g + 8;
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        cnt[k] = (float)n[k];
-        x[k] = n[k] == 0 ? -INFINITY : fmaf(x[k], qscale[k & 1], z[k]);
-      }
-    }
-    uint32_t w0[Y], w1[Y];         // V's pairs of the lane's positions
-    lds(pair_at + at + L::kVPairs, w0);
-    lds(pair_at + at + L::kVPairs + L::pair(8, 0), w1);
-    if (edge) {
-      // positions that no head sees may hold anything
-      if (unseen(mine, j)) {
-        x[0] = x[1] = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < Y; ++y) w0[y] = 0;
-      }
-      if (unseen(mine, j + 8)) {
-        x[2] = x[3] = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < Y; ++y) w1[y] = 0;
-      }
-    }
-    // does a score or a step outgrow what it is measured against?
-    bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
-#pragma unroll
-    for (int y = 0; y < Y; ++y) grow |= max(w0[y], w1[y]) > most[y];
-    if (__any_sync(FULL, grow)) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float to = max_rows(fmaxf(m[k], fmaxf(x[k], x[k + 2])));
-        const float f = ex2(m[k] - to);
-        m[k] = to;
-        l[k] *= f;
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
-          low[y][k] *= f;
+          float c[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[y][e >> 1][2 * (e & 1) + k] *= f;
+          for (int u = 0; u < PACK; ++u) {
+            const uint32_t v0 = k0[u][y], v1 = k1[u][y], h0 = v0 >> 8, h1 = v1 >> 8;
+            const uint32_t a[8] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u,
+                                   v1 & 0x00f000f0u, h0 & 0x000f000fu, h1 & 0x000f000fu,
+                                   h0 & 0x00f000f0u, h1 & 0x00f000f0u};
+            if (u == 0)
+              mma16816_first<false>(c, a[0], a[1], a[2], a[3], qa[y][0] & keep[u], qa[y][1] & keep[u]);
+            else
+              mma16816<false>(c, a[0], a[1], a[2], a[3], qa[y][0] & keep[u], qa[y][1] & keep[u]);
+            mma16816<false>(c, a[4], a[5], a[6], a[7], qa[y][2] & keep[u], qa[y][3] & keep[u]);
+            if constexpr (kTwo) {
+              mma16816<false>(c, a[0], a[1], a[2], a[3], qb[y][0] & keep[u], qb[y][1] & keep[u]);
+              mma16816<false>(c, a[4], a[5], a[6], a[7], qb[y][2] & keep[u], qb[y][3] & keep[u]);
+            }
+          }
+          const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
+          x[0] = fmaf(s0, c[0], x[0]);
+          x[1] = fmaf(s0, c[1], x[1]);
+          x[2] = fmaf(s1, c[2], x[2]);
+          x[3] = fmaf(s1, c[3], x[3]);
         }
       }
+      // the mask's weights; -inf where a head does not see a position
+      const int j = 32 * block + (sub + mine) * kTile + g;
+      float cnt[4];
+      if constexpr (EXACT) {
+        const float d0 = (float)(j - pc.pos), d1 = d0 + 8.f;
 #pragma unroll
-      for (int y = 0; y < Y; ++y) {
-        // a step that is not a number: its group of the row of every head
-        // that gives the position a weight is none either
-        const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
-        if (nan0) w0[y] = 0;
-        if (nan1) w1[y] = 0;
+        for (int k = 0; k < 4; ++k)
+          x[k] = fmaf(x[k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
+      } else {
+        // starts past the tile are behind us; those inside it count from their
+        // position on
+        const int j0 = j - g;
+        int n[4];
+        bool inside = false;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
-        const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]));
-        if (top > most[y]) {
-          const int old = (int)(most[y] >> 23) - 132;          // most: 2^(r + 5)
-          const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
-          const float f = most[y] == 0xffffu ? 0.f : pow2(old - r);
-          down[y] = pow2(-r);
-          most[y] = ((uint32_t)(r + 132) << 23) | 0xffffu;
+        for (int k = 0; k < 2; ++k) {
+          const int* lo = sm.lo[head + k];
+          while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
+          n[k] = n[k + 2] = seen[k];
+          inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
+        }
+        if (__any_sync(FULL, inside)) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[y][e >> 2][e & 3] *= f;
+          for (int k = 0; k < 2; ++k)
+            for (int y = seen[k] - 1; y >= 0; --y) {
+              const int a = sm.lo[head + k][y] - j0;
+              if (a <= 0) break;
+              n[k] -= a > g;
+              n[k + 2] -= a > g + 8;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          cnt[k] = (float)n[k];
+          x[k] = n[k] == 0 ? -INFINITY : fmaf(x[k], qscale[k & 1], z[k]);
         }
       }
-    }
-    float pw[4];
+      uint32_t w0[Y], w1[Y];         // V's pairs of the lane's positions
+      lds<L::kVPairs>(pair_at + at, w0);
+      lds<L::kVPairs + L::pair(8, 0)>(pair_at + at, w1);
+      if (edge) {
+        __syncwarp();          // (a branch: selects would cost every step)
+        // positions that no head sees may hold anything
+        const bool none = (gone >> (sub + mine)) & 1;
+        if (none || j < pc.first || j > pc.pos) {
+          x[0] = x[1] = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      pw[k] = ex2(x[k] - m[k & 1]);
-      if constexpr (!EXACT) pw[k] *= cnt[k];
-      l[k & 1] += pw[k];
-    }
-    // P V, group by group
-#pragma unroll
-    for (int yy = 0; yy < Y; yy += 2) {
-      uint4 v4[PACK];
-#pragma unroll
-      for (int u = 0; u < PACK; ++u) v4[u] = ld_shared_v4(v_at + at + u * L::kTileBytes + (yy >> 1) * 512);
-#pragma unroll
-      for (int y = yy; y < yy + 2; ++y) {
-        const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
-        low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
-        low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
-        const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
-        const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
-        uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
-        uint32_t f0 = 0, f1 = 0;
-        if constexpr (kTwo) {
-          const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
-          const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
-          f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
-          f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
+          for (int y = 0; y < Y; ++y) w0[y] = 0;
         }
-        e0 = transpose8x8(e0);
-        e1 = transpose8x8(e1);
+        if (none || j + 8 < pc.first || j + 8 > pc.pos) {
+          x[2] = x[3] = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < PACK; ++u) {
-          const uint32_t v0 = y == yy ? v4[u].x : v4[u].z, v1 = y == yy ? v4[u].y : v4[u].w;
-          const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
-          const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
-                                 v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
-                                 h1 & 0x000f000fu, h1 & 0x00f000f0u};
-          const uint32_t b[4] = {e0 & keep[u], e1 & keep[u], f0 & keep[u], f1 & keep[u]};
-          mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[0], b[1], false);
-          mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[0], b[1], false);
+          for (int y = 0; y < Y; ++y) w1[y] = 0;
+        }
+      }
+      // does a score or a step outgrow what it is measured against?
+      bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
+#pragma unroll
+      for (int y = 0; y < Y; ++y) grow |= max(w0[y], w1[y]) > most[y];
+      if (__any_sync(FULL, grow)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float to = max_rows(fmaxf(m[k], fmaxf(x[k], x[k + 2])));
+          const float f = ex2(m[k] - to);
+          m[k] = to;
+          l[k] *= f;
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            low[y][k] *= f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[y][e >> 1][2 * (e & 1) + k] *= f;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          // a step that is not a number: its group of the row of every head
+          // that gives the position a weight is none either
+          const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
+          if (nan0) w0[y] = 0;
+          if (nan1) w1[y] = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
+          const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]));
+          if (top > most[y]) {
+            const int old = (int)(most[y] >> 23) - 132;          // most: 2^(r + 5)
+            const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
+            const float f = most[y] == 0xffffu ? 0.f : pow2(old - r);
+            down[y] = pow2(-r);
+            most[y] = ((uint32_t)(r + 132) << 23) | 0xffffu;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[y][e >> 2][e & 3] *= f;
+          }
+        }
+      }
+      float pw[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        pw[k] = ex2(x[k] - m[k & 1]);
+        if constexpr (!EXACT) pw[k] *= cnt[k];
+        l[k & 1] += pw[k];
+      }
+      // P V, group by group
+#pragma unroll
+      for (int yy = 0; yy < Y; yy += 2) {
+        uint32_t v4[PACK][4];
+        if (yy == 0) {
+          lds<L::kV>(v_at + at, v4[0]);
+          if constexpr (PACK == 2) lds<L::kV + L::kTileBytes>(v_at + at, v4[PACK - 1]);
+        } else {
+          lds<L::kV + 512>(v_at + at, v4[0]);
+          if constexpr (PACK == 2) lds<L::kV + 512 + L::kTileBytes>(v_at + at, v4[PACK - 1]);
+        }
+#pragma unroll
+        for (int y = yy; y < yy + 2; ++y) {
+          const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
+          low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
+          low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
+          const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
+          const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
+          uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
+          uint32_t f0 = 0, f1 = 0;
           if constexpr (kTwo) {
-            mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[2], b[3], false);
-            mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[2], b[3], false);
+            const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
+            const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
+            f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
+            f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
+          }
+          e0 = transpose8x8(e0);
+          e1 = transpose8x8(e1);
+#pragma unroll
+          for (int u = 0; u < PACK; ++u) {
+            const uint32_t v0 = v4[u][2 * (y - yy)], v1 = v4[u][2 * (y - yy) + 1];
+            const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
+            const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
+                                   v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
+                                   h1 & 0x000f000fu, h1 & 0x00f000f0u};
+            const uint32_t b[4] = {e0 & keep[u], e1 & keep[u], f0 & keep[u], f1 & keep[u]};
+            mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[0], b[1]);
+            mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[0], b[1]);
+            if constexpr (kTwo) {
+              mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[2], b[3]);
+              mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[2], b[3]);
+            }
           }
         }
       }
     }
-    __syncwarp();            // the stages may be filled again
+    __syncwarp();            // the stage may be filled again
   }
   cp_async_wait<0>();
 
@@ -646,11 +692,11 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   __syncthreads();           // before the next piece fills the rings
 }
 
-// Tiles that the row of sequence b takes (exact); a position out of range
+// Blocks that the row of sequence b takes (exact); a position out of range
 // takes none.
-__device__ __forceinline__ int64_t row_tiles(const DecodeParams& p, int b) {
+__device__ __forceinline__ int64_t row_blocks(const DecodeParams& p, int b) {
   const int pos = p.pos[b];
-  return pos < 0 || pos >= p.limit ? 0 : (pos >> 4) + 1;
+  return pos < 0 || pos >= p.limit ? 0 : (pos >> 5) + 1;
 }
 
 // heads of unit u (a KV head and a share of its query heads)
@@ -661,8 +707,8 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& 
   pc.heads = min(p.per_chunk, p.G - c * p.per_chunk);
 }
 
-// Exact ALiBi.  The flat list of tiles runs over sequences, the units of a
-// sequence, and the row's tiles; CTA i takes tiles [i per, (i + 1) per) of it.
+// Exact ALiBi.  The flat list of blocks runs over sequences, the units of a
+// sequence, and the row's blocks; CTA i takes blocks [i per, (i + 1) per).
 // A row that lies within one CTA is finished there; of one that crosses CTAs,
 // each leaves a piece (slot 2 i when it begins with the CTA, else 2 i + 1),
 // and the CTA where it ends says in ends[i] which pieces to join.
@@ -674,16 +720,16 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   grid_dep_wait();
   const int tid = threadIdx.x, units = p.c.H * p.chunks;
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
-    if (row_tiles(p, b) > 0) continue;
+    if (row_blocks(p, b) > 0) continue;
     if (tid == 0 && p.pos[b] >= 0) atomicOr(p.err, kErrCachePlace);
     for (int e = tid; e < p.Hq * D; e += kThreads)
       static_cast<T*>(p.o)[(int64_t)b * p.Hq * D + e] = Elem<T>::put(0.f);
   }
-  // prefix sums of the sequences' tiles, a run of sequences per thread
+  // prefix sums of the sequences' blocks, a run of sequences per thread
   const int each = (p.c.B + kThreads - 1) / kThreads;
   const int b0 = min(p.c.B, tid * each), b1 = min(p.c.B, b0 + each);
   int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += row_tiles(p, b);
+  for (int b = b0; b < b1; ++b) sum += row_blocks(p, b);
   sm.scan[tid] = sum;
   __syncthreads();
   for (int o = 1; o < kThreads; o <<= 1) {
@@ -694,7 +740,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   }
   const int64_t total = sm.scan[kThreads - 1] * units;
   const int64_t fair = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t per = fair < kMinTiles ? kMinTiles : fair;
+  const int64_t per = fair < kMinBlocks ? kMinBlocks : fair;
   const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
   if (tid == 0) p.ends[blockIdx.x].x = -1;
   if (begin >= end) return;
@@ -702,7 +748,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     int64_t at = sm.scan[tid] - sum;
     int b = b0;
     for (;; ++b) {
-      const int64_t n = row_tiles(p, b);
+      const int64_t n = row_blocks(p, b);
       if (begin < (at + n) * units) break;
       at += n;
     }
@@ -715,7 +761,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   pc.first = 0;
   int64_t base = sm.found[1];
   for (int64_t f = begin; f < end;) {
-    const int64_t n = row_tiles(p, pc.b), rel = f - base;
+    const int64_t n = row_blocks(p, pc.b), rel = f - base;
     if (rel >= n * units) {
       base += n * units;
       ++pc.b;
@@ -852,9 +898,10 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   Query<T, D, PACK> query;
   query.load(p, pc);
   Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
-  // the newest tile is always needed: its copy need not wait for the bins
-  const bool ahead = share == 0 && !none;
-  if (ahead && tid < 32) ring.fetch(pc.pos >> 4, 0, ring.page_of(pc.pos >> 4));
+  // the newest block is always needed, and with pages of 32 or more positions
+  // its page too: its copy need not wait for the bins
+  const bool ahead = share == 0 && !none && p.c.page_shift > 4;
+  if (ahead && tid < 32) ring.fetch(pc.pos >> 5, 0, ring.page_of(pc.pos >> 5));
   if (!none) {
     for (int k = tid; k < kHeads * p.s; k += kThreads) {
       const int h = k / p.s, x = k % p.s;
@@ -875,7 +922,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     }
     __syncthreads();
     for (int h = 0; h < pc.heads; ++h) pc.first = min(pc.first, sm.lo[h][0]);
-    const int t_first = pc.first >> 4, n = (pc.pos >> 4) + 1 - t_first;
+    const int t_first = pc.first >> 5, n = (pc.pos >> 5) + 1 - t_first;
     const int len = (n + shares - 1) / shares;
     pc.t1 = t_first + n - share * len;             // share 0 the newest
     pc.t0 = max(t_first, pc.t1 - len);
@@ -935,8 +982,8 @@ template <typename T, int D>
 cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
   Slopes s;
   for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
-  const int64_t tiles = (int64_t)p.c.B * p.c.H * p.chunks * ((a.c.max_pages << a.c.page_shift) / kTile);
-  const int64_t want = (tiles + kMinTiles - 1) / kMinTiles;
+  const int64_t blocks = (int64_t)p.c.B * p.c.H * p.chunks * ((p.limit + 31) / 32);
+  const int64_t want = (blocks + kMinBlocks - 1) / kMinBlocks;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
   auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2> : q4_exact_kernel<T, D, 1>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
