@@ -177,6 +177,14 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
     asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(addr), "n"(OFF) : "memory");
 }
 
+// the same with an offset that unrolling makes a constant
+__device__ __forceinline__ void lds_at(uint32_t addr, int off, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr + off)
+               : "memory");
+}
+
 // What a CTA attends over: blocks [t0, t1) of 32 positions (two tiles) of
 // sequence b, KV head kvh, for the query heads h0 .. h0 + heads - 1.
 struct Piece {
@@ -186,6 +194,8 @@ struct Piece {
 
 template <typename T, int D>
 struct Smem {
+  // the queries' B operands by lane (fp32: two terms), and zeros
+  alignas(128) uint4 q[sizeof(T) / 2][Layout<D>::kGroups][33];
   alignas(128) uint8_t ring[kWarps][kStages][2 * Layout<D>::kTileBytes];
   float m[kWarps][kHeads], l[kWarps][kHeads];
   float weight[2 * kWarps][kHeads];    // of a warp's column in its head
@@ -324,7 +334,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   // column g); qlow takes the products of q's sums over a group with K's lo, a
   // bf16 number: k slots 2 t, 2 t + 1 and 2 t + 8 hold group t's sum as three
   // bf16 terms (24 bits)
-  uint32_t qa[Y][4], qb[kTwo ? Y : 1][4], qlow[2];
+  uint32_t qlow[2];
   float qscale[2];
   {
     float mx = 0.f;
@@ -355,23 +365,33 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
       sum += __shfl_xor_sync(FULL, sum, 1);
       sum += __shfl_xor_sync(FULL, sum, 2);
       if (y == t) group = sum * norm;
+      if (warp == 0) {
+        uint32_t w[4], r[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // odd codes are taken four bits up, as 16 c
-        const float k = (i & 1) ? up * 0.0625f : up;
-        const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
-        qa[y][i] = pack_f16(a, b);
-        if constexpr (kTwo) {
-          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&qa[y][i]));
-          qb[y][i] = pack_f16(a - f.x, b - f.y);
+        for (int i = 0; i < 4; ++i) {
+          // odd codes are taken four bits up, as 16 c
+          const float k = (i & 1) ? up * 0.0625f : up;
+          const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
+          w[i] = pack_f16(a, b);
+          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
+          r[i] = pack_f16(a - f.x, b - f.y);
         }
+        sm.q[0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        if constexpr (kTwo) sm.q[1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
       }
     }
+    if (threadIdx.x < (int)sizeof(T) / 2 * Y) sm.q[threadIdx.x / Y][threadIdx.x % Y][32] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
     const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
     const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
     qlow[0] = pack_bf16(hi, mid);
     qlow[1] = pack_bf16(group - hi - mid, 0.f);
   }
+  // the lane's operands where column g belongs to tile u of the block, else zeros
+  uint32_t q_at[PACK];
+#pragma unroll
+  for (int u = 0; u < PACK; ++u) q_at[u] = smem_u32(&sm.q[0][0][g / kCols == u ? lane : 32]);
+  constexpr int kQ = 33 * 16;                   // bytes from a group's operands to the next's
   // all ones where column g belongs to tile u of the block
   uint32_t keep[PACK];
 #pragma unroll
@@ -412,7 +432,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     __syncwarp();
     const uint32_t gone = (ring.absent >> (2 * st)) & 3u;
     const bool edge = 32 * block < pc.first || 32 * block + 31 > pc.pos || gone;
-#pragma unroll 1
+#pragma unroll
     for (int sub = 2 / PACK - 1; sub >= 0; --sub) {
       // scores of positions j and j + 8 of the lane's tile, its two heads
       const uint32_t at = (uint32_t)((2 * st + sub) * L::kTileBytes);
@@ -454,14 +474,17 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
             const uint32_t a[8] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u,
                                    v1 & 0x00f000f0u, h0 & 0x000f000fu, h1 & 0x000f000fu,
                                    h0 & 0x00f000f0u, h1 & 0x00f000f0u};
+            uint32_t q[4];
+            lds_at(q_at[u], y * kQ, q);
             if (u == 0)
-              mma16816_first<false>(c, a[0], a[1], a[2], a[3], qa[y][0] & keep[u], qa[y][1] & keep[u]);
+              mma16816_first<false>(c, a[0], a[1], a[2], a[3], q[0], q[1]);
             else
-              mma16816<false>(c, a[0], a[1], a[2], a[3], qa[y][0] & keep[u], qa[y][1] & keep[u]);
-            mma16816<false>(c, a[4], a[5], a[6], a[7], qa[y][2] & keep[u], qa[y][3] & keep[u]);
+              mma16816<false>(c, a[0], a[1], a[2], a[3], q[0], q[1]);
+            mma16816<false>(c, a[4], a[5], a[6], a[7], q[2], q[3]);
             if constexpr (kTwo) {
-              mma16816<false>(c, a[0], a[1], a[2], a[3], qb[y][0] & keep[u], qb[y][1] & keep[u]);
-              mma16816<false>(c, a[4], a[5], a[6], a[7], qb[y][2] & keep[u], qb[y][3] & keep[u]);
+              lds_at(q_at[u], (Y + y) * kQ, q);
+              mma16816<false>(c, a[0], a[1], a[2], a[3], q[0], q[1]);
+              mma16816<false>(c, a[4], a[5], a[6], a[7], q[2], q[3]);
             }
           }
           const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
