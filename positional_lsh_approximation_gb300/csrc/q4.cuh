@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "plsh_internal.h"
+#include "tc_ptx.cuh"
 
 namespace plsh {
 namespace q4 {
@@ -71,6 +72,25 @@ template <> struct Elem<float> {
   __device__ static float get(float v) { return v; }
   __device__ static float put(float v) { return v; }
 };
+
+// Launches a kernel as a programmatic dependent of the one before it on the
+// stream: its launch overlaps that one's tail, and it waits for its end
+// (grid_dep_wait) before any access.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
 
 }  // namespace q4
 }  // namespace plsh

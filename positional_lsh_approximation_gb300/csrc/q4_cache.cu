@@ -3,7 +3,10 @@
 // A group of 32 values x is held as codes c and a pair (lo, step):
 //   lo = min x (down to bf16), step = (max x - lo) / 15 (up to bf16),
 //   c = rint((x - lo) / step) in 0..15,   value = lo + step c.
-// A thread per group.
+// Both are bound by the rows' bytes (2 or 4 a value, against 5 bits in the
+// cache).  A warp takes the rows of one tile (16 positions of one sequence and
+// head) of K or of V, so that what it touches is contiguous on both sides: the
+// tile's rows, and its codes and pairs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -15,86 +18,272 @@ namespace plsh {
 namespace {
 
 using namespace q4;
+using namespace ptx;
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr unsigned FULL = 0xffffffffu;
 
-struct RowGroup {
+// The warp's tile and the rows of it that the call names.
+struct TileRows {
   uint8_t* tile;
-  int64_t at;      // first value of the group in K / V
-  int r, y;
+  int64_t row0;        // row of [B, H, m] that position 0 of the tile would be
+  int r0, r1;          // positions [r0, r1) of the tile
+  bool value;          // V's part
 };
 
+// Tiles that m consecutive positions can touch.
+__host__ __device__ __forceinline__ int64_t tiles_of(int64_t m) { return (m + 2 * (kTile - 1)) / kTile; }
+
 template <int D>
-__device__ bool row_group(const Q4RowsArgs& a, RowGroup& g) {
-  const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = id / Layout<D>::kGroups;
-  if (row >= (int64_t)a.c.B * a.c.H * a.m) return false;
-  const int64_t i = row % a.m;
-  const int b = (int)(row / a.m / a.c.H), h = (int)(row / a.m % a.c.H);
-  if (a.len != nullptr && i >= a.len[b]) return false;
-  const int64_t p = (int64_t)a.pos[b] + i;
-  g.y = (int)(id % Layout<D>::kGroups);
-  g.at = row * D + g.y * kGroup;
-  g.r = (int)(p & 15);
-  g.tile = tile_of<D>(a.c, b, h, p, a.err);
-  return g.tile != nullptr;
+__device__ __forceinline__ bool tile_rows(const Q4RowsArgs& a, TileRows& w) {
+  const int64_t id = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  // (fewer than 2^31 tiles in a call)
+  const uint32_t tiles = (uint32_t)tiles_of(a.m), unit = (uint32_t)(id >> 1);
+  w.value = id & 1;
+  const uint32_t bh = unit / tiles;
+  if (bh >= (uint32_t)a.c.B * (uint32_t)a.c.H) return false;
+  const int b = (int)(bh / (uint32_t)a.c.H), h = (int)(bh - (uint32_t)b * a.c.H);
+  const int64_t len = a.len == nullptr ? a.m : min((int64_t)a.len[b], a.m);
+  const int64_t p0 = a.pos[b], start = ((p0 >> 4) + (int64_t)(unit - bh * tiles)) * kTile;   // the tile's first position
+  w.r0 = (int)max((int64_t)0, p0 - start);
+  w.r1 = (int)min((int64_t)kTile, p0 + len - start);
+  if (w.r0 >= w.r1) return false;
+  w.row0 = (int64_t)bh * a.m + (start - p0);
+  w.tile = tile_of<D>(a.c, b, h, start, a.err);
+  return w.tile != nullptr;
+}
+
+// Eight consecutive values of a row: 16 bytes of bf16, 32 of fp32.
+template <typename T> struct Eight {
+  uint4 w[sizeof(T) / 2];
+  __device__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+  __device__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+      const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(T) == 4) {
+          v[4 * k + e] = __uint_as_float(x[e]);
+        } else {
+          v[2 * e] = __uint_as_float(x[e] << 16);
+          v[2 * e + 1] = __uint_as_float(x[e] & 0xffff0000u);
+        }
+      }
+    }
+  }
+};
+
+// rint(d / step), the quotient rounded to fp32 first, for 0 <= d <= 15 step
+// (about), from the product t with the rounded reciprocal: t is within
+// 15 2^-23 + 2^-21 of that quotient, which matters next to a half h alone.
+// There d - h step is exact (h has five bits, step eight) and tells the side;
+// a quotient within 2^-19 of the half, but not on it, takes the division.
+__device__ __forceinline__ float code_of(float d, float t, float step) {
+  constexpr float kMagic = 12582912.f;            // 1.5 2^23: the sum rounds to an integer
+  float c = (t + kMagic) - kMagic;
+  if (fabsf(t - c) > 0.5f - 0x1p-18f) {
+    const float h = floorf(t) + 0.5f, r = fmaf(-h, step, d);
+    if (r == 0.f)
+      c = rintf(h);
+    else if (fabsf(r) < step * 0x1p-19f)
+      c = rintf(__fdiv_rn(d, step));
+    else
+      c = r > 0.f ? h + 0.5f : h - 0.5f;
+  }
+  return c;
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) q4_write_kernel(Q4RowsArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_constant__ Q4RowsArgs a) {
   using L = Layout<D>;
-  RowGroup g;
-  if (!row_group<D>(a, g)) return;
-  for (int which = 0; which < 2; ++which) {
-    const T* x = static_cast<const T*>(which ? a.V : a.K) + g.at;
-    float v[kGroup];
-    float mn = INFINITY, mx = -INFINITY;
-    bool nan = false;
-    for (int i = 0; i < kGroup; ++i) {
-      v[i] = Elem<T>::get(x[i]);
-      nan |= v[i] != v[i];
-      mn = fminf(mn, v[i]);
-      mx = fmaxf(mx, v[i]);
+  constexpr int kLanes = D / 8;                   // lanes of a row
+  constexpr int kRows = 32 / kLanes;              // rows of a pass
+  constexpr int kPasses = kTile / kRows;
+  __shared__ alignas(16) uint8_t stage_s[kWarps][10 * D];    // a whole tile's codes and pairs
+  grid_dep_wait();
+  TileRows w;
+  if (!tile_rows<D>(a, w)) return;
+  const int lane = threadIdx.x & 31, t = lane & 3, y = (lane % kLanes) >> 2, sub = lane / kLanes;
+  const T* src = static_cast<const T*>(w.value ? a.V : a.K) + w.row0 * D + (lane % kLanes) * 8;
+  uint8_t* stage = stage_s[threadIdx.x >> 5];
+  const bool whole = w.r0 == 0 && w.r1 == kTile;
+  Eight<T> raw[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = kRows * i + sub;
+    if (r >= w.r0 && r < w.r1) raw[i].load(src + (int64_t)r * D);
+  }
+  uint8_t* codes = w.tile + (w.value ? L::kV : 0);
+  uint8_t* pairs = w.tile + (w.value ? L::kVPairs : L::kKPairs);
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = kRows * i + sub;
+    const bool in = r >= w.r0 && r < w.r1;
+    if (!__any_sync(FULL, in)) continue;
+    float v[8];
+    raw[i].get(v);
+    float mn = v[0], mx = v[0];
+    bool nan = v[0] != v[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+      nan |= v[e] != v[e];
+      mn = fminf(mn, v[e]);
+      mx = fmaxf(mx, v[e]);
     }
-    const uint32_t w = make_pair(nan ? NAN : mn, mx);
-    const float lo = pair_lo(w), step = pair_step(w);
-    *reinterpret_cast<uint32_t*>(g.tile + (which ? L::kVPairs : L::kKPairs) + L::pair(g.r, g.y)) = w;
-    for (int i = 0; i < kGroup; i += 2) {
-      uint32_t c[2];
-      for (int e = 0; e < 2; ++e)
-        c[e] = step > 0.f ? (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(v[i + e] - lo, step)), 0.f), 15.f) : 0u;
-      g.tile[which ? L::v_code(g.r, g.y, i) : L::k_code(g.r, g.y, i)] = (uint8_t)(c[0] | (c[1] << 4));
+    if (nan) mn = NAN, mx = INFINITY;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const float mn2 = __shfl_xor_sync(FULL, mn, o), mx2 = __shfl_xor_sync(FULL, mx, o);
+      mn = fminf(mn, mn2);
+      mx = fmaxf(mx, mx2);
     }
+    const uint32_t pair = make_pair(mn, mx);
+    const float lo = pair_lo(pair), step = pair_step(pair);
+    // codes as two sums of four, exact in fp32 (16 bits), then as bits
+    uint32_t half[2] = {0, 0};
+    if (step > 0.f) {
+      // a step whose reciprocal, or its products, leave fp32's normal range
+      // (never in earnest) takes the division for every value
+      const bool plain = step > 0x1p-100f && step < 0x1p100f;
+      const float inv = __frcp_rn(step);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float d = v[4 * k + e] - lo;
+          c[e] = plain ? code_of(d, d * inv, step) : rintf(__fdiv_rn(d, step));
+        }
+        const float sum = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
+        half[k] = __float_as_uint(sum + 8388608.f) & 0xffffu;
+      }
+    }
+    const uint32_t word = half[0] | (half[1] << 16);
+    uint8_t* c_at = whole ? stage : codes;
+    uint8_t* p_at = whole ? stage + 8 * D : pairs;
+    if (!in) continue;
+    if (!w.value) {
+      *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * t)) = word;
+    } else {
+      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t) - L::kV) = (uint16_t)word;
+      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t + 4) - L::kV) = (uint16_t)(word >> 16);
+    }
+    if (t == 0) *reinterpret_cast<uint32_t*>(p_at + L::pair(r, y)) = pair;
+  }
+  if (whole) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k)
+      reinterpret_cast<uint4*>(codes)[32 * k + lane] = reinterpret_cast<const uint4*>(stage)[32 * k + lane];
+    if (lane < D / 8)
+      reinterpret_cast<uint4*>(pairs)[lane] = reinterpret_cast<const uint4*>(stage + 8 * D)[lane];
   }
 }
 
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+// the values of the codes in bits 16 half .. 16 half + 15 of w
+__device__ __forceinline__ void four_values(uint32_t w, int half, uint32_t pair, float (&v)[4]) {
+  const float lo = pair_lo(pair), step = pair_step(pair);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t c = (w >> (16 * half + 4 * e)) & 15u;
+    v[e] = fmaf(step, __uint_as_float(c | 0x4b000000u) - 8388608.f, lo);
+  }
+}
+
+template <int N> struct Words { uint32_t w[N]; };
+template <int N>
+__device__ __forceinline__ Words<N> load_words(const uint8_t* p) {
+  Words<N> r;
+  if constexpr (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = v.x, r.w[1] = v.y;
+  }
+  return r;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) q4_read_kernel(Q4RowsArgs a) {
+__global__ void __launch_bounds__(32 * kWarps) q4_read_kernel(const __grid_constant__ Q4RowsArgs a) {
   using L = Layout<D>;
-  RowGroup g;
-  if (!row_group<D>(a, g)) return;
-  for (int which = 0; which < 2; ++which) {
-    T* x = static_cast<T*>(const_cast<void*>(which ? a.V : a.K)) + g.at;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(
-        g.tile + (which ? L::kVPairs : L::kKPairs) + L::pair(g.r, g.y));
-    const float lo = pair_lo(w), step = pair_step(w);
-    for (int i = 0; i < kGroup; i += 2) {
-      const uint32_t c = g.tile[which ? L::v_code(g.r, g.y, i) : L::k_code(g.r, g.y, i)];
-      x[i] = Elem<T>::put(fmaf(step, (float)(c & 15u), lo));
-      x[i + 1] = Elem<T>::put(fmaf(step, (float)(c >> 4), lo));
+  constexpr int Y = L::kGroups;
+  grid_dep_wait();
+  TileRows w;
+  if (!tile_rows<D>(a, w)) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  T* dst = static_cast<T*>(const_cast<void*>(w.value ? a.V : a.K)) + w.row0 * D;
+  auto in = [&](int r) { return r >= w.r0 && r < w.r1; };
+  if (!w.value) {
+    // lane (g, t): values 8 t .. 8 t + 7 of every group of positions g, g + 8
+    Words<Y> c[2], p[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      c[k] = load_words<Y>(w.tile + L::k_code(g + 8 * k, 0, 8 * t));
+      p[k] = load_words<Y>(w.tile + L::kKPairs + L::pair(g + 8 * k, 0));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int y = 0; y < Y; ++y) {
+        float v[2][4];
+        four_values(c[k].w[y], 0, p[k].w[y], v[0]);
+        four_values(c[k].w[y], 1, p[k].w[y], v[1]);
+        if (!in(g + 8 * k)) continue;
+        T* out = dst + (int64_t)(g + 8 * k) * D + 32 * y + 8 * t;
+        if constexpr (sizeof(T) == 2) {
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[e >> 1][2 * (e & 1)], v[e >> 1][2 * (e & 1) + 1]);
+            b[e] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          *reinterpret_cast<uint4*>(out) = make_uint4(b[0], b[1], b[2], b[3]);
+        } else {
+          store4(out, v[0]);
+          store4(out + 4, v[1]);
+        }
+      }
+  } else {
+    // lane (g, t): values 4 g .. 4 g + 3 of every group of positions 2 t,
+    // 2 t + 1, 2 t + 8, 2 t + 9
+    uint4 c[Y / 2];
+#pragma unroll
+    for (int k = 0; k < Y / 2; ++k) c[k] = *reinterpret_cast<const uint4*>(w.tile + L::kV + 512 * k + 16 * lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 2 * t + (k & 1) + 8 * (k >> 1);
+      const Words<Y> p = load_words<Y>(w.tile + L::kVPairs + L::pair(r, 0));
+#pragma unroll
+      for (int y = 0; y < Y; ++y) {
+        const uint4& q = c[y >> 1];
+        const uint32_t word = (y & 1) ? ((k >> 1) ? q.w : q.z) : ((k >> 1) ? q.y : q.x);
+        float v[4];
+        four_values(word, k & 1, p.w[y], v);
+        if (in(r)) store4(dst + (int64_t)r * D + 32 * y + 4 * g, v);
+      }
     }
   }
 }
 
 template <typename T, int D>
 cudaError_t launch_rows(const Q4RowsArgs& a, bool write, cudaStream_t st) {
-  const int64_t groups = (int64_t)a.c.B * a.c.H * a.m * Layout<D>::kGroups;
-  const unsigned grid = (unsigned)((groups + kThreads - 1) / kThreads);
-  if (write)
-    q4_write_kernel<T, D><<<grid, kThreads, 0, st>>>(a);
-  else
-    q4_read_kernel<T, D><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  const int64_t warps = 2 * (int64_t)a.c.B * a.c.H * tiles_of(a.m);
+  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+  return launch_dependent(write ? q4_write_kernel<T, D> : q4_read_kernel<T, D>, dim3(grid),
+                          32 * kWarps, 0, st, a);
 }
 
 cudaError_t launch_any(const Q4RowsArgs& a, bool write, cudaStream_t st) {

@@ -67,7 +67,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;          // blocks of 32 positions in a warp's ring
 constexpr int kCtasPerSm = 3;
 constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
-constexpr int kMinBlocks = 4;       // exact: blocks of a CTA at least
+constexpr int kMinBlocks = 8;       // exact: blocks of a CTA at least
+constexpr int kRowCost = 12;        // exact: blocks that beginning and ending a row costs
 constexpr int kMaxShares = 64;      // approximate: CTAs of one row at most
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
@@ -196,13 +197,15 @@ template <typename T, int D>
 struct Smem {
   // the queries' B operands by lane (fp32: two terms), and zeros
   alignas(128) uint4 q[sizeof(T) / 2][Layout<D>::kGroups][33];
+  uint2 qlow[32];
+  float scale[kHeads];
   alignas(128) uint8_t ring[kWarps][kStages][2 * Layout<D>::kTileBytes];
   float m[kWarps][kHeads], l[kWarps][kHeads];
-  float weight[2 * kWarps][kHeads];    // of a warp's column in its head
+  float weight[2 * kWarps][kHeads + 1];    // of a warp's column in its head
+  unsigned some[kHeads];               // which of them saw anything (NaN too)
   int raw_lo[kHeads][kMaxS];
   int lo[kHeads][kMaxS];               // a head's bin starts, ascending
-  int64_t scan[kThreads];
-  int64_t found[2];
+  int64_t split[4];                    // exact: entries, entries of a CTA, first sequence and its first entry
 };
 // the merge of the warps reuses the ring
 static_assert(kWarps * kHeads * 128 * 4 <= 2 * kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
@@ -213,6 +216,7 @@ template <typename T, int D, int PACK>
 struct Query {
   uint4 w[Layout<D>::kGroups][sizeof(T) / 2];
   __device__ void load(const DecodeParams& p, const Piece& pc) {
+    if (threadIdx.x >= 32) return;         // the first warp prepares it for all
     const int lane = threadIdx.x & 31, g = (lane >> 2) % (kHeads / PACK), t = lane & 3;
     const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + g) * D + 8 * t;
 #pragma unroll
@@ -334,9 +338,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   // column g); qlow takes the products of q's sums over a group with K's lo, a
   // bf16 number: k slots 2 t, 2 t + 1 and 2 t + 8 hold group t's sum as three
   // bf16 terms (24 bits)
-  uint32_t qlow[2];
-  float qscale[2];
-  {
+  if (warp == 0) {
     float mx = 0.f;
     bool bad = false;
 #pragma unroll
@@ -353,9 +355,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
     const float up = pow2(14 - e);
     const float norm = kLog2e / sqrtf((float)D);
-    const float scale = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
-    qscale[0] = __shfl_sync(FULL, scale, 8 * t);
-    qscale[1] = __shfl_sync(FULL, scale, 8 * t + 4);
+    if (t == 0) sm.scale[g] = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
     float group = 0.f;
 #pragma unroll
     for (int y = 0; y < Y; ++y) {
@@ -365,28 +365,27 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
       sum += __shfl_xor_sync(FULL, sum, 1);
       sum += __shfl_xor_sync(FULL, sum, 2);
       if (y == t) group = sum * norm;
-      if (warp == 0) {
-        uint32_t w[4], r[4];
+      uint32_t w[4], r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // odd codes are taken four bits up, as 16 c
-          const float k = (i & 1) ? up * 0.0625f : up;
-          const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
-          w[i] = pack_f16(a, b);
-          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
-          r[i] = pack_f16(a - f.x, b - f.y);
-        }
-        sm.q[0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
-        if constexpr (kTwo) sm.q[1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
+      for (int i = 0; i < 4; ++i) {
+        // odd codes are taken four bits up, as 16 c
+        const float k = (i & 1) ? up * 0.0625f : up;
+        const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
+        w[i] = pack_f16(a, b);
+        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
+        r[i] = pack_f16(a - f.x, b - f.y);
       }
+      sm.q[0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (kTwo) sm.q[1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    if (threadIdx.x < (int)sizeof(T) / 2 * Y) sm.q[threadIdx.x / Y][threadIdx.x % Y][32] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+    if (lane < (int)sizeof(T) / 2 * Y) sm.q[lane / Y][lane % Y][32] = make_uint4(0, 0, 0, 0);
     const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
     const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
-    qlow[0] = pack_bf16(hi, mid);
-    qlow[1] = pack_bf16(group - hi - mid, 0.f);
+    sm.qlow[lane] = make_uint2(pack_bf16(hi, mid), pack_bf16(group - hi - mid, 0.f));
   }
+  __syncthreads();
+  const uint32_t qlow[2] = {sm.qlow[lane].x, sm.qlow[lane].y};
+  const float qscale[2] = {sm.scale[2 * t], sm.scale[2 * t + 1]};
   // the lane's operands where column g belongs to tile u of the block, else zeros
   uint32_t q_at[PACK];
 #pragma unroll
@@ -651,41 +650,56 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   constexpr int kWays = kWarps * PACK;
   __syncthreads();           // every ring is done with
   float* merge = reinterpret_cast<float*>(sm.ring) + warp * kHeads * D;
+  if (steps > 0) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float sum = sum_rows(l[k]);
-    if (g == 0) {
-      sm.m[warp][2 * t + k] = m[k];
-      sm.l[warp][2 * t + k] = sum;
-    }
+    for (int k = 0; k < 2; ++k) {
+      const float sum = sum_rows(l[k]);
+      if (g == 0) {
+        sm.m[warp][2 * t + k] = m[k];
+        sm.l[warp][2 * t + k] = sum;
+      }
 #pragma unroll
-    for (int y = 0; y < Y; ++y) {
-      const float b = sum_rows(low[y][k]);
-      const float up = most[y] == 0xffffu ? 0.f : pow2((int)(most[y] >> 23) - 132);
-      float4 v;
-      v.x = fmaf(acc[y][0][k] * 0x1p24f, up, b);
-      v.y = fmaf(acc[y][0][2 + k] * 0x1p20f, up, b);
-      v.z = fmaf(acc[y][1][k] * 0x1p24f, up, b);
-      v.w = fmaf(acc[y][1][2 + k] * 0x1p20f, up, b);
-      *reinterpret_cast<float4*>(merge + (2 * t + k) * D + 32 * y + 4 * g) = v;
+      for (int y = 0; y < Y; ++y) {
+        const float b = sum_rows(low[y][k]);
+        const float up = most[y] == 0xffffu ? 0.f : pow2((int)(most[y] >> 23) - 132);
+        float4 v;
+        v.x = fmaf(acc[y][0][k] * 0x1p24f, up, b);
+        v.y = fmaf(acc[y][0][2 + k] * 0x1p20f, up, b);
+        v.z = fmaf(acc[y][1][k] * 0x1p24f, up, b);
+        v.w = fmaf(acc[y][1][2 + k] * 0x1p20f, up, b);
+        *reinterpret_cast<float4*>(merge + (2 * t + k) * D + 32 * y + 4 * g) = v;
+      }
     }
+  } else if (lane < kHeads) {
+    sm.m[warp][lane] = kNothing;
+    sm.l[warp][lane] = 0.f;
   }
   __syncthreads();
-  static_assert(kWarps * kHeads == 32, "a warp weighs the parts");
-  if (threadIdx.x < 32) {
-    const int h = threadIdx.x / kWays, w = threadIdx.x % kWays;
-    const int column = (w % PACK) * kCols + h;
-    const float mine = sm.m[w / PACK][column];
-    float mm = mine, ll = sm.l[w / PACK][column];
+  if (threadIdx.x < kCols) {
+    // a thread per head weighs its columns; a row divides by its sum, and one
+    // that sees nothing is 0
+    const int h = threadIdx.x;
+    float mm = kNothing, ll = 0.f, mw[kWays], lw[kWays];
+    unsigned some = 0;
 #pragma unroll
-    for (int k = 1; k < kWays; k <<= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
-    const float f = ll == 0.f ? 0.f : (mine == mm ? 1.f : ex2(mine - mm));
-    ll = ll == 0.f ? 0.f : ll * f;
+    for (int w = 0; w < kWays; ++w) {
+      const int column = w % PACK * kCols + h;
+      mw[w] = sm.m[w / PACK][column];
+      lw[w] = sm.l[w / PACK][column];
+      mm = fmaxf(mm, mw[w]);
+    }
 #pragma unroll
-    for (int k = 1; k < kWays; k <<= 1) ll += __shfl_xor_sync(FULL, ll, k);
-    // a row divides by its sum; one that sees nothing is 0
-    sm.weight[w][h] = o_row == nullptr ? f : (ll == 0.f ? 0.f : __fdividef(f, ll));
-    if (o_row == nullptr && w == 0 && h < pc.heads) {
+    for (int w = 0; w < kWays; ++w) {
+      if (lw[w] == 0.f) continue;
+      some |= 1u << w;
+      mw[w] = ex2(mw[w] - mm);
+      ll = fmaf(mw[w], lw[w], ll);
+    }
+    sm.some[h] = some;
+    const float over = o_row == nullptr ? 1.f : 1.f / ll;
+#pragma unroll
+    for (int w = 0; w < kWays; ++w) sm.weight[w][h] = mw[w] * over;
+    if (o_row == nullptr && h < pc.heads) {
       part[kHeads * D + h] = mm;
       part[kHeads * D + kHeads + h] = ll;
     }
@@ -695,15 +709,17 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   for (int e = 4 * threadIdx.x; e < pc.heads * D; e += 4 * kThreads) {
     const int h = e / D;
     float o[4] = {0.f, 0.f, 0.f, 0.f};
+    const unsigned some = sm.some[h];
 #pragma unroll
     for (int w = 0; w < kWays; ++w) {
+      const bool in = (some >> w) & 1;         // else the buffer holds anything
       const float f = sm.weight[w][h];
       const float4 v = *reinterpret_cast<const float4*>(
           all + (w / PACK * kHeads + w % PACK * kCols) * D + e);
-      o[0] = fmaf(f, v.x, o[0]);
-      o[1] = fmaf(f, v.y, o[1]);
-      o[2] = fmaf(f, v.z, o[2]);
-      o[3] = fmaf(f, v.w, o[3]);
+      o[0] = in ? fmaf(f, v.x, o[0]) : o[0];
+      o[1] = in ? fmaf(f, v.y, o[1]) : o[1];
+      o[2] = in ? fmaf(f, v.z, o[2]) : o[2];
+      o[3] = in ? fmaf(f, v.w, o[3]) : o[3];
     }
     if (o_row == nullptr)
       *reinterpret_cast<float4*>(part + e) = make_float4(o[0], o[1], o[2], o[3]);
@@ -730,11 +746,12 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& 
   pc.heads = min(p.per_chunk, p.G - c * p.per_chunk);
 }
 
-// Exact ALiBi.  The flat list of blocks runs over sequences, the units of a
-// sequence, and the row's blocks; CTA i takes blocks [i per, (i + 1) per).
-// A row that lies within one CTA is finished there; of one that crosses CTAs,
-// each leaves a piece (slot 2 i when it begins with the CTA, else 2 i + 1),
-// and the CTA where it ends says in ends[i] which pieces to join.
+// Exact ALiBi.  The flat list runs over sequences, the units of a sequence,
+// and a row's blocks, each row preceded by kRowCost entries that stand for the
+// time a row takes to begin and end; CTA i takes entries [i per, (i + 1) per).
+// A row whose blocks lie within one CTA is finished there; of one that crosses
+// CTAs, each leaves a piece (slot 2 i when it is the CTA's first, else
+// 2 i + 1), and the CTA where it ends says in ends[i] which pieces to join.
 template <typename T, int D, int PACK>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Slopes slopes) {
@@ -748,118 +765,151 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     for (int e = tid; e < p.Hq * D; e += kThreads)
       static_cast<T*>(p.o)[(int64_t)b * p.Hq * D + e] = Elem<T>::put(0.f);
   }
-  // prefix sums of the sequences' blocks, a run of sequences per thread
-  const int each = (p.c.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.c.B, tid * each), b1 = min(p.c.B, b0 + each);
-  int64_t sum = 0;
-  for (int b = b0; b < b1; ++b) sum += row_blocks(p, b);
-  sm.scan[tid] = sum;
-  __syncthreads();
-  for (int o = 1; o < kThreads; o <<= 1) {
-    const int64_t v = tid >= o ? sm.scan[tid - o] : 0;
-    __syncthreads();
-    sm.scan[tid] += v;
-    __syncthreads();
-  }
-  const int64_t total = sm.scan[kThreads - 1] * units;
-  const int64_t fair = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t per = fair < kMinBlocks ? kMinBlocks : fair;
-  const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
-  if (tid == 0) p.ends[blockIdx.x].x = -1;
-  if (begin >= end) return;
-  if (begin >= (sm.scan[tid] - sum) * units && begin < sm.scan[tid] * units) {
-    int64_t at = sm.scan[tid] - sum;
-    int b = b0;
-    for (;; ++b) {
-      const int64_t n = row_blocks(p, b);
-      if (begin < (at + n) * units) break;
-      at += n;
+  // prefix sums of the sequences' entries, a run of sequences per thread of
+  // the first warp
+  auto row_entries = [&](int b) -> int64_t {
+    const int64_t n = row_blocks(p, b);
+    return n == 0 ? 0 : n + kRowCost;
+  };
+  if (tid < 32) {
+    const int each = (p.c.B + 31) / 32;
+    const int b0 = min(p.c.B, tid * each), b1 = min(p.c.B, b0 + each);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) sum += row_entries(b);
+    int64_t upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(FULL, upto, o);
+      if (tid >= o) upto += v;
     }
-    sm.found[0] = b;
-    sm.found[1] = at * units;
+    const int64_t total = __shfl_sync(FULL, upto, 31) * units;
+    const int64_t fair = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t per = fair < kMinBlocks ? kMinBlocks : fair;
+    const int64_t begin = blockIdx.x * per;
+    if (tid == 0) {
+      p.ends[blockIdx.x].x = -1;
+      sm.split[0] = total;
+      sm.split[1] = per;
+    }
+    if (begin < total && begin >= (upto - sum) * units && begin < upto * units) {
+      int64_t at = upto - sum;
+      int b = b0;
+      for (;; ++b) {
+        const int64_t n = row_entries(b);
+        if (begin < (at + n) * units) break;
+        at += n;
+      }
+      sm.split[2] = b;
+      sm.split[3] = at * units;
+    }
   }
   __syncthreads();
+  const int64_t total = sm.split[0], per = sm.split[1];
+  const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
+  if (begin >= end) return;
   Piece pc;
-  pc.b = (int)sm.found[0];
+  pc.b = (int)sm.split[2];
   pc.first = 0;
-  int64_t base = sm.found[1];
+  int64_t base = sm.split[3];
+  int slot = 2 * blockIdx.x;
   for (int64_t f = begin; f < end;) {
-    const int64_t n = row_blocks(p, pc.b), rel = f - base;
+    const int64_t n = row_entries(pc.b), rel = f - base;
     if (rel >= n * units) {
       base += n * units;
       ++pc.b;
       continue;
     }
     const int u = (int)(rel / n);
+    const int64_t row = base + u * n, till = min(end, row + n);     // [row, row + n): its entries
     pc.pos = p.pos[pc.b];
-    pc.t0 = (int)(rel - u * n);
-    pc.t1 = (int)min(n, pc.t0 + (end - f));
+    pc.t0 = (int)max((int64_t)0, f - row - kRowCost);
+    pc.t1 = (int)(till - row - kRowCost);
+    f = till;
+    if (pc.t1 <= pc.t0) continue;                 // the row's cost alone
     unit_heads(p, u, pc);
-    const bool whole = pc.t0 == 0 && pc.t1 == n;
-    if (tid == 0 && pc.t0 > 0 && pc.t1 == n) {
-      const int64_t row = f - pc.t0;              // where the row begins
-      const int i0 = (int)(row / per);
-      p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row == i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
+    const bool last = till == row + n;
+    if (tid == 0 && pc.t0 > 0 && last) {
+      const int i0 = (int)((row + kRowCost) / per);    // the CTA of its first block
+      p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row <= i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
     }
     Query<T, D, PACK> query;
     query.load(p, pc);
     Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
     attend<T, D, true, PACK>(p, pc, query, slopes.v, sm, ring, false,
-                       whole ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D : nullptr,
-                       p.part + (2 * (int64_t)blockIdx.x + (f == begin ? 0 : 1)) * part_floats<D>());
-    f += pc.t1 - pc.t0;
+                             pc.t0 == 0 && last ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D
+                                                : nullptr,
+                             p.part + (int64_t)slot * part_floats<D>());
+    slot = 2 * blockIdx.x + 1;
   }
 }
 
 // One head of a row from its pieces: slot `first`, then first2 + step k, n
-// pieces in all.  A warp takes every kJoinWarps-th piece, a lane D / 32 values.
-constexpr int kJoinWarps = 4;
+// pieces in all.  A warp takes every kJoinWarps-th piece, kJoinAhead of them
+// in flight (the kernel is one round of loads long where that covers them), a
+// lane D / 32 values; the warps join in shared memory.
+constexpr int kJoinWarps = 8, kJoinAhead = 4;
 template <typename T, int D>
 __device__ void join_pieces(const DecodeParams& p, int first, int first2, int step, int n, int h,
                             T* o) {
   constexpr int V = D / 32;
   __shared__ float acc_s[kJoinWarps][D];
-  __shared__ float l_s[kJoinWarps];
+  __shared__ float m_s[kJoinWarps], l_s[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int k) {
-    return p.part + (int64_t)(k == 0 ? first : first2 + step * (k - 1)) * part_floats<D>();
-  };
-  float mm = -INFINITY;
-  for (int k = lane; k < n; k += 32) mm = fmaxf(mm, slot(k)[kHeads * D + h]);
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
-  float ll = 0.f, acc[V];
+  float mm = kNothing, ll = 0.f, acc[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int k = warp; k < n; k += kJoinWarps) {
-    const float* pt = slot(k);
-    const float mk = pt[kHeads * D + h], lk = pt[kHeads * D + kHeads + h];
-    float v[V];
-    if constexpr (V == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(pt + h * D + 4 * lane);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(pt + h * D + 2 * lane);
-      v[0] = x.x, v[1] = x.y;
-    }
-    const float f = mk == mm ? 1.f : ex2(mk - mm);
-    if (lk != 0.f) {                   // else nothing of the piece was seen, or written
-      ll = fmaf(f, lk, ll);
+  for (int k0 = warp; k0 < n; k0 += kJoinWarps * kJoinAhead) {
+    float mk[kJoinAhead], lk[kJoinAhead], v[kJoinAhead][V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+    for (int a = 0; a < kJoinAhead; ++a) {
+      const int k = k0 + a * kJoinWarps;
+      mk[a] = kNothing;
+      lk[a] = 0.f;
+      if (k >= n) continue;
+      const float* pt = p.part + (int64_t)(k == 0 ? first : first2 + step * (k - 1)) * part_floats<D>();
+      mk[a] = pt[kHeads * D + h];
+      lk[a] = pt[kHeads * D + kHeads + h];
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(pt + h * D + 4 * lane);
+        v[a][0] = x.x, v[a][1] = x.y, v[a][2] = x.z, v[a][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(pt + h * D + 2 * lane);
+        v[a][0] = x.x, v[a][1] = x.y;
+      }
+    }
+    float to = mm;
+#pragma unroll
+    for (int a = 0; a < kJoinAhead; ++a) to = fmaxf(to, mk[a]);
+    const float f0 = ex2(mm - to);
+    mm = to;
+    ll *= f0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int a = 0; a < kJoinAhead; ++a) {
+      if (lk[a] == 0.f) continue;          // nothing of the piece was seen, or written
+      const float f = ex2(mk[a] - mm);
+      ll = fmaf(f, lk[a], ll);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, v[a][e], acc[e]);
     }
   }
 #pragma unroll
   for (int e = 0; e < V; ++e) acc_s[warp][V * lane + e] = acc[e];
-  if (lane == 0) l_s[warp] = ll;
+  if (lane == 0) {
+    m_s[warp] = mm;
+    l_s[warp] = ll;
+  }
   __syncthreads();
   if (threadIdx.x < D) {
-    float sum = 0.f, a = 0.f;
+    float to = m_s[0], sum = 0.f, a = 0.f;
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) to = fmaxf(to, m_s[w]);
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-      sum += l_s[w];
-      a += acc_s[w][threadIdx.x];
+      const float f = ex2(m_s[w] - to);
+      sum = fmaf(f, l_s[w], sum);
+      a = fmaf(f, acc_s[w][threadIdx.x], a);
     }
     o[threadIdx.x] = Elem<T>::put(sum == 0.f ? 0.f : a / sum);
   }
@@ -954,7 +1004,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     if (shares == 1)
       for (int e = tid; e < pc.heads * D; e += kThreads) o[e] = Elem<T>::put(0.f);
     else if (tid < kHeads)
-      part[kHeads * D + tid] = -INFINITY, part[kHeads * D + kHeads + tid] = 0.f;
+      part[kHeads * D + tid] = kNothing, part[kHeads * D + kHeads + tid] = 0.f;
     return;
   }
   attend<T, D, false, PACK>(p, pc, query, nullptr, sm, ring, ahead, shares == 1 ? o : nullptr, part);
@@ -981,37 +1031,19 @@ q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_const
                     static_cast<T*>(p.o) + ((int64_t)b * p.Hq + pc.h0 + h) * D);
 }
 
-// Each kernel a programmatic dependent of the one before it: its launch
-// overlaps that one's tail, and it waits for its end before any access.
-template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                   const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 int max_ctas(int num_sms) { return num_sms * kCtasPerSm; }
 
 template <typename T, int D>
 cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
   Slopes s;
   for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
-  const int64_t blocks = (int64_t)p.c.B * p.c.H * p.chunks * ((p.limit + 31) / 32);
-  const int64_t want = (blocks + kMinBlocks - 1) / kMinBlocks;
+  const int64_t entries = (int64_t)p.c.B * p.c.H * p.chunks * ((p.limit + 31) / 32 + kRowCost);
+  const int64_t want = (entries + kMinBlocks - 1) / kMinBlocks;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
   auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2> : q4_exact_kernel<T, D, 1>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
-  if (e == cudaSuccess) e = launch(kern, dim3(grid), kThreads, sizeof(Smem<T, D>), st, p, s);
-  if (e == cudaSuccess) e = launch(q4_exact_join_kernel<T, D>, dim3(grid, kHeads), 32 * kJoinWarps, 0, st, p);
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), kThreads, sizeof(Smem<T, D>), st, p, s);
+  if (e == cudaSuccess) e = launch_dependent(q4_exact_join_kernel<T, D>, dim3(grid, p.per_chunk), 32 * kJoinWarps, 0, st, p);
   return e;
 }
 
@@ -1058,9 +1090,9 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
   }
   auto kern = p.per_chunk <= 4 ? q4_approx_kernel<T, D, 2> : q4_approx_kernel<T, D, 1>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
-  if (e == cudaSuccess) e = launch(kern, dim3((unsigned)grid), kThreads, sizeof(Smem<T, D>), st, p, gr);
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3((unsigned)grid), kThreads, sizeof(Smem<T, D>), st, p, gr);
   if (e == cudaSuccess && p.shares > 1)
-    e = launch(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), kHeads), 32 * kJoinWarps, 0, st, p, gr);
+    e = launch_dependent(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), p.per_chunk), 32 * kJoinWarps, 0, st, p, gr);
   return e;
 }
 
