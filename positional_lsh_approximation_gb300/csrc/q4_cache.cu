@@ -53,14 +53,25 @@ __device__ __forceinline__ bool tile_rows(const Q4RowsArgs& a, TileRows& w) {
   return w.tile != nullptr;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Eight consecutive values of a row: 16 bytes of bf16, 32 of fp32.
 template <typename T> struct Eight {
   uint4 w[sizeof(T) / 2];
-  __device__ void load(const T* p) {
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
     for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
   }
-  __device__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
     for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
       const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
@@ -75,26 +86,70 @@ template <typename T> struct Eight {
       }
     }
   }
+  // smallest and largest of the eight; NaN if one is NaN
+  __device__ __forceinline__ void range(const float (&v)[8], float& mn, float& mx) const {
+    if constexpr (sizeof(T) == 4) {
+      mn = mx = v[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) {
+        mn = min_nan(mn, v[e]);
+        mx = max_nan(mx, v[e]);
+      }
+    } else {
+      const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+      const __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(x[0], x[1]), __hmin2_nan(x[2], x[3]));
+      const __nv_bfloat162 hi = __hmax2_nan(__hmax2_nan(x[0], x[1]), __hmax2_nan(x[2], x[3]));
+      mn = min_nan(__low2float(lo), __high2float(lo));
+      mx = max_nan(__low2float(hi), __high2float(hi));
+    }
+  }
 };
 
-// rint(d / step), the quotient rounded to fp32 first, for 0 <= d <= 15 step
-// (about), from the product t with the rounded reciprocal: t is within
-// 15 2^-23 + 2^-21 of that quotient, which matters next to a half h alone.
-// There d - h step is exact (h has five bits, step eight) and tells the side;
-// a quotient within 2^-19 of the half, but not on it, takes the division.
-__device__ __forceinline__ float code_of(float d, float t, float step) {
+// Four codes as one number of 16 bits: c0 + 16 c1 + 256 c2 + 4096 c3, exact in
+// fp32, and as the low bits of its sum with 2^23.
+__device__ __forceinline__ uint32_t four_codes(const float* c) {
+  const float sum = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
+  return __float_as_uint(sum + 8388608.f) & 0xffffu;
+}
+
+// The codes of four values (d = x - lo) from the definition: the quotient
+// rounded to fp32, then to the nearest integer.
+__device__ __noinline__ uint32_t codes_by_division(float d0, float d1, float d2, float d3, float step) {
+  const float c[4] = {rintf(__fdiv_rn(d0, step)), rintf(__fdiv_rn(d1, step)),
+                      rintf(__fdiv_rn(d2, step)), rintf(__fdiv_rn(d3, step))};
+  return four_codes(c);
+}
+
+// The same from products with the rounded reciprocal, within 15 2^-23 + 2^-21
+// of the quotients, which matters next to a half alone.  There the remainder
+// e = d - c step is exact (c has four bits, step eight) and tells the side, or
+// the tie, which goes to the even code; a quotient within 2^-19 of a half but
+// not on it takes the division, and so does a step whose reciprocal or
+// products leave fp32's normal range.
+__device__ __forceinline__ uint32_t codes_of(const float* v, float lo, float step, float inv) {
   constexpr float kMagic = 12582912.f;            // 1.5 2^23: the sum rounds to an integer
-  float c = (t + kMagic) - kMagic;
-  if (fabsf(t - c) > 0.5f - 0x1p-18f) {
-    const float h = floorf(t) + 0.5f, r = fmaf(-h, step, d);
-    if (r == 0.f)
-      c = rintf(h);
-    else if (fabsf(r) < step * 0x1p-19f)
-      c = rintf(__fdiv_rn(d, step));
-    else
-      c = r > 0.f ? h + 0.5f : h - 0.5f;
+  float d[4], c[4], off = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    d[e] = v[e] - lo;
+    const float t = d[e] * inv;
+    c[e] = (t + kMagic) - kMagic;
+    off = fmaxf(off, fabsf(t - c[e]));
   }
-  return c;
+  if (!(off <= 0.5f - 0x1p-18f) || !(step > 0x1p-100f && step < 0x1p100f)) {
+    bool close = !(step > 0x1p-100f && step < 0x1p100f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float r = fmaf(-c[e], step, d[e]), past = fabsf(r) - 0.5f * step;
+      if (past == 0.f)
+        c[e] = rintf(c[e] + copysignf(0.5f, r));
+      else if (past > 0.f)
+        c[e] += copysignf(1.f, r);
+      close |= past != 0.f && fabsf(past) < step * 0x1p-19f;
+    }
+    if (close) return codes_by_division(d[0], d[1], d[2], d[3], step);
+  }
+  return four_codes(c);
 }
 
 template <typename T, int D>
@@ -102,7 +157,7 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
   using L = Layout<D>;
   constexpr int kLanes = D / 8;                   // lanes of a row
   constexpr int kRows = 32 / kLanes;              // rows of a pass
-  constexpr int kPasses = kTile / kRows;
+  constexpr int kAhead = 2;                       // passes whose rows are in flight
   __shared__ alignas(16) uint8_t stage_s[kWarps][10 * D];    // a whole tile's codes and pairs
   grid_dep_wait();
   TileRows w;
@@ -111,66 +166,47 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
   const T* src = static_cast<const T*>(w.value ? a.V : a.K) + w.row0 * D + (lane % kLanes) * 8;
   uint8_t* stage = stage_s[threadIdx.x >> 5];
   const bool whole = w.r0 == 0 && w.r1 == kTile;
-  Eight<T> raw[kPasses];
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = kRows * i + sub;
-    if (r >= w.r0 && r < w.r1) raw[i].load(src + (int64_t)r * D);
-  }
   uint8_t* codes = w.tile + (w.value ? L::kV : 0);
   uint8_t* pairs = w.tile + (w.value ? L::kVPairs : L::kKPairs);
+  uint8_t* c_at = whole ? stage : codes;
+  uint8_t* p_at = whole ? stage + 8 * D : pairs;
+  const int first = w.r0 / kRows * kRows;
+  Eight<T> raw[kAhead];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int r = kRows * i + sub;
-    const bool in = r >= w.r0 && r < w.r1;
-    if (!__any_sync(FULL, in)) continue;
-    float v[8];
-    raw[i].get(v);
-    float mn = v[0], mx = v[0];
-    bool nan = v[0] != v[0];
+  for (int k = 0; k < kAhead; ++k) {
+    const int r = first + k * kRows + sub;
+    if (r >= w.r0 && r < w.r1) raw[k].load(src + (int64_t)r * D);
+  }
+  // (not unrolled: eight passes of it would not stay in the instruction cache)
+#pragma unroll 1
+  for (int r = first + sub; r - sub < w.r1; r += kRows) {
+    const Eight<T> now = raw[0];
 #pragma unroll
-    for (int e = 1; e < 8; ++e) {
-      nan |= v[e] != v[e];
-      mn = fminf(mn, v[e]);
-      mx = fmaxf(mx, v[e]);
-    }
-    if (nan) mn = NAN, mx = INFINITY;
+    for (int k = 1; k < kAhead; ++k) raw[k - 1] = raw[k];
+    const int then = r + kAhead * kRows;
+    if (then < w.r1) raw[kAhead - 1].load(src + (int64_t)then * D);
+    float v[8], mn, mx;
+    now.get(v);
+    now.range(v, mn, mx);
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-      const float mn2 = __shfl_xor_sync(FULL, mn, o), mx2 = __shfl_xor_sync(FULL, mx, o);
-      mn = fminf(mn, mn2);
-      mx = fmaxf(mx, mx2);
+      mn = min_nan(mn, __shfl_xor_sync(FULL, mn, o));
+      mx = max_nan(mx, __shfl_xor_sync(FULL, mx, o));
     }
+    if (r < w.r0 || r >= w.r1) continue;
     const uint32_t pair = make_pair(mn, mx);
     const float lo = pair_lo(pair), step = pair_step(pair);
-    // codes as two sums of four, exact in fp32 (16 bits), then as bits
     uint32_t half[2] = {0, 0};
     if (step > 0.f) {
-      // a step whose reciprocal, or its products, leave fp32's normal range
-      // (never in earnest) takes the division for every value
-      const bool plain = step > 0x1p-100f && step < 0x1p100f;
       const float inv = __frcp_rn(step);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float c[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float d = v[4 * k + e] - lo;
-          c[e] = plain ? code_of(d, d * inv, step) : rintf(__fdiv_rn(d, step));
-        }
-        const float sum = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
-        half[k] = __float_as_uint(sum + 8388608.f) & 0xffffu;
-      }
+      half[0] = codes_of(v, lo, step, inv);
+      half[1] = codes_of(v + 4, lo, step, inv);
     }
-    const uint32_t word = half[0] | (half[1] << 16);
-    uint8_t* c_at = whole ? stage : codes;
-    uint8_t* p_at = whole ? stage + 8 * D : pairs;
-    if (!in) continue;
     if (!w.value) {
-      *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * t)) = word;
+      *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * t)) = half[0] | (half[1] << 16);
     } else {
-      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t) - L::kV) = (uint16_t)word;
-      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t + 4) - L::kV) = (uint16_t)(word >> 16);
+      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t) - L::kV) = (uint16_t)half[0];
+      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t + 4) - L::kV) = (uint16_t)half[1];
     }
     if (t == 0) *reinterpret_cast<uint32_t*>(p_at + L::pair(r, y)) = pair;
   }
