@@ -51,6 +51,18 @@ __device__ __forceinline__ uint8_t* tile_of(const Q4Cache& c, int b, int h, int6
 __device__ __forceinline__ float pair_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float pair_step(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// a / 15 correctly rounded, for a >= 0: from q = a y with y = 1 / 15 rounded,
+// the remainder r = a - 15 q is exact and q + r y rounds to the quotient
+// (Markstein's theorem on division by a number whose reciprocal is known
+// correctly rounded; checked here over every significand).  Quotients near the
+// end of fp32's range take the division.
+__device__ __forceinline__ float fifteenth(float a) {
+  constexpr float y = 1.f / 15.f;
+  if (a < 0x1p-100f) return __fdiv_rn(a, 15.f);
+  const float q = a * y;
+  return fmaf(fmaf(-15.f, q, a), y, q);
+}
+
 // The pair of a group with smallest and largest values mn and mx (NaN among
 // the values makes either NaN).
 __device__ __forceinline__ uint32_t make_pair(float mn, float mx) {
@@ -59,7 +71,7 @@ __device__ __forceinline__ uint32_t make_pair(float mn, float mx) {
   if (lo & 0xffffu) lo = (lo & 0xffff0000u) + ((lo >> 31) << 16);
   const float spread = mx - __uint_as_float(lo);
   if (mn != mn || !(fabsf(spread) <= 3.402823466e38f)) return 0x7fc00000u;   // lo 0, step NaN
-  const uint32_t step = (__float_as_uint(__fdiv_rn(spread, 15.f)) + 0xffffu) & 0xffff0000u;
+  const uint32_t step = (__float_as_uint(fifteenth(spread)) + 0xffffu) & 0xffff0000u;
   return (lo >> 16) | step;
 }
 

@@ -64,6 +64,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float reciprocal(float x) {      // within an ulp
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Eight consecutive values of a row: 16 bytes of bf16, 32 of fp32.
 template <typename T> struct Eight {
   uint4 w[sizeof(T) / 2];
@@ -120,8 +126,9 @@ __device__ __noinline__ uint32_t codes_by_division(float d0, float d1, float d2,
   return four_codes(c);
 }
 
-// The same from products with the rounded reciprocal, within 15 2^-23 + 2^-21
-// of the quotients, which matters next to a half alone.  There the remainder
+// The same from products with the reciprocal (within an ulp), which are within
+// 15 (2^-23 + 2^-24) + 2^-21 < 2^-18 of the rounded quotients; that matters
+// next to a half alone.  There the remainder
 // e = d - c step is exact (c has four bits, step eight) and tells the side, or
 // the tie, which goes to the even code; a quotient within 2^-19 of a half but
 // not on it takes the division, and so does a step whose reciprocal or
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
     const float lo = pair_lo(pair), step = pair_step(pair);
     uint32_t half[2] = {0, 0};
     if (step > 0.f) {
-      const float inv = __frcp_rn(step);
+      const float inv = reciprocal(step);
       half[0] = codes_of(v, lo, step, inv);
       half[1] = codes_of(v + 4, lo, step, inv);
     }
