@@ -14,6 +14,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -80,7 +81,6 @@ def load():
         I32, I64, U64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
         D = ctypes.POINTER(ctypes.c_double)
         TP = ctypes.POINTER(_Tensor)
-        CP = ctypes.POINTER(_Q4Cache)
         sig = {
             "plsh_sample_bins": [I64, D, I32, I32, U64, P, ctypes.POINTER(P)],
             "plsh_bins_resample": [P, D, U64, P],
@@ -101,12 +101,13 @@ def load():
             "plsh_alibi_attn_host": [TP, TP, TP, P, I32, TP, P],
             "plsh_alibi_exact": [TP, TP, TP, D, I32, TP, P],
             "plsh_alibi_decode": [TP, TP, TP, P, I64, TP, P],
+            # (descriptors as plain pointers: packed bytes, or byref of a struct)
             "plsh_q4_cache_bytes": [I64, I64, I32, I32, ctypes.POINTER(I64)],
-            "plsh_q4_cache_write": [TP, TP, CP, P, P, P],
-            "plsh_q4_cache_read": [CP, P, P, TP, TP, P],
-            "plsh_q4_decode_work_bytes": [TP, CP, ctypes.POINTER(I64)],
-            "plsh_alibi_decode_q4": [TP, CP, P, P, TP, P, I64, P],
-            "plsh_alibi_exact_decode_q4": [TP, CP, D, P, TP, P, I64, P],
+            "plsh_q4_cache_write": [P, P, P, P, P, P],
+            "plsh_q4_cache_read": [P, P, P, P, P, P],
+            "plsh_q4_decode_work_bytes": [P, P, ctypes.POINTER(I64)],
+            "plsh_alibi_decode_q4": [P, P, P, P, P, P, I64, P],
+            "plsh_alibi_exact_decode_q4": [P, P, P, P, P, P, I64, P],
             "plsh_stream_status": [P],
             "plsh_noalloc_status": [P],
             "plsh_attn_path": [TP, P, I32, ctypes.POINTER(I32)],
@@ -387,24 +388,52 @@ def q4_cache_bytes(pages: int, H: int, page: int, d: int) -> int:
     return out.value
 
 
-def _on_device(what: str, *tensors):
-    """Every tensor on the current CUDA device (the device a call runs on)."""
-    for t in tensors:
-        if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{what}: tensors must be on the current CUDA device")
+# A decode step is a few microseconds on the device, so what the host does per
+# call shows: these calls pack their descriptors (the bytes of a plsh_tensor)
+# and pass raw pointers instead of building ctypes objects.
+_pack_tensor = struct.Struct("@Pi4x4q").pack
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
 
 
-def _i32(what: str, t: torch.Tensor, B: int) -> ctypes.c_void_p:
-    if t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of B = {B} entries")
-    return ctypes.c_void_p(t.data_ptr())
+def _device(what: str, cache: "Q4Cache") -> int:
+    """The current device, which must be the cache's."""
+    dev = _current_device()
+    if cache.device_index != dev:
+        raise ValueError(f"{what}: the cache is not on the current CUDA device")
+    return dev
+
+
+def _packed(what: str, t: torch.Tensor, dev: int) -> bytes:
+    """A contiguous [B, H, n, d] tensor on device `dev` as a plsh_tensor."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: tensors must be on the current CUDA device")
+    dt = _DT.get(t.dtype)
+    if dt is None or t.dim() != 4 or not t.is_contiguous():
+        _desc(t)                                  # says what is wrong
+    return _pack_tensor(t.data_ptr(), dt, *t.shape)
+
+
+def _i32(what: str, t: torch.Tensor, B: int, dev: int) -> int:
+    if t.get_device() != dev or t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != B \
+            or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor of B = {B} entries on the "
+                         "current CUDA device")
+    return t.data_ptr()
+
+
+def _raw(stream, dev: int):
+    """The stream's handle as an integer (the current stream's when None)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 class Q4Cache:
     """A 4-bit paged K/V cache (plsh_q4_cache): `data`, uint8 device memory of
     pages * H * (page / 16) * 20 d bytes, and `table`, int32 [B, max_pages], the
     page of every sequence's positions [i page, (i + 1) page).  Both belong to
-    the caller, who may change the table's entries between calls."""
+    the caller, who may change their contents between calls."""
 
     def __init__(self, data: torch.Tensor, table: torch.Tensor, H: int, d: int, page: int = 64):
         one = q4_cache_bytes(1, H, page, d)
@@ -420,8 +449,11 @@ class Q4Cache:
         self.H, self.d, self.page = int(H), int(d), int(page)
         self.B, self.max_pages = table.shape
         self.pages = data.numel() // one
+        self.device_index = data.get_device()
         self._c = _Q4Cache(data.data_ptr(), table.data_ptr(), self.B, self.H, self.pages,
                            self.max_pages, self.page, self.d)
+        self._packed = bytes(self._c)
+        self._work = {}                           # decode workspaces by stream and number of heads
 
     @classmethod
     def empty(cls, pages: int, H: int, d: int, table: torch.Tensor, page: int = 64) -> "Q4Cache":
@@ -443,12 +475,13 @@ def q4_cache_write(cache: Q4Cache, K, V, pos, lens=None, stream=None):
     """plsh_q4_cache_write: rows i < lens[b] (all m without lens) of K, V
     [B, H, m, d] become positions pos[b] + i of the cache; pos, lens int32 [B]
     on the device."""
-    rest = () if lens is None else (lens,)
-    _on_device("q4_cache_write", K, V, cache.data, pos, *rest)
-    tk, tv = _desc(K), _desc(V)
-    _check(load().plsh_q4_cache_write(
-        ctypes.byref(tk), ctypes.byref(tv), ctypes.byref(cache._c), _i32("pos", pos, cache.B),
-        None if lens is None else _i32("lens", lens, cache.B), _stream(stream)))
+    dev = _device("q4_cache_write", cache)
+    st = (_lib or load()).plsh_q4_cache_write(
+        _packed("q4_cache_write", K, dev), _packed("q4_cache_write", V, dev), cache._packed,
+        _i32("pos", pos, cache.B, dev), None if lens is None else _i32("lens", lens, cache.B, dev),
+        _raw(stream, dev))
+    if st:
+        _check(st)
 
 
 def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=torch.bfloat16,
@@ -456,8 +489,7 @@ def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=to
     """plsh_q4_cache_read: (K, V) [B, H, m, d], the values of positions
     pos[b] + i, i < lens[b], of the cache.  `out`, a pair of tensors, keeps its
     other rows; without it they are new, of `dtype` and m rows, and zero there."""
-    rest = () if lens is None else (lens,)
-    _on_device("q4_cache_read", cache.data, pos, *rest)
+    dev = _device("q4_cache_read", cache)
     if out is None:
         if m is None:
             raise ValueError("q4_cache_read: give m, the rows of every sequence, or out")
@@ -465,36 +497,64 @@ def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=to
             out = tuple(torch.zeros(cache.B, cache.H, int(m), cache.d, dtype=dtype,
                                     device=cache.data.device) for _ in range(2))
     K, V = out
-    _on_device("q4_cache_read", K, V)
-    tk, tv = _desc(K), _desc(V)
-    _check(load().plsh_q4_cache_read(
-        ctypes.byref(cache._c), _i32("pos", pos, cache.B),
-        None if lens is None else _i32("lens", lens, cache.B), ctypes.byref(tk), ctypes.byref(tv),
-        _stream(stream)))
+    st = (_lib or load()).plsh_q4_cache_read(
+        cache._packed, _i32("pos", pos, cache.B, dev),
+        None if lens is None else _i32("lens", lens, cache.B, dev),
+        _packed("q4_cache_read", K, dev), _packed("q4_cache_read", V, dev), _raw(stream, dev))
+    if st:
+        _check(st)
     return K, V
 
 
 def q4_decode_work_bytes(q, cache: Q4Cache) -> int:
     """plsh_q4_decode_work_bytes: workspace of a 4-bit decode call."""
-    out, tq = ctypes.c_int64(), _desc(q)
-    _check(load().plsh_q4_decode_work_bytes(ctypes.byref(tq), ctypes.byref(cache._c),
+    dev = _device("q4_decode_work_bytes", cache)
+    out = ctypes.c_int64()
+    _check(load().plsh_q4_decode_work_bytes(_packed("q4_decode_work_bytes", q, dev), cache._packed,
                                             ctypes.byref(out)))
     return out.value
 
 
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) \
+    or torch.cuda.is_current_stream_capturing
+
+
+def _decode_work(q, cache: Q4Cache, stream, raw: int) -> torch.Tensor:
+    """Workspace of a decode call: the cache keeps one for each stream that is
+    current when a call is made (calls on a stream run one after the other); a
+    call that is captured, or given a stream, takes one of its own, so that
+    graphs that replay at once share none."""
+    own = stream is not None or _capturing()
+    key = (raw, q.shape[1])
+    w = None if own else cache._work.get(key)
+    if w is None:
+        need = q4_decode_work_bytes(q, cache)
+        with _stream_scope(stream):
+            w = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if not own:
+            cache._work[key] = w
+    return w
+
+
 def _decode_q4(what, fn, q, cache, extra, pos, out, work, stream):
-    _on_device(what, q, cache.data, pos)
-    with _stream_scope(stream):
-        o = torch.empty_like(q) if out is None else out
-        if work is None:
-            work = torch.empty(q4_decode_work_bytes(q, cache), dtype=torch.uint8, device=q.device)
-    _on_device(what, o, work)
-    if not work.is_contiguous():
-        raise ValueError(f"{what}: work must be contiguous")
-    tq, to = _desc(q), _desc(o)
-    _check(fn(ctypes.byref(tq), ctypes.byref(cache._c), extra, _i32("pos", pos, cache.B),
-              ctypes.byref(to), ctypes.c_void_p(work.data_ptr()),
-              work.numel() * work.element_size(), _stream(stream)))
+    dev = _device(what, cache)
+    tq = _packed(what, q, dev)
+    raw = _raw(stream, dev)
+    w = _decode_work(q, cache, stream, raw) if work is None else work
+    if out is not None:
+        o, to = out, _packed(what, out, dev)
+    elif stream is None:
+        o = torch.empty_like(q)
+        to = _pack_tensor(o.data_ptr(), _DT[q.dtype], *q.shape)
+    else:
+        with _stream_scope(stream):
+            o = torch.empty_like(q)
+        to = _packed(what, o, dev)
+    if w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"{what}: work must be contiguous memory of the current CUDA device")
+    st = fn(tq, cache._packed, extra, _i32("pos", pos, cache.B, dev), to, w.data_ptr(), w.nbytes, raw)
+    if st:
+        _check(st)
     return o
 
 
@@ -502,9 +562,10 @@ def alibi_decode_q4(q, cache: Q4Cache, bins: Bins, pos, out=None, work=None, str
     """plsh_alibi_decode_q4: one decode step over the 4-bit cache, for every
     sequence the row of T~ at its own position pos[b] (int32 [B] on the device;
     negative: an idle slot, o = 0), for the queries q [B, Hq, 1, d].  `work`:
-    device memory of q4_decode_work_bytes, allocated when not given."""
-    return _decode_q4("alibi_decode_q4", load().plsh_alibi_decode_q4, q, cache, bins.handle, pos,
-                      out, work, stream)
+    device memory of q4_decode_work_bytes that this call has for itself; without
+    it the cache keeps one per stream."""
+    return _decode_q4("alibi_decode_q4", (_lib or load()).plsh_alibi_decode_q4, q, cache,
+                      bins.handle, pos, out, work, stream)
 
 
 def alibi_exact_decode_q4(q, cache: Q4Cache, sigma, pos, out=None, work=None, stream=None):
@@ -513,8 +574,8 @@ def alibi_exact_decode_q4(q, cache: Q4Cache, sigma, pos, out=None, work=None, st
     sig = _f64(sigma)
     if sig.shape != (q.shape[1],):
         raise ValueError("alibi_exact_decode_q4: sigma must hold a scale per query head")
-    return _decode_q4("alibi_exact_decode_q4", load().plsh_alibi_exact_decode_q4, q, cache,
-                      sig.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), pos, out, work, stream)
+    return _decode_q4("alibi_exact_decode_q4", (_lib or load()).plsh_alibi_exact_decode_q4, q,
+                      cache, sig.tobytes(), pos, out, work, stream)
 
 
 def bias_error(bins: Bins, sigma: float, h: int, lanczos_iters: int = 60, seed: int = 0,
