@@ -45,6 +45,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -62,14 +63,17 @@ namespace {
 using namespace q4;
 using namespace ptx;
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 3;          // blocks of 32 positions in a warp's ring
-constexpr int kCtasPerSm = 3;
+// exact: three CTAs of four warps (168 registers a thread) and three blocks of
+// 32 positions in a warp's ring; approximate: two CTAs of eight warps, two
+// blocks (an envelope is a few blocks long)
+constexpr int kExactWarps = 4, kExactStages = 3, kExactCtas = 3;
+constexpr int kApproxWarps = 8, kApproxStages = 2, kApproxCtas = 2;
 constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
 constexpr int kMinBlocks = 8;       // exact: blocks of a CTA at least
 constexpr int kRowCost = 12;        // exact: blocks that beginning and ending a row costs
-constexpr int kMaxShares = 64;      // approximate: CTAs of one row at most
+constexpr int kMaxShares = 64;        // approximate: CTAs of one row at most
+constexpr double kTeamBlocks = 3.0;   // approximate: blocks of a warp, as a start
+constexpr double kShareBlocks = 40.0; // and of a CTA at most, while there is room
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float kNothing = -3.402823466e38f;   // a maximum over no score
@@ -91,7 +95,6 @@ struct DecodeParams {
   int s;
   int64_t W;
   int limit;                        // positions below this may be asked for
-  int shares;                       // approximate: CTAs of a (sequence, group)
   int4* ends;                       // exact: per CTA {row, first CTA, first piece} of a row that ends in it
   float* part;                      // pieces: o [8][D], m [8], l [8]
   int* err;
@@ -186,37 +189,40 @@ __device__ __forceinline__ void lds_at(uint32_t addr, int off, uint32_t (&w)[4])
                : "memory");
 }
 
-// What a CTA attends over: blocks [t0, t1) of 32 positions (two tiles) of
+__device__ __forceinline__ void store_row(float* p, const float (&o)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&o)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+}
+
+// What a team of warps attends over: blocks [t0, t1) of 32 positions (two tiles) of
 // sequence b, KV head kvh, for the query heads h0 .. h0 + heads - 1.
 struct Piece {
   int b, kvh, h0, heads, pos, t0, t1;
   int first;         // first position any of the heads sees
 };
 
-template <typename T, int D>
+// ROWS: rows that a CTA's warps may be attending at once (a team of warps each)
+template <typename T, int D, int WARPS, int STAGES, int ROWS>
 struct Smem {
   // the queries' B operands by lane (fp32: two terms), and zeros
-  alignas(128) uint4 q[sizeof(T) / 2][Layout<D>::kGroups][33];
-  uint2 qlow[32];
-  float scale[kHeads];
-  alignas(128) uint8_t ring[kWarps][kStages][2 * Layout<D>::kTileBytes];
-  float m[kWarps][kHeads], l[kWarps][kHeads];
-  float weight[2 * kWarps][kHeads + 1];    // of a warp's column in its head
-  unsigned some[kHeads];               // which of them saw anything (NaN too)
-  int raw_lo[kHeads][kMaxS];
-  int lo[kHeads][kMaxS];               // a head's bin starts, ascending
-  int64_t split[4];                    // exact: entries, entries of a CTA, first sequence and its first entry
+  alignas(128) uint4 q[ROWS][sizeof(T) / 2][Layout<D>::kGroups][33];
+  uint2 qlow[ROWS][32];
+  float scale[ROWS][kHeads];
+  alignas(128) uint8_t ring[WARPS][STAGES][2 * Layout<D>::kTileBytes];
+  float m[WARPS][kHeads], l[WARPS][kHeads];
+  float weight[2 * WARPS][kHeads + 1];   // of a warp's column in its head
+  unsigned some[ROWS][kHeads];           // which of them saw anything (NaN too)
+  int64_t split[4];                      // exact: entries, entries of a CTA, first sequence and its first entry
 };
-// the merge of the warps reuses the ring
-static_assert(kWarps * kHeads * 128 * 4 <= 2 * kWarps * kStages * Layout<128>::kTileBytes, "merge buffer");
-static_assert(kWarps * kHeads * 64 * 4 <= 2 * kWarps * kStages * Layout<64>::kTileBytes, "merge buffer");
 
 // Lane (g, t)'s values 8 t .. 8 t + 7 of every group of column g's query head.
 template <typename T, int D, int PACK>
 struct Query {
   uint4 w[Layout<D>::kGroups][sizeof(T) / 2];
-  __device__ void load(const DecodeParams& p, const Piece& pc) {
-    if (threadIdx.x >= 32) return;         // the first warp prepares it for all
+  __device__ void load(const DecodeParams& p, const Piece& pc, int rank) {
+    if (rank != 0) return;                 // a team's first warp prepares it for all
     const int lane = threadIdx.x & 31, g = (lane >> 2) % (kHeads / PACK), t = lane & 3;
     const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + g) * D + 8 * t;
 #pragma unroll
@@ -294,6 +300,62 @@ struct Ring {
   }
 };
 
+// The queries as B operands (lane (g, t) holds rows 2 t, 2 t + 1, ... of column
+// g), by the first warp of a team for all of it; qlow takes the products of q's
+// sums over a group with K's lo, a bf16 number: k slots 2 t, 2 t + 1 and
+// 2 t + 8 hold group t's sum as three bf16 terms (24 bits).  Visible to the
+// team after a barrier.
+template <typename T, int D, int PACK, typename S>
+__device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, int rank, int row, S& sm) {
+  constexpr int Y = Layout<D>::kGroups;
+  constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  if (rank != 0) return;
+  float mx = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int y = 0; y < Y; ++y)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = fabsf(query.get(y, i));
+      mx = fmaxf(mx, v);
+      bad |= !(v < 1.2980742e33f);      // 2^110
+    }
+  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+  const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 110);
+  bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
+  const float up = pow2(14 - e);
+  const float norm = kLog2e / sqrtf((float)D);
+  if (t == 0) sm.scale[row][g] = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
+  float group = 0.f;
+#pragma unroll
+  for (int y = 0; y < Y; ++y) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += query.get(y, i);
+    sum += __shfl_xor_sync(FULL, sum, 1);
+    sum += __shfl_xor_sync(FULL, sum, 2);
+    if (y == t) group = sum * norm;
+    uint32_t w[4], r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // odd codes are taken four bits up, as 16 c
+      const float k = (i & 1) ? up * 0.0625f : up;
+      const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
+      w[i] = pack_f16(a, b);
+      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
+      r[i] = pack_f16(a - f.x, b - f.y);
+    }
+    sm.q[row][0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (kTwo) sm.q[row][1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+  if (lane < (int)sizeof(T) / 2 * Y) sm.q[row][lane / Y][lane % Y][32] = make_uint4(0, 0, 0, 0);
+  const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
+  const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
+  sm.qlow[row][lane] = make_uint2(pack_bf16(hi, mid), pack_bf16(group - hi - mid, 0.f));
+}
+
 // One piece; the result (all heads, the warps merged) goes to `o_row` (o of
 // head h0, divided by the row sums) or, when that is null, to `part`.
 // A step takes a block of two tiles.  PACK = 1: one after the other, the scores
@@ -302,104 +364,73 @@ struct Ring {
 // one's in 4 - 7 (B is zero in the other tile's columns), so that what follows
 // the products (a lane holds two positions and two columns either way) is done
 // once for both.  Every column keeps a maximum, sums and accumulators of its
-// own.  `ahead`: the first warp's first block is in its ring already, not yet
+// own.  `ahead`: this warp's first block is in its ring already, not yet
 // committed.
-template <typename T, int D, bool EXACT, int PACK>
-__device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Query<T, D, PACK>& query,
-                                       const float* slopes, Smem<T, D>& sm, Ring<T, D>& ring,
-                                       bool ahead, T* o_row, float* part) {
+// The row's team: `size` warps from warp `first` on; all warps of the CTA call
+// this together.  `starts`: its heads' bin starts, padded to whole int4 by numbers
+// that no position reaches.
+struct Team {
+  int first, size;
+};
+template <typename T, int D, bool EXACT, int PACK, int WARPS, int STAGES, int ROWS>
+__device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Team& team,
+                                       const Query<T, D, PACK>& query, const float* slopes,
+                                       const int4* starts, Smem<T, D, WARPS, STAGES, ROWS>& sm,
+                                       Ring<T, D>& ring, bool ahead, T* o_row, float* part) {
   using L = Layout<D>;
   constexpr int Y = L::kGroups;
   constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
   constexpr float kLazy = EXACT ? 8.f : 4.f;    // weights up to 2^8, or 64 x 2^4
   constexpr int kCols = kHeads / PACK;          // columns of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = warp - team.first, kTeam = team.size;
+  const int row = team.first / kTeam;           // the team's number in the CTA
   const int mine = PACK == 2 ? t >> 1 : 0;      // the tile whose scores this lane holds
   const int head = (2 * t) % kCols;             // and its heads: head, head + 1
 
-  // ---- step i takes block newest - i kWarps, from the newest down (ALiBi's
+  // ---- step i takes block newest - i kTeam, from the newest down (ALiBi's
   // weights fall with the distance: the running maximum is met early)
-  const int newest = pc.t1 - 1 - warp;
-  const int steps = newest >= pc.t0 ? (newest - pc.t0) / kWarps + 1 : 0;
+  const int newest = pc.t1 - 1 - rank;
+  const int steps = newest >= pc.t0 ? (newest - pc.t0) / kTeam + 1 : 0;
   int32_t next_page;
   {
-    int32_t pg[kStages];
+    int32_t pg[STAGES];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) pg[i] = i < steps ? ring.page_of(newest - i * kWarps) : 0;
+    for (int i = 0; i < STAGES; ++i) pg[i] = i < steps ? ring.page_of(newest - i * kTeam) : 0;
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < steps && !(ahead && i == 0 && warp == 0)) ring.fetch(newest - i * kWarps, i, pg[i]);
+    for (int i = 0; i < STAGES - 1; ++i) {
+      if (i < steps && !(ahead && i == 0)) ring.fetch(newest - i * kTeam, i, pg[i]);
       cp_async_commit();
     }
-    next_page = pg[kStages - 1];
+    next_page = pg[STAGES - 1];
   }
 
-  // ---- the queries as B operands (lane (g, t) holds rows 2 t, 2 t + 1, ... of
-  // column g); qlow takes the products of q's sums over a group with K's lo, a
-  // bf16 number: k slots 2 t, 2 t + 1 and 2 t + 8 hold group t's sum as three
-  // bf16 terms (24 bits)
-  if (warp == 0) {
-    float mx = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int y = 0; y < Y; ++y)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float v = fabsf(query.get(y, i));
-        mx = fmaxf(mx, v);
-        bad |= !(v < 1.2980742e33f);      // 2^110
-      }
-    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 110);
-    bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
-    const float up = pow2(14 - e);
-    const float norm = kLog2e / sqrtf((float)D);
-    if (t == 0) sm.scale[g] = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
-    float group = 0.f;
-#pragma unroll
-    for (int y = 0; y < Y; ++y) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum += query.get(y, i);
-      sum += __shfl_xor_sync(FULL, sum, 1);
-      sum += __shfl_xor_sync(FULL, sum, 2);
-      if (y == t) group = sum * norm;
-      uint32_t w[4], r[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // odd codes are taken four bits up, as 16 c
-        const float k = (i & 1) ? up * 0.0625f : up;
-        const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
-        w[i] = pack_f16(a, b);
-        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
-        r[i] = pack_f16(a - f.x, b - f.y);
-      }
-      sm.q[0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
-      if constexpr (kTwo) sm.q[1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
-    }
-    if (lane < (int)sizeof(T) / 2 * Y) sm.q[lane / Y][lane % Y][32] = make_uint4(0, 0, 0, 0);
-    const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
-    const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
-    sm.qlow[lane] = make_uint2(pack_bf16(hi, mid), pack_bf16(group - hi - mid, 0.f));
-  }
+  if constexpr (EXACT) prepare_query<T, D, PACK>(query, rank, row, sm);
   __syncthreads();
-  const uint32_t qlow[2] = {sm.qlow[lane].x, sm.qlow[lane].y};
-  const float qscale[2] = {sm.scale[2 * t], sm.scale[2 * t + 1]};
+  const uint32_t qlow[2] = {sm.qlow[row][lane].x, sm.qlow[row][lane].y};
+  const float qscale[2] = {sm.scale[row][2 * t], sm.scale[row][2 * t + 1]};
   // the lane's operands where column g belongs to tile u of the block, else zeros
   uint32_t q_at[PACK];
 #pragma unroll
-  for (int u = 0; u < PACK; ++u) q_at[u] = smem_u32(&sm.q[0][0][g / kCols == u ? lane : 32]);
+  for (int u = 0; u < PACK; ++u) q_at[u] = smem_u32(&sm.q[row][0][0][g / kCols == u ? lane : 32]);
   constexpr int kQ = 33 * 16;                   // bytes from a group's operands to the next's
   // all ones where column g belongs to tile u of the block
   uint32_t keep[PACK];
 #pragma unroll
   for (int u = 0; u < PACK; ++u) keep[u] = g / kCols == u ? 0xffffffffu : 0u;
   float slope[2] = {0.f, 0.f};
-  int seen[2] = {p.s, p.s};        // bin starts at or before the last position of the tile
+  int newest_start = 0;            // the largest bin start of the lane's heads
+  const int quads = (p.s + 3) >> 2;
   if constexpr (EXACT) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) slope[k] = head + k < pc.heads ? slopes[pc.h0 + head + k] : 0.f;
+  } else if (steps > 0) {
+    for (int i = 0; i < 2 * quads; ++i) {
+      const int4 v = starts[head * quads + i];
+      const int a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) newest_start = a[k] <= pc.pos ? max(newest_start, a[k]) : newest_start;
+    }
   }
 
   // ---- the loop
@@ -420,14 +451,14 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   const uint32_t pair_at = ring.smem + mine * L::kTileBytes + L::pair(g, 0);
   const uint32_t low_at = ring.smem + L::pair(g, t & (Y - 1));
   const uint32_t v_at = ring.smem + 16 * lane;
-  for (int i = 0, st = 0; i < steps; ++i, st = st == kStages - 1 ? 0 : st + 1) {
-    const int block = newest - i * kWarps;
-    if (i + kStages - 1 < steps) {
-      ring.fetch(block - (kStages - 1) * kWarps, st == 0 ? kStages - 1 : st - 1, next_page);
-      if (i + kStages < steps) next_page = ring.page_of(block - kStages * kWarps);
+  for (int i = 0, st = 0; i < steps; ++i, st = st == STAGES - 1 ? 0 : st + 1) {
+    const int block = newest - i * kTeam;
+    if (i + STAGES - 1 < steps) {
+      ring.fetch(block - (STAGES - 1) * kTeam, st == 0 ? STAGES - 1 : st - 1, next_page);
+      if (i + STAGES < steps) next_page = ring.page_of(block - STAGES * kTeam);
     }
     cp_async_commit();
-    cp_async_wait<kStages - 1>();
+    cp_async_wait<STAGES - 1>();
     __syncwarp();
     const uint32_t gone = (ring.absent >> (2 * st)) & 3u;
     const bool edge = 32 * block < pc.first || 32 * block + 31 > pc.pos || gone;
@@ -502,27 +533,18 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         for (int k = 0; k < 4; ++k)
           x[k] = fmaf(x[k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
       } else {
-        // starts past the tile are behind us; those inside it count from their
-        // position on
-        const int j0 = j - g;
-        int n[4];
-        bool inside = false;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int* lo = sm.lo[head + k];
-          while (seen[k] > 0 && lo[seen[k] - 1] >= j0 + kTile) --seen[k];
-          n[k] = n[k + 2] = seen[k];
-          inside |= seen[k] > 0 && lo[seen[k] - 1] > j0;
-        }
-        if (__any_sync(FULL, inside)) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            for (int y = seen[k] - 1; y >= 0; --y) {
-              const int a = sm.lo[head + k][y] - j0;
-              if (a <= 0) break;
-              n[k] -= a > g;
-              n[k + 2] -= a > g + 8;
-            }
+        // c_j: every start in the row's past, or those at or before j
+        int n[4] = {p.s, p.s, p.s, p.s};
+        if (!__all_sync(FULL, j - g >= newest_start)) {
+          n[0] = n[1] = n[2] = n[3] = 0;
+#pragma unroll 4
+          for (int i = 0; i < quads; ++i) {
+            const int4 u = starts[head * quads + i], v = starts[(head + 1) * quads + i];
+            n[0] += (u.x <= j) + (u.y <= j) + (u.z <= j) + (u.w <= j);
+            n[1] += (v.x <= j) + (v.y <= j) + (v.z <= j) + (v.w <= j);
+            n[2] += (u.x <= j + 8) + (u.y <= j + 8) + (u.z <= j + 8) + (u.w <= j + 8);
+            n[3] += (v.x <= j + 8) + (v.y <= j + 8) + (v.z <= j + 8) + (v.w <= j + 8);
+          }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -645,11 +667,14 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   }
   cp_async_wait<0>();
 
-  // ---- merge the warps' columns: head h has column h of every warp, and with
+  // ---- merge the team's columns: head h has column h of every warp, and with
   // PACK = 2 column h + 4
-  constexpr int kWays = kWarps * PACK;
-  __syncthreads();           // every ring is done with
-  float* merge = reinterpret_cast<float*>(sm.ring) + warp * kHeads * D;
+  const int ways = kTeam * PACK, way0 = team.first * PACK;
+  constexpr int kStride = STAGES * 2 * L::kTileBytes / 4;      // floats of a warp's ring
+  static_assert(kStride >= kHeads * D, "a warp's columns fit its ring");
+  __syncwarp();              // the warp's ring is done with
+  float* all = reinterpret_cast<float*>(sm.ring);
+  float* merge = all + warp * kStride;
   if (steps > 0) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -675,58 +700,78 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     sm.l[warp][lane] = 0.f;
   }
   __syncthreads();
-  if (threadIdx.x < kCols) {
-    // a thread per head weighs its columns; a row divides by its sum, and one
-    // that sees nothing is 0
-    const int h = threadIdx.x;
-    float mm = kNothing, ll = 0.f, mw[kWays], lw[kWays];
+  if (rank == 0) {
+    // 32 / kCols lanes a head, two columns each at most; a row divides by its
+    // sum, and one that sees nothing is 0
+    constexpr int kPer = 32 / kCols;
+    const int h = lane / kPer, w0 = lane % kPer;
+    static_assert(2 * kPer >= WARPS * PACK, "two columns a lane");
+    float mw[2], lw[2], mm = kNothing;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int w = w0 + k * kPer;
+      mw[k] = kNothing;
+      lw[k] = 0.f;
+      if (w < ways) {
+        mw[k] = sm.m[team.first + w / PACK][w % PACK * kCols + h];
+        lw[k] = sm.l[team.first + w / PACK][w % PACK * kCols + h];
+      }
+      mm = fmaxf(mm, mw[k]);
+    }
+#pragma unroll
+    for (int k = 1; k < kPer; k <<= 1) mm = fmaxf(mm, __shfl_xor_sync(FULL, mm, k));
+    float ll = 0.f;
     unsigned some = 0;
 #pragma unroll
-    for (int w = 0; w < kWays; ++w) {
-      const int column = w % PACK * kCols + h;
-      mw[w] = sm.m[w / PACK][column];
-      lw[w] = sm.l[w / PACK][column];
-      mm = fmaxf(mm, mw[w]);
+    for (int k = 0; k < 2; ++k) {
+      const int w = w0 + k * kPer;
+      const float f = ex2(mw[k] - mm);
+      if (w < ways) sm.weight[way0 + w][h] = f;
+      if (lw[k] != 0.f) {
+        some |= 1u << w;
+        ll = fmaf(f, lw[k], ll);
+      }
     }
 #pragma unroll
-    for (int w = 0; w < kWays; ++w) {
-      if (lw[w] == 0.f) continue;
-      some |= 1u << w;
-      mw[w] = ex2(mw[w] - mm);
-      ll = fmaf(mw[w], lw[w], ll);
+    for (int k = 1; k < kPer; k <<= 1) {
+      ll += __shfl_xor_sync(FULL, ll, k);
+      some |= __shfl_xor_sync(FULL, some, k);
     }
-    sm.some[h] = some;
-    const float over = o_row == nullptr ? 1.f : 1.f / ll;
-#pragma unroll
-    for (int w = 0; w < kWays; ++w) sm.weight[w][h] = mw[w] * over;
-    if (o_row == nullptr && h < pc.heads) {
-      part[kHeads * D + h] = mm;
-      part[kHeads * D + kHeads + h] = ll;
+    if (w0 == 0) {
+      sm.some[row][h] = some;
+      sm.scale[row][h] = o_row == nullptr ? 1.f : 1.f / ll;      // (the query's scale is done with)
+      if (o_row == nullptr && part != nullptr && h < pc.heads) {
+        part[kHeads * D + h] = mm;
+        part[kHeads * D + kHeads + h] = ll;
+      }
     }
   }
   __syncthreads();
-  const float* all = reinterpret_cast<const float*>(sm.ring);
-  for (int e = 4 * threadIdx.x; e < pc.heads * D; e += 4 * kThreads) {
-    const int h = e / D;
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
-    const unsigned some = sm.some[h];
+  if (o_row != nullptr || part != nullptr) {
+    for (int e = 4 * (32 * rank + lane); e < pc.heads * D; e += 4 * 32 * kTeam) {
+      const int h = e / D;
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      const unsigned some = sm.some[row][h];
+#pragma unroll 8
+      for (int w = 0; w < ways; ++w) {
+        const bool in = (some >> w) & 1;         // else the buffer holds anything
+        const float f = sm.weight[way0 + w][h];
+        const float4 v = *reinterpret_cast<const float4*>(
+            all + (team.first + w / PACK) * kStride + w % PACK * kCols * D + e);
+        o[0] = in ? fmaf(f, v.x, o[0]) : o[0];
+        o[1] = in ? fmaf(f, v.y, o[1]) : o[1];
+        o[2] = in ? fmaf(f, v.z, o[2]) : o[2];
+        o[3] = in ? fmaf(f, v.w, o[3]) : o[3];
+      }
+      if (o_row == nullptr) {
+        *reinterpret_cast<float4*>(part + e) = make_float4(o[0], o[1], o[2], o[3]);
+      } else {
+        const float inv = some ? sm.scale[row][h] : 0.f;
 #pragma unroll
-    for (int w = 0; w < kWays; ++w) {
-      const bool in = (some >> w) & 1;         // else the buffer holds anything
-      const float f = sm.weight[w][h];
-      const float4 v = *reinterpret_cast<const float4*>(
-          all + (w / PACK * kHeads + w % PACK * kCols) * D + e);
-      o[0] = in ? fmaf(f, v.x, o[0]) : o[0];
-      o[1] = in ? fmaf(f, v.y, o[1]) : o[1];
-      o[2] = in ? fmaf(f, v.z, o[2]) : o[2];
-      o[3] = in ? fmaf(f, v.w, o[3]) : o[3];
+        for (int k = 0; k < 4; ++k) o[k] *= inv;
+        store_row(o_row + e, o);
+      }
     }
-    if (o_row == nullptr)
-      *reinterpret_cast<float4*>(part + e) = make_float4(o[0], o[1], o[2], o[3]);
-    else if constexpr (kTwo)
-      *reinterpret_cast<float4*>(o_row + e) = make_float4(o[0], o[1], o[2], o[3]);
-    else
-      *reinterpret_cast<uint2*>(o_row + e) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
   }
   __syncthreads();           // before the next piece fills the rings
 }
@@ -753,16 +798,17 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& 
 // CTAs, each leaves a piece (slot 2 i when it is the CTA's first, else
 // 2 i + 1), and the CTA where it ends says in ends[i] which pieces to join.
 template <typename T, int D, int PACK>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(32 * kExactWarps, kExactCtas)
 q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Slopes slopes) {
   extern __shared__ __align__(128) uint8_t raw[];
-  Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+  using S = Smem<T, D, kExactWarps, kExactStages, 1>;
+  S& sm = *reinterpret_cast<S*>(raw);
   grid_dep_wait();
   const int tid = threadIdx.x, units = p.c.H * p.chunks;
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
     if (row_blocks(p, b) > 0) continue;
     if (tid == 0 && p.pos[b] >= 0) atomicOr(p.err, kErrCachePlace);
-    for (int e = tid; e < p.Hq * D; e += kThreads)
+    for (int e = tid; e < p.Hq * D; e += 32 * kExactWarps)
       static_cast<T*>(p.o)[(int64_t)b * p.Hq * D + e] = Elem<T>::put(0.f);
   }
   // prefix sums of the sequences' entries, a run of sequences per thread of
@@ -833,9 +879,9 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
       p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row <= i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
     }
     Query<T, D, PACK> query;
-    query.load(p, pc);
+    query.load(p, pc, tid >> 5);
     Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
-    attend<T, D, true, PACK>(p, pc, query, slopes.v, sm, ring, false,
+    attend<T, D, true, PACK>(p, pc, Team{0, kExactWarps}, query, slopes.v, nullptr, sm, ring, false,
                              pc.t0 == 0 && last ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D
                                                 : nullptr,
                              p.part + (int64_t)slot * part_floats<D>());
@@ -928,171 +974,210 @@ __global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __
                     static_cast<T*>(p.o) + ((int64_t)(end.x / units) * p.Hq + pc.h0 + h) * D);
 }
 
-// Approximate: KV heads by the largest scale of their query heads, widest
-// first (the longest envelopes start first), all sequences of a KV head
-// together; shares_of[kvh] CTAs for each row.
+// Approximate.  KV heads by the largest scale of their query heads, widest
+// first (the longest envelopes start first), all rows (sequences and chunks) of
+// a KV head together.  A row is attended by a team of 1, 2, 4 or 8 warps, so
+// that a warp has a few blocks however wide the head's envelopes; a CTA has
+// 8 / team rows.  Rows wider than eight warps' worth go to several CTAs, where
+// the grid has room, and are joined.
 struct Groups {
-  int first[kMaxGroupOrder + 1];          // first CTA of each, in order
+  int first[kMaxGroupOrder + 1];          // first CTA of each KV head, in order
   uint8_t order[kMaxGroupOrder];
-  uint8_t shares_of[kMaxGroupOrder];      // by KV head
-  int ordered;                            // 0: index order, p.shares each
+  uint8_t shares[kMaxGroupOrder];         // CTAs of a row, in order
+  uint8_t team[kMaxGroupOrder];           // warps of a row, in order
+  int ordered;                            // 0: index order, shares[0] and team[0] for all
 };
 
+// CTAs of a KV head: `rows` rows by teams of `team` warps, or by `shares` CTAs each
+__host__ __device__ __forceinline__ int group_ctas(int rows, int team, int shares) {
+  const int held = kApproxWarps / team;
+  return shares > 1 ? rows * shares : (rows + held - 1) / held;
+}
+
 template <typename T, int D, int PACK>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(32 * kApproxWarps, kApproxCtas)
 q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Groups gr) {
   extern __shared__ __align__(128) uint8_t raw[];
-  Smem<T, D>& sm = *reinterpret_cast<Smem<T, D>*>(raw);
+  using S = Smem<T, D, kApproxWarps, kApproxStages, kApproxWarps>;
+  S& sm = *reinterpret_cast<S*>(raw);
   grid_dep_wait();
-  const int tid = threadIdx.x;
-  int cta = blockIdx.x, kvh, shares = p.shares;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rows = p.c.B * p.chunks;
+  int cta = blockIdx.x, k = 0;
   if (gr.ordered) {
-    int k = 0;
     while (k + 1 < p.c.H && cta >= gr.first[k + 1]) ++k;
     cta -= gr.first[k];
-    kvh = gr.order[k];
-    shares = gr.shares_of[kvh];
-  } else {
-    kvh = cta / (p.c.B * p.chunks * shares);
-    cta -= kvh * p.c.B * p.chunks * shares;
   }
-  const int share = cta % shares;
-  cta /= shares;
-  const int u = kvh * p.chunks + cta % p.chunks;
+  const int size = gr.team[k], shares = gr.shares[k];
+  int kvh = gr.ordered ? gr.order[k] : 0;
+  if (!gr.ordered) {
+    const int each = group_ctas(rows, size, shares);
+    kvh = cta / each;
+    cta -= kvh * each;
+  }
+  Team team;
+  team.size = size;
+  team.first = warp / size * size;
+  const int rank = warp - team.first, tt = 32 * rank + lane, step = 32 * size;
+  const int share = shares > 1 ? cta % shares : 0;
+  const int row = shares > 1 ? cta / shares : cta * (kApproxWarps / size) + warp / size;
+  const bool valid = row < rows;
   Piece pc;
-  pc.b = cta / p.chunks;
-  unit_heads(p, u, pc);
-  T* o = static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D;
-  float* part = p.part + (int64_t)blockIdx.x * part_floats<D>();
-  pc.pos = p.pos[pc.b];
+  pc.b = valid ? row / p.chunks : 0;
+  unit_heads(p, kvh * p.chunks + row % p.chunks, pc);
+  pc.pos = valid ? p.pos[pc.b] : -1;
   const bool none = pc.pos < 0 || pc.pos >= p.limit;
-  if (none && tid == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
-  pc.first = pc.pos;
+  if (valid && none && tt == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
   Query<T, D, PACK> query;
-  query.load(p, pc);
-  Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
-  // the newest block is always needed, and with pages of 32 or more positions
-  // its page too: its copy need not wait for the bins
-  const bool ahead = share == 0 && !none && p.c.page_shift > 4;
-  if (ahead && tid < 32) ring.fetch(pc.pos >> 5, 0, ring.page_of(pc.pos >> 5));
+  query.load(p, pc, rank);
+  Ring<T, D> ring(p, pc, sm.ring[warp]);
+  // A warp's first block is copied before the bins are known: the newest of the
+  // row, always needed, or the next ones, which the team's size makes likely
+  // (a page of its own only if its index is good: whether it is needed, and to
+  // be reported, is not known yet).
+  const int next = (pc.pos >> 5) - rank;
+  bool ahead = share == 0 && !none && p.c.page_shift > 4 && next >= 0;
+  int32_t next_page = ahead ? ring.page_of(next) : -1;
+  // the heads' bin starts; a thread's first one is on its way while the query
+  // is prepared
+  const int quads = (p.s + 3) >> 2, width = 4 * quads;
+  int4* starts = reinterpret_cast<int4*>(raw + sizeof(S)) + (team.first / size) * kHeads * quads;
+  auto start_of = [&](int i) {
+    const int h = i / width, x = i - h * width;
+    if (x >= p.s) return INT_MAX;
+    if (h >= pc.heads) return 0;
+    return bin_lo(load_record(p.rec, ((int64_t)(pc.h0 + h) * p.s + x) * p.W + (pc.pos >> 5)), pc.pos);
+  };
+  const bool mine = !none && tt < kHeads * width;
+  int oldest = mine ? start_of(tt) : INT_MAX;
+  ahead = ahead && (uint32_t)next_page < (uint32_t)p.c.pages;
+  if (ahead) ring.fetch(next, 0, next_page);
+  prepare_query<T, D, PACK>(query, rank, team.first / size, sm);
+  if (mine) {
+    reinterpret_cast<int*>(starts)[tt] = oldest;
+    if (tt >= pc.heads * width) oldest = INT_MAX;
+    for (int i = tt + step; i < kHeads * width; i += step) {
+      const int v = start_of(i);
+      reinterpret_cast<int*>(starts)[i] = v;
+      if (i < pc.heads * width) oldest = min(oldest, v);
+    }
+  }
+  oldest = __reduce_min_sync(FULL, oldest);
+  if (lane == 0) sm.some[0][warp] = (unsigned)oldest;       // (a row of kHeads, before its use)
+  __syncthreads();
+  pc.first = pc.pos;
+  pc.t0 = pc.t1 = 0;
   if (!none) {
-    for (int k = tid; k < kHeads * p.s; k += kThreads) {
-      const int h = k / p.s, x = k % p.s;
-      sm.raw_lo[h][x] = h < pc.heads
-          ? bin_lo(load_record(p.rec, ((int64_t)(pc.h0 + h) * p.s + x) * p.W + (pc.pos >> 5)), pc.pos)
-          : 0;
-    }
-    __syncthreads();
-    // each head's starts in ascending order, a start per thread by its rank
-    for (int k = tid; k < kHeads * p.s; k += kThreads) {
-      const int h = k / p.s, x = k % p.s, v = sm.raw_lo[h][x];
-      int rank = 0;
-      for (int y = 0; y < p.s; ++y) {
-        const int w = sm.raw_lo[h][y];
-        rank += w < v || (w == v && y < x);
-      }
-      sm.lo[h][rank] = v;
-    }
-    __syncthreads();
-    for (int h = 0; h < pc.heads; ++h) pc.first = min(pc.first, sm.lo[h][0]);
+    for (int w = 0; w < size; ++w) pc.first = min(pc.first, (int)sm.some[0][team.first + w]);
     const int t_first = pc.first >> 5, n = (pc.pos >> 5) + 1 - t_first;
     const int len = (n + shares - 1) / shares;
-    pc.t1 = t_first + n - share * len;             // share 0 the newest
+    pc.t1 = t_first + n - share * len;            // share 0 the newest
     pc.t0 = max(t_first, pc.t1 - len);
   }
-  if (none || pc.t0 >= pc.t1) {
-    if (shares == 1)
-      for (int e = tid; e < pc.heads * D; e += kThreads) o[e] = Elem<T>::put(0.f);
-    else if (tid < kHeads)
-      part[kHeads * D + tid] = kNothing, part[kHeads * D + kHeads + tid] = 0.f;
-    return;
-  }
-  attend<T, D, false, PACK>(p, pc, query, nullptr, sm, ring, ahead, shares == 1 ? o : nullptr, part);
+  T* o = static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D;
+  attend<T, D, false, PACK>(p, pc, team, query, nullptr, starts, sm, ring, ahead,
+                            valid && shares == 1 ? o : nullptr,
+                            valid && shares > 1 ? p.part + (int64_t)blockIdx.x * part_floats<D>() : nullptr);
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Groups gr) {
   grid_dep_wait();
-  const int units = p.c.H * p.chunks, u = blockIdx.x % units, b = blockIdx.x / units, h = blockIdx.y;
+  const int rows = p.c.B * p.chunks, k = blockIdx.x / rows, row = blockIdx.x - k * rows, h = blockIdx.y;
+  const int shares = gr.shares[gr.ordered ? k : 0];
   Piece pc;
-  unit_heads(p, u, pc);
-  const int shares = gr.ordered ? gr.shares_of[pc.kvh] : p.shares;
+  unit_heads(p, (gr.ordered ? gr.order[k] : k) * p.chunks + row % p.chunks, pc);
   if (h >= pc.heads || shares == 1) return;
-  // the row's first CTA: its KV head's, then (sequence, chunk, share)
-  int first = pc.kvh * p.c.B * p.chunks * shares;
-  if (gr.ordered) {
-    int k = 0;
-    while (gr.order[k] != pc.kvh) ++k;
-    first = gr.first[k];
-  }
-  first += (b * p.chunks + u % p.chunks) * shares;
+  const int first = (gr.ordered ? gr.first[k] : k * rows * shares) + row * shares;
   join_pieces<T, D>(p, first, first + 1, 1, shares, h,
-                    static_cast<T*>(p.o) + ((int64_t)b * p.Hq + pc.h0 + h) * D);
+                    static_cast<T*>(p.o) + ((int64_t)(row / p.chunks) * p.Hq + pc.h0 + h) * D);
 }
 
-int max_ctas(int num_sms) { return num_sms * kCtasPerSm; }
+int max_ctas(int num_sms) { return num_sms * kExactCtas; }
 
 template <typename T, int D>
 cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
+  using S = Smem<T, D, kExactWarps, kExactStages, 1>;
   Slopes s;
   for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
   const int64_t entries = (int64_t)p.c.B * p.c.H * p.chunks * ((p.limit + 31) / 32 + kRowCost);
   const int64_t want = (entries + kMinBlocks - 1) / kMinBlocks;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
   auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2> : q4_exact_kernel<T, D, 1>;
-  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
-  if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), kThreads, sizeof(Smem<T, D>), st, p, s);
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(S));
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), 32 * kExactWarps, sizeof(S), st, p, s);
   if (e == cudaSuccess) e = launch_dependent(q4_exact_join_kernel<T, D>, dim3(grid, p.per_chunk), 32 * kJoinWarps, 0, st, p);
   return e;
 }
 
 template <typename T, int D>
 cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
-  const int H = p.c.H;
-  const int64_t rows = (int64_t)p.c.B * p.chunks;          // of one KV head
+  const int H = p.c.H, rows = p.c.B * p.chunks;
   // The furthest of the s n bin starts of a KV head's n query heads lies about
   // sigma (1 + ln(s n)) back (the distance to a bin's start exceeds a with
-  // probability e^{-a/sigma} (1 + a / (2 sigma))).  A share for every
-  // kShareKeys of that, coarser while the shares outnumber two waves of CTAs.
-  constexpr double kShareKeys = 128.0;
+  // probability e^{-a/sigma} (1 + a / (2 sigma))).
   const double reach = 1.0 + log((double)p.s * std::min(p.G, kHeads));
   Groups gr;
   gr.ordered = H <= kMaxGroupOrder && a.sigma != nullptr;
-  double key[kMaxGroupOrder] = {};
-  double widest = a.sigma ? 0.0 : 1e30;
-  if (a.sigma)
-    for (int h = 0; h < a.Hq; ++h) {
-      widest = std::max(widest, a.sigma[h]);
-      if (gr.ordered) key[h / p.G] = std::max(key[h / p.G], a.sigma[h]);
-    }
-  if (gr.ordered) {
-    for (int k = 0; k < H; ++k) gr.order[k] = (uint8_t)k;
-    std::stable_sort(gr.order, gr.order + H, [&](int x, int y) { return key[x] > key[y]; });
+  const int groups = gr.ordered ? H : 1;
+  double blocks[kMaxGroupOrder] = {};             // a row's, expected, by KV head; [0] the widest if not ordered
+  for (int h = 0; h < a.Hq; ++h) {
+    const double sigma = a.sigma ? a.sigma[h] : 1e30;
+    double& x = blocks[gr.ordered ? h / p.G : 0];
+    x = std::max(x, std::min(reach * sigma, (double)p.limit) / 32.0 + 1.0);
   }
+  for (int k = 0; k < groups; ++k) gr.order[k] = (uint8_t)k;
+  std::stable_sort(gr.order, gr.order + groups, [&](int x, int y) { return blocks[x] > blocks[y]; });
+  // teams of kTeamBlocks blocks a warp, wider ones while all warps fit at once
+  const int64_t room = (int64_t)a.num_sms * kApproxCtas;
   int64_t grid = 0;
-  for (double keys = kShareKeys;; keys *= 2.0) {
-    auto shares = [&](double sigma) {
-      return (int)std::min((double)kMaxShares, std::min(reach * sigma, (double)p.limit) / keys + 1.0);
-    };
-    p.shares = shares(widest);
-    if (!gr.ordered) grid = rows * H * p.shares;
-    if (gr.ordered) {
-      grid = 0;
-      for (int k = 0; k < H; ++k) {
-        gr.shares_of[gr.order[k]] = (uint8_t)shares(key[gr.order[k]]);
-        gr.first[k] = (int)grid;
-        grid += rows * gr.shares_of[gr.order[k]];
-      }
-      gr.first[H] = (int)grid;
+  bool split = false;
+  for (double each = kTeamBlocks;; each *= 0.5) {
+    int64_t g = 0;
+    uint8_t team[kMaxGroupOrder];
+    for (int k = 0; k < groups; ++k) {
+      int size = 1;
+      while (size < kApproxWarps && size * each < blocks[gr.order[k]]) size *= 2;
+      team[k] = (uint8_t)size;
+      g += group_ctas(rows, size, 1);
     }
-    if (p.shares == 1 || grid <= 2 * max_ctas(a.num_sms)) break;
+    if (!gr.ordered) g *= H;
+    if (grid > 0 && (g > room || each < 1.0)) break;
+    std::copy(team, team + groups, gr.team);
+    grid = g;
   }
+  // and rows of more than kShareBlocks to several CTAs, evenly, while they fit
+  for (int k = 0; k < groups; ++k) gr.shares[k] = 1;
+  for (double each = kShareBlocks; each < blocks[gr.order[0]]; each *= 2.0) {
+    int64_t g = 0;
+    uint8_t shares[kMaxGroupOrder];
+    for (int k = 0; k < groups; ++k) {
+      shares[k] = (uint8_t)std::min((double)kMaxShares, std::max(1.0, ceil(blocks[gr.order[k]] / each)));
+      if (gr.team[k] < kApproxWarps) shares[k] = 1;
+      g += (int64_t)(gr.ordered ? 1 : H) * group_ctas(rows, gr.team[k], shares[k]);
+    }
+    if (g > room) continue;
+    std::copy(shares, shares + groups, gr.shares);
+    split = gr.shares[0] > 1;
+    grid = g;
+    break;
+  }
+  int64_t at = 0;
+  for (int k = 0; k < groups; ++k) {
+    gr.first[k] = (int)at;
+    at += group_ctas(rows, gr.team[k], gr.shares[k]);
+  }
+  gr.first[groups] = (int)at;
+  using S = Smem<T, D, kApproxWarps, kApproxStages, kApproxWarps>;
+  const size_t smem = sizeof(S) + sizeof(int4) * kApproxWarps * kHeads * ((p.s + 3) / 4);
   auto kern = p.per_chunk <= 4 ? q4_approx_kernel<T, D, 2> : q4_approx_kernel<T, D, 1>;
-  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(Smem<T, D>));
-  if (e == cudaSuccess) e = launch_dependent(kern, dim3((unsigned)grid), kThreads, sizeof(Smem<T, D>), st, p, gr);
-  if (e == cudaSuccess && p.shares > 1)
-    e = launch_dependent(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), p.per_chunk), 32 * kJoinWarps, 0, st, p, gr);
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern),
+                                 (int)(sizeof(S) + sizeof(int) * kApproxWarps * kHeads * kMaxS));
+  if (e == cudaSuccess)
+    e = launch_dependent(kern, dim3((unsigned)grid), 32 * kApproxWarps, smem, st, p, gr);
+  if (e == cudaSuccess && split)
+    e = launch_dependent(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), p.per_chunk),
+                         32 * kJoinWarps, 0, st, p, gr);
   return e;
 }
 
@@ -1123,7 +1208,6 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
   p.W = a.W;
   const int64_t held = a.c.max_pages << a.c.page_shift;
   p.limit = (int)(a.rec ? std::min(held, a.bins_n) : held);
-  p.shares = 1;
   p.ends = static_cast<int4*>(a.work);
   p.part = reinterpret_cast<float*>(p.ends + max_ctas(a.num_sms));
   p.err = a.err;
