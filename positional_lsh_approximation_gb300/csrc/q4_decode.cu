@@ -370,7 +370,7 @@ __device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, in
 // this together.  `starts`: its heads' bin starts, padded to whole int4 by numbers
 // that no position reaches.
 struct Team {
-  int first, size;
+  int first, size, number;     // number: of the CTA's teams
 };
 template <typename T, int D, bool EXACT, int PACK, int WARPS, int STAGES, int ROWS>
 __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Team& team,
@@ -384,7 +384,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   constexpr int kCols = kHeads / PACK;          // columns of a tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = warp - team.first, kTeam = team.size;
-  const int row = team.first / kTeam;           // the team's number in the CTA
+  const int row = EXACT ? 0 : team.number;
   const int mine = PACK == 2 ? t >> 1 : 0;      // the tile whose scores this lane holds
   const int head = (2 * t) % kCols;             // and its heads: head, head + 1
 
@@ -394,15 +394,15 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   const int steps = newest >= pc.t0 ? (newest - pc.t0) / kTeam + 1 : 0;
   int32_t next_page;
   {
-    int32_t pg[STAGES];
+    int32_t pg[STAGES + 1];
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) pg[i] = i < steps ? ring.page_of(newest - i * kTeam) : 0;
+    for (int i = 0; i <= STAGES; ++i) pg[i] = i < steps ? ring.page_of(newest - i * kTeam) : 0;
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
+    for (int i = 0; i < STAGES; ++i) {
       if (i < steps && !(ahead && i == 0)) ring.fetch(newest - i * kTeam, i, pg[i]);
       cp_async_commit();
     }
-    next_page = pg[STAGES - 1];
+    next_page = pg[STAGES];
   }
 
   if constexpr (EXACT) prepare_query<T, D, PACK>(query, rank, row, sm);
@@ -453,11 +453,6 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   const uint32_t v_at = ring.smem + 16 * lane;
   for (int i = 0, st = 0; i < steps; ++i, st = st == STAGES - 1 ? 0 : st + 1) {
     const int block = newest - i * kTeam;
-    if (i + STAGES - 1 < steps) {
-      ring.fetch(block - (STAGES - 1) * kTeam, st == 0 ? STAGES - 1 : st - 1, next_page);
-      if (i + STAGES < steps) next_page = ring.page_of(block - STAGES * kTeam);
-    }
-    cp_async_commit();
     cp_async_wait<STAGES - 1>();
     __syncwarp();
     const uint32_t gone = (ring.absent >> (2 * st)) & 3u;
@@ -664,6 +659,11 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
       }
     }
     __syncwarp();            // the stage may be filled again
+    if (i + STAGES < steps) {
+      ring.fetch(block - STAGES * kTeam, st, next_page);
+      if (i + STAGES + 1 < steps) next_page = ring.page_of(block - (STAGES + 1) * kTeam);
+    }
+    cp_async_commit();
   }
   cp_async_wait<0>();
 
@@ -783,10 +783,9 @@ __device__ __forceinline__ int64_t row_blocks(const DecodeParams& p, int b) {
   return pos < 0 || pos >= p.limit ? 0 : (pos >> 5) + 1;
 }
 
-// heads of unit u (a KV head and a share of its query heads)
-__device__ __forceinline__ void unit_heads(const DecodeParams& p, int u, Piece& pc) {
-  const int c = u % p.chunks;
-  pc.kvh = u / p.chunks;
+// heads of chunk c of a KV head
+__device__ __forceinline__ void unit_heads(const DecodeParams& p, int kvh, int c, Piece& pc) {
+  pc.kvh = kvh;
   pc.h0 = pc.kvh * p.G + c * p.per_chunk;
   pc.heads = min(p.per_chunk, p.G - c * p.per_chunk);
 }
@@ -872,7 +871,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     pc.t1 = (int)(till - row - kRowCost);
     f = till;
     if (pc.t1 <= pc.t0) continue;                 // the row's cost alone
-    unit_heads(p, u, pc);
+    unit_heads(p, u / p.chunks, u % p.chunks, pc);
     const bool last = till == row + n;
     if (tid == 0 && pc.t0 > 0 && last) {
       const int i0 = (int)((row + kRowCost) / per);    // the CTA of its first block
@@ -881,7 +880,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     Query<T, D, PACK> query;
     query.load(p, pc, tid >> 5);
     Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
-    attend<T, D, true, PACK>(p, pc, Team{0, kExactWarps}, query, slopes.v, nullptr, sm, ring, false,
+    attend<T, D, true, PACK>(p, pc, Team{0, kExactWarps, 0}, query, slopes.v, nullptr, sm, ring, false,
                              pc.t0 == 0 && last ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D
                                                 : nullptr,
                              p.part + (int64_t)slot * part_floats<D>());
@@ -968,7 +967,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __
   if (end.x < 0) return;
   const int units = p.c.H * p.chunks, h = blockIdx.y;
   Piece pc;
-  unit_heads(p, end.x % units, pc);
+  unit_heads(p, end.x % units / p.chunks, end.x % p.chunks, pc);
   if (h >= pc.heads) return;
   join_pieces<T, D>(p, end.z, 2 * (end.y + 1), 2, (int)blockIdx.x - end.y + 1, h,
                     static_cast<T*>(p.o) + ((int64_t)(end.x / units) * p.Hq + pc.h0 + h) * D);
@@ -984,7 +983,7 @@ struct Groups {
   int first[kMaxGroupOrder + 1];          // first CTA of each KV head, in order
   uint8_t order[kMaxGroupOrder];
   uint8_t shares[kMaxGroupOrder];         // CTAs of a row, in order
-  uint8_t team[kMaxGroupOrder];           // warps of a row, in order
+  uint8_t team[kMaxGroupOrder];           // log2 of the warps of a row, in order
   int ordered;                            // 0: index order, shares[0] and team[0] for all
 };
 
@@ -1007,7 +1006,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     while (k + 1 < p.c.H && cta >= gr.first[k + 1]) ++k;
     cta -= gr.first[k];
   }
-  const int size = gr.team[k], shares = gr.shares[k];
+  const int log_size = gr.team[k], size = 1 << log_size, shares = gr.shares[k];
   int kvh = gr.ordered ? gr.order[k] : 0;
   if (!gr.ordered) {
     const int each = group_ctas(rows, size, shares);
@@ -1016,17 +1015,19 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   }
   Team team;
   team.size = size;
-  team.first = warp / size * size;
-  const int rank = warp - team.first, tt = 32 * rank + lane, step = 32 * size;
+  team.first = warp & -size;
+  team.number = warp >> log_size;
+  const int rank = warp - team.first, number = team.number;
   const int share = shares > 1 ? cta % shares : 0;
-  const int row = shares > 1 ? cta / shares : cta * (kApproxWarps / size) + warp / size;
+  const int row = shares > 1 ? cta / shares : cta * (kApproxWarps >> log_size) + number;
   const bool valid = row < rows;
   Piece pc;
-  pc.b = valid ? row / p.chunks : 0;
-  unit_heads(p, kvh * p.chunks + row % p.chunks, pc);
+  const int b = p.chunks == 1 ? row : row / p.chunks;
+  pc.b = valid ? b : 0;
+  unit_heads(p, kvh, row - b * p.chunks, pc);
   pc.pos = valid ? p.pos[pc.b] : -1;
   const bool none = pc.pos < 0 || pc.pos >= p.limit;
-  if (valid && none && tt == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
+  if (valid && none && rank == 0 && lane == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
   Query<T, D, PACK> query;
   query.load(p, pc, rank);
   Ring<T, D> ring(p, pc, sm.ring[warp]);
@@ -1037,28 +1038,33 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   const int next = (pc.pos >> 5) - rank;
   bool ahead = share == 0 && !none && p.c.page_shift > 4 && next >= 0;
   int32_t next_page = ahead ? ring.page_of(next) : -1;
-  // the heads' bin starts; a thread's first one is on its way while the query
-  // is prepared
+  // the heads' bin starts: a head a warp and turn, a hash a lane; the first 32
+  // hashes' are on their way while the query is prepared
   const int quads = (p.s + 3) >> 2, width = 4 * quads;
-  int4* starts = reinterpret_cast<int4*>(raw + sizeof(S)) + (team.first / size) * kHeads * quads;
-  auto start_of = [&](int i) {
-    const int h = i / width, x = i - h * width;
-    if (x >= p.s) return INT_MAX;
-    if (h >= pc.heads) return 0;
+  int4* starts = reinterpret_cast<int4*>(raw + sizeof(S)) + number * kHeads * quads;
+  auto start_of = [&](int h, int x) {
     return bin_lo(load_record(p.rec, ((int64_t)(pc.h0 + h) * p.s + x) * p.W + (pc.pos >> 5)), pc.pos);
   };
-  const bool mine = !none && tt < kHeads * width;
-  int oldest = mine ? start_of(tt) : INT_MAX;
+  int v[kHeads];
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = rank + (i << log_size);
+    v[i] = h < pc.heads && lane < p.s && !none ? start_of(h, lane) : INT_MAX;
+  }
   ahead = ahead && (uint32_t)next_page < (uint32_t)p.c.pages;
   if (ahead) ring.fetch(next, 0, next_page);
-  prepare_query<T, D, PACK>(query, rank, team.first / size, sm);
-  if (mine) {
-    reinterpret_cast<int*>(starts)[tt] = oldest;
-    if (tt >= pc.heads * width) oldest = INT_MAX;
-    for (int i = tt + step; i < kHeads * width; i += step) {
-      const int v = start_of(i);
-      reinterpret_cast<int*>(starts)[i] = v;
-      if (i < pc.heads * width) oldest = min(oldest, v);
+  prepare_query<T, D, PACK>(query, rank, number, sm);
+  int oldest = INT_MAX;
+#pragma unroll
+  for (int i = 0; i < kHeads; ++i) {
+    const int h = rank + (i << log_size);
+    if (h >= kHeads) break;
+    oldest = min(oldest, v[i]);
+    if (lane < width) reinterpret_cast<int*>(starts)[h * width + lane] = v[i];
+    if (lane + 32 < width) {
+      const int w = h < pc.heads && lane + 32 < p.s && !none ? start_of(h, lane + 32) : INT_MAX;
+      oldest = min(oldest, w);
+      reinterpret_cast<int*>(starts)[h * width + lane + 32] = w;
     }
   }
   oldest = __reduce_min_sync(FULL, oldest);
@@ -1086,7 +1092,7 @@ q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_const
   const int rows = p.c.B * p.chunks, k = blockIdx.x / rows, row = blockIdx.x - k * rows, h = blockIdx.y;
   const int shares = gr.shares[gr.ordered ? k : 0];
   Piece pc;
-  unit_heads(p, (gr.ordered ? gr.order[k] : k) * p.chunks + row % p.chunks, pc);
+  unit_heads(p, gr.ordered ? gr.order[k] : k, row % p.chunks, pc);
   if (h >= pc.heads || shares == 1) return;
   const int first = (gr.ordered ? gr.first[k] : k * rows * shares) + row * shares;
   join_pieces<T, D>(p, first, first + 1, 1, shares, h,
@@ -1136,10 +1142,9 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
     int64_t g = 0;
     uint8_t team[kMaxGroupOrder];
     for (int k = 0; k < groups; ++k) {
-      int size = 1;
-      while (size < kApproxWarps && size * each < blocks[gr.order[k]]) size *= 2;
-      team[k] = (uint8_t)size;
-      g += group_ctas(rows, size, 1);
+      team[k] = 0;
+      while ((1 << team[k]) < kApproxWarps && (1 << team[k]) * each < blocks[gr.order[k]]) ++team[k];
+      g += group_ctas(rows, 1 << team[k], 1);
     }
     if (!gr.ordered) g *= H;
     if (grid > 0 && (g > room || each < 1.0)) break;
@@ -1153,8 +1158,8 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
     uint8_t shares[kMaxGroupOrder];
     for (int k = 0; k < groups; ++k) {
       shares[k] = (uint8_t)std::min((double)kMaxShares, std::max(1.0, ceil(blocks[gr.order[k]] / each)));
-      if (gr.team[k] < kApproxWarps) shares[k] = 1;
-      g += (int64_t)(gr.ordered ? 1 : H) * group_ctas(rows, gr.team[k], shares[k]);
+      if ((1 << gr.team[k]) < kApproxWarps) shares[k] = 1;
+      g += (int64_t)(gr.ordered ? 1 : H) * group_ctas(rows, 1 << gr.team[k], shares[k]);
     }
     if (g > room) continue;
     std::copy(shares, shares + groups, gr.shares);
@@ -1165,7 +1170,7 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
   int64_t at = 0;
   for (int k = 0; k < groups; ++k) {
     gr.first[k] = (int)at;
-    at += group_ctas(rows, gr.team[k], gr.shares[k]);
+    at += group_ctas(rows, 1 << gr.team[k], gr.shares[k]);
   }
   gr.first[groups] = (int)at;
   using S = Smem<T, D, kApproxWarps, kApproxStages, kApproxWarps>;
