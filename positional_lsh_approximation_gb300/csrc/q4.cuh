@@ -51,28 +51,25 @@ __device__ __forceinline__ uint8_t* tile_of(const Q4Cache& c, int b, int h, int6
 __device__ __forceinline__ float pair_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float pair_step(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// a / 15 correctly rounded, for a >= 0: from q = a y with y = 1 / 15 rounded,
-// the remainder r = a - 15 q is exact and q + r y rounds to the quotient
-// (Markstein's theorem on division by a number whose reciprocal is known
-// correctly rounded; checked here over every significand).  Quotients near the
-// end of fp32's range take the division.
-__device__ __forceinline__ float fifteenth(float a) {
-  constexpr float y = 1.f / 15.f;
-  if (a < 0x1p-100f) return __fdiv_rn(a, 15.f);
-  const float q = a * y;
-  return fmaf(fmaf(-15.f, q, a), y, q);
-}
-
-// The pair of a group with smallest and largest values mn and mx (NaN among
-// the values makes either NaN).
+// The pair of a group with smallest and largest values mn and mx (either is
+// NaN if one of the values is).  spread / 15 is correctly rounded: from
+// q = spread y with y = 1 / 15 rounded, the remainder r = spread - 15 q is exact
+// and q + r y rounds to the quotient (Markstein's theorem on division by a
+// number whose reciprocal is known correctly rounded; checked over every
+// significand).  Spreads near the ends of fp32's range take the division.
 __device__ __forceinline__ uint32_t make_pair(float mn, float mx) {
-  // mn rounded down, the spread's 15th rounded up, to the upper 16 bits
-  uint32_t lo = __float_as_uint(mn);
-  if (lo & 0xffffu) lo = (lo & 0xffff0000u) + ((lo >> 31) << 16);
+  // mn rounded down, the quotient rounded up, to the upper 16 bits
+  const uint32_t m = __float_as_uint(mn);
+  const uint32_t lo = (m & 0xffff0000u) + ((m & 0xffffu) && (m >> 31) ? 0x10000u : 0u);
   const float spread = mx - __uint_as_float(lo);
-  if (mn != mn || !(fabsf(spread) <= 3.402823466e38f)) return 0x7fc00000u;   // lo 0, step NaN
-  const uint32_t step = (__float_as_uint(fifteenth(spread)) + 0xffffu) & 0xffff0000u;
-  return (lo >> 16) | step;
+  constexpr float y = 1.f / 15.f;
+  float q = spread * y;
+  q = fmaf(fmaf(-15.f, q, spread), y, q);
+  if (!(spread >= 0x1p-100f && spread <= 3.402823466e38f)) {      // a constant group among them
+    if (!(mn == mn && spread <= 3.402823466e38f)) return 0x7fc00000u;       // lo 0, step NaN
+    q = __fdiv_rn(spread, 15.f);
+  }
+  return (lo >> 16) | ((__float_as_uint(q) + 0xffffu) & 0xffff0000u);
 }
 
 template <typename T> struct Elem;

@@ -128,12 +128,12 @@ __device__ __noinline__ uint32_t codes_by_division(float d0, float d1, float d2,
 
 // The same from products with the reciprocal (within an ulp), which are within
 // 15 (2^-23 + 2^-24) + 2^-21 < 2^-18 of the rounded quotients; that matters
-// next to a half alone.  There the remainder
-// e = d - c step is exact (c has four bits, step eight) and tells the side, or
-// the tie, which goes to the even code; a quotient within 2^-19 of a half but
-// not on it takes the division, and so does a step whose reciprocal or
-// products leave fp32's normal range.
-__device__ __forceinline__ uint32_t codes_of(const float* v, float lo, float step, float inv) {
+// next to a half alone.  There the remainder r = d - c step is exact (c has
+// four bits, step eight) and tells the side, or the tie, which goes to the even
+// code; a quotient within 2^-19 of a half but not on it takes the division, and
+// so does, with `rare`, a step whose reciprocal or products leave fp32's normal
+// range.
+__device__ __forceinline__ uint32_t codes_of(const float* v, float lo, float step, float inv, bool rare) {
   constexpr float kMagic = 12582912.f;            // 1.5 2^23: the sum rounds to an integer
   float d[4], c[4], off = 0.f;
 #pragma unroll
@@ -143,34 +143,33 @@ __device__ __forceinline__ uint32_t codes_of(const float* v, float lo, float ste
     c[e] = (t + kMagic) - kMagic;
     off = fmaxf(off, fabsf(t - c[e]));
   }
-  if (!(off <= 0.5f - 0x1p-18f) || !(step > 0x1p-100f && step < 0x1p100f)) {
-    bool close = !(step > 0x1p-100f && step < 0x1p100f);
+  if (off > 0.5f - 0x1p-18f || rare) {
+    bool close = rare;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float r = fmaf(-c[e], step, d[e]), past = fabsf(r) - 0.5f * step;
-      if (past == 0.f)
-        c[e] = rintf(c[e] + copysignf(0.5f, r));
-      else if (past > 0.f)
-        c[e] += copysignf(1.f, r);
-      close |= past != 0.f && fabsf(past) < step * 0x1p-19f;
+      const float r = fmaf(-c[e], step, d[e]), past = fmaf(-0.5f, step, fabsf(r));
+      const float half = copysignf(0.5f, r), even = rintf(c[e] + half);
+      c[e] = past == 0.f ? even : past > 0.f ? c[e] + 2.f * half : c[e];
+      close = close || (past != 0.f && fabsf(past) < step * 0x1p-19f);
     }
     if (close) return codes_by_division(d[0], d[1], d[2], d[3], step);
   }
   return four_codes(c);
 }
 
+// Two lanes a group, 16 values each (eights t and t + 2): what a group costs
+// beside its values (range, pair, reciprocal, addresses) is shared by more.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_constant__ Q4RowsArgs a) {
   using L = Layout<D>;
-  constexpr int kLanes = D / 8;                   // lanes of a row
+  constexpr int kLanes = D / 16;                  // lanes of a row
   constexpr int kRows = 32 / kLanes;              // rows of a pass
-  constexpr int kAhead = 2;                       // passes whose rows are in flight
   __shared__ alignas(16) uint8_t stage_s[kWarps][10 * D];    // a whole tile's codes and pairs
   grid_dep_wait();
   TileRows w;
   if (!tile_rows<D>(a, w)) return;
-  const int lane = threadIdx.x & 31, t = lane & 3, y = (lane % kLanes) >> 2, sub = lane / kLanes;
-  const T* src = static_cast<const T*>(w.value ? a.V : a.K) + w.row0 * D + (lane % kLanes) * 8;
+  const int lane = threadIdx.x & 31, t = lane & 1, y = (lane % kLanes) >> 1, sub = lane / kLanes;
+  const T* src = static_cast<const T*>(w.value ? a.V : a.K) + w.row0 * D + 32 * y + 8 * t;
   uint8_t* stage = stage_s[threadIdx.x >> 5];
   const bool whole = w.r0 == 0 && w.r1 == kTile;
   uint8_t* codes = w.tile + (w.value ? L::kV : 0);
@@ -178,42 +177,44 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
   uint8_t* c_at = whole ? stage : codes;
   uint8_t* p_at = whole ? stage + 8 * D : pairs;
   const int first = w.r0 / kRows * kRows;
-  Eight<T> raw[kAhead];
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int r = first + k * kRows + sub;
-    if (r >= w.r0 && r < w.r1) raw[k].load(src + (int64_t)r * D);
-  }
-  // (not unrolled: eight passes of it would not stay in the instruction cache)
+  Eight<T> raw[2];                                // of the pass ahead
+  auto load = [&](int r) {
+    if (r >= w.r0 && r < w.r1) {
+      raw[0].load(src + (int64_t)r * D);
+      raw[1].load(src + (int64_t)r * D + 16);
+    }
+  };
+  load(first + sub);
+  // (not unrolled: its passes would not stay in the instruction cache)
 #pragma unroll 1
   for (int r = first + sub; r - sub < w.r1; r += kRows) {
-    const Eight<T> now = raw[0];
-#pragma unroll
-    for (int k = 1; k < kAhead; ++k) raw[k - 1] = raw[k];
-    const int then = r + kAhead * kRows;
-    if (then < w.r1) raw[kAhead - 1].load(src + (int64_t)then * D);
-    float v[8], mn, mx;
-    now.get(v);
-    now.range(v, mn, mx);
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      mn = min_nan(mn, __shfl_xor_sync(FULL, mn, o));
-      mx = max_nan(mx, __shfl_xor_sync(FULL, mx, o));
-    }
+    float v[2][8], mn, mx, mn2, mx2;
+    raw[0].get(v[0]);
+    raw[0].range(v[0], mn, mx);
+    raw[1].get(v[1]);
+    raw[1].range(v[1], mn2, mx2);
+    mn = min_nan(mn, mn2);
+    mx = max_nan(mx, mx2);
+    load(r + kRows);
+    mn = min_nan(mn, __shfl_xor_sync(FULL, mn, 1));
+    mx = max_nan(mx, __shfl_xor_sync(FULL, mx, 1));
     if (r < w.r0 || r >= w.r1) continue;
     const uint32_t pair = make_pair(mn, mx);
     const float lo = pair_lo(pair), step = pair_step(pair);
-    uint32_t half[2] = {0, 0};
-    if (step > 0.f) {
-      const float inv = reciprocal(step);
-      half[0] = codes_of(v, lo, step, inv);
-      half[1] = codes_of(v + 4, lo, step, inv);
-    }
-    if (!w.value) {
-      *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * t)) = half[0] | (half[1] << 16);
-    } else {
-      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t) - L::kV) = (uint16_t)half[0];
-      *reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * t + 4) - L::kV) = (uint16_t)half[1];
+    const float inv = step > 0.f ? reciprocal(step) : 0.f;
+    const bool rare = !(step > 0x1p-100f && step < 0x1p100f) && step != 0.f;
+    const uint32_t keep = step > 0.f ? 0xffffu : 0u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t a0 = codes_of(v[k], lo, step, inv, rare) & keep;
+      const uint32_t a1 = codes_of(v[k] + 4, lo, step, inv, rare) & keep;
+      if (!w.value) {
+        *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * (t + 2 * k))) = a0 | (a1 << 16);
+      } else {
+        uint16_t* out = reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * (t + 2 * k)) - L::kV);
+        out[0] = (uint16_t)a0;
+        out[32] = (uint16_t)a1;                   // the next four values: 64 bytes on
+      }
     }
     if (t == 0) *reinterpret_cast<uint32_t*>(p_at + L::pair(r, y)) = pair;
   }
