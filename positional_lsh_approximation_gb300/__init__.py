@@ -13,8 +13,9 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 import numpy as np
@@ -81,6 +82,7 @@ def load():
         I32, I64, U64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
         D = ctypes.POINTER(ctypes.c_double)
         TP = ctypes.POINTER(_Tensor)
+        CP = ctypes.POINTER(_Q4Cache)
         sig = {
             "plsh_sample_bins": [I64, D, I32, I32, U64, P, ctypes.POINTER(P)],
             "plsh_bins_resample": [P, D, U64, P],
@@ -101,13 +103,12 @@ def load():
             "plsh_alibi_attn_host": [TP, TP, TP, P, I32, TP, P],
             "plsh_alibi_exact": [TP, TP, TP, D, I32, TP, P],
             "plsh_alibi_decode": [TP, TP, TP, P, I64, TP, P],
-            # (descriptors as plain pointers: packed bytes, or byref of a struct)
             "plsh_q4_cache_bytes": [I64, I64, I32, I32, ctypes.POINTER(I64)],
-            "plsh_q4_cache_write": [P, P, P, P, P, P],
-            "plsh_q4_cache_read": [P, P, P, P, P, P],
-            "plsh_q4_decode_work_bytes": [P, P, ctypes.POINTER(I64)],
-            "plsh_alibi_decode_q4": [P, P, P, P, P, P, I64, P],
-            "plsh_alibi_exact_decode_q4": [P, P, P, P, P, P, I64, P],
+            "plsh_q4_cache_write": [TP, TP, CP, P, P, P],
+            "plsh_q4_cache_read": [CP, P, P, TP, TP, P],
+            "plsh_q4_decode_work_bytes": [TP, CP, ctypes.POINTER(I64)],
+            "plsh_alibi_decode_q4": [TP, CP, P, P, TP, P, I64, P],
+            "plsh_alibi_exact_decode_q4": [TP, CP, D, P, TP, P, I64, P],
             "plsh_stream_status": [P],
             "plsh_noalloc_status": [P],
             "plsh_attn_path": [TP, P, I32, ctypes.POINTER(I32)],
@@ -388,45 +389,33 @@ def q4_cache_bytes(pages: int, H: int, page: int, d: int) -> int:
     return out.value
 
 
-# A decode step is a few microseconds on the device, so what the host does per
-# call shows: these calls pack their descriptors (the bytes of a plsh_tensor)
-# and pass raw pointers instead of building ctypes objects.
-_pack_tensor = struct.Struct("@Pi4x4q").pack
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
-    else torch.cuda.current_device
+_native = None
 
 
-def _device(what: str, cache: "Q4Cache") -> int:
-    """The current device, which must be the cache's."""
-    dev = _current_device()
-    if cache.device_index != dev:
-        raise ValueError(f"{what}: the cache is not on the current CUDA device")
-    return dev
+def _binding():
+    """The native binding of the 4-bit cache's calls; raises if it has not been
+    built."""
+    global _native
+    load()
+    with _lock:
+        if _native is None:
+            path = _build_mod.BINDING_PATH
+            if not os.path.exists(path):
+                raise RuntimeError(f"native binding not built ({path}); call "
+                                   "positional_lsh_approximation_gb300.build()")
+            loader = importlib.machinery.ExtensionFileLoader("_plsh_binding", path)
+            mod = importlib.util.module_from_spec(
+                importlib.util.spec_from_loader("_plsh_binding", loader))
+            loader.exec_module(mod)
+            mod.set_raise(_check)
+            _native = mod
+    return _native
 
 
-def _packed(what: str, t: torch.Tensor, dev: int) -> bytes:
-    """A contiguous [B, H, n, d] tensor on device `dev` as a plsh_tensor."""
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: tensors must be on the current CUDA device")
-    dt = _DT.get(t.dtype)
-    if dt is None or t.dim() != 4 or not t.is_contiguous():
-        _desc(t)                                  # says what is wrong
-    return _pack_tensor(t.data_ptr(), dt, *t.shape)
-
-
-def _i32(what: str, t: torch.Tensor, B: int, dev: int) -> int:
-    if t.get_device() != dev or t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != B \
-            or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor of B = {B} entries on the "
-                         "current CUDA device")
-    return t.data_ptr()
-
-
-def _raw(stream, dev: int):
-    """The stream's handle as an integer (the current stream's when None)."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    return _stream(stream)
+def _handle(stream):
+    """A given stream's handle as an integer, or None."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else \
+        None if stream is None else int(stream)
 
 
 class Q4Cache:
@@ -453,7 +442,7 @@ class Q4Cache:
         self._c = _Q4Cache(data.data_ptr(), table.data_ptr(), self.B, self.H, self.pages,
                            self.max_pages, self.page, self.d)
         self._packed = bytes(self._c)
-        self._work = {}                           # decode workspaces by stream and number of heads
+        self._work = {}                           # decode workspaces by stream
 
     @classmethod
     def empty(cls, pages: int, H: int, d: int, table: torch.Tensor, page: int = 64) -> "Q4Cache":
@@ -475,13 +464,8 @@ def q4_cache_write(cache: Q4Cache, K, V, pos, lens=None, stream=None):
     """plsh_q4_cache_write: rows i < lens[b] (all m without lens) of K, V
     [B, H, m, d] become positions pos[b] + i of the cache; pos, lens int32 [B]
     on the device."""
-    dev = _device("q4_cache_write", cache)
-    st = (_lib or load()).plsh_q4_cache_write(
-        _packed("q4_cache_write", K, dev), _packed("q4_cache_write", V, dev), cache._packed,
-        _i32("pos", pos, cache.B, dev), None if lens is None else _i32("lens", lens, cache.B, dev),
-        _raw(stream, dev))
-    if st:
-        _check(st)
+    (_native or _binding()).write(cache._packed, cache.device_index, K, V, pos, lens,
+                                  _handle(stream))
 
 
 def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=torch.bfloat16,
@@ -489,7 +473,6 @@ def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=to
     """plsh_q4_cache_read: (K, V) [B, H, m, d], the values of positions
     pos[b] + i, i < lens[b], of the cache.  `out`, a pair of tensors, keeps its
     other rows; without it they are new, of `dtype` and m rows, and zero there."""
-    dev = _device("q4_cache_read", cache)
     if out is None:
         if m is None:
             raise ValueError("q4_cache_read: give m, the rows of every sequence, or out")
@@ -497,65 +480,17 @@ def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=to
             out = tuple(torch.zeros(cache.B, cache.H, int(m), cache.d, dtype=dtype,
                                     device=cache.data.device) for _ in range(2))
     K, V = out
-    st = (_lib or load()).plsh_q4_cache_read(
-        cache._packed, _i32("pos", pos, cache.B, dev),
-        None if lens is None else _i32("lens", lens, cache.B, dev),
-        _packed("q4_cache_read", K, dev), _packed("q4_cache_read", V, dev), _raw(stream, dev))
-    if st:
-        _check(st)
+    (_native or _binding()).read(cache._packed, cache.device_index, K, V, pos, lens,
+                                 _handle(stream))
     return K, V
 
 
 def q4_decode_work_bytes(q, cache: Q4Cache) -> int:
     """plsh_q4_decode_work_bytes: workspace of a 4-bit decode call."""
-    dev = _device("q4_decode_work_bytes", cache)
-    out = ctypes.c_int64()
-    _check(load().plsh_q4_decode_work_bytes(_packed("q4_decode_work_bytes", q, dev), cache._packed,
+    out, tq = ctypes.c_int64(), _desc(q)
+    _check(load().plsh_q4_decode_work_bytes(ctypes.byref(tq), ctypes.byref(cache._c),
                                             ctypes.byref(out)))
     return out.value
-
-
-_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) \
-    or torch.cuda.is_current_stream_capturing
-
-
-def _decode_work(q, cache: Q4Cache, stream, raw: int) -> torch.Tensor:
-    """Workspace of a decode call: the cache keeps one for each stream that is
-    current when a call is made (calls on a stream run one after the other); a
-    call that is captured, or given a stream, takes one of its own, so that
-    graphs that replay at once share none."""
-    own = stream is not None or _capturing()
-    key = (raw, q.shape[1])
-    w = None if own else cache._work.get(key)
-    if w is None:
-        need = q4_decode_work_bytes(q, cache)
-        with _stream_scope(stream):
-            w = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if not own:
-            cache._work[key] = w
-    return w
-
-
-def _decode_q4(what, fn, q, cache, extra, pos, out, work, stream):
-    dev = _device(what, cache)
-    tq = _packed(what, q, dev)
-    raw = _raw(stream, dev)
-    w = _decode_work(q, cache, stream, raw) if work is None else work
-    if out is not None:
-        o, to = out, _packed(what, out, dev)
-    elif stream is None:
-        o = torch.empty_like(q)
-        to = _pack_tensor(o.data_ptr(), _DT[q.dtype], *q.shape)
-    else:
-        with _stream_scope(stream):
-            o = torch.empty_like(q)
-        to = _packed(what, o, dev)
-    if w.get_device() != dev or not w.is_contiguous():
-        raise ValueError(f"{what}: work must be contiguous memory of the current CUDA device")
-    st = fn(tq, cache._packed, extra, _i32("pos", pos, cache.B, dev), to, w.data_ptr(), w.nbytes, raw)
-    if st:
-        _check(st)
-    return o
 
 
 def alibi_decode_q4(q, cache: Q4Cache, bins: Bins, pos, out=None, work=None, stream=None):
@@ -563,19 +498,17 @@ def alibi_decode_q4(q, cache: Q4Cache, bins: Bins, pos, out=None, work=None, str
     sequence the row of T~ at its own position pos[b] (int32 [B] on the device;
     negative: an idle slot, o = 0), for the queries q [B, Hq, 1, d].  `work`:
     device memory of q4_decode_work_bytes that this call has for itself; without
-    it the cache keeps one per stream."""
-    return _decode_q4("alibi_decode_q4", (_lib or load()).plsh_alibi_decode_q4, q, cache,
-                      bins.handle, pos, out, work, stream)
+    it the cache keeps one for each stream that is current when a call is made,
+    and a call that is captured or given a stream takes its own."""
+    return (_native or _binding()).decode(cache._packed, cache.device_index, cache._work, q,
+                                          bins.handle.value, pos, out, work, _handle(stream))
 
 
 def alibi_exact_decode_q4(q, cache: Q4Cache, sigma, pos, out=None, work=None, stream=None):
     """plsh_alibi_exact_decode_q4: one decode step of exact ALiBi attention over
-    the 4-bit cache (see alibi_decode_q4)."""
-    sig = _f64(sigma)
-    if sig.shape != (q.shape[1],):
-        raise ValueError("alibi_exact_decode_q4: sigma must hold a scale per query head")
-    return _decode_q4("alibi_exact_decode_q4", (_lib or load()).plsh_alibi_exact_decode_q4, q,
-                      cache, sig.tobytes(), pos, out, work, stream)
+    the 4-bit cache (see alibi_decode_q4); sigma: a scale per query head."""
+    return (_native or _binding()).decode(cache._packed, cache.device_index, cache._work, q,
+                                          _f64(sigma).tobytes(), pos, out, work, _handle(stream))
 
 
 def bias_error(bins: Bins, sigma: float, h: int, lanczos_iters: int = 60, seed: int = 0,

@@ -1,7 +1,9 @@
 """Build libplsh.so (the C-ABI library) in-tree with nvcc for sm_103a.
 
 Each translation unit is compiled in parallel, then linked into one shared
-library next to this file (`_build/libplsh.so`).  No CMake.
+library next to this file (`_build/libplsh.so`).  The native binding of the
+4-bit cache's calls (`_build/_plsh_binding.so`, a Python extension against
+torch's headers) is compiled beside them and linked to it.  No CMake.
 """
 from __future__ import annotations
 
@@ -9,6 +11,7 @@ import concurrent.futures
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
@@ -16,6 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libplsh.so")
 SOURCES = ["api.cu", "sampler.cu", "attn_simt.cu", "attn_tc.cu", "decode.cu", "bias.cu", "bwd.cu",
            "bwd_tc.cu", "q4_cache.cu", "q4_decode.cu"]
+BINDING_PATH = os.path.join(BUILD_DIR, "_plsh_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-ffp-contract=off", "--expt-relaxed-constexpr"]
@@ -37,6 +41,29 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > os.path.getmtime(obj) for d in deps)
 
 
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _binding_compile(out: str) -> list:
+    import torch
+    t = os.path.join(_torch_dir(), "include")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I" + t, "-I" + os.path.join(t, "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+            "-c", os.path.join(SRC_DIR, "binding.cpp"), "-o", out]
+
+
+def _binding_link(obj: str, out: str) -> list:
+    return [shutil.which("g++") or "g++", "-shared", "-o", out, obj,
+            "-L" + os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L" + BUILD_DIR, "-lplsh",
+            "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     nv = nvcc()
@@ -50,16 +77,21 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    binding_obj = os.path.join(BUILD_DIR, "binding.o")
+    binding = force or _stale(binding_obj, os.path.join(SRC_DIR, "binding.cpp"))
+    if binding:
+        jobs.append(_binding_compile(binding_obj))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 print(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("compiler failed: " + " ".join(cmd) + "\n" + r.stderr)
     objs = [os.path.join(BUILD_DIR, s.replace(".cu", ".o")) for s in SOURCES]
     if jobs or not os.path.exists(LIB_PATH):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -68,6 +100,12 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB_PATH)
+    if binding or not os.path.exists(BINDING_PATH):
+        tmp = BINDING_PATH + f".tmp{os.getpid()}"
+        r = subprocess.run(_binding_link(binding_obj, tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
+        os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
 
