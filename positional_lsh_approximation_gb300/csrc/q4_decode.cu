@@ -149,6 +149,22 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// Two codes of a word as f16 operands: in bits 0 - 3 of each half (HIGH: 4 - 7,
+// as 16 c).  As they stand they are the subnormals c 2^-24; the matrix
+// instruction multiplies those exactly but aligns its sums as if they were
+// 2^-14, so that sums keep about 18 bits of their largest product: enough under
+// bf16 queries.  Under fp32 ones (NORMAL) they become the number c itself, by
+// way of 1024 + c.
+template <bool NORMAL, bool HIGH>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w) {
+  const uint32_t c = w & (HIGH ? 0x00f000f0u : 0x000f000fu);
+  if constexpr (NORMAL) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(c | 0x64006400u), "r"(0x64006400u));
+    return r;
+  }
+  return c;
+}
 // 2^e for -126 <= e <= 127, 0 below
 __device__ __forceinline__ float pow2(int e) {
   return e < -126 ? 0.f : __int_as_float((e + 127) << 23);
@@ -325,9 +341,12 @@ __device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, in
   mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
   const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 110);
   bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
-  const float up = pow2(14 - e);
+  // bf16: the largest in [2^14, 2^15); fp32: in [2^10, 2^11), as integers
+  constexpr int kTop = kTwo ? 10 : 14;
+  const float up = pow2(kTop - e);
   const float norm = kLog2e / sqrtf((float)D);
-  if (t == 0) sm.scale[row][g] = bad ? NAN : pow2(e + 10) * norm;       // 2^24 2^(e - 14)
+  // what q's power of two and a code's (2^-24, or 1) leave
+  if (t == 0) sm.scale[row][g] = bad ? NAN : pow2(e + (kTwo ? 0 : 24) - kTop) * norm;
   float group = 0.f;
 #pragma unroll
   for (int y = 0; y < Y; ++y) {
@@ -341,11 +360,15 @@ __device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // odd codes are taken four bits up, as 16 c
-      const float k = (i & 1) ? up * 0.0625f : up;
-      const float a = query.get(y, i) * k, b = query.get(y, i + 4) * k;
-      w[i] = pack_f16(a, b);
-      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w[i]));
-      r[i] = pack_f16(a - f.x, b - f.y);
+      const float k = (i & 1) ? 0.0625f : 1.f;
+      float a = query.get(y, i) * up, b = query.get(y, i + 4) * up;
+      if constexpr (kTwo) {
+        const float a0 = rintf(a), b0 = rintf(b);
+        r[i] = pack_f16(rintf((a - a0) * 2048.f) * k, rintf((b - b0) * 2048.f) * k);
+        a = a0;
+        b = b0;
+      }
+      w[i] = pack_f16(a * k, b * k);
     }
     sm.q[row][0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
     if constexpr (kTwo) sm.q[row][1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
@@ -492,13 +515,14 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         }
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
-          float c[4];
+          float c[4], c2[kTwo ? 4 : 1];
 #pragma unroll
           for (int u = 0; u < PACK; ++u) {
             const uint32_t v0 = k0[u][y], v1 = k1[u][y], h0 = v0 >> 8, h1 = v1 >> 8;
-            const uint32_t a[8] = {v0 & 0x000f000fu, v1 & 0x000f000fu, v0 & 0x00f000f0u,
-                                   v1 & 0x00f000f0u, h0 & 0x000f000fu, h1 & 0x000f000fu,
-                                   h0 & 0x00f000f0u, h1 & 0x00f000f0u};
+            const uint32_t a[8] = {two_codes<kTwo, false>(v0), two_codes<kTwo, false>(v1),
+                                   two_codes<kTwo, true>(v0),  two_codes<kTwo, true>(v1),
+                                   two_codes<kTwo, false>(h0), two_codes<kTwo, false>(h1),
+                                   two_codes<kTwo, true>(h0),  two_codes<kTwo, true>(h1)};
             uint32_t q[4];
             lds_at(q_at[u], y * kQ, q);
             if (u == 0)
@@ -508,9 +532,16 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
             mma16816<false>(c, a[4], a[5], a[6], a[7], q[2], q[3]);
             if constexpr (kTwo) {
               lds_at(q_at[u], (Y + y) * kQ, q);
-              mma16816<false>(c, a[0], a[1], a[2], a[3], q[0], q[1]);
-              mma16816<false>(c, a[4], a[5], a[6], a[7], q[2], q[3]);
+              if (u == 0)
+                mma16816_first<false>(c2, a[0], a[1], a[2], a[3], q[0], q[1]);
+              else
+                mma16816<false>(c2, a[0], a[1], a[2], a[3], q[0], q[1]);
+              mma16816<false>(c2, a[4], a[5], a[6], a[7], q[2], q[3]);
             }
+          }
+          if constexpr (kTwo) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = fmaf(c2[k], 0x1p-11f, c[k]);
           }
           const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
           x[0] = fmaf(s0, c[0], x[0]);
@@ -640,20 +671,36 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
           }
           e0 = transpose8x8(e0);
           e1 = transpose8x8(e1);
+          // fp32: the tile's own sums first, then added: the products' fp32 sums
+          // truncate, which over a long row would add up to one side
+          float own[kTwo ? 2 : 1][4];
 #pragma unroll
           for (int u = 0; u < PACK; ++u) {
             const uint32_t v0 = v4[u][2 * (y - yy)], v1 = v4[u][2 * (y - yy) + 1];
             const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
-            const uint32_t a[8] = {v0 & 0x000f000fu, v0 & 0x00f000f0u, v1 & 0x000f000fu,
-                                   v1 & 0x00f000f0u, h0 & 0x000f000fu, h0 & 0x00f000f0u,
-                                   h1 & 0x000f000fu, h1 & 0x00f000f0u};
+            const uint32_t a[8] = {two_codes<kTwo, false>(v0), two_codes<kTwo, true>(v0),
+                                   two_codes<kTwo, false>(v1), two_codes<kTwo, true>(v1),
+                                   two_codes<kTwo, false>(h0), two_codes<kTwo, true>(h0),
+                                   two_codes<kTwo, false>(h1), two_codes<kTwo, true>(h1)};
             const uint32_t b[4] = {e0 & keep[u], e1 & keep[u], f0 & keep[u], f1 & keep[u]};
-            mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[0], b[1]);
-            mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[0], b[1]);
             if constexpr (kTwo) {
-              mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[2], b[3]);
-              mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[2], b[3]);
+              if (u == 0) {
+                mma16816_first<false>(own[0], a[0], a[1], a[2], a[3], b[2], b[3]);
+                mma16816_first<false>(own[1], a[4], a[5], a[6], a[7], b[2], b[3]);
+              } else {
+                mma16816<false>(own[0], a[0], a[1], a[2], a[3], b[2], b[3]);
+                mma16816<false>(own[1], a[4], a[5], a[6], a[7], b[2], b[3]);
+              }
+              mma16816<false>(own[0], a[0], a[1], a[2], a[3], b[0], b[1]);
+              mma16816<false>(own[1], a[4], a[5], a[6], a[7], b[0], b[1]);
+            } else {
+              mma16816<false>(acc[y][0], a[0], a[1], a[2], a[3], b[0], b[1]);
+              mma16816<false>(acc[y][1], a[4], a[5], a[6], a[7], b[0], b[1]);
             }
+          }
+          if constexpr (kTwo) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[y][k >> 2][k & 3] += own[k >> 2][k & 3];
           }
         }
       }
@@ -688,10 +735,11 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         const float b = sum_rows(low[y][k]);
         const float up = most[y] == 0xffffu ? 0.f : pow2((int)(most[y] >> 23) - 132);
         float4 v;
-        v.x = fmaf(acc[y][0][k] * 0x1p24f, up, b);
-        v.y = fmaf(acc[y][0][2 + k] * 0x1p20f, up, b);
-        v.z = fmaf(acc[y][1][k] * 0x1p24f, up, b);
-        v.w = fmaf(acc[y][1][2 + k] * 0x1p20f, up, b);
+        constexpr float kLow = kTwo ? 1.f : 0x1p24f, kHigh = kTwo ? 0.0625f : 0x1p20f;
+        v.x = fmaf(acc[y][0][k] * kLow, up, b);
+        v.y = fmaf(acc[y][0][2 + k] * kHigh, up, b);
+        v.z = fmaf(acc[y][1][k] * kLow, up, b);
+        v.w = fmaf(acc[y][1][2 + k] * kHigh, up, b);
         *reinterpret_cast<float4*>(merge + (2 * t + k) * D + 32 * y + 4 * g) = v;
       }
     }
