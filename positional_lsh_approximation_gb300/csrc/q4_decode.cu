@@ -230,7 +230,7 @@ struct Smem {
   float m[WARPS][kHeads], l[WARPS][kHeads];
   float weight[2 * WARPS][kHeads + 1];   // of a warp's column in its head
   unsigned some[ROWS][kHeads];           // which of them saw anything (NaN too)
-  int64_t split[4];                      // exact: entries, entries of a CTA, first sequence and its first entry
+  int64_t sums[WARPS], found[2];         // exact: sequences' entries; the first sequence, its first entry
 };
 
 // Lane (g, t)'s values 8 t .. 8 t + 7 of every group of column g's query head.
@@ -851,59 +851,68 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   using S = Smem<T, D, kExactWarps, kExactStages, 1>;
   S& sm = *reinterpret_cast<S*>(raw);
   grid_dep_wait();
-  const int tid = threadIdx.x, units = p.c.H * p.chunks;
-  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
-    if (row_blocks(p, b) > 0) continue;
-    if (tid == 0 && p.pos[b] >= 0) atomicOr(p.err, kErrCachePlace);
-    for (int e = tid; e < p.Hq * D; e += 32 * kExactWarps)
-      static_cast<T*>(p.o)[(int64_t)b * p.Hq * D + e] = Elem<T>::put(0.f);
-  }
-  // prefix sums of the sequences' entries, a run of sequences per thread of
-  // the first warp
+  const int tid = threadIdx.x, warp = tid >> 5, units = p.c.H * p.chunks;
   auto row_entries = [&](int b) -> int64_t {
     const int64_t n = row_blocks(p, b);
     return n == 0 ? 0 : n + kRowCost;
   };
-  if (tid < 32) {
-    const int each = (p.c.B + 31) / 32;
-    const int b0 = min(p.c.B, tid * each), b1 = min(p.c.B, b0 + each);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) sum += row_entries(b);
-    int64_t upto = sum;
+  // all sequences' entries; idle sequences' rows (few) are zeroed on the way
+  int64_t sum = 0;
+#pragma unroll 4
+  for (int b = tid; b < p.c.B; b += 32 * kExactWarps) {
+    const int64_t n = row_entries(b);
+    sum += n;
+    if (n == 0 && b % gridDim.x == blockIdx.x) {
+      if (p.pos[b] >= 0) atomicOr(p.err, kErrCachePlace);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)b * p.Hq * D);
+      for (int e = 0; e < p.Hq * D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+  if ((tid & 31) == 0) sm.sums[warp] = sum;
+  if (tid == 0) p.ends[blockIdx.x].x = -1;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kExactWarps; ++w) total += sm.sums[w];
+  total *= units;
+  const int64_t fair = (total + gridDim.x - 1) / gridDim.x, per = fair < kMinBlocks ? kMinBlocks : fair;
+  const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
+  if (begin >= end) return;
+  // the sequence that entry `begin` is of, a turn of one sequence a thread
+  int64_t base = 0;                       // entries of one unit before the turn's sequences
+  for (int b0 = 0;; b0 += 32 * kExactWarps) {
+    const int64_t n = b0 + tid < p.c.B ? row_entries(b0 + tid) : 0;
+    int64_t upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(FULL, upto, o);
-      if (tid >= o) upto += v;
+      if ((tid & 31) >= o) upto += v;
     }
-    const int64_t total = __shfl_sync(FULL, upto, 31) * units;
-    const int64_t fair = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t per = fair < kMinBlocks ? kMinBlocks : fair;
-    const int64_t begin = blockIdx.x * per;
-    if (tid == 0) {
-      p.ends[blockIdx.x].x = -1;
-      sm.split[0] = total;
-      sm.split[1] = per;
+    __syncthreads();                      // the sums have been read
+    if ((tid & 31) == 31) sm.sums[warp] = upto;
+    __syncthreads();
+    int64_t turn = 0;
+#pragma unroll
+    for (int w = 0; w < kExactWarps; ++w) {
+      if (w < warp) upto += sm.sums[w];
+      turn += sm.sums[w];
     }
-    if (begin < total && begin >= (upto - sum) * units && begin < upto * units) {
-      int64_t at = upto - sum;
-      int b = b0;
-      for (;; ++b) {
-        const int64_t n = row_entries(b);
-        if (begin < (at + n) * units) break;
-        at += n;
+    if (begin < (base + turn) * units) {
+      if (begin >= (base + upto - n) * units && begin < (base + upto) * units) {
+        sm.found[0] = b0 + tid;
+        sm.found[1] = (base + upto - n) * units;
       }
-      sm.split[2] = b;
-      sm.split[3] = at * units;
+      break;
     }
+    base += turn;
   }
   __syncthreads();
-  const int64_t total = sm.split[0], per = sm.split[1];
-  const int64_t begin = blockIdx.x * per, end = min(total, begin + per);
-  if (begin >= end) return;
   Piece pc;
-  pc.b = (int)sm.split[2];
+  pc.b = (int)sm.found[0];
   pc.first = 0;
-  int64_t base = sm.split[3];
+  base = sm.found[1];
   int slot = 2 * blockIdx.x;
   for (int64_t f = begin; f < end;) {
     const int64_t n = row_entries(pc.b), rel = f - base;

@@ -390,6 +390,68 @@ def test_the_same_call_gives_the_same_bits():
         assert torch.equal(plsh.alibi_exact_decode_q4(s.q, s.cache, sig, pos, work=work), first)
 
 
+def test_many_sequences_with_idle_ones_among_them():
+    """More sequences than a block has threads, a third of them idle, some one
+    block long: the exact step's split runs over them all."""
+    B = 300
+    s = Setup(B, 2, 1, 64, 16, 100, "f32", seed=31)
+    pos = [-1 if b % 3 == 1 else (7 * b) % 100 if b % 2 else b % 20 for b in range(B)]
+    sigma = np.array([3.0, 40.0])
+    got = plsh.alibi_exact_decode_q4(s.q, s.cache, sigma, i32(pos))
+    plsh.stream_status()
+    s.check(got, pos, lambda p, n: q4.log_weights_exact(sigma, p, n))
+    bins = plsh.sample_bins(100, sigma, 3, 5)
+    off, st = bins.to_host()
+    got = plsh.alibi_decode_q4(s.q, s.cache, bins, i32(pos))
+    plsh.stream_status()
+    s.check(got, pos, lambda p, n: q4.log_weights_approx(off, st, 2, 3, p, n))
+    got = plsh.alibi_exact_decode_q4(s.q, s.cache, sigma, i32([-1] * B))
+    assert (got == 0).all()
+    bins.free()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [1, 6])
+def test_more_kv_heads_than_are_ordered(dtype, group):
+    """Forty KV heads (the approximate step orders up to 32 by their scales)."""
+    H = 40
+    s = Setup(2, H * group, H, 64, 64, 700, dtype, seed=33)
+    sigma = np.exp2(np.linspace(0, 11, H * group))
+    bins = plsh.sample_bins(700, sigma, 4, 6)
+    off, st = bins.to_host()
+    pos = [699, 310]
+    got = plsh.alibi_decode_q4(s.q, s.cache, bins, i32(pos))
+    plsh.stream_status()
+    s.check(got, pos, lambda p, n: q4.log_weights_approx(off, st, H * group, 4, p, n))
+    got = plsh.alibi_exact_decode_q4(s.q, s.cache, sigma, i32(pos))
+    plsh.stream_status()
+    s.check(got, pos, lambda p, n: q4.log_weights_exact(sigma, p, n))
+    bins.free()
+
+
+def test_pages_whose_bytes_begin_past_32_bits():
+    """The same rows in the first pages and in pages past 2^32 bytes."""
+    H, d, page = 8, 128, 256
+    one = plsh.q4_cache_bytes(1, H, page, d)
+    pages = 2 ** 32 // one + 40
+    table = i32([[0, 1, 2], [pages - 1, pages - 30, pages - 2]])
+    cache = plsh.Q4Cache.empty(pages, H, d, table, page)
+    g = torch.Generator("cuda").manual_seed(4)
+    k, v = (torch.randn(1, H, 700, d, device="cuda", generator=g).expand(2, -1, -1, -1).contiguous()
+            for _ in range(2))
+    q = torch.randn(1, 32, 1, d, device="cuda", generator=g).expand(2, -1, -1, -1).contiguous().bfloat16()
+    plsh.q4_cache_write(cache, k, v, i32([0, 0]))
+    sigma = alibi_sigmas(32)
+    bins = plsh.sample_bins(768, sigma, 6, 1)
+    o = plsh.alibi_decode_q4(q, cache, bins, i32([699, 699]))
+    assert torch.equal(o[0], o[1]) and torch.isfinite(o).all()
+    # alone, a row is cut as it is cut alone in the other place
+    e = [plsh.alibi_exact_decode_q4(q, cache, sigma, i32(p)) for p in ([699, -1], [-1, 699])]
+    plsh.stream_status()
+    assert torch.equal(e[0][0], e[1][1]) and torch.isfinite(e[0][0]).all() and (e[0][0] != 0).any()
+    bins.free()
+
+
 def test_shared_prefix_pages():
     """Two sequences whose tables name the same pages read the same keys.  (The
     exact step cuts the two rows at different tiles, so that their sums are
