@@ -7,41 +7,54 @@
 //   exact:        w_j = e^{-(pos - j) / sigma_h},     j <= pos
 // (Positional LSH, technical summary, Methodology 1 and 3, for one row.)
 //
-// What bounds it: the cache's bytes, 1.25 d a position and KV head.  At HBM
-// rate an SM has about 27 issue slots for a position of d = 128 (K and V), and
-// up to eight query heads share it; products on the CUDA cores would take
-// 2 d G / 32 of them alone, so they run as mma.sync m16n8k16 with the cached
-// values as the A operand (16 positions, or 16 values of a row) and the query
-// heads as the eight columns of B.  (tcgen05 takes A from shared or tensor
-// memory: the codes would be expanded to 16 bits, written there and read
-// again, which costs more than the products.)  The codes never become the
-// values they stand for:
+// What bounds it: the cache's bytes, 1.25 d a position and KV head, and next to
+// them the instructions of taking it apart.  At HBM rate an SM has about 27
+// issue slots for a position of d = 128 (K and V), which up to eight query
+// heads share; products on the CUDA cores would take 2 d G / 32 of them alone,
+// so they run as mma.sync m16n8k16 with the cached values as the A operand (16
+// positions, or 16 values of a row) and the query heads as the eight columns
+// of B.  (tcgen05 takes A from shared or tensor memory: the codes would be
+// expanded to 16 bits, written there and read again, 512 bytes a position,
+// which costs more than the products.)  The codes never become the values they
+// stand for:
 //   q . k_j = sum_y step_jy (sum_i q_yi c_jyi) + sum_y lo_jy (sum_i q_yi),
 //   sum_j p_j v_jyi = sum_j (p_j step_jy) c_jyi + sum_j p_j lo_jy,
 // so the products take the bare codes, step and lo act on sums of 32, in fp32.
-// A code becomes an f16 operand by one AND: c in the low bits of a half is the
-// subnormal c 2^-24, four bits up 16 c 2^-24, and the matrix instruction takes
-// subnormals exactly.  The cache holds the codes in the order of the operand
-// registers, so a word of eight codes gives four of them with four ANDs and a
-// shift.
-//   - q is scaled to f16 by a power of two per head (its largest magnitude in
-//     [2^14, 2^15); what is 2^-24 of that and less is lost); fp32 queries take
-//     two f16 terms, 22 bits.
+// The cache holds the codes in the order of the operand registers, so that a
+// word of eight codes gives four of them with four ANDs and a shift
+// (two_codes).
+//   - q is scaled to f16 by a power of two per head (bf16: its largest
+//     magnitude in [2^14, 2^15), exact down to 2^-24 of that; fp32: two terms
+//     of integers whose sums are exact, 22 bits).
 //   - p_j step_jy is scaled by a power of two per group that follows the
 //     largest step met, and rounded to f16 (2^-11 relative; fp32: two terms).
 //     f16 because bf16's 2^-8 would show beside the output's own rounding.
-// Each warp takes every kWarps-th tile of 16 positions with a maximum, row
-// sums and accumulators of its own, from a ring of asynchronous copies that
-// it alone fills and reads (no barrier in the loop); a warp's maximum moves
-// only when a score passes it by a factor 2^kLazy.  The warps of a CTA merge
-// in shared memory, pieces of a row that went to several CTAs in a second
-// kernel.
+// Each warp of a row's team takes every so-manieth block of 32 positions, with
+// a maximum, row sums and accumulators of its own, from a ring of asynchronous
+// copies that it alone fills and reads (no barrier in the loop); its maximum
+// moves only when a score passes it by a factor 2^kLazy.  The team merges in
+// shared memory, pieces of a row that went to several CTAs in a second kernel.
 //
-// Work split.  Exact: every CTA takes the same number of tiles of the flat
-// list (sequence, KV group, tile), found from the positions on the device, so
-// that ragged sequences balance.  Approximate: the row's key envelope is short
-// and known only after its bins are read; a CTA per (sequence, group), or a
-// few where the scales expect long envelopes and the grid is small.
+// Work split.  Exact: every CTA takes the same share of the flat list
+// (sequence, KV head, block), found from the positions on the device, so that
+// ragged sequences balance (counting 12 blocks for a row's beginning and end:
+// 75.6 -> 66.0 us for 64 ragged sequences).  Approximate: a row's key envelope
+// is short and known only after its bins are read; a team of 1 to 8 warps for
+// it, by the reach that its scales let expect.
+//
+// Measured on GB300 (CUDA graph, back to back; percentages of the measured copy
+// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 66
+// us (346 MB, 77 %); 2 x 131072 positions, 40/8 heads, 66 us (336 MB, 75 %);
+// one sequence of 8192 9.1 us.  Without the arithmetic the copies alone take
+// 57 us for the long case and the arithmetic alone 66: it is bound by
+// instructions (265 - 300 a tile of 16 positions, issued in 53 % of the cycles;
+// the logic pipe, which takes the ANDs, is 54 % busy).  Approximate, s = 10: 64
+// ragged sequences 14.5 us (24.5 MB), one 9.1 us: bound by latency (position,
+// bins, first block, 1.4 us a block in one warp, merge).
+// Tried and dropped: one more warp per scheduler at 128 registers (spills, 73
+// -> 79 us), products of the next block beside P V of this one (74 -> 81),
+// joining split rows in the CTA that arrives last (+3 us on the device),
+// 16-warp teams (14.6 -> 17.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -63,17 +76,22 @@ namespace {
 using namespace q4;
 using namespace ptx;
 
-// exact: three CTAs of four warps (168 registers a thread) and three blocks of
-// 32 positions in a warp's ring; approximate: two CTAs of eight warps, two
-// blocks (an envelope is a few blocks long)
+// Exact: three CTAs of four warps (168 registers a thread: 128 spill) and three
+// blocks of 32 positions in a warp's ring.  Approximate: two CTAs of eight
+// warps, two blocks (an envelope is a few blocks long).
 constexpr int kExactWarps = 4, kExactStages = 3, kExactCtas = 3;
 constexpr int kApproxWarps = 8, kApproxStages = 2, kApproxCtas = 2;
 constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
-constexpr int kMinBlocks = 8;       // exact: blocks of a CTA at least
-constexpr int kRowCost = 12;        // exact: blocks that beginning and ending a row costs
-constexpr int kMaxShares = 64;        // approximate: CTAs of one row at most
-constexpr double kTeamBlocks = 3.0;   // approximate: blocks of a warp, as a start
-constexpr double kShareBlocks = 40.0; // and of a CTA at most, while there is room
+// exact: blocks of a CTA at least (one sequence of 8192: 4 -> 12.2 us, 8 -> 8.9, 12 -> 9.8)
+constexpr int kMinBlocks = 8;
+// exact: blocks that beginning and ending a row costs (64 ragged sequences: 0 ->
+// 75.6 us, 6 -> 69.7, 12 -> 66.0, 20 -> 67.7)
+constexpr int kRowCost = 12;
+// approximate: blocks of a warp as a start (2 and 4 measure alike), of a CTA at
+// most while there is room (16 shaves 1 us off small grids, whose calls then
+// launch a second kernel, and costs 0.6 us on full ones), CTAs of one row at most
+constexpr double kTeamBlocks = 3.0, kShareBlocks = 40.0;
+constexpr int kMaxShares = 64;
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float kNothing = -3.402823466e38f;   // a maximum over no score
@@ -82,7 +100,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct Slopes {
   float v[kMaxExactHeads];          // log2(e) / sigma_h
 };
-struct NoSlopes {};
 
 struct DecodeParams {
   Q4Cache c;
