@@ -111,50 +111,68 @@ template <typename T> struct Eight {
   }
 };
 
-// Four codes as one number of 16 bits: c0 + 16 c1 + 256 c2 + 4096 c3, exact in
-// fp32, and as the low bits of its sum with 2^23.
-__device__ __forceinline__ uint32_t four_codes(const float* c) {
-  const float sum = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
-  return __float_as_uint(sum + 8388608.f) & 0xffffu;
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r, x, y, z;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
+}
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+
+// A code c is left as the bits of 1.5 2^23 + c, that is kMagicBits + c.
+constexpr float kMagic = 12582912.f;
+constexpr uint32_t kMagicBits = 0x4b400000u;
+
+// The word of eight codes, c0 + 16 c1 + ... + 16^7 c7, from such bits; their
+// constants add up to a constant (modulo 2^32).
+__device__ __forceinline__ uint32_t eight_codes(const float (&c)[8]) {
+  uint32_t w = __float_as_uint(c[0]) - kMagicBits * 0x11111111u;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) w += __float_as_uint(c[e]) << (4 * e);
+  return w;
 }
 
-// The codes of four values (d = x - lo) from the definition: the quotient
-// rounded to fp32, then to the nearest integer.
-__device__ __noinline__ uint32_t codes_by_division(float d0, float d1, float d2, float d3, float step) {
-  const float c[4] = {rintf(__fdiv_rn(d0, step)), rintf(__fdiv_rn(d1, step)),
-                      rintf(__fdiv_rn(d2, step)), rintf(__fdiv_rn(d3, step))};
-  return four_codes(c);
+// Eight codes from the definition: the quotient rounded to fp32, then to the
+// nearest integer.
+__device__ __noinline__ uint32_t codes_by_division(float d0, float d1, float d2, float d3, float d4, float d5,
+                                                   float d6, float d7, float step) {
+  const float c[8] = {__fdiv_rn(d0, step) + kMagic, __fdiv_rn(d1, step) + kMagic, __fdiv_rn(d2, step) + kMagic,
+                      __fdiv_rn(d3, step) + kMagic, __fdiv_rn(d4, step) + kMagic, __fdiv_rn(d5, step) + kMagic,
+                      __fdiv_rn(d6, step) + kMagic, __fdiv_rn(d7, step) + kMagic};
+  return eight_codes(c);
 }
 
-// The same from products with the reciprocal (within an ulp), which are within
-// 15 (2^-23 + 2^-24) + 2^-21 < 2^-18 of the rounded quotients; that matters
-// next to a half alone.  There the remainder r = d - c step is exact (c has
-// four bits, step eight) and tells the side, or the tie, which goes to the even
-// code; a quotient within 2^-19 of a half but not on it takes the division, and
-// so does, with `rare`, a step whose reciprocal or products leave fp32's normal
-// range.
-__device__ __forceinline__ uint32_t codes_of(const float* v, float lo, float step, float inv, bool rare) {
-  constexpr float kMagic = 12582912.f;            // 1.5 2^23: the sum rounds to an integer
-  float d[4], c[4], off = 0.f;
+// The same without a division (Markstein, 1990): q0 = d inv, with inv the
+// reciprocal of step within an ulp, is within three ulp of Q = d / step; the
+// remainder r = d - q0 step is exact (step has eight bits, so r has at most
+// eleven); and q0 + r inv, rounded once, is Q's rounding.  For its unrounded
+// value is within 3 2^-22 ulp of Q, and Q, unless it is an fp32 number itself,
+// is no nearer than 2^-9 ulp to a midpoint m of two of them: d - m step is a
+// multiple of half an ulp of Q times step's last bit, not zero (m step has 25
+// bits or more, d 24), and step is less than 256 of its last bits.  A step
+// whose reciprocal or products leave fp32's normal range is `rare` and takes
+// the division.
+// A pass of 32 lanes met an exact half (bf16 values: one in some hundreds)
+// nearly always, so settling halves in a branch cost every warp that branch;
+// this costs two packed products a pair of values.
+__device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float lo, float step, float inv, bool rare) {
+  float d[8], c[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    d[e] = v[e] - lo;
-    const float t = d[e] * inv;
-    c[e] = (t + kMagic) - kMagic;
-    off = fmaxf(off, fabsf(t - c[e]));
+  for (int e = 0; e < 8; e += 2) {
+    const float2 x = fma2(make_float2(v[e], v[e + 1]), two(1.f), two(-lo));
+    const float2 q0 = fma2(x, two(inv), two(0.f));
+    const float2 r = fma2(q0, two(-step), x);
+    const float2 q = fma2(r, two(inv), q0);
+    const float2 k = fma2(q, two(1.f), two(kMagic));
+    d[e] = x.x, d[e + 1] = x.y;
+    c[e] = k.x, c[e + 1] = k.y;
   }
-  if (off > 0.5f - 0x1p-18f || rare) {
-    bool close = rare;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float r = fmaf(-c[e], step, d[e]), past = fmaf(-0.5f, step, fabsf(r));
-      const float half = copysignf(0.5f, r), even = rintf(c[e] + half);
-      c[e] = past == 0.f ? even : past > 0.f ? c[e] + 2.f * half : c[e];
-      close = close || (past != 0.f && fabsf(past) < step * 0x1p-19f);
-    }
-    if (close) return codes_by_division(d[0], d[1], d[2], d[3], step);
-  }
-  return four_codes(c);
+  if (rare) return codes_by_division(d[0], d[1], d[2], d[3], d[4], d[5], d[6], d[7], step);
+  return eight_codes(c);
 }
 
 // Two lanes a group, 16 values each (eights t and t + 2): what a group costs
@@ -203,17 +221,16 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
     const float lo = pair_lo(pair), step = pair_step(pair);
     const float inv = step > 0.f ? reciprocal(step) : 0.f;
     const bool rare = !(step > 0x1p-100f && step < 0x1p100f) && step != 0.f;
-    const uint32_t keep = step > 0.f ? 0xffffu : 0u;
+    const uint32_t keep = step > 0.f ? 0xffffffffu : 0u;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const uint32_t a0 = codes_of(v[k], lo, step, inv, rare) & keep;
-      const uint32_t a1 = codes_of(v[k] + 4, lo, step, inv, rare) & keep;
+      const uint32_t w8 = codes_of(v[k], lo, step, inv, rare) & keep;
       if (!w.value) {
-        *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * (t + 2 * k))) = a0 | (a1 << 16);
+        *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * (t + 2 * k))) = w8;
       } else {
         uint16_t* out = reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * (t + 2 * k)) - L::kV);
-        out[0] = (uint16_t)a0;
-        out[32] = (uint16_t)a1;                   // the next four values: 64 bytes on
+        out[0] = (uint16_t)w8;
+        out[32] = (uint16_t)(w8 >> 16);           // the next four values: 64 bytes on
       }
     }
     if (t == 0) *reinterpret_cast<uint32_t*>(p_at + L::pair(r, y)) = pair;
