@@ -501,7 +501,11 @@ plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache*
  * whose page index is not in [0, pages) counts as absent; either is reported
  * as PLSH_ERR_INVALID by plsh_stream_status.  A key or value of c_j = 0, a
  * position past pos[b] and whatever else a page holds have no effect, be it
- * NaN.  Asynchronous on `stream`; allocates nothing; may be captured.
+ * NaN.  A head whose q holds a NaN or an infinity, or reaches 2^110, gives a
+ * row of NaN.  bf16: products of codes with q run as f16 ones of q scaled by a
+ * power of two, so a value below 2^-24 of its head's largest counts as 0, and
+ * P step is rounded to f16; fp32: two such terms each, about 22 bits.  Sums
+ * are fp32's.  Asynchronous on `stream`; allocates nothing; may be captured.
  */
 plsh_status plsh_alibi_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
                                  const plsh_bins* bins, const int32_t* pos, plsh_tensor* o,

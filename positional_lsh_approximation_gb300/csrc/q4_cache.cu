@@ -70,12 +70,12 @@ __device__ __forceinline__ float reciprocal(float x) {      // within an ulp
   return r;
 }
 
-// Eight consecutive values of a row: 16 bytes of bf16, 32 of fp32.
+// Eight consecutive values of a row: 16 bytes of bf16, 32 of fp32; read once.
 template <typename T> struct Eight {
   uint4 w[sizeof(T) / 2];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = reinterpret_cast<const uint4*>(p)[k];
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) w[k] = __ldcs(reinterpret_cast<const uint4*>(p) + k);
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
