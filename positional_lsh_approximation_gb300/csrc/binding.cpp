@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <mutex>
 #include <optional>
 #include <stdexcept>
 #include <string>
@@ -142,8 +143,10 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The call's workspace: `kept`, a dict of the cache, has one for each stream
 // that is current when a call is made (calls on a stream run one after the
-// other); a call that is captured, or given a stream, takes one of its own, so
-// that graphs that replay at once share none.
+// other; g_launch keeps the launches of two threads' calls apart); a call that
+// is captured, or given a stream, takes one of its own, so that graphs that
+// replay at once share none.
+std::mutex g_launch;
 at::Tensor workspace(const Call& c, const plsh_tensor& q, const at::Tensor& like, PyObject* kept) {
   const bool own = c.given.has_value() || c10::cuda::currentStreamCaptureStatusMayInitCtx() !=
                                               c10::cuda::CaptureStatus::None;
@@ -220,6 +223,9 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t bytes = (int64_t)w.nbytes();
     const double* sigma = exact ? reinterpret_cast<const double*>(PyBytes_AS_STRING(a[4])) : nullptr;
     const bool ok = ran([&] {
+      // a call's kernels follow one another on the stream, with no other call's
+      // between them that writes the same workspace
+      const std::lock_guard<std::mutex> hold(g_launch);
       return exact ? plsh_alibi_exact_decode_q4(&tq, &c.cache, sigma, pos, &to, work, bytes, st)
                    : plsh_alibi_decode_q4(&tq, &c.cache, static_cast<const plsh_bins*>(bins), pos, &to,
                                           work, bytes, st);

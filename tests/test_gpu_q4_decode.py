@@ -16,6 +16,8 @@ weigh 2^-40), R the largest |lo| + 15 step of V and S the largest 15 step:
     f16 term), times a code's S;
   - the output's rounding: 2^-24 or 2^-8 of |o|.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -378,6 +380,28 @@ def test_two_streams_and_two_graphs_with_their_own_workspaces():
         assert torch.equal(ga, wa) and torch.equal(gb, wb)
     plsh.stream_status()
     bins.free()
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two threads on one stream share the cache's workspace; the
+    kernels of one are not parted by the other's."""
+    s = Setup(6, 8, 2, 128, 64, 3000, "bf16", seed=11)
+    sig = alibi_sigmas(8)
+    at = [i32([2999 - 17 * b for b in range(6)]), i32([100 + 450 * b for b in range(6)])]
+    want = [plsh.alibi_exact_decode_q4(s.q, s.cache, sig, p) for p in at]
+    got = [[], []]
+
+    def work(k):
+        for _ in range(200):
+            got[k].append(plsh.alibi_exact_decode_q4(s.q, s.cache, sig, at[k]))
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert len(got[k]) == 200 and all(torch.equal(o, want[k]) for o in got[k])
 
 
 def test_the_same_call_gives_the_same_bits():
