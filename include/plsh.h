@@ -473,8 +473,8 @@ plsh_status plsh_q4_cache_write(const plsh_tensor* K, const plsh_tensor* V,
  * the cache stand for, as rows of K and V [B, H, m, d] (PLSH_BF16, rounded
  * once, or PLSH_F32, exact up to one fp32 rounding).  Rows from len[b] on, and
  * rows whose position or page index is out of range (reported as for
- * plsh_q4_cache_write), are left as they were.  Asynchronous on `stream`;
- * allocates nothing.
+ * plsh_q4_cache_write), are left as they were.  K and V must not overlap.
+ * Asynchronous on `stream`; allocates nothing.
  */
 plsh_status plsh_q4_cache_read(const plsh_q4_cache* cache, const int32_t* pos,
                                const int32_t* len, plsh_tensor* K, plsh_tensor* V,
@@ -491,7 +491,8 @@ plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache*
  *   o_b = sum_j c_j e^{S_j} v_j / sum_j c_j e^{S_j},  S_j = q_b . k_j / sqrt(d),
  *   c_j = #{t : lo_t(pos[b]) <= j},  j in [min_t lo_t(pos[b]), pos[b]],
  * with k_j, v_j the cached values.
- *   q, o [B, Hq, 1, d], PLSH_BF16 or PLSH_F32; Hq a multiple of the cache's H;
+ *   q, o [B, Hq, 1, d], PLSH_BF16 or PLSH_F32, which must not overlap; Hq a
+ *        multiple of the cache's H;
  *   bins->H == Hq, bins of any length: pos[b] must lie below bins->n.
  *   pos  device int32 [B]; a negative one is an idle slot: o_b = 0.
  *   work device memory of plsh_q4_decode_work_bytes, 16-byte aligned, used by

@@ -1357,6 +1357,12 @@ plsh_status check_q4_cache(const plsh_q4_cache* c, plsh::Q4Cache* out) {
   return PLSH_OK;
 }
 
+bool q4_overlap(const plsh_tensor* a, const plsh_tensor* b) {     // of one shape and type
+  const uint64_t bytes = (uint64_t)a->B * a->H * a->n * a->d * (a->dtype == PLSH_F32 ? 4 : 2);
+  const uintptr_t x = (uintptr_t)a->data, y = (uintptr_t)b->data;
+  return x < y ? y - x < bytes : x - y < bytes;
+}
+
 plsh_status q4_rows(const plsh_tensor* K, const plsh_tensor* V, const plsh_q4_cache* cache,
                     const int32_t* pos, const int32_t* len, bool write, cudaStream_t cs) {
   plsh_status st;
@@ -1373,6 +1379,7 @@ plsh_status q4_rows(const plsh_tensor* K, const plsh_tensor* V, const plsh_q4_ca
   if (pos == nullptr) return fail(PLSH_ERR_INVALID, "pos is NULL");
   if ((((uintptr_t)pos | (uintptr_t)len) & 3u) != 0)
     return fail(PLSH_ERR_INVALID, "pos and len must be int32 device pointers");
+  if (!write && q4_overlap(K, V)) return fail(PLSH_ERR_INVALID, "K and V must not overlap");
   plsh::DeviceCtx* ctx = nullptr;
   if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
   a.K = K->data;
@@ -1410,6 +1417,8 @@ plsh_status q4_decode(const plsh_tensor* q, const plsh_q4_cache* cache, const pl
     return fail(PLSH_ERR_INVALID, "o must have q's shape and dtype");
   if (pos == nullptr || ((uintptr_t)pos & 3u) != 0)
     return fail(PLSH_ERR_INVALID, "pos must be an int32 device pointer");
+  // (a row may be read by several CTAs, one of them done before another begins)
+  if (q4_overlap(q, o)) return fail(PLSH_ERR_INVALID, "o must not overlap q");
   if (bins != nullptr) {
     if (bins->H != q->H) return fail(PLSH_ERR_INVALID, "bins were drawn for another number of heads");
     if ((st = check_bins_device(bins)) != PLSH_OK) return st;

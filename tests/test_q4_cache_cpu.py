@@ -184,6 +184,25 @@ def test_bad_queries_are_refused(lib):
         == plsh.PLSH_ERR_INVALID                                       # bins NULL
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    r = ctypes.byref
+    c = cache()
+    sig = np.ones(4)
+    sp = sig.ctypes.data_as(ctypes.POINTER(ctypes.c_double))
+    k = T(PTR, 1, 2, 2, 5, 128)
+    q = T(PTR, 1, 2, 4, 1, 128)
+    rows, row = 2 * 2 * 5 * 128 * 2, 2 * 4 * 128 * 2
+    for off in (0, 16, rows - 16, 16 - rows):
+        v = T(PTR + off, 1, 2, 2, 5, 128)
+        assert lib.plsh_q4_cache_read(r(c), PTR, None, r(k), r(v), None) == plsh.PLSH_ERR_INVALID
+        assert b"overlap" in lib.plsh_last_error()
+    for off in (0, 16, row - 16, 16 - row):
+        o = T(PTR + off, 1, 2, 4, 1, 128)
+        assert lib.plsh_alibi_exact_decode_q4(r(q), r(c), sp, PTR, r(o), PTR, 1 << 40, None) \
+            == plsh.PLSH_ERR_INVALID
+        assert b"overlap" in lib.plsh_last_error()
+
+
 def test_binding_refuses_host_tensors():
     data = torch.zeros(plsh.q4_cache_bytes(2, 1, 16, 64), dtype=torch.uint8)
     table = torch.zeros(1, 2, dtype=torch.int32)
