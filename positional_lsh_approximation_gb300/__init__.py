@@ -422,7 +422,11 @@ class Q4Cache:
     """A 4-bit paged K/V cache (plsh_q4_cache): `data`, uint8 device memory of
     pages * H * (page / 16) * 20 d bytes, and `table`, int32 [B, max_pages], the
     page of every sequence's positions [i page, (i + 1) page).  Both belong to
-    the caller, who may change their contents between calls."""
+    the caller, who may change their contents between calls; a cache of other
+    tensors is another Q4Cache."""
+
+    data = property(lambda self: self._data)
+    table = property(lambda self: self._table)
 
     def __init__(self, data: torch.Tensor, table: torch.Tensor, H: int, d: int, page: int = 64):
         one = q4_cache_bytes(1, H, page, d)
@@ -434,7 +438,7 @@ class Q4Cache:
             raise ValueError("Q4Cache: table must be contiguous int32 [B, max_pages]")
         if data.device.type != "cuda" or table.device != data.device:
             raise ValueError("Q4Cache: data and table must be on one CUDA device")
-        self.data, self.table = data, table
+        self._data, self._table = data, table
         self.H, self.d, self.page = int(H), int(d), int(page)
         self.B, self.max_pages = table.shape
         self.pages = data.numel() // one

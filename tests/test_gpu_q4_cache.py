@@ -256,3 +256,12 @@ def test_binding_refuses_what_it_cannot_pass_on():
         plsh.q4_cache_write(cache, k.cpu(), v, pos)
     with pytest.raises(plsh.PlshError):
         plsh.q4_cache_write(cache, k[:1].contiguous(), v[:1].contiguous(), pos)
+
+
+def test_tensors_of_a_cache_are_not_exchanged():
+    """A call's addresses are taken when the cache is made."""
+    cache = plsh.Q4Cache.empty(4, 1, 64, torch.zeros(1, 4, dtype=torch.int32, device="cuda"), 16)
+    with pytest.raises(AttributeError):
+        cache.table = cache.table.clone()
+    with pytest.raises(AttributeError):
+        cache.data = cache.data.clone()

@@ -189,15 +189,16 @@ def test_outputs_that_overlap_are_refused(lib):
     c = cache()
     sig = np.ones(4)
     sp = sig.ctypes.data_as(ctypes.POINTER(ctypes.c_double))
-    k = T(PTR, 1, 2, 2, 5, 128)
-    q = T(PTR, 1, 2, 4, 1, 128)
+    base = 1 << 20
+    k = T(base, 1, 2, 2, 5, 128)
+    q = T(base, 1, 2, 4, 1, 128)
     rows, row = 2 * 2 * 5 * 128 * 2, 2 * 4 * 128 * 2
     for off in (0, 16, rows - 16, 16 - rows):
-        v = T(PTR + off, 1, 2, 2, 5, 128)
+        v = T(base + off, 1, 2, 2, 5, 128)
         assert lib.plsh_q4_cache_read(r(c), PTR, None, r(k), r(v), None) == plsh.PLSH_ERR_INVALID
         assert b"overlap" in lib.plsh_last_error()
     for off in (0, 16, row - 16, 16 - row):
-        o = T(PTR + off, 1, 2, 4, 1, 128)
+        o = T(base + off, 1, 2, 4, 1, 128)
         assert lib.plsh_alibi_exact_decode_q4(r(q), r(c), sp, PTR, r(o), PTR, 1 << 40, None) \
             == plsh.PLSH_ERR_INVALID
         assert b"overlap" in lib.plsh_last_error()
