@@ -22,7 +22,8 @@
 // so the products take the bare codes, step and lo act on sums of 32, in fp32.
 // The cache holds the codes in the order of the operand registers, so that a
 // word of eight codes gives four of them with four ANDs and a shift
-// (two_codes).
+// (two_codes), or, where the sums of c + 16 c' may stand for those of c', three
+// ANDs and a byte permutation (V: 66.4 -> 65.0 us for 64 ragged sequences).
 //   - q is scaled to f16 by a power of two per head (bf16: its largest
 //     magnitude in [2^14, 2^15), exact down to 2^-24 of that; fp32: two terms
 //     of integers whose sums are exact, 22 bits).
@@ -43,17 +44,18 @@
 // it, by the reach that its scales let expect.
 //
 // Measured on GB300 (CUDA graph, back to back; percentages of the measured copy
-// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 66
-// us (346 MB, 77 %); 2 x 131072 positions, 40/8 heads, 66 us (336 MB, 75 %);
-// one sequence of 8192 9.1 us.  Without the arithmetic the copies alone take
+// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 65
+// us (346 MB, 78 %); 2 x 131072 positions, 40/8 heads, 65 us (336 MB, 76 %);
+// one sequence of 8192 9.2 us.  Without the arithmetic the copies alone take
 // 57 us for the long case and the arithmetic alone 66: it is bound by
-// instructions (265 - 300 a tile of 16 positions, issued in 53 % of the cycles;
+// instructions (about 260 - 300 a tile of 16 positions, issued in 53 % of the cycles;
 // the logic pipe, which takes the ANDs, is 54 % busy).  Approximate, s = 10: 64
 // ragged sequences 14.5 us (24.5 MB), one 9.1 us: bound by latency (position,
 // bins, first block, 1.4 us a block in one warp, merge).
 // Tried and dropped: one more warp per scheduler at 128 registers (spills, 73
 // -> 79 us), products of the next block beside P V of this one (74 -> 81),
-// joining split rows in the CTA that arrives last (+3 us on the device),
+// K's codes as e4m3 operands of m16n8k32 (half the ANDs, but 65 -> 83), joining
+// split rows in the CTA that arrives last (+3 us on the device),
 // 16-warp teams (14.6 -> 17.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -172,15 +174,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 // 2^-14, so that sums keep about 18 bits of their largest product: enough under
 // bf16 queries.  Under fp32 ones (NORMAL) they become the number c itself, by
 // way of 1024 + c.
-template <bool NORMAL, bool HIGH>
-__device__ __forceinline__ uint32_t two_codes(uint32_t w) {
-  const uint32_t c = w & (HIGH ? 0x00f000f0u : 0x000f000fu);
+template <bool NORMAL>
+__device__ __forceinline__ uint32_t f16_codes(uint32_t c) {
   if constexpr (NORMAL) {
     uint32_t r;
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(c | 0x64006400u), "r"(0x64006400u));
     return r;
   }
   return c;
+}
+template <bool NORMAL, bool HIGH>
+__device__ __forceinline__ uint32_t two_codes(uint32_t w) {
+  return f16_codes<NORMAL>(w & (HIGH ? 0x00f000f0u : 0x000f000fu));
 }
 // 2^e for -126 <= e <= 127, 0 below
 __device__ __forceinline__ float pow2(int e) {
@@ -694,11 +699,14 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
 #pragma unroll
           for (int u = 0; u < PACK; ++u) {
             const uint32_t v0 = v4[u][2 * (y - yy)], v1 = v4[u][2 * (y - yy) + 1];
-            const uint32_t h0 = v0 >> 8, h1 = v1 >> 8;
-            const uint32_t a[8] = {two_codes<kTwo, false>(v0), two_codes<kTwo, true>(v0),
-                                   two_codes<kTwo, false>(v1), two_codes<kTwo, true>(v1),
-                                   two_codes<kTwo, false>(h0), two_codes<kTwo, true>(h0),
-                                   two_codes<kTwo, false>(h1), two_codes<kTwo, true>(h1)};
+            // rows of c and of c + 16 c', whose c the merge takes off again: a
+            // byte permutation gives the latter for the upper bytes at once
+            const uint32_t n0 = v0 & 0x00ff00ffu, n1 = v1 & 0x00ff00ffu;
+            const uint32_t h0 = __byte_perm(v0, 0, 0x4341), h1 = __byte_perm(v1, 0, 0x4341);
+            const uint32_t a[8] = {two_codes<kTwo, false>(v0), f16_codes<kTwo>(n0),
+                                   two_codes<kTwo, false>(v1), f16_codes<kTwo>(n1),
+                                   two_codes<kTwo, false>(h0), f16_codes<kTwo>(h0),
+                                   two_codes<kTwo, false>(h1), f16_codes<kTwo>(h1)};
             const uint32_t b[4] = {e0 & keep[u], e1 & keep[u], f0 & keep[u], f1 & keep[u]};
             if constexpr (kTwo) {
               if (u == 0) {
@@ -754,9 +762,9 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         float4 v;
         constexpr float kLow = kTwo ? 1.f : 0x1p24f, kHigh = kTwo ? 0.0625f : 0x1p20f;
         v.x = fmaf(acc[y][0][k] * kLow, up, b);
-        v.y = fmaf(acc[y][0][2 + k] * kHigh, up, b);
+        v.y = fmaf((acc[y][0][2 + k] - acc[y][0][k]) * kHigh, up, b);
         v.z = fmaf(acc[y][1][k] * kLow, up, b);
-        v.w = fmaf(acc[y][1][2 + k] * kHigh, up, b);
+        v.w = fmaf((acc[y][1][2 + k] - acc[y][1][k]) * kHigh, up, b);
         *reinterpret_cast<float4*>(merge + (2 * t + k) * D + 32 * y + 4 * g) = v;
       }
     }
