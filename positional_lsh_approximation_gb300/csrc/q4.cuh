@@ -84,21 +84,29 @@ template <> struct Elem<float> {
 
 // Launches a kernel as a programmatic dependent of the one before it on the
 // stream: its launch overlaps that one's tail, and it waits for its end
-// (grid_dep_wait) before any access.
+// (grid_dep_wait) before any access.  `cluster` CTAs form a cluster.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem,
-                             cudaStream_t st, const A&... args) {
+cudaError_t launch_clusters(unsigned cluster, void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                            cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t st, const A&... args) {
+  return launch_clusters(1, kern, grid, threads, smem, st, args...);
 }
 
 }  // namespace q4

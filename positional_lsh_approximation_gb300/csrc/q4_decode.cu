@@ -93,7 +93,7 @@ constexpr int kRowCost = 12;
 // most while there is room (16 shaves 1 us off small grids, whose calls then
 // launch a second kernel, and costs 0.6 us on full ones), CTAs of one row at most
 constexpr double kTeamBlocks = 3.0, kShareBlocks = 40.0;
-constexpr int kMaxShares = 64;
+constexpr int kMaxShares = 64, kMaxCluster = 8;
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float kNothing = -3.402823466e38f;   // a maximum over no score
@@ -131,6 +131,30 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// All threads of a cluster; what they wrote to shared memory is seen after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// address of `at` of this CTA's shared memory in that of CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t at, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t at) {
+  float r;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(at) : "memory");
+  return r;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at) {
+  float4 r;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(at)
+               : "memory");
+  return r;
+}
 
 // c += A (16 x 16, row) B (16 x 8): f16 operands (bf16 with BF), fp32 sums
 template <bool BF>
@@ -1060,19 +1084,65 @@ __global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __
 // a KV head together.  A row is attended by a team of 1, 2, 4 or 8 warps, so
 // that a warp has a few blocks however wide the head's envelopes; a CTA has
 // 8 / team rows.  Rows wider than eight warps' worth go to several CTAs, where
-// the grid has room, and are joined.
+// the grid has room: to a cluster, which joins them in its shared memory, or,
+// where 8 CTAs leave too much for one, to more that a second kernel joins.
 struct Groups {
   int first[kMaxGroupOrder + 1];          // first CTA of each KV head, in order
   uint8_t order[kMaxGroupOrder];
   uint8_t shares[kMaxGroupOrder];         // CTAs of a row, in order
   uint8_t team[kMaxGroupOrder];           // log2 of the warps of a row, in order
   int ordered;                            // 0: index order, shares[0] and team[0] for all
+  int cluster;                            // > 1: a row's shares, and the CTAs of a cluster
 };
 
 // CTAs of a KV head: `rows` rows by teams of `team` warps, or by `shares` CTAs each
 __host__ __device__ __forceinline__ int group_ctas(int rows, int team, int shares) {
   const int held = kApproxWarps / team;
   return shares > 1 ? rows * shares : (rows + held - 1) / held;
+}
+
+// The pieces of one row that the CTAs of a cluster hold at `part` of their
+// shared memory, joined and stored by the first; all threads call it.
+template <typename T, int D>
+__device__ __forceinline__ void join_cluster(const float* part, int rank, int n, int heads, T* o) {
+  static_assert(kHeads * D <= 4 * 32 * kApproxWarps, "four values a thread");
+  cluster_sync();
+  const int e = 4 * threadIdx.x, h = e / D;
+  if (rank == 0 && h < heads) {
+    const uint32_t at = smem_u32(part);
+    float m[kMaxCluster], l[kMaxCluster];
+    float4 v[kMaxCluster];
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      m[k] = kNothing;
+      l[k] = 0.f;
+      if (k < n) {
+        const uint32_t there = cluster_addr(at, k);
+        m[k] = ld_cluster(there + 4 * (kHeads * D + h));
+        l[k] = ld_cluster(there + 4 * (kHeads * D + kHeads + h));
+        v[k] = ld_cluster4(there + 4 * e);
+      }
+    }
+    float mm = m[0], sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 1; k < kMaxCluster; ++k) mm = fmaxf(mm, m[k]);
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      if (l[k] == 0.f) continue;           // nothing of the piece was seen
+      const float f = ex2(m[k] - mm);
+      sum = fmaf(f, l[k], sum);
+      acc[0] = fmaf(f, v[k].x, acc[0]);
+      acc[1] = fmaf(f, v[k].y, acc[1]);
+      acc[2] = fmaf(f, v[k].z, acc[2]);
+      acc[3] = fmaf(f, v[k].w, acc[3]);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] *= inv;
+    store_row(o + e, acc);
+  }
+  __syncwarp();
+  cluster_sync();                          // the others' shared memory has been read
 }
 
 template <typename T, int D, int PACK>
@@ -1162,9 +1232,13 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     pc.t0 = max(t_first, pc.t1 - len);
   }
   T* o = static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D;
+  // (the queries' operands are done with when a piece is written)
+  static_assert(sizeof(sm.q) >= sizeof(float) * part_floats<D>(), "a piece fits");
+  float* part = gr.cluster > 1 ? reinterpret_cast<float*>(sm.q)
+                               : p.part + (int64_t)blockIdx.x * part_floats<D>();
   attend<T, D, false, PACK>(p, pc, team, query, nullptr, starts, sm, ring, ahead,
-                            valid && shares == 1 ? o : nullptr,
-                            valid && shares > 1 ? p.part + (int64_t)blockIdx.x * part_floats<D>() : nullptr);
+                            valid && shares == 1 ? o : nullptr, valid && shares > 1 ? part : nullptr);
+  if (gr.cluster > 1 && shares > 1 && valid) join_cluster<T, D>(part, share, shares, pc.heads, o);
 }
 
 template <typename T, int D>
@@ -1216,26 +1290,37 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
   }
   for (int k = 0; k < groups; ++k) gr.order[k] = (uint8_t)k;
   std::stable_sort(gr.order, gr.order + groups, [&](int x, int y) { return blocks[x] > blocks[y]; });
-  // teams of kTeamBlocks blocks a warp, wider ones while all warps fit at once
+  // teams of kTeamBlocks blocks a warp, wider ones while all warps fit at once;
+  // a KV head that wants more than a CTA's warps takes a cluster
   const int64_t room = (int64_t)a.num_sms * kApproxCtas;
   int64_t grid = 0;
-  bool split = false;
-  for (double each = kTeamBlocks;; each *= 0.5) {
-    int64_t g = 0;
-    uint8_t team[kMaxGroupOrder];
-    for (int k = 0; k < groups; ++k) {
-      team[k] = 0;
-      while ((1 << team[k]) < kApproxWarps && (1 << team[k]) * each < blocks[gr.order[k]]) ++team[k];
-      g += group_ctas(rows, 1 << team[k], 1);
+  gr.cluster = 1;
+  for (double each = kTeamBlocks; grid == 0 || each >= 1.0; each *= 0.5) {
+    uint8_t team[kMaxGroupOrder], shares[kMaxGroupOrder];
+    int cluster = 1;
+    while (cluster < kMaxCluster && cluster * kApproxWarps * each < blocks[gr.order[0]]) cluster *= 2;
+    int64_t g;
+    for (;; cluster = 1) {
+      g = 0;
+      for (int k = 0; k < groups; ++k) {
+        const double wide = blocks[gr.order[k]];
+        team[k] = 0;
+        while ((1 << team[k]) < kApproxWarps && (1 << team[k]) * each < wide) ++team[k];
+        shares[k] = (uint8_t)(kApproxWarps * each < wide ? cluster : 1);
+        g += group_ctas(rows, 1 << team[k], shares[k]);
+      }
+      if (!gr.ordered) g *= H;
+      if (g <= room || cluster == 1) break;
     }
-    if (!gr.ordered) g *= H;
-    if (grid > 0 && (g > room || each < 1.0)) break;
+    if (grid > 0 && g > room) break;
     std::copy(team, team + groups, gr.team);
+    std::copy(shares, shares + groups, gr.shares);
+    gr.cluster = cluster;
     grid = g;
   }
-  // and rows of more than kShareBlocks to several CTAs, evenly, while they fit
-  for (int k = 0; k < groups; ++k) gr.shares[k] = 1;
-  for (double each = kShareBlocks; each < blocks[gr.order[0]]; each *= 2.0) {
+  // and rows of more than kShareBlocks a CTA to more of them, evenly, while they fit
+  bool split = false;
+  for (double each = kShareBlocks; each * gr.cluster < blocks[gr.order[0]]; each *= 2.0) {
     int64_t g = 0;
     uint8_t shares[kMaxGroupOrder];
     for (int k = 0; k < groups; ++k) {
@@ -1245,10 +1330,12 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
     }
     if (g > room) continue;
     std::copy(shares, shares + groups, gr.shares);
+    gr.cluster = 1;
     split = gr.shares[0] > 1;
     grid = g;
     break;
   }
+  grid = (grid + gr.cluster - 1) / gr.cluster * gr.cluster;     // (rows past the last group's are none)
   int64_t at = 0;
   for (int k = 0; k < groups; ++k) {
     gr.first[k] = (int)at;
@@ -1261,7 +1348,7 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern),
                                  (int)(sizeof(S) + sizeof(int) * kApproxWarps * kHeads * kMaxS));
   if (e == cudaSuccess)
-    e = launch_dependent(kern, dim3((unsigned)grid), 32 * kApproxWarps, smem, st, p, gr);
+    e = launch_clusters((unsigned)gr.cluster, kern, dim3((unsigned)grid), 32 * kApproxWarps, smem, st, p, gr);
   if (e == cudaSuccess && split)
     e = launch_dependent(q4_approx_join_kernel<T, D>, dim3((unsigned)(rows * H), p.per_chunk),
                          32 * kJoinWarps, 0, st, p, gr);
