@@ -284,7 +284,7 @@ template <typename T, int D, int PACK>
 struct Query {
   uint4 w[Layout<D>::kGroups][sizeof(T) / 2];
   __device__ void load(const DecodeParams& p, const Piece& pc, int rank) {
-    if (rank != 0) return;                 // a team's first warp prepares it for all
+    if (rank >= Layout<D>::kGroups) return;        // (prepare_query)
     const int lane = threadIdx.x & 31, g = (lane >> 2) % (kHeads / PACK), t = lane & 3;
     const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + g) * D + 8 * t;
 #pragma unroll
@@ -293,14 +293,40 @@ struct Query {
       for (int k = 0; k < (int)sizeof(T) / 2; ++k)
         w[y][k] = g < pc.heads ? reinterpret_cast<const uint4*>(q + 32 * y)[k] : make_uint4(0, 0, 0, 0);
   }
-  __device__ float get(int y, int i) const {
-    if constexpr (sizeof(T) == 4) {
-      const uint4& x = w[y][i >> 2];
-      return __uint_as_float((i & 3) == 0 ? x.x : (i & 3) == 1 ? x.y : (i & 3) == 2 ? x.z : x.w);
-    } else {
-      const uint4& x = w[y][0];
-      const uint32_t v = i < 2 ? x.x : i < 4 ? x.y : i < 6 ? x.z : x.w;
-      return __uint_as_float((i & 1) ? v & 0xffff0000u : v << 16);
+  // bits of the largest magnitude of column g (a NaN's are larger than any)
+  __device__ uint32_t largest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int y = 0; y < Layout<D>::kGroups; ++y)
+#pragma unroll
+      for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+        const uint32_t x[4] = {w[y][k].x, w[y][k].y, w[y][k].z, w[y][k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m = sizeof(T) == 4 ? max(m, x[i] & 0x7fffffffu) : __vmaxu2(m, x[i] & 0x7fff7fffu);
+      }
+    if (sizeof(T) == 2) m = max(m & 0xffff0000u, m << 16);
+    m = max(m, __shfl_xor_sync(FULL, m, 1));
+    return max(m, __shfl_xor_sync(FULL, m, 2));
+  }
+  // the values of group y
+  __device__ void get(int y, float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+      uint4 c = w[0][k];
+#pragma unroll
+      for (int z = 1; z < Layout<D>::kGroups; ++z)
+        if (y == z) c = w[z][k];
+      const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+          v[4 * k + i] = __uint_as_float(x[i]);
+        } else {
+          v[2 * i] = __uint_as_float(x[i] << 16);
+          v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+        }
+      }
     }
   }
 };
@@ -363,51 +389,44 @@ struct Ring {
 };
 
 // The queries as B operands (lane (g, t) holds rows 2 t, 2 t + 1, ... of column
-// g), by the first warp of a team for all of it; qlow takes the products of q's
-// sums over a group with K's lo, a bf16 number: k slots 2 t, 2 t + 1 and
+// g), a group of values a warp of the team and turn; qlow takes the products of
+// q's sums over a group with K's lo, a bf16 number: k slots 2 t, 2 t + 1 and
 // 2 t + 8 hold group t's sum as three bf16 terms (24 bits).  Visible to the
 // team after a barrier.
 template <typename T, int D, int PACK, typename S>
-__device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, int rank, int row, S& sm) {
+__device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, int rank, int size, int row, S& sm) {
   constexpr int Y = Layout<D>::kGroups;
   constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (rank != 0) return;
-  float mx = 0.f;
-  bool bad = false;
-#pragma unroll
-  for (int y = 0; y < Y; ++y)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = fabsf(query.get(y, i));
-      mx = fmaxf(mx, v);
-      bad |= !(v < 1.2980742e33f);      // 2^110
-    }
-  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
-  const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 110);
-  bad = (__ballot_sync(FULL, bad) >> (lane & 28)) & 15;
+  if (rank >= Y) return;
+  const uint32_t mx = query.largest();
+  const int e = min(max((int)(mx >> 23) - 127, -100), 110);
   // bf16: the largest in [2^14, 2^15); fp32: in [2^10, 2^11), as integers
   constexpr int kTop = kTwo ? 10 : 14;
   const float up = pow2(kTop - e);
   const float norm = kLog2e / sqrtf((float)D);
-  // what q's power of two and a code's (2^-24, or 1) leave
-  if (t == 0) sm.scale[row][g] = bad ? NAN : pow2(e + (kTwo ? 0 : 24) - kTop) * norm;
-  float group = 0.f;
+  if (rank == 0) {
+    // what q's power of two and a code's (2^-24, or 1) leave
+    const bool bad = mx >= (110u + 127u) << 23;           // 2^110, infinities, NaN
+    if (t == 0) sm.scale[row][g] = bad ? NAN : pow2(e + (kTwo ? 0 : 24) - kTop) * norm;
+    if (lane < (int)sizeof(T) / 2 * Y) sm.q[row][lane / Y][lane % Y][32] = make_uint4(0, 0, 0, 0);
+    if (t >= Y) sm.qlow[row][lane] = make_uint2(0, 0);
+  }
+  // (not unrolled: most warps take one turn, all the same instructions)
+#pragma unroll 1
+  for (int y = rank; y < Y; y += size) {
+    float v[8], sum = 0.f;
+    query.get(y, v);
 #pragma unroll
-  for (int y = 0; y < Y; ++y) {
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += query.get(y, i);
+    for (int i = 0; i < 8; ++i) sum += v[i];
     sum += __shfl_xor_sync(FULL, sum, 1);
     sum += __shfl_xor_sync(FULL, sum, 2);
-    if (y == t) group = sum * norm;
     uint32_t w[4], r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // odd codes are taken four bits up, as 16 c
       const float k = (i & 1) ? 0.0625f : 1.f;
-      float a = query.get(y, i) * up, b = query.get(y, i + 4) * up;
+      float a = v[i] * up, b = v[i + 4] * up;
       if constexpr (kTwo) {
         const float a0 = rintf(a), b0 = rintf(b);
         r[i] = pack_f16(rintf((a - a0) * 2048.f) * k, rintf((b - b0) * 2048.f) * k);
@@ -418,11 +437,11 @@ __device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, in
     }
     sm.q[row][0][y][lane] = make_uint4(w[0], w[1], w[2], w[3]);
     if constexpr (kTwo) sm.q[row][1][y][lane] = make_uint4(r[0], r[1], r[2], r[3]);
+    const float group = sum * norm;
+    const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
+    const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
+    if (t == y) sm.qlow[row][lane] = make_uint2(pack_bf16(hi, mid), pack_bf16(group - hi - mid, 0.f));
   }
-  if (lane < (int)sizeof(T) / 2 * Y) sm.q[row][lane / Y][lane % Y][32] = make_uint4(0, 0, 0, 0);
-  const float hi = __uint_as_float(__float_as_uint(group) & 0xffff0000u);
-  const float mid = __uint_as_float(__float_as_uint(group - hi) & 0xffff0000u);
-  sm.qlow[row][lane] = make_uint2(pack_bf16(hi, mid), pack_bf16(group - hi - mid, 0.f));
 }
 
 // One piece; the result (all heads, the warps merged) goes to `o_row` (o of
@@ -474,7 +493,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     next_page = pg[STAGES];
   }
 
-  if constexpr (EXACT) prepare_query<T, D, PACK>(query, rank, row, sm);
+  if constexpr (EXACT) prepare_query<T, D, PACK>(query, rank, kTeam, row, sm);
   __syncthreads();
   const uint32_t qlow[2] = {sm.qlow[row][lane].x, sm.qlow[row][lane].y};
   const float qscale[2] = {sm.scale[row][2 * t], sm.scale[row][2 * t + 1]};
@@ -1201,11 +1220,12 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
     const int h = rank + (i << log_size);
-    v[i] = h < pc.heads && lane < p.s && !none ? start_of(h, lane) : INT_MAX;
+    v[i] = INT_MAX;
+    if (h < pc.heads && !none && lane < p.s) v[i] = start_of(h, lane);
   }
   ahead = ahead && (uint32_t)next_page < (uint32_t)p.c.pages;
   if (ahead) ring.fetch(next, 0, next_page);
-  prepare_query<T, D, PACK>(query, rank, number, sm);
+  prepare_query<T, D, PACK>(query, rank, size, number, sm);
   int oldest = INT_MAX;
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
