@@ -89,10 +89,11 @@ constexpr int kMinBlocks = 8;
 // exact: blocks that beginning and ending a row costs (64 ragged sequences: 0 ->
 // 75.6 us, 6 -> 69.7, 12 -> 66.0, 20 -> 67.7)
 constexpr int kRowCost = 12;
-// approximate: blocks of a warp as a start (2 and 4 measure alike), of a CTA at
-// most while there is room (16 shaves 1 us off small grids, whose calls then
-// launch a second kernel, and costs 0.6 us on full ones), CTAs of one row at most
-constexpr double kTeamBlocks = 3.0, kShareBlocks = 40.0;
+// approximate: blocks of a warp as a start (16 sequences of 20 hashes: 3 -> 10.8
+// us, 2 -> 10.2; 64 sequences of 10: 14.3, 14.2), blocks of a CTA at most while
+// there is room, beyond what a cluster takes (below that the cluster is faster:
+// it needs no second kernel), CTAs of one row at most
+constexpr double kTeamBlocks = 2.0, kShareBlocks = 40.0;
 constexpr int kMaxShares = 64, kMaxCluster = 8;
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;

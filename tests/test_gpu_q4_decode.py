@@ -138,6 +138,33 @@ def test_approximate_decode_matches_the_oracle(case, hashes):
     bins.free()
 
 
+WIDE = [
+    # shape as above, scales, positions: rows of 2, 4 and 8 CTAs, some with
+    # nothing for most of them; the last two by a second kernel
+    ((3, 3, 1, 64, 16, 3000, "f32"), [700.0, 20, 300], [2999, 5, -1]),
+    ((2, 5, 1, 128, 64, 1100, "bf16"), [900.0, 3, 40, 500, 2], [1099, 640]),
+    ((2, 8, 2, 64, 32, 1200, "bf16"), [1.0, 2, 4, 8, 60, 80, 100, 120], [1199, 33]),
+    ((1, 34, 34, 64, 32, 2100, "f32"), [300.0] * 34, [2077]),           # more KV heads than are ordered
+    ((2, 11, 1, 128, 128, 5000, "bf16"), [1e4] * 11, [4999, 4095]),     # two chunks of heads
+    ((1, 4, 1, 64, 64, 12001, "bf16"), [1e5] * 4, [12000]),
+    ((30, 4, 2, 64, 64, 2000, "f32"), [1e4] * 4, [1999 - 61 * b for b in range(30)]),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
+def test_rows_that_several_ctas_share(case):
+    shape, sigma, pos = case
+    s = Setup(*shape, seed=5)
+    bins = plsh.sample_bins(s.n, sigma, 7, seed=3)
+    off, st = bins.to_host()
+    got = plsh.alibi_decode_q4(s.q, s.cache, bins, i32(pos))
+    plsh.stream_status()
+    s.check(got, pos, lambda p, m: q4.log_weights_approx(off, st, s.Hq, 7, p, m))
+    again = plsh.alibi_decode_q4(s.q, s.cache, bins, i32(pos))
+    assert torch.equal(got, again)
+    bins.free()
+
+
 @pytest.mark.parametrize("sigma", [0.05, 1e6])
 def test_one_bin_and_the_steepest_and_flattest_slopes(sigma):
     s = Setup(2, 4, 2, 128, 64, 3000, "f32", seed=8)
