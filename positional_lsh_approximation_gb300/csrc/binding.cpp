@@ -6,7 +6,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -208,7 +208,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[6] == Py_None) {
       c10::cuda::OptionalCUDAStreamGuard guard;
       if (c.given) guard.reset_stream(*c.given);
-      const at::Tensor o = at::empty_like(q, q.options().requires_grad(false));
+      const at::Tensor o = at::detail::empty_cuda(q.sizes(), q.scalar_type(), q.device(), std::nullopt);
       to = tq;
       to.data = o.data_ptr();
       result = THPVariable_Wrap(o);
