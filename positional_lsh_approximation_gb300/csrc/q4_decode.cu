@@ -41,22 +41,26 @@
 // ragged sequences balance (counting 12 blocks for a row's beginning and end:
 // 75.6 -> 66.0 us for 64 ragged sequences).  Approximate: a row's key envelope
 // is short and known only after its bins are read; a team of 1 to 8 warps for
-// it, by the reach that its scales let expect.
+// it, by the reach that its scales let expect, or a cluster of 2 to 8 CTAs that
+// joins its pieces in distributed shared memory (one sequence 9.2 -> 7.0 us).
 //
 // Measured on GB300 (CUDA graph, back to back; percentages of the measured copy
-// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 65
-// us (346 MB, 78 %); 2 x 131072 positions, 40/8 heads, 65 us (336 MB, 76 %);
-// one sequence of 8192 9.2 us.  Without the arithmetic the copies alone take
-// 57 us for the long case and the arithmetic alone 66: it is bound by
-// instructions (about 260 - 300 a tile of 16 positions, issued in 53 % of the cycles;
-// the logic pipe, which takes the ANDs, is 54 % busy).  Approximate, s = 10: 64
-// ragged sequences 14.5 us (24.5 MB), one 9.1 us: bound by latency (position,
-// bins, first block, 1.4 us a block in one warp, merge).
+// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 64
+// us (346 MB, 79 %); 2 x 131072 positions, 40/8 heads, 64 us (336 MB, 77 %);
+// one sequence of 8192 9.2 us.  Without the arithmetic the copies alone took
+// 57 us for the long case when the whole took 66: it is bound by instructions
+// (about 260 a tile of 16 positions, issued in 53 % of the cycles; the logic
+// pipe, which takes the ANDs, is 52 % busy).  Approximate, s = 10: 64 ragged
+// sequences 14.2 us (24.5 MB), bound by instructions of beginning and ending
+// rows (2400 a warp, half of them not in blocks, issued in 43 % of the cycles);
+// one 7.0 us, bound by latency (position, bins, first block, 1.4 us a block in
+// one warp, merge).
 // Tried and dropped: one more warp per scheduler at 128 registers (spills, 73
 // -> 79 us), products of the next block beside P V of this one (74 -> 81),
 // K's codes as e4m3 operands of m16n8k32 (half the ANDs, but 65 -> 83), joining
-// split rows in the CTA that arrives last (+3 us on the device),
-// 16-warp teams (14.6 -> 17.1).
+// split rows in the CTA that arrives last (+3 us on the device), 16-warp teams
+// (14.6 -> 17.1), dependents launched at a kernel's start (waiting CTAs take the
+// slots unevenly: 14.2 -> 17.2).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -9,6 +9,10 @@ weigh 2^-40), R the largest |lo| + 15 step of V and S the largest 15 step:
     that may truncate, a product with step, two with lo and the bias): off by
     at most 32 * 2^-23 A in natural units, which moves o, a convex combination
     of values within R, by at most twice that times R;
+    (bf16 queries: the codes are f16 subnormals, whose products the matrix
+    instruction may truncate at 2^-18 of the largest in a sum; with q's and the
+    codes' signs and sizes mixed that is far inside the bound above, and P V's
+    is inside the next but one);
   - sums over L keys accumulate L / 16 + 64 terms one after the other at most:
     2 (L / 16 + 64) 2^-24 R for the numerator and the row sum together;
   - ex2 is within 2^-21: 2^-20 R for both;
