@@ -1388,6 +1388,7 @@ plsh_status q4_rows(const plsh_tensor* K, const plsh_tensor* V, const plsh_q4_ca
   a.len = len;
   a.m = K->n;
   a.dtype = K->dtype;
+  a.num_sms = ctx->num_sms;
   a.err = ctx->d_err;
   PLSH_TRY_CUDA(write ? plsh::launch_q4_write(a, cs) : plsh::launch_q4_read(a, cs),
                 write ? "cache write launch" : "cache read launch");

@@ -270,6 +270,7 @@ struct Q4RowsArgs {
   const int32_t* len;      // [B] or null
   int64_t m;
   int dtype;
+  int num_sms;
   int* err;
 };
 cudaError_t launch_q4_write(const Q4RowsArgs& a, cudaStream_t st);

@@ -7,6 +7,17 @@
 // cache).  A warp takes the rows of one tile (16 positions of one sequence and
 // head) of K or of V, so that what it touches is contiguous on both sides: the
 // tile's rows, and its codes and pairs.
+//
+// Measured on GB300 (CUDA graph, back to back; of the measured copy rate of
+// 6.80 TB/s): 8 x 4096 rows of 8 heads, d = 128, bf16, written and read back,
+// 63 us for 352 MB (82 %): writing about 37 us (176 MB, 70 %; with two lanes a
+// group 40 us, 16.5 instructions a value issued in 74 % of the cycles, the
+// logic pipe 64 % busy), reading about 26 us, at the copy rate.  One token of
+// each of 64 sequences, written and read, 4.6 us: two launches' latency.
+// A thread per group took 520 us for the first of these (its lanes' addresses
+// lie apart), a warp per tile 133, one pass of loads in flight ahead of the
+// other 88, two lanes a group instead of four 82, codes without a branch for
+// exact halves 67, streaming loads 65.7, one lane a group 63.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -175,18 +186,21 @@ __device__ __forceinline__ uint32_t codes_of(const float (&v)[8], float lo, floa
   return eight_codes(c);
 }
 
-// Two lanes a group, 16 values each (eights t and t + 2): what a group costs
-// beside its values (range, pair, reciprocal, addresses) is shared by more.
-template <typename T, int D>
+// G lanes a group, 32 / G values each (eights t, t + G, ...): what a group costs
+// beside its values (range, pair, reciprocal, addresses) is shared by more of
+// them where one lane has a group, and a row is done sooner where two have it
+// (launch_rows).
+template <typename T, int D, int G>
 __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_constant__ Q4RowsArgs a) {
   using L = Layout<D>;
-  constexpr int kLanes = D / 16;                  // lanes of a row
+  constexpr int kLanes = D / 32 * G;              // lanes of a row
+  constexpr int kEights = 4 / G;                  // eights t, t + G, ... of a group
   constexpr int kRows = 32 / kLanes;              // rows of a pass
   __shared__ alignas(16) uint8_t stage_s[kWarps][10 * D];    // a whole tile's codes and pairs
   grid_dep_wait();
   TileRows w;
   if (!tile_rows<D>(a, w)) return;
-  const int lane = threadIdx.x & 31, t = lane & 1, y = (lane % kLanes) >> 1, sub = lane / kLanes;
+  const int lane = threadIdx.x & 31, t = lane % G, y = lane % kLanes / G, sub = lane / kLanes;
   const T* src = static_cast<const T*>(w.value ? a.V : a.K) + w.row0 * D + 32 * y + 8 * t;
   uint8_t* stage = stage_s[threadIdx.x >> 5];
   const bool whole = w.r0 == 0 && w.r1 == kTile;
@@ -195,27 +209,31 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
   uint8_t* c_at = whole ? stage : codes;
   uint8_t* p_at = whole ? stage + 8 * D : pairs;
   const int first = w.r0 / kRows * kRows;
-  Eight<T> raw[2];                                // of the pass ahead
+  Eight<T> raw[kEights];                          // of the pass ahead
   auto load = [&](int r) {
     if (r >= w.r0 && r < w.r1) {
-      raw[0].load(src + (int64_t)r * D);
-      raw[1].load(src + (int64_t)r * D + 16);
+#pragma unroll
+      for (int k = 0; k < kEights; ++k) raw[k].load(src + (int64_t)r * D + 8 * G * k);
     }
   };
   load(first + sub);
   // (not unrolled: its passes would not stay in the instruction cache)
 #pragma unroll 1
   for (int r = first + sub; r - sub < w.r1; r += kRows) {
-    float v[2][8], mn, mx, mn2, mx2;
-    raw[0].get(v[0]);
-    raw[0].range(v[0], mn, mx);
-    raw[1].get(v[1]);
-    raw[1].range(v[1], mn2, mx2);
-    mn = min_nan(mn, mn2);
-    mx = max_nan(mx, mx2);
+    float v[kEights][8], mn, mx;
+#pragma unroll
+    for (int k = 0; k < kEights; ++k) {
+      float mn1, mx1;
+      raw[k].get(v[k]);
+      raw[k].range(v[k], mn1, mx1);
+      mn = k == 0 ? mn1 : min_nan(mn, mn1);
+      mx = k == 0 ? mx1 : max_nan(mx, mx1);
+    }
     load(r + kRows);
-    mn = min_nan(mn, __shfl_xor_sync(FULL, mn, 1));
-    mx = max_nan(mx, __shfl_xor_sync(FULL, mx, 1));
+    if (G == 2) {
+      mn = min_nan(mn, __shfl_xor_sync(FULL, mn, 1));
+      mx = max_nan(mx, __shfl_xor_sync(FULL, mx, 1));
+    }
     if (r < w.r0 || r >= w.r1) continue;
     const uint32_t pair = make_pair(mn, mx);
     const float lo = pair_lo(pair), step = pair_step(pair);
@@ -223,12 +241,12 @@ __global__ void __launch_bounds__(32 * kWarps) q4_write_kernel(const __grid_cons
     const bool rare = !(step > 0x1p-100f && step < 0x1p100f) && step != 0.f;
     const uint32_t keep = step > 0.f ? 0xffffffffu : 0u;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < kEights; ++k) {
       const uint32_t w8 = codes_of(v[k], lo, step, inv, rare) & keep;
       if (!w.value) {
-        *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * (t + 2 * k))) = w8;
+        *reinterpret_cast<uint32_t*>(c_at + L::k_code(r, y, 8 * (t + G * k))) = w8;
       } else {
-        uint16_t* out = reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * (t + 2 * k)) - L::kV);
+        uint16_t* out = reinterpret_cast<uint16_t*>(c_at + L::v_code(r, y, 8 * (t + G * k)) - L::kV);
         out[0] = (uint16_t)w8;
         out[32] = (uint16_t)(w8 >> 16);           // the next four values: 64 bytes on
       }
@@ -343,8 +361,12 @@ template <typename T, int D>
 cudaError_t launch_rows(const Q4RowsArgs& a, bool write, cudaStream_t st) {
   const int64_t warps = 2 * (int64_t)a.c.B * a.c.H * tiles_of(a.m);
   const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
-  return launch_dependent(write ? q4_write_kernel<T, D> : q4_read_kernel<T, D>, dim3(grid),
-                          32 * kWarps, 0, st, a);
+  // writing: one lane a group where there are warps enough to be bound by
+  // instructions (8 x 4096 rows, written and read back: 65.7 -> 63.4 us; the
+  // 333 rows of 5 fp32 sequences: 4.8 -> 5.6)
+  const bool many = warps >= 32 * (int64_t)a.num_sms;
+  return launch_dependent(!write ? q4_read_kernel<T, D> : many ? q4_write_kernel<T, D, 1> : q4_write_kernel<T, D, 2>,
+                          dim3(grid), 32 * kWarps, 0, st, a);
 }
 
 cudaError_t launch_any(const Q4RowsArgs& a, bool write, cudaStream_t st) {

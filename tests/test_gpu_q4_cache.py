@@ -265,3 +265,32 @@ def test_tensors_of_a_cache_are_not_exchanged():
         cache.table = cache.table.clone()
     with pytest.raises(AttributeError):
         cache.data = cache.data.clone()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_are_written_as_few_are(dtype, d):
+    """A call of many rows and calls of ten leave the same bytes (the latter are
+    held to the oracle above): ragged positions and lengths, groups of ties,
+    constants, infinities and NaN among them."""
+    B, H, m, page, per = 16, 8, 350, 32, 12
+    gen = torch.Generator("cuda").manual_seed(d)
+    table = torch.randperm(B * per, device="cuda", generator=gen).to(torch.int32).view(B, per)
+    a, b = (plsh.Q4Cache(torch.full((plsh.q4_cache_bytes(B * per, H, page, d),), 9, dtype=torch.uint8,
+                                    device="cuda"), table, H, d, page) for _ in range(2))
+    k, v = (torch.randn(B, H, m, d, device="cuda", generator=gen) for _ in range(2))
+    k[:, :, ::7] = (k[:, :, ::7] * 4).round() / 2                    # halves of codes
+    k[:, ::3, 5::11] = 1.5
+    v[1, :, 3::9, 40] = float("inf")
+    v[2, 1, 4::9, 7] = float("nan")
+    v[3] *= 1e-39
+    v[4] *= 1e37
+    k, v = k.to(DT[dtype]), v.to(DT[dtype])
+    pos = torch.arange(B, dtype=torch.int32, device="cuda") * 2 % 31
+    lens = m - torch.arange(B, dtype=torch.int32, device="cuda") * 13
+    plsh.q4_cache_write(a, k, v, pos, lens)
+    for i in range(0, m, 10):
+        plsh.q4_cache_write(b, k[:, :, i:i + 10].contiguous(), v[:, :, i:i + 10].contiguous(),
+                            pos + i, (lens - i).clamp(-1, 10))
+    plsh.stream_status()
+    assert torch.equal(a.data, b.data)
