@@ -51,7 +51,7 @@
 // 57 us for the long case when the whole took 66: it is bound by instructions
 // (about 260 a tile of 16 positions, issued in 53 % of the cycles; the logic
 // pipe, which takes the ANDs, is 52 % busy).  Approximate, s = 10: 64 ragged
-// sequences 14.2 us (24.5 MB), bound by instructions of beginning and ending
+// sequences 13.8 us (24.5 MB), bound by instructions of beginning and ending
 // rows (2400 a warp, half of them not in blocks, issued in 43 % of the cycles);
 // one 7.0 us, bound by latency (position, bins, first block, 1.4 us a block in
 // one warp, merge).
@@ -93,11 +93,10 @@ constexpr int kMinBlocks = 8;
 // exact: blocks that beginning and ending a row costs (64 ragged sequences: 0 ->
 // 75.6 us, 6 -> 69.7, 12 -> 66.0, 20 -> 67.7)
 constexpr int kRowCost = 12;
-// approximate: blocks of a warp as a start (16 sequences of 20 hashes: 3 -> 10.8
-// us, 2 -> 10.2; 64 sequences of 10: 14.3, 14.2), blocks of a CTA at most while
-// there is room, beyond what a cluster takes (below that the cluster is faster:
-// it needs no second kernel), CTAs of one row at most
-constexpr double kTeamBlocks = 2.0, kShareBlocks = 40.0;
+// approximate: blocks of a warp where not all warps fit at once, blocks of a CTA
+// at most while there is room, beyond what a cluster takes (below that the
+// cluster is faster: it needs no second kernel), CTAs of one row at most
+constexpr double kTeamBlocks = 2.5, kShareBlocks = 40.0;
 constexpr int kMaxShares = 64, kMaxCluster = 8;
 constexpr int kMaxGroupOrder = 32;
 constexpr unsigned FULL = 0xffffffffu;
@@ -1315,33 +1314,29 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
   }
   for (int k = 0; k < groups; ++k) gr.order[k] = (uint8_t)k;
   std::stable_sort(gr.order, gr.order + groups, [&](int x, int y) { return blocks[x] > blocks[y]; });
-  // teams of kTeamBlocks blocks a warp, wider ones while all warps fit at once;
-  // a KV head that wants more than a CTA's warps takes a cluster
+  // the fewest blocks a warp for which all warps fit at once (found in steps of a
+  // fifth; in halves: 64 sequences 14.3 us against 13.8, 16 of 20 hashes 12.5
+  // against 10.1, means over ten draws), a KV head that
+  // wants more than a CTA's taking a cluster (of eight CTAs, no more than 288 of
+  // 304 find room); else kTeamBlocks, in turns
   const int64_t room = (int64_t)a.num_sms * kApproxCtas;
   int64_t grid = 0;
-  gr.cluster = 1;
-  for (double each = kTeamBlocks; grid == 0 || each >= 1.0; each *= 0.5) {
-    uint8_t team[kMaxGroupOrder], shares[kMaxGroupOrder];
-    int cluster = 1;
-    while (cluster < kMaxCluster && cluster * kApproxWarps * each < blocks[gr.order[0]]) cluster *= 2;
-    int64_t g;
-    for (;; cluster = 1) {
-      g = 0;
-      for (int k = 0; k < groups; ++k) {
-        const double wide = blocks[gr.order[k]];
-        team[k] = 0;
-        while ((1 << team[k]) < kApproxWarps && (1 << team[k]) * each < wide) ++team[k];
-        shares[k] = (uint8_t)(kApproxWarps * each < wide ? cluster : 1);
-        g += group_ctas(rows, 1 << team[k], shares[k]);
-      }
-      if (!gr.ordered) g *= H;
-      if (g <= room || cluster == 1) break;
+  for (double each = 1.0;; each *= 1.19) {
+    const bool last = each > 8.0;
+    if (last) each = kTeamBlocks;
+    gr.cluster = 1;
+    while (!last && gr.cluster < kMaxCluster && gr.cluster * kApproxWarps * each < blocks[gr.order[0]]) gr.cluster *= 2;
+    grid = 0;
+    for (int k = 0; k < groups; ++k) {
+      const double wide = blocks[gr.order[k]];
+      int team = 0;
+      while ((1 << team) < kApproxWarps && (1 << team) * each < wide) ++team;
+      gr.team[k] = (uint8_t)team;
+      gr.shares[k] = (uint8_t)(kApproxWarps * each < wide ? gr.cluster : 1);
+      grid += group_ctas(rows, 1 << team, gr.shares[k]);
     }
-    if (grid > 0 && g > room) break;
-    std::copy(team, team + groups, gr.team);
-    std::copy(shares, shares + groups, gr.shares);
-    gr.cluster = cluster;
-    grid = g;
+    if (!gr.ordered) grid *= H;
+    if (last || grid <= (gr.cluster > 2 ? room - room / 16 : room)) break;
   }
   // and rows of more than kShareBlocks a CTA to more of them, evenly, while they fit
   bool split = false;
