@@ -152,6 +152,8 @@ WIDE = [
     ((2, 11, 1, 128, 128, 5000, "bf16"), [1e4] * 11, [4999, 4095]),     # two chunks of heads
     ((1, 4, 1, 64, 64, 12001, "bf16"), [1e5] * 4, [12000]),
     ((30, 4, 2, 64, 64, 2000, "f32"), [1e4] * 4, [1999 - 61 * b for b in range(30)]),
+    # and more rows than fit at once, idle ones among them
+    ((700, 4, 2, 64, 64, 400, "bf16"), [1.0, 5, 40, 300], [(97 * b) % 401 - 1 for b in range(700)]),
 ]
 
 
