@@ -505,8 +505,14 @@ plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache*
  * NaN.  A head whose q holds a NaN or an infinity, or reaches 2^110, gives a
  * row of NaN.  bf16: products of codes with q run as f16 ones of q scaled by a
  * power of two, so a value below 2^-24 of its head's largest counts as 0, and
- * P step is rounded to f16; fp32: two such terms each, about 22 bits.  Sums
- * are fp32's.  Asynchronous on `stream`; allocates nothing; may be captured.
+ * P step is rounded to f16: 2^-11 of itself, no finer than 2^-33 of the largest
+ * P step of the head's row and group of 32 values; sums of such products over
+ * 16 values or 16 positions keep about 18 bits of their largest one.  fp32: two
+ * such terms each, 2^-22 of a head's largest q and of P step itself (no finer
+ * than 2^-36 of the largest), in fp32 sums.  What a key does to a row is bound
+ * by its weight there: a value of a key that weighs nothing, however large,
+ * takes no precision from the others.  All other sums are fp32's.  Asynchronous
+ * on `stream`; allocates nothing; may be captured.
  */
 plsh_status plsh_alibi_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
                                  const plsh_bins* bins, const int32_t* pos, plsh_tensor* o,

@@ -27,9 +27,14 @@
 //   - q is scaled to f16 by a power of two per head (bf16: its largest
 //     magnitude in [2^14, 2^15), exact down to 2^-24 of that; fp32: two terms
 //     of integers whose sums are exact, 22 bits).
-//   - p_j step_jy is scaled by a power of two per group that follows the
-//     largest step met, and rounded to f16 (2^-11 relative; fp32: two terms).
-//     f16 because bf16's 2^-8 would show beside the output's own rounding.
+//   - p_j step_jy is scaled by a power of two per head (column) and group, which
+//     follows the largest p_j step_jy met, and rounded to f16 (2^-11 relative, no
+//     finer than 2^-33 of that largest; fp32: two terms, 2^-36).  A large step of
+//     a key that weighs nothing, for this head or for all, takes no precision
+//     from the others (one power for all heads, by the largest step, was half a
+//     microsecond faster in the approximate step and 1.5 us in the exact one of 64
+//     sequences, but a head's row could vanish under a key that it does not
+//     see).  f16 because bf16's 2^-8 would show beside the output's own rounding.
 // Each warp of a row's team takes every so-manieth block of 32 positions, with
 // a maximum, row sums and accumulators of its own, from a ring of asynchronous
 // copies that it alone fills and reads (no barrier in the loop); its maximum
@@ -214,6 +219,15 @@ __device__ __forceinline__ uint32_t f16_codes(uint32_t c) {
 template <bool NORMAL, bool HIGH>
 __device__ __forceinline__ uint32_t two_codes(uint32_t w) {
   return f16_codes<NORMAL>(w & (HIGH ? 0x00f000f0u : 0x000f000fu));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r, x, y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+  return o;
 }
 // 2^e for -126 <= e <= 127, 0 below
 __device__ __forceinline__ float pow2(int e) {
@@ -529,12 +543,16 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   float acc[Y][2][4];             // P V: values 32 y + 4 g + 2 tau + (r >> 1), columns 2 t + (r & 1)
   float low[Y][2];                // sum of p lo, this lane's positions
   float m[2] = {kNothing, kNothing}, l[2] = {0.f, 0.f};
-  float down[Y];                  // 2^-r of the group's weights
-  uint32_t most[Y];               // bits of the largest step that fits, low half set
+  // Weights times step of a group and column are held times 2^-r.  r puts the
+  // largest met into [2^kTop, 2^(kTop + 1)) and is raised when one reaches 2^15, so
+  // that f16's smallest, 2^-24, lies far below the largest (bf16: with more room
+  // above, so that it is raised less often: one sequence 9.7 -> 9.4 us).
+  constexpr int kTop = kTwo ? 11 : 8;
+  constexpr int kLeast = -100;    // r's smallest, where nothing was met
+  float2 down[Y];                 // 2^-r, -100 <= r <= 124
 #pragma unroll
   for (int y = 0; y < Y; ++y) {
-    down[y] = 1.f;
-    most[y] = 0xffffu;
+    down[y] = make_float2(pow2(-kLeast), pow2(-kLeast));
     low[y][0] = low[y][1] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[y][k >> 2][k & 3] = 0.f;
@@ -665,53 +683,97 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
           for (int y = 0; y < Y; ++y) w1[y] = 0;
         }
       }
-      // does a score or a step outgrow what it is measured against?
-      bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
+      // the weights, and P step of each group as f16 operands (times 2^-r):
+      // positions j (e0) and j + 8 (e1) of two heads
+      float pw[4];
+      uint32_t e0[Y], e1[Y];
+      auto weigh = [&](int y, float2& u0, float2& u1) {
+        const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
+        u0 = mul2(mul2(make_float2(pw[0], pw[1]), down[y]), make_float2(s0, s0));
+        u1 = mul2(mul2(make_float2(pw[2], pw[3]), down[y]), make_float2(s1, s1));
+      };
+      auto weights = [&]() {
 #pragma unroll
-      for (int y = 0; y < Y; ++y) grow |= max(w0[y], w1[y]) > most[y];
-      if (__any_sync(FULL, grow)) {
+        for (int k = 0; k < 4; ++k) {
+          pw[k] = ex2(x[k] - m[k & 1]);
+          if constexpr (!EXACT) pw[k] *= cnt[k];
+        }
+      };
+#pragma unroll 1
+      for (bool again = false;; again = true) {
+        weights();
+        uint32_t top = 0;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          float2 u0, u1;
+          weigh(y, u0, u1);
+          e0[y] = pack_f16(u0.x, u0.y);
+          e1[y] = pack_f16(u1.x, u1.y);
+          top = __vimax3_u16x2(top, e0[y], e1[y]);
+        }
+        // does a score outgrow what it is measured against, or a product reach
+        // 2^15 (or is it no number)?  (one vote for both, behind the exponentials:
+        // with one each, 4 us in 66)
+        const bool grow = fmaxf(x[0], x[2]) > m[0] + kLazy || fmaxf(x[1], x[3]) > m[1] + kLazy;
+        if (again || !__any_sync(FULL, grow || ((top + 0x08000800u) & 0x80008000u))) break;
+        const bool some = __any_sync(FULL, m[0] != kNothing || m[1] != kNothing);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
+          // The maximum moves, and r by as many whole binary places, so that what
+          // the accumulators hold keeps its place.  (The maximum itself, not the
+          // next whole number: the key that it belongs to then weighs 1, and 1
+          // times a step, eight bits, takes no rounding.)
           const float to = max_rows(fmaxf(m[k], fmaxf(x[k], x[k + 2])));
-          const float f = ex2(m[k] - to);
+          const float by = m[k] - to;
           m[k] = to;
+          if (!some) continue;               // a warp's first tile
+          const int n = (int)fminf(rintf(-by), 400.f);
+          const float f = ex2(by), rest = ex2(by + (float)n);
           l[k] *= f;
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
             low[y][k] *= f;
+            float& dn = k == 0 ? down[y].x : down[y].y;
+            const int r = 127 - (__float_as_int(dn) >> 23), least = max(r - n, kLeast);
+            dn = pow2(-least);
+            const float past = pow2(r - n - least) * rest;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[y][e >> 1][2 * (e & 1) + k] *= f;
+            for (int e = 0; e < 4; ++e) acc[y][e >> 1][2 * (e & 1) + k] *= past;
           }
         }
+        weights();
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
           // a step that is not a number: its group of the row of every head
           // that gives the position a weight is none either
-          const bool nan0 = w0[y] >= 0x7f800000u, nan1 = w1[y] >= 0x7f800000u;
+          const bool nan0 = (w0[y] & 0x7f800000u) == 0x7f800000u, nan1 = (w1[y] & 0x7f800000u) == 0x7f800000u;
           if (nan0) w0[y] = 0;
           if (nan1) w1[y] = 0;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if ((nan0 && x[k] != -INFINITY) || (nan1 && x[k + 2] != -INFINITY)) low[y][k] = NAN;
-          const uint32_t top = __reduce_max_sync(FULL, max(w0[y], w1[y]));
-          if (top > most[y]) {
-            const int old = (int)(most[y] >> 23) - 132;          // most: 2^(r + 5)
-            const int r = max((int)(top >> 23) - 129, -100);     // the largest step in [2^2, 2^3) 2^r
-            const float f = most[y] == 0xffffu ? 0.f : pow2(old - r);
-            down[y] = pow2(-r);
-            most[y] = ((uint32_t)(r + 132) << 23) | 0xffffu;
+          // the columns' largest, by the upper halves of their bits
+          const float s0 = pair_step(w0[y]), s1 = pair_step(w1[y]);
+          uint32_t most = __byte_perm(__float_as_uint(fmaxf(pw[0] * s0, pw[2] * s1)),
+                                      __float_as_uint(fmaxf(pw[1] * s0, pw[3] * s1)), 0x7632);
+          most = __vmaxu2(most, __shfl_xor_sync(FULL, most, 4));
+          most = __vmaxu2(most, __shfl_xor_sync(FULL, most, 8));
+          most = __vmaxu2(most, __shfl_xor_sync(FULL, most, 16));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[y][e >> 2][e & 3] *= f;
+          for (int k = 0; k < 2; ++k) {
+            const int e = (int)((most >> (16 * k + 7)) & 255u) - 127;       // (128: infinite, or no number)
+            float& dn = k == 0 ? down[y].x : down[y].y;
+            const int r = 127 - (__float_as_int(dn) >> 23);
+            const int to = e - r < 15 ? r : e == 128 ? 124 : e - kTop;
+            dn = pow2(-to);
+            const float f = pow2(r - to);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[y][i >> 1][2 * (i & 1) + k] *= f;
           }
         }
       }
-      float pw[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        pw[k] = ex2(x[k] - m[k & 1]);
-        if constexpr (!EXACT) pw[k] *= cnt[k];
-        l[k & 1] += pw[k];
-      }
+      for (int k = 0; k < 4; ++k) l[k & 1] += pw[k];
       // P V, group by group
 #pragma unroll
       for (int yy = 0; yy < Y; yy += 2) {
@@ -728,18 +790,16 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
           const float b0 = pair_lo(w0[y]), b1 = pair_lo(w1[y]);
           low[y][0] = fmaf(pw[0], b0, fmaf(pw[2], b1, low[y][0]));
           low[y][1] = fmaf(pw[1], b0, fmaf(pw[3], b1, low[y][1]));
-          const float s0 = pair_step(w0[y]) * down[y], s1 = pair_step(w1[y]) * down[y];
-          const float u0 = pw[0] * s0, u1 = pw[1] * s0, u2 = pw[2] * s1, u3 = pw[3] * s1;
-          uint32_t e0 = pack_f16(u0, u1), e1 = pack_f16(u2, u3);
           uint32_t f0 = 0, f1 = 0;
           if constexpr (kTwo) {
-            const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0));
-            const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1));
-            f0 = transpose8x8(pack_f16(u0 - c0.x, u1 - c0.y));
-            f1 = transpose8x8(pack_f16(u2 - c1.x, u3 - c1.y));
+            float2 u0, u1;
+            weigh(y, u0, u1);
+            const float2 c0 = __half22float2(*reinterpret_cast<__half2*>(&e0[y]));
+            const float2 c1 = __half22float2(*reinterpret_cast<__half2*>(&e1[y]));
+            f0 = transpose8x8(pack_f16(u0.x - c0.x, u0.y - c0.y));
+            f1 = transpose8x8(pack_f16(u1.x - c1.x, u1.y - c1.y));
           }
-          e0 = transpose8x8(e0);
-          e1 = transpose8x8(e1);
+          const uint32_t g0 = transpose8x8(e0[y]), g1 = transpose8x8(e1[y]);
           // fp32: the tile's own sums first, then added: the products' fp32 sums
           // truncate, which over a long row would add up to one side
           float own[kTwo ? 2 : 1][4];
@@ -754,7 +814,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
                                    two_codes<kTwo, false>(v1), f16_codes<kTwo>(n1),
                                    two_codes<kTwo, false>(h0), f16_codes<kTwo>(h0),
                                    two_codes<kTwo, false>(h1), f16_codes<kTwo>(h1)};
-            const uint32_t b[4] = {e0 & keep[u], e1 & keep[u], f0 & keep[u], f1 & keep[u]};
+            const uint32_t b[4] = {g0 & keep[u], g1 & keep[u], f0 & keep[u], f1 & keep[u]};
             if constexpr (kTwo) {
               if (u == 0) {
                 mma16816_first<false>(own[0], a[0], a[1], a[2], a[3], b[2], b[3]);
@@ -805,7 +865,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
 #pragma unroll
       for (int y = 0; y < Y; ++y) {
         const float b = sum_rows(low[y][k]);
-        const float up = most[y] == 0xffffu ? 0.f : pow2((int)(most[y] >> 23) - 132);
+        const float up = __uint_as_float((254u << 23) - __float_as_uint(k == 0 ? down[y].x : down[y].y));
         float4 v;
         constexpr float kLow = kTwo ? 1.f : 0x1p24f, kHigh = kTwo ? 0.0625f : 0x1p20f;
         v.x = fmaf(acc[y][0][k] * kLow, up, b);
