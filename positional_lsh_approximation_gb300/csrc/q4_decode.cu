@@ -1346,7 +1346,8 @@ cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st
   using S = Smem<T, D, kExactWarps, kExactStages, 1>;
   Slopes s;
   for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
-  const int64_t entries = (int64_t)p.c.B * p.c.H * p.chunks * ((p.limit + 31) / 32 + kRowCost);
+  // (a limit up to 2^31 - 16)
+  const int64_t entries = (int64_t)p.c.B * p.c.H * p.chunks * (((int64_t)p.limit + 31) / 32 + kRowCost);
   const int64_t want = (entries + kMinBlocks - 1) / kMinBlocks;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
   auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2> : q4_exact_kernel<T, D, 1>;
