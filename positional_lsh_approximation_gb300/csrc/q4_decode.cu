@@ -380,7 +380,8 @@ struct Ring {
   __device__ int32_t page_of(int block) const {
     return table[log_blocks >= 0 ? block >> log_blocks : 2 * block];
   }
-  __device__ void fetch(int block, int st, int32_t pg) {
+  // `first`: the first position that the row reaches back to
+  __device__ void fetch(int block, int st, int32_t pg, int first) {
     const uint32_t dst = smem + st * (2 * L::kTileBytes) + 16 * lane;
     absent &= ~(3u << (2 * st));
     if (log_blocks >= 0) {
@@ -390,8 +391,10 @@ struct Ring {
       else
         absent |= 3u << (2 * st);
     } else {
-      // the second tile's page is looked up only if the row reaches it
-      const int32_t pg1 = 2 * block + 1 <= last ? table[2 * block + 1] : -1;
+      // the second tile's page is looked up only if the row reaches it; the first
+      // one's counts only if the row reaches back to it
+      const bool need0 = 32 * block + kTile > first, need1 = 2 * block + 1 <= last;
+      const int32_t pg1 = need1 ? table[2 * block + 1] : -1;
       if ((uint32_t)pg < pages)
         copy_async<L::kTileBytes>(dst, head_data + pg * page_bytes, lane);
       else
@@ -400,7 +403,7 @@ struct Ring {
         copy_async<L::kTileBytes>(dst + L::kTileBytes, head_data + pg1 * page_bytes, lane);
       else
         absent |= 2u << (2 * st);
-      if (2 * block + 1 > last && (uint32_t)pg < pages) return;     // nothing that is needed is absent
+      if ((!need0 || (uint32_t)pg < pages) && (!need1 || (uint32_t)pg1 < pages)) return;
     }
     if (((absent >> (2 * st)) & 3u) && lane == 0) atomicOr(err, kErrCachePlace);
   }
@@ -505,7 +508,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     for (int i = 0; i <= STAGES; ++i) pg[i] = i < steps ? ring.page_of(newest - i * kTeam) : 0;
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      if (i < steps && !(ahead && i == 0)) ring.fetch(newest - i * kTeam, i, pg[i]);
+      if (i < steps && !(ahead && i == 0)) ring.fetch(newest - i * kTeam, i, pg[i], pc.first);
       cp_async_commit();
     }
     next_page = pg[STAGES];
@@ -839,7 +842,7 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     }
     __syncwarp();            // the stage may be filled again
     if (i + STAGES < steps) {
-      ring.fetch(block - STAGES * kTeam, st, next_page);
+      ring.fetch(block - STAGES * kTeam, st, next_page, pc.first);
       if (i + STAGES + 1 < steps) next_page = ring.page_of(block - (STAGES + 1) * kTeam);
     }
     cp_async_commit();
@@ -1288,7 +1291,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
     if (h < pc.heads && !none && lane < p.s) v[i] = start_of(h, lane);
   }
   ahead = ahead && (uint32_t)next_page < (uint32_t)p.c.pages;
-  if (ahead) ring.fetch(next, 0, next_page);
+  if (ahead) ring.fetch(next, 0, next_page, 0);       // (a page holds both tiles)
   prepare_query<T, D, PACK>(query, rank, size, number, sm);
   int oldest = INT_MAX;
 #pragma unroll

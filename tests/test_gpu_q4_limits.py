@@ -55,3 +55,28 @@ def test_the_most_pages_a_sequence_may_have():
             # of either: 60 * 2^-24 * 4 * 4 < 6e-5
             assert np.abs(got[0, :, 0].double().cpu().numpy() - want).max() < 6e-5
     bins.free()
+
+
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("first", [16, 30, 47, 160, 175])
+def test_pages_before_the_bins_may_be_gone(page, first):
+    """An approximate row reaches back to its bins' first start: the pages
+    before it may have been handed back (an index out of range), and those
+    behind the position may not have been given yet; nothing is reported."""
+    n, Hq, d, pos = 200, 4, 128, 177
+    cache, _, _ = filled(2, 1, n, page, 40, d=d)
+    q = torch.randn(2, Hq, 1, d, device="cuda").bfloat16()
+    bins = plsh.bins_from_host(n, Hq, 1, np.arange(0, 3 * Hq + 1, 3), np.tile([0, first, n], Hq))
+    want = plsh.alibi_decode_q4(q, cache, bins, i32([pos, pos]))
+    plsh.stream_status()
+    cache.table[:, :first // page] = -1
+    cache.table[:, pos // page + 1:] = 10 ** 9
+    got = plsh.alibi_decode_q4(q, cache, bins, i32([pos, pos]))
+    plsh.stream_status()
+    assert torch.equal(got, want)
+    # the page that the first start lies in counts
+    cache.table[:, first // page] = -1
+    plsh.alibi_decode_q4(q, cache, bins, i32([pos, pos]))
+    with pytest.raises(plsh.PlshError):
+        plsh.stream_status()
+    bins.free()
