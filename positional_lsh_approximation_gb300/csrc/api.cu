@@ -1498,7 +1498,9 @@ plsh_status plsh_alibi_exact_decode_q4(const plsh_tensor* q, const plsh_q4_cache
     return fail(PLSH_ERR_UNSUPPORTED, "exact path serves at most 512 heads");
   if ((st = check_sigma(sigma_h, (int32_t)q->H)) != PLSH_OK) return st;
   float slopes[plsh::kMaxExactHeads];
-  for (int64_t h = 0; h < q->H; ++h) slopes[h] = (float)(1.4426950408889634 / sigma_h[h]);
+  // (a scale whose slope fp32 does not hold gets one that leaves the key at the
+  // position itself its weight, 0 times infinity being no number, and the next 0)
+  for (int64_t h = 0; h < q->H; ++h) slopes[h] = (float)std::min(1.4426950408889634 / sigma_h[h], 1e30);
   return q4_decode(q, cache, nullptr, slopes, pos, o, work, work_bytes, (cudaStream_t)stream);
 }
 

@@ -80,3 +80,23 @@ def test_pages_before_the_bins_may_be_gone(page, first):
     with pytest.raises(plsh.PlshError):
         plsh.stream_status()
     bins.free()
+
+
+STEEP = [1e-30, 1e-37, 1e-39, 1e-45, 1e-300]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_scales_whose_slope_fp32_does_not_hold(dtype):
+    """Every sigma above 0 is admitted; so steep a bias leaves the key at the
+    row's own position alone: o is its value."""
+    n, Hq, d = 70, len(STEEP), 64
+    cache, _, V = filled(2, 1, n, 32, 8, d=d)
+    q = torch.randn(2, Hq, 1, d, device="cuda").to(dtype)
+    pos = [69, 32]
+    got = plsh.alibi_exact_decode_q4(q, cache, STEEP, i32(pos))
+    plsh.stream_status()
+    # one rounding of P step to f16 (2^-11 of 15 steps, a span of 8 at most),
+    # fp32 sums, the output's 2^-8
+    for b in range(2):
+        want = np.broadcast_to(V[b, 0, pos[b]], (Hq, d))
+        np.testing.assert_allclose(got[b, :, 0].double().cpu().numpy(), want, atol=8 * 2.0 ** -11, rtol=2.0 ** -8)
