@@ -3,7 +3,9 @@
 Each translation unit is compiled in parallel, then linked into one shared
 library next to this file (`_build/libplsh.so`).  The native binding of the
 4-bit cache's calls (`_build/_plsh_binding.so`, a Python extension against
-torch's headers) is compiled beside them and linked to it.  No CMake.
+torch's headers) is compiled beside them and linked to it; where it cannot be
+(no torch, no Python headers, no host compiler), the library is built all the
+same, a warning says why, and the 4-bit cache's calls raise.  No CMake.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
@@ -64,6 +67,24 @@ def _binding_link(obj: str, out: str) -> list:
             "-Wl,-rpath,$ORIGIN"]
 
 
+def _run_host(cmd: list) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compiler failed: " + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+
+
+def _compile_binding(force: bool):
+    """The binding's object if it is to be linked anew, else None."""
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    if force or _stale(obj, os.path.join(SRC_DIR, "binding.cpp")):
+        if os.path.exists(obj):
+            os.remove(obj)
+        _run_host(_binding_compile(obj))
+    elif os.path.exists(BINDING_PATH):
+        return None
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     nv = nvcc()
@@ -77,21 +98,17 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
-    binding_obj = os.path.join(BUILD_DIR, "binding.o")
-    binding = force or _stale(binding_obj, os.path.join(SRC_DIR, "binding.cpp"))
-    if binding:
-        jobs.append(_binding_compile(binding_obj))
-
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_compile_binding, force)
         for cmd, r in ex.map(run, jobs):
             if verbose or r.returncode != 0:
                 print(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("compiler failed: " + " ".join(cmd) + "\n" + r.stderr)
+                raise RuntimeError("nvcc failed: " + " ".join(cmd))
     objs = [os.path.join(BUILD_DIR, s.replace(".cu", ".o")) for s in SOURCES]
     if jobs or not os.path.exists(LIB_PATH):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
@@ -100,12 +117,17 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
         os.replace(tmp, LIB_PATH)
-    if binding or not os.path.exists(BINDING_PATH):
-        tmp = BINDING_PATH + f".tmp{os.getpid()}"
-        r = subprocess.run(_binding_link(binding_obj, tmp), capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n" + r.stdout + r.stderr)
-        os.replace(tmp, BINDING_PATH)
+    try:
+        obj = binding.result()
+        if obj is not None:
+            tmp = BINDING_PATH + f".tmp{os.getpid()}"
+            _run_host(_binding_link(obj, tmp))
+            os.replace(tmp, BINDING_PATH)
+    except (ImportError, OSError, RuntimeError) as e:
+        if os.path.exists(BINDING_PATH):          # of other sources
+            os.remove(BINDING_PATH)
+        warnings.warn(f"the native binding of the 4-bit cache's calls was not built: {e}",
+                      RuntimeWarning, stacklevel=2)
     return LIB_PATH
 
 
