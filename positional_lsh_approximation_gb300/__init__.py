@@ -394,7 +394,7 @@ _native = None
 
 def _binding():
     """The native binding of the 4-bit cache's calls; raises if it has not been
-    built."""
+    built, or was built for another torch or Python."""
     global _native
     load()
     with _lock:
@@ -402,6 +402,10 @@ def _binding():
             path = _build_mod.BINDING_PATH
             if not os.path.exists(path):
                 raise RuntimeError(f"native binding not built ({path}); call "
+                                   "positional_lsh_approximation_gb300.build()")
+            have, want = _build_mod.built_binding_abi(), _build_mod.binding_abi()
+            if have != want:
+                raise RuntimeError(f"native binding built for {have}, not for {want}; call "
                                    "positional_lsh_approximation_gb300.build()")
             loader = importlib.machinery.ExtensionFileLoader("_plsh_binding", path)
             mod = importlib.util.module_from_spec(

@@ -67,6 +67,23 @@ def _binding_link(obj: str, out: str) -> list:
             "-Wl,-rpath,$ORIGIN"]
 
 
+def binding_abi() -> str:
+    """What a binding compiled now would be for."""
+    import torch
+    return f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, " \
+           f"Python {sysconfig.get_config_var('SOABI')}"
+
+
+def built_binding_abi():
+    """What the binding was compiled for, or None: it is of no use to another
+    torch, whose tensors are laid out otherwise."""
+    try:
+        with open(BINDING_PATH + ".for") as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
 def _run_host(cmd: list) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -76,7 +93,7 @@ def _run_host(cmd: list) -> None:
 def _compile_binding(force: bool):
     """The binding's object if it is to be linked anew, else None."""
     obj = os.path.join(BUILD_DIR, "binding.o")
-    if force or _stale(obj, os.path.join(SRC_DIR, "binding.cpp")):
+    if force or _stale(obj, os.path.join(SRC_DIR, "binding.cpp")) or built_binding_abi() != binding_abi():
         if os.path.exists(obj):
             os.remove(obj)
         _run_host(_binding_compile(obj))
@@ -122,7 +139,11 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if obj is not None:
             tmp = BINDING_PATH + f".tmp{os.getpid()}"
             _run_host(_binding_link(obj, tmp))
+            if os.path.exists(BINDING_PATH + ".for"):
+                os.remove(BINDING_PATH + ".for")
             os.replace(tmp, BINDING_PATH)
+            with open(BINDING_PATH + ".for", "w") as f:
+                f.write(binding_abi())
     except (ImportError, OSError, RuntimeError) as e:
         if os.path.exists(BINDING_PATH):          # of other sources
             os.remove(BINDING_PATH)

@@ -4,6 +4,7 @@ import sys
 import warnings
 
 import pytest
+import torch
 
 import positional_lsh_approximation_gb300 as plsh
 
@@ -63,6 +64,24 @@ def test_the_library_does_not_need_torch(tree, monkeypatch):
     with pytest.warns(RuntimeWarning, match="torch"):
         build_mod.build()
     assert os.path.exists(build_mod.LIB_PATH)
+
+
+def test_a_binding_of_another_torch_is_not_used(tree, monkeypatch):
+    build_mod.build()
+    made = os.stat(build_mod.BINDING_PATH).st_mtime_ns
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    # without a build: refused before it is loaded
+    monkeypatch.setattr(plsh, "_native", None)
+    monkeypatch.setattr(plsh, "load", lambda: None)
+    with pytest.raises(RuntimeError, match="0.0.0"):
+        plsh._binding()
+    # a build makes it anew, once, and leaves the library
+    lib = os.stat(build_mod.LIB_PATH).st_mtime_ns
+    build_mod.build()
+    anew = os.stat(build_mod.BINDING_PATH).st_mtime_ns
+    assert anew != made and os.stat(build_mod.LIB_PATH).st_mtime_ns == lib
+    build_mod.build()
+    assert os.stat(build_mod.BINDING_PATH).st_mtime_ns == anew
 
 
 def test_a_unit_that_does_not_compile_is_an_error(tree):
