@@ -417,6 +417,8 @@ plsh_status plsh_alibi_decode(const plsh_tensor* q, const plsh_tensor* K,
  *   lo = min x rounded down to bf16,  step = (max x - lo) / 15 rounded up to
  *   bf16,  c = (x - lo) / step rounded to the nearest integer, ties to even,
  *   within 0..15 (0 where step is 0): a value is off by at most about step / 2.
+ * -0 counts as less than +0: a group whose least value is 0 has lo = -0 if one
+ * of its zeros is -0.
  * A group that holds a NaN or an infinity, or spans more than fp32 does, is
  * stored as lo = 0, step = NaN: it reads back as NaN, and so does every
  * attention row that gives one of its keys a weight.

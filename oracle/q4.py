@@ -26,7 +26,9 @@ def quantise(x: np.ndarray):
     """x [..., d] fp32 -> codes uint8 [..., d], lo, step fp32 [..., d / 32]."""
     g = x.astype(np.float32).reshape(*x.shape[:-1], -1, GROUP)
     with np.errstate(all="ignore"):
-        lo = _round_bf16(g.min(-1), False)
+        mn = g.min(-1)
+        # (-0 is less than +0, whichever of them numpy's minimum picks)
+        lo = _round_bf16(np.where((mn == 0) & (np.signbit(g) & (g == 0)).any(-1), np.float32(-0.0), mn), False)
         spread = (g.max(-1) - lo).astype(np.float32)
         bad = ~np.isfinite(spread)
         step = _round_bf16((spread / np.float32(15)).astype(np.float32), True)
