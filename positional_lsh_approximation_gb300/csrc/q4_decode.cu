@@ -50,16 +50,18 @@
 // joins its pieces in distributed shared memory (one sequence 9.2 -> 7.0 us).
 //
 // Measured on GB300 (CUDA graph, back to back; percentages of the measured copy
-// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 64
-// us (346 MB, 79 %); 2 x 131072 positions, 40/8 heads, 64 us (336 MB, 77 %);
-// one sequence of 8192 9.2 us.  Without the arithmetic the copies alone took
+// rate of 6.80 TB/s): exact, 64 ragged sequences of up to 8192, 32/8 heads, 66
+// us (346 MB, 77 %); 2 x 131072 positions, 40/8 heads, 64 us (336 MB, 77 %);
+// one sequence of 8192 9.3 us.  Without the arithmetic the copies alone took
 // 57 us for the long case when the whole took 66: it is bound by instructions
-// (about 260 a tile of 16 positions, issued in 53 % of the cycles; the logic
-// pipe, which takes the ANDs, is 52 % busy).  Approximate, s = 10: 64 ragged
-// sequences 13.8 us (24.5 MB), bound by instructions of beginning and ending
-// rows (2400 a warp, half of them not in blocks, issued in 43 % of the cycles);
-// one 7.0 us, bound by latency (position, bins, first block, 1.4 us a block in
-// one warp, merge).
+// (about 260 a tile of 16 positions, issued in 52 % of the cycles; the logic
+// pipe, which takes the ANDs, is 53 % busy).  Approximate, s = 10: 64 ragged
+// sequences 14.4 us (19.7 MB, means over draws), bound by instructions of
+// beginning and ending rows (2600 a warp, half of them not in blocks, issued in
+// 46 % of the cycles); one 7.6 us, bound by latency (position, bins, first
+// block, 1.4 us a block in one warp, merge).  fp32 queries (twice the products,
+// codes made normal numbers): the exact step of those 64 sequences 98 us, the
+// approximate one 26 us, with one CTA an SM (launch_approx).
 // Tried and dropped: one more warp per scheduler at 128 registers (spills, 73
 // -> 79 us), products of the next block beside P V of this one (74 -> 81),
 // K's codes as e4m3 operands of m16n8k32 (half the ANDs, but 65 -> 83), joining
@@ -89,7 +91,9 @@ using namespace ptx;
 
 // Exact: three CTAs of four warps (168 registers a thread: 128 spill) and three
 // blocks of 32 positions in a warp's ring.  Approximate: two CTAs of eight
-// warps, two blocks (an envelope is a few blocks long).
+// warps (one where the queries' operands or the bin starts take more than half of
+// the shared memory: fp32 with d = 128; bf16 with d = 128 and 64 hashes), two
+// blocks (an envelope is a few blocks long).
 constexpr int kExactWarps = 4, kExactStages = 3, kExactCtas = 3;
 constexpr int kApproxWarps = 8, kApproxStages = 2, kApproxCtas = 2;
 constexpr int kHeads = 8;           // query heads of a CTA (columns of the products)
@@ -991,7 +995,8 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     const int64_t n = row_blocks(p, b);
     return n == 0 ? 0 : n + kRowCost;
   };
-  // all sequences' entries; idle sequences' rows (few) are zeroed on the way
+  // all sequences' entries; idle sequences' rows are zeroed on the way, by a
+  // thread each (made for a few of them: each is Hq D / 8 stores in a row)
   int64_t sum = 0;
 #pragma unroll 4
   for (int b = tid; b < p.c.B; b += 32 * kExactWarps) {
@@ -1363,11 +1368,13 @@ cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st
 template <typename T, int D>
 cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
   const int H = p.c.H, rows = p.c.B * p.chunks;
-  // The furthest of the s n bin starts of a KV head's n query heads lies about
-  // sigma (1 + ln(s n)) back (the distance to a bin's start exceeds a with
-  // probability e^{-a/sigma} (1 + a / (2 sigma))).
+  // The distance back to the start of a position's bin exceeds a with probability
+  // e^{-a/sigma}, so that the furthest of the s n bin starts of a KV head's n query
+  // heads lies about sigma (0.58 + ln(s n)) back; 1 for a little more than the mean.
   const double reach = 1.0 + log((double)p.s * std::min(p.G, kHeads));
   Groups gr;
+  // (more KV heads are not ordered, and all get the team of the widest: 8 sequences
+  // of 64 heads with ALiBi's scales 19.5 us, of 32 heads 10.2)
   gr.ordered = H <= kMaxGroupOrder && a.sigma != nullptr;
   const int groups = gr.ordered ? H : 1;
   double blocks[kMaxGroupOrder] = {};             // a row's, expected, by KV head; [0] the widest if not ordered
@@ -1378,11 +1385,13 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
   }
   for (int k = 0; k < groups; ++k) gr.order[k] = (uint8_t)k;
   std::stable_sort(gr.order, gr.order + groups, [&](int x, int y) { return blocks[x] > blocks[y]; });
-  // the fewest blocks a warp for which all warps fit at once (found in steps of a
+  // the fewest blocks a warp for which all warps fit `room` (found in steps of a
   // fifth; in halves: 64 sequences 14.3 us against 13.8, 16 of 20 hashes 12.5
   // against 10.1, means over ten draws), a KV head that
   // wants more than a CTA's taking a cluster (of eight CTAs, no more than 288 of
   // 304 find room); else kTeamBlocks, in turns
+  // (two CTAs an SM are counted on; where one fits, such a grid runs in two turns:
+  // 16 sequences of 32/8 heads of 128, s = 10, 17.8 us in fp32, 10.5 in bf16)
   const int64_t room = (int64_t)a.num_sms * kApproxCtas;
   int64_t grid = 0;
   for (double each = 1.0;; each *= 1.19) {
