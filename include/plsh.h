@@ -482,6 +482,51 @@ plsh_status plsh_q4_cache_read(const plsh_q4_cache* cache, const int32_t* pos,
                                const int32_t* len, plsh_tensor* K, plsh_tensor* V,
                                void* stream);
 
+/*
+ * plsh_q4_cache_reserve -- the cache's page table kept on the device from the
+ * positions that its sequences ask for.
+ *   table  (of the cache; it is written, and must be writable) row b holds
+ *          sequence b's pages in its first held[b] entries, -1 behind them.
+ *   need   device int32 [B]: positions sequence b is to hold; <= 0: none.
+ *   held   device int32 [B]: pages that it holds, updated.
+ *   pool   device int32 [1 + pool_pages]: the number of free pages, then their
+ *          stack from the bottom, updated.
+ *   prefix device int32 [prefix_pages], 0 <= prefix_pages <= max_pages: pages of
+ *          a prompt that all sequences share; the first prefix_pages entries of
+ *          every row that holds anything are these.  They never come from or go
+ *          to the stack.  NULL with prefix_pages = 0.
+ * A sequence wants w = max(ceil(need[b] / page), prefix_pages) pages (0 for
+ * need[b] <= 0).  First the pages held beyond w are pushed, from the last
+ * sequence's last page to the first one's first, and their entries become -1;
+ * then, from the first sequence on, the missing pages are popped, first entry
+ * first, as long as a sequence's fit: the first one whose do not and all after
+ * it that want more than they hold are left as they were (held[b] * page <
+ * need[b] says which).  Growing and then releasing leaves the stack as it was.
+ * A sequence with held[b] outside 0..max_pages, or that wants more than
+ * max_pages, is left as it was; a free count outside 0..pool_pages counts as the
+ * nearest, and pages pushed beyond pool_pages are dropped: each is reported as
+ * PLSH_ERR_INVALID by plsh_stream_status.  The arrays must not overlap.
+ * Asynchronous on `stream`; allocates nothing; may be captured.
+ */
+plsh_status plsh_q4_cache_reserve(const plsh_q4_cache* cache, const int32_t* need, int32_t* held,
+                                  int32_t* pool, int64_t pool_pages, const int32_t* prefix,
+                                  int64_t prefix_pages, void* stream);
+
+/*
+ * plsh_q4_cache_slots -- the slot of every new row: row i < len[b] of sequence b
+ * is position p = pos[b] + i and has slot table[b, p / page] * page + p % page
+ * (whatever else is kept by slot: a position of every head of the cache, its
+ * token, its owner); -1 for rows from len[b] on, rows whose position is negative,
+ * and rows whose page index is not in [0, pages).  A row whose position is not
+ * below max_pages * page is -1 too and reported as PLSH_ERR_INVALID by
+ * plsh_stream_status.
+ *   pos    device int32 [B];  len  device int32 [B] or NULL for m rows of each
+ *   slots  device int64 [B, m], 16-byte aligned; B * m < 2^31 - 512
+ * Asynchronous on `stream`; allocates nothing; may be captured.
+ */
+plsh_status plsh_q4_cache_slots(const plsh_q4_cache* cache, const int32_t* pos, const int32_t* len,
+                                int64_t m, int64_t* slots, void* stream);
+
 /* Bytes of workspace of a plsh_alibi_decode_q4 or plsh_alibi_exact_decode_q4
  * call with these q and cache on the current device. */
 plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,

@@ -130,3 +130,46 @@ def log_weights_approx(offsets, starts, H: int, s: int, pos: int, n: int) -> np.
         c[hs // s] += (j >= lo) & (j <= pos)
     with np.errstate(divide="ignore"):
         return np.log(c)
+
+
+def reserve(table, held, pool, need, page: int, prefix=()):
+    """A page table kept from the positions that sequences ask for: table [B,
+    max_pages], held [B] and pool (free count, then the stack) are updated in
+    place, one sequence and one page after the other."""
+    S, (B, cap) = len(prefix), table.shape
+    want = [max(-(-int(n) // page), S) if n > 0 else 0 for n in need]
+    want = [w if w <= cap else int(h) for w, h in zip(want, held)]
+    for b in reversed(range(B)):
+        for i in reversed(range(want[b], int(held[b]))):
+            if i >= S:
+                pool[0] += 1
+                pool[pool[0]] = table[b, i]
+            table[b, i] = -1
+        held[b] = min(held[b], want[b])
+    full = False
+    for b in range(B):
+        if want[b] <= held[b]:
+            continue
+        missing = range(max(int(held[b]), S), want[b])
+        full = full or len(missing) > pool[0]
+        if full:
+            continue
+        if held[b] < S:
+            table[b, held[b]:S] = prefix[held[b]:]
+        for i in missing:
+            table[b, i] = pool[pool[0]]
+            pool[0] -= 1
+        held[b] = want[b]
+
+
+def slots(table, pages: int, page: int, pos, lens, m: int):
+    """[B, m]: page * page size + row of positions pos[b] + i, i < lens[b]; -1
+    where there is none."""
+    B, cap = table.shape
+    out = np.full((B, m), -1, np.int64)
+    for b in range(B):
+        for i in range(min(m, int(lens[b]))):
+            p = int(pos[b]) + i
+            if 0 <= p < cap * page and 0 <= table[b, p // page] < pages:
+                out[b, i] = int(table[b, p // page]) * page + p % page
+    return out

@@ -26,7 +26,8 @@ from . import build as _build_mod
 __all__ = ["build", "load", "sample_bins", "bins_from_host", "bins_fixed", "bins_share_groups", "Bins", "alibi_attn",
            "alibi_attn_noalloc", "alibi_attn_host",
            "alibi_exact", "alibi_decode", "alibi_attn_backward", "bias_error", "stream_status",
-           "Q4Cache", "q4_cache_bytes", "q4_cache_write", "q4_cache_read", "q4_decode_work_bytes",
+           "Q4Cache", "q4_cache_bytes", "q4_cache_write", "q4_cache_read", "q4_cache_reserve",
+           "q4_cache_slots", "q4_decode_work_bytes",
            "alibi_decode_q4", "alibi_exact_decode_q4",
            "noalloc_status", "attn_path", "set_split_parts", "set_wait_limit_ns", "PlshError",
            "library_path"]
@@ -106,6 +107,8 @@ def load():
             "plsh_q4_cache_bytes": [I64, I64, I32, I32, ctypes.POINTER(I64)],
             "plsh_q4_cache_write": [TP, TP, CP, P, P, P],
             "plsh_q4_cache_read": [CP, P, P, TP, TP, P],
+            "plsh_q4_cache_reserve": [CP, P, P, P, I64, P, I64, P],
+            "plsh_q4_cache_slots": [CP, P, P, I64, P, P],
             "plsh_q4_decode_work_bytes": [TP, CP, ctypes.POINTER(I64)],
             "plsh_alibi_decode_q4": [TP, CP, P, P, TP, P, I64, P],
             "plsh_alibi_exact_decode_q4": [TP, CP, D, P, TP, P, I64, P],
@@ -491,6 +494,30 @@ def q4_cache_read(cache: Q4Cache, pos, lens=None, m: int | None = None, dtype=to
     (_native or _binding()).read(cache._packed, cache.device_index, K, V, pos, lens,
                                  _handle(stream))
     return K, V
+
+
+def q4_cache_reserve(cache: Q4Cache, need, held, pool, prefix=None, stream=None):
+    """plsh_q4_cache_reserve: the cache's table kept on the device from the
+    positions need[b] that its sequences ask for (<= 0: none).  held, int32 [B],
+    the pages that each holds (its first table entries, -1 behind them), and pool,
+    int32 [1 + pages], the number of free pages and their stack, are updated;
+    prefix, int32 [n], are the pages that every row that holds anything begins
+    with.  Pages held beyond the need go to the stack, missing ones come from it,
+    sequence by sequence as long as they fit."""
+    (_native or _binding()).reserve(cache._packed, cache.device_index, need, held, pool, prefix,
+                                    _handle(stream))
+
+
+def q4_cache_slots(cache: Q4Cache, pos, lens=None, m: int | None = None, out=None, stream=None):
+    """plsh_q4_cache_slots: int64 [B, m], the slot (page * page size + row) of
+    positions pos[b] + i, i < lens[b], of every sequence; -1 where there is none."""
+    if out is None:
+        if m is None:
+            raise ValueError("q4_cache_slots: give m, the rows of every sequence, or out")
+        with _stream_scope(stream):
+            out = torch.empty(cache.B, int(m), dtype=torch.int64, device=cache.data.device)
+    (_native or _binding()).slots(cache._packed, cache.device_index, pos, lens, out, _handle(stream))
+    return out
 
 
 def q4_decode_work_bytes(q, cache: Q4Cache) -> int:

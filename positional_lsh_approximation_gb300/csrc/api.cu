@@ -1470,6 +1470,59 @@ plsh_status plsh_q4_cache_read(const plsh_q4_cache* cache, const int32_t* pos, c
   return q4_rows(K, V, cache, pos, len, false, (cudaStream_t)stream);
 }
 
+plsh_status plsh_q4_cache_reserve(const plsh_q4_cache* cache, const int32_t* need, int32_t* held,
+                                  int32_t* pool, int64_t pool_pages, const int32_t* prefix,
+                                  int64_t prefix_pages, void* stream) {
+  plsh::Q4ReserveArgs a;
+  plsh_status st = check_q4_cache(cache, &a.c);
+  if (st != PLSH_OK) return st;
+  if (need == nullptr || held == nullptr || pool == nullptr)
+    return fail(PLSH_ERR_INVALID, "need, held and pool must not be NULL");
+  if ((((uintptr_t)need | (uintptr_t)held | (uintptr_t)pool | (uintptr_t)prefix) & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "need, held, pool and prefix must be int32 device pointers");
+  if (pool_pages < 0 || pool_pages >= ((int64_t)1 << 31))
+    return fail(PLSH_ERR_INVALID, "pool_pages must be in [0, 2^31)");
+  if (prefix_pages < 0 || prefix_pages > cache->max_pages)
+    return fail(PLSH_ERR_INVALID, "prefix_pages must be in [0, max_pages]");
+  if (prefix_pages > 0 && prefix == nullptr) return fail(PLSH_ERR_INVALID, "prefix is NULL");
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  a.need = need;
+  a.held = held;
+  a.pool = pool;
+  a.pool_pages = pool_pages;
+  a.prefix = prefix;
+  a.prefix_pages = (int)prefix_pages;
+  a.err = ctx->d_err;
+  PLSH_TRY_CUDA(plsh::launch_q4_reserve(a, (cudaStream_t)stream), "cache reserve launch");
+  return PLSH_OK;
+}
+
+plsh_status plsh_q4_cache_slots(const plsh_q4_cache* cache, const int32_t* pos, const int32_t* len,
+                                int64_t m, int64_t* slots, void* stream) {
+  plsh::Q4SlotsArgs a;
+  plsh_status st = check_q4_cache(cache, &a.c);
+  if (st != PLSH_OK) return st;
+  if (pos == nullptr || slots == nullptr)
+    return fail(PLSH_ERR_INVALID, "pos and slots must not be NULL");
+  if ((((uintptr_t)pos | (uintptr_t)len) & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "pos and len must be int32 device pointers");
+  if (((uintptr_t)slots & 15u) != 0)
+    return fail(PLSH_ERR_INVALID, "slots must be a 16-byte aligned int64 device pointer");
+  if (m < 1) return fail(PLSH_ERR_INVALID, "m must be >= 1");
+  if (m >= ((int64_t)1 << 31) || cache->B * m >= ((int64_t)1 << 31) - 512)
+    return fail(PLSH_ERR_UNSUPPORTED, "B * m must be < 2^31 - 512");
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  a.pos = pos;
+  a.len = len;
+  a.m = m;
+  a.slots = slots;
+  a.err = ctx->d_err;
+  PLSH_TRY_CUDA(plsh::launch_q4_slots(a, (cudaStream_t)stream), "cache slots launch");
+  return PLSH_OK;
+}
+
 plsh_status plsh_q4_decode_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
                                       int64_t* bytes) {
   if (bytes == nullptr) return fail(PLSH_ERR_INVALID, "bytes is NULL");

@@ -141,6 +141,56 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// A contiguous int32 vector on the device: its data and length.
+int32_t* vector(PyObject* o, int dev, const char* what, int64_t* n) {
+  const at::Tensor& t = tensor(o, what);
+  on_device(t, dev, what);
+  if (t.scalar_type() != at::kInt || t.dim() != 1 || !t.is_contiguous())
+    throw Refused(std::string(what) + " must be a contiguous int32 vector");
+  *n = t.size(0);
+  return static_cast<int32_t*>(t.data_ptr());
+}
+
+// reserve(cache, device, need, held, pool, prefix | None, stream | None)
+PyObject* reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!counted(n, 7)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Call c(a[0], a[1], a[6]);
+    const int32_t* need = indices(a[2], c.cache, c.dev, "need");
+    int32_t* held = const_cast<int32_t*>(indices(a[3], c.cache, c.dev, "held"));
+    int64_t places = 0, shared = 0;
+    int32_t* pool = vector(a[4], c.dev, "pool", &places);
+    if (places < 1) throw Refused("pool must hold the number of free pages and their stack");
+    const int32_t* prefix = a[5] == Py_None ? nullptr : vector(a[5], c.dev, "prefix", &shared);
+    void* st = c.stream();
+    if (!ran([&] {
+          return plsh_q4_cache_reserve(&c.cache, need, held, pool, places - 1, shared ? prefix : nullptr,
+                                       shared, st);
+        }))
+      return nullptr;
+    Py_RETURN_NONE;
+  });
+}
+
+// slots(cache, device, pos, lens | None, out, stream | None)
+PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!counted(n, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Call c(a[0], a[1], a[5]);
+    const int32_t* pos = indices(a[2], c.cache, c.dev, "pos");
+    const int32_t* len = a[3] == Py_None ? nullptr : indices(a[3], c.cache, c.dev, "lens");
+    const at::Tensor& t = tensor(a[4], "out");
+    on_device(t, c.dev, "out");
+    if (t.scalar_type() != at::kLong || t.dim() != 2 || t.size(0) != c.cache.B || !t.is_contiguous())
+      throw Refused("out must be a contiguous int64 tensor [B, m]");
+    int64_t* out = static_cast<int64_t*>(t.data_ptr());
+    const int64_t m = t.size(1);
+    void* st = c.stream();
+    if (!ran([&] { return plsh_q4_cache_slots(&c.cache, pos, len, m, out, st); })) return nullptr;
+    Py_RETURN_NONE;
+  });
+}
+
 // The call's workspace: `kept`, a dict of the cache, has one for each stream
 // that is current when a call is made (calls on a stream run one after the
 // other; g_launch keeps the launches of two threads' calls apart); a call that
@@ -245,6 +295,8 @@ PyObject* set_raise(PyObject*, PyObject* f) {
 PyMethodDef kMethods[] = {
     {"write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(write)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(read)), METH_FASTCALL, nullptr},
+    {"reserve", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(reserve)), METH_FASTCALL, nullptr},
+    {"slots", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(slots)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
     {"set_raise", set_raise, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -275,6 +275,27 @@ struct Q4RowsArgs {
 };
 cudaError_t launch_q4_write(const Q4RowsArgs& a, cudaStream_t st);
 cudaError_t launch_q4_read(const Q4RowsArgs& a, cudaStream_t st);
+// q4_pages.cu
+struct Q4ReserveArgs {
+  Q4Cache c;               // its table is written
+  const int32_t* need;     // [B] positions asked for
+  int32_t* held;           // [B] pages held
+  int32_t* pool;           // free pages: their number, then the stack [pool_pages]
+  int64_t pool_pages;
+  const int32_t* prefix;   // [prefix_pages] pages that every row begins with
+  int prefix_pages;
+  int* err;
+};
+cudaError_t launch_q4_reserve(const Q4ReserveArgs& a, cudaStream_t st);
+struct Q4SlotsArgs {
+  Q4Cache c;
+  const int32_t* pos;      // [B]
+  const int32_t* len;      // [B] or null
+  int64_t m;
+  int64_t* slots;          // [B, m]
+  int* err;
+};
+cudaError_t launch_q4_slots(const Q4SlotsArgs& a, cudaStream_t st);
 // q4_decode.cu
 struct Q4DecodeArgs {
   Q4Cache c;
