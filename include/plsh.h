@@ -578,6 +578,55 @@ plsh_status plsh_alibi_exact_decode_q4(const plsh_tensor* q, const plsh_q4_cache
                                        plsh_tensor* o, void* work, int64_t work_bytes,
                                        void* stream);
 
+/* Bytes of workspace of a plsh_alibi_exact_chunk_q4 call with these q and cache
+ * on the current device. */
+plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                     int64_t* bytes);
+
+/*
+ * plsh_alibi_exact_chunk_q4 -- exact ALiBi attention of several new tokens of
+ * every sequence over the 4-bit cache (a prompt's next piece, drafted tokens to
+ * verify): row i < len[b] of sequence b is at position p = pos[b] + i,
+ *   o_bi = sum_j e^{S_j - (p - j) / sigma_h} v_j / sum_j (the weights),
+ *   S_j = q_bi . k_j / sqrt(d),  0 <= j <= p,
+ * with k_j, v_j the cached values, the new tokens' own among them: they are
+ * written (plsh_q4_cache_write) before the call.
+ *   q, o [B, Hq, m, d], which must not overlap; B * Hq * m < 2^30.
+ *   pos  device int32 [B]; a negative one is an idle slot: o_bi = 0, i < len[b].
+ *   len  device int32 [B], or NULL for m rows of each; rows from len[b] on are
+ *        left as they were.
+ *   work device memory of plsh_q4_chunk_work_bytes, as for plsh_alibi_decode_q4.
+ * A row whose position is not below max_pages * page gives 0, and a key whose
+ * page index is not in [0, pages) counts as absent; either is reported as
+ * PLSH_ERR_INVALID by plsh_stream_status.  What lies behind a row's position has
+ * no effect on it.  Everything else as for plsh_alibi_exact_decode_q4.
+ */
+plsh_status plsh_alibi_exact_chunk_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                      const double* sigma_h, const int32_t* pos, const int32_t* len,
+                                      plsh_tensor* o, void* work, int64_t work_bytes, void* stream);
+
+/* Bytes of workspace of a plsh_alibi_exact_prefix_decode_q4 call with these q and
+ * cache on the current device. */
+plsh_status plsh_q4_prefix_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                      int64_t* bytes);
+
+/*
+ * plsh_alibi_exact_prefix_decode_q4 -- plsh_alibi_exact_decode_q4 for sequences
+ * that share their first positions: positions below prefix_pages * page are read
+ * from the pages prefix[0 .. prefix_pages), the others from the cache's table at
+ * the same index as ever (its first prefix_pages entries are not read).
+ *   prefix device int32 [prefix_pages], 1 <= prefix_pages <= max_pages.
+ *   work   device memory of plsh_q4_prefix_work_bytes, as for
+ *          plsh_alibi_decode_q4.
+ * A sequence may be anywhere, within the prefix too (pos[b] negative: idle).
+ * Everything else as for plsh_alibi_exact_decode_q4.
+ */
+plsh_status plsh_alibi_exact_prefix_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                              const double* sigma_h, const int32_t* pos,
+                                              const int32_t* prefix, int64_t prefix_pages,
+                                              plsh_tensor* o, void* work, int64_t work_bytes,
+                                              void* stream);
+
 /* Synchronises `stream`, then reports CUDA errors and the library's device
  * error flag, clearing the flag: PLSH_ERR_TIMEOUT when a bounded device wait
  * ran out, else PLSH_ERR_RANGE when a tensor-core attention call met a value

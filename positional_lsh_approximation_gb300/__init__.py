@@ -28,7 +28,8 @@ __all__ = ["build", "load", "sample_bins", "bins_from_host", "bins_fixed", "bins
            "alibi_exact", "alibi_decode", "alibi_attn_backward", "bias_error", "stream_status",
            "Q4Cache", "q4_cache_bytes", "q4_cache_write", "q4_cache_read", "q4_cache_reserve",
            "q4_cache_slots", "q4_decode_work_bytes",
-           "alibi_decode_q4", "alibi_exact_decode_q4",
+           "alibi_decode_q4", "alibi_exact_decode_q4", "q4_chunk_work_bytes", "alibi_exact_chunk_q4",
+           "q4_prefix_work_bytes", "alibi_exact_prefix_decode_q4",
            "noalloc_status", "attn_path", "set_split_parts", "set_wait_limit_ns", "PlshError",
            "library_path"]
 
@@ -112,6 +113,10 @@ def load():
             "plsh_q4_decode_work_bytes": [TP, CP, ctypes.POINTER(I64)],
             "plsh_alibi_decode_q4": [TP, CP, P, P, TP, P, I64, P],
             "plsh_alibi_exact_decode_q4": [TP, CP, D, P, TP, P, I64, P],
+            "plsh_q4_chunk_work_bytes": [TP, CP, ctypes.POINTER(I64)],
+            "plsh_alibi_exact_chunk_q4": [TP, CP, D, P, P, TP, P, I64, P],
+            "plsh_q4_prefix_work_bytes": [TP, CP, ctypes.POINTER(I64)],
+            "plsh_alibi_exact_prefix_decode_q4": [TP, CP, D, P, P, I64, TP, P, I64, P],
             "plsh_stream_status": [P],
             "plsh_noalloc_status": [P],
             "plsh_attn_path": [TP, P, I32, ctypes.POINTER(I32)],
@@ -544,6 +549,46 @@ def alibi_exact_decode_q4(q, cache: Q4Cache, sigma, pos, out=None, work=None, st
     the 4-bit cache (see alibi_decode_q4); sigma: a scale per query head."""
     return (_native or _binding()).decode(cache._packed, cache.device_index, cache._work, q,
                                           _f64(sigma).tobytes(), pos, out, work, _handle(stream))
+
+
+def _work_bytes(fn, q, cache: Q4Cache) -> int:
+    out, tq = ctypes.c_int64(), _desc(q)
+    _check(fn(ctypes.byref(tq), ctypes.byref(cache._c), ctypes.byref(out)))
+    return out.value
+
+
+def q4_chunk_work_bytes(q, cache: Q4Cache) -> int:
+    """plsh_q4_chunk_work_bytes: workspace of an alibi_exact_chunk_q4 call."""
+    return _work_bytes(load().plsh_q4_chunk_work_bytes, q, cache)
+
+
+def alibi_exact_chunk_q4(q, cache: Q4Cache, sigma, pos, lens=None, out=None, work=None, stream=None):
+    """plsh_alibi_exact_chunk_q4: exact ALiBi attention of several new tokens a
+    sequence over the 4-bit cache, for the queries q [B, Hq, m, d]: row i < lens[b]
+    (all m without lens) is at position pos[b] + i and sees every key up to it, the
+    new tokens' own among them, which are written before.  A negative pos[b]: an
+    idle slot, rows of 0.  Rows from lens[b] on keep what `out` holds; without it
+    they are 0.  `work`: device memory of q4_chunk_work_bytes (see
+    alibi_decode_q4)."""
+    return (_native or _binding()).chunk(cache._packed, cache.device_index, cache._work, q,
+                                         _f64(sigma).tobytes(), pos, lens, out, work, _handle(stream))
+
+
+def q4_prefix_work_bytes(q, cache: Q4Cache) -> int:
+    """plsh_q4_prefix_work_bytes: workspace of an alibi_exact_prefix_decode_q4 call."""
+    return _work_bytes(load().plsh_q4_prefix_work_bytes, q, cache)
+
+
+def alibi_exact_prefix_decode_q4(q, cache: Q4Cache, sigma, pos, prefix, out=None, work=None,
+                                 stream=None):
+    """plsh_alibi_exact_prefix_decode_q4: alibi_exact_decode_q4 for sequences that
+    share their first positions: those below len(prefix) * page are read from the
+    pages `prefix` (int32 on the device), the others through the cache's table as
+    ever (its first len(prefix) entries are not read).  `work`: device memory of
+    q4_prefix_work_bytes (see alibi_decode_q4)."""
+    return (_native or _binding()).prefix_decode(cache._packed, cache.device_index, cache._work, q,
+                                                 _f64(sigma).tobytes(), pos, prefix, out, work,
+                                                 _handle(stream))
 
 
 def bias_error(bins: Bins, sigma: float, h: int, lanczos_iters: int = 60, seed: int = 0,

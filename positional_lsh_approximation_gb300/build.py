@@ -21,7 +21,8 @@ SRC_DIR = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libplsh.so")
 SOURCES = ["api.cu", "sampler.cu", "attn_simt.cu", "attn_tc.cu", "decode.cu", "bias.cu", "bwd.cu",
-           "bwd_tc.cu", "q4_cache.cu", "q4_decode.cu", "q4_pages.cu"]
+           "bwd_tc.cu", "q4_cache.cu", "q4_decode.cu", "q4_pages.cu",
+           "q4_many.cu"]
 BINDING_PATH = os.path.join(BUILD_DIR, "_plsh_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -1395,15 +1395,94 @@ plsh_status q4_rows(const plsh_tensor* K, const plsh_tensor* V, const plsh_q4_ca
   return PLSH_OK;
 }
 
-plsh_status check_q4_query(const plsh_tensor* q, const plsh_q4_cache* cache, plsh::Q4Cache* c) {
+plsh_status check_q4_query(const plsh_tensor* q, const plsh_q4_cache* cache, plsh::Q4Cache* c,
+                           bool rows = false) {
   plsh_status st;
   if ((st = check_tensor(q, "q")) != PLSH_OK || (st = check_q4_cache(cache, c)) != PLSH_OK) return st;
-  if (q->n != 1) return fail(PLSH_ERR_INVALID, "q must be [B, Hq, 1, d]");
+  if (q->n != 1 && !rows) return fail(PLSH_ERR_INVALID, "q must be [B, Hq, 1, d]");
   if (q->B != cache->B || q->d != cache->d)
     return fail(PLSH_ERR_INVALID, "q must have the cache's B and d");
   if (q->H % cache->H != 0) return fail(PLSH_ERR_INVALID, "Hq must be a multiple of the cache's H");
   if (q->H >= ((int64_t)1 << 24) || q->B * q->H >= ((int64_t)1 << 24))
     return fail(PLSH_ERR_UNSUPPORTED, "B * Hq must be < 2^24");
+  if (q->n >= ((int64_t)1 << 30) / (q->B * q->H))
+    return fail(PLSH_ERR_UNSUPPORTED, "B * Hq * m must be < 2^30");
+  return PLSH_OK;
+}
+
+// log2(e) / sigma_h of every head (a scale whose slope fp32 does not hold gets one
+// that leaves the key at the position itself its weight, 0 times infinity being no
+// number, and the next 0)
+plsh_status q4_slopes(const plsh_tensor* q, const double* sigma_h, float* slopes) {
+  if (q->H > plsh::kMaxExactHeads)
+    return fail(PLSH_ERR_UNSUPPORTED, "exact path serves at most 512 heads");
+  const plsh_status st = check_sigma(sigma_h, (int32_t)q->H);
+  if (st != PLSH_OK) return st;
+  for (int64_t h = 0; h < q->H; ++h) slopes[h] = (float)std::min(1.4426950408889634 / sigma_h[h], 1e30);
+  return PLSH_OK;
+}
+
+// Whether a chunk's rows, or the rows behind a prefix, go to the tensor cores.
+bool q4_many(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix) {
+  const int64_t rows = q->H / c.H * (prefix ? q->B : q->n);      // of a KV head
+  return q->dtype == PLSH_BF16 && rows >= 32;
+}
+
+int64_t q4_rows_work_bytes(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix, int num_sms) {
+  int64_t bytes = plsh::q4_decode_work_bytes(c.d, num_sms);
+  if (q4_many(q, c, prefix))
+    bytes = plsh::q4_many_work_bytes(c.d, num_sms) +
+            (prefix ? plsh::q4_own_work_bytes(c.d, num_sms, c.B, c.H, (int)(q->H / c.H)) : 0);
+  return bytes;
+}
+
+// The exact step of several rows a sequence (prefix NULL) or behind a shared prefix.
+plsh_status q4_rows_step(const plsh_tensor* q, const plsh_q4_cache* cache, const double* sigma_h,
+                         const int32_t* pos, const int32_t* len, const int32_t* prefix,
+                         int64_t prefix_pages, plsh_tensor* o, void* work, int64_t work_bytes,
+                         cudaStream_t cs) {
+  plsh_status st;
+  plsh::Q4DecodeArgs a;
+  if ((st = check_q4_query(q, cache, &a.c, prefix == nullptr)) != PLSH_OK ||
+      (st = check_tensor(o, "o")) != PLSH_OK)
+    return st;
+  if (o->dtype != q->dtype || o->B != q->B || o->H != q->H || o->n != q->n || o->d != q->d)
+    return fail(PLSH_ERR_INVALID, "o must have q's shape and dtype");
+  if (pos == nullptr || (((uintptr_t)pos | (uintptr_t)len) & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "pos and len must be int32 device pointers");
+  if (q4_overlap(q, o)) return fail(PLSH_ERR_INVALID, "o must not overlap q");
+  float slopes[plsh::kMaxExactHeads];
+  if ((st = q4_slopes(q, sigma_h, slopes)) != PLSH_OK) return st;
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  const int64_t need = q4_rows_work_bytes(q, a.c, prefix != nullptr, ctx->num_sms);
+  if (work == nullptr || ((uintptr_t)work & 15u) != 0 || work_bytes < need)
+    return fail(PLSH_ERR_INVALID, "work must be 16-byte aligned device memory of at least " +
+                                      std::to_string(need) + " bytes");
+  a.q = q->data;
+  a.o = o->data;
+  a.pos = pos;
+  a.Hq = (int)q->H;
+  a.dtype = q->dtype;
+  a.rec = nullptr;
+  a.s = 0;
+  a.W = a.bins_n = 0;
+  a.slope_log2 = slopes;
+  a.sigma = nullptr;
+  a.work = work;
+  a.num_sms = ctx->num_sms;
+  a.err = ctx->d_err;
+  a.m = prefix == nullptr ? (int)q->n : 0;
+  a.len = len;
+  a.prefix = prefix;
+  a.prefix_pages = (int)prefix_pages;
+  a.wait_ns = ctx->wait_ns;
+  if (!q4_many(q, a.c, prefix != nullptr))
+    PLSH_TRY_CUDA(plsh::launch_q4_decode(a, cs), "4-bit decode launch");
+  else if (prefix == nullptr)
+    PLSH_TRY_CUDA(plsh::launch_q4_chunk(a, cs), "4-bit chunk launch");
+  else
+    PLSH_TRY_CUDA(plsh::launch_q4_prefix(a, cs), "4-bit prefix launch");
   return PLSH_OK;
 }
 
@@ -1547,14 +1626,53 @@ plsh_status plsh_alibi_exact_decode_q4(const plsh_tensor* q, const plsh_q4_cache
                                        void* work, int64_t work_bytes, void* stream) {
   plsh_status st = check_tensor(q, "q");
   if (st != PLSH_OK) return st;
-  if (q->H > plsh::kMaxExactHeads)
-    return fail(PLSH_ERR_UNSUPPORTED, "exact path serves at most 512 heads");
-  if ((st = check_sigma(sigma_h, (int32_t)q->H)) != PLSH_OK) return st;
   float slopes[plsh::kMaxExactHeads];
-  // (a scale whose slope fp32 does not hold gets one that leaves the key at the
-  // position itself its weight, 0 times infinity being no number, and the next 0)
-  for (int64_t h = 0; h < q->H; ++h) slopes[h] = (float)std::min(1.4426950408889634 / sigma_h[h], 1e30);
+  if ((st = q4_slopes(q, sigma_h, slopes)) != PLSH_OK) return st;
   return q4_decode(q, cache, nullptr, slopes, pos, o, work, work_bytes, (cudaStream_t)stream);
+}
+
+plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                     int64_t* bytes) {
+  if (bytes == nullptr) return fail(PLSH_ERR_INVALID, "bytes is NULL");
+  plsh::Q4Cache c;
+  plsh_status st = check_q4_query(q, cache, &c, true);
+  if (st != PLSH_OK) return st;
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  *bytes = q4_rows_work_bytes(q, c, false, ctx->num_sms);
+  return PLSH_OK;
+}
+
+plsh_status plsh_alibi_exact_chunk_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                      const double* sigma_h, const int32_t* pos, const int32_t* len,
+                                      plsh_tensor* o, void* work, int64_t work_bytes, void* stream) {
+  return q4_rows_step(q, cache, sigma_h, pos, len, nullptr, 0, o, work, work_bytes,
+                      (cudaStream_t)stream);
+}
+
+plsh_status plsh_q4_prefix_work_bytes(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                      int64_t* bytes) {
+  if (bytes == nullptr) return fail(PLSH_ERR_INVALID, "bytes is NULL");
+  plsh::Q4Cache c;
+  plsh_status st = check_q4_query(q, cache, &c);
+  if (st != PLSH_OK) return st;
+  plsh::DeviceCtx* ctx = nullptr;
+  if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
+  *bytes = q4_rows_work_bytes(q, c, true, ctx->num_sms);
+  return PLSH_OK;
+}
+
+plsh_status plsh_alibi_exact_prefix_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
+                                              const double* sigma_h, const int32_t* pos,
+                                              const int32_t* prefix, int64_t prefix_pages,
+                                              plsh_tensor* o, void* work, int64_t work_bytes,
+                                              void* stream) {
+  if (prefix == nullptr || ((uintptr_t)prefix & 3u) != 0)
+    return fail(PLSH_ERR_INVALID, "prefix must be an int32 device pointer");
+  if (cache != nullptr && (prefix_pages < 1 || prefix_pages > cache->max_pages))
+    return fail(PLSH_ERR_INVALID, "prefix_pages must be in [1, max_pages]");
+  return q4_rows_step(q, cache, sigma_h, pos, nullptr, prefix, prefix_pages, o, work, work_bytes,
+                      (cudaStream_t)stream);
 }
 
 plsh_status plsh_stream_status(void* stream) {

@@ -8,6 +8,7 @@
 
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -197,6 +198,12 @@ PyObject* slots(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // is captured, or given a stream, takes one of its own, so that graphs that
 // replay at once share none.
 std::mutex g_launch;
+using WorkBytes = plsh_status (*)(const plsh_tensor*, const plsh_q4_cache*, int64_t*);
+at::Tensor new_workspace(const Call& c, int64_t bytes, const at::Tensor& like) {
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  if (c.given) guard.reset_stream(*c.given);
+  return at::empty({bytes}, like.options().dtype(at::kByte).requires_grad(false));
+}
 at::Tensor workspace(const Call& c, const plsh_tensor& q, const at::Tensor& like, PyObject* kept) {
   const bool own = c.given.has_value() || c10::cuda::currentStreamCaptureStatusMayInitCtx() !=
                                               c10::cuda::CaptureStatus::None;
@@ -214,12 +221,7 @@ at::Tensor workspace(const Call& c, const plsh_tensor& q, const at::Tensor& like
     Py_XDECREF(key);
     throw Refused("work");
   }
-  at::Tensor w;
-  {
-    c10::cuda::OptionalCUDAStreamGuard guard;
-    if (c.given) guard.reset_stream(*c.given);
-    w = at::empty({bytes}, like.options().dtype(at::kByte).requires_grad(false));
-  }
+  const at::Tensor w = new_workspace(c, bytes, like);
   if (!own) {
     PyObject* o = THPVariable_Wrap(w);
     const int bad = o == nullptr ? -1 : PyDict_SetItem(kept, key, o);
@@ -286,6 +288,96 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The workspace of a chunk's or a prefix's call: as above, but in an entry of
+// `kept` of its own, replaced by a larger one when a call needs that.
+at::Tensor rows_workspace(const Call& c, const plsh_tensor& q, const at::Tensor& like, PyObject* kept,
+                          const char* name, WorkBytes need) {
+  int64_t bytes = 0;
+  if (!ran([&] { return need(&q, &c.cache, &bytes); })) throw Refused("work");
+  if (c.given.has_value() ||
+      c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+    return new_workspace(c, bytes, like);
+  PyObject* key = Py_BuildValue("(sK)", name, (unsigned long long)(uintptr_t)c.stream());
+  if (key == nullptr) throw Refused("stream handle");
+  if (PyObject* have = PyDict_GetItemWithError(kept, key)) {
+    const at::Tensor w = tensor(have, "work");
+    if ((int64_t)w.nbytes() >= bytes) {
+      Py_DECREF(key);
+      return w;
+    }
+  }
+  const at::Tensor w = new_workspace(c, bytes, like);
+  PyObject* o = THPVariable_Wrap(w);
+  const int bad = o == nullptr ? -1 : PyDict_SetItem(kept, key, o);
+  Py_XDECREF(o);
+  Py_DECREF(key);
+  if (bad) throw Refused("workspace");
+  return w;
+}
+
+// chunk(cache, device, kept, q, scales as bytes, pos, lens | None, out | None,
+//       work | None, stream | None) -> o
+// prefix_decode(..., pos, prefix, out | None, ...) -> o
+template <bool PREFIX>
+PyObject* rows_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!counted(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Call c(a[0], a[1], a[9]);
+    const at::Tensor& q = tensor(a[3], "q");
+    const plsh_tensor tq = rows(q, c.dev, "q");
+    const int32_t* pos = indices(a[5], c.cache, c.dev, "pos");
+    if (!PyBytes_Check(a[4]) || PyBytes_GET_SIZE(a[4]) != (Py_ssize_t)(tq.H * sizeof(double)))
+      throw Refused("sigma must hold a scale per query head");
+    const double* sigma = reinterpret_cast<const double*>(PyBytes_AS_STRING(a[4]));
+    const int32_t *len = nullptr, *prefix = nullptr;
+    int64_t shared = 0;
+    if constexpr (PREFIX)
+      prefix = vector(a[6], c.dev, "prefix", &shared);
+    else
+      len = a[6] == Py_None ? nullptr : indices(a[6], c.cache, c.dev, "lens");
+    at::Tensor w;
+    if (a[8] == Py_None) {
+      if (!PyDict_Check(a[2])) throw Refused("not a cache");
+      w = PREFIX ? rows_workspace(c, tq, q, a[2], "prefix", plsh_q4_prefix_work_bytes)
+                 : rows_workspace(c, tq, q, a[2], "chunk", plsh_q4_chunk_work_bytes);
+    } else {
+      w = tensor(a[8], "work");
+      on_device(w, c.dev, "work");
+      if (!w.is_contiguous()) throw Refused("work must be contiguous");
+    }
+    PyObject* result;
+    plsh_tensor to;
+    if (a[7] == Py_None) {
+      c10::cuda::OptionalCUDAStreamGuard guard;
+      if (c.given) guard.reset_stream(*c.given);
+      // (rows from lens on are not written)
+      const at::Tensor o = len != nullptr
+                               ? at::zeros(q.sizes(), q.options().requires_grad(false))
+                               : at::detail::empty_cuda(q.sizes(), q.scalar_type(), q.device(), std::nullopt);
+      to = tq;
+      to.data = o.data_ptr();
+      result = THPVariable_Wrap(o);
+      if (result == nullptr) return nullptr;
+    } else {
+      to = rows(tensor(a[7], "out"), c.dev, "out");
+      result = a[7];
+      Py_INCREF(result);
+    }
+    void* st = c.stream();
+    void* work = w.data_ptr();
+    const int64_t bytes = (int64_t)w.nbytes();
+    const bool ok = ran([&] {
+      const std::lock_guard<std::mutex> hold(g_launch);      // (decode)
+      return PREFIX ? plsh_alibi_exact_prefix_decode_q4(&tq, &c.cache, sigma, pos, prefix, shared, &to,
+                                                        work, bytes, st)
+                    : plsh_alibi_exact_chunk_q4(&tq, &c.cache, sigma, pos, len, &to, work, bytes, st);
+    });
+    if (ok) return result;
+    Py_DECREF(result);
+    return nullptr;
+  });
+}
+
 PyObject* set_raise(PyObject*, PyObject* f) {
   Py_INCREF(f);
   Py_XSETREF(g_raise, f);
@@ -298,6 +390,8 @@ PyMethodDef kMethods[] = {
     {"reserve", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(reserve)), METH_FASTCALL, nullptr},
     {"slots", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(slots)), METH_FASTCALL, nullptr},
     {"decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(decode)), METH_FASTCALL, nullptr},
+    {"chunk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rows_step<false>)), METH_FASTCALL, nullptr},
+    {"prefix_decode", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rows_step<true>)), METH_FASTCALL, nullptr},
     {"set_raise", set_raise, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_plsh_binding", nullptr, -1, kMethods,

@@ -312,8 +312,28 @@ struct Q4DecodeArgs {
   void* work;
   int num_sms;
   int* err;
+  // exact ALiBi: m > 0: m rows a sequence (q, o [B, Hq, m, d]), row i < len[b] at
+  // pos[b] + i; with `prefix`, the first prefix_pages pages of every sequence;
+  // with `rows` too (bf16), only the keys behind them, rows left as pieces:
+  // rows[(b * Hkv + kv head) * chunks + chunk of its heads] = {first piece,
+  // second, pieces, 0} of pieces behind `work`'s ends (piece k > 0 is second +
+  // 2 (k - 1)): o [8][d], maximum [8], sum [8], base 2
+  int m = 0;
+  const int32_t* len = nullptr;
+  const int32_t* prefix = nullptr;
+  int prefix_pages = 0;
+  int4* rows = nullptr;
+  uint64_t wait_ns = 0;    // q4_many.cu
 };
 int64_t q4_decode_work_bytes(int d, int num_sms);
+// the workspace of `rows`, and its pieces
+int64_t q4_own_work_bytes(int d, int num_sms, int B, int Hkv, int G);
+const float* q4_own_pieces(const void* work, int num_sms);
+// q4_many.cu (bf16): many rows a KV head on the tensor cores; m rows a sequence, or
+// behind a prefix.  work: q4_many_work_bytes; a prefix's, behind q4_own_work_bytes
+int64_t q4_many_work_bytes(int d, int num_sms);
+cudaError_t launch_q4_chunk(const Q4DecodeArgs& a, cudaStream_t st);
+cudaError_t launch_q4_prefix(const Q4DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st);
 
 }  // namespace plsh

@@ -116,6 +116,15 @@ struct Slopes {
   float v[kMaxExactHeads];          // log2(e) / sigma_h
 };
 
+// What a launch of the exact step's kernel attends over:
+//   kStep    one row a sequence, every key up to its position;
+//   kRows    m rows a sequence (q, o [B, Hq, m, d]), row i at pos[b] + i, each a
+//            row of the flat list by itself;
+//   kShared  as kStep, the first pages being a prefix's that all sequences share;
+//   kOwn     as kStep, only the keys behind that prefix; rows are left as pieces,
+//            which a kernel elsewhere joins with the prefix's part.
+enum Form { kStep, kRows, kShared, kOwn };
+
 struct DecodeParams {
   Q4Cache c;
   const void* q;
@@ -130,6 +139,13 @@ struct DecodeParams {
   int4* ends;                       // exact: per CTA {row, first CTA, first piece} of a row that ends in it
   float* part;                      // pieces: o [8][D], m [8], l [8]
   int* err;
+  int m;                            // kRows: rows of a sequence
+  const int32_t* len;               // kRows: [B] rows that count, or null
+  const int32_t* prefix;            // kShared: the prefix's pages
+  int prefix_pages;
+  int first;                        // kOwn: the prefix's positions
+  int4* rows;                       // kOwn: per row {first piece, second, pieces, 0}
+  int row_pieces;                   // kOwn: piece of row 0 where a CTA has all of it
 };
 
 template <int D>
@@ -285,7 +301,19 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&o)[4])
 struct Piece {
   int b, kvh, h0, heads, pos, t0, t1;
   int first;         // first position any of the heads sees
+  int i;             // kRows: row of the sequence
 };
+
+// Element of head h of the row in q and o, and elements from a head to the next.
+template <int FORM, int D>
+__device__ __forceinline__ int64_t head_at(const DecodeParams& p, const Piece& pc, int h) {
+  const int64_t bh = (int64_t)pc.b * p.Hq + h;
+  return (FORM == kRows ? bh * p.m + pc.i : bh) * D;
+}
+template <int FORM, int D>
+__device__ __forceinline__ int64_t head_stride(const DecodeParams& p) {
+  return FORM == kRows ? (int64_t)p.m * D : D;
+}
 
 // ROWS: rows that a CTA's warps may be attending at once (a team of warps each)
 template <typename T, int D, int WARPS, int STAGES, int ROWS>
@@ -305,10 +333,11 @@ struct Smem {
 template <typename T, int D, int PACK>
 struct Query {
   uint4 w[Layout<D>::kGroups][sizeof(T) / 2];
+  template <int FORM>
   __device__ void load(const DecodeParams& p, const Piece& pc, int rank) {
     if (rank >= Layout<D>::kGroups) return;        // (prepare_query)
     const int lane = threadIdx.x & 31, g = (lane >> 2) % (kHeads / PACK), t = lane & 3;
-    const T* q = static_cast<const T*>(p.q) + ((int64_t)pc.b * p.Hq + pc.h0 + g) * D + 8 * t;
+    const T* q = static_cast<const T*>(p.q) + head_at<FORM, D>(p, pc, pc.h0 + g) + 8 * t;
 #pragma unroll
     for (int y = 0; y < Layout<D>::kGroups; ++y)
 #pragma unroll
@@ -362,11 +391,13 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const uint8_t* src, int
 
 // A warp's ring of blocks of one piece.  A block's two tiles lie one after the
 // other in a page, except with pages of 16 positions.
-template <typename T, int D>
+template <typename T, int D, int FORM>
 struct Ring {
   using L = Layout<D>;
   const uint8_t* head_data;
   const int32_t* table;
+  const int32_t* prefix;
+  int prefix_pages;
   int64_t page_bytes;
   uint32_t pages;
   uint32_t smem;
@@ -374,15 +405,20 @@ struct Ring {
   uint32_t absent = 0;          // two bits a stage: tiles that have no page
   int* err;
   __device__ Ring(const DecodeParams& p, const Piece& pc, const void* ring)
-      : table(p.c.table + (int64_t)pc.b * p.c.max_pages), pages((uint32_t)p.c.pages),
+      : table(p.c.table + (int64_t)pc.b * p.c.max_pages), prefix(p.prefix),
+        prefix_pages(p.prefix_pages), pages((uint32_t)p.c.pages),
         smem(smem_u32(ring)), log_blocks(p.c.page_shift - 5), last(pc.pos >> 4),
         lane(threadIdx.x & 31), err(p.err) {
     page_bytes = ((int64_t)p.c.H << (p.c.page_shift - 4)) * L::kTileBytes;
     head_data = p.c.data + ((int64_t)pc.kvh << (p.c.page_shift - 4)) * L::kTileBytes + 16 * lane;
   }
+  __device__ int32_t entry(int i) const {
+    if constexpr (FORM == kShared) return i < prefix_pages ? prefix[i] : table[i];
+    return table[i];
+  }
   // the page of a block's first tile (and, in general, of its second)
   __device__ int32_t page_of(int block) const {
-    return table[log_blocks >= 0 ? block >> log_blocks : 2 * block];
+    return entry(log_blocks >= 0 ? block >> log_blocks : 2 * block);
   }
   // `first`: the first position that the row reaches back to
   __device__ void fetch(int block, int st, int32_t pg, int first) {
@@ -398,7 +434,7 @@ struct Ring {
       // the second tile's page is looked up only if the row reaches it; the first
       // one's counts only if the row reaches back to it
       const bool need0 = 32 * block + kTile > first, need1 = 2 * block + 1 <= last;
-      const int32_t pg1 = need1 ? table[2 * block + 1] : -1;
+      const int32_t pg1 = need1 ? entry(2 * block + 1) : -1;
       if ((uint32_t)pg < pages)
         copy_async<L::kTileBytes>(dst, head_data + pg * page_bytes, lane);
       else
@@ -485,11 +521,11 @@ __device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, in
 struct Team {
   int first, size, number;     // number: of the CTA's teams
 };
-template <typename T, int D, bool EXACT, int PACK, int WARPS, int STAGES, int ROWS>
+template <typename T, int D, bool EXACT, int PACK, int FORM, int WARPS, int STAGES, int ROWS>
 __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, const Team& team,
                                        const Query<T, D, PACK>& query, const float* slopes,
                                        const int4* starts, Smem<T, D, WARPS, STAGES, ROWS>& sm,
-                                       Ring<T, D>& ring, bool ahead, T* o_row, float* part) {
+                                       Ring<T, D, FORM>& ring, bool ahead, T* o_row, float* part) {
   using L = Layout<D>;
   constexpr int Y = L::kGroups;
   constexpr bool kTwo = sizeof(T) == 4;         // two f16 terms
@@ -956,18 +992,32 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         const float inv = some ? sm.scale[row][h] : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] *= inv;
-        store_row(o_row + e, o);
+        if constexpr (FORM == kRows)
+          store_row(o_row + (e - h * D) + h * head_stride<FORM, D>(p), o);
+        else
+          store_row(o_row + e, o);
       }
     }
   }
   __syncthreads();           // before the next piece fills the rings
 }
 
-// Blocks that the row of sequence b takes (exact); a position out of range
-// takes none.
-__device__ __forceinline__ int64_t row_blocks(const DecodeParams& p, int b) {
-  const int pos = p.pos[b];
-  return pos < 0 || pos >= p.limit ? 0 : (pos >> 5) + 1;
+// The row of entry b of the flat list (exact): its sequence (and row), position
+// and blocks, the first of them the one that position pc.first is in; none where
+// the position is out of range.  False: a row past its sequence's last.
+template <int FORM>
+__device__ __forceinline__ bool find_row(const DecodeParams& p, int b, Piece& pc, int& blocks) {
+  pc.b = FORM == kRows ? b / p.m : b;
+  pc.i = FORM == kRows ? b - pc.b * p.m : 0;
+  pc.first = FORM == kOwn ? p.first : 0;
+  pc.pos = p.pos[pc.b];
+  if (FORM == kRows && pc.pos >= 0) pc.pos = (int)min((int64_t)pc.pos + pc.i, (int64_t)p.limit);
+  blocks = pc.pos < pc.first || pc.pos >= p.limit ? 0 : (pc.pos >> 5) - (pc.first >> 5) + 1;
+  if (FORM == kRows && p.len != nullptr && pc.i >= p.len[pc.b]) {
+    blocks = 0;
+    return false;
+  }
+  return true;
 }
 
 // heads of chunk c of a KV head
@@ -983,7 +1033,7 @@ __device__ __forceinline__ void unit_heads(const DecodeParams& p, int kvh, int c
 // A row whose blocks lie within one CTA is finished there; of one that crosses
 // CTAs, each leaves a piece (slot 2 i when it is the CTA's first, else
 // 2 i + 1), and the CTA where it ends says in ends[i] which pieces to join.
-template <typename T, int D, int PACK>
+template <typename T, int D, int PACK, int FORM>
 __global__ void __launch_bounds__(32 * kExactWarps, kExactCtas)
 q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ Slopes slopes) {
   extern __shared__ __align__(128) uint8_t raw[];
@@ -991,21 +1041,34 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   S& sm = *reinterpret_cast<S*>(raw);
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, units = p.c.H * p.chunks;
+  const int list = FORM == kRows ? p.c.B * p.m : p.c.B;
+  Piece pc;
   auto row_entries = [&](int b) -> int64_t {
-    const int64_t n = row_blocks(p, b);
+    int n;
+    find_row<FORM>(p, b, pc, n);
     return n == 0 ? 0 : n + kRowCost;
   };
   // all sequences' entries; idle sequences' rows are zeroed on the way, by a
   // thread each (made for a few of them: each is Hq D / 8 stores in a row)
   int64_t sum = 0;
 #pragma unroll 4
-  for (int b = tid; b < p.c.B; b += 32 * kExactWarps) {
-    const int64_t n = row_entries(b);
-    sum += n;
-    if (n == 0 && b % gridDim.x == blockIdx.x) {
-      if (p.pos[b] >= 0) atomicOr(p.err, kErrCachePlace);
-      uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)b * p.Hq * D);
-      for (int e = 0; e < p.Hq * D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
+  for (int b = tid; b < list; b += 32 * kExactWarps) {
+    int n;
+    const bool row = find_row<FORM>(p, b, pc, n);
+    sum += n == 0 ? 0 : n + kRowCost;
+    if (row && n == 0 && b % gridDim.x == blockIdx.x) {
+      if (pc.pos >= p.limit) atomicOr(p.err, kErrCachePlace);
+      if constexpr (FORM == kOwn) {
+        for (int u = 0; u < units; ++u) p.rows[b * units + u] = make_int4(0, 0, 0, 0);
+      } else if constexpr (FORM == kRows) {
+        for (int h = 0; h < p.Hq; ++h) {
+          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + head_at<FORM, D>(p, pc, h));
+          for (int e = 0; e < D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
+        }
+      } else {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)b * p.Hq * D);
+        for (int e = 0; e < p.Hq * D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
 #pragma unroll
@@ -1023,7 +1086,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   // the sequence that entry `begin` is of, a turn of one sequence a thread
   int64_t base = 0;                       // entries of one unit before the turn's sequences
   for (int b0 = 0;; b0 += 32 * kExactWarps) {
-    const int64_t n = b0 + tid < p.c.B ? row_entries(b0 + tid) : 0;
+    const int64_t n = b0 + tid < list ? row_entries(b0 + tid) : 0;
     int64_t upto = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1049,38 +1112,48 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     base += turn;
   }
   __syncthreads();
-  Piece pc;
-  pc.b = (int)sm.found[0];
-  pc.first = 0;
+  int at = (int)sm.found[0];
   base = sm.found[1];
   int slot = 2 * blockIdx.x;
   for (int64_t f = begin; f < end;) {
-    const int64_t n = row_entries(pc.b), rel = f - base;
+    const int64_t n = row_entries(at), rel = f - base;
     if (rel >= n * units) {
       base += n * units;
-      ++pc.b;
+      ++at;
       continue;
     }
     const int u = (int)(rel / n);
     const int64_t row = base + u * n, till = min(end, row + n);     // [row, row + n): its entries
-    pc.pos = p.pos[pc.b];
     pc.t0 = (int)max((int64_t)0, f - row - kRowCost);
     pc.t1 = (int)(till - row - kRowCost);
     f = till;
     if (pc.t1 <= pc.t0) continue;                 // the row's cost alone
     unit_heads(p, u / p.chunks, u % p.chunks, pc);
-    const bool last = till == row + n;
-    if (tid == 0 && pc.t0 > 0 && last) {
+    const bool first = pc.t0 == 0, last = till == row + n;
+    if (tid == 0 && last && (FORM == kOwn || !first)) {
       const int i0 = (int)((row + kRowCost) / per);    // the CTA of its first block
-      p.ends[blockIdx.x] = make_int4(pc.b * units + u, i0, row <= i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
+      const int slot0 = row <= i0 * per ? 2 * i0 : 2 * i0 + 1;
+      if constexpr (FORM == kOwn) {
+        const int r = at * units + u;
+        p.rows[r] = first ? make_int4(p.row_pieces + r, 0, 1, 0)
+                          : make_int4(slot0, 2 * (i0 + 1), (int)blockIdx.x - i0 + 1, 0);
+      } else {
+        p.ends[blockIdx.x] = make_int4(at * units + u, i0, slot0, 0);
+      }
+    }
+    int64_t piece = slot;
+    if constexpr (FORM == kOwn) {
+      pc.t0 += pc.first >> 5;
+      pc.t1 += pc.first >> 5;
+      if (first && last) piece = p.row_pieces + at * units + u;
     }
     Query<T, D, PACK> query;
-    query.load(p, pc, tid >> 5);
-    Ring<T, D> ring(p, pc, sm.ring[tid >> 5]);
-    attend<T, D, true, PACK>(p, pc, Team{0, kExactWarps, 0}, query, slopes.v, nullptr, sm, ring, false,
-                             pc.t0 == 0 && last ? static_cast<T*>(p.o) + ((int64_t)pc.b * p.Hq + pc.h0) * D
-                                                : nullptr,
-                             p.part + (int64_t)slot * part_floats<D>());
+    query.template load<FORM>(p, pc, tid >> 5);
+    Ring<T, D, FORM> ring(p, pc, sm.ring[tid >> 5]);
+    attend<T, D, true, PACK, FORM>(
+        p, pc, Team{0, kExactWarps, 0}, query, slopes.v, nullptr, sm, ring, false,
+        FORM != kOwn && first && last ? static_cast<T*>(p.o) + head_at<FORM, D>(p, pc, pc.h0) : nullptr,
+        p.part + piece * part_floats<D>());
     slot = 2 * blockIdx.x + 1;
   }
 }
@@ -1157,7 +1230,7 @@ __device__ void join_pieces(const DecodeParams& p, int first, int first2, int st
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int FORM>
 __global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __grid_constant__ DecodeParams p) {
   grid_dep_wait();
   const int4 end = p.ends[blockIdx.x];
@@ -1166,8 +1239,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __
   Piece pc;
   unit_heads(p, end.x % units / p.chunks, end.x % p.chunks, pc);
   if (h >= pc.heads) return;
+  int blocks;
+  find_row<FORM>(p, end.x / units, pc, blocks);
   join_pieces<T, D>(p, end.z, 2 * (end.y + 1), 2, (int)blockIdx.x - end.y + 1, h,
-                    static_cast<T*>(p.o) + ((int64_t)(end.x / units) * p.Hq + pc.h0 + h) * D);
+                    static_cast<T*>(p.o) + head_at<FORM, D>(p, pc, pc.h0 + h));
 }
 
 // Approximate.  KV heads by the largest scale of their query heads, widest
@@ -1272,8 +1347,8 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   const bool none = pc.pos < 0 || pc.pos >= p.limit;
   if (valid && none && rank == 0 && lane == 0 && pc.pos >= 0) atomicOr(p.err, kErrCachePlace);
   Query<T, D, PACK> query;
-  query.load(p, pc, rank);
-  Ring<T, D> ring(p, pc, sm.ring[warp]);
+  query.template load<kStep>(p, pc, rank);
+  Ring<T, D, kStep> ring(p, pc, sm.ring[warp]);
   // A warp's first block is copied before the bins are known: the newest of the
   // row, always needed, or the next ones, which the team's size makes likely
   // (a page of its own only if its index is good: whether it is needed, and to
@@ -1328,7 +1403,7 @@ q4_approx_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__
   static_assert(sizeof(sm.q) >= sizeof(float) * part_floats<D>(), "a piece fits");
   float* part = gr.cluster > 1 ? reinterpret_cast<float*>(sm.q)
                                : p.part + (int64_t)blockIdx.x * part_floats<D>();
-  attend<T, D, false, PACK>(p, pc, team, query, nullptr, starts, sm, ring, ahead,
+  attend<T, D, false, PACK, kStep>(p, pc, team, query, nullptr, starts, sm, ring, ahead,
                             valid && shares == 1 ? o : nullptr, valid && shares > 1 ? part : nullptr);
   if (gr.cluster > 1 && shares > 1 && valid) join_cluster<T, D>(part, share, shares, pc.heads, o);
 }
@@ -1349,19 +1424,21 @@ q4_approx_join_kernel(const __grid_constant__ DecodeParams p, const __grid_const
 
 int max_ctas(int num_sms) { return num_sms * kExactCtas; }
 
-template <typename T, int D>
+template <typename T, int D, int FORM>
 cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
   using S = Smem<T, D, kExactWarps, kExactStages, 1>;
   Slopes s;
   for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
   // (a limit up to 2^31 - 16)
-  const int64_t entries = (int64_t)p.c.B * p.c.H * p.chunks * (((int64_t)p.limit + 31) / 32 + kRowCost);
+  const int64_t list = (int64_t)p.c.B * (FORM == kRows ? p.m : 1);
+  const int64_t entries = list * p.c.H * p.chunks * (((int64_t)p.limit + 31) / 32 + kRowCost);
   const int64_t want = (entries + kMinBlocks - 1) / kMinBlocks;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
-  auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2> : q4_exact_kernel<T, D, 1>;
+  auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2, FORM> : q4_exact_kernel<T, D, 1, FORM>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(S));
   if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), 32 * kExactWarps, sizeof(S), st, p, s);
-  if (e == cudaSuccess) e = launch_dependent(q4_exact_join_kernel<T, D>, dim3(grid, p.per_chunk), 32 * kJoinWarps, 0, st, p);
+  if (e == cudaSuccess && FORM != kOwn)
+    e = launch_dependent(q4_exact_join_kernel<T, D, FORM>, dim3(grid, p.per_chunk), 32 * kJoinWarps, 0, st, p);
   return e;
 }
 
@@ -1450,7 +1527,12 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
 
 template <typename T, int D>
 cudaError_t launch_typed(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
-  return a.rec ? launch_approx<T, D>(p, a, st) : launch_exact<T, D>(p, a, st);
+  if (a.rec) return launch_approx<T, D>(p, a, st);
+  if (a.m > 0) return launch_exact<T, D, kRows>(p, a, st);
+  if constexpr (sizeof(T) == 2)
+    if (a.rows != nullptr) return launch_exact<T, D, kOwn>(p, a, st);
+  if (a.prefix != nullptr) return launch_exact<T, D, kShared>(p, a, st);
+  return launch_exact<T, D, kStep>(p, a, st);
 }
 
 }  // namespace
@@ -1458,6 +1540,17 @@ cudaError_t launch_typed(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st
 // ends [CTAs] int4, then two pieces of a CTA (exact), or one of a share
 int64_t q4_decode_work_bytes(int d, int num_sms) {
   return (int64_t)max_ctas(num_sms) * (sizeof(int4) + 2 * sizeof(float) * kHeads * (d + 2));
+}
+
+// behind these, a piece and an int4 of every row
+int q4_own_rows(int B, int Hkv, int G) { return B * Hkv * ((G + kHeads - 1) / kHeads); }
+int64_t q4_own_work_bytes(int d, int num_sms, int B, int Hkv, int G) {
+  return q4_decode_work_bytes(d, num_sms) +
+         (int64_t)q4_own_rows(B, Hkv, G) * (sizeof(int4) + sizeof(float) * kHeads * (d + 2));
+}
+
+const float* q4_own_pieces(const void* work, int num_sms) {
+  return reinterpret_cast<const float*>(static_cast<const int4*>(work) + max_ctas(num_sms));
 }
 
 cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
@@ -1478,6 +1571,13 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
   p.ends = static_cast<int4*>(a.work);
   p.part = reinterpret_cast<float*>(p.ends + max_ctas(a.num_sms));
   p.err = a.err;
+  p.m = a.m;
+  p.len = a.len;
+  p.prefix = a.prefix;
+  p.prefix_pages = a.prefix_pages;
+  p.first = a.prefix_pages << a.c.page_shift;
+  p.rows = a.rows;
+  p.row_pieces = 2 * max_ctas(a.num_sms);
   if (a.dtype == PLSH_BF16)
     return a.c.d == 64 ? launch_typed<__nv_bfloat16, 64>(p, a, st)
                        : launch_typed<__nv_bfloat16, 128>(p, a, st);
