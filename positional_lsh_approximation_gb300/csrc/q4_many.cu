@@ -20,17 +20,19 @@
 //   K  times one per position, largest below 2^-6: undone in the fp32 scores
 //      (cs_j, times q's and log2(e) / sqrt(d));
 //   V  times one per group of 32 values, R_y, by the first step of a piece, and one
-//      per step, ev, by how far any group exceeds that: largest below 1.  2^ev goes
+//      per step, ev, by how far any group exceeds that: largest below 2^-6.  2^ev goes
 //      into the step's weights, P = 2^{x + ev - M} with M the running maximum of
 //      x + ev, so that a large value takes precision from others of its own step
 //      alone; the row sum takes P 2^-ev in fp32.
 // P and V are rounded to f16 (2^-11 of themselves): bf16's 2^-8 would show beside
 // the output's own rounding.  Scores, sums and maxima are fp32.
 //
-// Warps of a CTA (one per SM): 0-3 and 4-7 softmax of the two tiles, a thread a
-// row; 8-11 take codes apart; 12 issues the products, PV_A(g-1) S_A(g) PV_B(g-1)
-// S_B(g), so that the tensor cores work on one tile while the other's scores become
-// weights; 13 lists the items and copies the codes.  The flat list (KV head, item,
+// Warps of a CTA (one per SM): 0-7 and 8-15 softmax of the two tiles, two threads a
+// row with 64 of a step's keys each; 16-19 take K's codes apart and 20-23 V's, so
+// that K (two tiles) runs ahead of V (one tile); 24 issues
+// the products, PV_A(g-1) S_A(g) PV_B(g-1) S_B(g), so that the tensor cores work on
+// one tile while the other's scores become weights; 25 lists the items and copies
+// the codes.  Registers are split 80 / 64 / 56.  The flat list (KV head, item,
 // step), each item preceded by kItemCost entries for its beginning and end, is cut
 // into equal shares of the CTAs; items cut by a CTA's edge are joined by a second
 // kernel, in a fixed order.  Every wait is bounded; on expiry the CTA raises the
@@ -42,6 +44,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "plsh_internal.h"
 #include "q4.cuh"
@@ -55,16 +58,17 @@ using namespace ptx;
 
 constexpr int BM = 128, BN = 128;       // rows of a tile, keys of a step
 constexpr int kItemRows = 2 * BM;
-constexpr int kDeqWarp = 8, kDeqWarps = 4, kMmaWarp = 12, kProdWarp = 13, kWarps = 14;
-constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps;
-constexpr int kTiles = BN / kTile;      // tiles of 16 positions of a step
+constexpr int kSoftWarps = 16, kKWarp = 16, kVWarp = 20, kDeqWarps = 4, kMmaWarp = 24, kProdWarp = 25, kWarps = 28;
+constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps, kTileThreads = 256;
+// of 896 threads' 72 at launch: 512 x 80 + 256 x 64 + 128 x 56 = 64512, all of them
+constexpr int kRegsSoftmax = 80, kRegsDeq = 64, kRegsRest = 56;
+enum { BAR_V = 1, BAR_TILE = 2, BAR_PAIR = 4 };      // named barriers: V's warps, a tile's, two warps of a row
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
 constexpr int kItemCost = 2;            // steps that beginning and ending an item costs
 constexpr int kMinSteps = 4;            // steps of a CTA at least
 constexpr uint32_t kTmemCols = 512;     // S_A | S_B | O_A | O_B; P over S
 constexpr uint32_t kColP = 64, kColO = 256;
-constexpr float kRescaleLog2 = 8.f;     // a maximum that grew by more moves the reference
-constexpr float kGrowLog2 = 15.f;       // largest weight 2^15
+constexpr float kGrowLog2 = 15.f;       // largest weight 2^15: above, the reference moves
 constexpr float kNothing = -3.402823466e38f;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -74,15 +78,13 @@ template <int D>
 struct Sizes {
   static constexpr int Y = D / kGroup;
   static constexpr uint32_t kTileB = BM * D * 2;               // an f16 tile
-  static constexpr uint32_t kRaw = kTiles * Layout<D>::kTileBytes;
-  static constexpr int kRawStages = D == 128 ? 2 : 4;
-  static constexpr uint32_t kQ = 0, kK = 2 * kTileB, kV = 4 * kTileB, kRawAt = 5 * kTileB,
-                            kEnd = kRawAt + kRawStages * kRaw;
+  static constexpr uint32_t kQ = 0, kK = 2 * kTileB, kV = 4 * kTileB, kEnd = 6 * kTileB;      // two of each
 };
 
 enum {
-  B_IFULL = 0, B_IEMPTY = 2, B_RAWFULL = 4, B_RAWEMPTY = 8, B_KREADY = 12, B_KEMPTY = 14, B_VREADY = 16,
-  B_VEMPTY, B_QFULL, B_SFULL = 20, B_PFULL = 22, B_ODONE = 24, B_DRAIN = 26, NUM_BARS
+  B_IFULL = 0, B_IEMPTY = 2, B_VEMPTY = 4, B_VREADY = 6, B_VINFO = 8, B_KREADY = 12,
+  B_KEMPTY = 16, B_QFULL = 22, B_SFULL = 24, B_PFULL = 26, B_ODONE = 28,
+  B_DRAIN = 30, NUM_BARS
 };
 
 // Rows [row0, row1) of a sequence's (or the batch's) rows of one KV head against the
@@ -98,15 +100,16 @@ struct Ctl {
   Item ring[2];
   alignas(16) uint2 kq[BN][Y];          // per position and group: step, lo as f16 pairs
   alignas(16) uint2 vq[Y][BN];
-  alignas(16) float cs[2][2][BN];       // per step and tile: a position's factor of the scores
-  uint32_t mask[2][4];                  // per step: positions that count
-  uint32_t vnan[2][Y][4];               // positions whose group of V is no number
-  int ev[2], any_nan[2];
-  int vr[2][Y];                         // per item slot: V's exponents R_y + 1
-  uint32_t vmax[kDeqWarps][Y];
-  uint32_t qmax[2][4];
-  float qs[2];
-  int present[4];                       // per raw stage: tiles that were copied
+  // K and V run up to two steps ahead of the products, the softmax up to one behind
+  alignas(16) float cs[4][4];           // per step and 32 positions: K's factor, to be undone
+  alignas(16) uint32_t mask[4][4];      // per step: positions that count
+  uint32_t vnan[4][Y][4];               // positions whose group of V is no number
+  alignas(16) int ev[4][4];             // per step and 32 positions: V's exponent beyond R_y
+  alignas(16) int any_nan[4][4];
+  int vr[2][Y];                         // per item slot: V's exponents R_y, less 14
+  int vmax[kDeqWarps][Y];
+  uint32_t qmax[2][8];
+  float pair[2][2][BM];                 // per tile and half: what the two threads of a row tell each other
   int64_t sums[kWarps], found[2];
   uint32_t tmem_base;
   int abort;
@@ -130,12 +133,27 @@ struct ManyParams {
   float slope[kMaxExactHeads];          // log2(e) / sigma_h
 };
 
+template <int N>
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void leave_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 template <int D>
 __host__ __device__ constexpr int64_t part_floats() { return kItemRows * (D + 2); }
 
 __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23); }
 
 // A barrier of `n` threads that tells all of them whether all say ok.
+__device__ __forceinline__ bool barrier_or(int id, int n, bool any) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((int)any)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ bool barrier_and(int id, int n, bool ok) {
   int r;
   asm volatile(
@@ -147,26 +165,107 @@ __device__ __forceinline__ bool barrier_and(int id, int n, bool ok) {
   return r != 0;
 }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
   return d;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
+}
+// Two codes of a word as f16 numbers: bits 0-3 of each half (1024 + c, less 1024),
+// or 4-7 (64 + c, less 64).
+__device__ __forceinline__ uint32_t low_codes(uint32_t w) {
+  return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64006400u);
+}
+__device__ __forceinline__ uint32_t high_codes(uint32_t w) {
+  return hsub2((w & 0x00f000f0u) | 0x54005400u, 0x54005400u);
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// The products and the commit of tc_ptx.cuh, by the lane whose `lead` is set.
+__device__ __forceinline__ void product_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void product_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
+// A 128-byte swizzled operand's descriptor from its lower word; rows 1024 bytes apart
+// by eights.
+__device__ __forceinline__ uint64_t descriptor(uint32_t low) {
+  return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | low;
 }
 
 // Bit e set when key jc + e is at or before position jc + eb.
 __device__ __forceinline__ uint32_t upto_mask(int eb) {
   return eb < 0 ? 0u : eb >= 31 ? 0xffffffffu : (2u << eb) - 1u;
+}
+
+// Where the warp's 32 positions of a step lie: two tiles of 16, or nullptr.
+template <int D, bool PREFIX>
+struct Source {
+  const uint8_t* head;           // tile 0 of page 0 of the KV head
+  const int32_t* table;
+  int64_t page_bytes, pages;
+  int shift, last, first;        // first: of the warp's positions, within a step
+  __device__ Source(const ManyParams& p, const Item& it, int first)
+      : table(PREFIX ? p.prefix : p.c.table + (int64_t)it.b * p.c.max_pages), pages(p.c.pages), shift(p.c.page_shift),
+        last(it.last), first(first) {
+    const int64_t tile = Layout<D>::kTileBytes;
+    page_bytes = ((int64_t)p.c.H << (shift - 4)) * tile;
+    head = p.c.data + ((int64_t)it.kvh << (shift - 4)) * tile;
+  }
+  // the table's entries of step s (-1: none needed)
+  __device__ int2 entries(int s, int k0) const {
+    const int at = BN * s + first;
+    int2 e = make_int2(-1, -1);
+    if (s >= k0 && at <= last) {
+      e.x = table[at >> shift];
+      if (at + kTile <= last) e.y = shift == 4 ? table[(at >> 4) + 1] : e.x;
+    }
+    return e;
+  }
+  __device__ const uint8_t* tile(int s, int k, int32_t pg) const {
+    if (pg < 0 || pg >= pages) return nullptr;
+    const int in_page = (BN * s + first + kTile * k) & ((1 << shift) - 1);
+    return head + pg * page_bytes + (in_page >> 4) * Layout<D>::kTileBytes;
+  }
+};
+
+// N words from global memory, zeros from nowhere.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* at, bool there, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 a = there ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  } else {
+    static_assert(N == 2, "a group of 32 or two");
+    const uint2 a = there ? *reinterpret_cast<const uint2*>(at) : make_uint2(0, 0);
+    w[0] = a.x, w[1] = a.y;
+  }
 }
 
 template <int N>
@@ -230,20 +329,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
   if (tid == 0) {
     for (int k = 0; k < 2; ++k) {
       mbar_init(bar(B_IFULL + k), 1);
-      mbar_init(bar(B_IEMPTY + k), 8 + kDeqWarps + 1);
-      mbar_init(bar(B_KREADY + k), kDeqWarps);
+      mbar_init(bar(B_IEMPTY + k), kSoftWarps + 2 * kDeqWarps + 1);
+      mbar_init(bar(B_VREADY + k), kDeqWarps);
+      mbar_init(bar(B_VEMPTY + k), 1);
       mbar_init(bar(B_KEMPTY + k), 1);
-      mbar_init(bar(B_QFULL + k), BM);
+      mbar_init(bar(B_QFULL + k), kTileThreads);
       mbar_init(bar(B_SFULL + k), 1);
-      mbar_init(bar(B_PFULL + k), BM);
+      mbar_init(bar(B_PFULL + k), kTileThreads);
       mbar_init(bar(B_ODONE + k), 1);
     }
     for (int k = 0; k < 4; ++k) {
-      mbar_init(bar(B_RAWFULL + k), 1);
-      mbar_init(bar(B_RAWEMPTY + k), kDeqWarps);
+      mbar_init(bar(B_KREADY + k), kDeqWarps);
+      mbar_init(bar(B_VINFO + k), kDeqWarps);
     }
-    mbar_init(bar(B_VREADY), kDeqWarps);
-    mbar_init(bar(B_VEMPTY), 1);
     mbar_init(bar(B_DRAIN), 1);
     ctl->abort = 0;
     fence_barrier_init();
@@ -322,11 +420,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     __syncthreads();
   }
 
+  if (warp >= kMmaWarp) {
+    leave_registers<kRegsRest>();
   if (warp == kProdWarp) {
-    // ---------------------------------------------------- items, copies of codes
+    // ----------------------------------------------------------------- items
     bool ok = true;
-    int seq = 0, g = 0, slot = 2 * blockIdx.x;
-    int issued[4] = {0, 0, 0, 0};
+    int seq = 0, slot = 2 * blockIdx.x;
     auto publish = [&](const Item& it) {
       const int s = seq & 1;
       ok = __all_sync(FULL, mbar_wait(bar(B_IEMPTY + s), ((uint32_t)(seq >> 1) & 1u) ^ 1u, abort, lim));
@@ -368,38 +467,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         publish(Item{1, b, kvh, kItemRows * t, min(rows, kItemRows * (t + 1)), t0, t1, pos, last,
                      whole ? -1 : slot});
         slot = 2 * blockIdx.x + 1;
-        // a lane of the first eight a tile of 16 positions; the table entries of a
-        // step are read while the step before waits for its room
-        const int32_t* table = PREFIX ? p.prefix : p.c.table + (int64_t)b * p.c.max_pages;
-        auto entry = [&](int s) -> int32_t {
-          const int at = BN * s + kTile * lane;
-          return lane < kTiles && s >= t0 && at <= last ? table[at >> p.c.page_shift] : -1;
-        };
-        int32_t next = entry(t1 - 1);
-        for (int s = t1 - 1; ok && s >= t0; --s, ++g) {
-          const int32_t pg = next;
-          next = entry(s - 1);
-          const int st = g % S::kRawStages;
-          ok = __all_sync(FULL, mbar_wait(bar(B_RAWEMPTY + st), ((uint32_t)(g / S::kRawStages) & 1u) ^ 1u, abort, lim));
-          if (!ok) break;
-          const int at = BN * s + kTile * lane;
-          const bool want = lane < kTiles && at <= last, here = want && pg >= 0 && pg < p.c.pages;
-          if (want && !here) atomicOr(p.err, kErrCachePlace);
-          const unsigned got = __ballot_sync(FULL, here);
-          if (lane == 0) {
-            *reinterpret_cast<volatile int*>(&ctl->present[st]) = (int)got;
-            mbar_arrive_expect_tx(bar(B_RAWFULL + st), __popc(got) * Layout<D>::kTileBytes);
-          }
-          ++issued[st];
-          __syncwarp();
-          if (here) {
-            const int in_page = at & ((1 << p.c.page_shift) - 1);
-            const uint8_t* src = p.c.data + (((int64_t)pg * p.c.H + kvh) * (1 << (p.c.page_shift - 4)) + (in_page >> 4)) *
-                                                (int64_t)Layout<D>::kTileBytes;
-            bulk_load(sbase + S::kRawAt + st * S::kRaw + lane * Layout<D>::kTileBytes, src, Layout<D>::kTileBytes,
-                      bar(B_RAWFULL + st));
-          }
-        }
       }
     }
     if (ok) publish(Item{});
@@ -407,149 +474,157 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       *abort = 1;
       atomicOr(p.err, kErrTimeout);
     }
-    // every copy this warp started lands before the CTA can exit
-#pragma unroll
-    for (int st = 0; st < S::kRawStages; ++st)
-      if (issued[st]) mbar_wait(bar(B_RAWFULL + st), (uint32_t)(issued[st] - 1) & 1u, nullptr, lim);
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ the products
-    if (lane == 0) {
+    // (The whole warp runs this, and one lane's predicate issues: so everything a
+    // product takes stays in uniform registers.  With one lane in a branch of its own
+    // they were moved there one by one, about 100 cycles a product of 64.  A
+    // descriptor's upper word is a constant, its lower one an address / 16 and the
+    // leading offset.)
+    {
+      const uint32_t lead = elect_one();
+      const uint32_t tm = __shfl_sync(FULL, tmem, 0);
       constexpr uint32_t id_s = idesc_f16_f32(BM, BN, 0, 0), id_pv = idesc_f16_f32(BM, D, 0, 1);
-      const uint64_t dq0 = desc_sw128(sbase + S::kQ, 16, 1024);
-      const uint64_t dk0 = desc_sw128(sbase + S::kK, 16, 1024);
-      const uint64_t dv0 = desc_sw128(sbase + S::kV, kHalf, 1024);
-      auto issue_s = [&](int tile, int kb) {
+      const uint32_t base = (__shfl_sync(FULL, sbase, 0) >> 4) & 0x3fffu;
+      auto issue_s = [&](int tile, uint32_t kb) {
+        const uint32_t q = (base + ((S::kQ + tile * S::kTileB) >> 4)) | (16u >> 4) << 16;
+        const uint32_t k = (base + ((S::kK + kb * S::kTileB) >> 4)) | (16u >> 4) << 16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tmem + tile * BN, desc_add(dq0, tile * (S::kTileB >> 4) + off),
-                      desc_add(dk0, kb * (S::kTileB >> 4) + off), id_s, kk > 0 ? 1u : 0u);
+          product_ss(lead, tm + tile * BN, descriptor(q + off), descriptor(k + off), id_s, kk > 0 ? 1u : 0u);
         }
-        mma_commit(bar(B_SFULL + tile));
+        commit(lead, bar(B_SFULL + tile));
       };
-      auto issue_pv = [&](int tile, bool first) {
+      auto issue_pv = [&](int tile, uint32_t first, uint32_t vb) {
+        const uint32_t v = (base + ((S::kV + vb * S::kTileB) >> 4)) | (kHalf >> 4) << 16;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_f16kind_ts(tmem + kColO + tile * 128, tmem + tile * BN + kColP + kk * 8,
-                         desc_add(dv0, kk * (2048 >> 4)), id_pv, first && kk == 0 ? 0u : 1u);
+          product_ts(lead, tm + kColO + tile * 128, tm + tile * BN + kColP + kk * 8,
+                     descriptor(v + kk * (2048 >> 4)), id_pv, kk == 0 ? 1u - first : 1u);
+      };
+      auto wait = [&](int k, uint32_t parity) -> bool {
+        return __all_sync(FULL, mbar_wait(bar(k), parity, abort, lim));
       };
       bool ok = true;
-      int g = 0, gb = 0, seq = 0, jj = 0;        // steps, steps with both tiles, items, step of the item
-      bool have = false, pfirst = false, plast = false, ptwo = false;
-      int pslot = 0;
-      Item it{};
+      uint32_t g = 0, gb = 0, seq = 0;           // steps, steps with both tiles, items
+      int jj = 0, steps = 0;                     // step of the item, its steps (0: the end)
+      bool two = false, ptwo = false, pfirst = false, plast = false;      // p: of the step before
       auto next_item = [&]() {
-        ok = mbar_wait(bar(B_IFULL + (seq & 1)), (uint32_t)(seq >> 1) & 1u, abort, lim);
-        it = ok ? read_item(ctl->ring, seq & 1) : Item{};
+        ok = wait(B_IFULL + (seq & 1), (seq >> 1) & 1u);
+        const volatile Item& it = ctl->ring[seq & 1];
+        steps = __shfl_sync(FULL, ok && it.valid ? it.k1 - it.k0 : 0, 0);
+        two = __shfl_sync(FULL, it.row1 - it.row0, 0) > BM;
         jj = 0;
       };
       // P V of the step before, tile A or B
       auto close_a = [&]() -> bool {
-        if (!mbar_wait(bar(B_PFULL), (uint32_t)(g - 1) & 1u, abort, lim) ||
-            !mbar_wait(bar(B_VREADY), (uint32_t)(g - 1) & 1u, abort, lim))
-          return false;
+        const uint32_t vb = (g - 1) & 1;
+        if (!wait(B_VREADY + vb, ((g - 1) >> 1) & 1u) || !wait(B_PFULL, (g - 1) & 1u)) return false;
         tc_fence_after();
-        issue_pv(0, pfirst);
-        if (plast) mma_commit(bar(B_ODONE));
-        if (!ptwo) mma_commit(bar(B_VEMPTY));
+        issue_pv(0, pfirst, vb);
+        if (plast) commit(lead, bar(B_ODONE));
+        if (!ptwo) commit(lead, bar(B_VEMPTY + vb));
         return true;
       };
-      auto close_b = [&](int steps) -> bool {
+      auto close_b = [&]() -> bool {
+        const uint32_t vb = (g - 1) & 1;
         if (ptwo) {
-          if (!mbar_wait(bar(B_PFULL + 1), (uint32_t)(steps - 1) & 1u, abort, lim)) return false;
+          if (!wait(B_PFULL + 1, (gb - 1) & 1u)) return false;
           tc_fence_after();
-          issue_pv(1, pfirst);
-          mma_commit(bar(B_VEMPTY));
-          if (plast) mma_commit(bar(B_ODONE + 1));
+          issue_pv(1, pfirst, vb);
+          commit(lead, bar(B_VEMPTY + vb));
+          if (plast) commit(lead, bar(B_ODONE + 1));
         }
-        if (plast) mbar_arrive(bar(B_IEMPTY + pslot));
         return true;
       };
       next_item();
-      while (ok && it.valid) {
-        const bool two = it.row1 - it.row0 > BM;
-        const int kb = g & 1;
-        if (have && !(ok = close_a())) break;
-        ok = mbar_wait(bar(B_KREADY + kb), (uint32_t)(g >> 1) & 1u, abort, lim) &&
-             (jj > 0 || mbar_wait(bar(B_QFULL), (uint32_t)seq & 1u, abort, lim));
+      uint32_t done = 0;                         // items whose slot was released
+      while (ok && steps > 0) {
+        // (K first, which is ready long before: nothing stands between the two products)
+        ok = wait(B_KREADY + (g & 3), (g >> 2) & 1u);
+        if (!ok || (g > 0 && !(ok = close_a()))) break;
+        if (jj == 0) ok = wait(B_QFULL, seq & 1u);
         if (!ok) break;
         tc_fence_after();
-        issue_s(0, kb);
-        if (!two) mma_commit(bar(B_KEMPTY + kb));
-        if (have && !(ok = close_b(gb))) break;
+        issue_s(0, g & 1);
+        if (!two) commit(lead, bar(B_KEMPTY + (g & 1)));
+        if (g > 0) {
+          if (!(ok = close_b())) break;
+          if (plast && lead) mbar_arrive(bar(B_IEMPTY + (done & 1)));
+          if (plast) ++done;
+        }
         if (two) {
-          ok = jj > 0 || mbar_wait(bar(B_QFULL + 1), (uint32_t)seq & 1u, abort, lim);
+          ok = jj > 0 || wait(B_QFULL + 1, seq & 1u);
           if (!ok) break;
           tc_fence_after();
-          issue_s(1, kb);
-          mma_commit(bar(B_KEMPTY + kb));
+          issue_s(1, g & 1);
+          commit(lead, bar(B_KEMPTY + (g & 1)));
           ++gb;
         }
-        have = true;
         pfirst = jj == 0;
-        plast = jj == it.k1 - it.k0 - 1;
         ptwo = two;
-        pslot = seq & 1;
         ++g;
-        ++jj;
+        plast = ++jj == steps;
         if (plast) {
           ++seq;
           next_item();
         }
       }
-      if (ok && have) ok = close_a() && close_b(gb);
-      if (!ok) {
+      if (ok && g > 0) ok = close_a() && close_b();
+      if (ok && g > 0 && lead) mbar_arrive(bar(B_IEMPTY + (done & 1)));
+      if (!ok && lead) {
         *abort = 1;
         atomicOr(p.err, kErrTimeout);
       }
       // every product of this thread has completed once this arrives
-      mma_commit(bar(B_DRAIN));
+      commit(lead, bar(B_DRAIN));
       mbar_wait(bar(B_DRAIN), 0, nullptr, lim);
     }
     __syncwarp();
-  } else if (warp >= kDeqWarp) {
-    // ------------------------------------------------- codes into f16 tiles
-    const int dw = warp - kDeqWarp, t = tid - 32 * kDeqWarp;     // t: a position of the step
+  }
+  } else if (warp >= kVWarp) {
+    leave_registers<kRegsDeq>();
+    // ------------------------------------------------- V's codes into f16 tiles
+    const int dw = warp - kVWarp, t = 32 * dw + lane;            // t: a position of the step
     bool ok = true, range = false;
     int g = 0;
     int vr[Y];
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim));
-      ok = barrier_and(1, kDeqThreads, ok);
+      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim);
+      ok = barrier_and(BAR_V, kDeqThreads, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
-      const bool two = it.row1 - it.row0 > BM;
-      for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
-        const int st = g % S::kRawStages, kb = g & 1;
-        const uint32_t raw = sbase + S::kRawAt + st * S::kRaw;
-        ok = ok && mbar_wait(bar(B_RAWFULL + st), (uint32_t)(g / S::kRawStages) & 1u, abort, lim);
-        // -- this position's pairs of K and V
-        const bool counts = ok && ((*reinterpret_cast<volatile int*>(&ctl->present[st]) >> (t >> 4)) & 1) &&
-                            BN * s + t <= it.last;
-        const uint32_t pairs = raw + (t >> 4) * Layout<D>::kTileBytes + Layout<D>::pair(t & 15, 0);
-        uint32_t kw[Y], vw[Y];
-        if constexpr (Y == 4) {
-          const uint4 a = ld_shared_v4(pairs + Layout<D>::kKPairs), b = ld_shared_v4(pairs + Layout<D>::kVPairs);
-          kw[0] = a.x, kw[1] = a.y, kw[2] = a.z, kw[3] = a.w;
-          vw[0] = b.x, vw[1] = b.y, vw[2] = b.z, vw[3] = b.w;
-        } else {
+      const Source<D, PREFIX> src(p, it, 32 * dw);
+      uint32_t pairs[Y], code[Y][4];       // of tile i / (Y / 2), groups 2 (i % (Y / 2)) and the next
+      int there;                           // of which tiles
+      auto load = [&](int s, int2 e) {
+        const uint8_t* t0 = src.tile(s, 0, e.x);
+        const uint8_t* t1 = src.tile(s, 1, e.y);
+        there = (t0 != nullptr) | (t1 != nullptr) << 1;
+        load_words<Y>((lane < 16 ? t0 : t1) + Layout<D>::kVPairs + Layout<D>::pair(lane & 15, 0), (there >> (lane >> 4)) & 1, pairs);
 #pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            kw[y] = ld_shared_u32(pairs + Layout<D>::kKPairs + 4 * y);
-            vw[y] = ld_shared_u32(pairs + Layout<D>::kVPairs + 4 * y);
-          }
-        }
-        float kmax = 0.f;
+        for (int i = 0; i < Y; ++i)
+          load_words<4>((i < Y / 2 ? t0 : t1) + Layout<D>::kV + i % (Y / 2) * 512 + lane * 16, (there >> (i / (Y / 2))) & 1, code[i]);
+      };
+      load(it.k1 - 1, src.entries(it.k1 - 1, it.k0));
+      int2 ahead = src.entries(it.k1 - 2, it.k0);
+      for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
+        const int st = g & 1;
+        // -- this position's pairs
+        const bool counts = BN * s + t <= it.last && ((there >> (lane >> 4)) & 1);
+        uint32_t vw[Y];
+#pragma unroll
+        for (int y = 0; y < Y; ++y) vw[y] = pairs[y];
         int bad = 0;
+        int e[Y];                            // exponents of the warp's largest, by group
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
-          if (!counts) kw[y] = vw[y] = 0;
+          if (!counts) vw[y] = 0;
           // the largest magnitude of a group is at one of its ends
-          const float k = fmaxf(fabsf(pair_lo(kw[y])), fabsf(fmaf(15.f, pair_step(kw[y]), pair_lo(kw[y]))));
-          if (k <= 3.402823466e38f) kmax = fmaxf(kmax, k);
           const float a = fabsf(pair_lo(vw[y])), b = fabsf(fmaf(15.f, pair_step(vw[y]), pair_lo(vw[y])));
           const bool fine = a <= 3.402823466e38f && b <= 3.402823466e38f;
           if (!fine) {
@@ -557,152 +632,93 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
             vw[y] = 0;
           }
           const uint32_t top = __reduce_max_sync(FULL, fine ? __float_as_uint(fmaxf(a, b)) : 0u);
-          if (lane == 0) ctl->vmax[dw][y] = top;
+          e[y] = top == 0 ? -1000 : max((int)(top >> 23) - 127, -100);
         }
-        const uint32_t there = __ballot_sync(FULL, counts);
-        if (lane == 0) ctl->mask[kb][dw] = there;
+        const bool any_bad = __any_sync(FULL, bad != 0);
+        if (lane == 0) ctl->any_nan[g & 3][dw] = any_bad;
+        if (any_bad) {
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const uint32_t w = __ballot_sync(FULL, (bad >> y) & 1);
+            if (lane == 0) ctl->vnan[g & 3][y][dw] = w;
+          }
+        }
+        // -- R_y from the item's first step, all four warps'
+        if (s == it.k1 - 1) {
+          if (lane == 0) {
+#pragma unroll
+            for (int y = 0; y < Y; ++y) ctl->vmax[dw][y] = e[y];
+          }
+          ok = barrier_and(BAR_V, kDeqThreads, ok);
+          if (!ok) break;
+          int base = -1000;
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            vr[y] = -1000;
+#pragma unroll
+            for (int w = 0; w < kDeqWarps; ++w) vr[y] = max(vr[y], ctl->vmax[w][y]);
+            base = max(base, vr[y]);
+          }
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            vr[y] = min(base == -1000 ? 0 : vr[y] == -1000 ? base : max(vr[y], base - 48), 110);
+            if (t == 0) ctl->vr[islot][y] = vr[y] - 14;
+          }
+        }
+        int ev = -1000;
+#pragma unroll
+        for (int y = 0; y < Y; ++y)
+          if (e[y] != -1000) ev = max(ev, e[y] - vr[y]);
+        ev = ev == -1000 ? 0 : max(-48, min(48, ev));
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
-          const uint32_t w = __ballot_sync(FULL, (bad >> y) & 1);
-          if (lane == 0) ctl->vnan[kb][y][dw] = w;
+          range = range || e[y] - vr[y] - ev > 0;
+          // largest below 2^15
+          const float up = pow2(14 - vr[y] - ev), vs = pair_step(vw[y]) * up, vl = pair_lo(vw[y]) * up;
+          ctl->vq[y][t] = make_uint2(pack_f16(vs, vs), pack_f16(vl, vl));
         }
-        // The queries' scale goes into the positions' factors: by the softmax warps in
-        // the item's first step (to wait for it here would hold up that step's K,
-        // behind which the item before ends), from here on later.
-        const bool first = s == it.k1 - 1;
-        if (s == it.k1 - 2 && ok)
-          ok = mbar_wait(bar(B_QFULL), (uint32_t)seq & 1u, abort, lim) &&
-               (!two || mbar_wait(bar(B_QFULL + 1), (uint32_t)seq & 1u, abort, lim));
-        ok = barrier_and(1, kDeqThreads, ok);
-        if (!ok) break;
-        // -- scales
-        int ev = -1000;
-        {
-          int top[Y], base = -1000;
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int w = 0; w < kDeqWarps; ++w) v = max(v, ctl->vmax[w][y]);
-            top[y] = v == 0 ? -1000 : max((int)(v >> 23) - 127, -100);
-            base = max(base, top[y]);
-          }
-          if (first) {
-#pragma unroll
-            for (int y = 0; y < Y; ++y) {
-              vr[y] = base == -1000 ? 0 : top[y] == -1000 ? base : max(top[y], base - 48);
-              vr[y] = min(vr[y], 110);
-              if (t == 0) ctl->vr[islot][y] = vr[y] + 1;
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < Y; ++y)
-            if (top[y] != -1000) ev = max(ev, top[y] - vr[y]);
-          if (ev == -1000) ev = 0;
-          ev = max(-48, min(48, ev));
-#pragma unroll
-          for (int y = 0; y < Y; ++y) range = range || top[y] - vr[y] - ev > 14;
-        }
-        {
-          const int e = min(max((int)(__float_as_uint(kmax) >> 23) - 127, -100), 118);
-          const float f = pow2(-(e + 7));
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            const float step = pair_step(kw[y]) * (f * 0x1p24f), lo = pair_lo(kw[y]) * f;
-            ctl->kq[t][y] = make_uint2(pack_f16(step, step), pack_f16(lo, lo));
-            const float fv = pow2(-(vr[y] + ev + 1)), sv = pow2(18 - (vr[y] + ev + 1));
-            const float vs = pair_step(vw[y]) * sv, vl = pair_lo(vw[y]) * fv;
-            ctl->vq[y][t] = make_uint2(pack_f16(vs, vs), pack_f16(vl, vl));
-          }
-          const float back = pow2(e + 7);
-          ctl->cs[kb][0][t] = first ? back : fminf(back * ctl->qs[0], 3.402823466e38f);
-          if (two) ctl->cs[kb][1][t] = first ? back : fminf(back * ctl->qs[1], 3.402823466e38f);
-        }
-        if (t == 0) ctl->ev[kb] = ev;
-        ok = mbar_wait(bar(B_KEMPTY + kb), ((uint32_t)(g >> 1) & 1u) ^ 1u, abort, lim);
-        ok = barrier_and(1, kDeqThreads, ok);
-        if (!ok) break;
-        if (t == 0) {
-          uint32_t any = 0;
-#pragma unroll
-          for (int y = 0; y < Y; ++y)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) any |= ctl->vnan[kb][y][w];
-          ctl->any_nan[kb] = any != 0;
-        }
-        // -- K: a lane a position and a quarter of each group; eight positions a
-        // warp and turn, bit 2 of the position in bit 2 of the lane, so that eight
-        // lanes' stores lie in eight different banks
-        {
-          const uint32_t dst = sbase + S::kK + kb * S::kTileB;
-          const int u = lane & 3, r8 = (lane & 4) | ((lane >> 3) & 3);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = dw * 32 + i * 8 + r8;
-            const uint32_t at = raw + (row >> 4) * Layout<D>::kTileBytes + (row & 15) * (D / 2) + u * (D / 8);
-            uint32_t w[Y];
-            if constexpr (Y == 4) {
-              const uint4 a = ld_shared_v4(at);
-              w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-            } else {
-#pragma unroll
-              for (int y = 0; y < Y; ++y) w[y] = ld_shared_u32(at + 4 * y);
-            }
-#pragma unroll
-            for (int y = 0; y < Y; ++y) {
-              const uint2 k = ctl->kq[row][y];
-              const uint32_t s24 = k.x, s20 = hmul2(k.x, 0x2c002c00u), hi = w[y] >> 8;    // 2^-4
-              st_shared_v4(dst + (y >> 1) * kHalf + row * 128 + ((((y & 1) * 4 + u) ^ (row & 7)) << 4),
-                           hfma2(w[y] & 0x000f000fu, s24, k.y), hfma2(w[y] & 0x00f000f0u, s20, k.y),
-                           hfma2(hi & 0x000f000fu, s24, k.y), hfma2(hi & 0x00f000f0u, s20, k.y));
-            }
-          }
-        }
-        fence_proxy_async_smem();
+        if (lane == 0) ctl->ev[g & 3][dw] = ev;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_KREADY + kb));
-        // -- V: a lane a quarter group of two neighbouring groups, four positions
-        ok = mbar_wait(bar(B_VEMPTY), ((uint32_t)g & 1u) ^ 1u, abort, lim);
-        ok = __all_sync(FULL, ok);
+        if (lane == 0) mbar_arrive(bar(B_VINFO + (g & 3)));
+        // -- a lane a quarter group of two neighbouring groups, four positions; the
+        // codes are in registers before the tile is free
+        ok = __all_sync(FULL, mbar_wait(bar(B_VEMPTY + st), ((uint32_t)(g >> 1) & 1u) ^ 1u, abort, lim));
         if (ok) {
           const int gq = lane >> 2, tq = lane & 3;
+          const uint32_t row0 = sbase + S::kV + st * S::kTileB + (dw * 32 + 2 * tq) * 128;
+          const uint32_t dst[2] = {row0 + ((gq ^ (2 * tq)) << 4), row0 + 128 + ((gq ^ (2 * tq + 1)) << 4)};
+          const uint32_t scales = smem_u32(&ctl->vq[0][dw * 32 + 2 * tq]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tile = dw * 2 + i;
+          for (int i = 0; i < Y; ++i) {
+            const int yy = i % (Y / 2), tile = i / (Y / 2);
 #pragma unroll
-            for (int yy = 0; yy < Y / 2; ++yy) {
-              const uint4 a = ld_shared_v4(raw + tile * Layout<D>::kTileBytes + Layout<D>::kV + yy * 512 + lane * 16);
-              const uint32_t w[2][2] = {{a.x, a.y}, {a.z, a.w}};
+            for (int blk = 0; blk < 2; ++blk) {
+              const uint32_t w0 = code[i][blk], w1 = code[i][2 + blk];
+              const uint32_t at = scales + (2 * yy * BN + tile * 16 + blk * 8) * 8;
+              const uint4 q0 = ld_shared_v4(at), q1 = ld_shared_v4(at + BN * 8);      // step, lo of two positions
 #pragma unroll
-              for (int blk = 0; blk < 2; ++blk) {
-                const int key = tile * 16 + blk * 8 + 2 * tq;
-                const uint4 q0 = ld_shared_v4(smem_u32(&ctl->vq[2 * yy][key]));
-                const uint4 q1 = ld_shared_v4(smem_u32(&ctl->vq[2 * yy + 1][key]));
-#pragma unroll
-                for (int par = 0; par < 2; ++par) {
-                  const uint32_t x0 = __byte_perm(w[0][blk], 0, par ? 0x4342 : 0x4140);
-                  const uint32_t x1 = __byte_perm(w[1][blk], 0, par ? 0x4342 : 0x4140);
-                  const uint32_t s0 = par ? q0.z : q0.x, l0 = par ? q0.w : q0.y;
-                  const uint32_t s1 = par ? q1.z : q1.x, l1 = par ? q1.w : q1.y;
-                  const int row = key + par;
-                  st_shared_v4(sbase + S::kV + yy * kHalf + row * 128 + ((gq ^ (row & 7)) << 4),
-                               hfma2((x0 << 6) & 0x03c003c0u, s0, l0), hfma2((x0 << 2) & 0x03c003c0u, s0, l0),
-                               hfma2((x1 << 6) & 0x03c003c0u, s1, l1), hfma2((x1 << 2) & 0x03c003c0u, s1, l1));
-                }
+              for (int par = 0; par < 2; ++par) {
+                const uint32_t x0 = __byte_perm(w0, 0, par ? 0x4342 : 0x4140);
+                const uint32_t x1 = __byte_perm(w1, 0, par ? 0x4342 : 0x4140);
+                const uint32_t s0 = par ? q0.z : q0.x, l0 = par ? q0.w : q0.y;
+                const uint32_t s1 = par ? q1.z : q1.x, l1 = par ? q1.w : q1.y;
+                st_shared_v4(dst[par] + yy * kHalf + (tile * 16 + blk * 8) * 128,
+                             hfma2(low_codes(x0), s0, l0), hfma2(high_codes(x0), s0, l0),
+                             hfma2(low_codes(x1), s1, l1), hfma2(high_codes(x1), s1, l1));
               }
             }
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(B_VREADY));
-            mbar_arrive(bar(B_RAWEMPTY + st));
-          }
+          if (lane == 0) mbar_arrive(bar(B_VREADY + st));
         }
-        // (a wait that ran out is told to the others at the next barrier)
-        if (!ok && lane == 0) *abort = 1;
+        if (!ok) break;
+        if (s > it.k0) load(s - 1, ahead);
+        ahead = src.entries(s - 2, it.k0);
       }
-      ok = barrier_and(1, kDeqThreads, ok);
+      // (a wait that ran out is told to the others at the next item's first barrier)
+      if (!ok && lane == 0) *abort = 1;
+      ok = barrier_and(BAR_V, kDeqThreads, ok);
       if (!ok) break;
       if (lane == 0) mbar_arrive(bar(B_IEMPTY + islot));
     }
@@ -714,17 +730,118 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       if (range) atomicOr(p.err, kErrRange);
     }
     __syncwarp();
+  } else if (warp >= kKWarp) {
+    leave_registers<kRegsDeq>();
+    // ------------------------------------------------- K's codes into f16 tiles
+    // (a warp takes its own 32 positions apart: nothing to tell the others)
+    const int dw = warp - kKWarp, t = 32 * dw + lane;
+    bool ok = true;
+    int g = 0;
+    for (int seq = 0; ok; ++seq) {
+      const int islot = seq & 1;
+      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim));
+      if (!ok) break;
+      const Item it = read_item(ctl->ring, islot);
+      if (!it.valid) break;
+      const Source<D, PREFIX> src(p, it, 32 * dw);
+      // a lane a position and a quarter of each group; eight positions a turn, bit 2
+      // of the position in bit 2 of the lane, so that eight lanes' stores lie in eight
+      // different banks; two turns a tile
+      const int u = lane & 3, r8 = (lane & 4) | ((lane >> 3) & 3);
+      uint32_t kp[Y], code[4][Y];
+      int there;                           // which tiles
+      auto load = [&](int s, int2 e) {
+        const uint8_t* t0 = src.tile(s, 0, e.x);
+        const uint8_t* t1 = src.tile(s, 1, e.y);
+        there = (t0 != nullptr) | (t1 != nullptr) << 1;
+        // (pages that are needed and not there are told once, by K's warps)
+        const int at = BN * s + 32 * dw;
+        if (lane == 0 && ((t0 == nullptr && at <= it.last) || (t1 == nullptr && at + kTile <= it.last)))
+          atomicOr(p.err, kErrCachePlace);
+        load_words<Y>((lane < 16 ? t0 : t1) + Layout<D>::kKPairs + Layout<D>::pair(lane & 15, 0), (there >> (lane >> 4)) & 1, kp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          load_words<Y>((i < 2 ? t0 : t1) + (i & 1) * 4 * D + r8 * (D / 2) + u * (D / 8), (there >> (i >> 1)) & 1, code[i]);
+      };
+      load(it.k1 - 1, src.entries(it.k1 - 1, it.k0));
+      int2 ahead = src.entries(it.k1 - 2, it.k0);
+      for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
+        const int st = g & 1, ring = g & 3;
+        const bool counts = BN * s + t <= it.last && ((there >> (lane >> 4)) & 1);
+        uint32_t kw[Y];
+#pragma unroll
+        for (int y = 0; y < Y; ++y) kw[y] = kp[y];
+        float top = 0.f;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          if (!counts) kw[y] = 0;
+          const float k = fmaxf(fabsf(pair_lo(kw[y])), fabsf(fmaf(15.f, pair_step(kw[y]), pair_lo(kw[y]))));
+          if (k <= 3.402823466e38f) top = fmaxf(top, k);
+        }
+        // the warp's largest below 2^15
+        const int e = min(max((int)(__reduce_max_sync(FULL, __float_as_uint(top)) >> 23) - 127, -100), 126);
+        const float up = pow2(14 - e);
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+          const float step = pair_step(kw[y]) * up, lo = pair_lo(kw[y]) * up;
+          ctl->kq[t][y] = make_uint2(pack_f16(step, step), pack_f16(lo, lo));
+        }
+        const uint32_t there = __ballot_sync(FULL, counts);
+        ok = __all_sync(FULL, mbar_wait(bar(B_KEMPTY + st), ((uint32_t)(g >> 1) & 1u) ^ 1u, abort, lim));
+        if (!ok) break;
+        if (lane == 0) {
+          ctl->cs[ring][dw] = pow2(e - 14);
+          ctl->mask[ring][dw] = there;
+        }
+        __syncwarp();
+        const uint32_t dst = sbase + S::kK + st * S::kTileB + (dw * 32 + r8) * 128 + ((u ^ r8) << 4);     // of even groups
+        const uint32_t pairs = smem_u32(&ctl->kq[dw * 32 + r8][0]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint2 k[Y];
+#pragma unroll
+          for (int y = 0; y < Y; y += 2) {
+            const uint4 a = ld_shared_v4(pairs + i * 8 * Y * 8 + y * 8);
+            k[y] = make_uint2(a.x, a.y);
+            k[y + 1] = make_uint2(a.z, a.w);
+          }
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const uint32_t w = code[i][y], hi = w >> 8;
+            st_shared_v4((y & 1 ? dst ^ 64u : dst) + (y >> 1) * kHalf + i * 1024,
+                         hfma2(low_codes(w), k[y].x, k[y].y), hfma2(high_codes(w), k[y].x, k[y].y),
+                         hfma2(low_codes(hi), k[y].x, k[y].y), hfma2(high_codes(hi), k[y].x, k[y].y));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_KREADY + ring));
+        if (s > it.k0) load(s - 1, ahead);
+        ahead = src.entries(s - 2, it.k0);
+      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(bar(B_IEMPTY + islot));
+    }
+    if (!ok && lane == 0) {
+      *abort = 1;
+      atomicOr(p.err, kErrTimeout);
+    }
+    __syncwarp();
   } else {
+    take_registers<kRegsSoftmax>();
     // ------------------------------------------------------ softmax, epilogue
-    const int tile = warp >> 2, r = tid & (BM - 1);
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int tile = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_col = tmem + lane_base + tile * BN, o_col = tmem + lane_base + kColO + tile * 128;
+    const int pair = BAR_PAIR + tile * 4 + quarter;
     const float norm = kLog2e * (D == 64 ? 0.125f : 0.08838834764831845f);
     bool ok = true;
     int g = 0, gt = 0, items = 0;        // steps, this tile's steps and items
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim));
+      // (whether a wait ran out is told to all who share a barrier, before any leaves)
+      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim);
+      ok = barrier_and(BAR_TILE + tile, kTileThreads, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
@@ -740,18 +857,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       bool row_ok = row < it.row1, row_bad = false;
       int h = 0, pos = -1;
       int64_t at = 0;
-      float slope = 0.f;
+      float slope = 0.f, qs;                 // qs: what q's power of two leaves of the scores' scale
       if (row_ok) {
         at = row_at<PREFIX, D>(p, it.b, it.kvh, it.pos, row, h, pos);
         slope = p.slope[h];
         row_ok = pos >= 0;
       }
       {
-        uint4 qv[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
+        // (half of the row)
+        uint4 qv[D / 16];
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at) + half * (D / 16);
         uint32_t mx = 0;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
+        for (int c = 0; c < D / 16; ++c) {
           qv[c] = row_ok ? src[c] : make_uint4(0, 0, 0, 0);
           mx = __vmaxu2(mx, qv[c].x & 0x7fff7fffu);
           mx = __vmaxu2(mx, qv[c].y & 0x7fff7fffu);
@@ -761,18 +879,21 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         mx = max(mx & 0xffff0000u, mx << 16);
         row_bad = mx >= (110u + 127u) << 23;             // 2^110, infinities, NaN
         const uint32_t top = __reduce_max_sync(FULL, row_bad ? 0u : mx);
-        if (lane == 0) ctl->qmax[tile][warp & 3] = top;
-        ok = barrier_and(2 + tile, BM, ok);
+        if (lane == 0) ctl->qmax[tile][warp & 7] = top;
+        ctl->pair[tile][half][r] = row_bad ? 1.f : 0.f;
+        ok = barrier_and(BAR_TILE + tile, kTileThreads, ok);
+        row_bad = row_bad || ctl->pair[tile][half ^ 1][r] != 0.f;
         uint32_t all = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) all = max(all, ctl->qmax[tile][w]);
+        for (int w = 0; w < 8; ++w) all = max(all, ctl->qmax[tile][w]);
         const int e = min(max((int)(all >> 23) - 127, -100), 110);
         const float up = row_bad ? 0.f : pow2(14 - e);
-        if (r == 0) ctl->qs[tile] = pow2(e - 14) * norm;
+        qs = pow2(e - 14) * norm;
         const uint32_t dst = sbase + S::kQ + tile * S::kTileB + r * 128;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t w[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+        for (int i = 0; i < D / 16; ++i) {
+          const int c = half * (D / 16) + i;
+          const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
           float v[8];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -787,159 +908,134 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         mbar_arrive(bar(B_QFULL + tile));
       }
       if (!ok) break;
-      uint64_t eslope[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) eslope[e] = f2_pack((float)(2 * e) * slope, (float)(2 * e + 1) * slope);
+      if (!row_ok) {                         // (a row of no one: it sees everything, and is not written)
+        pos = 1 << 30;
+        slope = 0.f;
+      }
+      const uint64_t rise0 = f2_pack(0.f, slope), rise2 = f2_pack(2.f * slope, 2.f * slope),
+                     rise4 = f2_pack(4.f * slope, 4.f * slope);        // of the bias
       float m_ref = -INFINITY, l = 0.f;
       int nan_groups = 0;
       for (int s = it.k1 - 1; s >= it.k0; --s, ++g, ++gt) {
-        const int kb = g & 1, jt = s * BN;
+        const int ring = g & 3, jt = s * BN;
         // (the step's scales, then its scores)
-        ok = mbar_wait(bar(B_KREADY + kb), (uint32_t)(g >> 1) & 1u, abort, lim);
-        if (s == it.k1 - 1) {
-          ctl->cs[kb][tile][r] = fminf(ctl->cs[kb][tile][r] * ctl->qs[tile], 3.402823466e38f);
-          ok = barrier_and(2 + tile, BM, ok);
-        }
-        ok = ok && mbar_wait(bar(B_SFULL + tile), (uint32_t)gt & 1u, abort, lim);
-        ok = __all_sync(FULL, ok);
-        if (!ok) break;
+        ok = __all_sync(FULL, mbar_wait(bar(B_KREADY + ring), (uint32_t)(g >> 2) & 1u, abort, lim) &&
+                                  mbar_wait(bar(B_VINFO + ring), (uint32_t)(g >> 2) & 1u, abort, lim));
+        const uint4 m4 = ld_shared_v4(smem_u32(&ctl->mask[ring][0]));
+        const uint4 c4 = ld_shared_v4(smem_u32(&ctl->cs[ring][0]));
+        const uint4 e4 = ld_shared_v4(smem_u32(&ctl->ev[g & 3][0]));
+        // this thread's keys: two chunks of 32
+        const int j0 = jt + 64 * half;
+        const uint32_t m2[2] = {half ? m4.z : m4.x, half ? m4.w : m4.y};
+        const int e2[2] = {(int)(half ? e4.z : e4.x), (int)(half ? e4.w : e4.y)};
+        const float cs[2] = {fminf(__uint_as_float(half ? c4.z : c4.x) * qs, 3.402823466e38f),
+                             fminf(__uint_as_float(half ? c4.w : c4.y) * qs, 3.402823466e38f)};
+        // whether every row of the warp sees every key
+        const bool full = __all_sync(FULL, pos >= j0 + 63 && (m2[0] & m2[1]) == 0xffffffffu);
+        auto mask = [&](int q) { return upto_mask(pos - j0 - 32 * q) & m2[q]; };
+        ok = __all_sync(FULL, ok && mbar_wait(bar(B_SFULL + tile), (uint32_t)gt & 1u, abort, lim));
         tc_fence_after();
-        const int ev = ctl->ev[kb];
-        const uint32_t cs = smem_u32(&ctl->cs[kb][tile][0]);
-        auto mask = [&](int q) { return row_ok ? upto_mask(pos - jt - 32 * q) & ctl->mask[kb][q] : 0u; };
-        // exponents of a chunk of 32 keys: x + ev - mu, -inf where masked
-        auto exponents = [&](int q, float mu, const uint32_t (&rr)[32], uint32_t vm, float (&x)[32]) {
-          const float off = fmaf((float)(jt + 32 * q - pos), slope, (float)ev - mu);
-          const uint64_t off2 = f2_pack(off, off);
+        // The step's weights, kept in registers until it is known that the reference
+        // they are taken against stands, for both threads of a row: x + ev - mu is at
+        // most kGrowLog2, and the row has one.  Else the reference moves to the step's
+        // maximum, O and l follow, and the weights are taken again (at the start of a
+        // piece, and where scores jump).
+        uint32_t pk[32];
+        float sum, top;
+        float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        auto weigh = [&](auto masked) {
+          top = -INFINITY;
+          sum = 0.f;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const uint4 c4 = ld_shared_v4(cs + 128 * q + 4 * e);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(rr[e]), __uint_as_float(rr[e + 1])),
-                             f2_pack(__uint_as_float(c4.x), __uint_as_float(c4.y)), f2_add(eslope[e >> 1], off2)),
-                      x[e], x[e + 1]);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(rr[e + 2]), __uint_as_float(rr[e + 3])),
-                             f2_pack(__uint_as_float(c4.z), __uint_as_float(c4.w)),
-                             f2_add(eslope[(e >> 1) + 1], off2)),
-                      x[e + 2], x[e + 3]);
-          }
-          if (__any_sync(FULL, vm != 0xffffffffu)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(vm & (1u << e))) x[e] = -INFINITY;
-          }
-        };
-        // The first step of a row finds its maximum first; later ones take their
-        // weights against the maximum as it stands and watch for growth.
-        const bool one_pass = s < it.k1 - 1 && !__any_sync(FULL, row_ok && m_ref == -INFINITY);
-        float m_use = m_ref, alpha = 1.f;
-        bool resc = false;
-        if (!one_pass) {
-          float mt = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t vm = mask(q);
-            if (!__any_sync(FULL, vm != 0u)) continue;
+          for (int q = 0; q < 2; ++q) {
             uint32_t rr[32];
-            tmem_ld32(s_col + q * 32, rr);
+            tmem_ld32(s_col + 64 * half + 32 * q, rr);
+            const float off = fmaf((float)(j0 + 32 * q - pos), slope, (float)e2[q] - mu);
+            const uint64_t cs2 = f2_pack(cs[q], cs[q]);
+            uint64_t b[2];
+            b[0] = f2_add(rise0, f2_pack(off, off));
+            b[1] = f2_add(b[0], rise2);
             tmem_wait_ld();
             float x[32];
-            exponents(q, 0.f, rr, vm, x);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) mt = max3(mt, x[e], x[e + 1]);
-          }
-          const float m_new = fmaxf(m_ref, mt);
-          resc = m_new > m_ref + kRescaleLog2;
-          m_use = resc ? m_new : m_ref;
-          alpha = resc ? ex2(m_ref - m_new) : 1.f;
-        }
-        float mu = m_use == -INFINITY ? 0.f : m_use;
-        if (s < it.k1 - 1 && __any_sync(FULL, resc)) {
-          // (the commit behind these scores proves that P V of the step before is done)
-          const float f = resc ? alpha : 1.f;
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tmem_ld32(o_col + q * 32, o);
-            tmem_wait_ld();
+            for (int e = 0; e < 16; ++e) {
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), cs2, b[e & 1]),
+                        x[2 * e], x[2 * e + 1]);
+              b[e & 1] = f2_add(b[e & 1], rise4);
+            }
+            if constexpr (decltype(masked)::value) {
+              const uint32_t vm = mask(q);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(o_col + q * 32, o);
-          }
-        }
-        uint64_t lsum = f2_pack(0.f, 0.f);
-#pragma unroll 1
-        for (int q = 3; q >= 0; --q) {
-          const uint32_t vm = mask(q);
-          if (!__any_sync(FULL, vm != 0u)) {
-            const uint32_t z[16] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            tmem_st16(s_col + kColP + q * 16, z);
-            continue;
-          }
-          uint32_t rr[32];
-          tmem_ld32(s_col + q * 32, rr);
-          tmem_wait_ld();
-          float x[32];
-          exponents(q, mu, rr, vm, x);
-          if (one_pass) {
-            float c0 = -INFINITY, c1 = -INFINITY;
+              for (int e = 0; e < 32; ++e)
+                if (!(vm & (1u << e))) x[e] = -INFINITY;
+            }
+            float c0 = max3(x[0], x[1], x[2]), c1 = max3(x[3], x[4], x[5]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
+            for (int e = 6; e < 30; e += 4) {
               c0 = max3(c0, x[e], x[e + 1]);
               c1 = max3(c1, x[e + 2], x[e + 3]);
             }
-            const float cm = fmaxf(c0, c1);
-            if (__any_sync(FULL, cm > kGrowLog2)) {
-              // a jump of the scores: O, l and the weights of this step written so
-              // far are scaled to the new maximum
-              const float d = cm > kGrowLog2 ? cm : 0.f, f = ex2(-d);
-              mu += d;
-              if (row_ok) m_use = mu;
+            top = max3(top, c1, max3(c0, x[30], x[31]));
+            uint64_t t[2];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] -= d;
-              l *= f;
-              lsum = f2_mul(lsum, f2_pack(f, f));
-#pragma unroll 1
-              for (int q3 = 0; q3 < D / 32; ++q3) {
-                uint32_t o[32];
-                tmem_ld32(o_col + q3 * 32, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(o_col + q3 * 32, o);
-              }
-#pragma unroll 1
-              for (int q3 = 3; q3 > q; --q3) {
-                uint32_t w[16];
-                tmem_ld16(s_col + kColP + q3 * 16, w);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-                  w[e] = pack_f16(v.x * f, v.y * f);
-                }
-                tmem_st16(s_col + kColP + q3 * 16, w);
-              }
+            for (int e = 0; e < 16; ++e) {
+              const float u = ex2(x[2 * e]), v = ex2(x[2 * e + 1]);
+              t[e & 1] = e < 2 ? f2_pack(u, v) : f2_add(t[e & 1], f2_pack(u, v));
+              pk[16 * q + e] = pack_f16(u, v);
             }
+            float s0, s1;
+            f2_unpack(f2_add(t[0], t[1]), s0, s1);
+            sum = fmaf(s0 + s1, pow2(-e2[q]), sum);
           }
-          uint32_t pk[16];
+        };
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          if (full)
+            weigh(std::false_type{});
+          else
+            weigh(std::true_type{});
+          const bool fresh = m_ref == -INFINITY;
+          const bool grow = pass < 2 && (top > kGrowLog2 || (fresh && top > -INFINITY));
+          // (also: both have read the scores that the weights are written over)
+          tc_fence_before();
+          const bool again = barrier_or(pair, 64, grow || !ok);
+          tc_fence_after();
+          if (!again) break;
+          ctl->pair[tile][half][r] = top;
+          ok = barrier_and(pair, 64, ok);
+          if (!ok) break;
+          top = fmaxf(top, ctl->pair[tile][half ^ 1][r]);
+          // (to no less than the maximum, whatever its own rounding: a second pass is
+          // the last; the bound is for the third that no row needs)
+          const bool move = top > kGrowLog2 || (fresh && top > -INFINITY);
+          const float d = move ? fmaf(fabsf(mu + top), 0x1p-20f, top) : 0.f, f = fresh ? 0.f : ex2(-d);
+          mu += d;
+          if (move) m_ref = mu;
+          l *= f;
+          // (the commit behind these scores proves that P V of the step before is done)
+#pragma unroll 1
+          for (int k = s < it.k1 - 1 ? 0 : D / 32; k < D / 32; ++k) {
+            uint32_t o[16];
+            tmem_ld16(o_col + half * (D / 2) + k * 16, o);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float a = ex2(x[2 * e]), b = ex2(x[2 * e + 1]);
-            lsum = f2_add(lsum, f2_pack(a, b));
-            pk[e] = pack_f16(a, b);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(o_col + half * (D / 2) + k * 16, o);
           }
-          tmem_st16(s_col + kColP + q * 16, pk);
         }
-        float ls0, ls1;
-        f2_unpack(lsum, ls0, ls1);
-        l = fmaf(ls0 + ls1, pow2(-ev), l * alpha);
-        m_ref = m_use;
-        if (ctl->any_nan[kb]) {
-          for (int q = 0; q < 4; ++q) {
+        if (!ok) break;
+        l += sum;
+        tmem_st32(s_col + kColP + 32 * half, pk);
+        const uint4 nan4 = ld_shared_v4(smem_u32(&ctl->any_nan[g & 3][0]));
+        if (nan4.x | nan4.y | nan4.z | nan4.w) {
+          const uint32_t some[2] = {half ? nan4.z : nan4.x, half ? nan4.w : nan4.y};
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (!some[q]) continue;
             const uint32_t vm = mask(q);
 #pragma unroll
             for (int y = 0; y < Y; ++y)
-              if (ctl->vnan[kb][y][q] & vm) nan_groups |= 1 << y;
+              if (ctl->vnan[g & 3][y][2 * half + q] & vm) nan_groups |= 1 << y;
           }
         }
         tmem_wait_st();
@@ -948,10 +1044,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       }
       if (!ok) break;
       // -- the row
-      ok = __all_sync(FULL, mbar_wait(bar(B_ODONE + tile), (uint32_t)items & 1u, abort, lim));
+      ok = mbar_wait(bar(B_ODONE + tile), (uint32_t)items & 1u, abort, lim);
+      // both threads' row sums and groups that are no numbers
+      ctl->pair[tile][half][r] = l;
+      ok = barrier_and(pair, 64, ok);
       if (!ok) break;
       ++items;
       tc_fence_after();
+      l += ctl->pair[tile][half ^ 1][r];
+      barrier_or(pair, 64, false);
+      ctl->pair[tile][half][r] = __int_as_float(nan_groups);
+      barrier_or(pair, 64, false);
+      nan_groups |= __float_as_int(ctl->pair[tile][half ^ 1][r]);
       if (row_bad) l = NAN;
       const bool whole = it.slot < 0;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -961,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
 #pragma unroll
       for (int y = 0; y < Y; ++y) up[y] = (nan_groups >> y) & 1 ? NAN : pow2(ctl->vr[islot][y]) * inv;
 #pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
+      for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) {      // half of the columns
         uint32_t o[32];
         tmem_ld32(o_col + q * 32, o);
         tmem_wait_ld();
@@ -996,7 +1100,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           }
         }
       }
-      if (!whole) {
+      if (!whole && half == 0) {
         part[kItemRows * D + pr] = m_ref == -INFINITY ? kNothing : m_ref;
         part[kItemRows * (D + 1) + pr] = row_ok ? l : 0.f;
       }
