@@ -6,37 +6,42 @@
 //
 // The rows of all query heads of a KV head see the same keys, so an item is 256
 // such rows (two tiles of 128) and the keys up to the last of their positions, in
-// steps of 128.  A step's codes (20 d bytes for 16 positions) are taken apart once
-// for the 256 rows, into f16 tiles in shared memory, and the products run on the
-// tensor cores (tcgen05): S = Q K^T from shared memory, P V with P in tensor
-// memory.  Next to the products' 2048 cycles a step (at 4096 multiply-adds a cycle)
-// stand about 1900 issue slots a scheduler of softmax and of taking codes apart.
+// steps of 128, last step first.  A step's codes (20 d bytes for 16 positions) are
+// taken apart once for the 256 rows, into f16 tiles in shared memory, and the products
+// run on the tensor cores (tcgen05): S = Q K^T from shared memory, P V with P in
+// tensor memory.
 //
 // Numbers.  Codes are exact in f16, so a value lo + step c is rounded once, in one
-// f16 multiply-add: a code in the low bits of an f16 is the subnormal c 2^-24 (or
-// 16 c 2^-24, or 2^6 c 2^-24 behind a shift), and the power of two goes into step.
+// f16 multiply-add (c is taken from the low bits of 1024 + c or 64 + c, exactly).
 // Powers of two keep everything within f16's range:
 //   q  times one per tile of 128 rows, the largest magnitude in [2^14, 2^15);
-//   K  times one per position, largest below 2^-6: undone in the fp32 scores
-//      (cs_j, times q's and log2(e) / sqrt(d));
-//   V  times one per group of 32 values, R_y, by the first step of a piece, and one
-//      per step, ev, by how far any group exceeds that: largest below 2^-6.  2^ev goes
-//      into the step's weights, P = 2^{x + ev - M} with M the running maximum of
-//      x + ev, so that a large value takes precision from others of its own step
-//      alone; the row sum takes P 2^-ev in fp32.
+//   K  times one per 32 positions, likewise: undone in the fp32 scores (with q's, and
+//      log2(e) / sqrt(d));
+//   V  times one per group of 32 values, R_y, by the first step of a piece (undone in
+//      the epilogue), and one per 32 positions, 2^-ev, by how far any group exceeds
+//      that or stays below it: likewise.  2^ev goes into these positions' weights,
+//      P = 2^{x + ev - M} with M near the maximum of x + ev so far, so that a large
+//      value takes precision from others of its own 32 positions alone; the row sum
+//      takes P 2^-ev in fp32.
 // P and V are rounded to f16 (2^-11 of themselves): bf16's 2^-8 would show beside
 // the output's own rounding.  Scores, sums and maxima are fp32.
 //
 // Warps of a CTA (one per SM): 0-7 and 8-15 softmax of the two tiles, two threads a
-// row with 64 of a step's keys each; 16-19 take K's codes apart and 20-23 V's, so
-// that K (two tiles) runs ahead of V (one tile); 24 issues
-// the products, PV_A(g-1) S_A(g) PV_B(g-1) S_B(g), so that the tensor cores work on
-// one tile while the other's scores become weights; 25 lists the items and copies
-// the codes.  Registers are split 80 / 64 / 56.  The flat list (KV head, item,
-// step), each item preceded by kItemCost entries for its beginning and end, is cut
-// into equal shares of the CTAs; items cut by a CTA's edge are joined by a second
-// kernel, in a fixed order.  Every wait is bounded; on expiry the CTA raises the
-// error flag, lets its copies and products drain, frees its tensor memory and exits.
+// row with 64 of a step's keys each; 16-19 take K's codes apart and 20-23 V's, up to
+// two steps ahead; 24 issues the products, PV_A(g-1) S_A(g) PV_B(g-1) S_B(g), so that
+// the tensor cores work on one tile while the other's scores become weights; 25 lists
+// the items.  The flat list (KV head, item, step), each item preceded by kItemCost
+// entries for its beginning and end, is cut into equal shares of the CTAs; items cut
+// by a CTA's edge are joined by a second kernel, in a fixed order.  Every wait is
+// bounded; on expiry the CTA raises the error flag, lets its copies and products
+// drain, frees its tensor memory and exits.
+//
+// What bounds it.  The products of a step take 2048 cycles (4096 multiply-adds a
+// cycle); the kernel takes about 3700.  Neither the tensor cores (55 %) nor the
+// schedulers' issue slots (about 2700 of softmax and of taking codes apart) are full:
+// a tile's steps follow one another through its scores, its softmax and P V, as P
+// stands where its scores stood (S, O of two tiles fill the tensor memory), and the
+// two tiles' chains fill each other's gaps in part.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -60,8 +65,8 @@ constexpr int BM = 128, BN = 128;       // rows of a tile, keys of a step
 constexpr int kItemRows = 2 * BM;
 constexpr int kSoftWarps = 16, kKWarp = 16, kVWarp = 20, kDeqWarps = 4, kMmaWarp = 24, kProdWarp = 25, kWarps = 28;
 constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps, kTileThreads = 256;
-// of 896 threads' 72 at launch: 512 x 80 + 256 x 64 + 128 x 56 = 64512, all of them
-constexpr int kRegsSoftmax = 80, kRegsDeq = 64, kRegsRest = 56;
+// of 896 threads' 72 at launch: 512 x 96 + 256 x 48 + 128 x 24 = 64512, all of them
+constexpr int kRegsSoftmax = 96, kRegsDeq = 48, kRegsRest = 24;
 enum { BAR_V = 1, BAR_TILE = 2, BAR_PAIR = 4 };      // named barriers: V's warps, a tile's, two warps of a row
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
 constexpr int kItemCost = 2;            // steps that beginning and ending an item costs
@@ -82,9 +87,9 @@ struct Sizes {
 };
 
 enum {
-  B_IFULL = 0, B_IEMPTY = 2, B_VEMPTY = 4, B_VREADY = 6, B_VINFO = 8, B_KREADY = 12,
-  B_KEMPTY = 16, B_QFULL = 22, B_SFULL = 24, B_PFULL = 26, B_ODONE = 28,
-  B_DRAIN = 30, NUM_BARS
+  B_IFULL = 0, B_IEMPTY = 2, B_VEMPTY = 4, B_VREADY = 6, B_INFO = 8, B_KREADY = 12,
+  B_KEMPTY = 16, B_QFULL = 18, B_SFULL = 20, B_PFULL = 22, B_ODONE = 24,
+  B_DRAIN = 26, NUM_BARS
 };
 
 // Rows [row0, row1) of a sequence's (or the batch's) rows of one KV head against the
@@ -101,13 +106,11 @@ struct Ctl {
   alignas(16) uint2 kq[BN][Y];          // per position and group: step, lo as f16 pairs
   alignas(16) uint2 vq[Y][BN];
   // K and V run up to two steps ahead of the products, the softmax up to one behind
-  alignas(16) float cs[4][4];           // per step and 32 positions: K's factor, to be undone
-  alignas(16) uint32_t mask[4][4];      // per step: positions that count
+  alignas(16) uint2 kinfo[4][4];        // per step and 32 positions: K's factor, to be undone; positions that count
+  alignas(16) uint2 vinfo[4][4];        // V's exponent beyond R_y; 2^-that, negative where a group is no number
   uint32_t vnan[4][Y][4];               // positions whose group of V is no number
-  alignas(16) int ev[4][4];             // per step and 32 positions: V's exponent beyond R_y
-  alignas(16) int any_nan[4][4];
   int vr[2][Y];                         // per item slot: V's exponents R_y, less 14
-  int vmax[kDeqWarps][Y];
+  int vmax[2][kDeqWarps][Y];
   uint32_t qmax[2][8];
   float pair[2][2][BM];                 // per tile and half: what the two threads of a row tell each other
   int64_t sums[kWarps], found[2];
@@ -143,7 +146,7 @@ __host__ __device__ constexpr int64_t part_floats() { return kItemRows * (D + 2)
 
 __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23); }
 
-// A barrier of `n` threads that tells all of them whether all say ok.
+// A barrier of `n` threads that tells all of them whether any says so, or all do.
 __device__ __forceinline__ bool barrier_or(int id, int n, bool any) {
   int r;
   asm volatile(
@@ -219,6 +222,12 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t low) {
   return (uint64_t)((1024u >> 4) | 1u << 14 | 2u << 29) << 32 | low;
 }
 
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 // Bit e set when key jc + e is at or before position jc + eb.
 __device__ __forceinline__ uint32_t upto_mask(int eb) {
   return eb < 0 ? 0u : eb >= 31 ? 0xffffffffu : (2u << eb) - 1u;
@@ -228,6 +237,7 @@ __device__ __forceinline__ uint32_t upto_mask(int eb) {
 template <int D, bool PREFIX>
 struct Source {
   const uint8_t* head;           // tile 0 of page 0 of the KV head
+  const uint8_t* any;            // of the cache
   const int32_t* table;
   int64_t page_bytes, pages;
   int shift, last, first;        // first: of the warp's positions, within a step
@@ -236,6 +246,7 @@ struct Source {
         last(it.last), first(first) {
     const int64_t tile = Layout<D>::kTileBytes;
     page_bytes = ((int64_t)p.c.H << (shift - 4)) * tile;
+    any = p.c.data;
     head = p.c.data + ((int64_t)it.kvh << (shift - 4)) * tile;
   }
   // the table's entries of step s (-1: none needed)
@@ -248,22 +259,23 @@ struct Source {
     }
     return e;
   }
-  __device__ const uint8_t* tile(int s, int k, int32_t pg) const {
-    if (pg < 0 || pg >= pages) return nullptr;
+  // tile k of the two (an absent one: some tile, whose codes count for nothing)
+  __device__ const uint8_t* tile(int s, int k, int32_t pg, bool& there) const {
+    there = pg >= 0 && pg < pages;
     const int in_page = (BN * s + first + kTile * k) & ((1 << shift) - 1);
-    return head + pg * page_bytes + (in_page >> 4) * Layout<D>::kTileBytes;
+    return there ? head + pg * page_bytes + (in_page >> 4) * Layout<D>::kTileBytes : any;
   }
 };
 
-// N words from global memory, zeros from nowhere.
+// N words from global memory.
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* at, bool there, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[N]) {
   if constexpr (N == 4) {
-    const uint4 a = there ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+    const uint4 a = *reinterpret_cast<const uint4*>(at);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
   } else {
     static_assert(N == 2, "a group of 32 or two");
-    const uint2 a = there ? *reinterpret_cast<const uint2*>(at) : make_uint2(0, 0);
+    const uint2 a = *reinterpret_cast<const uint2*>(at);
     w[0] = a.x, w[1] = a.y;
   }
 }
@@ -340,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     }
     for (int k = 0; k < 4; ++k) {
       mbar_init(bar(B_KREADY + k), kDeqWarps);
-      mbar_init(bar(B_VINFO + k), kDeqWarps);
+      mbar_init(bar(B_INFO + k), 2 * kDeqWarps);
     }
     mbar_init(bar(B_DRAIN), 1);
     ctl->abort = 0;
@@ -590,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     const int dw = warp - kVWarp, t = 32 * dw + lane;            // t: a position of the step
     bool ok = true, range = false;
     int g = 0;
-    int vr[Y];
+    float unit[Y];                       // 2^-R_y
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
       ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim);
@@ -600,42 +612,42 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       if (!it.valid) break;
       const Source<D, PREFIX> src(p, it, 32 * dw);
       uint32_t pairs[Y], code[Y][4];       // of tile i / (Y / 2), groups 2 (i % (Y / 2)) and the next
-      int there;                           // of which tiles
+      bool there;                          // whether this lane's position is
+      const int pair_at = Layout<D>::kVPairs + Layout<D>::pair(lane & 15, 0);
       auto load = [&](int s, int2 e) {
-        const uint8_t* t0 = src.tile(s, 0, e.x);
-        const uint8_t* t1 = src.tile(s, 1, e.y);
-        there = (t0 != nullptr) | (t1 != nullptr) << 1;
-        load_words<Y>((lane < 16 ? t0 : t1) + Layout<D>::kVPairs + Layout<D>::pair(lane & 15, 0), (there >> (lane >> 4)) & 1, pairs);
+        bool h0, h1;
+        const uint8_t *t0 = src.tile(s, 0, e.x, h0), *t1 = src.tile(s, 1, e.y, h1);
+        there = lane < 16 ? h0 : h1;
+        load_words<Y>((lane < 16 ? t0 : t1) + pair_at, pairs);
+        t0 += lane * 16;
+        t1 += lane * 16;
 #pragma unroll
-        for (int i = 0; i < Y; ++i)
-          load_words<4>((i < Y / 2 ? t0 : t1) + Layout<D>::kV + i % (Y / 2) * 512 + lane * 16, (there >> (i / (Y / 2))) & 1, code[i]);
+        for (int i = 0; i < Y; ++i) load_words<4>((i < Y / 2 ? t0 : t1) + Layout<D>::kV + i % (Y / 2) * 512, code[i]);
       };
       load(it.k1 - 1, src.entries(it.k1 - 1, it.k0));
       int2 ahead = src.entries(it.k1 - 2, it.k0);
       for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
         const int st = g & 1;
         // -- this position's pairs
-        const bool counts = BN * s + t <= it.last && ((there >> (lane >> 4)) & 1);
+        const bool counts = BN * s + t <= it.last && there;
         uint32_t vw[Y];
 #pragma unroll
         for (int y = 0; y < Y; ++y) vw[y] = pairs[y];
         int bad = 0;
-        int e[Y];                            // exponents of the warp's largest, by group
+        float top[Y], most = 0.f;            // largest magnitudes: of the groups, of all in units of 2^R_y
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
           if (!counts) vw[y] = 0;
-          // the largest magnitude of a group is at one of its ends
-          const float a = fabsf(pair_lo(vw[y])), b = fabsf(fmaf(15.f, pair_step(vw[y]), pair_lo(vw[y])));
-          const bool fine = a <= 3.402823466e38f && b <= 3.402823466e38f;
-          if (!fine) {
+          // (at one of a group's ends; a NaN of either number is one of hi)
+          const float hi = fmaf(15.f, pair_step(vw[y]), pair_lo(vw[y]));
+          top[y] = fmaxf(fabsf(pair_lo(vw[y])), fabsf(hi));
+          if (!(top[y] <= 3.402823466e38f) || hi != hi) {
             bad |= 1 << y;
             vw[y] = 0;
+            top[y] = 0.f;
           }
-          const uint32_t top = __reduce_max_sync(FULL, fine ? __float_as_uint(fmaxf(a, b)) : 0u);
-          e[y] = top == 0 ? -1000 : max((int)(top >> 23) - 127, -100);
         }
         const bool any_bad = __any_sync(FULL, bad != 0);
-        if (lane == 0) ctl->any_nan[g & 3][dw] = any_bad;
         if (any_bad) {
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
@@ -645,41 +657,43 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         }
         // -- R_y from the item's first step, all four warps'
         if (s == it.k1 - 1) {
-          if (lane == 0) {
 #pragma unroll
-            for (int y = 0; y < Y; ++y) ctl->vmax[dw][y] = e[y];
+          for (int y = 0; y < Y; ++y) {
+            const uint32_t a = __reduce_max_sync(FULL, __float_as_uint(top[y]));
+            if (lane == 0) ctl->vmax[islot][dw][y] = a == 0 ? -1000 : max((int)(a >> 23) - 127, -100);
           }
           ok = barrier_and(BAR_V, kDeqThreads, ok);
           if (!ok) break;
-          int base = -1000;
+          int e[Y], base = -1000;
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
-            vr[y] = -1000;
+            e[y] = -1000;
 #pragma unroll
-            for (int w = 0; w < kDeqWarps; ++w) vr[y] = max(vr[y], ctl->vmax[w][y]);
-            base = max(base, vr[y]);
+            for (int w = 0; w < kDeqWarps; ++w) e[y] = max(e[y], ctl->vmax[islot][w][y]);
+            base = max(base, e[y]);
           }
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
-            vr[y] = min(base == -1000 ? 0 : vr[y] == -1000 ? base : max(vr[y], base - 48), 110);
-            if (t == 0) ctl->vr[islot][y] = vr[y] - 14;
+            e[y] = min(base == -1000 ? 0 : e[y] == -1000 ? base : max(e[y], base - 48), 110);
+            if (t == 0) ctl->vr[islot][y] = e[y] - 14;
+            unit[y] = pow2(-e[y]);
           }
         }
-        int ev = -1000;
 #pragma unroll
-        for (int y = 0; y < Y; ++y)
-          if (e[y] != -1000) ev = max(ev, e[y] - vr[y]);
-        ev = ev == -1000 ? 0 : max(-48, min(48, ev));
+        for (int y = 0; y < Y; ++y) most = fmaxf(most, top[y] * unit[y]);
+        const uint32_t all = __reduce_max_sync(FULL, __float_as_uint(most));
+        const int e = (int)(all >> 23) - 127, ev = all == 0 ? 0 : max(-48, min(48, e));
+        range = range || e > 48;
+        const float down = pow2(-ev), to = down * 0x1p14f;       // largest below 2^15
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
-          range = range || e[y] - vr[y] - ev > 0;
-          // largest below 2^15
-          const float up = pow2(14 - vr[y] - ev), vs = pair_step(vw[y]) * up, vl = pair_lo(vw[y]) * up;
+          const float up = unit[y] * to, vs = pair_step(vw[y]) * up, vl = pair_lo(vw[y]) * up;
           ctl->vq[y][t] = make_uint2(pack_f16(vs, vs), pack_f16(vl, vl));
         }
-        if (lane == 0) ctl->ev[g & 3][dw] = ev;
+        if (lane == 0)
+          ctl->vinfo[g & 3][dw] = make_uint2(__float_as_uint((float)ev), __float_as_uint(any_bad ? -down : down));
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_VINFO + (g & 3)));
+        if (lane == 0) mbar_arrive(bar(B_INFO + (g & 3)));
         // -- a lane a quarter group of two neighbouring groups, four positions; the
         // codes are in registers before the tile is free
         ok = __all_sync(FULL, mbar_wait(bar(B_VEMPTY + st), ((uint32_t)(g >> 1) & 1u) ^ 1u, abort, lim));
@@ -688,25 +702,35 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           const uint32_t row0 = sbase + S::kV + st * S::kTileB + (dw * 32 + 2 * tq) * 128;
           const uint32_t dst[2] = {row0 + ((gq ^ (2 * tq)) << 4), row0 + 128 + ((gq ^ (2 * tq + 1)) << 4)};
           const uint32_t scales = smem_u32(&ctl->vq[0][dw * 32 + 2 * tq]);
+          // (step, lo of two positions and two groups, read one turn ahead: these
+          // accesses stay in the order written)
+          uint4 q0 = ld_shared_v4(scales), q1 = ld_shared_v4(scales + BN * 8);
 #pragma unroll
-          for (int i = 0; i < Y; ++i) {
-            const int yy = i % (Y / 2), tile = i / (Y / 2);
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-              const uint32_t w0 = code[i][blk], w1 = code[i][2 + blk];
-              const uint32_t at = scales + (2 * yy * BN + tile * 16 + blk * 8) * 8;
-              const uint4 q0 = ld_shared_v4(at), q1 = ld_shared_v4(at + BN * 8);      // step, lo of two positions
-#pragma unroll
-              for (int par = 0; par < 2; ++par) {
-                const uint32_t x0 = __byte_perm(w0, 0, par ? 0x4342 : 0x4140);
-                const uint32_t x1 = __byte_perm(w1, 0, par ? 0x4342 : 0x4140);
-                const uint32_t s0 = par ? q0.z : q0.x, l0 = par ? q0.w : q0.y;
-                const uint32_t s1 = par ? q1.z : q1.x, l1 = par ? q1.w : q1.y;
-                st_shared_v4(dst[par] + yy * kHalf + (tile * 16 + blk * 8) * 128,
-                             hfma2(low_codes(x0), s0, l0), hfma2(high_codes(x0), s0, l0),
-                             hfma2(low_codes(x1), s1, l1), hfma2(high_codes(x1), s1, l1));
-              }
+          for (int n = 0; n < 2 * Y; ++n) {
+            const int blk = n & 1, i = n >> 1, yy = i % (Y / 2), tile = i / (Y / 2);
+            const uint32_t w0 = code[i][blk], w1 = code[i][2 + blk];
+            const uint4 a = q0, b = q1;
+            if (n + 1 < 2 * Y) {
+              const int i1 = (n + 1) >> 1;
+              const uint32_t at = scales + (2 * (i1 % (Y / 2)) * BN + i1 / (Y / 2) * 16 + ((n + 1) & 1) * 8) * 8;
+              q0 = ld_shared_v4(at);
+              q1 = ld_shared_v4(at + BN * 8);
             }
+            uint32_t v[2][4];
+#pragma unroll
+            for (int par = 0; par < 2; ++par) {
+              const uint32_t x0 = __byte_perm(w0, 0, par ? 0x4342 : 0x4140);
+              const uint32_t x1 = __byte_perm(w1, 0, par ? 0x4342 : 0x4140);
+              const uint32_t s0 = par ? a.z : a.x, l0 = par ? a.w : a.y;
+              const uint32_t s1 = par ? b.z : b.x, l1 = par ? b.w : b.y;
+              v[par][0] = hfma2(low_codes(x0), s0, l0);
+              v[par][1] = hfma2(high_codes(x0), s0, l0);
+              v[par][2] = hfma2(low_codes(x1), s1, l1);
+              v[par][3] = hfma2(high_codes(x1), s1, l1);
+            }
+#pragma unroll
+            for (int par = 0; par < 2; ++par)
+              st_shared_v4(dst[par] + yy * kHalf + (tile * 16 + blk * 8) * 128, v[par][0], v[par][1], v[par][2], v[par][3]);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -749,25 +773,25 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       // different banks; two turns a tile
       const int u = lane & 3, r8 = (lane & 4) | ((lane >> 3) & 3);
       uint32_t kp[Y], code[4][Y];
-      int there;                           // which tiles
+      bool there;                          // whether this lane's position is
+      const int pair_at = Layout<D>::kKPairs + Layout<D>::pair(lane & 15, 0);
       auto load = [&](int s, int2 e) {
-        const uint8_t* t0 = src.tile(s, 0, e.x);
-        const uint8_t* t1 = src.tile(s, 1, e.y);
-        there = (t0 != nullptr) | (t1 != nullptr) << 1;
+        bool h0, h1;
+        const uint8_t *t0 = src.tile(s, 0, e.x, h0), *t1 = src.tile(s, 1, e.y, h1);
+        there = lane < 16 ? h0 : h1;
         // (pages that are needed and not there are told once, by K's warps)
-        const int at = BN * s + 32 * dw;
-        if (lane == 0 && ((t0 == nullptr && at <= it.last) || (t1 == nullptr && at + kTile <= it.last)))
-          atomicOr(p.err, kErrCachePlace);
-        load_words<Y>((lane < 16 ? t0 : t1) + Layout<D>::kKPairs + Layout<D>::pair(lane & 15, 0), (there >> (lane >> 4)) & 1, kp);
+        if (!there && BN * s + t <= it.last) atomicOr(p.err, kErrCachePlace);
+        load_words<Y>((lane < 16 ? t0 : t1) + pair_at, kp);
+        t0 += r8 * (D / 2) + u * (D / 8);
+        t1 += r8 * (D / 2) + u * (D / 8);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          load_words<Y>((i < 2 ? t0 : t1) + (i & 1) * 4 * D + r8 * (D / 2) + u * (D / 8), (there >> (i >> 1)) & 1, code[i]);
+        for (int i = 0; i < 4; ++i) load_words<Y>((i < 2 ? t0 : t1) + (i & 1) * 4 * D, code[i]);
       };
       load(it.k1 - 1, src.entries(it.k1 - 1, it.k0));
       int2 ahead = src.entries(it.k1 - 2, it.k0);
       for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
         const int st = g & 1, ring = g & 3;
-        const bool counts = BN * s + t <= it.last && ((there >> (lane >> 4)) & 1);
+        const bool counts = BN * s + t <= it.last && there;
         uint32_t kw[Y];
 #pragma unroll
         for (int y = 0; y < Y; ++y) kw[y] = kp[y];
@@ -786,36 +810,38 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           const float step = pair_step(kw[y]) * up, lo = pair_lo(kw[y]) * up;
           ctl->kq[t][y] = make_uint2(pack_f16(step, step), pack_f16(lo, lo));
         }
-        const uint32_t there = __ballot_sync(FULL, counts);
+        const uint32_t positions = __ballot_sync(FULL, counts);
         ok = __all_sync(FULL, mbar_wait(bar(B_KEMPTY + st), ((uint32_t)(g >> 1) & 1u) ^ 1u, abort, lim));
         if (!ok) break;
-        if (lane == 0) {
-          ctl->cs[ring][dw] = pow2(e - 14);
-          ctl->mask[ring][dw] = there;
-        }
+        if (lane == 0) ctl->kinfo[ring][dw] = make_uint2(__float_as_uint(pow2(e - 14)), positions);
         __syncwarp();
         const uint32_t dst = sbase + S::kK + st * S::kTileB + (dw * 32 + r8) * 128 + ((u ^ r8) << 4);     // of even groups
         const uint32_t pairs = smem_u32(&ctl->kq[dw * 32 + r8][0]);
+        // (step, lo of two groups, read one turn ahead)
+        uint4 next = ld_shared_v4(pairs);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint2 k[Y];
+        for (int n = 0; n < 4 * (Y / 2); ++n) {
+          const int i = n / (Y / 2), yy = n % (Y / 2);
+          const uint4 k = next;
+          if (n + 1 < 4 * (Y / 2)) next = ld_shared_v4(pairs + (n + 1) / (Y / 2) * 8 * Y * 8 + (n + 1) % (Y / 2) * 16);
+          uint32_t v[2][4];
 #pragma unroll
-          for (int y = 0; y < Y; y += 2) {
-            const uint4 a = ld_shared_v4(pairs + i * 8 * Y * 8 + y * 8);
-            k[y] = make_uint2(a.x, a.y);
-            k[y + 1] = make_uint2(a.z, a.w);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t w = code[i][2 * yy + y], hi = w >> 8, s = y ? k.z : k.x, l = y ? k.w : k.y;
+            v[y][0] = hfma2(low_codes(w), s, l);
+            v[y][1] = hfma2(high_codes(w), s, l);
+            v[y][2] = hfma2(low_codes(hi), s, l);
+            v[y][3] = hfma2(high_codes(hi), s, l);
           }
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            const uint32_t w = code[i][y], hi = w >> 8;
-            st_shared_v4((y & 1 ? dst ^ 64u : dst) + (y >> 1) * kHalf + i * 1024,
-                         hfma2(low_codes(w), k[y].x, k[y].y), hfma2(high_codes(w), k[y].x, k[y].y),
-                         hfma2(low_codes(hi), k[y].x, k[y].y), hfma2(high_codes(hi), k[y].x, k[y].y));
-          }
+          st_shared_v4(dst + yy * kHalf + i * 1024, v[0][0], v[0][1], v[0][2], v[0][3]);
+          st_shared_v4((dst ^ 64u) + yy * kHalf + i * 1024, v[1][0], v[1][1], v[1][2], v[1][3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_KREADY + ring));
+        if (lane == 0) {
+          mbar_arrive(bar(B_KREADY + ring));
+          mbar_arrive(bar(B_INFO + ring));
+        }
         if (s > it.k0) load(s - 1, ahead);
         ahead = src.entries(s - 2, it.k0);
       }
@@ -832,11 +858,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     // ------------------------------------------------------ softmax, epilogue
     const int tile = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + tile * BN, o_col = tmem + lane_base + kColO + tile * 128;
+    const uint32_t s_col = tmem + lane_base + tile * BN + 64 * half, p_col = tmem + lane_base + tile * BN + kColP + 32 * half;
+    const uint32_t o_col = tmem + lane_base + kColO + tile * 128;
     const int pair = BAR_PAIR + tile * 4 + quarter;
     const float norm = kLog2e * (D == 64 ? 0.125f : 0.08838834764831845f);
     bool ok = true;
-    int g = 0, gt = 0, items = 0;        // steps, this tile's steps and items
+    uint32_t g = 0, gt = 0, items = 0;   // steps, this tile's steps and items
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
       // (whether a wait ran out is told to all who share a barrier, before any leaves)
@@ -845,12 +872,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
-      const int steps = it.k1 - it.k0, row = it.row0 + tile * BM + r;
+      const int row = it.row0 + tile * BM + r;
       if (tile == 1 && it.row1 - it.row0 <= BM) {
         mbar_arrive(bar(B_QFULL + 1));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + islot));
-        g += steps;
+        g += it.k1 - it.k0;
         continue;
       }
       // -- the row's query
@@ -912,102 +939,108 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         pos = 1 << 30;
         slope = 0.f;
       }
-      const uint64_t rise0 = f2_pack(0.f, slope), rise2 = f2_pack(2.f * slope, 2.f * slope),
-                     rise4 = f2_pack(4.f * slope, 4.f * slope);        // of the bias
+      const int pos_min = __reduce_min_sync(FULL, pos);
+      const uint64_t rise2 = f2_pack(2.f * slope, 2.f * slope), rise4 = f2_pack(4.f * slope, 4.f * slope);      // of the bias
       float m_ref = -INFINITY, l = 0.f;
       int nan_groups = 0;
       for (int s = it.k1 - 1; s >= it.k0; --s, ++g, ++gt) {
-        const int ring = g & 3, jt = s * BN;
-        // (the step's scales, then its scores)
-        ok = __all_sync(FULL, mbar_wait(bar(B_KREADY + ring), (uint32_t)(g >> 2) & 1u, abort, lim) &&
-                                  mbar_wait(bar(B_VINFO + ring), (uint32_t)(g >> 2) & 1u, abort, lim));
-        const uint4 m4 = ld_shared_v4(smem_u32(&ctl->mask[ring][0]));
-        const uint4 c4 = ld_shared_v4(smem_u32(&ctl->cs[ring][0]));
-        const uint4 e4 = ld_shared_v4(smem_u32(&ctl->ev[g & 3][0]));
-        // this thread's keys: two chunks of 32
-        const int j0 = jt + 64 * half;
-        const uint32_t m2[2] = {half ? m4.z : m4.x, half ? m4.w : m4.y};
-        const int e2[2] = {(int)(half ? e4.z : e4.x), (int)(half ? e4.w : e4.y)};
-        const float cs[2] = {fminf(__uint_as_float(half ? c4.z : c4.x) * qs, 3.402823466e38f),
-                             fminf(__uint_as_float(half ? c4.w : c4.y) * qs, 3.402823466e38f)};
-        // whether every row of the warp sees every key
-        const bool full = __all_sync(FULL, pos >= j0 + 63 && (m2[0] & m2[1]) == 0xffffffffu);
-        auto mask = [&](int q) { return upto_mask(pos - j0 - 32 * q) & m2[q]; };
-        ok = __all_sync(FULL, ok && mbar_wait(bar(B_SFULL + tile), (uint32_t)gt & 1u, abort, lim));
+        const int j0 = s * BN + 64 * half;               // this thread's keys: 64 from here
+        const uint32_t kinfo = smem_u32(&ctl->kinfo[g & 3][2 * half]), vinfo = smem_u32(&ctl->vinfo[g & 3][2 * half]);
+        // (The scores first: a tile that was left out of the item before runs ahead of
+        // the others, and only behind its own scores is the step's phase of the scales'
+        // barrier the next to complete.)
+        ok = mbar_wait(bar(B_SFULL + tile), gt & 1u, abort, lim) &&
+             mbar_wait(bar(B_INFO + (g & 3)), (g >> 2) & 1u, abort, lim);
+        ok = __all_sync(FULL, ok);
         tc_fence_after();
+        float mu = m_ref == -INFINITY ? 0.f : m_ref, sum;
         // The step's weights, kept in registers until it is known that the reference
-        // they are taken against stands, for both threads of a row: x + ev - mu is at
-        // most kGrowLog2, and the row has one.  Else the reference moves to the step's
-        // maximum, O and l follow, and the weights are taken again (at the start of a
-        // piece, and where scores jump).
-        uint32_t pk[32];
-        float sum, top;
-        float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        auto weigh = [&](auto masked) {
-          top = -INFINITY;
-          sum = 0.f;
+        // they are taken against stands, for both threads of a row: they are below 2^15,
+        // and the row has one.  Else the reference moves to the step's maximum, O and l
+        // follow, and the weights are taken again (at the start of a piece, and where
+        // scores jump).
+        uint32_t pk[32], most;
+        int some_nan = 0;
+        // exponents of sixteen keys, x + ev - mu, -inf where masked
+        auto exponents = [&](int c, const uint32_t (&rr)[16], uint2 kq, float ev, float (&x)[16]) {
+          const int jc = j0 + 16 * c;
+          const float cs = fminf(__uint_as_float(kq.x) * qs, 3.402823466e38f);
+          const uint64_t cs2 = f2_pack(cs, cs);
+          const float off = fmaf((float)(jc - pos), slope, ev - mu);
+          uint64_t b[2];
+          b[0] = f2_pack(off, off + slope);
+          b[1] = f2_add(b[0], rise2);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t rr[32];
-            tmem_ld32(s_col + 64 * half + 32 * q, rr);
-            const float off = fmaf((float)(j0 + 32 * q - pos), slope, (float)e2[q] - mu);
-            const uint64_t cs2 = f2_pack(cs[q], cs[q]);
-            uint64_t b[2];
-            b[0] = f2_add(rise0, f2_pack(off, off));
-            b[1] = f2_add(b[0], rise2);
-            tmem_wait_ld();
-            float x[32];
+          for (int e = 0; e < 8; ++e) {
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), cs2, b[e & 1]),
+                      x[2 * e], x[2 * e + 1]);
+            b[e & 1] = f2_add(b[e & 1], rise4);
+          }
+          if (pos_min < jc + 15 || kq.y != 0xffffffffu) {
+            const uint32_t vm = upto_mask(pos - jc) & (kq.y >> (16 * (c & 1)));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(rr[2 * e]), __uint_as_float(rr[2 * e + 1])), cs2, b[e & 1]),
-                        x[2 * e], x[2 * e + 1]);
-              b[e & 1] = f2_add(b[e & 1], rise4);
-            }
-            if constexpr (decltype(masked)::value) {
-              const uint32_t vm = mask(q);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(vm & (1u << e))) x[e] = -INFINITY;
-            }
-            float c0 = max3(x[0], x[1], x[2]), c1 = max3(x[3], x[4], x[5]);
-#pragma unroll
-            for (int e = 6; e < 30; e += 4) {
-              c0 = max3(c0, x[e], x[e + 1]);
-              c1 = max3(c1, x[e + 2], x[e + 3]);
-            }
-            top = max3(top, c1, max3(c0, x[30], x[31]));
-            uint64_t t[2];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float u = ex2(x[2 * e]), v = ex2(x[2 * e + 1]);
-              t[e & 1] = e < 2 ? f2_pack(u, v) : f2_add(t[e & 1], f2_pack(u, v));
-              pk[16 * q + e] = pack_f16(u, v);
-            }
-            float s0, s1;
-            f2_unpack(f2_add(t[0], t[1]), s0, s1);
-            sum = fmaf(s0 + s1, pow2(-e2[q]), sum);
+            for (int e = 0; e < 16; ++e)
+              if (!(vm & (1u << e))) x[e] = -INFINITY;
           }
         };
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
-          if (full)
-            weigh(std::false_type{});
-          else
-            weigh(std::true_type{});
+          most = 0;
+          sum = 0.f;
+          uint32_t ra[16], rb[16];
+          tmem_ld16(s_col, ra);
+          uint2 kq, vq;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t(&rr)[16] = c & 1 ? rb : ra;
+            if (!(c & 1)) {
+              kq = ld_shared_v2(kinfo + 4 * c);
+              vq = ld_shared_v2(vinfo + 4 * c);
+              some_nan |= (int)vq.y;
+            }
+            tmem_wait_ld();
+            if (c < 3) tmem_ld16(s_col + 16 * (c + 1), c & 1 ? ra : rb);
+            float x[16];
+            exponents(c, rr, kq, __uint_as_float(vq.x), x);
+            uint64_t t[2];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float u = ex2(x[2 * e]), v = ex2(x[2 * e + 1]);
+              t[e & 1] = e < 2 ? f2_pack(u, v) : f2_add(t[e & 1], f2_pack(u, v));
+              pk[8 * c + e] = pack_f16(u, v);
+              if (e & 1) most = __vimax3_u16x2(most, pk[8 * c + e - 1], pk[8 * c + e]);
+            }
+            float s0, s1;
+            f2_unpack(f2_add(t[0], t[1]), s0, s1);
+            sum = fmaf(s0 + s1, fabsf(__uint_as_float(vq.y)), sum);
+          }
           const bool fresh = m_ref == -INFINITY;
-          const bool grow = pass < 2 && (top > kGrowLog2 || (fresh && top > -INFINITY));
+          // does a weight reach 2^15 (or is it no number)?  or has the row no reference?
+          const bool grow = fresh || ((most + 0x08000800u) & 0x80008000u) != 0;
           // (also: both have read the scores that the weights are written over)
           tc_fence_before();
           const bool again = barrier_or(pair, 64, grow || !ok);
           tc_fence_after();
           if (!again) break;
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t rr[16];
+            float x[16];
+            tmem_ld16(s_col + 16 * c, rr);
+            const uint2 kc = ld_shared_v2(kinfo + 8 * (c >> 1)), vc = ld_shared_v2(vinfo + 8 * (c >> 1));
+            tmem_wait_ld();
+            exponents(c, rr, kc, __uint_as_float(vc.x), x);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) top = max3(top, x[e], x[e + 1]);
+          }
           ctl->pair[tile][half][r] = top;
           ok = barrier_and(pair, 64, ok);
           if (!ok) break;
           top = fmaxf(top, ctl->pair[tile][half ^ 1][r]);
           // (to no less than the maximum, whatever its own rounding: a second pass is
           // the last; the bound is for the third that no row needs)
-          const bool move = top > kGrowLog2 || (fresh && top > -INFINITY);
+          const bool move = pass < 2 && (top > kGrowLog2 || (fresh && top > -INFINITY));
           const float d = move ? fmaf(fabsf(mu + top), 0x1p-20f, top) : 0.f, f = fresh ? 0.f : ex2(-d);
           mu += d;
           if (move) m_ref = mu;
@@ -1022,29 +1055,28 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tmem_st16(o_col + half * (D / 2) + k * 16, o);
           }
+          if (!barrier_or(pair, 64, move)) break;          // (a row that sees nothing yet)
         }
         if (!ok) break;
-        l += sum;
-        tmem_st32(s_col + kColP + 32 * half, pk);
-        const uint4 nan4 = ld_shared_v4(smem_u32(&ctl->any_nan[g & 3][0]));
-        if (nan4.x | nan4.y | nan4.z | nan4.w) {
-          const uint32_t some[2] = {half ? nan4.z : nan4.x, half ? nan4.w : nan4.y};
-#pragma unroll
+        tmem_st32(p_col, pk);
+        if (some_nan < 0) {
+          // (before the arrival: behind it the products may hand the step's slot on)
+#pragma unroll 1
           for (int q = 0; q < 2; ++q) {
-            if (!some[q]) continue;
-            const uint32_t vm = mask(q);
-#pragma unroll
+            if ((int)ld_shared_u32(vinfo + 8 * q + 4) >= 0) continue;      // a group of V that is no number
+            const uint32_t vm = upto_mask(pos - j0 - 32 * q) & ld_shared_u32(kinfo + 8 * q + 4);
             for (int y = 0; y < Y; ++y)
               if (ctl->vnan[g & 3][y][2 * half + q] & vm) nan_groups |= 1 << y;
           }
         }
+        l += sum;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(B_PFULL + tile));
       }
       if (!ok) break;
       // -- the row
-      ok = mbar_wait(bar(B_ODONE + tile), (uint32_t)items & 1u, abort, lim);
+      ok = mbar_wait(bar(B_ODONE + tile), items & 1u, abort, lim);
       // both threads' row sums and groups that are no numbers
       ctl->pair[tile][half][r] = l;
       ok = barrier_and(pair, 64, ok);
