@@ -1422,18 +1422,37 @@ plsh_status q4_slopes(const plsh_tensor* q, const double* sigma_h, float* slopes
   return PLSH_OK;
 }
 
-// Whether a chunk's rows, or the rows behind a prefix, go to the tensor cores.
-bool q4_many(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix) {
-  const int64_t rows = q->H / c.H * (prefix ? q->B : q->n);      // of a KV head
-  return q->dtype == PLSH_BF16 && rows >= 32;
+// Whether a chunk's rows, or the rows behind a prefix, may go to the tensor cores, and
+// whether they do.  The decode step's kernel reads a KV head's keys once for a token
+// and eight query heads, a pass; the tensor cores' takes about as long for up to 128
+// rows as the other for seven passes: 64 sequences of 4096 positions and 8 KV heads, 6
+// passes 306 us and 320, 8 passes 404 and 320, 32 passes 1548 and 331.  It takes longer
+// to begin (22 us and 10 at the least, behind a prefix 29 and 10), so there has to be
+// work: passes x KV heads x positions.  A chunk's positions are on the device, its
+// table's length bounds them: with 8 KV heads and 1024 positions, 0.26 M (one sequence,
+// 32 passes) take 20.5 us and 24.6, 0.79 M (8 sequences, 12 passes) 37 and 31; one KV
+// head with 131072, 0.79 M 33 and 39, 2.1 M 66 and 39.  Behind a prefix: 1.05 M (16384
+// positions, 8 KV heads, 8 passes) 33 and 41, 4.2 M (65536) 104 and 90, 64 passes of
+// 8192 positions 111 and 51.
+bool q4_may_be_many(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix, double* passes) {
+  *passes = (double)((q->H / c.H + 7) / 8) * (double)(prefix ? q->B : q->n);
+  return q->dtype == PLSH_BF16 && *passes >= 7;
+}
+bool q4_many(const plsh_tensor* q, const plsh::Q4Cache& c, int64_t prefix_pages) {
+  const bool prefix = prefix_pages > 0;
+  double passes;
+  if (!q4_may_be_many(q, c, prefix, &passes)) return false;
+  const double positions = (double)(prefix ? prefix_pages : c.B * (int64_t)c.max_pages) * (1 << c.page_shift);
+  return passes * c.H * positions >= (prefix ? 3 << 19 : 1 << 19);
 }
 
 int64_t q4_rows_work_bytes(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix, int num_sms) {
-  int64_t bytes = plsh::q4_decode_work_bytes(c.d, num_sms);
-  if (q4_many(q, c, prefix))
-    bytes = plsh::q4_many_work_bytes(c.d, num_sms) +
-            (prefix ? plsh::q4_own_work_bytes(c.d, num_sms, c.B, c.H, (int)(q->H / c.H)) : 0);
-  return bytes;
+  const int64_t bytes = plsh::q4_decode_work_bytes(c.d, num_sms);
+  double passes;
+  if (prefix ? !q4_may_be_many(q, c, true, &passes) : !q4_many(q, c, 0)) return bytes;
+  // (a prefix's: whatever its length)
+  const int64_t own = prefix ? plsh::q4_own_work_bytes(c.d, num_sms, c.B, c.H, (int)(q->H / c.H)) : 0;
+  return std::max(bytes, own + plsh::q4_many_work_bytes(c.d, num_sms));
 }
 
 // The exact step of several rows a sequence (prefix NULL) or behind a shared prefix.
@@ -1477,7 +1496,7 @@ plsh_status q4_rows_step(const plsh_tensor* q, const plsh_q4_cache* cache, const
   a.prefix = prefix;
   a.prefix_pages = (int)prefix_pages;
   a.wait_ns = ctx->wait_ns;
-  if (!q4_many(q, a.c, prefix != nullptr))
+  if (!q4_many(q, a.c, prefix_pages))
     PLSH_TRY_CUDA(plsh::launch_q4_decode(a, cs), "4-bit decode launch");
   else if (prefix == nullptr)
     PLSH_TRY_CUDA(plsh::launch_q4_chunk(a, cs), "4-bit chunk launch");

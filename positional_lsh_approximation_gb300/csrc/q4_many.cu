@@ -70,7 +70,6 @@ constexpr int kRegsSoftmax = 96, kRegsDeq = 48, kRegsRest = 24;
 enum { BAR_V = 1, BAR_TILE = 2, BAR_PAIR = 4 };      // named barriers: V's warps, a tile's, two warps of a row
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
 constexpr int kItemCost = 2;            // steps that beginning and ending an item costs
-constexpr int kMinSteps = 4;            // steps of a CTA at least
 constexpr uint32_t kTmemCols = 512;     // S_A | S_B | O_A | O_B; P over S
 constexpr uint32_t kColP = 64, kColO = 256;
 constexpr float kGrowLog2 = 15.f;       // largest weight 2^15: above, the reference moves
@@ -395,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       total += ctl->sums[w];
     }
     const int64_t all = total * p.c.H, fair = (all + gridDim.x - 1) / gridDim.x;
-    per = fair < kMinSteps + kItemCost ? kMinSteps + kItemCost : fair;
+    per = fair < kItemCost + 1 ? kItemCost + 1 : fair;
     begin = blockIdx.x * per;
     end = min(all, begin + per);
     if (begin < end) {
@@ -1122,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
               }
             }
           }
-        } else {
+        } else if (row_ok) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             const float u = c & 1 ? u1 : u0;
@@ -1155,8 +1154,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------- joining
-// A lane a row, a warp every eighth of the columns' quads; 32 rows of an item a CTA.
-constexpr int kJoinThreads = 256;
+// A lane a row of 32 rows of an item.  Few pieces: a warp every eighth of the columns'
+// quads (4 columns), all pieces.  kSplit pieces or more: a warp every eighth of the
+// pieces of two quads, the warps' sums joined in their order; a CTA for each two quads.
+// So an item that all CTAs work on (one sequence behind a long context) is read by many
+// threads, with loads of several pieces in flight: one CTA for all columns and pieces
+// took longer than the attention itself (131072 keys, one KV head: 100 of 121 us).
+constexpr int kJoinThreads = 256, kSplit = 8;
 
 template <int D>
 __device__ __forceinline__ void store4(__nv_bfloat16* o, int quad, const float4& a) {
@@ -1165,45 +1169,148 @@ __device__ __forceinline__ void store4(__nv_bfloat16* o, int quad, const float4&
   *reinterpret_cast<uint2*>(o + 32 * y + 4 * g) = make_uint2(pack_bf16(a.x, a.z), pack_bf16(a.y, a.w));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) q4_many_join_kernel(const __grid_constant__ ManyParams p) {
-  grid_dep_wait();
-  const int4 end = p.ends[blockIdx.x];
-  if (end.x < 0) return;
-  const int entries = p.c.B * p.tiles, kvh = end.x / entries, e = end.x - kvh * entries, b = e / p.tiles;
-  int pos0, rows, last;
-  item_steps<false>(p, b, e - b * p.tiles, pos0, rows, last);
-  const int pr = blockIdx.y * 32 + (threadIdx.x & 31), row = kItemRows * (e - b * p.tiles) + pr;
-  if (row >= rows) return;
-  int h, pos;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + row_at<false, D>(p, b, kvh, pos0, row, h, pos);
-  const int n = (int)blockIdx.x - end.y + 1;
-  auto piece = [&](int k) { return p.part + (int64_t)(k == 0 ? end.z : 2 * (end.y + k)) * part_floats<D>(); };
-  float mm = kNothing, sum = 0.f;
-  for (int k = 0; k < n; ++k) mm = fmaxf(mm, piece(k)[kItemRows * D + pr]);
-  float4 acc[D / 32];
+// A row's sum of pieces: maximum, sum of weights, columns of NQ quads.
+template <int NQ>
+struct RowSum {
+  float m = kNothing, l = 0.f;
+  float4 o[NQ];
+  __device__ RowSum() {
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < n; ++k) {
+    for (int c = 0; c < NQ; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ void scale(float f) {
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < NQ; ++c) o[c].x *= f, o[c].y *= f, o[c].z *= f, o[c].w *= f;
+  }
+  __device__ static void add(float4& a, float f, const float4& v) {
+    a.x = fmaf(f, v.x, a.x);
+    a.y = fmaf(f, v.y, a.y);
+    a.z = fmaf(f, v.z, a.z);
+    a.w = fmaf(f, v.w, a.w);
+  }
+};
+
+// Pieces first, first + every, .. of n; quads q0, q0 + stride, ..
+template <int D, int NQ, typename Piece>
+__device__ __forceinline__ void add_pieces(RowSum<NQ>& a, Piece piece, int first, int every, int n, int pr, int q0,
+                                           int stride) {
+  float mm = kNothing;
+#pragma unroll 8
+  for (int k = first; k < n; k += every) mm = fmaxf(mm, piece(k)[kItemRows * D + pr]);
+  a.m = mm;
+#pragma unroll 4
+  for (int k = first; k < n; k += every) {
     const float* pt = piece(k);
-    const float l = pt[kItemRows * (D + 1) + pr];
-    if (l == 0.f) continue;
-    const float f = ex2(pt[kItemRows * D + pr] - mm);
-    sum = fmaf(f, l, sum);
+    const float l = pt[kItemRows * (D + 1) + pr], f = l == 0.f ? 0.f : ex2(pt[kItemRows * D + pr] - mm);
+    a.l = fmaf(f, l, a.l);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const float4 v = reinterpret_cast<const float4*>(pt)[((threadIdx.x >> 5) + 8 * c) * kItemRows + pr];
-      acc[c].x = fmaf(f, v.x, acc[c].x);
-      acc[c].y = fmaf(f, v.y, acc[c].y);
-      acc[c].z = fmaf(f, v.z, acc[c].z);
-      acc[c].w = fmaf(f, v.w, acc[c].w);
+    for (int c = 0; c < NQ; ++c) {
+      float4 v = reinterpret_cast<const float4*>(pt)[(q0 + stride * c) * kItemRows + pr];
+      if (l == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);       // (not written, or of nothing)
+      RowSum<NQ>::add(a.o[c], f, v);
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+}
+
+// The warps' sums of a row (two quads), and the row.
+template <int D>
+__device__ __forceinline__ void join_warps(const RowSum<2>& a, __nv_bfloat16* o, int q0, bool there) {
+  __shared__ float ms[8][32], ls[8][32];
+  __shared__ float4 os[2][8][32];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();                       // (another unit's were read)
+  ms[w][lane] = a.m;
+  ls[w][lane] = a.l;
+  os[0][w][lane] = a.o[0];
+  os[1][w][lane] = a.o[1];
+  __syncthreads();
+  if (w >= 2 || !there) return;
+  float mm = kNothing, sum = 0.f;
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    store4<D>(o, (threadIdx.x >> 5) + 8 * c,
-              make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv));
+  for (int i = 0; i < 8; ++i) mm = fmaxf(mm, ms[i][lane]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float l = ls[i][lane], f = l == 0.f ? 0.f : ex2(ms[i][lane] - mm);
+    sum = fmaf(f, l, sum);
+    RowSum<2>::add(acc, f, os[w][i][lane]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  store4<D>(o, q0 + w, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+}
+
+template <int D, int NQ>
+__device__ __forceinline__ void store_row(const RowSum<NQ>& a, __nv_bfloat16* o, int q0, int stride) {
+  const float inv = a.l == 0.f ? 0.f : 1.f / a.l;
+#pragma unroll
+  for (int c = 0; c < NQ; ++c)
+    store4<D>(o, q0 + stride * c, make_float4(a.o[c].x * inv, a.o[c].y * inv, a.o[c].z * inv, a.o[c].w * inv));
+}
+
+// Units (32 rows of an item, and two quads where its pieces are many) of all the items
+// that end in a CTA, a CTA every gridDim.x-th.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) q4_many_join_kernel(const __grid_constant__ ManyParams p, int ctas) {
+  grid_dep_wait();
+  __shared__ int starts[kJoinThreads + 1], sums[kJoinThreads / 32];
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, entries = p.c.B * p.tiles;
+  auto rows_of = [&](const int4& end, int& e, int& kvh, int& b, int& pos) {      // rows of the item
+    kvh = end.x / entries;
+    e = end.x - kvh * entries;
+    b = e / p.tiles;
+    int rows, last;
+    item_steps<false>(p, b, e - b * p.tiles, pos, rows, last);
+    return min(rows - kItemRows * (e - b * p.tiles), kItemRows);
+  };
+  int units = 0;
+  if (tid < ctas) {
+    const int4 end = p.ends[tid];
+    if (end.x >= 0) {
+      int e, kvh, b, pos;
+      units = ((rows_of(end, e, kvh, b, pos) + 31) / 32) * (tid - end.y + 1 >= kSplit ? D / 8 : 1);
+    }
+  }
+  int upto = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 31) sums[w] = upto;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) upto += sums[i];
+  starts[tid + 1] = upto;
+  if (tid == 0) starts[0] = 0;
+  __syncthreads();
+  const int total = starts[kJoinThreads];
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int t = 0;                             // starts[t] <= u < starts[t + 1]
+#pragma unroll
+    for (int o = kJoinThreads / 2; o > 0; o >>= 1)
+      if (starts[t + o] <= u) t += o;
+    const int4 end = p.ends[t];
+    const int n = t - end.y + 1;
+    int e, kvh, b, pos0;
+    const int rows = rows_of(end, e, kvh, b, pos0);
+    const bool split = n >= kSplit;
+    const int blk = split ? (u - starts[t]) / (D / 8) : u - starts[t], pr = 32 * blk + lane;
+    const bool there = pr < rows;
+    int h, pos;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) +
+                       row_at<false, D>(p, b, kvh, pos0, kItemRows * (e - b * p.tiles) + min(pr, rows - 1), h, pos);
+    auto piece = [&](int k) { return p.part + (int64_t)(k == 0 ? end.z : 2 * (end.y + k)) * part_floats<D>(); };
+    if (split) {
+      const int q0 = 2 * (u - starts[t] - blk * (D / 8));
+      RowSum<2> a;
+      if (there) add_pieces<D>(a, piece, w, 8, n, pr, q0, 1);
+      join_warps<D>(a, o, q0, there);
+    } else if (there) {
+      RowSum<D / 32> a;
+      add_pieces<D>(a, piece, 0, 1, n, pr, w, 8);
+      store_row<D>(a, o, w, 8);
+    }
+  }
 }
 
 // A decode step's rows: the prefix's pieces and those of the sequences' own keys.
@@ -1214,14 +1321,15 @@ struct PrefixJoin {
   int chunks, per_chunk;
 };
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kJoinThreads)
 q4_prefix_join_kernel(const __grid_constant__ ManyParams p, const __grid_constant__ PrefixJoin j) {
   grid_dep_wait();
-  constexpr int kOwn = 8 * (D + 2);
-  const int kvh = blockIdx.x / p.tiles, t = blockIdx.x - kvh * p.tiles;
-  const int pr = blockIdx.y * 32 + (threadIdx.x & 31), row = kItemRows * t + pr;
-  if (row >= p.c.B * p.G) return;
+  constexpr int kOwn = 8 * (D + 2), NQ = SPLIT ? 2 : D / 32;
+  const int kvh = blockIdx.x / p.tiles, t = blockIdx.x - kvh * p.tiles, w = threadIdx.x >> 5;
+  const int pr = blockIdx.y * 32 + (threadIdx.x & 31), rows = p.c.B * p.G, row = min(kItemRows * t + pr, rows - 1);
+  const bool there = kItemRows * t + pr < rows;
+  if (kItemRows * t + (int)blockIdx.y * 32 >= rows) return;
   int h, pos;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + row_at<true, D>(p, 0, kvh, 0, row, h, pos);
   // the item's entries [base, base + cost): its pieces' CTAs
@@ -1229,51 +1337,32 @@ q4_prefix_join_kernel(const __grid_constant__ ManyParams p, const __grid_constan
   const int i0 = (int)((base + kItemCost) / j.per), i1 = (int)((base + cost - 1) / j.per);
   const int slot0 = base <= i0 * j.per ? 2 * i0 : 2 * i0 + 1, n = i1 - i0 + 1;
   auto piece = [&](int k) { return p.part + (int64_t)(k == 0 ? slot0 : 2 * (i0 + k)) * part_floats<D>(); };
-  const int b = row / p.G, hh = row - b * p.G, ch = hh / j.per_chunk, hc = hh - ch * j.per_chunk;
-  const int4 own = j.rows[((int64_t)b * p.c.H + kvh) * j.chunks + ch];
-  auto own_piece = [&](int k) { return j.own + (int64_t)(k == 0 ? own.x : own.y + 2 * (k - 1)) * kOwn; };
-  float mm = kNothing, sum = 0.f;
-  for (int k = 0; k < n; ++k) mm = fmaxf(mm, piece(k)[kItemRows * D + pr]);
-  for (int k = 0; k < own.z; ++k) mm = fmaxf(mm, own_piece(k)[8 * D + hc]);
-  float4 acc[D / 32];
+  const int q0 = SPLIT ? 2 * blockIdx.z : w, stride = SPLIT ? 1 : 8;
+  RowSum<NQ> a;
+  if (there) {
+    add_pieces<D>(a, piece, SPLIT ? w : 0, SPLIT ? 8 : 1, n, pr, q0, stride);
+    const int b = row / p.G, hh = row - b * p.G, ch = hh / j.per_chunk, hc = hh - ch * j.per_chunk;
+    const int4 own = j.rows[((int64_t)b * p.c.H + kvh) * j.chunks + ch];
+    for (int k = SPLIT ? w : 0; k < own.z; k += SPLIT ? 8 : 1) {
+      const float* pt = j.own + (int64_t)(k == 0 ? own.x : own.y + 2 * (k - 1)) * kOwn;
+      const float l = pt[8 * D + 8 + hc], m = pt[8 * D + hc], mm = fmaxf(a.m, m);
+      if (l == 0.f) continue;
+      a.scale(a.l == 0.f ? 0.f : ex2(a.m - mm));
+      a.m = mm;
+      const float f = ex2(m - mm);
+      a.l = fmaf(f, l, a.l);
 #pragma unroll
-  for (int c = 0; c < D / 32; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < n; ++k) {
-    const float* pt = piece(k);
-    const float l = pt[kItemRows * (D + 1) + pr];
-    if (l == 0.f) continue;
-    const float f = ex2(pt[kItemRows * D + pr] - mm);
-    sum = fmaf(f, l, sum);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const float4 v = reinterpret_cast<const float4*>(pt)[((threadIdx.x >> 5) + 8 * c) * kItemRows + pr];
-      acc[c].x = fmaf(f, v.x, acc[c].x);
-      acc[c].y = fmaf(f, v.y, acc[c].y);
-      acc[c].z = fmaf(f, v.z, acc[c].z);
-      acc[c].w = fmaf(f, v.w, acc[c].w);
+      for (int c = 0; c < NQ; ++c) {
+        const int quad = q0 + stride * c, x = quad >> 1;
+        const float4 v = *reinterpret_cast<const float4*>(pt + hc * D + 32 * (2 * (x >> 3) + (quad & 1)) + 4 * (x & 7));
+        RowSum<NQ>::add(a.o[c], f, make_float4(v.x, v.z, v.y, v.w));
+      }
     }
   }
-  for (int k = 0; k < own.z; ++k) {
-    const float* pt = own_piece(k);
-    const float l = pt[8 * D + 8 + hc];
-    if (l == 0.f) continue;
-    const float f = ex2(pt[8 * D + hc] - mm);
-    sum = fmaf(f, l, sum);
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      const int quad = (threadIdx.x >> 5) + 8 * c, x = quad >> 1;
-      const float4 v = *reinterpret_cast<const float4*>(pt + hc * D + 32 * (2 * (x >> 3) + (quad & 1)) + 4 * (x & 7));
-      acc[c].x = fmaf(f, v.x, acc[c].x);
-      acc[c].y = fmaf(f, v.z, acc[c].y);
-      acc[c].z = fmaf(f, v.y, acc[c].z);
-      acc[c].w = fmaf(f, v.w, acc[c].w);
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    store4<D>(o, (threadIdx.x >> 5) + 8 * c,
-              make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv));
+  if constexpr (SPLIT)
+    join_warps<D>(a, o, q0, there);
+  else if (there)
+    store_row<D>(a, o, q0, stride);
 }
 
 template <int D>
@@ -1306,9 +1395,10 @@ cudaError_t launch_chunk(const Q4DecodeArgs& a, cudaStream_t st) {
   p.tiles = (int)(((int64_t)p.m * p.G + kItemRows - 1) / kItemRows);
   auto kern = q4_many_kernel<D, false>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)smem_bytes<D>());
-  if (e == cudaSuccess) e = launch_dependent(kern, dim3(a.num_sms), kThreads, smem_bytes<D>(), st, p);
+  const int ctas = std::min(a.num_sms, kJoinThreads);
+  if (e == cudaSuccess) e = launch_dependent(kern, dim3(ctas), kThreads, smem_bytes<D>(), st, p);
   if (e == cudaSuccess)
-    e = launch_dependent(q4_many_join_kernel<D>, dim3(a.num_sms, kItemRows / 32), kJoinThreads, 0, st, p);
+    e = launch_dependent(q4_many_join_kernel<D>, dim3(4 * a.num_sms), kJoinThreads, 0, st, p, ctas);
   return e;
 }
 
@@ -1324,7 +1414,7 @@ cudaError_t launch_prefix(const Q4DecodeArgs& a, cudaStream_t st) {
   // (as the kernel finds them)
   j.total = (int64_t)p.tiles * ((p.keys + BN - 1) / BN + kItemCost);
   const int64_t all = j.total * a.c.H;
-  j.per = std::max<int64_t>((all + a.num_sms - 1) / a.num_sms, kMinSteps + kItemCost);
+  j.per = std::max<int64_t>((all + a.num_sms - 1) / a.num_sms, kItemCost + 1);
   // the sequences' own keys, then the prefix's, then both together
   Q4DecodeArgs b = a;
   uint8_t* w = static_cast<uint8_t*>(a.work);
@@ -1335,8 +1425,13 @@ cudaError_t launch_prefix(const Q4DecodeArgs& a, cudaStream_t st) {
   auto kern = q4_many_kernel<D, true>;
   if (e == cudaSuccess) e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)smem_bytes<D>());
   if (e == cudaSuccess) e = launch_dependent(kern, dim3(a.num_sms), kThreads, smem_bytes<D>(), st, p);
+  // (pieces of an item: as many as its entries touch CTAs, or one less)
+  const int64_t pieces = (j.total / p.tiles + j.per - 1) / j.per;
   if (e == cudaSuccess)
-    e = launch_dependent(q4_prefix_join_kernel<D>, dim3(a.c.H * p.tiles, kItemRows / 32), kJoinThreads, 0, st, p, j);
+    e = pieces >= kSplit ? launch_dependent(q4_prefix_join_kernel<D, true>, dim3(a.c.H * p.tiles, kItemRows / 32, D / 8),
+                                            kJoinThreads, 0, st, p, j)
+                         : launch_dependent(q4_prefix_join_kernel<D, false>, dim3(a.c.H * p.tiles, kItemRows / 32),
+                                            kJoinThreads, 0, st, p, j);
   return e;
 }
 

@@ -48,11 +48,18 @@ def bound(q, K, V, o, dtype, G):
 
 
 class Rows(Setup):
-    def __init__(self, B, Hq, H, d, page, n, dtype, m, **kw):
+    def __init__(self, B, Hq, H, d, page, n, dtype, m, wide=True, **kw):
         super().__init__(B, Hq, H, d, page, n, dtype, **kw)
         g = torch.Generator("cuda").manual_seed(99)
         self.m = m
         self.q = torch.randn(B, Hq, m, d, device="cuda", generator=g).to(DT[dtype])
+        passes = m * -(-(Hq // H) // 8)
+        if wide and dtype == "bf16" and passes >= 7:
+            # a table long enough for the tensor cores to be taken (its pages again and again)
+            per = self.table.shape[1]
+            long = max(per, -(-2 ** 19 // (B * H * passes * page)))
+            self.table = np.tile(self.table, (1, -(-long // per)))[:, :long].copy()
+            self.cache = plsh.Q4Cache(self.cache.data, torch.from_numpy(self.table).cuda(), H, d, page)
 
     def want(self, b, p, i, sigma, drop=None):
         data = self.host()
@@ -110,10 +117,11 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
-def test_chunk_matches_the_oracle(case):
+def test_chunk_matches_the_oracle(case, wide):
     *shape, pos, lens = case
-    s = Rows(*shape, seed=shape[5])
+    s = Rows(*shape, wide=wide, seed=shape[5])
     sigma = alibi_sigmas(s.Hq)
     out = torch.full_like(s.q, 7.0)
     got = plsh.alibi_exact_chunk_q4(s.q, s.cache, sigma, i32(pos), None if lens is None else i32(lens), out=out)
@@ -253,10 +261,22 @@ def test_a_large_key_or_value_that_weighs_nothing(which, factor):
 
 
 def test_values_past_the_range_are_reported():
+    """Of one piece (how many steps lie in one follows from the batch): reported, or
+    the pieces' ranges hold them and the result is right."""
     s = Rows(1, 4, 1, 128, 64, 400, "bf16", 16, seed=9)
     s.v[:, :, 100] *= 1e25                           # against the newest step's
     plsh.q4_cache_write(s.cache, s.k, s.v, i32([0]))
-    plsh.alibi_exact_chunk_q4(s.q, s.cache, np.full(4, 50.0), i32([384]))
+    sigma = np.full(4, 50.0)
+    got = plsh.alibi_exact_chunk_q4(s.q, s.cache, sigma, i32([384]))
+    try:
+        plsh.stream_status()
+        s.check_rows(got, [384], None, sigma)
+    except plsh.PlshError as e:
+        assert e.status == plsh.PLSH_ERR_RANGE
+    s = Rows(300, 4, 1, 128, 64, 400, "bf16", 16, seed=9)      # a CTA has several steps of a sequence
+    s.v[:, :, 100] *= 1e25
+    plsh.q4_cache_write(s.cache, s.k, s.v, i32([0] * 300))
+    plsh.alibi_exact_chunk_q4(s.q, s.cache, sigma, i32([384] * 300))
     with pytest.raises(plsh.PlshError) as e:
         plsh.stream_status()
     assert e.value.status == plsh.PLSH_ERR_RANGE
@@ -284,10 +304,11 @@ def test_places_out_of_range_are_reported(dtype, m):
         with pytest.raises(plsh.PlshError) as err:
             plsh.stream_status()
         assert err.value.status == plsh.PLSH_ERR_INVALID
-    good = [64 - m, 5, 0]
+    cap = 16 * s.table.shape[1]
+    good = [cap - m, 5, 0]
     want = plsh.alibi_exact_chunk_q4(s.q, s.cache, sigma, i32(good))
     plsh.stream_status()
-    got = plsh.alibi_exact_chunk_q4(s.q, s.cache, sigma, i32([64 - m + 2, 2 ** 31 - 1, 0]))
+    got = plsh.alibi_exact_chunk_q4(s.q, s.cache, sigma, i32([cap - m + 2, 2 ** 31 - 1, 0]))
     failed()
     assert (got[0, :, m - 2:] == 0).all() and (got[0, :, :m - 2] != 0).any() and (got[1] == 0).all()
     assert torch.equal(got[2], want[2])
@@ -366,8 +387,16 @@ PREFIXES = [
     (70, 3, 1, 128, 16, 13, 33, "bf16", [207 + (5 * b) % 34 for b in range(70)]),     # a step that ends inside
     (17, 20, 4, 128, 128, 4, 200, "bf16", [511 + (31 * b) % 201 for b in range(17)]),
     (12, 17, 1, 64, 64, 2, 64, "bf16", [127 + (11 * b) % 65 for b in range(12)]),     # three chunks of heads
+    (300, 2, 1, 64, 64, 6, 3, "bf16", [384 + b % 3 for b in range(300)]),
+    # the tensor cores'
+    (64, 4, 1, 128, 64, 390, 70, "bf16", [24960 + (17 * b) % 70 for b in range(64)]),
+    (96, 8, 2, 64, 32, 260, 40, "bf16", [-1 if b % 7 == 3 else (131 * b) % 8360 for b in range(96)]),     # some within
+    (128, 3, 1, 128, 16, 773, 33, "bf16", [12367 + (5 * b) % 34 for b in range(128)]),      # a step that ends inside
+    (50, 20, 4, 128, 128, 62, 200, "bf16", [7935 + (31 * b) % 201 for b in range(50)]),
+    (40, 17, 1, 64, 64, 205, 64, "bf16", [13119 + (11 * b) % 65 for b in range(40)]),       # three chunks of heads
+    (16, 32, 8, 128, 256, 48, 600, "bf16", [12288 + (97 * b) % 600 for b in range(16)]),
+    (300, 2, 1, 64, 64, 82, 3, "bf16", [5248 + b % 3 for b in range(300)]),                 # more rows than an item
     (16, 32, 8, 128, 256, 16, 600, "bf16", [4096 + (97 * b) % 600 for b in range(16)]),
-    (300, 2, 1, 64, 64, 6, 3, "bf16", [384 + b % 3 for b in range(300)]),             # more rows than an item
     (3, 8, 2, 128, 64, 3, 70, "bf16", [200, -1, 30]),
     (5, 3, 1, 64, 16, 9, 33, "f32", [144, 143, 176, -1, 0]),
     (34, 8, 1, 128, 64, 2, 10, "f32", [128 + b % 10 for b in range(34)]),
@@ -404,12 +433,19 @@ class Shared:
     def check(self, got, pos, sigma, drop=None):
         data, got = self.host(), got.double().cpu().numpy()[:, :, 0]
         err = size = 0.0
+        P = self.P
+        shared = q4.read_sequence(data, self.prefix, self.page, self.d, P)
         for b in range(self.B):
             if pos[b] < 0:
                 assert (got[b] == 0).all()
                 continue
+            if self.B * P > 10 ** 5 and b % 9 not in (0, 4) and b < self.B - 2:
+                continue
             n = pos[b] + 1
-            K, V = q4.read_sequence(data, self.table[b], self.page, self.d, n)
+            K, V = (x[:, :n] for x in shared)
+            if n > P:
+                mine = q4.read_sequence(data, self.table[b, P // self.page:], self.page, self.d, n - P)
+                K, V = (np.concatenate([x, y], 1) for x, y in zip(shared, mine))
             w = q4.log_weights_exact(sigma, pos[b], n)
             if drop is not None:
                 w[:, drop] = -np.inf
@@ -443,10 +479,10 @@ def test_prefix_decode_matches_the_oracle(case):
     plsh.stream_status()
 
 
-@pytest.mark.parametrize("dtype,B", [("bf16", 40), ("bf16", 3), ("f32", 4)])
-def test_prefix_places_out_of_range_are_reported(dtype, B):
-    s = Shared(B, 4, 2, 128, 16, 12, 40, dtype, seed=B)
-    sigma, pos = np.full(4, 100.0), [192 + (7 * b) % 40 for b in range(B)]
+@pytest.mark.parametrize("dtype,B,shared", [("bf16", 96, 520), ("bf16", 40, 12), ("bf16", 3, 12), ("f32", 4, 12)])
+def test_prefix_places_out_of_range_are_reported(dtype, B, shared):
+    s = Shared(B, 4, 2, 128, 16, shared, 40, dtype, seed=B)
+    sigma, pos = np.full(4, s.P / 2), [s.P + (7 * b) % 40 for b in range(B)]
 
     def failed():
         with pytest.raises(plsh.PlshError) as err:
@@ -462,9 +498,10 @@ def test_prefix_places_out_of_range_are_reported(dtype, B):
     s.check(got, pos, sigma, drop=slice(48, 64))
 
 
-def test_prefix_nan_and_queries_that_are_no_numbers():
-    s = Shared(40, 4, 1, 128, 64, 3, 60, "bf16", seed=4)
-    sigma, pos = np.full(4, 60.0), [192 + b for b in range(40)]
+@pytest.mark.parametrize("B,shared", [(64, 390), (40, 3)])
+def test_prefix_nan_and_queries_that_are_no_numbers(B, shared):
+    s = Shared(B, 4, 1, 128, 64, shared, 64, "bf16", seed=4)
+    sigma, pos = np.full(4, 60.0), [s.P + b for b in range(B)]
     pos[7] = 100                                     # does not see position 150
     want = plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sigma, i32(pos), s.d_prefix)
     s.q[5, 1, 0, 3] = float("inf")
@@ -475,7 +512,7 @@ def test_prefix_nan_and_queries_that_are_no_numbers():
     plsh.q4_cache_write(plsh.Q4Cache(s.cache.data, i32(s.prefix[None]), 1, 128, 64), k, v, i32([150]))
     got = plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sigma, i32(pos), s.d_prefix)
     assert torch.equal(got[7], want[7])
-    others = [b for b in range(40) if b not in (5, 7)]
+    others = [b for b in range(B) if b not in (5, 7)]
     assert torch.isnan(got[others][..., 96:]).all() and torch.isfinite(got[others][..., :96]).all()
 
 
@@ -485,7 +522,7 @@ def test_a_server_s_loop_of_prompts_and_tokens():
     H, Hq, d, page, B = 2, 8, 128, 16, 6
     pages, cap = 80, 12
     pool = i32(np.concatenate([[pages], np.random.default_rng(0).permutation(pages)]))
-    held, table = i32([0]), i32(np.full((1, cap), -1))
+    held, table = i32([0]), i32(np.full((1, 512), -1))
     data = torch.randint(0, 256, (pages, H, 1, 20 * d), dtype=torch.uint8, device="cuda")
     one = plsh.Q4Cache(data, table, H, d, page)
     sigma = alibi_sigmas(Hq)
