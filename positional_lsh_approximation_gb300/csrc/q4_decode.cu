@@ -120,10 +120,17 @@ struct Slopes {
 //   kStep    one row a sequence, every key up to its position;
 //   kRows    m rows a sequence (q, o [B, Hq, m, d]), row i at pos[b] + i, each a
 //            row of the flat list by itself;
+//   kPacked  the same where a KV head has at most four query heads: as many of a
+//            sequence's rows as the eight columns hold (`tokens`) are one row of the
+//            flat list, column i G + h for head h of the i-th of them, and the keys'
+//            codes are taken apart once for all of them (64 sequences of 4096
+//            positions, 32/8 heads, 4 tokens: 211 -> 142 us; as a matter of kRows
+//            with one row of eight heads the columns' positions cost 7 %);
 //   kShared  as kStep, the first pages being a prefix's that all sequences share;
 //   kOwn     as kStep, only the keys behind that prefix; rows are left as pieces,
 //            which a kernel elsewhere joins with the prefix's part.
-enum Form { kStep, kRows, kShared, kOwn };
+enum Form { kStep, kRows, kPacked, kShared, kOwn };
+constexpr bool of_rows(int form) { return form == kRows || form == kPacked; }
 
 struct DecodeParams {
   Q4Cache c;
@@ -139,8 +146,9 @@ struct DecodeParams {
   int4* ends;                       // exact: per CTA {row, first CTA, first piece} of a row that ends in it
   float* part;                      // pieces: o [8][D], m [8], l [8]
   int* err;
-  int m;                            // kRows: rows of a sequence
-  const int32_t* len;               // kRows: [B] rows that count, or null
+  int m;                            // rows of a sequence
+  int tokens, each;                 // of them that one row of the list holds, at most; rows of the list
+  const int32_t* len;               // [B] rows that count, or null
   const int32_t* prefix;            // kShared: the prefix's pages
   int prefix_pages;
   int first;                        // kOwn: the prefix's positions
@@ -297,22 +305,28 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&o)[4])
 }
 
 // What a team of warps attends over: blocks [t0, t1) of 32 positions (two tiles) of
-// sequence b, KV head kvh, for the query heads h0 .. h0 + heads - 1.
+// sequence b, KV head kvh, for the query heads h0 .. h0 + heads - 1 (kPacked: `heads`
+// columns, of several rows).
 struct Piece {
   int b, kvh, h0, heads, pos, t0, t1;
   int first;         // first position any of the heads sees
-  int i;             // kRows: row of the sequence
+  int i, tokens;     // first row of the sequence, and rows (the last at pos)
 };
 
-// Element of head h of the row in q and o, and elements from a head to the next.
-template <int FORM, int D>
-__device__ __forceinline__ int64_t head_at(const DecodeParams& p, const Piece& pc, int h) {
-  const int64_t bh = (int64_t)pc.b * p.Hq + h;
-  return (FORM == kRows ? bh * p.m + pc.i : bh) * D;
+// Head of column c among the piece's, and how many rows before the last it is.
+template <int FORM>
+__device__ __forceinline__ int head_of(const DecodeParams& p, const Piece& pc, int c) {
+  return FORM == kPacked ? c % p.G : c;
 }
+template <int FORM>
+__device__ __forceinline__ int back_of(const DecodeParams& p, const Piece& pc, int c) {
+  return FORM == kPacked ? pc.tokens - 1 - c / p.G : 0;
+}
+// Element of column c in q and o.
 template <int FORM, int D>
-__device__ __forceinline__ int64_t head_stride(const DecodeParams& p) {
-  return FORM == kRows ? (int64_t)p.m * D : D;
+__device__ __forceinline__ int64_t column_at(const DecodeParams& p, const Piece& pc, int c) {
+  const int64_t bh = (int64_t)pc.b * p.Hq + pc.h0 + head_of<FORM>(p, pc, c);
+  return (of_rows(FORM) ? bh * p.m + pc.i + (FORM == kPacked ? c / p.G : 0) : bh) * D;
 }
 
 // ROWS: rows that a CTA's warps may be attending at once (a team of warps each)
@@ -337,7 +351,7 @@ struct Query {
   __device__ void load(const DecodeParams& p, const Piece& pc, int rank) {
     if (rank >= Layout<D>::kGroups) return;        // (prepare_query)
     const int lane = threadIdx.x & 31, g = (lane >> 2) % (kHeads / PACK), t = lane & 3;
-    const T* q = static_cast<const T*>(p.q) + head_at<FORM, D>(p, pc, pc.h0 + g) + 8 * t;
+    const T* q = static_cast<const T*>(p.q) + column_at<FORM, D>(p, pc, g < pc.heads ? g : 0) + 8 * t;
 #pragma unroll
     for (int y = 0; y < Layout<D>::kGroups; ++y)
 #pragma unroll
@@ -505,8 +519,8 @@ __device__ __forceinline__ void prepare_query(const Query<T, D, PACK>& query, in
   }
 }
 
-// One piece; the result (all heads, the warps merged) goes to `o_row` (o of
-// head h0, divided by the row sums) or, when that is null, to `part`.
+// One piece; the result (all columns, the warps merged) goes to `o_row` (o of
+// head h0; chunks: o itself; divided by the row sums) or, when that is null, to `part`.
 // A step takes a block of two tiles.  PACK = 1: one after the other, the scores
 // of eight heads in the eight columns of the product.  PACK = 2 (at most four
 // heads): both at once, the first one's scores in columns 0 - 3 and the second
@@ -567,12 +581,16 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   uint32_t keep[PACK];
 #pragma unroll
   for (int u = 0; u < PACK; ++u) keep[u] = g / kCols == u ? 0xffffffffu : 0u;
-  float slope[2] = {0.f, 0.f};
+  float slope[2] = {0.f, 0.f}, back[2] = {0.f, 0.f};      // back: positions before the last row's
   int newest_start = 0;            // the largest bin start of the lane's heads
   const int quads = (p.s + 3) >> 2;
   if constexpr (EXACT) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) slope[k] = head + k < pc.heads ? slopes[pc.h0 + head + k] : 0.f;
+    for (int k = 0; k < 2; ++k)
+      if (head + k < pc.heads) {
+        slope[k] = slopes[pc.h0 + head_of<FORM>(p, pc, head + k)];
+        back[k] = (float)back_of<FORM>(p, pc, head + k);
+      }
   } else if (steps > 0) {
     for (int i = 0; i < 2 * quads; ++i) {
       const int4 v = starts[head * quads + i];
@@ -609,7 +627,8 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
     cp_async_wait<STAGES - 1>();
     __syncwarp();
     const uint32_t gone = (ring.absent >> (2 * st)) & 3u;
-    const bool edge = 32 * block < pc.first || 32 * block + 31 > pc.pos || gone;
+    const bool edge =
+        32 * block < pc.first || 32 * block + 31 > pc.pos - (FORM == kPacked ? pc.tokens - 1 : 0) || gone;
 #pragma unroll
     for (int sub = 2 / PACK - 1; sub >= 0; --sub) {
       // scores of positions j and j + 8 of the lane's tile, its two heads
@@ -687,7 +706,8 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         const float d0 = (float)(j - pc.pos), d1 = d0 + 8.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          x[k] = fmaf(x[k], qscale[k & 1], fmaf(k < 2 ? d0 : d1, slope[k & 1], z[k]));
+          x[k] = fmaf(x[k], qscale[k & 1],
+                      fmaf((k < 2 ? d0 : d1) + (FORM == kPacked ? back[k & 1] : 0.f), slope[k & 1], z[k]));
       } else {
         // c_j: every start in the row's past, or those at or before j
         int n[4] = {p.s, p.s, p.s, p.s};
@@ -724,6 +744,11 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
           x[2] = x[3] = -INFINITY;
 #pragma unroll
           for (int y = 0; y < Y; ++y) w1[y] = 0;
+        }
+        if constexpr (FORM == kPacked) {         // rows before the last
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (j + 8 * (k >> 1) > pc.pos - (int)back[k & 1]) x[k] = -INFINITY;
         }
       }
       // the weights, and P step of each group as f16 operands (times 2^-r):
@@ -992,8 +1017,8 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
         const float inv = some ? sm.scale[row][h] : 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[k] *= inv;
-        if constexpr (FORM == kRows)
-          store_row(o_row + (e - h * D) + h * head_stride<FORM, D>(p), o);
+        if constexpr (of_rows(FORM))
+          store_row(o_row + column_at<FORM, D>(p, pc, h) + (e - h * D), o);
         else
           store_row(o_row + e, o);
       }
@@ -1002,22 +1027,32 @@ __device__ __forceinline__ void attend(const DecodeParams& p, const Piece& pc, c
   __syncthreads();           // before the next piece fills the rings
 }
 
-// The row of entry b of the flat list (exact): its sequence (and row), position
+// The row of entry b of the flat list (exact): its sequence (and rows), position
 // and blocks, the first of them the one that position pc.first is in; none where
-// the position is out of range.  False: a row past its sequence's last.
+// the position is out of range.  Returns how many rows of the sequence the entry is
+// for, pc.tokens of them with a position (chunks).
 template <int FORM>
-__device__ __forceinline__ bool find_row(const DecodeParams& p, int b, Piece& pc, int& blocks) {
-  pc.b = FORM == kRows ? b / p.m : b;
-  pc.i = FORM == kRows ? b - pc.b * p.m : 0;
+__device__ __forceinline__ int find_row(const DecodeParams& p, int b, Piece& pc, int& blocks) {
+  int rows = 1;
+  pc.b = b;
+  pc.i = 0;
+  pc.tokens = 1;
   pc.first = FORM == kOwn ? p.first : 0;
-  pc.pos = p.pos[pc.b];
-  if (FORM == kRows && pc.pos >= 0) pc.pos = (int)min((int64_t)pc.pos + pc.i, (int64_t)p.limit);
-  blocks = pc.pos < pc.first || pc.pos >= p.limit ? 0 : (pc.pos >> 5) - (pc.first >> 5) + 1;
-  if (FORM == kRows && p.len != nullptr && pc.i >= p.len[pc.b]) {
-    blocks = 0;
-    return false;
+  if constexpr (of_rows(FORM)) {
+    pc.b = b / p.each;
+    pc.i = (b - pc.b * p.each) * p.tokens;
+    const int count = p.len == nullptr ? p.m : min(p.len[pc.b], p.m);
+    rows = max(0, min(p.tokens, count - pc.i));
+    pc.pos = p.pos[pc.b];
+    const int64_t room = pc.pos < 0 ? 0 : (int64_t)p.limit - pc.pos - pc.i;
+    pc.tokens = (int)max((int64_t)0, min((int64_t)rows, room));
+    if (pc.pos >= 0) pc.pos = (int)min((int64_t)pc.pos + pc.i + max(pc.tokens, 1) - 1, (int64_t)p.limit);
+    blocks = pc.tokens == 0 ? 0 : (pc.pos >> 5) + 1;
+  } else {
+    pc.pos = p.pos[pc.b];
+    blocks = pc.pos < pc.first || pc.pos >= p.limit ? 0 : (pc.pos >> 5) - (pc.first >> 5) + 1;
   }
-  return true;
+  return rows;
 }
 
 // heads of chunk c of a KV head
@@ -1041,7 +1076,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
   S& sm = *reinterpret_cast<S*>(raw);
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, units = p.c.H * p.chunks;
-  const int list = FORM == kRows ? p.c.B * p.m : p.c.B;
+  const int list = of_rows(FORM) ? p.c.B * p.each : p.c.B;
   Piece pc;
   auto row_entries = [&](int b) -> int64_t {
     int n;
@@ -1054,17 +1089,21 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
 #pragma unroll 4
   for (int b = tid; b < list; b += 32 * kExactWarps) {
     int n;
-    const bool row = find_row<FORM>(p, b, pc, n);
+    const int rows = find_row<FORM>(p, b, pc, n);
     sum += n == 0 ? 0 : n + kRowCost;
-    if (row && n == 0 && b % gridDim.x == blockIdx.x) {
+    if constexpr (of_rows(FORM)) {
+      if (pc.tokens < rows && b % gridDim.x == blockIdx.x) {
+        if (p.pos[pc.b] >= 0) atomicOr(p.err, kErrCachePlace);
+        for (int h = 0; h < p.Hq; ++h) {
+          const int64_t at = ((int64_t)pc.b * p.Hq + h) * p.m + pc.i + pc.tokens;
+          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + at * D);
+          for (int e = 0; e < (rows - pc.tokens) * D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
+        }
+      }
+    } else if (n == 0 && b % gridDim.x == blockIdx.x) {
       if (pc.pos >= p.limit) atomicOr(p.err, kErrCachePlace);
       if constexpr (FORM == kOwn) {
         for (int u = 0; u < units; ++u) p.rows[b * units + u] = make_int4(0, 0, 0, 0);
-      } else if constexpr (FORM == kRows) {
-        for (int h = 0; h < p.Hq; ++h) {
-          uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + head_at<FORM, D>(p, pc, h));
-          for (int e = 0; e < D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
-        }
       } else {
         uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.o) + (int64_t)b * p.Hq * D);
         for (int e = 0; e < p.Hq * D * (int)sizeof(T) / 16; ++e) o[e] = make_uint4(0, 0, 0, 0);
@@ -1129,6 +1168,7 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     f = till;
     if (pc.t1 <= pc.t0) continue;                 // the row's cost alone
     unit_heads(p, u / p.chunks, u % p.chunks, pc);
+    if (FORM == kPacked) pc.heads *= pc.tokens;
     const bool first = pc.t0 == 0, last = till == row + n;
     if (tid == 0 && last && (FORM == kOwn || !first)) {
       const int i0 = (int)((row + kRowCost) / per);    // the CTA of its first block
@@ -1152,7 +1192,9 @@ q4_exact_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ 
     Ring<T, D, FORM> ring(p, pc, sm.ring[tid >> 5]);
     attend<T, D, true, PACK, FORM>(
         p, pc, Team{0, kExactWarps, 0}, query, slopes.v, nullptr, sm, ring, false,
-        FORM != kOwn && first && last ? static_cast<T*>(p.o) + head_at<FORM, D>(p, pc, pc.h0) : nullptr,
+        FORM != kOwn && first && last
+            ? static_cast<T*>(p.o) + (of_rows(FORM) ? 0 : ((int64_t)pc.b * p.Hq + pc.h0) * D)
+            : nullptr,
         p.part + piece * part_floats<D>());
     slot = 2 * blockIdx.x + 1;
   }
@@ -1237,12 +1279,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) q4_exact_join_kernel(const __
   if (end.x < 0) return;
   const int units = p.c.H * p.chunks, h = blockIdx.y;
   Piece pc;
-  unit_heads(p, end.x % units / p.chunks, end.x % p.chunks, pc);
-  if (h >= pc.heads) return;
   int blocks;
   find_row<FORM>(p, end.x / units, pc, blocks);
+  unit_heads(p, end.x % units / p.chunks, end.x % p.chunks, pc);
+  if (FORM == kPacked) pc.heads *= pc.tokens;
+  if (h >= pc.heads) return;
   join_pieces<T, D>(p, end.z, 2 * (end.y + 1), 2, (int)blockIdx.x - end.y + 1, h,
-                    static_cast<T*>(p.o) + head_at<FORM, D>(p, pc, pc.h0 + h));
+                    static_cast<T*>(p.o) + column_at<FORM, D>(p, pc, h));
 }
 
 // Approximate.  KV heads by the largest scale of their query heads, widest
@@ -1430,15 +1473,16 @@ cudaError_t launch_exact(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st
   Slopes s;
   for (int h = 0; h < a.Hq; ++h) s.v[h] = a.slope_log2[h];
   // (a limit up to 2^31 - 16)
-  const int64_t list = (int64_t)p.c.B * (FORM == kRows ? p.m : 1);
+  const int64_t list = (int64_t)p.c.B * (of_rows(FORM) ? p.each : 1);
+  const int columns = p.per_chunk * (FORM == kPacked ? p.tokens : 1);
   const int64_t entries = list * p.c.H * p.chunks * (((int64_t)p.limit + 31) / 32 + kRowCost);
   const int64_t want = (entries + kMinBlocks - 1) / kMinBlocks;
   const unsigned grid = (unsigned)std::min<int64_t>(max_ctas(a.num_sms), want);
-  auto kern = p.per_chunk <= 4 ? q4_exact_kernel<T, D, 2, FORM> : q4_exact_kernel<T, D, 1, FORM>;
+  auto kern = columns <= 4 ? q4_exact_kernel<T, D, 2, FORM> : q4_exact_kernel<T, D, 1, FORM>;
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(kern), (int)sizeof(S));
   if (e == cudaSuccess) e = launch_dependent(kern, dim3(grid), 32 * kExactWarps, sizeof(S), st, p, s);
   if (e == cudaSuccess && FORM != kOwn)
-    e = launch_dependent(q4_exact_join_kernel<T, D, FORM>, dim3(grid, p.per_chunk), 32 * kJoinWarps, 0, st, p);
+    e = launch_dependent(q4_exact_join_kernel<T, D, FORM>, dim3(grid, columns), 32 * kJoinWarps, 0, st, p);
   return e;
 }
 
@@ -1528,7 +1572,7 @@ cudaError_t launch_approx(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t s
 template <typename T, int D>
 cudaError_t launch_typed(DecodeParams& p, const Q4DecodeArgs& a, cudaStream_t st) {
   if (a.rec) return launch_approx<T, D>(p, a, st);
-  if (a.m > 0) return launch_exact<T, D, kRows>(p, a, st);
+  if (a.m > 0) return p.tokens > 1 ? launch_exact<T, D, kPacked>(p, a, st) : launch_exact<T, D, kRows>(p, a, st);
   if constexpr (sizeof(T) == 2)
     if (a.rows != nullptr) return launch_exact<T, D, kOwn>(p, a, st);
   if (a.prefix != nullptr) return launch_exact<T, D, kShared>(p, a, st);
@@ -1572,6 +1616,10 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st) {
   p.part = reinterpret_cast<float*>(p.ends + max_ctas(a.num_sms));
   p.err = a.err;
   p.m = a.m;
+  // (evenly: nine rows of one head are five and four)
+  const int most = p.G <= 4 ? kHeads / p.G : 1;
+  p.each = std::max(1, (a.m + most - 1) / most);
+  p.tokens = std::max(1, (a.m + p.each - 1) / p.each);
   p.len = a.len;
   p.prefix = a.prefix;
   p.prefix_pages = a.prefix_pages;

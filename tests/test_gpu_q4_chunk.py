@@ -53,8 +53,9 @@ class Rows(Setup):
         g = torch.Generator("cuda").manual_seed(99)
         self.m = m
         self.q = torch.randn(B, Hq, m, d, device="cuda", generator=g).to(DT[dtype])
-        passes = m * -(-(Hq // H) // 8)
-        if wide and dtype == "bf16" and passes >= 7:
+        G = Hq // H
+        passes = m * -(-G // 8) if G > 4 else -(-m // (8 // G))
+        if wide and dtype == "bf16" and passes >= 6:
             # a table long enough for the tensor cores to be taken (its pages again and again)
             per = self.table.shape[1]
             long = max(per, -(-2 ** 19 // (B * H * passes * page)))
@@ -110,6 +111,12 @@ CASES = [
     (9, 4, 4, 128, 64, 200, "bf16", 40, [(37 * b) % 160 for b in range(9)], [5 * b for b in range(9)]),
     (1, 4, 2, 128, 16, 129, "bf16", 129, [0], None),
     (2, 2, 1, 64, 64, 5000, "bf16", 16, [4984, 2500], None),
+    (2, 2, 1, 64, 64, 5000, "bf16", 32, [4968, 2500], [31, 32]),
+    (9, 4, 4, 128, 64, 200, "bf16", 64, [(37 * b) % 130 for b in range(9)], [8 * b for b in range(9)]),
+    (2, 2, 2, 64, 32, 90, "bf16", 5, [31, 80], [5, 4]),                # five rows a pass
+    (2, 2, 2, 128, 32, 90, "f32", 9, [62, 1], None),                   # five and four
+    (3, 6, 2, 128, 16, 130, "bf16", 7, [100, 0, 60], [6, 7, 1]),       # two rows of three heads, and one
+    (4, 8, 2, 64, 64, 260, "f32", 3, [63, 254, -1, 7], [3, 3, 3, 0]),
     (3, 8, 2, 128, 64, 300, "bf16", 2, [298, -1, 30], [2, 2, 1]),      # few rows: not on the tensor cores
     (2, 3, 1, 64, 16, 150, "f32", 11, [139, 20], [11, 5]),
     (2, 8, 2, 128, 64, 700, "f32", 5, [600, 250], None),
@@ -140,10 +147,10 @@ def test_chunk_matches_the_oracle(case, wide):
 @pytest.mark.parametrize("sigma", [0.05, 3.0, 1e6])
 @pytest.mark.parametrize("d", [64, 128])
 def test_steep_and_flat_slopes_and_scores_that_jump(sigma, d):
-    s = Rows(2, 4, 2, d, 32, 900, "bf16", 24, seed=5)
+    s = Rows(2, 4, 2, d, 32, 900, "bf16", 28, seed=5)
     s.k[:, :, 100:140] *= 8                          # met late: the newest keys come first
     plsh.q4_cache_write(s.cache, s.k, s.v, i32([0, 0]))
-    pos, sig = [876, 300], np.full(4, sigma)
+    pos, sig = [872, 300], np.full(4, sigma)
     got = plsh.alibi_exact_chunk_q4(s.q, s.cache, sig, i32(pos))
     plsh.stream_status()
     s.check_rows(got, pos, None, sig)
@@ -168,7 +175,7 @@ def test_a_chunk_is_what_its_tokens_are_one_by_one():
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_what_was_never_written_has_no_effect(heads, d, dtype):
     Hq, H = heads
-    s = Rows(2, Hq, H, d, 32, 200, dtype, 40, seed=21)
+    s = Rows(2, Hq, H, d, 32, 200, dtype, 60, seed=21)
     pos, lens = [93, 129], [40, 33]
     sigma = alibi_sigmas(Hq)
     got = []
@@ -295,7 +302,7 @@ def test_a_query_that_is_not_finite_spoils_its_own_row_alone(bad):
     assert torch.equal(got[0].cpu()[rest], want[0].cpu()[rest])
 
 
-@pytest.mark.parametrize("dtype,m", [("bf16", 24), ("bf16", 3), ("f32", 9)])
+@pytest.mark.parametrize("dtype,m", [("bf16", 28), ("bf16", 3), ("bf16", 6), ("f32", 9)])
 def test_places_out_of_range_are_reported(dtype, m):
     s = Rows(3, 4, 2, 128, 16, 64, dtype, m, seed=3)
     sigma = alibi_sigmas(4)
@@ -522,7 +529,7 @@ def test_a_server_s_loop_of_prompts_and_tokens():
     H, Hq, d, page, B = 2, 8, 128, 16, 6
     pages, cap = 80, 12
     pool = i32(np.concatenate([[pages], np.random.default_rng(0).permutation(pages)]))
-    held, table = i32([0]), i32(np.full((1, 512), -1))
+    held, table = i32([0]), i32(np.full((1, 1024), -1))
     data = torch.randint(0, 256, (pages, H, 1, 20 * d), dtype=torch.uint8, device="cuda")
     one = plsh.Q4Cache(data, table, H, d, page)
     sigma = alibi_sigmas(Hq)
