@@ -67,7 +67,7 @@ constexpr int kSoftWarps = 16, kKWarp = 16, kVWarp = 20, kDeqWarps = 4, kMmaWarp
 constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps, kTileThreads = 256;
 // of 896 threads' 72 at launch: 512 x 96 + 256 x 48 + 128 x 24 = 64512, all of them
 constexpr int kRegsSoftmax = 96, kRegsDeq = 48, kRegsRest = 24;
-enum { BAR_V = 1, BAR_TILE = 2, BAR_PAIR = 4 };      // named barriers: V's warps, a tile's, two warps of a row
+enum { BAR_V = 1, BAR_PAIR = 2 };      // named barriers: V's warps, two warps of a row
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
 constexpr int kItemCost = 2;            // steps that beginning and ending an item costs
 constexpr uint32_t kTmemCols = 512;     // S_A | S_B | O_A | O_B; P over S
@@ -88,7 +88,7 @@ struct Sizes {
 enum {
   B_IFULL = 0, B_IEMPTY = 2, B_VEMPTY = 4, B_VREADY = 6, B_INFO = 8, B_KREADY = 12,
   B_KEMPTY = 16, B_QFULL = 18, B_SFULL = 20, B_PFULL = 22, B_ODONE = 24,
-  B_DRAIN = 26, NUM_BARS
+  B_DRAIN = 26, B_ROWS = 27, NUM_BARS = 29
 };
 
 // Rows [row0, row1) of a sequence's (or the batch's) rows of one KV head against the
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       mbar_init(bar(B_SFULL + k), 1);
       mbar_init(bar(B_PFULL + k), kTileThreads);
       mbar_init(bar(B_ODONE + k), 1);
+      mbar_init(bar(B_ROWS + k), kSoftWarps / 2);
     }
     for (int k = 0; k < 4; ++k) {
       mbar_init(bar(B_KREADY + k), kDeqWarps);
@@ -865,9 +866,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     uint32_t g = 0, gt = 0, items = 0;   // steps, this tile's steps and items
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      // (whether a wait ran out is told to all who share a barrier, before any leaves)
+      // (whether a wait ran out is told to the two warps of a row, which alone share
+      // barriers without a limit, before either leaves)
       ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim);
-      ok = barrier_and(BAR_TILE + tile, kTileThreads, ok);
+      ok = barrier_and(pair, 64, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
@@ -907,7 +909,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         const uint32_t top = __reduce_max_sync(FULL, row_bad ? 0u : mx);
         if (lane == 0) ctl->qmax[tile][warp & 7] = top;
         ctl->pair[tile][half][r] = row_bad ? 1.f : 0.f;
-        ok = barrier_and(BAR_TILE + tile, kTileThreads, ok);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_ROWS + tile));
+        ok = mbar_wait(bar(B_ROWS + tile), items & 1u, abort, lim);
+        ok = barrier_and(pair, 64, ok);
         row_bad = row_bad || ctl->pair[tile][half ^ 1][r] != 0.f;
         uint32_t all = 0;
 #pragma unroll
