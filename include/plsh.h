@@ -600,6 +600,18 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  * page index is not in [0, pages) counts as absent; either is reported as
  * PLSH_ERR_INVALID by plsh_stream_status.  What lies behind a row's position has
  * no effect on it.  Everything else as for plsh_alibi_exact_decode_q4.
+ *
+ * bf16 calls of many rows (decided by sizes alone: tokens and query heads of a KV
+ * head, and the table's length) run on the tensor cores with the cached values
+ * themselves in f16: q, k and v are rounded to 2^-11 of themselves under powers of
+ * two that put the largest of a KV head's next 128 rows of q, of 32 positions of K,
+ * and of 32 positions of V (relative to the sizes of their groups of 32 in the
+ * newest keys) just below 2^15, no finer than 2^-24; weights to 2^-11 of
+ * themselves, no finer than 2^-24 of about the row's largest.  So a key or a value
+ * 2^29 times the others takes precision from the 31 positions beside it alone.  A
+ * group of V more than 2^48 times what the newest keys' steps hold (of those that
+ * one thread block attends over) is reported as PLSH_ERR_RANGE by
+ * plsh_stream_status, and o is then not to be used.
  */
 plsh_status plsh_alibi_exact_chunk_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
                                       const double* sigma_h, const int32_t* pos, const int32_t* len,
@@ -619,7 +631,9 @@ plsh_status plsh_q4_prefix_work_bytes(const plsh_tensor* q, const plsh_q4_cache*
  *   work   device memory of plsh_q4_prefix_work_bytes, as for
  *          plsh_alibi_decode_q4.
  * A sequence may be anywhere, within the prefix too (pos[b] negative: idle).
- * Everything else as for plsh_alibi_exact_decode_q4.
+ * Everything else as for plsh_alibi_exact_decode_q4; bf16 calls of many sequences
+ * behind a long prefix take the prefix's part on the tensor cores, as described at
+ * plsh_alibi_exact_chunk_q4.
  */
 plsh_status plsh_alibi_exact_prefix_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
                                               const double* sigma_h, const int32_t* pos,
@@ -630,7 +644,8 @@ plsh_status plsh_alibi_exact_prefix_decode_q4(const plsh_tensor* q, const plsh_q
 /* Synchronises `stream`, then reports CUDA errors and the library's device
  * error flag, clearing the flag: PLSH_ERR_TIMEOUT when a bounded device wait
  * ran out, else PLSH_ERR_RANGE when a tensor-core attention call met a value
- * of V beyond +-65504, else PLSH_ERR_INVALID when a call on a 4-bit cache met
+ * of V beyond +-65504 (over a 4-bit cache: beyond what plsh_alibi_exact_chunk_q4
+ * says), else PLSH_ERR_INVALID when a call on a 4-bit cache met
  * a position or a page index out of range. */
 plsh_status plsh_stream_status(void* stream);
 

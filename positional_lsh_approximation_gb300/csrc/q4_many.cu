@@ -36,12 +36,31 @@
 // bounded; on expiry the CTA raises the error flag, lets its copies and products
 // drain, frees its tensor memory and exits.
 //
-// What bounds it.  The products of a step take 2048 cycles (4096 multiply-adds a
-// cycle); the kernel takes about 3700.  Neither the tensor cores (55 %) nor the
-// schedulers' issue slots (about 2700 of softmax and of taking codes apart) are full:
-// a tile's steps follow one another through its scores, its softmax and P V, as P
-// stands where its scores stood (S, O of two tiles fill the tensor memory), and the
-// two tiles' chains fill each other's gaps in part.
+// What bounds it.  The products of a step (two tiles) take 2048 cycles at 4096
+// multiply-adds a cycle.  Measured (CUDA graph, back to back; shares of the measured
+// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2550 us (1060
+// TFLOP/s, 55 %), 2.4 us a step; 512 tokens behind 7680, 32/8 heads, 104 us (26 steps
+// a CTA); a batch of eight ragged chunks 292 us; 128 sequences behind a prefix of
+// 65536, 40/8 heads, 252 us, 64 behind 8192, 32/8 heads, 52 us (four steps a CTA).
+// Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 33 %,
+// issue slots 54 %): a tile's steps follow one another through its scores (1000
+// cycles with P V before them), its softmax (2100 of weights, 500 until they are in
+// tensor memory) and the products' barriers, as P stands where its scores stood (S
+// and O of two tiles fill the tensor memory), and the two tiles' chains fill each
+// other's gaps in part.  Beginning an item costs more: 12000 cycles from its listing
+// to the first scores, where table, pages and queries come one after another from
+// memory not touched before, and 7000 for the first step, whose weights are taken
+// twice.
+//
+// What it took (2048 behind 63488): one thread's product issue from a branch of its
+// own 3311 us, the whole warp's with a predicate 2835 (operands stay in uniform
+// registers); softmax by sixteen columns with the next ones' load in flight, V's
+// exponents from one reduction, 96 registers for softmax 2550.  Slower, and dropped:
+// one thread a row (3100), 80 registers for softmax (3070), scalar instead of paired
+// fp32 multiply-adds (2710), the first step's weights not tried before its maximum is
+// known (2910, the loop's code suffers), K's and V's next codes loaded while these
+// are taken apart (2700 to 3080), and for items of one tile the other tile on every
+// second step of the same keys (146 -> 166 us for 64 rows of 131072 keys).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -4,13 +4,13 @@ cache holds.
 
 Tolerance: that of the decode step's tests (derived there), and for bf16, where
 many rows of a KV head go to the tensor cores with values rounded to f16 (2^-11 of
-themselves: half a step of 11 bits):
-  - K: every product of a score is off by 2^-11 of itself, and by 2^-18 of the
-    position's largest (f16's subnormals under a largest of 2^-7): the score by
-    2^-11 (1 + 2^-7 d) A at most, with A as there without the bias; o by twice that
-    times R;
-  - P and V: 2^-11 each of a convex combination of values within R, and V's
-    subnormals 2^-24 of the largest of a step, which the 2^-10 R covers.
+themselves at most, half a step of 11 bits; the largest of 32 positions' lies in
+[2^14, 2^15), so f16's smallest step, 2^-24, is 2^-38 of it):
+  - K: every product of a score is off by 2^-11 of itself: the score by 2^-11 A at
+    most, with A as there without the bias; o by twice that times R.  Where keys of
+    32 positions differ by more than 2^29 the small ones lose more, 2^-38 of the
+    largest: the bound leaves 2^-7 d of 2^-11 A for it;
+  - P and V: 2^-11 each of a convex combination of values within R: 2^-10 R.
 These are bounds of the worst signs.  Roundings of independent sign leave much
 less, and the whole output is held to that: its relative 2-norm error is below
 2.5e-3 in bf16 (the output's own rounding: at most 2^-8 / sqrt(3) = 2.26e-3 for
