@@ -1457,7 +1457,8 @@ int64_t q4_rows_work_bytes(const plsh_tensor* q, const plsh::Q4Cache& c, bool pr
   if (prefix ? !q4_may_be_many(q, c, true, &passes) : !q4_many(q, c, 0)) return bytes;
   // (a prefix's: whatever its length)
   const int64_t own = prefix ? plsh::q4_own_work_bytes(c.d, num_sms, c.B, c.H, (int)(q->H / c.H)) : 0;
-  return std::max(bytes, own + plsh::q4_many_work_bytes(c.d, num_sms));
+  const int64_t rows = prefix ? q->B * (q->H / c.H) : 0;
+  return std::max(bytes, own + plsh::q4_many_work_bytes(c.d, num_sms, rows, c.H));
 }
 
 // The exact step of several rows a sequence (prefix NULL) or behind a shared prefix.

@@ -331,7 +331,7 @@ int64_t q4_own_work_bytes(int d, int num_sms, int B, int Hkv, int G);
 const float* q4_own_pieces(const void* work, int num_sms);
 // q4_many.cu (bf16): many rows a KV head on the tensor cores; m rows a sequence, or
 // behind a prefix.  work: q4_many_work_bytes; a prefix's, behind q4_own_work_bytes
-int64_t q4_many_work_bytes(int d, int num_sms);
+int64_t q4_many_work_bytes(int d, int num_sms, int64_t rows, int Hkv);
 cudaError_t launch_q4_chunk(const Q4DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_q4_prefix(const Q4DecodeArgs& a, cudaStream_t st);
 cudaError_t launch_q4_decode(const Q4DecodeArgs& a, cudaStream_t st);

@@ -39,8 +39,8 @@
 // What bounds it.  The products of a step (two tiles) take 2048 cycles at 4096
 // multiply-adds a cycle.  Measured (CUDA graph, back to back; shares of the measured
 // GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2550 us (1060
-// TFLOP/s, 55 %), 2.4 us a step; 512 tokens behind 7680, 32/8 heads, 104 us (26 steps
-// a CTA); a batch of eight ragged chunks 292 us; 128 sequences behind a prefix of
+// TFLOP/s, 55 %), 2.4 us a step; 512 tokens behind 7680, 32/8 heads, 101 us (26 steps
+// a CTA); a batch of eight ragged chunks 248 us; 128 sequences behind a prefix of
 // 65536, 40/8 heads, 252 us, 64 behind 8192, 32/8 heads, 52 us (four steps a CTA).
 // Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 33 %,
 // issue slots 54 %): a tile's steps follow one another through its scores (1000
@@ -88,7 +88,11 @@ constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps, kTileThreads
 constexpr int kRegsSoftmax = 96, kRegsDeq = 48, kRegsRest = 24;
 enum { BAR_V = 1, BAR_PAIR = 2 };      // named barriers: V's warps, two warps of a row
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
-constexpr int kItemCost = 2;            // steps that beginning and ending an item costs
+// Steps that beginning and ending an item costs (a batch of eight ragged chunks: 2 ->
+// 293 us, 4 -> 266, 6 -> 248, 12 -> 250; 512 tokens behind 7680: 104, 100, 101, 107),
+// and entries of a CTA at least (64 sequences behind a prefix of 8192: 3 -> 52 us, 6 ->
+// 53, 9 -> 60).
+constexpr int kItemCost = 6, kMinShare = 3;
 constexpr uint32_t kTmemCols = 512;     // S_A | S_B | O_A | O_B; P over S
 constexpr uint32_t kColP = 64, kColO = 256;
 constexpr float kGrowLog2 = 15.f;       // largest weight 2^15: above, the reference moves
@@ -111,7 +115,9 @@ enum {
 };
 
 // Rows [row0, row1) of a sequence's (or the batch's) rows of one KV head against the
-// key steps [k0, k1), of which positions up to `last` count.
+// key steps [k0, k1), of which positions up to `last` count.  slot: the piece it
+// leaves; a CTA's first piece 2 i, its last 2 i + 1, and, behind all of these, a
+// prefix's item that lies in one CTA, of which a CTA may have many.
 struct Item {
   int valid, b, kvh, row0, row1, k0, k1, pos, last, slot;      // slot < 0: the whole item
 };
@@ -414,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       total += ctl->sums[w];
     }
     const int64_t all = total * p.c.H, fair = (all + gridDim.x - 1) / gridDim.x;
-    per = fair < kItemCost + 1 ? kItemCost + 1 : fair;
+    per = fair < kMinShare ? kMinShare : fair;
     begin = blockIdx.x * per;
     end = min(all, begin + per);
     if (begin < end) {
@@ -490,13 +496,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         const int t0 = (int)max((int64_t)0, f - base - kItemCost), t1 = (int)(till - base - kItemCost);
         f = till;
         if (t1 <= t0) continue;
-        const bool closes = till == base + cost, whole = !PREFIX && t0 == 0 && closes;
+        const bool closes = till == base + cost, whole = t0 == 0 && closes;
         if (!PREFIX && closes && !whole && lane == 0) {
           const int i0 = (int)((base + kItemCost) / per);          // the CTA of its first step
           p.ends[blockIdx.x] = make_int4(kvh * entries + e, i0, base <= i0 * per ? 2 * i0 : 2 * i0 + 1, 0);
         }
         publish(Item{1, b, kvh, kItemRows * t, min(rows, kItemRows * (t + 1)), t0, t1, pos, last,
-                     whole ? -1 : slot});
+                     !whole ? slot : PREFIX ? (int)(2 * gridDim.x) + kvh * p.tiles + t : -1});
         slot = 2 * blockIdx.x + 1;
       }
     }
@@ -1184,6 +1190,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
 // So an item that all CTAs work on (one sequence behind a long context) is read by many
 // threads, with loads of several pieces in flight: one CTA for all columns and pieces
 // took longer than the attention itself (131072 keys, one KV head: 100 of 121 us).
+// (64 sequences behind a prefix of 8192, 16 pieces an item: 4 or 8 -> 55 us, 16 -> 59;
+// 512 tokens behind 7680, 4 to 5: 4 -> 108, 8 -> 104.)
 constexpr int kJoinThreads = 256, kSplit = 8;
 
 template <int D>
@@ -1342,7 +1350,7 @@ struct PrefixJoin {
   int64_t total, per;                 // of the prefix's list: entries of a KV head, of a CTA
   const int4* rows;                   // own keys: per row {first piece, second, pieces, 0}
   const float* own;                   // their pieces: o [8][D], maximum [8], sum [8]
-  int chunks, per_chunk;
+  int chunks, per_chunk, ctas;
 };
 
 template <int D, bool SPLIT>
@@ -1359,7 +1367,7 @@ q4_prefix_join_kernel(const __grid_constant__ ManyParams p, const __grid_constan
   // the item's entries [base, base + cost): its pieces' CTAs
   const int64_t cost = ((p.keys + BN - 1) / BN) + kItemCost, base = kvh * j.total + t * cost;
   const int i0 = (int)((base + kItemCost) / j.per), i1 = (int)((base + cost - 1) / j.per);
-  const int slot0 = base <= i0 * j.per ? 2 * i0 : 2 * i0 + 1, n = i1 - i0 + 1;
+  const int n = i1 - i0 + 1, slot0 = n == 1 ? 2 * j.ctas + (int)blockIdx.x : base <= i0 * j.per ? 2 * i0 : 2 * i0 + 1;
   auto piece = [&](int k) { return p.part + (int64_t)(k == 0 ? slot0 : 2 * (i0 + k)) * part_floats<D>(); };
   const int q0 = SPLIT ? 2 * blockIdx.z : w, stride = SPLIT ? 1 : 8;
   RowSum<NQ> a;
@@ -1433,12 +1441,13 @@ cudaError_t launch_prefix(const Q4DecodeArgs& a, cudaStream_t st) {
   fill(p, a, static_cast<uint8_t*>(a.work) + own);
   p.tiles = (int)(((int64_t)a.c.B * p.G + kItemRows - 1) / kItemRows);
   PrefixJoin j;
+  j.ctas = a.num_sms;
   j.chunks = (p.G + 7) / 8;
   j.per_chunk = (p.G + j.chunks - 1) / j.chunks;
   // (as the kernel finds them)
   j.total = (int64_t)p.tiles * ((p.keys + BN - 1) / BN + kItemCost);
   const int64_t all = j.total * a.c.H;
-  j.per = std::max<int64_t>((all + a.num_sms - 1) / a.num_sms, kItemCost + 1);
+  j.per = std::max<int64_t>((all + a.num_sms - 1) / a.num_sms, kMinShare);
   // the sequences' own keys, then the prefix's, then both together
   Q4DecodeArgs b = a;
   uint8_t* w = static_cast<uint8_t*>(a.work);
@@ -1461,8 +1470,9 @@ cudaError_t launch_prefix(const Q4DecodeArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-int64_t q4_many_work_bytes(int d, int num_sms) {
-  return (int64_t)num_sms * (sizeof(int4) + 2 * sizeof(float) * kItemRows * (d + 2));
+int64_t q4_many_work_bytes(int d, int num_sms, int64_t rows, int Hkv) {
+  const int64_t items = (rows + kItemRows - 1) / kItemRows * Hkv;
+  return num_sms * (int64_t)sizeof(int4) + (2 * num_sms + items) * (int64_t)sizeof(float) * kItemRows * (d + 2);
 }
 
 cudaError_t launch_q4_chunk(const Q4DecodeArgs& a, cudaStream_t st) {

@@ -404,6 +404,8 @@ PREFIXES = [
     (16, 32, 8, 128, 256, 48, 600, "bf16", [12288 + (97 * b) % 600 for b in range(16)]),
     (300, 2, 1, 64, 64, 82, 3, "bf16", [5248 + b % 3 for b in range(300)]),                 # more rows than an item
     (16, 32, 8, 128, 256, 16, 600, "bf16", [4096 + (97 * b) % 600 for b in range(16)]),
+    (1100, 40, 40, 64, 16, 8, 5, "bf16", [127 + b % 6 for b in range(1100)]),               # several items in a CTA
+    (700, 64, 64, 128, 16, 7, 3, "bf16", [(7 * b) % 115 for b in range(700)]),
     (3, 8, 2, 128, 64, 3, 70, "bf16", [200, -1, 30]),
     (5, 3, 1, 64, 16, 9, 33, "f32", [144, 143, 176, -1, 0]),
     (34, 8, 1, 128, 64, 2, 10, "f32", [128 + b % 10 for b in range(34)]),
