@@ -95,6 +95,9 @@ constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte s
 constexpr int kItemCost = 6, kMinShare = 3;
 constexpr uint32_t kTmemCols = 512;     // S_A | S_B | O_A | O_B; P over S
 constexpr uint32_t kColP = 64, kColO = 256;
+// A wait for an item to begin or end may last as long as one (a step's does not), and
+// ends when a step's wait ran out: its limit is this many of theirs.
+constexpr uint64_t kItemWaits = 64;
 constexpr float kGrowLog2 = 15.f;       // largest weight 2^15: above, the reference moves
 constexpr float kNothing = -3.402823466e38f;
 constexpr unsigned FULL = 0xffffffffu;
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     int seq = 0, slot = 2 * blockIdx.x;
     auto publish = [&](const Item& it) {
       const int s = seq & 1;
-      ok = __all_sync(FULL, mbar_wait(bar(B_IEMPTY + s), ((uint32_t)(seq >> 1) & 1u) ^ 1u, abort, lim));
+      ok = __all_sync(FULL, mbar_wait(bar(B_IEMPTY + s), ((uint32_t)(seq >> 1) & 1u) ^ 1u, abort, lim * kItemWaits));
       if (ok && lane == 0) {
         volatile int* v = reinterpret_cast<volatile int*>(&ctl->ring[s]);
         v[0] = it.valid; v[1] = it.b; v[2] = it.kvh; v[3] = it.row0; v[4] = it.row1;
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       int jj = 0, steps = 0;                     // step of the item, its steps (0: the end)
       bool two = false, ptwo = false, pfirst = false, plast = false;      // p: of the step before
       auto next_item = [&]() {
-        ok = wait(B_IFULL + (seq & 1), (seq >> 1) & 1u);
+        ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + (seq & 1)), (seq >> 1) & 1u, abort, lim * kItemWaits));
         const volatile Item& it = ctl->ring[seq & 1];
         steps = __shfl_sync(FULL, ok && it.valid ? it.k1 - it.k0 : 0, 0);
         two = __shfl_sync(FULL, it.row1 - it.row0, 0) > BM;
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     float unit[Y];                       // 2^-R_y
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim);
+      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim * kItemWaits);
       ok = barrier_and(BAR_V, kDeqThreads, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
@@ -788,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     int g = 0;
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim));
+      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim * kItemWaits));
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       const int islot = seq & 1;
       // (whether a wait ran out is told to the two warps of a row, which alone share
       // barriers without a limit, before either leaves)
-      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim);
+      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim * kItemWaits);
       ok = barrier_and(pair, 64, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);

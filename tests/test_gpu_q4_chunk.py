@@ -525,6 +525,40 @@ def test_prefix_nan_and_queries_that_are_no_numbers(B, shared):
     assert torch.isnan(got[others][..., 96:]).all() and torch.isfinite(got[others][..., :96]).all()
 
 
+@pytest.mark.parametrize("B,shared", [(64, 390), (6, 3)])
+def test_prefix_streams_graphs_and_workspaces(B, shared):
+    """Captured, replayed at other positions on two streams at once, beside the same
+    call made directly; a workspace no smaller than it must be."""
+    s = Shared(B, 4, 1, 128, 64, shared, 70, "bf16", seed=8)
+    sig = alibi_sigmas(4)
+    pos = i32([s.P + (11 * b) % 70 for b in range(B)])
+    plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sig, pos, s.d_prefix)
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sig, pos, s.d_prefix))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for at in ([s.P + (7 * b) % 60 for b in range(B)], [(997 * b) % s.P if b % 3 else -1 for b in range(B)]):
+        pos.copy_(i32(at))
+        s.q.copy_(torch.randn_like(s.q))
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+            got = plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sig, pos, s.d_prefix)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], got) and torch.equal(outs[1], got)
+        s.check(got, at, sig)
+    need = plsh.q4_prefix_work_bytes(s.q, s.cache)
+    w = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sig, pos, s.d_prefix, work=w), got)
+    with pytest.raises(plsh.PlshError, match="work must be"):
+        plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, sig, pos, s.d_prefix, work=w[:-16])
+    plsh.stream_status()
+
+
 def test_a_server_s_loop_of_prompts_and_tokens():
     """The calls as they are used together: pages reserved, a shared prompt written
     and attended to in pieces, sequences of their own behind it, a token each."""
