@@ -41,7 +41,7 @@
 // GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2550 us (1060
 // TFLOP/s, 55 %), 2.4 us a step; 512 tokens behind 7680, 32/8 heads, 101 us (26 steps
 // a CTA); a batch of eight ragged chunks 248 us; 128 sequences behind a prefix of
-// 65536, 40/8 heads, 252 us, 64 behind 8192, 32/8 heads, 52 us (four steps a CTA).
+// 65536, 40/8 heads, 252 us, 64 behind 8192, 32/8 heads, 51 us (four steps a CTA).
 // Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 33 %,
 // issue slots 54 %): a tile's steps follow one another through its scores (1000
 // cycles with P V before them), its softmax (2100 of weights, 500 until they are in

@@ -20,9 +20,9 @@
 // 1 to 8 CTAs, so that one launch does it all: every CTA makes the prefix sums for
 // itself, the cluster's warps move the pages of a sequence each, and the cluster's
 // barrier stands between what is read and what is written over it.  Measured with the
-// slots of the new rows (two launches, CUDA graph): 64 sequences growing by a token 8.8
-// us, 256 of which a quarter finish and a quarter bring prompts of up to 2048 tokens
-// 19.6 (4 MB of slots).
+// slots of the new rows (requests taken back, made again, slots: three launches): 64
+// sequences growing by a token 8.9 us, 256 of which a quarter finish and a quarter bring prompts of up to 2048 tokens
+// 19.4 (4 MB of slots).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(256) q4_slots_kernel(const __grid_constant__ Q
 cudaError_t launch_q4_reserve(const Q4ReserveArgs& a, cudaStream_t st) {
   // a CTA's 32 warps take a sequence each at a time; more CTAs where rows are
   // many and long enough to pay for the cluster's barriers (256 rows of 512: 8 CTAs
-  // 22.5 us with the slots, 4 26.6, 1 30.7; 64 rows of 128: 1 CTA 10.3, 8 12.3)
+  // 22.5 us for two calls and the slots, 4 26.6, 1 30.7; 64 rows of 128: 1 CTA 10.3, 8 12.3)
   const int64_t pages = (int64_t)a.c.B * a.c.max_pages;
   unsigned cluster = 1;
   while (cluster < kMaxCluster && pages > (int64_t)cluster * 8192 && a.c.B > (int)cluster * kWarps) cluster *= 2;
