@@ -38,10 +38,10 @@
 //
 // What bounds it.  The products of a step (two tiles) take 2048 cycles at 4096
 // multiply-adds a cycle.  Measured (CUDA graph, back to back; shares of the measured
-// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2550 us (1060
-// TFLOP/s, 55 %), 2.4 us a step; 512 tokens behind 7680, 32/8 heads, 101 us (26 steps
-// a CTA); a batch of eight ragged chunks 248 us; 128 sequences behind a prefix of
-// 65536, 40/8 heads, 252 us, 64 behind 8192, 32/8 heads, 51 us (four steps a CTA).
+// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2430 us (1110
+// TFLOP/s, 58 %), 2.3 us a step; 512 tokens behind 7680, 32/8 heads, 95 us (26 steps
+// a CTA); a batch of eight ragged chunks 234 us; 128 sequences behind a prefix of
+// 65536, 40/8 heads, 239 us, 64 behind 8192, 32/8 heads, 51 us (four steps a CTA).
 // Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 33 %,
 // issue slots 54 %): a tile's steps follow one another through its scores (1000
 // cycles with P V before them), its softmax (2100 of weights, 500 until they are in
@@ -55,12 +55,13 @@
 // What it took (2048 behind 63488): one thread's product issue from a branch of its
 // own 3311 us, the whole warp's with a predicate 2835 (operands stay in uniform
 // registers); softmax by sixteen columns with the next ones' load in flight, V's
-// exponents from one reduction, 96 registers for softmax 2550.  Slower, and dropped:
-// one thread a row (3100), 80 registers for softmax (3070), scalar instead of paired
-// fp32 multiply-adds (2710), the first step's weights not tried before its maximum is
-// known (2910, the loop's code suffers), K's and V's next codes loaded while these
-// are taken apart (2700 to 3080), and for items of one tile the other tile on every
-// second step of the same keys (146 -> 166 us for 64 rows of 131072 keys).
+// exponents from one reduction 2550; whether anything is masked decided once a step,
+// and registers given to the codes 2430.  Slower, and dropped: one thread a row
+// (3100), 80 registers for softmax (2770), scalar instead of paired fp32 multiply-adds
+// (+6 %), the first step's weights not tried before its maximum is known (+14 %, the
+// loop's code suffers), K's and V's next codes loaded while these are taken apart
+// (2415 to 2480, shorter items lose more), and for items of one tile the other tile on
+// every second step of the same keys (64 rows of 131072 keys: 146 -> 166 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -84,8 +85,8 @@ constexpr int BM = 128, BN = 128;       // rows of a tile, keys of a step
 constexpr int kItemRows = 2 * BM;
 constexpr int kSoftWarps = 16, kKWarp = 16, kVWarp = 20, kDeqWarps = 4, kMmaWarp = 24, kProdWarp = 25, kWarps = 28;
 constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps, kTileThreads = 256;
-// of 896 threads' 72 at launch: 512 x 96 + 256 x 48 + 128 x 24 = 64512, all of them
-constexpr int kRegsSoftmax = 96, kRegsDeq = 48, kRegsRest = 24;
+// of 896 threads' 72 at launch: 512 x 88 + 256 x 64 + 128 x 24 = 64512, all of them
+constexpr int kRegsSoftmax = 88, kRegsDeq = 64, kRegsRest = 24;
 enum { BAR_V = 1, BAR_PAIR = 2 };      // named barriers: V's warps, two warps of a row
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
 // Steps that beginning and ending an item costs (a batch of eight ragged chunks: 2 ->
@@ -1004,8 +1005,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         // scores jump).
         uint32_t pk[32], most;
         int some_nan = 0;
-        // exponents of sixteen keys, x + ev - mu, -inf where masked
-        auto exponents = [&](int c, const uint32_t (&rr)[16], uint2 kq, float ev, float (&x)[16]) {
+        // exponents of sixteen keys, x + ev - mu, -inf where masked (if any are)
+        auto exponents = [&](auto masked, int c, const uint32_t (&rr)[16], uint2 kq, float ev, float (&x)[16]) {
           const int jc = j0 + 16 * c;
           const float cs = fminf(__uint_as_float(kq.x) * qs, 3.402823466e38f);
           const uint64_t cs2 = f2_pack(cs, cs);
@@ -1019,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
                       x[2 * e], x[2 * e + 1]);
             b[e & 1] = f2_add(b[e & 1], rise4);
           }
-          if (pos_min < jc + 15 || kq.y != 0xffffffffu) {
+          if constexpr (decltype(masked)::value) {
             const uint32_t vm = upto_mask(pos - jc) & (kq.y >> (16 * (c & 1)));
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -1030,33 +1031,39 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         for (int pass = 0;; ++pass) {
           most = 0;
           sum = 0.f;
-          uint32_t ra[16], rb[16];
-          tmem_ld16(s_col, ra);
-          uint2 kq, vq;
+          const uint4 kk = ld_shared_v4(kinfo), vv = ld_shared_v4(vinfo);
+          some_nan = (int)(vv.y | vv.w);
+          auto take = [&](auto masked) {
+            uint32_t ra[16], rb[16];
+            tmem_ld16(s_col, ra);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t(&rr)[16] = c & 1 ? rb : ra;
-            if (!(c & 1)) {
-              kq = ld_shared_v2(kinfo + 4 * c);
-              vq = ld_shared_v2(vinfo + 4 * c);
-              some_nan |= (int)vq.y;
-            }
-            tmem_wait_ld();
-            if (c < 3) tmem_ld16(s_col + 16 * (c + 1), c & 1 ? ra : rb);
-            float x[16];
-            exponents(c, rr, kq, __uint_as_float(vq.x), x);
-            uint64_t t[2];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t(&rr)[16] = c & 1 ? rb : ra;
+              const uint2 kq = c < 2 ? make_uint2(kk.x, kk.y) : make_uint2(kk.z, kk.w);
+              const uint2 vq = c < 2 ? make_uint2(vv.x, vv.y) : make_uint2(vv.z, vv.w);
+              tmem_wait_ld();
+              if (c < 3) tmem_ld16(s_col + 16 * (c + 1), c & 1 ? ra : rb);
+              float x[16];
+              exponents(masked, c, rr, kq, __uint_as_float(vq.x), x);
+              uint64_t t[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float u = ex2(x[2 * e]), v = ex2(x[2 * e + 1]);
-              t[e & 1] = e < 2 ? f2_pack(u, v) : f2_add(t[e & 1], f2_pack(u, v));
-              pk[8 * c + e] = pack_f16(u, v);
-              if (e & 1) most = __vimax3_u16x2(most, pk[8 * c + e - 1], pk[8 * c + e]);
+              for (int e = 0; e < 8; ++e) {
+                const float u = ex2(x[2 * e]), v = ex2(x[2 * e + 1]);
+                t[e & 1] = e < 2 ? f2_pack(u, v) : f2_add(t[e & 1], f2_pack(u, v));
+                pk[8 * c + e] = pack_f16(u, v);
+                if (e & 1) most = __vimax3_u16x2(most, pk[8 * c + e - 1], pk[8 * c + e]);
+              }
+              float s0, s1;
+              f2_unpack(f2_add(t[0], t[1]), s0, s1);
+              sum = fmaf(s0 + s1, fabsf(__uint_as_float(vq.y)), sum);
             }
-            float s0, s1;
-            f2_unpack(f2_add(t[0], t[1]), s0, s1);
-            sum = fmaf(s0 + s1, fabsf(__uint_as_float(vq.y)), sum);
-          }
+          };
+          // (One decision a step: with one every sixteen keys nothing moved across it,
+          // 2550 us against 2430 for 2048 tokens behind 63488.)
+          if (pos_min < j0 + 63 || (kk.y & kk.w) != FULL)
+            take(std::true_type());
+          else
+            take(std::false_type());
           const bool fresh = m_ref == -INFINITY;
           // does a weight reach 2^15 (or is it no number)?  or has the row no reference?
           const bool grow = fresh || ((most + 0x08000800u) & 0x80008000u) != 0;
@@ -1073,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
             tmem_ld16(s_col + 16 * c, rr);
             const uint2 kc = ld_shared_v2(kinfo + 8 * (c >> 1)), vc = ld_shared_v2(vinfo + 8 * (c >> 1));
             tmem_wait_ld();
-            exponents(c, rr, kc, __uint_as_float(vc.x), x);
+            exponents(std::true_type(), c, rr, kc, __uint_as_float(vc.x), x);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) top = max3(top, x[e], x[e + 1]);
           }
