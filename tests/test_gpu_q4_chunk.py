@@ -525,6 +525,38 @@ def test_prefix_nan_and_queries_that_are_no_numbers(B, shared):
     assert torch.isnan(got[others][..., 96:]).all() and torch.isfinite(got[others][..., :96]).all()
 
 
+@pytest.mark.parametrize("dtype,m,B", [("bf16", 40, 64), ("bf16", 3, 4), ("f32", 3, 4)])
+def test_pages_past_four_gigabytes(dtype, m, B):
+    """The same rows in a small cache and in the last pages of one of 4.6 GB."""
+    H, Hq, d, page, shared, far = 8, 32, 128, 256, 16, 13900
+    one = plsh.q4_cache_bytes(1, H, page, d)
+    g = torch.Generator("cuda").manual_seed(3)
+    prefix = torch.randperm(shared, device="cuda", generator=g).to(torch.int32)
+    own = shared + torch.randperm(B, device="cuda", generator=g).to(torch.int32)
+    table = torch.cat([prefix.expand(B, -1), own[:, None]], 1).contiguous()
+    P = shared * page
+    k, v = (torch.randn(1, H, P, d, device="cuda", generator=g) for _ in range(2))
+    ko, vo = (torch.randn(B, H, 50, d, device="cuda", generator=g) for _ in range(2))
+    q = torch.randn(B, Hq, 1, d, device="cuda", generator=g).to(DT[dtype])
+    qc = torch.randn(2, Hq, m, d, device="cuda", generator=g).to(DT[dtype])
+    pos = i32([P + (13 * b) % 50 for b in range(B)])
+    outs = []
+    for base in (0, far):
+        data = torch.zeros((base + shared + B) * one, dtype=torch.uint8, device="cuda")
+        at = plsh.Q4Cache(data, table + base, H, d, page)
+        whole = plsh.Q4Cache(data, (prefix + base)[None].contiguous(), H, d, page)
+        plsh.q4_cache_write(whole, k, v, i32([0]))
+        plsh.q4_cache_write(at, ko, vo, i32([P] * B))
+        two = plsh.Q4Cache(data, (table[:2] + base).contiguous(), H, d, page)
+        sig = np.full(Hq, 2000.0)
+        outs.append((plsh.alibi_exact_prefix_decode_q4(q, at, sig, pos, prefix + base),
+                     plsh.alibi_exact_chunk_q4(qc, two, sig, i32([P + 50 - m, 100]))))
+        plsh.stream_status()
+        del data, at, whole, two
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert all(torch.isfinite(o).all() and (o != 0).any() for pair in outs for o in pair)
+
+
 @pytest.mark.parametrize("B,shared", [(64, 390), (6, 3)])
 def test_prefix_streams_graphs_and_workspaces(B, shared):
     """Captured, replayed at other positions on two streams at once, beside the same
