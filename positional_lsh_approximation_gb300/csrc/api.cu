@@ -1425,23 +1425,23 @@ plsh_status q4_slopes(const plsh_tensor* q, const double* sigma_h, float* slopes
 // Whether a chunk's rows, or the rows behind a prefix, may go to the tensor cores, and
 // whether they do.  The decode step's kernel reads a KV head's keys once for eight
 // columns (a chunk's tokens times query heads; one sequence of a prefix's), a pass; the
-// tensor cores' takes as long for up to 128 rows as the other for six passes, behind a
-// prefix seven.  us, decode step's and tensor cores': 64 sequences of 4096 positions, 8 KV
-// heads of 4 query heads: 4 passes 252 and 322, 6 passes 366 and 322, 16 passes 935 and
-// 332; one KV head of 8: 4 passes 45 and 57, 6 passes 60 and 57, 16 passes 133 and 61;
-// behind 65536 positions, 8 KV heads: 6 passes 81 and 89, 8 passes 104 and 90, 32 passes
-// 373 and 97.  It takes longer to begin (21 us and 10 at the least, behind a prefix 27
-// and 10), so there has to be work: passes x KV heads x positions.  A chunk's positions
-// are on the device, its table's length bounds them: 0.39 M (8 sequences of 1024
-// positions, 8 KV heads, 6 passes) take 31 and 31, 0.52 M (8 passes) 35 and 31; 0.26 M (64
-// sequences of 512, one KV head, 8 passes) 27 and 27, 0.52 M (16 passes) 41 and 27.
-// Behind a prefix: 0.52 M (4096 positions, 8 KV heads, 16 passes) 26 and 31, 1.05 M (32
-// passes) 39 and 34, but (16384 positions, 8 passes) 33 and 41; 4.2 M (65536 positions, 8
-// passes) 104 and 90.
+// tensor cores' takes as long for up to 128 rows as the other for five to six passes.
+// us, decode step's and tensor cores': 64 sequences of 4096 positions, 8 KV heads of 4
+// query heads: 4 passes 252 and 279, 6 passes 366 and 281, 16 passes 938 and 288; one KV
+// head of 8: 4 passes 45 and 54, 6 passes 61 and 55, 16 passes 133 and 56; behind 65536
+// positions, 8 KV heads: 4 passes 58 and 77, 6 passes 81 and 78, 8 passes 104 and 80.
+// It takes longer to begin (21 us and 10 at the least, behind a prefix 27 and 10), so
+// there has to be work: passes x KV heads x positions.  A chunk's positions are on the
+// device, its table's length bounds them: 0.39 M (8 sequences of 1024 positions, 8 KV
+// heads, 6 passes) take 31 and 33, 0.52 M (8 passes) 35 and 33; 0.26 M (64 sequences of
+// 512, one KV head, 8 passes) 27 and 25, 0.52 M (16 passes) 41 and 27.  Behind a prefix:
+// 0.52 M (4096 positions, 8 KV heads, 16 passes) 26 and 29, 1.05 M (32 passes) 39 and
+// 33, but (16384 positions, 8 passes) 33 and 41; 4.2 M (65536 positions, 8 passes) 104
+// and 80.
 bool q4_may_be_many(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix, double* passes) {
   const int64_t G = q->H / c.H, each = G > 4 || prefix ? 1 : 8 / G;      // tokens of a pass
   *passes = (double)((G + 7) / 8) * (double)(prefix ? q->B : (q->n + each - 1) / each);
-  return q->dtype == PLSH_BF16 && *passes >= (prefix ? 7 : 6);
+  return q->dtype == PLSH_BF16 && *passes >= 6;
 }
 bool q4_many(const plsh_tensor* q, const plsh::Q4Cache& c, int64_t prefix_pages) {
   const bool prefix = prefix_pages > 0;
