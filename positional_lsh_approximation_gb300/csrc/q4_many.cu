@@ -560,7 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         return __all_sync(FULL, mbar_wait(bar(k), parity, abort, lim));
       };
       bool ok = true;
-      uint32_t g = 0, gb = 0, seq = 0;           // steps, steps with both tiles, items
+      // steps, steps with both tiles; items, items with both tiles (an item that leaves
+      // the second tile out completes no phase of that tile's barriers)
+      uint32_t g = 0, gb = 0, seq = 0, seqb = 0;
       int jj = 0, steps = 0;                     // step of the item, its steps (0: the end)
       bool two = false, ptwo = false, pfirst = false, plast = false;      // p: of the step before
       auto next_item = [&]() {
@@ -608,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           if (plast) ++done;
         }
         if (two) {
-          ok = jj > 0 || wait(B_QFULL + 1, seq & 1u);
+          if (jj == 0) ok = wait(B_QFULL + 1, seqb++ & 1u);
           if (!ok) break;
           tc_fence_after();
           issue_s(1, g & 1);
@@ -915,7 +917,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       if (!it.valid) break;
       const int row = it.row0 + tile * BM + r;
       if (tile == 1 && it.row1 - it.row0 <= BM) {
-        mbar_arrive(bar(B_QFULL + 1));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_IEMPTY + islot));
         g += it.k1 - it.k0;
