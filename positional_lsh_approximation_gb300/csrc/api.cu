@@ -74,8 +74,8 @@ plsh::DeviceCtx g_ctx[kMaxDevices];
 
 // Fault injection for the tests, from the environment: PLSH_FAULT=oom fails
 // every device allocation; PLSH_FAULT=stall makes the next tensor-core
-// attention publish no work item, so every device-side wait runs out (with
-// nothing in flight) and the error flag reports PLSH_ERR_TIMEOUT.
+// attention (over a 4-bit cache too) publish no work item, so every device-side
+// wait runs out (with nothing in flight) and the error flag reports PLSH_ERR_TIMEOUT.
 bool fault_is(const char* what) {
   const char* f = getenv("PLSH_FAULT");
   return f != nullptr && strcmp(f, what) == 0;
@@ -1502,6 +1502,7 @@ plsh_status q4_rows_step(const plsh_tensor* q, const plsh_q4_cache* cache, const
   a.prefix = prefix;
   a.prefix_pages = (int)prefix_pages;
   a.wait_ns = ctx->wait_ns;
+  a.stall = fault_is("stall") ? 1 : 0;
   if (!q4_many(q, a.c, prefix_pages))
     PLSH_TRY_CUDA(plsh::launch_q4_decode(a, cs), "4-bit decode launch");
   else if (prefix == nullptr)

@@ -502,12 +502,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       // let every copy this warp started land before the CTA can exit
       if (q_issued) {
-        mbar_wait(bar(B_QFULL + 0), (uint32_t)(q_issued - 1) & 1u, nullptr, lim);
-        mbar_wait(bar(B_QFULL + 1), (uint32_t)(q_issued - 1) & 1u, nullptr, lim);
+        mbar_drain(bar(B_QFULL + 0), (uint32_t)(q_issued - 1) & 1u);
+        mbar_drain(bar(B_QFULL + 1), (uint32_t)(q_issued - 1) & 1u);
       }
       for (uint32_t sl = 0; sl < nslots; ++sl)
         if (kv_issued[sl])
-          mbar_wait(bar(B_KVFULL + sl), (uint32_t)(kv_issued[sl] - 1) & 1u, nullptr, lim);
+          mbar_drain(bar(B_KVFULL + sl), (uint32_t)(kv_issued[sl] - 1) & 1u);
     }
     __syncwarp();
   } else if (warp == kConvWarp) {
@@ -700,7 +700,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
       }
       // every MMA issued by this thread has completed once this arrives
       mma_commit(bar(B_DRAIN));
-      mbar_wait(bar(B_DRAIN), 0, nullptr, lim);
+      mbar_drain(bar(B_DRAIN), 0);
     }
     __syncwarp();
   } else {

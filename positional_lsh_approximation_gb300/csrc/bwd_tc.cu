@@ -484,10 +484,10 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     }
     // every copy this warp started lands before the CTA can exit
     if (lane == 0) {
-      if (nq0 > 0) mbar_wait(bar(B_QFULL), (uint32_t)(nq0 - 1) & 1u, nullptr, lim);
-      if (nq1 > 0) mbar_wait(bar(B_QFULL1), (uint32_t)(nq1 - 1) & 1u, nullptr, lim);
-      if (ndo > 0) mbar_wait(bar(B_DOFULL), (uint32_t)(ndo - 1) & 1u, nullptr, lim);
-      if (kv_loads > 0) mbar_wait(bar(B_KVFULL), (uint32_t)(kv_loads - 1) & 1u, nullptr, lim);
+      if (nq0 > 0) mbar_drain(bar(B_QFULL), (uint32_t)(nq0 - 1) & 1u);
+      if (nq1 > 0) mbar_drain(bar(B_QFULL1), (uint32_t)(nq1 - 1) & 1u);
+      if (ndo > 0) mbar_drain(bar(B_DOFULL), (uint32_t)(ndo - 1) & 1u);
+      if (kv_loads > 0) mbar_drain(bar(B_KVFULL), (uint32_t)(kv_loads - 1) & 1u);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -585,7 +585,7 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         atomicOr(p.err, 1);
       }
       mma_commit(bar(B_DRAIN));
-      mbar_wait(bar(B_DRAIN), 0, nullptr, lim);
+      mbar_drain(bar(B_DRAIN), 0);
     }
     __syncwarp();
   } else {

@@ -344,7 +344,7 @@ decode_group_kernel(const __grid_constant__ CUtensorMap tmK, DecodeParams p) {
     // memory goes away
     if (warp == 0) {
       for (int k = blk; k < issued; ++k)
-        mbar_wait(smem_u32(&full[k & 1]), (uint32_t)(k >> 1) & 1u, no_abort, p.wait_ns);
+        mbar_drain(smem_u32(&full[k & 1]), (uint32_t)(k >> 1) & 1u);
       if (lane == 0) atomicOr(p.err, 1);
     }
     return;

@@ -324,6 +324,7 @@ struct Q4DecodeArgs {
   int prefix_pages = 0;
   int4* rows = nullptr;
   uint64_t wait_ns = 0;    // q4_many.cu
+  int stall = 0;           // q4_many.cu, fault injection: no item is listed
 };
 int64_t q4_decode_work_bytes(int d, int num_sms);
 // the workspace of `rows`, and its pieces

@@ -161,6 +161,7 @@ struct ManyParams {
   float* part;                          // pieces: o [D / 4][256][4], maximum [256], sum [256]
   int* err;
   uint64_t wait_ns;
+  int stall;                            // fault injection: no item is listed
   float slope[kMaxExactHeads];          // log2(e) / sigma_h
 };
 
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       __syncwarp();
       ++seq;
     };
-    if (begin < end) {
+    if (begin < end && !p.stall) {
       int e = (int)ctl->found[0], kvh = (int)(begin / total);
       int64_t base = (int64_t)kvh * total + ctl->found[1];
       for (int64_t f = begin; ok && f < end;) {
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         slot = 2 * blockIdx.x + 1;
       }
     }
-    if (ok) publish(Item{});
+    if (ok && !p.stall) publish(Item{});
     if (!ok && lane == 0) {
       *abort = 1;
       atomicOr(p.err, kErrTimeout);
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       }
       // every product of this thread has completed once this arrives
       commit(lead, bar(B_DRAIN));
-      mbar_wait(bar(B_DRAIN), 0, nullptr, lim);
+      mbar_drain(bar(B_DRAIN), 0);
     }
     __syncwarp();
   }
@@ -1439,6 +1440,7 @@ void fill(ManyParams& p, const Q4DecodeArgs& a, void* work) {
   p.part = reinterpret_cast<float*>(p.ends + a.num_sms);
   p.err = a.err;
   p.wait_ns = a.wait_ns;
+  p.stall = a.stall;
   for (int h = 0; h < a.Hq; ++h) p.slope[h] = a.slope_log2[h];
 }
 

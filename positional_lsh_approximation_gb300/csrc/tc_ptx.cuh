@@ -65,6 +65,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// A wait for what the CTA itself has in flight, which ends by itself: as long as it
+// takes, whatever limit the other waits were given, so that no tensor memory is freed
+// under products still running (bounded all the same).
+constexpr uint64_t kDrainNs = 2000000000ull;
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  mbar_wait(bar, parity, nullptr, kDrainNs);
+}
+
 __device__ __forceinline__ void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
