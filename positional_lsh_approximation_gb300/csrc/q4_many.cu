@@ -160,7 +160,7 @@ struct ManyParams {
   int4* ends;                           // chunk: per CTA {item, first CTA, first piece} that ends in it
   float* part;                          // pieces: o [D / 4][256][4], maximum [256], sum [256]
   int* err;
-  uint64_t wait_ns;
+  uint64_t wait_ns, item_wait_ns;       // of a step's waits, of an item's
   int stall;                            // fault injection: no item is listed
   float slope[kMaxExactHeads];          // log2(e) / sigma_h
 };
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
   Ctl<D>* ctl = reinterpret_cast<Ctl<D>*>(smem_raw + (sbase - raw_u32) + S::kEnd);
   auto bar = [&](int k) { return smem_u32(&ctl->bars[k]); };
   volatile int* abort = &ctl->abort;
-  const uint64_t lim = p.wait_ns;
+  const uint64_t lim = p.wait_ns, item_lim = p.item_wait_ns;
 
   if (tid == 0) {
     for (int k = 0; k < 2; ++k) {
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     int seq = 0, slot = 2 * blockIdx.x;
     auto publish = [&](const Item& it) {
       const int s = seq & 1;
-      ok = __all_sync(FULL, mbar_wait(bar(B_IEMPTY + s), ((uint32_t)(seq >> 1) & 1u) ^ 1u, abort, lim * kItemWaits));
+      ok = __all_sync(FULL, mbar_wait(bar(B_IEMPTY + s), ((uint32_t)(seq >> 1) & 1u) ^ 1u, abort, item_lim));
       if (ok && lane == 0) {
         volatile int* v = reinterpret_cast<volatile int*>(&ctl->ring[s]);
         v[0] = it.valid; v[1] = it.b; v[2] = it.kvh; v[3] = it.row0; v[4] = it.row1;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       int jj = 0, steps = 0;                     // step of the item, its steps (0: the end)
       bool two = false, ptwo = false, pfirst = false, plast = false;      // p: of the step before
       auto next_item = [&]() {
-        ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + (seq & 1)), (seq >> 1) & 1u, abort, lim * kItemWaits));
+        ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + (seq & 1)), (seq >> 1) & 1u, abort, item_lim));
         const volatile Item& it = ctl->ring[seq & 1];
         steps = __shfl_sync(FULL, ok && it.valid ? it.k1 - it.k0 : 0, 0);
         two = __shfl_sync(FULL, it.row1 - it.row0, 0) > BM;
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     float unit[Y];                       // 2^-R_y
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim * kItemWaits);
+      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, item_lim);
       ok = barrier_and(BAR_V, kDeqThreads, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     int g = 0;
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
-      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim * kItemWaits));
+      ok = __all_sync(FULL, mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, item_lim));
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       const int islot = seq & 1;
       // (whether a wait ran out is told to the two warps of a row, which alone share
       // barriers without a limit, before either leaves)
-      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, lim * kItemWaits);
+      ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, item_lim);
       ok = barrier_and(pair, 64, ok);
       if (!ok) break;
       const Item it = read_item(ctl->ring, islot);
@@ -1440,6 +1440,7 @@ void fill(ManyParams& p, const Q4DecodeArgs& a, void* work) {
   p.part = reinterpret_cast<float*>(p.ends + a.num_sms);
   p.err = a.err;
   p.wait_ns = a.wait_ns;
+  p.item_wait_ns = std::min(a.wait_ns, UINT64_MAX / kItemWaits) * kItemWaits;
   p.stall = a.stall;
   for (int h = 0; h < a.Hq; ++h) p.slope[h] = a.slope_log2[h];
 }

@@ -103,3 +103,20 @@ def test_waits_that_give_up_at_once_leave_the_next_call_right(call, d):
             plsh.set_wait_limit_ns(0)
         assert torch.equal(f(), want)
         plsh.stream_status()
+
+
+@pytest.mark.parametrize("limit", [2 ** 58, 2 ** 63, 2 ** 64 - 1])
+@pytest.mark.parametrize("call", [chunk_call, prefix_call])
+def test_a_limit_that_nothing_reaches(call, limit):
+    """An item's waits have 64 times a step's limit: of the largest limits, no less."""
+    f = call(128)
+    want = f()
+    plsh.stream_status()
+    plsh.set_wait_limit_ns(limit)
+    try:
+        for _ in range(3):
+            got = f()
+            plsh.stream_status()
+            assert torch.equal(got, want)
+    finally:
+        plsh.set_wait_limit_ns(0)
