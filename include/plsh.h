@@ -603,15 +603,23 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  *
  * bf16 calls of many rows (decided by sizes alone: tokens and query heads of a KV
  * head, and the table's length) run on the tensor cores with the cached values
- * themselves in f16: q, k and v are rounded to 2^-11 of themselves under powers of
- * two that put the largest of a KV head's next 128 rows of q, of 32 positions of K,
- * and of 32 positions of V (relative to the sizes of their groups of 32 in the
- * newest keys) just below 2^15, no finer than 2^-24; weights to 2^-11 of
- * themselves, no finer than 2^-24 of about the row's largest.  So a key or a value
- * 2^29 times the others takes precision from the 31 positions beside it alone.  A
- * group of V more than 2^48 times what the newest keys' steps hold (of those that
- * one thread block attends over) is reported as PLSH_ERR_RANGE by
- * plsh_stream_status, and o is then not to be used.
+ * themselves in f16: q, k and v are rounded to 2^-11 of themselves, but
+ *   q  no finer than 2^-39 of the largest of a KV head's next 128 rows (the rows of a
+ *      chunk by token, then query head; behind a prefix, by sequence);
+ *   k  no finer than 2^-39 of the largest of its 32 positions (from a multiple of 32);
+ *   v  no finer than 2^-27 of the largest of its group of 32 values in its 32
+ *      positions, and 2^-37 of that in its step of 128 positions;
+ *   weights  no finer than 2^-20 of the row's largest (2^(k - 20) in 32 positions
+ *      that are 2^k times smaller than others in all their groups).
+ * So a key 2^28 times the others takes precision (more than bf16's own 2^-8 of their
+ * scores' terms) from the 31 positions beside it, and a group of V 2^18 times the
+ * others from the same group of these, and no value from other groups or steps.
+ * Where a group of V of 32 positions would keep no 2^-8 of itself, which is when a
+ * step's groups of 32 positions, each divided by the largest of its group in the step,
+ * differ by more than 2^31 within 32 positions (a position that is large in all its
+ * groups alike does not count: up to 2^79 between positions, 2^151 between steps), the
+ * call is reported as PLSH_ERR_RANGE by plsh_stream_status, and o is then not to be
+ * used.
  */
 plsh_status plsh_alibi_exact_chunk_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
                                       const double* sigma_h, const int32_t* pos, const int32_t* len,
@@ -644,8 +652,8 @@ plsh_status plsh_alibi_exact_prefix_decode_q4(const plsh_tensor* q, const plsh_q
 /* Synchronises `stream`, then reports CUDA errors and the library's device
  * error flag, clearing the flag: PLSH_ERR_TIMEOUT when a bounded device wait
  * ran out, else PLSH_ERR_RANGE when a tensor-core attention call met a value
- * of V beyond +-65504 (over a 4-bit cache: beyond what plsh_alibi_exact_chunk_q4
- * says), else PLSH_ERR_INVALID when a call on a 4-bit cache met
+ * of V beyond +-65504 (over a 4-bit cache: values as far apart as
+ * plsh_alibi_exact_chunk_q4 says), else PLSH_ERR_INVALID when a call on a 4-bit cache met
  * a position or a page index out of range. */
 plsh_status plsh_stream_status(void* stream);
 

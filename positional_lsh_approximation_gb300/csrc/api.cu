@@ -577,14 +577,15 @@ bool tc_path_ok(int dtype, int64_t d, int s, int causal, int exact) {
          plsh::attn_tc_smem_bytes(s, causal, exact) <= 232448;
 }
 
-// Status of the device error word: bit 0 a bounded wait ran out, bit 1 a
-// value of V beyond f16's range on the tensor-core path, bit 2 a position or
+// Status of the device error word: bit 0 a bounded wait ran out, bit 1
+// values of V beyond f16's range on the tensor-core path, bit 2 a position or
 // page index of a 4-bit cache out of range.
 plsh_status device_flag_status(int flag) {
   if (flag & 1) return fail(PLSH_ERR_TIMEOUT, "a device-side wait ran out of time");
   if (flag & 2)
     return fail(PLSH_ERR_RANGE, "V holds a value beyond +-65504, which the tensor-core path "
-                                "takes in f16 (scale V down by a power of two: O scales with it)");
+                                "takes in f16 (scale V down by a power of two: O scales with it); or, over a "
+                                "4-bit cache, groups of 32 values too far apart for it within 128 positions");
   if (flag & plsh::kErrCachePlace)
     return fail(PLSH_ERR_INVALID, "a position or a page index of a 4-bit cache is out of range");
   return PLSH_OK;

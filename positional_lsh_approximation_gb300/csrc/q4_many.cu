@@ -17,12 +17,17 @@
 //   q  times one per tile of 128 rows, the largest magnitude in [2^14, 2^15);
 //   K  times one per 32 positions, likewise: undone in the fp32 scores (with q's, and
 //      log2(e) / sqrt(d));
-//   V  times one per group of 32 values, R_y, by the first step of a piece (undone in
-//      the epilogue), and one per 32 positions, 2^-ev, by how far any group exceeds
-//      that or stays below it: likewise.  2^ev goes into these positions' weights,
-//      P = 2^{x + ev - M} with M near the maximum of x + ev so far, so that a large
-//      value takes precision from others of its own 32 positions alone; the row sum
-//      takes P 2^-ev in fp32.
+//   V  times one per group of 32 values, 2^-R_y, the step's largest in that group
+//      (undone in the epilogue), and one per 32 positions, 2^-ev, by how far all their
+//      groups stay below that: likewise.  R_y stays while every group of every 32
+//      positions is within 2^-8 and 2^4 of it; else it moves, and O's columns of that
+//      group with it, as a row's O does with its reference: what is large in one
+//      group moves nothing of the others.  2^ev goes into these positions' weights,
+//      P = 2^{x + ev - M} with M near the maximum of x + ev so far; the row sum takes
+//      P 2^-ev in fp32.  ev is below 4 (values from 2^111 on aside), so a weight keeps
+//      2^-20 of the row's largest.  A value of V keeps 2^-37 of the largest of its
+//      group in the step, 2^-27 in its 32 positions; where a group of 32 positions
+//      keeps no 2^-8 of itself, the call is reported.
 // P and V are rounded to f16 (2^-11 of themselves): bf16's 2^-8 would show beside
 // the output's own rounding.  Scores, sums and maxima are fp32.
 //
@@ -100,6 +105,12 @@ constexpr uint32_t kColP = 64, kColO = 256;
 // ends when a step's wait ran out: its limit is this many of theirs.
 constexpr uint64_t kItemWaits = 64;
 constexpr float kGrowLog2 = 15.f;       // largest weight 2^15: above, the reference moves
+// V's groups within 2^-8 and 2^4 of R_y leave it where it is; R_y comes down to 2^-72 of
+// an item's largest at most (O, below 2^30 of each key, goes up with it, and has to stay
+// a number for 2^24 keys); 32 positions' group 2^32 below where f16 has them and more
+// (its half step is 2^-39 of that) has lost 2^-8 of itself.
+constexpr float kVBelow = 0x1p-8f;
+constexpr int kVAbove = 4, kVSpan = 72, kVLost = 31, kNoGroup = -1000;
 constexpr float kNothing = -3.402823466e38f;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -135,10 +146,13 @@ struct Ctl {
   alignas(16) uint2 vq[Y][BN];
   // K and V run up to two steps ahead of the products, the softmax up to one behind
   alignas(16) uint2 kinfo[4][4];        // per step and 32 positions: K's factor, to be undone; positions that count
-  alignas(16) uint2 vinfo[4][4];        // V's exponent beyond R_y; 2^-that, negative where a group is no number
+  // V's exponent beyond R_y; 2^-that, negative for a step with either of:
+  alignas(16) uint2 vinfo[4][4];
   uint32_t vnan[4][Y][4];               // positions whose group of V is no number
+  int vmoved[4][4];                     // R_y moved: O's columns follow by these factors
+  float vscale[4][Y];
   int vr[2][Y];                         // per item slot: V's exponents R_y, less 14
-  int vmax[2][kDeqWarps][Y];
+  int vmax[kDeqWarps][Y], vhigh[Y];     // a step's exponents by 32 positions; the largest R_y of an item
   uint32_t qmax[2][8];
   float pair[2][2][BM];                 // per tile and half: what the two threads of a row tell each other
   int64_t sums[kWarps], found[2];
@@ -646,6 +660,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     bool ok = true, range = false;
     int g = 0;
     float unit[Y];                       // 2^-R_y
+#pragma unroll
+    for (int y = 0; y < Y; ++y) unit[y] = 1.f;
     for (int seq = 0; ok; ++seq) {
       const int islot = seq & 1;
       ok = mbar_wait(bar(B_IFULL + islot), (uint32_t)(seq >> 1) & 1u, abort, item_lim);
@@ -677,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
 #pragma unroll
         for (int y = 0; y < Y; ++y) vw[y] = pairs[y];
         int bad = 0;
+        uint32_t seen = 0;                   // groups that are not 0, and of these the ones within reach of R_y
         float top[Y], most = 0.f;            // largest magnitudes: of the groups, of all in units of 2^R_y
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
@@ -689,44 +706,73 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
             vw[y] = 0;
             top[y] = 0.f;
           }
+          const float r = top[y] * unit[y];
+          most = fmaxf(most, r);
+          if (top[y] > 0.f) seen |= (r >= kVBelow ? 0x101u : 0x100u) << y;
         }
+        // -- R_y: kept while every group of every 32 positions is near it, else moved
+        // to the step's largest (an item's first step takes this way always)
+        const bool first = s == it.k1 - 1;
+        uint32_t all = 0;
+        bool moved = false, near = false;
+        if (!first) {
+          all = __reduce_max_sync(FULL, __float_as_uint(most));
+          seen = __reduce_or_sync(FULL, seen);
+          near = (int)(all >> 23) - 127 < kVAbove && ((seen >> 8) & ~seen & 0xffu) == 0;
+          near = barrier_and(BAR_V, kDeqThreads, ok && near);
+        }
+        if (!near) {
+          int own[Y], high[Y];
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            top[y] = fmaxf(fabsf(pair_lo(vw[y])), fabsf(fmaf(15.f, pair_step(vw[y]), pair_lo(vw[y]))));
+            const uint32_t a = __reduce_max_sync(FULL, __float_as_uint(top[y]));
+            own[y] = a == 0 ? kNoGroup : max((int)(a >> 23) - 127, -100);
+            if (lane == 0) ctl->vmax[dw][y] = own[y];
+            high[y] = first ? kNoGroup : ctl->vhigh[y];
+          }
+          // (a wait that ran out is told to the other warps here, or behind the item)
+          ok = barrier_and(BAR_V, kDeqThreads, ok);
+          if (!ok) break;
+          int e[Y], base = kNoGroup;
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            e[y] = kNoGroup;
+#pragma unroll
+            for (int w = 0; w < kDeqWarps; ++w) e[y] = max(e[y], ctl->vmax[w][y]);
+            base = max(base, e[y]);
+          }
+          most = 0.f;
+#pragma unroll
+          for (int y = 0; y < Y; ++y) {
+            const int now = 127 - (int)(__float_as_uint(unit[y]) >> 23);
+            const int none = !first ? now : base == kNoGroup ? 0 : min(base, 110);
+            const int to = e[y] == kNoGroup ? none : min(max(e[y], high[y] - kVSpan), 110);
+            moved = moved || (!first && to != now);
+            if (t == 0) {
+              ctl->vr[islot][y] = to - 14;
+              ctl->vhigh[y] = e[y] == kNoGroup ? high[y] : max(high[y], to);
+              ctl->vscale[g & 3][y] = pow2(now - to);
+            }
+            unit[y] = pow2(-to);
+            most = fmaxf(most, top[y] * unit[y]);
+          }
+          all = __reduce_max_sync(FULL, __float_as_uint(most));
+          const int ev = all == 0 ? 0 : max(-48, min(48, (int)(all >> 23) - 127));
+#pragma unroll
+          for (int y = 0; y < Y; ++y)
+            range = range || (own[y] != kNoGroup && 127 - (int)(__float_as_uint(unit[y]) >> 23) + ev - own[y] > kVLost);
+        }
+        const int ev = all == 0 ? 0 : max(-48, min(48, (int)(all >> 23) - 127));
         const bool any_bad = __any_sync(FULL, bad != 0);
-        if (any_bad) {
+        if (any_bad || moved) {
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
             const uint32_t w = __ballot_sync(FULL, (bad >> y) & 1);
             if (lane == 0) ctl->vnan[g & 3][y][dw] = w;
           }
+          if (lane == 0) ctl->vmoved[g & 3][dw] = moved;
         }
-        // -- R_y from the item's first step, all four warps'
-        if (s == it.k1 - 1) {
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            const uint32_t a = __reduce_max_sync(FULL, __float_as_uint(top[y]));
-            if (lane == 0) ctl->vmax[islot][dw][y] = a == 0 ? -1000 : max((int)(a >> 23) - 127, -100);
-          }
-          ok = barrier_and(BAR_V, kDeqThreads, ok);
-          if (!ok) break;
-          int e[Y], base = -1000;
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            e[y] = -1000;
-#pragma unroll
-            for (int w = 0; w < kDeqWarps; ++w) e[y] = max(e[y], ctl->vmax[islot][w][y]);
-            base = max(base, e[y]);
-          }
-#pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            e[y] = min(base == -1000 ? 0 : e[y] == -1000 ? base : max(e[y], base - 48), 110);
-            if (t == 0) ctl->vr[islot][y] = e[y] - 14;
-            unit[y] = pow2(-e[y]);
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < Y; ++y) most = fmaxf(most, top[y] * unit[y]);
-        const uint32_t all = __reduce_max_sync(FULL, __float_as_uint(most));
-        const int e = (int)(all >> 23) - 127, ev = all == 0 ? 0 : max(-48, min(48, e));
-        range = range || e > 48;
         const float down = pow2(-ev), to = down * 0x1p14f;       // largest below 2^15
 #pragma unroll
         for (int y = 0; y < Y; ++y) {
@@ -734,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           ctl->vq[y][t] = make_uint2(pack_f16(vs, vs), pack_f16(vl, vl));
         }
         if (lane == 0)
-          ctl->vinfo[g & 3][dw] = make_uint2(__float_as_uint((float)ev), __float_as_uint(any_bad ? -down : down));
+          ctl->vinfo[g & 3][dw] = make_uint2(__float_as_uint((float)ev), __float_as_uint(any_bad || moved ? -down : down));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_INFO + (g & 3)));
         // -- a lane a quarter group of two neighbouring groups, four positions; the
@@ -779,11 +825,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_VREADY + st));
         }
-        if (!ok) break;
         if (s > it.k0) load(s - 1, ahead);
         ahead = src.entries(s - 2, it.k0);
       }
-      // (a wait that ran out is told to the others at the next item's first barrier)
       if (!ok && lane == 0) *abort = 1;
       ok = barrier_and(BAR_V, kDeqThreads, ok);
       if (!ok) break;
@@ -1006,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         // follow, and the weights are taken again (at the start of a piece, and where
         // scores jump).
         uint32_t pk[32], most;
-        int some_nan = 0;
+        int rare = 0;
         // exponents of sixteen keys, x + ev - mu, -inf where masked (if any are)
         auto exponents = [&](auto masked, int c, const uint32_t (&rr)[16], uint2 kq, float ev, float (&x)[16]) {
           const int jc = j0 + 16 * c;
@@ -1034,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           most = 0;
           sum = 0.f;
           const uint4 kk = ld_shared_v4(kinfo), vv = ld_shared_v4(vinfo);
-          some_nan = (int)(vv.y | vv.w);
+          rare = (int)(vv.y | vv.w);
           auto take = [&](auto masked) {
             uint32_t ra[16], rb[16];
             tmem_ld16(s_col, ra);
@@ -1111,14 +1155,29 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         }
         if (!ok) break;
         tmem_st32(p_col, pk);
-        if (some_nan < 0) {
+        if (rare < 0) {
           // (before the arrival: behind it the products may hand the step's slot on)
+          bool moved = false;
 #pragma unroll 1
           for (int q = 0; q < 2; ++q) {
-            if ((int)ld_shared_u32(vinfo + 8 * q + 4) >= 0) continue;      // a group of V that is no number
+            if ((int)ld_shared_u32(vinfo + 8 * q + 4) >= 0) continue;      // a group of V that is no number, or R_y moved
+            moved = moved || ctl->vmoved[g & 3][2 * half + q] != 0;
             const uint32_t vm = upto_mask(pos - j0 - 32 * q) & ld_shared_u32(kinfo + 8 * q + 4);
             for (int y = 0; y < Y; ++y)
               if (ctl->vnan[g & 3][y][2 * half + q] & vm) nan_groups |= 1 << y;
+          }
+          if (moved && s < it.k1 - 1) {
+            const int y = D == 64 ? 0 : 2 * half;          // (columns in turn, four of a group)
+            const float f0 = ctl->vscale[g & 3][y], f1 = ctl->vscale[g & 3][y + 1];
+#pragma unroll 1
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t o[16];
+              tmem_ld16(o_col + half * (D / 2) + k * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (e & 4 ? f1 : f0));
+              tmem_st16(o_col + half * (D / 2) + k * 16, o);
+            }
           }
         }
         l += sum;
