@@ -602,7 +602,7 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  * no effect on it.  Everything else as for plsh_alibi_exact_decode_q4.
  *
  * bf16 calls of many rows (decided by sizes alone: tokens and query heads of a KV
- * head, and the table's length) run on the tensor cores with the cached values
+ * head, and the table's length; and no sigma_h below 1.4e-6) run on the tensor cores with the cached values
  * themselves in f16: q, k and v are rounded to 2^-11 of themselves, but
  *   q  no finer than 2^-39 of the largest of a KV head's next 128 rows (the rows of a
  *      chunk by token, then query head; behind a prefix, by sequence);

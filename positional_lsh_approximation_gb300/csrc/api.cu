@@ -1504,7 +1504,14 @@ plsh_status q4_rows_step(const plsh_tensor* q, const plsh_q4_cache* cache, const
   a.prefix_pages = (int)prefix_pages;
   a.wait_ns = ctx->wait_ns;
   a.stall = fault_is("stall") ? 1 : 0;
-  if (!q4_many(q, a.c, prefix_pages))
+  // (The tensor cores' kernel adds up a row's bias in fp32, by 16 keys and with the
+  // reference that its weights are taken against: within 6 x 2^-20 slopes of what it is
+  // in powers of two, which is nothing beside the scores' own rounding while the slope
+  // is small, and scales the one weight that is left where it is not, up to slopes of
+  // 2^20, by 2^6 at most.  Steeper ones go where the bias is a product, and 0 at the
+  // row's own position.)
+  const bool steep = *std::max_element(slopes, slopes + q->H) > 0x1p20f;
+  if (steep || !q4_many(q, a.c, prefix_pages))
     PLSH_TRY_CUDA(plsh::launch_q4_decode(a, cs), "4-bit decode launch");
   else if (prefix == nullptr)
     PLSH_TRY_CUDA(plsh::launch_q4_chunk(a, cs), "4-bit chunk launch");

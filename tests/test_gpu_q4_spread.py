@@ -157,3 +157,35 @@ def test_what_cannot_be_held_is_refused_however_the_list_is_cut(B):
                 plsh.stream_status()
             assert e.value.status == plsh.PLSH_ERR_RANGE
         plsh.stream_status()
+
+
+@pytest.mark.parametrize("sigma", [0.05, 1e-4, 2e-6, 1.4e-6, 1e-6, 1e-8, 1e-9, 1e-35, 1e-300])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,wide", [(1, True), (300, True), (1, False)])
+def test_slopes_so_steep_that_a_row_is_its_own_value(B, wide, d, sigma):
+    """Rows at every alignment: o is v at the row's own position, but for its rounding
+    and those of V and of the one weight."""
+    s = Rows(B, 4, 1, d, 64, 400, "bf16", 150, wide=wide, seed=12)
+    pos = 217
+    got = plsh.alibi_exact_chunk_q4(s.q, s.cache, np.full(4, sigma), i32([pos] * B)).double().cpu().numpy()
+    plsh.stream_status()
+    for b in {0, B - 1}:
+        _, V = q4.read_sequence(s.host(), s.table[b], s.page, d, pos + 150)
+        want = V[:, pos:]
+        lost = np.abs(V).max() * 2.0 ** -18              # f16's step beside a step's largest value
+        assert (np.abs(got[b] - want) <= np.abs(want) * (2.0 ** -8 + 2 * 2.0 ** -11) + lost).all()
+
+
+@pytest.mark.parametrize("sigma", [2e-6, 1e-8, 1e-35])
+def test_steep_slopes_behind_a_prefix(sigma):
+    s = Shared(64, 4, 1, 128, 64, 390, 64, "bf16", seed=4)
+    pos = [s.P - 64 + 2 * b for b in range(64)]              # within, at its end and behind
+    got = plsh.alibi_exact_prefix_decode_q4(s.q, s.cache, np.full(4, sigma), i32(pos), s.d_prefix).double().cpu().numpy()
+    plsh.stream_status()
+    data = s.host()
+    _, Vp = q4.read_sequence(data, s.prefix, s.page, s.d, s.P)
+    for b in range(64):
+        _, V = q4.read_sequence(data, s.table[b, 390:], s.page, s.d, 64)
+        want = Vp[:, pos[b]] if pos[b] < s.P else V[:, pos[b] - s.P]
+        lost = np.abs(Vp).max() * 2.0 ** -18
+        assert (np.abs(got[b, :, 0] - want) <= np.abs(want) * (2.0 ** -8 + 2 * 2.0 ** -11) + lost).all(), b
