@@ -551,6 +551,9 @@ def alibi_exact_decode_q4(q, cache: Q4Cache, sigma, pos, out=None, work=None, st
                                           _f64(sigma).tobytes(), pos, out, work, _handle(stream))
 
 
+_rows_work: dict = {}                             # their workspaces, by device and stream
+
+
 def _work_bytes(fn, q, cache: Q4Cache) -> int:
     out, tq = ctypes.c_int64(), _desc(q)
     _check(fn(ctypes.byref(tq), ctypes.byref(cache._c), ctypes.byref(out)))
@@ -568,9 +571,12 @@ def alibi_exact_chunk_q4(q, cache: Q4Cache, sigma, pos, lens=None, out=None, wor
     (all m without lens) is at position pos[b] + i and sees every key up to it, the
     new tokens' own among them, which are written before.  A negative pos[b]: an
     idle slot, rows of 0.  Rows from lens[b] on keep what `out` holds; without it
-    they are 0.  `work`: device memory of q4_chunk_work_bytes (see
-    alibi_decode_q4)."""
-    return (_native or _binding()).chunk(cache._packed, cache.device_index, cache._work, q,
+    they are 0.  `work`: device memory of q4_chunk_work_bytes (40 MB where the tensor
+    cores are taken) that this call has for itself; without it all caches share one,
+    as large as a call needed so far, for each stream that is current when a call is
+    made, kept until the process ends; a call that is captured or given a stream
+    takes its own."""
+    return (_native or _binding()).chunk(cache._packed, cache.device_index, _rows_work, q,
                                          _f64(sigma).tobytes(), pos, lens, out, work, _handle(stream))
 
 
@@ -585,8 +591,8 @@ def alibi_exact_prefix_decode_q4(q, cache: Q4Cache, sigma, pos, prefix, out=None
     share their first positions: those below len(prefix) * page are read from the
     pages `prefix` (int32 on the device), the others through the cache's table as
     ever (its first len(prefix) entries are not read).  `work`: device memory of
-    q4_prefix_work_bytes (see alibi_decode_q4)."""
-    return (_native or _binding()).prefix_decode(cache._packed, cache.device_index, cache._work, q,
+    q4_prefix_work_bytes (see alibi_exact_chunk_q4, which it shares it with)."""
+    return (_native or _binding()).prefix_decode(cache._packed, cache.device_index, _rows_work, q,
                                                  _f64(sigma).tobytes(), pos, prefix, out, work,
                                                  _handle(stream))
 

@@ -288,16 +288,18 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The workspace of a chunk's or a prefix's call: as above, but in an entry of
-// `kept` of its own, replaced by a larger one when a call needs that.
+// The workspace of a chunk's or a prefix's call: as above, but `kept` is a dict that
+// all caches have in common, as this workspace is ten times as large (a device's
+// stream has one, whatever the layers of a model), and it is replaced by a larger one
+// when a call needs that.
 at::Tensor rows_workspace(const Call& c, const plsh_tensor& q, const at::Tensor& like, PyObject* kept,
-                          const char* name, WorkBytes need) {
+                          WorkBytes need) {
   int64_t bytes = 0;
   if (!ran([&] { return need(&q, &c.cache, &bytes); })) throw Refused("work");
   if (c.given.has_value() ||
       c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
     return new_workspace(c, bytes, like);
-  PyObject* key = Py_BuildValue("(sK)", name, (unsigned long long)(uintptr_t)c.stream());
+  PyObject* key = Py_BuildValue("(iK)", c.dev, (unsigned long long)(uintptr_t)c.stream());
   if (key == nullptr) throw Refused("stream handle");
   if (PyObject* have = PyDict_GetItemWithError(kept, key)) {
     const at::Tensor w = tensor(have, "work");
@@ -337,9 +339,8 @@ PyObject* rows_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
       len = a[6] == Py_None ? nullptr : indices(a[6], c.cache, c.dev, "lens");
     at::Tensor w;
     if (a[8] == Py_None) {
-      if (!PyDict_Check(a[2])) throw Refused("not a cache");
-      w = PREFIX ? rows_workspace(c, tq, q, a[2], "prefix", plsh_q4_prefix_work_bytes)
-                 : rows_workspace(c, tq, q, a[2], "chunk", plsh_q4_chunk_work_bytes);
+      if (!PyDict_Check(a[2])) throw Refused("not a dict of workspaces");
+      w = rows_workspace(c, tq, q, a[2], PREFIX ? plsh_q4_prefix_work_bytes : plsh_q4_chunk_work_bytes);
     } else {
       w = tensor(a[8], "work");
       on_device(w, c.dev, "work");
