@@ -92,7 +92,7 @@ constexpr int kSoftWarps = 16, kKWarp = 16, kVWarp = 20, kDeqWarps = 4, kMmaWarp
 constexpr int kThreads = 32 * kWarps, kDeqThreads = 32 * kDeqWarps, kTileThreads = 256;
 // of 896 threads' 72 at launch: 512 x 88 + 256 x 64 + 128 x 24 = 64512, all of them
 constexpr int kRegsSoftmax = 88, kRegsDeq = 64, kRegsRest = 24;
-enum { BAR_V = 1, BAR_PAIR = 2 };      // named barriers: V's warps, two warps of a row
+enum { BAR_V = 1, BAR_PAIR = 2, BAR_CODES = 10 };      // named barriers: V's warps, two warps of a row, K's and V's
 constexpr uint32_t kHalf = BM * 128;    // 128 rows of 64 f16 values, 128-byte swizzle
 // Steps that beginning and ending an item costs (a batch of eight ragged chunks: 2 ->
 // 293 us, 4 -> 266, 6 -> 248, 12 -> 250; 512 tokens behind 7680: 104, 100, 101, 107),
@@ -153,6 +153,7 @@ struct Ctl {
   float vscale[4][Y];
   int vr[2][Y];                         // per item slot: V's exponents R_y, less 14
   int vmax[kDeqWarps][Y], vhigh[Y];     // a step's exponents by 32 positions; the largest R_y of an item
+  alignas(16) int tops[2 * kDeqWarps];  // prefix: the furthest positions of any row
   uint32_t qmax[2][8];
   float pair[2][2][BM];                 // per tile and half: what the two threads of a row tell each other
   int64_t sums[kWarps], found[2];
@@ -334,6 +335,33 @@ __device__ __forceinline__ int tokens_of(const ManyParams& p, int b, int& pos) {
   pos = p.pos[b];
   const int n = p.len == nullptr ? p.m : max(0, min(p.len[b], p.m));
   return pos < 0 ? 0 : max(0, min(n, p.limit - pos));
+}
+
+// Prefix: the last position that any sequence of the batch has come to, found by the
+// warps that take codes apart while the list is made.  What lies behind it counts for
+// nothing, be it not written, not there or no number.
+template <int D>
+__device__ __forceinline__ void find_tops(const ManyParams& p, Ctl<D>* ctl) {
+  const int t = threadIdx.x - 32 * kKWarp;
+  int top = -1;
+#pragma unroll 4
+  for (int b = t; b < p.c.B; b += 2 * kDeqThreads) {
+    const int pos = p.pos[b];
+    if (pos < p.limit) top = max(top, pos);
+  }
+  top = __reduce_max_sync(FULL, top);
+  if ((t & 31) == 0) ctl->tops[t >> 5] = top;
+  barrier_or(BAR_CODES, 2 * kDeqThreads, false);
+}
+template <int D, bool PREFIX>
+__device__ __forceinline__ int last_seen(const Ctl<D>* ctl, int last) {
+  if constexpr (PREFIX) {
+    int top = -1;
+#pragma unroll
+    for (int w = 0; w < 2 * kDeqWarps; ++w) top = max(top, ctl->tops[w]);
+    last = min(last, top);
+  }
+  return last;
 }
 
 // Item t of entry e = (sequence, t): its rows, steps and last position.
@@ -657,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     leave_registers<kRegsDeq>();
     // ------------------------------------------------- V's codes into f16 tiles
     const int dw = warp - kVWarp, t = 32 * dw + lane;            // t: a position of the step
+    if constexpr (PREFIX) find_tops<D>(p, ctl);
     bool ok = true, range = false;
     int g = 0;
     float unit[Y];                       // 2^-R_y
@@ -670,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
       const Source<D, PREFIX> src(p, it, 32 * dw);
+      const int last = last_seen<D, PREFIX>(ctl, it.last);
       uint32_t pairs[Y], code[Y][4];       // of tile i / (Y / 2), groups 2 (i % (Y / 2)) and the next
       bool there;                          // whether this lane's position is
       const int pair_at = Layout<D>::kVPairs + Layout<D>::pair(lane & 15, 0);
@@ -688,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
         const int st = g & 1;
         // -- this position's pairs
-        const bool counts = BN * s + t <= it.last && there;
+        const bool counts = BN * s + t <= last && there;
         uint32_t vw[Y];
 #pragma unroll
         for (int y = 0; y < Y; ++y) vw[y] = pairs[y];
@@ -846,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
     // ------------------------------------------------- K's codes into f16 tiles
     // (a warp takes its own 32 positions apart: nothing to tell the others)
     const int dw = warp - kKWarp, t = 32 * dw + lane;
+    if constexpr (PREFIX) find_tops<D>(p, ctl);
     bool ok = true;
     int g = 0;
     for (int seq = 0; ok; ++seq) {
@@ -855,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       const Item it = read_item(ctl->ring, islot);
       if (!it.valid) break;
       const Source<D, PREFIX> src(p, it, 32 * dw);
+      const int last = last_seen<D, PREFIX>(ctl, it.last);
       // a lane a position and a quarter of each group; eight positions a turn, bit 2
       // of the position in bit 2 of the lane, so that eight lanes' stores lie in eight
       // different banks; two turns a tile
@@ -867,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         const uint8_t *t0 = src.tile(s, 0, e.x, h0), *t1 = src.tile(s, 1, e.y, h1);
         there = lane < 16 ? h0 : h1;
         // (pages that are needed and not there are told once, by K's warps)
-        if (!there && BN * s + t <= it.last) atomicOr(p.err, kErrCachePlace);
+        if (!there && BN * s + t <= last) atomicOr(p.err, kErrCachePlace);
         load_words<Y>((lane < 16 ? t0 : t1) + pair_at, kp);
         t0 += r8 * (D / 2) + u * (D / 8);
         t1 += r8 * (D / 2) + u * (D / 8);
@@ -878,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       int2 ahead = src.entries(it.k1 - 2, it.k0);
       for (int s = it.k1 - 1; s >= it.k0; --s, ++g) {
         const int st = g & 1, ring = g & 3;
-        const bool counts = BN * s + t <= it.last && there;
+        const bool counts = BN * s + t <= last && there;
         uint32_t kw[Y];
 #pragma unroll
         for (int y = 0; y < Y; ++y) kw[y] = kp[y];
