@@ -505,7 +505,8 @@ plsh_status plsh_q4_cache_read(const plsh_q4_cache* cache, const int32_t* pos,
  * A sequence with held[b] outside 0..max_pages, or that wants more than
  * max_pages, is left as it was; a free count outside 0..pool_pages counts as the
  * nearest, and pages pushed beyond pool_pages are dropped: each is reported as
- * PLSH_ERR_INVALID by plsh_stream_status.  The arrays must not overlap.
+ * PLSH_ERR_INVALID by plsh_stream_status.  The table, held and pool must overlap
+ * neither one another nor need and prefix (a prefix is a copy of a row's entries).
  * Asynchronous on `stream`; allocates nothing; may be captured.
  */
 plsh_status plsh_q4_cache_reserve(const plsh_q4_cache* cache, const int32_t* need, int32_t* held,

@@ -1598,6 +1598,16 @@ plsh_status plsh_q4_cache_reserve(const plsh_q4_cache* cache, const int32_t* nee
   if (prefix_pages < 0 || prefix_pages > cache->max_pages)
     return fail(PLSH_ERR_INVALID, "prefix_pages must be in [0, max_pages]");
   if (prefix_pages > 0 && prefix == nullptr) return fail(PLSH_ERR_INVALID, "prefix is NULL");
+  // (what is written, by many threads at once: the table, held and the pool)
+  const struct { const int32_t* p; int64_t n; } all[] = {{cache->table, cache->B * cache->max_pages},
+                                                         {held, cache->B}, {pool, 1 + pool_pages},
+                                                         {need, cache->B}, {prefix, prefix_pages}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 5; ++j) {
+      const uintptr_t x = (uintptr_t)all[i].p, y = (uintptr_t)all[j].p;
+      if (x < y + 4 * (uint64_t)all[j].n && y < x + 4 * (uint64_t)all[i].n && all[j].n > 0)
+        return fail(PLSH_ERR_INVALID, "the table, need, held, pool and prefix must not overlap");
+    }
   plsh::DeviceCtx* ctx = nullptr;
   if ((st = current_ctx(&ctx)) != PLSH_OK) return st;
   a.need = need;
