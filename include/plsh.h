@@ -520,7 +520,9 @@ plsh_status plsh_q4_cache_reserve(const plsh_q4_cache* cache, const int32_t* nee
  * token, its owner); -1 for rows from len[b] on, rows whose position is negative,
  * and rows whose page index is not in [0, pages).  A row whose position is not
  * below max_pages * page is -1 too and reported as PLSH_ERR_INVALID by
- * plsh_stream_status.
+ * plsh_stream_status.  Rows count by their own positions, as plsh_q4_cache_write and
+ * plsh_q4_cache_read take them: a negative pos[b] with several rows is no idle
+ * sequence here (its rows from position 0 on have slots); give that len 0.
  *   pos    device int32 [B];  len  device int32 [B] or NULL for m rows of each
  *   slots  device int64 [B, m], 16-byte aligned; B * m < 2^31 - 512
  * Asynchronous on `stream`; allocates nothing; may be captured.

@@ -515,7 +515,9 @@ def q4_cache_reserve(cache: Q4Cache, need, held, pool, prefix=None, stream=None)
 
 def q4_cache_slots(cache: Q4Cache, pos, lens=None, m: int | None = None, out=None, stream=None):
     """plsh_q4_cache_slots: int64 [B, m], the slot (page * page size + row) of
-    positions pos[b] + i, i < lens[b], of every sequence; -1 where there is none."""
+    positions pos[b] + i, i < lens[b], of every sequence; -1 where there is none
+    (an idle sequence has lens 0, as for q4_cache_write: a negative pos[b] leaves
+    only the rows before position 0 without a slot)."""
     if out is None:
         if m is None:
             raise ValueError("q4_cache_slots: give m, the rows of every sequence, or out")
