@@ -505,11 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       const int rows = p.len == nullptr ? p.m : max(0, min(p.len[b], p.m));
       if (n == rows) continue;
       if (pos >= 0 && tid == 0) atomicOr(p.err, kErrCachePlace);
-      const int vecs = (rows - n) * (D / 8);               // of a head
-      for (int64_t x = tid; x < (int64_t)vecs * p.Hq; x += kThreads) {
-        const int h = (int)(x / vecs), v = (int)(x - (int64_t)h * vecs);
+      const int64_t vecs = (int64_t)(rows - n) * (D / 8);     // of a head
+      for (int64_t x = tid; x < vecs * p.Hq; x += kThreads) {
+        const int64_t h = x / vecs, v = x - h * vecs;
         reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
-                                 (((int64_t)b * p.Hq + h) * p.m + n) * D)[v] = make_uint4(0, 0, 0, 0);
+                                 ((b * (int64_t)p.Hq + h) * p.m + n) * D)[v] = make_uint4(0, 0, 0, 0);
       }
     }
     __syncthreads();
