@@ -607,8 +607,7 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  * bf16 calls of many rows (decided by sizes alone: tokens and query heads of a KV
  * head, and the table's length; and no sigma_h below 1.4e-6) run on the tensor cores with the cached values
  * themselves in f16: q, k and v are rounded to 2^-11 of themselves, but
- *   q  no finer than 2^-39 of the largest of a KV head's next 128 rows (the rows of a
- *      chunk by token, then query head; behind a prefix, by sequence);
+ *   q  no finer than 2^-39 of the largest of its row;
  *   k  no finer than 2^-39 of the largest of its 32 positions (from a multiple of 32);
  *   v  no finer than 2^-27 of the largest of its group of 32 values in its 32
  *      positions, and 2^-37 of that in its step of 128 positions;

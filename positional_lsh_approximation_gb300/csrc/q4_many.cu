@@ -14,7 +14,7 @@
 // Numbers.  Codes are exact in f16, so a value lo + step c is rounded once, in one
 // f16 multiply-add (c is taken from the low bits of 1024 + c or 64 + c, exactly).
 // Powers of two keep everything within f16's range:
-//   q  times one per tile of 128 rows, the largest magnitude in [2^14, 2^15);
+//   q  times one per row, the largest magnitude in [2^14, 2^15);
 //   K  times one per 32 positions, likewise: undone in the fp32 scores (with q's, and
 //      log2(e) / sqrt(d));
 //   V  times one per group of 32 values, 2^-R_y, the step's largest in that group
@@ -126,7 +126,7 @@ struct Sizes {
 enum {
   B_IFULL = 0, B_IEMPTY = 2, B_VEMPTY = 4, B_VREADY = 6, B_INFO = 8, B_KREADY = 12,
   B_KEMPTY = 16, B_QFULL = 18, B_SFULL = 20, B_PFULL = 22, B_ODONE = 24,
-  B_DRAIN = 26, B_ROWS = 27, NUM_BARS = 29
+  B_DRAIN = 26, NUM_BARS = 27
 };
 
 // Rows [row0, row1) of a sequence's (or the batch's) rows of one KV head against the
@@ -154,7 +154,6 @@ struct Ctl {
   int vr[2][Y];                         // per item slot: V's exponents R_y, less 14
   int vmax[kDeqWarps][Y], vhigh[Y];     // a step's exponents by 32 positions; the largest R_y of an item
   alignas(16) int tops[2 * kDeqWarps];  // prefix: the furthest positions of any row
-  uint32_t qmax[2][8];
   float pair[2][2][BM];                 // per tile and half: what the two threads of a row tell each other
   int64_t sums[kWarps], found[2];
   uint32_t tmem_base;
@@ -420,7 +419,6 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
       mbar_init(bar(B_SFULL + k), 1);
       mbar_init(bar(B_PFULL + k), kTileThreads);
       mbar_init(bar(B_ODONE + k), 1);
-      mbar_init(bar(B_ROWS + k), kSoftWarps / 2);
     }
     for (int k = 0; k < 4; ++k) {
       mbar_init(bar(B_KREADY + k), kDeqWarps);
@@ -1023,19 +1021,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           mx = __vmaxu2(mx, qv[c].w & 0x7fff7fffu);
         }
         mx = max(mx & 0xffff0000u, mx << 16);
-        row_bad = mx >= (110u + 127u) << 23;             // 2^110, infinities, NaN
-        const uint32_t top = __reduce_max_sync(FULL, row_bad ? 0u : mx);
-        if (lane == 0) ctl->qmax[tile][warp & 7] = top;
-        ctl->pair[tile][half][r] = row_bad ? 1.f : 0.f;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_ROWS + tile));
-        ok = mbar_wait(bar(B_ROWS + tile), items & 1u, abort, lim);
+        // (each row's own: behind a prefix a tile's rows are several requests')
+        ctl->pair[tile][half][r] = __uint_as_float(mx);
         ok = barrier_and(pair, 64, ok);
-        row_bad = row_bad || ctl->pair[tile][half ^ 1][r] != 0.f;
-        uint32_t all = 0;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) all = max(all, ctl->qmax[tile][w]);
-        const int e = min(max((int)(all >> 23) - 127, -100), 110);
+        mx = max(mx, __float_as_uint(ctl->pair[tile][half ^ 1][r]));
+        row_bad = mx >= (110u + 127u) << 23;             // 2^110, infinities, NaN
+        const int e = min(max((int)(mx >> 23) - 127, -100), 110);
         const float up = row_bad ? 0.f : pow2(14 - e);
         qs = pow2(e - 14) * norm;
         const uint32_t dst = sbase + S::kQ + tile * S::kTileB + r * 128;
