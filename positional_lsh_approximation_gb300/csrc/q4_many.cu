@@ -750,46 +750,44 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           near = barrier_and(BAR_V, kDeqThreads, ok && near);
         }
         if (!near) {
-          int own[Y], high[Y];
+          // (lane y: group y)
+          const int y0 = lane & (Y - 1);
+          int own = kNoGroup, unit_of = 0;
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
             top[y] = fmaxf(fabsf(pair_lo(vw[y])), fabsf(fmaf(15.f, pair_step(vw[y]), pair_lo(vw[y]))));
             const uint32_t a = __reduce_max_sync(FULL, __float_as_uint(top[y]));
-            own[y] = a == 0 ? kNoGroup : max((int)(a >> 23) - 127, -100);
-            if (lane == 0) ctl->vmax[dw][y] = own[y];
-            high[y] = first ? kNoGroup : ctl->vhigh[y];
+            if (y0 == y) {
+              own = a == 0 ? kNoGroup : max((int)(a >> 23) - 127, -100);
+              unit_of = __float_as_int(unit[y]);
+            }
           }
+          if (lane < Y) ctl->vmax[dw][lane] = own;
+          const int high = first ? kNoGroup : ctl->vhigh[y0], now = 127 - (unit_of >> 23);
           // (a wait that ran out is told to the other warps here, or behind the item)
           ok = barrier_and(BAR_V, kDeqThreads, ok);
           if (!ok) break;
-          int e[Y], base = kNoGroup;
+          int e = kNoGroup;
 #pragma unroll
-          for (int y = 0; y < Y; ++y) {
-            e[y] = kNoGroup;
-#pragma unroll
-            for (int w = 0; w < kDeqWarps; ++w) e[y] = max(e[y], ctl->vmax[w][y]);
-            base = max(base, e[y]);
+          for (int w = 0; w < kDeqWarps; ++w) e = max(e, ctl->vmax[w][y0]);
+          const int base = __reduce_max_sync(FULL, e);
+          const int none = !first ? now : base == kNoGroup ? 0 : min(base, 110);
+          const int to = e == kNoGroup ? none : min(max(e, high - kVSpan), 110);
+          moved = __any_sync(FULL, !first && to != now);
+          if (t < Y) {
+            ctl->vr[islot][t] = to - 14;
+            ctl->vhigh[t] = e == kNoGroup ? high : max(high, to);
+            ctl->vscale[g & 3][t] = pow2(now - to);
           }
           most = 0.f;
 #pragma unroll
           for (int y = 0; y < Y; ++y) {
-            const int now = 127 - (int)(__float_as_uint(unit[y]) >> 23);
-            const int none = !first ? now : base == kNoGroup ? 0 : min(base, 110);
-            const int to = e[y] == kNoGroup ? none : min(max(e[y], high[y] - kVSpan), 110);
-            moved = moved || (!first && to != now);
-            if (t == 0) {
-              ctl->vr[islot][y] = to - 14;
-              ctl->vhigh[y] = e[y] == kNoGroup ? high[y] : max(high[y], to);
-              ctl->vscale[g & 3][y] = pow2(now - to);
-            }
-            unit[y] = pow2(-to);
+            unit[y] = pow2(-__shfl_sync(FULL, to, y));
             most = fmaxf(most, top[y] * unit[y]);
           }
           all = __reduce_max_sync(FULL, __float_as_uint(most));
           const int ev = all == 0 ? 0 : max(-48, min(48, (int)(all >> 23) - 127));
-#pragma unroll
-          for (int y = 0; y < Y; ++y)
-            range = range || (own[y] != kNoGroup && 127 - (int)(__float_as_uint(unit[y]) >> 23) + ev - own[y] > kVLost);
+          range = range || __any_sync(FULL, own != kNoGroup && to + ev - own > kVLost);
         }
         const int ev = all == 0 ? 0 : max(-48, min(48, (int)(all >> 23) - 127));
         const bool any_bad = __any_sync(FULL, bad != 0);
