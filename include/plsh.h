@@ -43,9 +43,10 @@ typedef enum {
   PLSH_ERR_NOMEM = 3,        /* device or host allocation failed            */
   PLSH_ERR_TIMEOUT = 4,      /* a device-side bounded wait ran out          */
   PLSH_ERR_UNSUPPORTED = 5,  /* valid request the library does not serve    */
-  PLSH_ERR_RANGE = 6         /* an input value beyond the range the kernel
+  PLSH_ERR_RANGE = 6         /* input values beyond the range the kernel
                                 computes in (V beyond +-65504 on the
-                                tensor-core path), found on the device      */
+                                tensor-core path; over a 4-bit cache V's
+                                groups too far apart), found on the device  */
 } plsh_status;
 
 /* Which kernel serves an attention call (plsh_attn_path). */
@@ -602,10 +603,12 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  * A row whose position is not below max_pages * page gives 0, and a key whose
  * page index is not in [0, pages) counts as absent; either is reported as
  * PLSH_ERR_INVALID by plsh_stream_status.  What lies behind a row's position has
- * no effect on it.  Everything else as for plsh_alibi_exact_decode_q4.
+ * no effect on it (what another row of the call sees there may take part in the
+ * powers of two below).  Everything else as for plsh_alibi_exact_decode_q4.
  *
  * bf16 calls of many rows (decided by sizes alone: tokens and query heads of a KV
- * head, and the table's length; and no sigma_h below 1.4e-6) run on the tensor cores with the cached values
+ * head, and the table's length, also where the sequences are far shorter than that;
+ * and no sigma_h below 1.4e-6) run on the tensor cores with the cached values
  * themselves in f16: q, k and v are rounded to 2^-11 of themselves, but
  *   q  no finer than 2^-39 of the largest of its row;
  *   k  no finer than 2^-39 of the largest of its 32 positions (from a multiple of 32);
@@ -642,8 +645,9 @@ plsh_status plsh_q4_prefix_work_bytes(const plsh_tensor* q, const plsh_q4_cache*
  *          plsh_alibi_decode_q4.
  * A sequence may be anywhere, within the prefix too (pos[b] negative: idle).
  * Everything else as for plsh_alibi_exact_decode_q4; bf16 calls of many sequences
- * behind a long prefix take the prefix's part on the tensor cores, as described at
- * plsh_alibi_exact_chunk_q4.
+ * behind a long prefix take the prefix's part on the tensor cores, once for all of
+ * them, as described at plsh_alibi_exact_chunk_q4; other calls read it once a
+ * sequence.  Positions of the prefix that no sequence has come to have no effect.
  */
 plsh_status plsh_alibi_exact_prefix_decode_q4(const plsh_tensor* q, const plsh_q4_cache* cache,
                                               const double* sigma_h, const int32_t* pos,

@@ -572,7 +572,8 @@ def alibi_exact_chunk_q4(q, cache: Q4Cache, sigma, pos, lens=None, out=None, wor
     sequence over the 4-bit cache, for the queries q [B, Hq, m, d]: row i < lens[b]
     (all m without lens) is at position pos[b] + i and sees every key up to it, the
     new tokens' own among them, which are written before.  A negative pos[b]: an
-    idle slot, rows of 0.  Rows from lens[b] on keep what `out` holds; without it
+    idle slot, rows of 0.  Values of V too far apart for the tensor cores are
+    reported by stream_status.  Rows from lens[b] on keep what `out` holds; without it
     they are 0.  `work`: device memory of q4_chunk_work_bytes (40 MB where the tensor
     cores are taken) that this call has for itself; without it all caches share one,
     as large as a call needed so far, for each stream that is current when a call is

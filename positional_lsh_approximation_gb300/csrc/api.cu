@@ -1433,12 +1433,16 @@ plsh_status q4_slopes(const plsh_tensor* q, const double* sigma_h, float* slopes
 // positions, 8 KV heads: 4 passes 58 and 77, 6 passes 81 and 78, 8 passes 104 and 80.
 // It takes longer to begin (21 us and 10 at the least, behind a prefix 27 and 10), so
 // there has to be work: passes x KV heads x positions.  A chunk's positions are on the
-// device, its table's length bounds them: 0.39 M (8 sequences of 1024 positions, 8 KV
+// device, and its table's length, which bounds them, stands for them: a short chunk in a
+// table for a long context goes to the tensor cores and pays for it (24 tokens at
+// position 300, 32/8 heads: 15.1 us, 22.5 in a table for 131072, where the decode step's
+// kernel takes 16.4; at position 976 18.4 and 24.6).  With tables as long as the
+// sequences: 0.39 M (8 sequences of 1024 positions, 8 KV
 // heads, 6 passes) take 31 and 33, 0.52 M (8 passes) 35 and 33; 0.26 M (64 sequences of
 // 512, one KV head, 8 passes) 27 and 25, 0.52 M (16 passes) 41 and 27.  Behind a prefix:
-// 0.52 M (4096 positions, 8 KV heads, 16 passes) 26 and 29, 1.05 M (32 passes) 39 and
-// 33, but (16384 positions, 8 passes) 33 and 41; 4.2 M (65536 positions, 8 passes) 104
-// and 80.
+// 0.52 M (4096 positions, 8 KV heads, 16 passes) 26 and 29, 1.05 M (32 passes) 37 and
+// 31 (on the wrong side of the rule), but (16384 positions, 8 passes) 33 and 41; 1.57 M
+// (4096, 48 passes) 51 and 37; 4.2 M (65536 positions, 8 passes) 104 and 80.
 bool q4_may_be_many(const plsh_tensor* q, const plsh::Q4Cache& c, bool prefix, double* passes) {
   const int64_t G = q->H / c.H, each = G > 4 || prefix ? 1 : 8 / G;      // tokens of a pass
   *passes = (double)((G + 7) / 8) * (double)(prefix ? q->B : (q->n + each - 1) / each);

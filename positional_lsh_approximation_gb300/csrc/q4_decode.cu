@@ -124,8 +124,9 @@ struct Slopes {
 //            sequence's rows as the eight columns hold (`tokens`) are one row of the
 //            flat list, column i G + h for head h of the i-th of them, and the keys'
 //            codes are taken apart once for all of them (64 sequences of 4096
-//            positions, 32/8 heads, 4 tokens: 211 -> 142 us; as a matter of kRows
-//            with one row of eight heads the columns' positions cost 7 %);
+//            positions, 32/8 heads, 4 tokens: 210 -> 137 us, 8 tokens 401 -> 252;
+//            as a matter of kRows with one row of eight heads the columns'
+//            positions cost 7 %);
 //   kShared  as kStep, the first pages being a prefix's that all sequences share;
 //   kOwn     as kStep, only the keys behind that prefix; rows are left as pieces,
 //            which a kernel elsewhere joins with the prefix's part.

@@ -43,30 +43,37 @@
 //
 // What bounds it.  The products of a step (two tiles) take 2048 cycles at 4096
 // multiply-adds a cycle.  Measured (CUDA graph, back to back; shares of the measured
-// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2430 us (1110
-// TFLOP/s, 58 %), 2.3 us a step; 512 tokens behind 7680, 32/8 heads, 95 us (26 steps
-// a CTA); a batch of eight ragged chunks 234 us; 128 sequences behind a prefix of
-// 65536, 40/8 heads, 239 us, 64 behind 8192, 32/8 heads, 51 us (four steps a CTA).
-// Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 33 %,
-// issue slots 54 %): a tile's steps follow one another through its scores (1000
+// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2280 us (1190
+// TFLOP/s, 62 %), 2.15 us a step; 512 tokens behind 7680, 32/8 heads, 91 us (26 steps
+// a CTA); a batch of eight ragged chunks 237 us; 128 sequences behind a prefix of
+// 65536, 40/8 heads, 219 us, 64 behind 8192, 32/8 heads, 50 us (four steps a CTA).
+// Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 36 %,
+// issue slots 55 %): a tile's steps follow one another through its scores (1000
 // cycles with P V before them), its softmax (2100 of weights, 500 until they are in
-// tensor memory) and the products' barriers, as P stands where its scores stood (S
-// and O of two tiles fill the tensor memory), and the two tiles' chains fill each
-// other's gaps in part.  Beginning an item costs more: 12000 cycles from its listing
-// to the first scores, where table, pages and queries come one after another from
-// memory not touched before, and 7000 for the first step, whose weights are taken
-// twice.
+// tensor memory) and the products' barriers, as P stands where its scores stood (with
+// steps of 128 keys S and O of two tiles fill the tensor memory; steps of 64 with two
+// buffers of scores a tile would fit, and are not tried), and the two tiles' chains
+// fill each other's gaps in part.  Beginning an item costs more: 12000 cycles from its
+// listing to the first scores, where table, pages and queries come one after another
+// from memory not touched before, and 7000 for the first step, whose weights are taken
+// twice.  (Cycles as stamped when a step took 4600; it takes 4200 now.)
 //
 // What it took (2048 behind 63488): one thread's product issue from a branch of its
 // own 3311 us, the whole warp's with a predicate 2835 (operands stay in uniform
 // registers); softmax by sixteen columns with the next ones' load in flight, V's
 // exponents from one reduction 2550; whether anything is masked decided once a step,
-// and registers given to the codes 2430.  Slower, and dropped: one thread a row
-// (3100), 80 registers for softmax (2770), scalar instead of paired fp32 multiply-adds
-// (+6 %), the first step's weights not tried before its maximum is known (+14 %, the
-// loop's code suffers), K's and V's next codes loaded while these are taken apart
-// (2415 to 2480, shorter items lose more), and for items of one tile the other tile on
-// every second step of the same keys (64 rows of 131072 keys: 146 -> 166 us).
+// and registers given to the codes 2430; V's exponents moving with the step (a barrier
+// of V's warps a step) 2360, q's by row 2465, the exponents by a lane a group 2280.
+// Slower, and dropped: one thread a row (3100), 80 registers for softmax (2770), scalar
+// instead of paired fp32 multiply-adds (+6 %), the first step's weights not tried
+// before its maximum is known (+14 %, the loop's code suffers), K's and V's next codes
+// loaded while these are taken apart (2415 to 2480, shorter items lose more), O
+// following V's exponents by V's warps behind the softmax (2590 to 2780) or at a step's
+// start (2590), the bias from positions instead of added up (2700), and for items of one
+// tile the other tile on every second step of the same keys (64 rows of 131072 keys:
+// 146 -> 166 us).  The softmax's 88 registers spill 84 to 132 bytes a thread (0.8 % of
+// the instructions of 512 behind 7680); which values, and with them 5 % of the time,
+// changes with the code around the loop.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -391,9 +398,6 @@ __device__ __forceinline__ int64_t row_at(const ManyParams& p, int b, int kvh, i
   pos = pos0 + i;
   return (((int64_t)b * p.Hq + h) * p.m + i) * D;
 }
-
-// Value of the row that column x of O stands for: columns 8 c .. 8 c + 7 are values
-// 4 g .. 4 g + 3 of groups y and y + 1, c = 4 y + g, in the order 0, 2, 1, 3.
 
 template <int D, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_constant__ ManyParams p) {
@@ -1233,7 +1237,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
         uint32_t o[32];
         tmem_ld32(o_col + q * 32, o);
         tmem_wait_ld();
-        // four quarter groups of groups y and y + 1
+        // columns 8 c .. 8 c + 7 of O are values 4 g .. 4 g + 3 of groups y and y + 1,
+        // c = 4 y + g, in the order 0, 2, 1, 3: here four quarters of each
         const int y = 2 * (q >> 1), g0 = 4 * (q & 1);
         float u0 = up[0], u1 = up[1];
         if constexpr (Y == 4) {

@@ -21,8 +21,10 @@
 // itself, the cluster's warps move the pages of a sequence each, and the cluster's
 // barrier stands between what is read and what is written over it.  Measured with the
 // slots of the new rows (requests taken back, made again, slots: three launches): 64
-// sequences growing by a token 8.9 us, 256 of which a quarter finish and a quarter bring prompts of up to 2048 tokens
-// 19.4 (4 MB of slots).
+// sequences growing by a token 8.8 us, 256 of which a quarter finish and a quarter
+// bring prompts of up to 2048 tokens 19.6 (4 MB of slots).  There each trip of the loops
+// that move a request's pages waits for the one before, as table and pool might be one
+// memory: 15 trips for a request of 460 pages.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -216,8 +218,9 @@ __global__ void __launch_bounds__(256) q4_slots_kernel(const __grid_constant__ Q
 
 cudaError_t launch_q4_reserve(const Q4ReserveArgs& a, cudaStream_t st) {
   // a CTA's 32 warps take a sequence each at a time; more CTAs where rows are
-  // many and long enough to pay for the cluster's barriers (256 rows of 512: 8 CTAs
-  // 22.5 us for two calls and the slots, 4 26.6, 1 30.7; 64 rows of 128: 1 CTA 10.3, 8 12.3)
+  // many and long enough to pay for the cluster's barriers (two calls and the slots in a
+  // graph: 256 rows of 512, a quarter coming and going: 8 CTAs 24.6 us, 4 26.7, 2 30.7,
+  // 1 34.9; 64 rows of 128 growing by a token: 1 CTA 10.3, 2 to 8 12.3)
   const int64_t pages = (int64_t)a.c.B * a.c.max_pages;
   unsigned cluster = 1;
   while (cluster < kMaxCluster && pages > (int64_t)cluster * 8192 && a.c.B > (int)cluster * kWarps) cluster *= 2;
