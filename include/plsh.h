@@ -616,9 +616,10 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  *      positions, and 2^-37 of that in its step of 128 positions;
  *   weights  no finer than 2^-20 of the row's largest (2^(k - 20) in 32 positions
  *      that are 2^k times smaller than others in all their groups).
- * So a key 2^28 times the others takes precision (more than bf16's own 2^-8 of their
- * scores' terms) from the 31 positions beside it, and a group of V 2^18 times the
- * others from the same group of these, and no value from other groups or steps.
+ * So a key 2^31 times the others, or a group of V 2^19 times the others, leaves the 31
+ * positions beside it (of V: the same group of theirs; 2^29 times: of the other 96 of
+ * the step) precise to 2^-8 of themselves, and less where it is larger still; no value
+ * takes anything from other groups or steps.
  * Where a group of V of 32 positions would keep no 2^-8 of itself, which is when a
  * step's groups of 32 positions, each divided by the largest of its group in the step,
  * differ by more than 2^31 within 32 positions (a position that is large in all its
