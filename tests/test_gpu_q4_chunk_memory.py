@@ -75,3 +75,37 @@ def test_a_small_call_then_a_large_one_on_two_streams():
     for g, w in zip(got, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
     plsh.stream_status()
+
+
+def test_threads_that_share_a_stream_share_its_workspace():
+    """Two caches' calls of different sizes from two threads, on one stream: the calls'
+    launches stay together, whoever's workspace was there first."""
+    import threading
+    caches = list(layers(2))
+    for c in caches:
+        k, v = torch.randn(2, 64, 2, 32, 128, device="cuda")
+        for at in range(0, 3200, 320):
+            plsh.q4_cache_write(c, k, v, i32([at] * 64))
+    sigma, pos = np.full(8, 100.0), i32(np.arange(64) * 50)
+    qs = [torch.randn(64, 8, m, 128, device="cuda").bfloat16() for m in (16, 2)]
+    want = [plsh.alibi_exact_chunk_q4(q, c, sigma, pos) for q, c in zip(qs, caches)]
+    torch.cuda.synchronize()
+    side, got, failed = torch.cuda.Stream(), [[], []], []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(side):
+                for _ in range(60):
+                    got[i].append(plsh.alibi_exact_chunk_q4(qs[i], caches[i], sigma, pos))
+        except Exception as e:                       # noqa: BLE001 (told to the test's own thread)
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for i in range(2):
+        assert len(got[i]) == 60 and all(torch.equal(g, want[i]) for g in got[i])
+    plsh.stream_status()
