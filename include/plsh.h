@@ -612,15 +612,16 @@ plsh_status plsh_q4_chunk_work_bytes(const plsh_tensor* q, const plsh_q4_cache* 
  * themselves in f16: q, k and v are rounded to 2^-11 of themselves, but
  *   q  no finer than 2^-39 of the largest of its row;
  *   k  no finer than 2^-39 of the largest of its 32 positions (from a multiple of 32);
- *   v  no finer than 2^-27 of the largest of its group of 32 values in its 32
- *      positions, and 2^-37 of that in its step of 128 positions;
- *   weights  no finer than 2^-20 of the row's largest (2^(k - 20) in 32 positions
- *      that are 2^k times smaller than others in all their groups).
- * So a key 2^31 times the others, or a group of V 2^19 times the others, leaves the 31
- * positions beside it (of V: the same group of theirs; 2^29 times: of the other 96 of
- * the step) precise to 2^-8 of themselves, and less where it is larger still; no value
- * takes anything from other groups or steps.
- * Where a group of V of 32 positions would keep no 2^-8 of itself, which is when a
+ *   v  no finer than 2^-24 of the largest of its group of 32 values in its 32
+ *      positions;
+ *   weights  no finer than 2^-14 of the row's largest, and 2^-22 where a group of the
+ *      position's value is 2^15 times others of the group and more (2^-25 and 2^-33
+ *      unless such a position has the row's largest; 2^k times less fine in 32
+ *      positions that are 2^k times smaller than others in all their groups).
+ * So a key 2^31 times the others, or a group of V 2^16 times the others, leaves the 31
+ * positions beside it (of V: the same group of theirs) precise to 2^-8 of themselves,
+ * and less where it is larger still; no value takes that from other groups or positions.
+ * Where a group of V of 32 positions would keep no 2^-14 of itself, which is when a
  * step's groups of 32 positions, each divided by the largest of its group in the step,
  * differ by more than 2^31 within 32 positions (a position that is large in all its
  * groups alike does not count: up to 2^79 between positions, 2^151 between steps), the

@@ -17,17 +17,19 @@
 //   q  times one per row, the largest magnitude in [2^14, 2^15);
 //   K  times one per 32 positions, likewise: undone in the fp32 scores (with q's, and
 //      log2(e) / sqrt(d));
-//   V  times one per group of 32 values, 2^-R_y, the step's largest in that group
+//   V  times one per group of 32 values, 2^-R_y, by the step's largest in that group
 //      (undone in the epilogue), and one per 32 positions, 2^-ev, by how far all their
-//      groups stay below that: likewise.  R_y stays while every group of every 32
-//      positions is within 2^-8 and 2^4 of it; else it moves, and O's columns of that
+//      groups stay below that (or one exceeds it): likewise.  R_y stays while every
+//      group of every 32 positions is near it; else it moves, and O's columns of that
 //      group with it, as a row's O does with its reference: what is large in one
-//      group moves nothing of the others.  2^ev goes into these positions' weights,
+//      group moves little of the others.  2^ev goes into these positions' weights,
 //      P = 2^{x + ev - M} with M near the maximum of x + ev so far; the row sum takes
-//      P 2^-ev in fp32.  ev is below 4 (values from 2^111 on aside), so a weight keeps
-//      2^-20 of the row's largest.  A value of V keeps 2^-37 of the largest of its
-//      group in the step, 2^-27 in its 32 positions; where a group of 32 positions
-//      keeps no 2^-8 of itself, the call is reported.
+//      P 2^-ev in fp32.  ev is below 10 (values from 2^111 on aside), so a weight keeps
+//      2^-14 of the row's largest (2^-25 where ev is 0 throughout); where a group is far
+//      above the item's others, ev is 8 there, and these positions' weights keep 2^-8
+//      of that.  A value of V keeps 2^-24 of the largest of its group in its 32
+//      positions; where a group of 32 positions keeps no 2^-14 of itself, the call is
+//      reported.
 // P and V are rounded to f16 (2^-11 of themselves): bf16's 2^-8 would show beside
 // the output's own rounding.  Scores, sums and maxima are fp32.
 //
@@ -112,12 +114,15 @@ constexpr uint32_t kColP = 64, kColO = 256;
 // ends when a step's wait ran out: its limit is this many of theirs.
 constexpr uint64_t kItemWaits = 64;
 constexpr float kGrowLog2 = 15.f;       // largest weight 2^15: above, the reference moves
-// V's groups within 2^-8 and 2^4 of R_y leave it where it is; R_y comes down to 2^-72 of
-// an item's largest at most (O, below 2^30 of each key, goes up with it, and has to stay
-// a number for 2^24 keys); 32 positions' group 2^32 below where f16 has them and more
-// (its half step is 2^-39 of that) has lost 2^-8 of itself.
-constexpr float kVBelow = 0x1p-8f;
-constexpr int kVAbove = 4, kVSpan = 72, kVLost = 31, kNoGroup = -1000;
+// V's groups within 2^-5 and 2^10 of R_y leave it where it is.  A group 2^7 above the
+// item's smallest and more gets an R_y up to 2^8 below itself, so that ev raises the
+// weights of its positions: as large as they are, they may count where their weights are
+// below what f16 holds beside the row's largest.  R_y comes down to 2^-72 of an item's
+// largest at most (O, below 2^30 of each key, goes up with it, and has to stay a number
+// for 2^24 keys); 32 positions' group more than 2^24 below where f16 has them (its half
+// step is 2^-39 of that) no longer keeps 2^-14 of itself, and is reported.
+constexpr float kVBelow = 0x1p-5f;
+constexpr int kVAbove = 10, kVRise = 7, kVRiseMost = 8, kVSpan = 72, kVLost = 24, kNoGroup = -1000;
 constexpr float kNothing = -3.402823466e38f;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -159,7 +164,8 @@ struct Ctl {
   int vmoved[4][4];                     // R_y moved: O's columns follow by these factors
   float vscale[4][Y];
   int vr[2][Y];                         // per item slot: V's exponents R_y, less 14
-  int vmax[kDeqWarps][Y], vhigh[Y];     // a step's exponents by 32 positions; the largest R_y of an item
+  int vmax[kDeqWarps][Y];               // a step's exponents by 32 positions
+  int vhigh[Y], vlow[Y];                // an item's largest R_y, and smallest group of 32 positions
   alignas(16) int tops[2 * kDeqWarps];  // prefix: the furthest positions of any row
   float pair[2][2][BM];                 // per tile and half: what the two threads of a row tell each other
   int64_t sums[kWarps], found[2];
@@ -768,19 +774,26 @@ __global__ void __launch_bounds__(kThreads, 1) q4_many_kernel(const __grid_const
           }
           if (lane < Y) ctl->vmax[dw][lane] = own;
           const int high = first ? kNoGroup : ctl->vhigh[y0], now = 127 - (unit_of >> 23);
+          int low = first ? -kNoGroup : ctl->vlow[y0];
           // (a wait that ran out is told to the other warps here, or behind the item)
           ok = barrier_and(BAR_V, kDeqThreads, ok);
           if (!ok) break;
           int e = kNoGroup;
 #pragma unroll
-          for (int w = 0; w < kDeqWarps; ++w) e = max(e, ctl->vmax[w][y0]);
+          for (int w = 0; w < kDeqWarps; ++w) {
+            const int v = ctl->vmax[w][y0];
+            e = max(e, v);
+            low = v == kNoGroup ? low : min(low, v);
+          }
           const int base = __reduce_max_sync(FULL, e);
           const int none = !first ? now : base == kNoGroup ? 0 : min(base, 110);
-          const int to = e == kNoGroup ? none : min(max(e, high - kVSpan), 110);
+          const int rise = max(0, min(e - low - kVRise, kVRiseMost));
+          const int to = e == kNoGroup ? none : min(max(e - rise, high - kVSpan), 110);
           moved = __any_sync(FULL, !first && to != now);
           if (t < Y) {
             ctl->vr[islot][t] = to - 14;
             ctl->vhigh[t] = e == kNoGroup ? high : max(high, to);
+            ctl->vlow[t] = low;
             ctl->vscale[g & 3][t] = pow2(now - to);
           }
           most = 0.f;

@@ -107,6 +107,22 @@ def test_whole_positions_far_apart(B, power):
                 check(got, want)
 
 
+@pytest.mark.parametrize("power", [16, 20, 22])
+@pytest.mark.parametrize("lean", [-4, 0, 4])
+@pytest.mark.parametrize("B,wide", [(1, True), (300, True), (1, False)])
+def test_large_values_of_small_weights(B, wide, lean, power):
+    """A position so far back that its weight and its group's size make up for one
+    another (to 2^lean): the weight, 2^-power and less of the row's largest, counts.
+    It is held to 2^-33 of that largest: 2^(power - 33), less than 2^-11, of the group's."""
+    s = Rows(B, 4, 1, 128, 64, 600, "bf16", 32, wide=wide, seed=9)
+    at, pos = 150, 568
+    s.v[:, :, at, 32:64] *= 2.0 ** power
+    plsh.q4_cache_write(s.cache, s.k, s.v, i32([0] * B))
+    sigma = np.full(4, (pos - at) / ((power - lean) * np.log(2)))
+    for got, want in chunk(s, sigma, pos, (0, B - 1)):
+        check(got, want, (1,))
+
+
 @pytest.mark.parametrize("power", [16, 20, 24])
 @pytest.mark.parametrize("wide", [True, False])
 def test_a_later_token_takes_nothing_from_an_earlier_one(wide, power):
@@ -146,17 +162,21 @@ def test_one_group_of_a_shared_position(B, shared, power):
 
 @pytest.mark.parametrize("B", [1, 300])
 def test_what_cannot_be_held_is_refused_however_the_list_is_cut(B):
-    """A group 2^33 above and more what other 32 positions of its step hold."""
+    """A group 2^33 above and more what other 32 positions of its step hold; below, the
+    rows are right."""
     for power, wrong in ((29, False), (36, True), (80, True)):
         s = Rows(B, 4, 1, 128, 64, 600, "bf16", 32, seed=9)
         s.v[:, :, 300, 32:64] *= 2.0 ** power
         plsh.q4_cache_write(s.cache, s.k, s.v, i32([0] * B))
+        if not wrong:
+            for sigma in (np.full(4, 50.0), np.full(4, 1e6)):
+                for got, want in chunk(s, sigma, 568, (0, B - 1)):
+                    check(got, want, (1,))
+            continue
         plsh.alibi_exact_chunk_q4(s.q, s.cache, np.full(4, 50.0), i32([568] * B))
-        if wrong:
-            with pytest.raises(plsh.PlshError) as e:
-                plsh.stream_status()
-            assert e.value.status == plsh.PLSH_ERR_RANGE
-        plsh.stream_status()
+        with pytest.raises(plsh.PlshError) as e:
+            plsh.stream_status()
+        assert e.value.status == plsh.PLSH_ERR_RANGE
 
 
 @pytest.mark.parametrize("sigma", [0.05, 1e-4, 2e-6, 1.4e-6, 1e-6, 1e-8, 1e-9, 1e-35, 1e-300])
