@@ -45,10 +45,10 @@
 //
 // What bounds it.  The products of a step (two tiles) take 2048 cycles at 4096
 // multiply-adds a cycle.  Measured (CUDA graph, back to back; shares of the measured
-// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2280 us (1190
-// TFLOP/s, 62 %), 2.15 us a step; 512 tokens behind 7680, 32/8 heads, 91 us (26 steps
-// a CTA); a batch of eight ragged chunks 237 us; 128 sequences behind a prefix of
-// 65536, 40/8 heads, 219 us, 64 behind 8192, 32/8 heads, 50 us (four steps a CTA).
+// GEMM rate of 1918 TFLOP/s): 2048 tokens behind 63488, 40/8 heads, 2395 us (1130
+// TFLOP/s, 59 %), 2.25 us a step; 512 tokens behind 7680, 32/8 heads, 91 us (26 steps
+// a CTA); a batch of eight ragged chunks 236 us; 128 sequences behind a prefix of
+// 65536, 40/8 heads, 220 us, 64 behind 8192, 32/8 heads, 50 us (four steps a CTA).
 // Neither the tensor cores nor the schedulers are full (512 behind 7680: pipe 36 %,
 // issue slots 55 %): a tile's steps follow one another through its scores (1000
 // cycles with P V before them), its softmax (2100 of weights, 500 until they are in
@@ -58,20 +58,23 @@
 // fill each other's gaps in part.  Beginning an item costs more: 12000 cycles from its
 // listing to the first scores, where table, pages and queries come one after another
 // from memory not touched before, and 7000 for the first step, whose weights are taken
-// twice.  (Cycles as stamped when a step took 4600; it takes 4200 now.)
+// twice.  (Cycles as stamped when a step took 4600; it takes 4400 now.)
 //
 // What it took (2048 behind 63488): one thread's product issue from a branch of its
 // own 3311 us, the whole warp's with a predicate 2835 (operands stay in uniform
 // registers); softmax by sixteen columns with the next ones' load in flight, V's
 // exponents from one reduction 2550; whether anything is masked decided once a step,
 // and registers given to the codes 2430; V's exponents moving with the step (a barrier
-// of V's warps a step) 2360, q's by row 2465, the exponents by a lane a group 2280.
+// of V's warps a step) 2360, q's by row 2465, the exponents by a lane a group 2280, part
+// of a large group's excess left in its weights 2395.
 // Slower, and dropped: one thread a row (3100), 80 registers for softmax (2770), scalar
 // instead of paired fp32 multiply-adds (+6 %), the first step's weights not tried
 // before its maximum is known (+14 %, the loop's code suffers), K's and V's next codes
 // loaded while these are taken apart (2415 to 2480, shorter items lose more), O
 // following V's exponents by V's warps behind the softmax (2590 to 2780) or at a step's
-// start (2590), the bias from positions instead of added up (2700), and for items of one
+// start (2590), the row's largest weight at 2^10 instead of 1, which would hold small
+// weights of large values without V's part in them (heads of flat slopes and scores of
+// sigma 3 move their references 40 % longer), the bias from positions instead of added up (2700), and for items of one
 // tile the other tile on every second step of the same keys (64 rows of 131072 keys:
 // 146 -> 166 us).  The softmax's 88 registers spill 84 to 132 bytes a thread (0.8 % of
 // the instructions of 512 behind 7680); which values, and with them 5 % of the time,
