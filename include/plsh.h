@@ -675,7 +675,8 @@ plsh_status plsh_attn_path(const plsh_tensor* Q, const plsh_bins* bins, int32_t 
                            int32_t* path);
 
 /* Debug knob: limit in nanoseconds of every device-side wait launched after
- * this call on the current device (0 restores the default of 2 s). */
+ * this call on the current device (0 restores the default of 2 s), but for a thread
+ * block's wait for its own copies and products before it ends, which is 2 s always. */
 plsh_status plsh_set_wait_limit_ns(uint64_t ns);
 
 /*
